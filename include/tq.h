@@ -209,7 +209,60 @@ typedef struct {
   float boundaries_v[15];
 } tq_cache_desc;
 
+/* Rotary positions.  A head carries rotary_dim / 2 pairs (a, b); at position p
+ * pair i turns by the angle p f_i:
+ *     y_a = A (x_a cos - x_b sin),  y_b = A (x_b cos + x_a sin);
+ * the pairs are (i, i + rotary_dim / 2) in the half layout and (2 i, 2 i + 1) in
+ * the interleaved one, coordinates from rotary_dim on pass through.  The
+ * frequency f_i travels as a fraction of a turn in 64 bits, so that p f_i modulo a
+ * turn is exact for any position: turns[i] = round(f_i / (2 pi) mod 1 * 2^64). */
+enum { TQ_ROPE_HALF = 0, TQ_ROPE_INTERLEAVED = 1 };
+
+typedef struct {
+  int32_t layout;     /* TQ_ROPE_HALF or TQ_ROPE_INTERLEAVED */
+  int32_t rotary_dim; /* even, 2 .. head_dim */
+  float amplitude;    /* A */
+  int32_t reserved;   /* 0 */
+  uint64_t turns[64]; /* entries from rotary_dim / 2 on are ignored */
+} tq_rope;
+
+/* Frequencies f_i = base^(-2 i / rotary_dim) and their scalings for long contexts:
+ *   LINEAR  f / factor
+ *   NTK     base * factor^(rotary_dim / (rotary_dim - 2)) in place of base
+ *   BANDED  with t_i = length f_i / (2 pi) turns in `length` positions: f kept where
+ *           t_i >= high, f / factor where t_i <= low, linear in t_i between
+ *   YARN    with d(t) = rotary_dim ln(length / (2 pi t)) / (2 ln base): f kept for
+ *           i <= floor(d(high)), f / factor for i >= ceil(d(low)), linear in i between
+ *           (both ends clipped to [0, rotary_dim - 1]); A = 0.1 ln(factor) + 1 */
+enum { TQ_ROPE_SCALE_NONE = 0, TQ_ROPE_SCALE_LINEAR = 1, TQ_ROPE_SCALE_NTK = 2, TQ_ROPE_SCALE_BANDED = 3,
+       TQ_ROPE_SCALE_YARN = 4 };
+
+typedef struct {
+  int32_t kind;  /* TQ_ROPE_SCALE_* */
+  double factor; /* >= 1 */
+  double low, high, length; /* BANDED, YARN: 0 < low < high, length > 0 */
+} tq_rope_scaling;
+
+/* Rows of one tensor of heads: element (t, h, j) of in is at in[t * in_token_stride
+ * + h * in_head_stride + j] (strides in elements, any value, the last dimension is
+ * contiguous), likewise out.  out == in with equal strides rotates in place; any
+ * other overlap of in and out is the caller's error.  Bases and strides that are
+ * multiples of 16 bytes take the wide loads. */
+typedef struct {
+  const void* in;
+  void* out;
+  int32_t num_heads;
+  int64_t in_token_stride, in_head_stride;
+  int64_t out_token_stride, out_head_stride;
+} tq_heads;
+
 /* ---- set-up (host only, no GPU needed) ---------------------------------- */
+
+/* Frequencies of a rotation ("Rotary positions" above).  scaling may be NULL (none);
+ * inv_freq, if not NULL, is a host array of rotary_dim / 2 frequencies in radians a
+ * position that replaces base (and takes no scaling). */
+tq_status tq_make_rope(int layout, int rotary_dim, double base, const tq_rope_scaling* scaling,
+                       const double* inv_freq, tq_rope* out);
 
 /* Lloyd-Max codebook for one coordinate of a rotated unit vector in R^head_dim
  * ([P1] §第1段; density and emission rule above).  Host outputs:
@@ -341,6 +394,51 @@ tq_status tq_decode_step(const tq_cache_desc* desc, const void* k_new, const voi
                          const void* q, int q_dtype, int batch, int num_q_heads, const int32_t* block_table,
                          int max_blocks_per_seq, const int32_t* context_lens, float sm_scale, void* out,
                          int out_dtype, void* workspace, size_t workspace_bytes, int num_splits, void* stream);
+
+/* Rotary positions of the query and key heads of n_tokens tokens: device rows of
+ * dtype (TQ_F32 or TQ_BF16; computed in fp32, rounded once), either tensor may be
+ * NULL; positions: device int64[n_tokens], any value.  transpose = 1 applies the
+ * transposed rotation (angles negated, the same amplitude): the gradient with
+ * respect to the input of a gradient with respect to the output, and for A = 1 the
+ * inverse. */
+tq_status tq_rope_apply(const tq_rope* rope, int transpose, const tq_heads* q, const tq_heads* k, int dtype,
+                        const int64_t* positions, int64_t n_tokens, void* stream);
+
+/* Append with the rotation applied on the way, in one kernel: the keys of token t
+ * are rotated to positions[t] in fp32 and stored, with the values, in slot
+ * slot_mapping[t] in the layer's format ("Memory layout"; skipped if the slot is
+ * negative); the keys are not rounded between the rotation and the quantizer.  q
+ * (NULL: none) is rotated to q->out, negative slots too.  k->out, if not NULL, takes
+ * the rotated keys (for a prompt's own attention), v->out must be NULL.  k or v may be
+ * NULL to append only the other.  Equal to tq_rope_apply in fp32 followed by
+ * tq_quantize_append of the fp32 rows, but for codes whose y lies within the 1e-5 tie
+ * band of a boundary.  bf16, k8v4 and packed layers with a Hadamard rotation and
+ * without QJL keys (TQ_ERR_UNSUPPORTED otherwise). */
+tq_status tq_rope_append(const tq_cache_desc* desc, const tq_rope* rope, const tq_heads* q, const tq_heads* k,
+                         const tq_heads* v, int in_dtype, const int64_t* positions, const int64_t* slot_mapping,
+                         int64_t n_tokens, void* stream);
+
+/* Workspace bytes tq_prefix_decode needs for these sizes; 0 on error. */
+size_t tq_prefix_workspace_bytes(const tq_cache_desc* desc, int batch, int num_q_heads, int64_t prefix_len,
+                                 int max_blocks_per_seq);
+
+/* Decode attention of a batch whose sequences share a prefix: the prefix's
+ * prefix_len tokens lie in the blocks prefix_table[0 .. ceil(prefix_len / 16)) (device
+ * int32) and are read once for the whole batch; sequence b's own context_lens[b]
+ * tokens follow them, by its row of block_table as in tq_decode_attention:
+ *     out[b] = softmax(sm_scale q[b] [K_prefix; K_own,b]^T) [V_prefix; V_own,b].
+ * prefix_len (host, 0 .. 2^31 - 1) may be 0; max_blocks_per_seq = 0 says that no
+ * sequence has own tokens (block_table and context_lens are then not read); a
+ * sequence without any token gets a zero row.  An entry of prefix_table outside
+ * [0, num_blocks) is skipped and recorded (TQ_DEV_BAD_BLOCK).  The other arguments, the
+ * workspace contract (at least tq_prefix_workspace_bytes(...), zero before the first
+ * call) and errors as for tq_decode_attention; one workspace serves both calls.
+ * bf16, k8v4 and packed layers with a Hadamard rotation and without QJL keys
+ * (TQ_ERR_UNSUPPORTED otherwise). */
+tq_status tq_prefix_decode(const tq_cache_desc* desc, const void* q, int q_dtype, int batch, int num_q_heads,
+                           const int32_t* prefix_table, int64_t prefix_len, const int32_t* block_table,
+                           int max_blocks_per_seq, const int32_t* context_lens, float sm_scale, void* out,
+                           int out_dtype, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Dequantize records ([P2] "Incremental dequantization"): slots: device int64[n];
  * out: device [n][num_kv_heads][head_dim] (out_dtype) with

@@ -25,6 +25,8 @@ TQ_F32, TQ_BF16 = 0, 1
 TQ_ROT_HADAMARD, TQ_ROT_DENSE, TQ_RNG_QJL = 1, 2, 3
 TQ_KV_PACKED, TQ_KV_BF16, TQ_KV_K8V4, TQ_KV_POLAR = 0, 1, 2, 3
 TQ_NORM_CORRECTED, TQ_NORM_RAW = 0, 1
+TQ_ROPE_HALF, TQ_ROPE_INTERLEAVED = 0, 1
+TQ_ROPE_SCALE_NONE, TQ_ROPE_SCALE_LINEAR, TQ_ROPE_SCALE_NTK, TQ_ROPE_SCALE_BANDED, TQ_ROPE_SCALE_YARN = range(5)
 TQ_DEV_BAD_SLOT, TQ_DEV_BAD_BLOCK, TQ_DEV_BAD_CONTEXT, TQ_DEV_WAIT_TIMEOUT = 1, 2, 4, 8
 
 STATUS_NAMES = {
@@ -54,8 +56,26 @@ class CacheDesc(ctypes.Structure):
                 ("centroids_v", ctypes.c_float * 16), ("boundaries_v", ctypes.c_float * 15)]
 
 
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("layout", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("amplitude", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("turns", ctypes.c_uint64 * 64)]
+
+
+class RopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("length", ctypes.c_double)]
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("inp", ctypes.c_void_p), ("out", ctypes.c_void_p), ("num_heads", ctypes.c_int32),
+                ("in_token_stride", ctypes.c_int64), ("in_head_stride", ctypes.c_int64),
+                ("out_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64)]
+
+
 _P = ctypes.POINTER
 _D = ctypes.POINTER(CacheDesc)
+_R = ctypes.POINTER(RopeDesc)
+_H = ctypes.POINTER(Heads)
 _SIGNATURES = {
     "tq_make_codebook": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, _P(ctypes.c_float), _P(ctypes.c_float)]),
     "tq_make_rotation": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_uint64, ctypes.c_int, _P(ctypes.c_float)]),
@@ -81,6 +101,17 @@ _SIGNATURES = {
                                       ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_int,
                                       ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p, ctypes.c_int,
                                       ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_void_p]),
+    "tq_make_rope": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_double, _P(RopeScaling), _P(ctypes.c_double),
+                                    _R]),
+    "tq_rope_apply": (ctypes.c_int, [_R, ctypes.c_int, _H, _H, ctypes.c_int, ctypes.c_void_p, ctypes.c_int64,
+                                     ctypes.c_void_p]),
+    "tq_rope_append": (ctypes.c_int, [_D, _R, _H, _H, _H, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+                                      ctypes.c_int64, ctypes.c_void_p]),
+    "tq_prefix_workspace_bytes": (ctypes.c_size_t, [_D, ctypes.c_int, ctypes.c_int, ctypes.c_int64, ctypes.c_int]),
+    "tq_prefix_decode": (ctypes.c_int, [_D, ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                        ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int,
+                                        ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p, ctypes.c_int,
+                                        ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "tq_dequantize": (ctypes.c_int, [_D, ctypes.c_int, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
                                      ctypes.c_int, ctypes.c_void_p]),
     "tq_image_bytes": (ctypes.c_size_t, [_D, ctypes.c_int64]),
@@ -173,6 +204,104 @@ def _stream(stream):
     torch = _torch()
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _heads(t, out, name, positions):
+    """A tq_heads of t [n_tokens, heads, d] (any token and head strides) and its output rows."""
+    if t is None:
+        return None
+    h = Heads()
+    for x, what in ((t, name), (out, name + "_out")):
+        if x is None:
+            continue
+        if not x.is_cuda:
+            raise ValueError("%s must be a CUDA tensor" % what)
+        if x.dim() != 3 or x.shape[2] != TQ_HEAD_DIM or x.shape[0] != positions.shape[0]:
+            raise ValueError("%s must be [%d, heads, %d], got %s" % (what, positions.shape[0], TQ_HEAD_DIM,
+                                                                     tuple(x.shape)))
+        if x.numel() > 0 and x.stride(2) != 1:
+            raise ValueError("%s must be contiguous in its last dimension" % what)
+    if out is not None and (out.shape != t.shape or out.dtype != t.dtype):
+        raise ValueError("%s_out must have %s's shape and type" % (name, name))
+    h.inp, h.num_heads = t.data_ptr(), t.shape[1]
+    h.in_token_stride, h.in_head_stride = t.stride(0), t.stride(1)
+    if out is not None:
+        h.out = out.data_ptr()
+        h.out_token_stride, h.out_head_stride = out.stride(0), out.stride(1)
+    return h
+
+
+def _index_ptr(t, name, dtype, shape):
+    """Device pointer of an index tensor after checking its type and shape."""
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    return _ptr(t, name)
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
+class Rope:
+    """Rotary positions: the frequencies of a rotation (tq_make_rope).
+
+    layout: "half" (pairs i, i + rotary_dim / 2) or "interleaved" (pairs 2 i, 2 i + 1).
+    scaling: None or a dict {"kind": "linear" | "ntk" | "banded" | "yarn", "factor": f},
+    for banded and yarn also "low", "high" and "length".  inv_freq: rotary_dim / 2
+    frequencies in radians a position that replace base.
+    """
+
+    _LAYOUTS = {"half": TQ_ROPE_HALF, "interleaved": TQ_ROPE_INTERLEAVED}
+    _KINDS = {"linear": TQ_ROPE_SCALE_LINEAR, "ntk": TQ_ROPE_SCALE_NTK, "banded": TQ_ROPE_SCALE_BANDED,
+              "yarn": TQ_ROPE_SCALE_YARN}
+
+    def __init__(self, rotary_dim=TQ_HEAD_DIM, base=10000.0, layout="half", scaling=None, inv_freq=None):
+        if layout not in self._LAYOUTS:
+            raise ValueError("layout must be 'half' or 'interleaved'")
+        s = None
+        if scaling is not None:
+            if scaling.get("kind") not in self._KINDS:
+                raise ValueError("scaling kind must be one of %s" % sorted(self._KINDS))
+            s = RopeScaling(self._KINDS[scaling["kind"]], float(scaling["factor"]), float(scaling.get("low", 0.0)),
+                            float(scaling.get("high", 0.0)), float(scaling.get("length", 0.0)))
+        freqs = None
+        if inv_freq is not None:
+            values = np.asarray(inv_freq, np.float64).reshape(-1)
+            if values.size != rotary_dim // 2:
+                raise ValueError("inv_freq must hold rotary_dim / 2 frequencies")
+            freqs = (ctypes.c_double * values.size)(*values)
+        self.desc = RopeDesc()
+        _check(lib().tq_make_rope(self._LAYOUTS[layout], rotary_dim, base, _ref(s), freqs, ctypes.byref(self.desc)))
+        self.layout, self.rotary_dim = layout, int(rotary_dim)
+        self.amplitude = float(self.desc.amplitude)
+
+    def turns(self):
+        """Turns a position of each pair (fp64 [rotary_dim / 2], modulo one turn)."""
+        return np.array(self.desc.turns[: self.rotary_dim // 2], dtype=np.uint64).astype(np.float64) * 2.0 ** -64
+
+
+def apply_rope(rope, positions, q, k=None, q_out=None, k_out=None, transpose=False, stream=None):
+    """Rotary positions of q and k [n_tokens, heads, d] (tq_rope_apply); positions int64
+    [n_tokens].  transpose: the transposed rotation (the gradient).  q_out / k_out may be
+    q / k (in place).  Returns (q_out, k_out), contiguous where they were not given."""
+    torch = _torch()
+    if q is None and k is None:
+        raise ValueError("q or k is needed")
+    ref = q if q is not None else k
+    if q is not None and k is not None and q.dtype != k.dtype:
+        raise TypeError("q and k must have one type")
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    n = int(ref.shape[0])
+    pos = _index_ptr(positions, "positions", torch.int64, (n,))
+    hq, hk = _heads(q, q_out, "q", positions), _heads(k, k_out, "k", positions)
+    _check(lib().tq_rope_apply(ctypes.byref(rope.desc), 1 if transpose else 0, _ref(hq), _ref(hk), _dtype_code(ref),
+                               pos, n, _stream(stream)))
+    return q_out, k_out
 
 
 class Layer:
@@ -346,6 +475,66 @@ class Layer:
                                     _ptr(block_table, "block_table"), max_blocks, _ptr(context_lens, "context_lens"),
                                     ctypes.c_float(sm_scale), _ptr(out, "out"), _dtype_code(out),
                                     _ptr(workspace, "workspace"), workspace.numel(), num_splits, _stream(stream)))
+        return out
+
+    def rope_append(self, rope, k, v, positions, slot_mapping, q=None, q_out=None, k_out=None, stream=None):
+        """Append with the rotation applied on the way (tq_rope_append): k [n_tokens, H_kv, d]
+        rotated to positions [n_tokens] (int64), stored with v in slot_mapping [n_tokens]
+        (int64).  q [n_tokens, H_q, d] is rotated to q_out (may be q); k_out, if given, takes
+        the rotated keys.  Token and head strides are free.  Returns q_out."""
+        torch = _torch()
+        ref = k if k is not None else v
+        if ref is None:
+            raise ValueError("k or v is needed")
+        if any(t is not None and t.dtype != ref.dtype for t in (q, v)):
+            raise TypeError("q, k and v must have one type")
+        n = int(ref.shape[0])
+        pos = _index_ptr(positions, "positions", torch.int64, (n,))
+        slots = _index_ptr(slot_mapping, "slot_mapping", torch.int64, (n,))
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        hq, hk = _heads(q, q_out, "q", positions), _heads(k, k_out, "k", positions)
+        hv = _heads(v, None, "v", positions)
+        _check(lib().tq_rope_append(ctypes.byref(self.desc), ctypes.byref(rope.desc), _ref(hq), _ref(hk), _ref(hv),
+                                    _dtype_code(ref), pos, slots, n, _stream(stream)))
+        return q_out
+
+    def prefix_workspace_bytes(self, batch, num_q_heads, prefix_len, max_blocks_per_seq):
+        n = lib().tq_prefix_workspace_bytes(ctypes.byref(self.desc), batch, num_q_heads, prefix_len,
+                                            max_blocks_per_seq)
+        if n == 0:
+            raise TQError(TQ_ERR_INVALID_ARG, last_error() or "invalid sizes")
+        return int(n)
+
+    def prefix_decode(self, q, prefix_table, prefix_len, block_table=None, context_lens=None, sm_scale=None, out=None,
+                      out_dtype=None, workspace=None, stream=None):
+        """Decode attention of a batch with a shared prefix (tq_prefix_decode).  q [B, H_q, d];
+        prefix_table int32 [>= ceil(prefix_len / 16)] blocks of the prefix; block_table int32
+        [B, max_blocks] and context_lens int32 [B]: the sequences' own tokens (None: none)."""
+        torch = _torch()
+        bsz, hq, _ = q.shape
+        prefix_len = int(prefix_len)
+        if prefix_len > 0 and (prefix_table.dim() != 1 or prefix_table.shape[0] * TQ_BLOCK_SIZE < prefix_len):
+            raise ValueError("prefix_table must be one row of at least ceil(prefix_len / %d) blocks" % TQ_BLOCK_SIZE)
+        max_blocks = 0 if block_table is None else int(block_table.shape[1])
+        if max_blocks > 0 and context_lens is None:
+            raise ValueError("block_table needs context_lens")
+        if sm_scale is None:
+            sm_scale = 1.0 / math.sqrt(self.head_dim)
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype if out_dtype is None else out_dtype, device=q.device)
+        if workspace is None and bsz > 0:
+            workspace = torch.zeros(self.prefix_workspace_bytes(bsz, hq, prefix_len, max_blocks), dtype=torch.uint8,
+                                    device=q.device)
+        table = None if prefix_len <= 0 else _index_ptr(prefix_table, "prefix_table", torch.int32, prefix_table.shape)
+        rows = lens = None
+        if max_blocks > 0:
+            rows = _index_ptr(block_table, "block_table", torch.int32, (bsz, max_blocks))
+            lens = _index_ptr(context_lens, "context_lens", torch.int32, (bsz,))
+        _check(lib().tq_prefix_decode(ctypes.byref(self.desc), _ptr(q, "q"), _dtype_code(q), bsz, hq, table,
+                                      prefix_len, rows, max_blocks, lens, ctypes.c_float(sm_scale), _ptr(out, "out"),
+                                      _dtype_code(out), _ptr(workspace, "workspace"),
+                                      0 if workspace is None else workspace.numel(), _stream(stream)))
         return out
 
     def image_bytes(self, n_blocks):

@@ -154,6 +154,35 @@ tq_status prepare_decode(const tq_cache_desc* desc, const void* q, int q_dtype, 
   return TQ_OK;
 }
 
+// Checks of a tq_rope (as tq_make_rope emits it).
+tq_status check_rope(const tq_rope* r, const char* fn) {
+  if (!r) return fail(TQ_ERR_INVALID_ARG, "%s: null rope", fn);
+  if (r->layout != TQ_ROPE_HALF && r->layout != TQ_ROPE_INTERLEAVED)
+    return fail(TQ_ERR_INVALID_ARG, "%s: rope layout %d", fn, r->layout);
+  if (r->rotary_dim < 2 || r->rotary_dim > TQ_HEAD_DIM || r->rotary_dim % 2 != 0)
+    return fail(TQ_ERR_INVALID_ARG, "%s: rope rotary_dim %d", fn, r->rotary_dim);
+  if (!(r->amplitude - r->amplitude == 0.0f)) return fail(TQ_ERR_INVALID_ARG, "%s: rope amplitude is not finite", fn);
+  return TQ_OK;
+}
+
+// Checks of one tensor of heads.
+tq_status check_heads(const tq_heads& h, int dtype, int64_t n_tokens, bool need_out, const char* what) {
+  const uintptr_t mask = dtype == TQ_F32 ? 3 : 1;
+  if (n_tokens > 0 && (!h.in || (need_out && !h.out))) return fail(TQ_ERR_INVALID_ARG, "%s: null rows", what);
+  if (h.num_heads < 1) return fail(TQ_ERR_INVALID_ARG, "%s: num_heads %d", what, h.num_heads);
+  if ((reinterpret_cast<uintptr_t>(h.in) | reinterpret_cast<uintptr_t>(h.out)) & mask)
+    return fail(TQ_ERR_INVALID_ARG, "%s: rows not aligned to their elements", what);
+  return TQ_OK;
+}
+
+// Workspace of the own tokens' decode inside tq_prefix_decode; without own tokens the
+// counter region alone, so that it stays zero for later decode calls.
+size_t own_workspace(const tq_cache_desc* desc, int batch, int num_q_heads, int max_blocks) {
+  if (max_blocks < 1) return kCounterRegionBytes;
+  return decode_workspace(batch, num_q_heads, resolve_splits(desc, batch, num_q_heads, max_blocks, 0), desc->head_dim,
+                          false).total;
+}
+
 }  // namespace
 }  // namespace tq
 
@@ -300,6 +329,155 @@ tq_status tq_append_decode(const tq_cache_desc* desc, const void* k, const void*
   }
   if (batch == 0) return TQ_OK;
   return cuda_result(launch_decode(c, st), "decode attention");
+}
+
+tq_status tq_rope_apply(const tq_rope* rope, int transpose, const tq_heads* q, const tq_heads* k, int dtype,
+                        const int64_t* positions, int64_t n_tokens, void* stream) {
+  clear_error();
+  tq_status s = check_rope(rope, "tq_rope_apply");
+  if (s != TQ_OK) return s;
+  if (!valid_dtype(dtype)) return fail(TQ_ERR_INVALID_ARG, "tq_rope_apply: dtype %d", dtype);
+  if (n_tokens < 0) return fail(TQ_ERR_INVALID_ARG, "tq_rope_apply: n_tokens < 0");
+  if (!q && !k) return fail(TQ_ERR_INVALID_ARG, "tq_rope_apply: both q and k are null");
+  if ((q && (s = check_heads(*q, dtype, n_tokens, true, "tq_rope_apply: q")) != TQ_OK) ||
+      (k && (s = check_heads(*k, dtype, n_tokens, true, "tq_rope_apply: k")) != TQ_OK))
+    return s;
+  if (n_tokens == 0) return TQ_OK;
+  if (!positions) return fail(TQ_ERR_INVALID_ARG, "tq_rope_apply: null positions");
+  DeviceInfo di;
+  if ((s = device_info(&di)) != TQ_OK) return s;
+  RopeCall c = {};
+  c.rope = rope;
+  c.transpose = transpose ? 1 : 0;
+  c.dtype = dtype;
+  c.heads[0] = q;
+  c.heads[1] = k;
+  c.positions = positions;
+  c.n_tokens = n_tokens;
+  c.status = di.status;
+  c.num_sms = di.num_sms;
+  return cuda_result(launch_rope_apply(c, reinterpret_cast<cudaStream_t>(stream)), "rope");
+}
+
+tq_status tq_rope_append(const tq_cache_desc* desc, const tq_rope* rope, const tq_heads* q, const tq_heads* k,
+                         const tq_heads* v, int in_dtype, const int64_t* positions, const int64_t* slot_mapping,
+                         int64_t n_tokens, void* stream) {
+  clear_error();
+  tq_status s = check_desc(desc);
+  if (s != TQ_OK) return s;
+  if ((s = check_rope(rope, "tq_rope_append")) != TQ_OK) return s;
+  const tq_layer_format& f = desc->fmt;
+  if (f.kv_format == TQ_KV_POLAR || (f.kv_format == TQ_KV_PACKED && f.qjl_k) ||
+      (f.kv_format != TQ_KV_BF16 && f.rot_kind != TQ_ROT_HADAMARD))
+    return fail(TQ_ERR_UNSUPPORTED,
+                "tq_rope_append: bf16, k8v4 and packed layers with a Hadamard rotation and no QJL keys only; rotate "
+                "with tq_rope_apply and append for the others");
+  if (!valid_dtype(in_dtype)) return fail(TQ_ERR_INVALID_ARG, "tq_rope_append: in_dtype %d", in_dtype);
+  if (n_tokens < 0) return fail(TQ_ERR_INVALID_ARG, "tq_rope_append: n_tokens < 0");
+  if (!k && !v) return fail(TQ_ERR_INVALID_ARG, "tq_rope_append: both k and v are null");
+  if ((q && (s = check_heads(*q, in_dtype, n_tokens, true, "tq_rope_append: q")) != TQ_OK) ||
+      (k && (s = check_heads(*k, in_dtype, n_tokens, false, "tq_rope_append: k")) != TQ_OK) ||
+      (v && (s = check_heads(*v, in_dtype, n_tokens, false, "tq_rope_append: v")) != TQ_OK))
+    return s;
+  if ((k && k->num_heads != desc->num_kv_heads) || (v && v->num_heads != desc->num_kv_heads))
+    return fail(TQ_ERR_INVALID_ARG, "tq_rope_append: k and v must have the layer's %d heads", desc->num_kv_heads);
+  if (v && v->out) return fail(TQ_ERR_INVALID_ARG, "tq_rope_append: v has no output rows");
+  const bool coded_k = k && f.kv_format == TQ_KV_PACKED, coded_v = v && f.kv_format != TQ_KV_BF16;
+  if ((coded_k && !cell_table_ok(desc->boundaries_k, (1 << f.bits_k) - 1)) ||
+      (coded_v && !cell_table_ok(desc->boundaries_v, (1 << f.bits_v) - 1)))
+    return fail(TQ_ERR_UNSUPPORTED, "tq_rope_append: codebook boundaries closer than 1/63 apart");
+  if (n_tokens == 0) return TQ_OK;
+  if (!positions || !slot_mapping) return fail(TQ_ERR_INVALID_ARG, "tq_rope_append: null positions/slot_mapping");
+  DeviceInfo di;
+  if ((s = device_info(&di)) != TQ_OK) return s;
+  RopeCall c = {};
+  c.rope = rope;
+  c.dtype = in_dtype;
+  c.heads[0] = q;
+  c.heads[1] = k;
+  c.heads[2] = v;
+  c.positions = positions;
+  c.slots = slot_mapping;
+  c.n_tokens = n_tokens;
+  c.status = di.status;
+  c.num_sms = di.num_sms;
+  return cuda_result(launch_rope_append(c, *desc, reinterpret_cast<cudaStream_t>(stream)), "rotated append");
+}
+
+size_t tq_prefix_workspace_bytes(const tq_cache_desc* desc, int batch, int num_q_heads, int64_t prefix_len,
+                                 int max_blocks_per_seq) {
+  clear_error();
+  if (check_desc(desc, false) != TQ_OK) return 0;
+  if (batch < 1 || num_q_heads < 1 || num_q_heads % desc->num_kv_heads != 0 || prefix_len < 0 ||
+      prefix_len > INT32_MAX || max_blocks_per_seq < 0) {
+    fail(TQ_ERR_INVALID_ARG, "tq_prefix_workspace_bytes: batch %d, num_q_heads %d, prefix_len %lld, max_blocks %d",
+         batch, num_q_heads, (long long)prefix_len, max_blocks_per_seq);
+    return 0;
+  }
+  DeviceInfo di;
+  if (device_info(&di) != TQ_OK) return 0;
+  return own_workspace(desc, batch, num_q_heads, max_blocks_per_seq) +
+         prefix_partial_bytes(*desc, batch, num_q_heads, prefix_len, di.num_sms);
+}
+
+tq_status tq_prefix_decode(const tq_cache_desc* desc, const void* q, int q_dtype, int batch, int num_q_heads,
+                           const int32_t* prefix_table, int64_t prefix_len, const int32_t* block_table,
+                           int max_blocks_per_seq, const int32_t* context_lens, float sm_scale, void* out,
+                           int out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  clear_error();
+  const char* fn = "tq_prefix_decode";
+  tq_status s = check_desc(desc);
+  if (s != TQ_OK) return s;
+  const tq_layer_format& f = desc->fmt;
+  if (f.kv_format == TQ_KV_POLAR || (f.kv_format == TQ_KV_PACKED && f.qjl_k) ||
+      (f.kv_format != TQ_KV_BF16 && f.rot_kind != TQ_ROT_HADAMARD))
+    return fail(TQ_ERR_UNSUPPORTED, "%s: bf16, k8v4 and packed layers with a Hadamard rotation and no QJL keys only", fn);
+  if (prefix_len < 0 || prefix_len > INT32_MAX)
+    return fail(TQ_ERR_INVALID_ARG, "%s: prefix_len %lld", fn, (long long)prefix_len);
+  if (prefix_len > 0 && !prefix_table) return fail(TQ_ERR_INVALID_ARG, "%s: null prefix_table", fn);
+  if (max_blocks_per_seq < 0) return fail(TQ_ERR_INVALID_ARG, "%s: max_blocks_per_seq < 0", fn);
+  if (max_blocks_per_seq > 0 && (!block_table || !context_lens))
+    return fail(TQ_ERR_INVALID_ARG, "%s: null block_table/context_lens", fn);
+  if (batch < 0) return fail(TQ_ERR_INVALID_ARG, "%s: batch < 0", fn);
+  if (num_q_heads < 1 || num_q_heads % desc->num_kv_heads != 0)
+    return fail(TQ_ERR_INVALID_ARG, "%s: num_q_heads %d not a multiple of num_kv_heads %d", fn, num_q_heads,
+                desc->num_kv_heads);
+  if (batch == 0) return TQ_OK;
+  if (batch > 65535) return fail(TQ_ERR_UNSUPPORTED, "%s: batch %d > 65535", fn, batch);
+  if (!valid_dtype(q_dtype) || !valid_dtype(out_dtype))
+    return fail(TQ_ERR_INVALID_ARG, "%s: q_dtype %d / out_dtype %d", fn, q_dtype, out_dtype);
+  if (!q || !out) return fail(TQ_ERR_INVALID_ARG, "%s: null q/out", fn);
+  if (!(sm_scale == sm_scale)) return fail(TQ_ERR_INVALID_ARG, "%s: sm_scale is NaN", fn);
+  if (reinterpret_cast<uintptr_t>(q) & 15) return fail(TQ_ERR_INVALID_ARG, "%s: q must be 16-byte aligned", fn);
+  DeviceInfo di;
+  if ((s = device_info(&di)) != TQ_OK) return s;
+  const size_t own = own_workspace(desc, batch, num_q_heads, max_blocks_per_seq);
+  const size_t need = own + prefix_partial_bytes(*desc, batch, num_q_heads, prefix_len, di.num_sms);
+  if (!workspace || workspace_bytes < need)
+    return fail(TQ_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, workspace_bytes, need);
+  if (reinterpret_cast<uintptr_t>(workspace) & 255)
+    return fail(TQ_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", fn);
+  PrefixCall c = {};
+  if (max_blocks_per_seq > 0) {
+    s = prepare_decode(desc, q, q_dtype, batch, num_q_heads, block_table, max_blocks_per_seq, context_lens, sm_scale,
+                       out, out_dtype, workspace, own, 0, fn, &c.own);
+    if (s != TQ_OK) return s;
+  } else {
+    c.own.desc = desc;
+    c.own.q = q;
+    c.own.q_dtype = q_dtype;
+    c.own.batch = batch;
+    c.own.num_q_heads = num_q_heads;
+    c.own.sm_scale = sm_scale;
+    c.own.out = out;
+    c.own.out_dtype = out_dtype;
+    c.own.workspace = reinterpret_cast<uint8_t*>(workspace);
+    c.own.status = di.status;
+  }
+  c.prefix_table = prefix_table;
+  c.prefix_len = prefix_len;
+  c.num_sms = di.num_sms;
+  return cuda_result(launch_prefix_decode(c, reinterpret_cast<cudaStream_t>(stream)), "prefix decode");
 }
 
 tq_status tq_dequantize(const tq_cache_desc* desc, int which, const int64_t* slots, int64_t n, void* out,

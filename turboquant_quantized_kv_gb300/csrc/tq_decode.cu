@@ -722,7 +722,12 @@ __device__ __forceinline__ void bf16_block(SoftmaxState<NT>& st, const WarpConst
     // coordinates [16 g_, 16 g_ + 16) of tokens ta + 8 kt (F) and tb + 8 kt (S)
     const uint4* rf = reinterpret_cast<const uint4*>(sv + (tok_a(tig) + 8 * kt) * RB + 32 * g_);
     const uint4* rs = reinterpret_cast<const uint4*>(sv + (tok_b(tig) + 8 * kt) * RB + 32 * g_);
-    const uint4 f0 = rf[0], f1 = rf[1], s0 = rs[0], s1 = rs[1];
+    uint4 f0 = rf[0], f1 = rf[1], s0 = rs[0], s1 = rs[1];
+    if (t0 + kBlock > ctx) {  // a weight of zero does not silence a NaN or an infinity past the context
+      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+      if (t0 + tok_a(tig) + 8 * kt >= ctx) f0 = f1 = zero;
+      if (t0 + tok_b(tig) + 8 * kt >= ctx) s0 = s1 = zero;
+    }
     const uint32_t wf[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
     const uint32_t ws[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
@@ -738,13 +743,6 @@ __device__ __forceinline__ void bf16_block(SoftmaxState<NT>& st, const WarpConst
 }
 
 // ------------------------------------------------------------ decode kernel
-
-// Live partial slots.  Chunk ch = unit * splits + s runs on CTA ch / NW; the
-// warps of one CTA that share a unit are merged into the slot of the first of
-// them, so slot s of a unit is live iff s == 0 or (unit * splits + s) % NW == 0.
-__device__ __forceinline__ bool slot_live(int unit, int splits, int s, int nw) {
-  return s == 0 || ((int64_t)unit * splits + s) % nw == 0;
-}
 
 // KIND 0: packed codes (BK, BV, QJL); KIND 1: bf16 pages.  NT n-tiles of 4 heads
 // per warp, NW warps per CTA, one CTA per SM holding all of the SM's shared memory.
@@ -1598,11 +1596,6 @@ __global__ void __launch_bounds__(kRotWarps * 32) k_rotate_q(const TQ* __restric
 
 // ------------------------------------------------------------- combine
 
-// Heads of a decode unit and the CTA width of the decode launch, for the live slots.
-struct UnitMap {
-  int Hq, Hkv, g, hpw, ngroups, nw;
-};
-
 template <typename TO>
 __global__ void __launch_bounds__(128) k_combine(const float* __restrict__ part, const float* __restrict__ ml,
                                                  int splits, UnitMap um, int kind, const float* __restrict__ rot,
@@ -1674,6 +1667,17 @@ int decode_warps(const tq_cache_desc& d, int g) {
   const bool k8 = d.fmt.kv_format == TQ_KV_K8V4;
   const bool qjl = d.fmt.kv_format == TQ_KV_PACKED && d.fmt.qjl_k;
   return decode_nw((d.fmt.kv_format == TQ_KV_PACKED && !d.fmt.qjl_k) || k8, g <= 4 ? 1 : 2, k8, qjl);
+}
+
+UnitMap unit_map(const tq_cache_desc& d, int num_q_heads) {
+  UnitMap um;
+  um.Hq = num_q_heads;
+  um.Hkv = d.num_kv_heads;
+  um.g = num_q_heads / d.num_kv_heads;
+  um.hpw = um.g <= 4 ? 4 : 8;
+  um.ngroups = (um.g + um.hpw - 1) / um.hpw;
+  um.nw = decode_warps(d, um.g);
+  return um;
 }
 
 template <int KIND, int BK, int BV, bool QJL, int NT>
@@ -1822,7 +1826,7 @@ cudaError_t launch_decode(const DecodeCall& c, cudaStream_t st) {
   // the decode kernel finishes the job itself (merge and inverse rotation) unless the
   // splits are too many for its merge or the dense rotation's rows are not 16-byte aligned
   const bool rot_aligned = (reinterpret_cast<uintptr_t>(d.rotation) & 15) == 0;
-  a.fuse_combine = (c.splits > kMaxFusedSplits || (kind == ROTQ_DENSE && !rot_aligned))
+  a.fuse_combine = (c.partials_only || c.splits > kMaxFusedSplits || (kind == ROTQ_DENSE && !rot_aligned))
                        ? 0
                        : (kind == ROTQ_HADAMARD ? 2 : (kind == ROTQ_DENSE ? 3 : 1));
   a.counters = counters;
@@ -1853,15 +1857,9 @@ cudaError_t launch_decode(const DecodeCall& c, cudaStream_t st) {
     }
   }
   if (e != cudaSuccess) return e;
-  if (a.fuse_combine) return cudaSuccess;
+  if (a.fuse_combine || c.partials_only) return cudaSuccess;
   const unsigned cgrid = (unsigned)rows;
-  UnitMap um;
-  um.Hq = a.Hq;
-  um.Hkv = a.Hkv;
-  um.g = a.g;
-  um.hpw = a.g <= 4 ? 4 : 8;
-  um.ngroups = a.ngroups;
-  um.nw = decode_warps(d, a.g);
+  const UnitMap um = unit_map(d, a.Hq);
   if (c.out_dtype == TQ_F32)
     k_combine<float><<<cgrid, 128, 0, st>>>(a.part, a.ml, c.splits, um, kind, d.rotation,
                                             reinterpret_cast<float*>(c.out));

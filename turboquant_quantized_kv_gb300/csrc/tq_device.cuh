@@ -19,6 +19,18 @@ struct Codebook {
   float b[15];
 };
 
+// Live partial slots of a decode.  Chunk ch = unit * splits + s runs on CTA ch / nw; the
+// warps of one CTA that share a unit are merged into the slot of the first of
+// them, so slot s of a unit is live iff s == 0 or (unit * splits + s) % nw == 0.
+__device__ __forceinline__ bool slot_live(int unit, int splits, int s, int nw) {
+  return s == 0 || ((int64_t)unit * splits + s) % nw == 0;
+}
+
+// Heads of a decode unit and the CTA width of the decode launch, for the live slots.
+struct UnitMap {
+  int Hq, Hkv, g, hpw, ngroups, nw;
+};
+
 __device__ __forceinline__ void flag_status(unsigned* status, unsigned bits) {
   if (status) atomicOr(status, bits);
 }

@@ -289,6 +289,66 @@ tq_status tq_make_rotation(int kind, int head_dim, uint64_t seed, int layer, flo
   return fail(TQ_ERR_INVALID_ARG, "tq_make_rotation: unknown kind %d", kind);
 }
 
+// The fraction of a turn a pair advances a position, in 2^-64 turns.
+static uint64_t turns_of(double radians) {
+  double t = radians / 6.283185307179586476925286766559;
+  t -= std::floor(t);
+  const double scaled = std::nearbyint(std::ldexp(t, 64));
+  return scaled >= 0x1.0p64 ? 0u : (uint64_t)scaled;
+}
+
+tq_status tq_make_rope(int layout, int rotary_dim, double base, const tq_rope_scaling* scaling,
+                       const double* inv_freq, tq_rope* out) {
+  clear_error();
+  if (!out) return fail(TQ_ERR_INVALID_ARG, "tq_make_rope: null output");
+  if (layout != TQ_ROPE_HALF && layout != TQ_ROPE_INTERLEAVED)
+    return fail(TQ_ERR_INVALID_ARG, "tq_make_rope: layout %d", layout);
+  if (rotary_dim < 2 || rotary_dim > TQ_HEAD_DIM || rotary_dim % 2 != 0)
+    return fail(TQ_ERR_INVALID_ARG, "tq_make_rope: rotary_dim %d is not even in [2, %d]", rotary_dim, TQ_HEAD_DIM);
+  if (!inv_freq && !(base > 1.0 && std::isfinite(base)))
+    return fail(TQ_ERR_INVALID_ARG, "tq_make_rope: base %g must be above 1", base);
+  const tq_rope_scaling none = {TQ_ROPE_SCALE_NONE, 1.0, 0.0, 0.0, 0.0};
+  const tq_rope_scaling& s = scaling ? *scaling : none;
+  if (s.kind < TQ_ROPE_SCALE_NONE || s.kind > TQ_ROPE_SCALE_YARN)
+    return fail(TQ_ERR_INVALID_ARG, "tq_make_rope: scaling kind %d", s.kind);
+  if (inv_freq && s.kind != TQ_ROPE_SCALE_NONE)
+    return fail(TQ_ERR_INVALID_ARG, "tq_make_rope: explicit frequencies take no scaling");
+  if (s.kind != TQ_ROPE_SCALE_NONE && !(s.factor >= 1.0 && std::isfinite(s.factor)))
+    return fail(TQ_ERR_INVALID_ARG, "tq_make_rope: scaling factor %g must be at least 1", s.factor);
+  if ((s.kind == TQ_ROPE_SCALE_BANDED || s.kind == TQ_ROPE_SCALE_YARN) &&
+      !(s.low > 0.0 && s.high > s.low && std::isfinite(s.high) && s.length > 0.0 && std::isfinite(s.length)))
+    return fail(TQ_ERR_INVALID_ARG, "tq_make_rope: scaling needs 0 < low < high and length > 0");
+  const int pairs = rotary_dim / 2;
+  const double two_pi = 6.283185307179586476925286766559;
+  for (int i = 0; inv_freq && i < pairs; ++i)
+    if (!std::isfinite(inv_freq[i])) return fail(TQ_ERR_INVALID_ARG, "tq_make_rope: frequency %d is not finite", i);
+  if (s.kind == TQ_ROPE_SCALE_NTK && rotary_dim > 2)
+    base *= std::pow(s.factor, (double)rotary_dim / (rotary_dim - 2.0));
+  double lo = 0.0, hi = 0.0;
+  if (s.kind == TQ_ROPE_SCALE_YARN) {  // the pairs that turn s.high and s.low times in s.length positions
+    lo = std::floor(rotary_dim * std::log(s.length / (two_pi * s.high)) / (2.0 * std::log(base)));
+    hi = std::ceil(rotary_dim * std::log(s.length / (two_pi * s.low)) / (2.0 * std::log(base)));
+    lo = lo < 0.0 ? 0.0 : lo;
+    hi = hi > rotary_dim - 1.0 ? rotary_dim - 1.0 : hi;
+  }
+  tq_rope r = {};
+  r.layout = layout;
+  r.rotary_dim = rotary_dim;
+  r.amplitude = s.kind == TQ_ROPE_SCALE_YARN ? (float)(0.1 * std::log(s.factor) + 1.0) : 1.0f;
+  for (int i = 0; i < pairs; ++i) {
+    double f = inv_freq ? inv_freq[i] : std::pow(base, -2.0 * i / rotary_dim);
+    double keep = 1.0;  // share of the unscaled frequency
+    if (s.kind == TQ_ROPE_SCALE_LINEAR) keep = 0.0;
+    if (s.kind == TQ_ROPE_SCALE_BANDED) keep = (s.length * f / two_pi - s.low) / (s.high - s.low);
+    if (s.kind == TQ_ROPE_SCALE_YARN) keep = 1.0 - (i - lo) / (hi - lo > 0.001 ? hi - lo : 0.001);
+    keep = keep < 0.0 ? 0.0 : (keep > 1.0 ? 1.0 : keep);
+    if (keep < 1.0) f = (1.0 - keep) * f / s.factor + keep * f;
+    r.turns[i] = turns_of(f);
+  }
+  *out = r;
+  return TQ_OK;
+}
+
 size_t tq_page_bytes(const tq_cache_desc* desc, int which) {
   if (check_desc(desc, false) != TQ_OK || (which != 0 && which != 1)) return 0;
   return page_bytes_of(*desc, which);

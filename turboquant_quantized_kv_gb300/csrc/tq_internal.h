@@ -68,7 +68,34 @@ struct DecodeCall {
   const void* new_k = nullptr;
   const void* new_v = nullptr;
   int new_dtype = 0;
+  // the chunks' partials stay in the workspace for the caller to merge (live slots as
+  // slot_live says); out is not written
+  bool partials_only = false;
 };
+
+// One validated call of tq_rope_apply or tq_rope_append, as the launchers see it.
+struct RopeCall {
+  const tq_rope* rope;
+  int transpose;
+  int dtype;
+  const tq_heads* heads[3];  // queries, keys, values (null: none)
+  const int64_t* positions;
+  const int64_t* slots;  // append only
+  int64_t n_tokens;
+  unsigned* status;
+  int num_sms;
+};
+
+// One validated call of tq_prefix_decode: `own` holds the arguments of the sequences'
+// own tokens (own.max_blocks == 0: none) and the workspace.
+struct PrefixCall {
+  DecodeCall own;
+  const int32_t* prefix_table;
+  int64_t prefix_len;
+  int num_sms;
+};
+// Bytes of the prefix's partials, which follow the workspace of the own tokens' decode.
+size_t prefix_partial_bytes(const tq_cache_desc& d, int batch, int num_q_heads, int64_t prefix_len, int num_sms);
 
 // True if the append quantizer's cell table can hold these (ascending) boundaries:
 // each boundary in a cell of its own (cells are 1/63 wide on [-1, 1]).
@@ -89,6 +116,9 @@ cudaError_t launch_quantize(const tq_cache_desc& d, int which, const void* x, in
 cudaError_t launch_dequant(const tq_cache_desc& d, int which, const int64_t* slots, int64_t n, void* out,
                            int out_dtype, unsigned* status, int num_sms, cudaStream_t st);
 cudaError_t launch_decode(const DecodeCall& c, cudaStream_t st);
+cudaError_t launch_prefix_decode(const PrefixCall& c, cudaStream_t st);
+cudaError_t launch_rope_apply(const RopeCall& c, cudaStream_t st);
+cudaError_t launch_rope_append(const RopeCall& c, const tq_cache_desc& d, cudaStream_t st);
 // Polar layers (tq_polar.cu); the generic launchers above route them here.
 cudaError_t launch_polar_append(const tq_cache_desc& d, int which, const void* x, int in_dtype,
                                 const int64_t* slots, int64_t n_tok, unsigned* status, int num_sms, cudaStream_t st);

@@ -1,0 +1,635 @@
+// Rotary positions and the rotated append (libtq, sm_103a).
+//
+// A head of 128 coordinates carries rotary_dim / 2 pairs (x_a, x_b); token t at
+// position p turns pair i by the angle p f_i:
+//     y_a = A (x_a cos - x_b sin),   y_b = A (x_b cos + x_a sin)
+// (the transposed rotation has -sin).  Pairs are (i, i + rotary_dim / 2) in the half
+// layout and (2 i, 2 i + 1) in the interleaved one; coordinates from rotary_dim on
+// pass through.
+//
+// The angle.  f_i is held as a 64-bit fraction of a turn, so p f_i modulo one turn
+// is one wrapping 64-bit product: the angle of a position of a million is as exact as
+// that of position one.  The top 32 bits become a fraction of a half turn in fp32
+// (rounded to 2^-25 half turns, about 1e-7 rad) for sincospif.
+//
+// Kernels:
+//   k_rope_apply   query and key rows; a CTA takes tiles of tokens, its threads first
+//                  form the tile's cosines and sines in shared memory (once a token,
+//                  not once a head) and then rotate 16 coordinates an item.
+//   k_rope_append  the same rows path for the queries and for keys and values that are
+//                  stored as bf16 or FP8, and a second kind of CTA for keys and values
+//                  stored as codes: four lanes a vector, the rotation in registers
+//                  between the load and the quantizer.
+// Both read and write each element once: what bounds them is memory bandwidth.
+#include <cuda_fp8.h>
+
+#include <cmath>
+
+#include "tq_cells.cuh"
+#include "tq_device.cuh"
+#include "tq_internal.h"
+
+namespace tq {
+
+constexpr int kRThreads = 256;
+constexpr int kPairs = kD / 2;
+constexpr int kVecTile = kRThreads / 4;  // coded vectors per tile: four lanes each
+
+// Where rows of one tensor come from and go to.
+struct RopeRows {
+  const void* in;
+  void* out;  // rotated rows (may equal in; null: none)
+  int64_t in_tok, in_head, out_tok, out_head;  // strides in elements
+  uint8_t* pool;  // pages the rows are stored in as well (null: none)
+  int page;       // 0: none, 1: bf16 pages, 2: FP8 pages
+  int heads;
+  int rotate;
+};
+
+struct RopeArgs {
+  uint64_t turns[kPairs];  // frequency of each pair, in 2^-64 turns a position
+  float amplitude;
+  int pairs;        // rotary_dim / 2
+  int interleaved;
+  int transpose;
+  const int64_t* positions;
+  int64_t n_tok;
+  // rows part
+  RopeRows rows[3];
+  int n_rows;       // tensors
+  int heads;        // of all of them
+  int tile_tok;     // tokens a tile
+  unsigned row_blocks;  // CTAs of the rows part, after the coded part's
+  // coded part: keys (0) and values (1)
+  const int64_t* slots;
+  int64_t max_slot;
+  struct Coded {
+    const void* in;
+    int64_t in_tok, in_head;
+    void* out;        // rotated rows as well (null: none)
+    int64_t out_tok, out_head;
+    uint8_t* pool;
+    int page_bytes;
+    int bits;
+    int rotate;
+    unsigned blocks;  // CTAs
+    Codebook cb;
+  } coded[2];
+  int coded_tok;  // tokens a tile of coded vectors can touch
+  int kv_heads;
+  const float* signs;
+  int norm_raw;
+  unsigned* status;
+};
+
+// cos and sin of position * turns, times the amplitude.
+__device__ __forceinline__ float2 turn_of(uint64_t turns, int64_t position, float amplitude, bool transpose) {
+  const int hi = (int)(uint32_t)(((uint64_t)position * turns) >> 32);  // signed: [-1/2, 1/2) turn
+  float s, c;
+  sincospif((float)hi * 0x1.0p-31f, &s, &c);
+  return make_float2(c * amplitude, (transpose ? -s : s) * amplitude);
+}
+
+// One pair turned; the products and the sum are spelled out so that every path rounds alike.
+__device__ __forceinline__ void turn_pair(float& x0, float& x1, const float2& t) {
+  const float u = __fmaf_rn(x0, t.x, -__fmul_rn(x1, t.y));
+  x1 = __fmaf_rn(x1, t.x, __fmul_rn(x0, t.y));
+  x0 = u;
+}
+
+// Eight consecutive elements as fp32.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&x)[8]);
+template <>
+__device__ __forceinline__ void load8<float>(const float* p, float (&x)[8]) {
+  const float4 u = reinterpret_cast<const float4*>(p)[0], v = reinterpret_cast<const float4*>(p)[1];
+  x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+  x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+}
+template <>
+__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&x)[8]) {
+  const uint4 v = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    x[2 * k] = __uint_as_float(w[k] << 16);
+    x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&x)[8]);
+template <>
+__device__ __forceinline__ void store8<float>(float* p, const float (&x)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+template <>
+__device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const float (&x)[8]) {
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
+}
+__device__ __forceinline__ uint32_t fp8_pair(float lo, float hi) {
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+// One item of the rows part: W = 8 pairs (16 coordinates in two runs of eight, aligned) or
+// one pair, of one head of one token.
+template <typename T, int W>
+struct RowItem {
+  float a[W], b[W];  // the pairs' coordinates (or 2 W coordinates that pass through)
+  int oa, ob;        // their places in the head (interleaved: run starts, W = 8)
+  int pair;          // first pair, or -1: not rotated
+};
+
+template <typename T, int W>
+__device__ __forceinline__ void item_load(RowItem<T, W>& it, const T* head, int c, int pairs, bool interleaved) {
+  if (W == 8) {
+    if (interleaved) {
+      it.oa = 16 * c;
+      it.ob = 16 * c + 8;
+      it.pair = 8 * c < pairs ? 8 * c : -1;
+    } else if (8 * c < pairs) {
+      it.oa = 8 * c;
+      it.ob = pairs + 8 * c;
+      it.pair = 8 * c;
+    } else {
+      it.oa = 16 * c;  // the head's coordinates from 2 pairs on, 16 an item
+      it.ob = 16 * c + 8;
+      it.pair = -1;
+    }
+    if constexpr (W == 8) {
+      load8<T>(head + it.oa, it.a);
+      load8<T>(head + it.ob, it.b);
+    }
+  } else {
+    const bool live = c < pairs;
+    it.oa = (interleaved || !live) ? 2 * c : c;
+    it.ob = (interleaved || !live) ? 2 * c + 1 : c + pairs;
+    it.pair = live ? c : -1;
+    it.a[0] = load_elem<T>(head + it.oa);
+    it.b[0] = load_elem<T>(head + it.ob);
+  }
+}
+
+template <typename T, int W>
+__device__ __forceinline__ void item_rotate(RowItem<T, W>& it, const float2* cs, int pairs, bool interleaved) {
+  if (it.pair < 0) return;
+  if (W == 8 && interleaved) {  // a: pairs 0..3 of the item, b: pairs 4..7
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      if (it.pair + k < pairs) {
+        const float2 t = cs[it.pair + k];
+        float& x0 = k < 4 ? it.a[(2 * k) % W] : it.b[(2 * k) % W];
+        float& x1 = k < 4 ? it.a[(2 * k + 1) % W] : it.b[(2 * k + 1) % W];
+        turn_pair(x0, x1, t);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      turn_pair(it.a[k], it.b[k], cs[it.pair + k]);
+    }
+  }
+}
+
+template <typename T, int W>
+__device__ __forceinline__ void item_store(const RowItem<T, W>& it, T* head) {
+  if constexpr (W == 8) {
+    store8<T>(head + it.oa, it.a);
+    store8<T>(head + it.ob, it.b);
+  } else {
+    store_elem<T>(head + it.oa, it.a[0]);
+    store_elem<T>(head + it.ob, it.b[0]);
+  }
+}
+
+// The item in its record of a page: bf16 rounded to nearest, FP8 E4M3 saturating.
+template <typename T, int W>
+__device__ __forceinline__ void item_store_page(const RowItem<T, W>& it, uint8_t* pool, int page, int64_t slot, int head,
+                                                int heads) {
+  const int64_t row = ((slot >> 4) * heads + head) * kBlock + (slot & 15);
+  if (page == 1) {
+    __nv_bfloat16* r = reinterpret_cast<__nv_bfloat16*>(pool) + row * kD;
+    if constexpr (W == 8) {
+      store8<__nv_bfloat16>(r + it.oa, it.a);
+      store8<__nv_bfloat16>(r + it.ob, it.b);
+    } else {
+      r[it.oa] = __float2bfloat16_rn(it.a[0]);
+      r[it.ob] = __float2bfloat16_rn(it.b[0]);
+    }
+  } else {
+    uint8_t* r = pool + row * kD;
+    if constexpr (W == 8) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float(&x)[8] = h ? it.b : it.a;
+        *reinterpret_cast<uint2*>(r + (h ? it.ob : it.oa)) =
+            make_uint2(fp8_pair(x[0], x[1]) | (fp8_pair(x[2], x[3]) << 16), fp8_pair(x[4], x[5]) | (fp8_pair(x[6], x[7]) << 16));
+      }
+    } else {
+      const uint32_t two = fp8_pair(it.a[0], it.b[0]);
+      r[it.oa] = (uint8_t)two;
+      r[it.ob] = (uint8_t)(two >> 8);
+    }
+  }
+}
+
+// Tiles of tokens: cosines and sines to shared memory, then the items of all heads.
+template <typename T, int W>
+__device__ __forceinline__ void rope_rows(const RopeArgs& a, unsigned block, unsigned blocks, float2* cs,
+                                          const uint64_t* turns) {
+  constexpr int PER = kPairs / W;  // items per head
+  const int tid = threadIdx.x;
+  const int64_t tiles = (a.n_tok + a.tile_tok - 1) / a.tile_tok;
+  const bool inter = a.interleaved != 0;
+  for (int64_t tile = block; tile < tiles; tile += blocks) {
+    const int64_t t0 = tile * a.tile_tok;
+    const int nt = (int)min((int64_t)a.tile_tok, a.n_tok - t0);
+    __syncthreads();  // the table of the previous tile is no longer read
+    for (int i = tid; i < nt * kPairs; i += kRThreads) {
+      const int p = i & (kPairs - 1);
+      if (p < a.pairs) cs[i] = turn_of(turns[p], __ldg(a.positions + t0 + i / kPairs), a.amplitude, a.transpose);
+    }
+    __syncthreads();
+    const int items = nt * a.heads * PER;
+    for (int i = tid; i < items; i += kRThreads) {
+      const int c = i % PER, th = i / PER;
+      const int lt = th / a.heads;
+      int h = th - lt * a.heads, s = 0;
+      while (s + 1 < a.n_rows && h >= a.rows[s].heads) h -= a.rows[s++].heads;
+      const RopeRows& r = a.rows[s];
+      const int64_t tok = t0 + lt;
+      RowItem<T, W> it;
+      item_load<T, W>(it, reinterpret_cast<const T*>(r.in) + tok * r.in_tok + h * r.in_head, c, r.rotate ? a.pairs : 0,
+                      inter);
+      item_rotate<T, W>(it, cs + lt * kPairs, a.pairs, inter);
+      if (r.out) item_store<T, W>(it, reinterpret_cast<T*>(r.out) + tok * r.out_tok + h * r.out_head);
+      if (r.page) {
+        const int64_t slot = __ldg(a.slots + tok);
+        if (slot >= a.max_slot) {
+          if (c == 0) flag_status(a.status, TQ_DEV_BAD_SLOT);
+        } else if (slot >= 0) {
+          item_store_page<T, W>(it, r.pool, r.page, slot, h, a.kv_heads);
+        }
+      }
+    }
+  }
+}
+
+// One coded tensor: a quad of lanes a vector.  Lane q holds coordinates [16 q, 16 q + 16)
+// and [64 + 16 q, 64 + 16 q + 16): the pairs of a full rotation in either layout lie in
+// one lane, and the butterfly over them is the quad transform with the coordinate's bits
+// 0..3 and 6 inside the lane and bits 4 and 5 across lanes.
+template <typename T, int BITS>
+__device__ __forceinline__ void rope_coded(const RopeArgs& a, const RopeArgs::Coded& t, unsigned block, float2* cs,
+                                           const uint64_t* turns, const uint32_t* signw, uint32_t qtab_addr) {
+  constexpr int R = 16 * BITS;
+  const int tid = threadIdx.x, lane = tid & 31, q = tid & 3, vl = tid >> 2;
+  const int H = a.kv_heads;
+  const uint32_t qrow_addr = qtab_addr | (16u * (uint32_t)(lane & 7));
+  const uint32_t sw = ((signw[q >> 1] >> (16 * (q & 1))) & 0xFFFFu) | ((signw[2 + (q >> 1)] >> (16 * (q & 1))) << 16);
+  const int64_t n_vec = a.n_tok * H;
+  const int64_t tiles = (n_vec + kVecTile - 1) / kVecTile;
+  const bool aligned = ((reinterpret_cast<uintptr_t>(t.in) | (t.in_tok * sizeof(T)) | (t.in_head * sizeof(T))) & 15) == 0;
+  const bool out_aligned =
+      ((reinterpret_cast<uintptr_t>(t.out) | (t.out_tok * sizeof(T)) | (t.out_head * sizeof(T))) & 15) == 0;
+  for (int64_t tile = block; tile < tiles; tile += t.blocks) {
+    const int64_t v0 = tile * kVecTile;
+    const int64_t t0 = v0 / H;  // first token of the tile
+    const int64_t vec_raw = v0 + vl;
+    const bool valid = vec_raw < n_vec;
+    const int64_t vec = valid ? vec_raw : n_vec - 1;
+    const int64_t tok = vec / H;
+    const int head = (int)(vec - tok * H);
+    const T* src = reinterpret_cast<const T*>(t.in) + tok * t.in_tok + head * t.in_head;
+    float x[32];
+    if (aligned) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float v[8];
+        load8<T>(src + 64 * (r >> 1) + 16 * q + 8 * (r & 1), v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[8 * r + k] = v[k];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = load_elem<T>(src + 64 * (i >> 4) + 16 * q + (i & 15));
+    }
+    const int64_t slot = __ldg(a.slots + tok);
+    if (t.rotate) {
+      __syncthreads();  // the table of the previous tile is no longer read
+      const int nt = (int)min((int64_t)a.coded_tok, a.n_tok - t0);
+      for (int i = tid; i < nt * kPairs; i += kRThreads) {
+        const int p = i & (kPairs - 1);
+        if (p < a.pairs) cs[i] = turn_of(turns[p], __ldg(a.positions + t0 + i / kPairs), a.amplitude, a.transpose);
+      }
+      __syncthreads();
+      const float2* ct = cs + (tok - t0) * kPairs;
+      if (a.interleaved) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int p = 32 * (i >> 3) + 8 * q + (i & 7);
+          if (p < a.pairs) turn_pair(x[2 * i], x[2 * i + 1], ct[p]);
+        }
+      } else if (a.pairs == kPairs) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          turn_pair(x[i], x[16 + i], ct[16 * q + i]);
+        }
+      } else {  // part of the head: a coordinate's partner may be another lane's; read again (from L1)
+        const int rot = 2 * a.pairs;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const int j = 64 * (i >> 4) + 16 * q + (i & 15);
+          if (j < rot) {
+            const bool low = j < a.pairs;
+            const float2 c = ct[low ? j : j - a.pairs];
+            const float o = load_elem<T>(src + (low ? j + a.pairs : j - a.pairs));
+            x[i] = __fmaf_rn(x[i], c.x, low ? -__fmul_rn(o, c.y) : __fmul_rn(o, c.y));
+          }
+        }
+      }
+      __syncwarp();  // (out may be in: every partner has been read)
+      if (t.out && valid) {
+        T* dst = reinterpret_cast<T*>(t.out) + tok * t.out_tok + head * t.out_head;
+        if (out_aligned) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = x[8 * r + k];
+            store8<T>(dst + 64 * (r >> 1) + 16 * q + 8 * (r & 1), v);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) store_elem<T>(dst + 64 * (i >> 4) + 16 * q + (i & 15), x[i]);
+        }
+      }
+    }
+    float2 ss = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float2 xi = make_float2(x[2 * i], x[2 * i + 1]);
+      ss = __ffma2_rn(xi, xi, ss);
+    }
+    const float n = sqrtf(quad_sum(ss.x + ss.y));
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = flip_sign(x[i], sw, i);
+    fwht128_quad_f2(x, q);  // H D x = sqrt(d) Pi x
+    const float inv_n = n > 0.0f ? 0.08838834764831845f / n : 0.0f;  // 1 / sqrt(128) folded in
+    uint32_t code[32];
+    float2 c2v = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const float2 y = __fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(inv_n, inv_n));
+      const float4 e0 = lds128f((qcell_bits(y.x) & kQRowMask) | qrow_addr);
+      const float4 e1 = lds128f((qcell_bits(y.y) & kQRowMask) | qrow_addr);
+      const bool up0 = y.x >= e0.x, up1 = y.y >= e1.x;
+      code[i] = __float_as_uint(e0.w) + (up0 ? 1u : 0u);
+      code[i + 1] = __float_as_uint(e1.w) + (up1 ? 1u : 0u);
+      c2v = __fadd2_rn(c2v, make_float2(up0 ? e0.z : e0.y, up1 ? e1.z : e1.y));
+    }
+    const float c2 = quad_sum(c2v.x + c2v.y);
+    const float gamma = a.norm_raw ? n : ((n > 0.0f && c2 > 0.0f) ? n / sqrtf(c2) : 0.0f);
+    if (valid && slot >= a.max_slot) {
+      if (q == 0) flag_status(a.status, TQ_DEV_BAD_SLOT);
+    } else if (valid && slot >= 0) {
+      uint8_t* page = t.pool + ((slot >> 4) * H + head) * (int64_t)t.page_bytes;
+      const int off = (int)(slot & 15);
+      uint32_t w[BITS];
+      pack32<BITS>(code, w);  // the low half: codes of the first run, the high half: of the second
+      uint8_t* rec = page + off * R + 2 * BITS * q;
+      if constexpr (BITS == 4) {
+        *reinterpret_cast<uint2*>(rec) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2*>(rec + R / 2) = make_uint2(w[2], w[3]);
+      } else if constexpr (BITS == 2) {
+        *reinterpret_cast<uint32_t*>(rec) = w[0];
+        *reinterpret_cast<uint32_t*>(rec + R / 2) = w[1];
+      } else {  // 48 bits a run
+        uint16_t* lo = reinterpret_cast<uint16_t*>(rec);
+        uint16_t* hi = reinterpret_cast<uint16_t*>(rec + R / 2);
+        lo[0] = (uint16_t)w[0]; lo[1] = (uint16_t)(w[0] >> 16); lo[2] = (uint16_t)w[1];
+        hi[0] = (uint16_t)(w[1] >> 16); hi[1] = (uint16_t)w[2]; hi[2] = (uint16_t)(w[2] >> 16);
+      }
+      if (q == 0) *reinterpret_cast<float*>(page + 16 * R + 4 * off) = gamma;
+    }
+  }
+}
+
+template <typename T, int W>
+__global__ void __launch_bounds__(kRThreads) k_rope_apply(const __grid_constant__ RopeArgs a) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  uint64_t* turns = reinterpret_cast<uint64_t*>(smem_raw);
+  if (threadIdx.x < kPairs) turns[threadIdx.x] = a.turns[threadIdx.x];
+  rope_rows<T, W>(a, blockIdx.x, gridDim.x, reinterpret_cast<float2*>(smem_raw + kPairs * 8), turns);
+}
+
+// CTAs [0, coded[0].blocks): coded keys; then coded[1].blocks of coded values; then the rows.
+template <typename T, int W>
+__global__ void __launch_bounds__(kRThreads, 3) k_rope_append(const __grid_constant__ RopeArgs a, int cs_tokens) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // a dependent decode may start its prologue
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  __shared__ uint32_t signw[4];
+  uint64_t* turns = reinterpret_cast<uint64_t*>(smem_raw);
+  float2* cs = reinterpret_cast<float2*>(smem_raw + kPairs * 8);
+  if (threadIdx.x < kPairs) turns[threadIdx.x] = a.turns[threadIdx.x];
+  unsigned block = blockIdx.x;
+  int which = 0;
+  if (block >= a.coded[0].blocks) {
+    block -= a.coded[0].blocks;
+    which = 1;
+    if (block >= a.coded[1].blocks) {
+      rope_rows<T, W>(a, block - a.coded[1].blocks, a.row_blocks, cs, turns);
+      return;
+    }
+  }
+  const RopeArgs::Coded& t = a.coded[which];
+  // the cell table at the first 16 KB aligned shared address past the cosines
+  const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem_raw);
+  const uint32_t qtab_addr = (base + kPairs * 8 + (uint32_t)cs_tokens * kPairs * 8 + 16383u) & ~16383u;
+  float4* qtab = reinterpret_cast<float4*>(smem_raw + (qtab_addr - base));
+  const int tid = threadIdx.x;
+  if (tid < 32) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t m = __ballot_sync(0xffffffffu, __ldg(a.signs + 32 * k + tid) < 0.0f);
+      if (tid == 0) signw[k] = m;
+    }
+  }
+  if (t.bits == 4) build_cell_table<4>(t.cb, qtab, tid);
+  else if (t.bits == 3) build_cell_table<3>(t.cb, qtab, tid);
+  else build_cell_table<2>(t.cb, qtab, tid);
+  __syncthreads();
+  if (t.bits == 4) rope_coded<T, 4>(a, t, block, cs, turns, signw, qtab_addr);
+  else if (t.bits == 3) rope_coded<T, 3>(a, t, block, cs, turns, signw, qtab_addr);
+  else rope_coded<T, 2>(a, t, block, cs, turns, signw, qtab_addr);
+}
+
+// ----------------------------------------------------------------- launchers
+
+Codebook codebook_of(const tq_cache_desc& d, int which);
+
+static RopeRows rows_of(const tq_heads& h, bool rotate) {
+  RopeRows r = {};
+  r.in = h.in;
+  r.out = h.out;
+  r.in_tok = h.in_token_stride;
+  r.in_head = h.in_head_stride;
+  r.out_tok = h.out_token_stride;
+  r.out_head = h.out_head_stride;
+  r.heads = h.num_heads;
+  r.rotate = rotate ? 1 : 0;
+  return r;
+}
+
+// Eight pairs an item need 16-byte aligned runs: bases, strides and the half layout's
+// second half on 16-byte boundaries.  Otherwise one pair an item.
+static bool wide_rows(const RopeArgs& a, int elem) {
+  if (!a.interleaved && a.pairs % 8 != 0) return false;
+  for (int s = 0; s < a.n_rows; ++s) {
+    const RopeRows& r = a.rows[s];
+    uintptr_t bits = reinterpret_cast<uintptr_t>(r.in) | (uintptr_t)(r.in_tok * elem) | (uintptr_t)(r.in_head * elem);
+    if (r.out)
+      bits |= reinterpret_cast<uintptr_t>(r.out) | (uintptr_t)(r.out_tok * elem) | (uintptr_t)(r.out_head * elem);
+    if (bits & 15) return false;
+  }
+  return true;
+}
+
+static void fill_common(RopeArgs& a, const RopeCall& c) {
+  for (int i = 0; i < kPairs; ++i) a.turns[i] = c.rope->turns[i];
+  a.amplitude = c.rope->amplitude;
+  a.pairs = c.rope->rotary_dim / 2;
+  a.interleaved = c.rope->layout == TQ_ROPE_INTERLEAVED ? 1 : 0;
+  a.transpose = c.transpose;
+  a.positions = c.positions;
+  a.n_tok = c.n_tokens;
+  a.slots = c.slots;
+  a.status = c.status;
+}
+
+// Tokens a tile of the rows part: enough items for the CTA's threads to have four each,
+// one token while the tiles would not fill the GPU.
+static int rows_tile(const RopeArgs& a, int num_sms) {
+  int t = 1;
+  while (t < 8 && t * a.heads * (kPairs / 8) < 4 * kRThreads && a.n_tok / (2 * t) >= 8 * (int64_t)num_sms) t *= 2;
+  return t;
+}
+
+template <typename T>
+static cudaError_t run_apply(const RopeArgs& a, int num_sms, cudaStream_t st) {
+  const bool wide = wide_rows(a, (int)sizeof(T));
+  auto kern = wide ? k_rope_apply<T, 8> : k_rope_apply<T, 1>;
+  const size_t smem = kPairs * 8 + (size_t)a.tile_tok * kPairs * 8;
+  kern<<<a.row_blocks, kRThreads, smem, st>>>(a);
+  count_launch();
+  return cudaGetLastError();
+}
+
+cudaError_t launch_rope_apply(const RopeCall& c, cudaStream_t st) {
+  RopeArgs a = {};
+  fill_common(a, c);
+  for (int s = 0; s < 2; ++s)
+    if (c.heads[s] && c.heads[s]->num_heads > 0) {
+      a.rows[a.n_rows++] = rows_of(*c.heads[s], true);
+      a.heads += c.heads[s]->num_heads;
+    }
+  a.tile_tok = rows_tile(a, c.num_sms);
+  const int64_t tiles = (a.n_tok + a.tile_tok - 1) / a.tile_tok;
+  const int64_t cap = (int64_t)c.num_sms * 8;
+  a.row_blocks = (unsigned)(tiles < cap ? tiles : cap);
+  return c.dtype == TQ_F32 ? run_apply<float>(a, c.num_sms, st) : run_apply<__nv_bfloat16>(a, c.num_sms, st);
+}
+
+template <typename T>
+static cudaError_t run_append(const RopeArgs& a, unsigned grid, cudaStream_t st) {
+  const bool wide = wide_rows(a, (int)sizeof(T));
+  auto kern = wide ? k_rope_append<T, 8> : k_rope_append<T, 1>;
+  const bool coded = a.coded[0].blocks + a.coded[1].blocks > 0;
+  const int tok = (coded && a.coded_tok > a.tile_tok) ? a.coded_tok : a.tile_tok;
+  const size_t smem = kPairs * 8 + (size_t)tok * kPairs * 8 + (coded ? 16384 + kLutQBytes : 0);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kRThreads, smem, st>>>(a, tok);
+  count_launch();
+  return cudaGetLastError();
+}
+
+cudaError_t launch_rope_append(const RopeCall& c, const tq_cache_desc& d, cudaStream_t st) {
+  RopeArgs a = {};
+  fill_common(a, c);
+  a.max_slot = d.num_blocks * kBlock;
+  a.kv_heads = d.num_kv_heads;
+  a.signs = d.rotation;
+  a.norm_raw = d.fmt.norm_mode == TQ_NORM_RAW ? 1 : 0;
+  const int fmt = d.fmt.kv_format;
+  if (c.heads[0]) {
+    a.rows[a.n_rows++] = rows_of(*c.heads[0], true);
+    a.heads += c.heads[0]->num_heads;
+  }
+  int64_t coded_tensors = 0;
+  for (int which = 0; which < 2; ++which) {
+    const tq_heads* h = c.heads[1 + which];
+    if (!h) continue;
+    uint8_t* pool = reinterpret_cast<uint8_t*>(which == 0 ? d.k_cache : d.v_cache);
+    if (fmt == TQ_KV_PACKED || (fmt == TQ_KV_K8V4 && which == 1)) {
+      RopeArgs::Coded& t = a.coded[which];
+      t.in = h->in;
+      t.in_tok = h->in_token_stride;
+      t.in_head = h->in_head_stride;
+      t.out = which == 0 ? h->out : nullptr;
+      t.out_tok = h->out_token_stride;
+      t.out_head = h->out_head_stride;
+      t.pool = pool;
+      t.page_bytes = (int)page_bytes_of(d, which);
+      t.bits = which == 0 ? d.fmt.bits_k : d.fmt.bits_v;
+      t.rotate = which == 0 ? 1 : 0;
+      t.cb = codebook_of(d, which);
+      t.blocks = 1;
+      ++coded_tensors;
+    } else {
+      RopeRows r = rows_of(*h, which == 0);
+      if (which == 1) r.out = nullptr;
+      r.pool = pool;
+      r.page = fmt == TQ_KV_BF16 ? 1 : 2;
+      a.rows[a.n_rows++] = r;
+      a.heads += h->num_heads;
+    }
+  }
+  a.tile_tok = a.n_rows ? rows_tile(a, c.num_sms) : 1;
+  const int64_t n_vec = c.n_tokens * d.num_kv_heads;
+  const int64_t vec_tiles = (n_vec + kVecTile - 1) / kVecTile;
+  const int64_t row_tiles = a.n_rows ? (c.n_tokens + a.tile_tok - 1) / a.tile_tok : 0;
+  // three CTAs an SM; when there are more tiles than that, the CTAs are shared out by
+  // estimated time: a coded vector about as long as one and a half rows of a query
+  const int64_t cap = (int64_t)c.num_sms * 3;
+  int64_t coded_blocks = vec_tiles, row_blocks = row_tiles;
+  if (coded_tensors * vec_tiles + row_tiles > cap) {
+    const double wc = 1.5 * (double)coded_tensors * d.num_kv_heads, wr = a.heads;
+    const double share = wc / (wc + wr);
+    if (coded_tensors) {
+      coded_blocks = (int64_t)(share * (double)cap / (double)coded_tensors);
+      if (coded_blocks < 1) coded_blocks = 1;
+      if (coded_blocks > vec_tiles) coded_blocks = vec_tiles;
+    }
+    if (a.n_rows) {
+      row_blocks = cap - coded_blocks * coded_tensors;
+      if (row_blocks < 1) row_blocks = 1;
+      if (row_blocks > row_tiles) row_blocks = row_tiles;
+    }
+  }
+  for (int which = 0; which < 2; ++which)
+    if (a.coded[which].blocks) a.coded[which].blocks = (unsigned)coded_blocks;
+  a.row_blocks = (unsigned)row_blocks;
+  const unsigned grid = a.coded[0].blocks + a.coded[1].blocks + a.row_blocks;
+  // tokens a tile of coded vectors can touch
+  const int64_t touch = (kVecTile - 1) / d.num_kv_heads + 2;
+  a.coded_tok = (int)(touch < kVecTile ? touch : kVecTile);
+  return c.dtype == TQ_F32 ? run_append<float>(a, grid, st) : run_append<__nv_bfloat16>(a, grid, st);
+}
+
+}  // namespace tq
