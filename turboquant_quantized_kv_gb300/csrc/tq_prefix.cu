@@ -3,156 +3,670 @@
 //     out[b] = softmax(sm_scale q[b] [K_prefix; K_own,b]^T) [V_prefix; V_own,b]
 //
 // The prefix is the same for every sequence, so its keys and values are read once and
-// met with all rows (sequence, query head) of a KV head; each sequence's own tokens are
-// one decode of their own.  Three launches: k_prefix leaves one partial (weighted value
-// sum, maximum, denominator) per (row, split of the prefix), the decode kernel leaves
-// those of the own tokens in its workspace, and k_prefix_merge joins both and applies
-// the inverse rotation.
+// met with all rows (sequence, query head) of a KV head: for a KV head the logits are one
+// matrix product Q' K^T of [rows x 128] by [128 x tokens], the weighted values another.
+// Each sequence's own tokens are one decode of their own.  Three launches: k_prefix leaves
+// one partial (weighted value sum, reference, denominator) per (row, split of the prefix),
+// the decode kernel leaves those of the own tokens in its workspace, and k_prefix_merge
+// joins both and applies the inverse rotation.
+//
+// k_prefix: one CTA per SM, two "streams" of 128 rows x 128 tokens through the
+// fifth-generation tensor cores.
+//   8 producer warps  turn 8 blocks (128 tokens) of K and V pages into 16-bit operands in
+//                     shared memory, two stages each: bf16 pages as they are, codes as
+//                     fp16 centroids by byte permutes from tables in registers (a centroid
+//                     table is antisymmetric: magnitude lookup, then the sign bit), FP8
+//                     keys as fp16.  The norms gamma stay fp32 and are applied to the
+//                     logits and to the weights.
+//   1 MMA warp        S = Q' K^T (A, B in shared memory), O += P V (A = P in tensor
+//                     memory), one elected thread.
+//   8 softmax warps   a thread a row: two passes over the row's 128 logits in tensor memory
+//                     (the maximum; then base-2 weights, written back as 16-bit P over S).
+//                     The reference moves only when a logit exceeds it by 2^8, so the
+//                     accumulator is rarely rescaled; the weights gamma' 2^(s - M) carry a
+//                     common power of two that keeps them in fp16's range whatever the
+//                     values' norms.
+// With more than 128 rows a KV head the streams are two tiles of rows over the same
+// tokens; with fewer they share the rows and take every other tile of tokens, each with an
+// accumulator of its own (two partials).
+//
+// Roundings: Q' and the centroids to fp16 (half a step 2^-12; a row of Q' is first scaled by
+// a power of two), weights to fp16 (2^-12) with coded values and to bf16 (2^-9) in bf16
+// layers, whose q and K stay exact (an fp32 q is split in two bf16 parts); sums, maxima and
+// denominators are fp32, the denominator of the unrounded weights.
 #include <cuda_fp8.h>
 
+#include "tq_async.cuh"
 #include "tq_device.cuh"
 #include "tq_internal.h"
+#include "tq_tcgen05.cuh"
 
 namespace tq {
 
 Codebook codebook_of(const tq_cache_desc& d, int which);
 UnitMap unit_map(const tq_cache_desc& d, int num_q_heads);
 
-constexpr int kPRows = 16;  // rows a CTA
+constexpr int kPTile = 128;            // tokens a tile, rows a stream
+constexpr int kPBlocks = kPTile / kBlock;
+constexpr int kPSoftWarps = 8, kPProdWarps = 8;
+constexpr int kPThreads = (kPSoftWarps + kPProdWarps + 1) * 32;
+constexpr uint32_t kPPanel = kPTile * 128;       // 128 rows of 64 16-bit elements, swizzled
+constexpr uint32_t kPOperand = 2 * kPPanel;      // a 128 x 128 operand
+constexpr int kPNormSlots = 4;                   // tiles whose norms and masks are kept
+constexpr float kPSlack = 8.0f;                  // log2 units a logit may exceed the reference
+constexpr int kPNormSlack = 4;                   // log2 units a norm may exceed its reference
+constexpr int kPShift = 3;                       // weights are scaled by 2^3: at most 2^15 in fp16
+
+// Shared memory past the operands (byte offsets from its 1024-aligned start).
+constexpr uint32_t kPOffQ = 0, kPOffK = 2 * kPOperand, kPOffV = 4 * kPOperand, kPOffGk = 6 * kPOperand;
+constexpr uint32_t kPOffGv = kPOffGk + kPNormSlots * kPTile * 4;
+constexpr uint32_t kPOffMask = kPOffGv + kPNormSlots * kPTile * 4;       // u16 [slots][8]
+constexpr uint32_t kPOffExp = kPOffMask + kPNormSlots * 16;              // int [slots][8]
+constexpr uint32_t kPOffScale = kPOffExp + kPNormSlots * 32;             // float [256]
+constexpr uint32_t kPOffBar = kPOffScale + 2 * kPTile * 4;
+constexpr int kPBars = 2 + 2 + 2 + 2 + kPNormSlots + 2 + 2 + 2;
+constexpr uint32_t kPOffTmem = kPOffBar + kPBars * 8;
+constexpr uint32_t kPSmem = kPOffTmem + 16 + 1024;  // 1024: alignment of the start
 
 struct PrefixArgs {
   const uint8_t* kpool;
   const uint8_t* vpool;
-  int kpage, vpage;
   int64_t num_blocks;
   const int32_t* table;
   int len;
   const void* q;
   int q_bf16;
-  int batch, Hq, Hkv, g;
-  int fmt, bits_k, bits_v;
-  float scale;  // sm_scale * log2 e
-  const float* rot;
-  int splits, blocks_per_split;
-  float* part;  // [splits][B * Hq][d]
-  float* ml;    // [splits][B * Hq][2]
+  int Hq, Hkv, g;
+  int rows;        // batch * g: rows of a KV head
+  int row_blocks;  // CTAs over the rows of a KV head
+  int pair;        // 1: the streams are two tiles of rows; 0: two sets of tiles of tokens
+  int split_q;     // bf16 layers with an fp32 q: the second tile of Q holds its low parts
+  int tiles_per_split;
+  float scale;     // sm_scale * log2 e
+  const float* rot;  // signs, for packed keys (null: q is not rotated)
+  int64_t all_rows;  // batch * Hq
+  float* part;     // [partials][B * Hq][d]
+  float* ml;       // [partials][B * Hq][2]
   Codebook cbk, cbv;
   unsigned* status;
 };
 
-__device__ __forceinline__ float coded_at(const uint8_t* page, int bits, int tok, int j, const float* table) {
-  const uint8_t* rec = page + tok * 16 * bits;
-  const int bit = bits * j;
-  const uint32_t w = rec[bit >> 3] | ((bit & 7) + bits > 8 ? (uint32_t)rec[(bit >> 3) + 1] << 8 : 0u);
-  const float gamma = *reinterpret_cast<const float*>(page + 256 * bits + 4 * tok);
-  return gamma * table[(w >> (bit & 7)) & ((1u << bits) - 1u)];
+// ------------------------------------------------------------------ operands
+
+// fp16 centroids of the upper half of a codebook as byte tables for permutes: entry i < 8,
+// low bytes and high bytes apart.
+struct HalfTable {
+  uint32_t lo0, lo1, hi0, hi1;
+};
+template <int BITS>
+__device__ __forceinline__ HalfTable half_table(const Codebook& cb) {
+  constexpr int H = 1 << (BITS - 1);
+  uint32_t h[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h[i] = (uint32_t)__half_as_ushort(__float2half_rn(cb.c[H + (i & (H - 1))]));
+  HalfTable t;
+  t.lo0 = (h[0] & 255u) | (h[1] & 255u) << 8 | (h[2] & 255u) << 16 | (h[3] & 255u) << 24;
+  t.lo1 = (h[4] & 255u) | (h[5] & 255u) << 8 | (h[6] & 255u) << 16 | (h[7] & 255u) << 24;
+  t.hi0 = h[0] >> 8 | (h[1] >> 8) << 8 | (h[2] >> 8) << 16 | (h[3] >> 8) << 24;
+  t.hi1 = h[4] >> 8 | (h[5] >> 8) << 8 | (h[6] >> 8) << 16 | (h[7] >> 8) << 24;
+  return t;
 }
 
-// A CTA: 16 rows of one KV head, one split of the prefix's blocks; thread t holds
-// coordinate t of the rows' value sums.
-__global__ void __launch_bounds__(kD) k_prefix(const __grid_constant__ PrefixArgs a) {
-  __shared__ float qs[kPRows][kD], ks[kBlock][kD + 1], vs[kBlock][kD], ps[kPRows][kBlock];
-  __shared__ float rm[kPRows], rl[kPRows], ra[kPRows], tk[16], tv[16];
-  const int t = threadIdx.x;
-  const int rows = a.batch * a.g;
-  const int tiles = (rows + kPRows - 1) / kPRows;
-  const int kvh = blockIdx.x / tiles, r0 = (blockIdx.x % tiles) * kPRows;
-  const int nr = min(kPRows, rows - r0);
-  if (t < 16) {
-    tk[t] = a.cbk.c[t];
-    tv[t] = a.cbv.c[t];
-    rm[t] = -INFINITY;
-    rl[t] = 0.0f;
+// Eight codes, one in each nibble of v, to eight fp16 centroids.
+template <int BITS>
+__device__ __forceinline__ uint4 centroids8(uint32_t v, const HalfTable& t) {
+  constexpr uint32_t top = 0x11111111u << (BITS - 1);
+  const uint32_t n = ~v & top;                       // negative: the top bit of a code is clear
+  const uint32_t m = n - (n >> (BITS - 1));          // the low bits of the negative ones
+  const uint32_t sel = (v ^ m) & (top - 0x11111111u);  // magnitude index
+  const uint32_t l0 = prmt(t.lo0, t.lo1, sel), l1 = prmt(t.lo0, t.lo1, sel >> 16);
+  uint32_t h0 = prmt(t.hi0, t.hi1, sel), h1 = prmt(t.hi0, t.hi1, sel >> 16);
+  const uint32_t ne = n << (8 - BITS), no = n << (4 - BITS);  // signs of even and odd codes at the tops of bytes
+  h0 ^= prmt(ne, no, 0x5140u) & 0x80808080u;
+  h1 ^= prmt(ne, no, 0x7362u) & 0x80808080u;
+  return make_uint4(prmt(l0, h0, 0x5140u), prmt(l0, h0, 0x7362u), prmt(l1, h1, 0x5140u), prmt(l1, h1, 0x7362u));
+}
+
+// A lane's half record (64 coordinates of one token) of a page of format F (0: bf16, 8: FP8,
+// else code bits), as loaded.
+template <int F>
+struct HalfRecord {
+  static constexpr int kBytes = F == 0 ? 128 : 8 * F;
+  static constexpr int kWords = kBytes / 4;
+  uint32_t w[kWords];
+  float gamma;
+};
+
+// Chunk order: lane half h visits chunk i ^ (4 h) in step i, so that the eight lanes of a
+// 128-bit store phase (four tokens, two halves) hit eight different 16-byte columns.
+template <int F>
+__device__ __forceinline__ void load_half(HalfRecord<F>& r, const uint8_t* page, int tok, int half) {
+  constexpr int B = HalfRecord<F>::kBytes;
+  const uint8_t* p = page + tok * 2 * B + half * B;
+  if constexpr (F == 3) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p) + i);
+      r.w[2 * i] = v.x;
+      r.w[2 * i + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < B / 16; ++i) {
+      const int c = B >= 32 ? i ^ (half * (B / 32)) : i;  // (the upper half of the record's half first for h = 1)
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + c);
+      r.w[4 * i] = v.x;
+      r.w[4 * i + 1] = v.y;
+      r.w[4 * i + 2] = v.z;
+      r.w[4 * i + 3] = v.w;
+    }
   }
-  for (int r = 0; r < kPRows; ++r) {
-    float v = 0.0f;
-    if (r < nr) {
+  r.gamma = (F >= 2 && F <= 4) ? __ldg(reinterpret_cast<const float*>(page + kBlock * 2 * B) + tok) : 1.0f;
+}
+
+template <int F>
+__device__ __forceinline__ void zero_half(HalfRecord<F>& r) {
+#pragma unroll
+  for (int i = 0; i < HalfRecord<F>::kWords; ++i) r.w[i] = 0u;
+  r.gamma = 0.0f;
+}
+
+// Step i of the half record: its chunk's place (0..7) and its eight 16-bit values.
+template <int F>
+__device__ __forceinline__ uint4 chunk_of(const HalfRecord<F>& r, int i, const HalfTable& t) {
+  if constexpr (F == 0) {
+    return make_uint4(r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]);
+  } else if constexpr (F == 8) {
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t w = r.w[2 * i + (k >> 1)];
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((k & 1) ? w >> 16 : w & 0xFFFFu), __NV_E4M3);
+      o[k] = (uint32_t)h.x | ((uint32_t)h.y << 16);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+  } else if constexpr (F == 4) {
+    return centroids8<4>(r.w[i], t);
+  } else if constexpr (F == 3) {  // 24 bits to nibbles
+    const int bit = 24 * i;
+    uint32_t x = r.w[bit >> 5] >> (bit & 31);
+    if ((bit & 31) > 8) x |= r.w[(bit >> 5) + 1] << (32 - (bit & 31));
+    const uint32_t u = (x & 0x00000FFFu) | ((x & 0x00FFF000u) << 4);
+    const uint32_t v = (u & 0x003F003Fu) | ((u & 0x0FC00FC0u) << 2);
+    return centroids8<3>((v & 0x07070707u) | ((v & 0x38383838u) << 1), t);
+  } else {  // 16 bits to nibbles
+    const uint32_t x = (r.w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu;
+    uint32_t u = (x | x << 8) & 0x00FF00FFu;
+    u = (u | u << 4) & 0x0F0F0F0Fu;
+    return centroids8<2>((u | u << 2) & 0x33333333u, t);
+  }
+}
+
+// The token's half row to the operand at `dst`: panel = half, row = token of the tile,
+// 16-byte chunk c at c ^ (row & 7).
+template <int F>
+__device__ __forceinline__ void store_half(const HalfRecord<F>& r, uint32_t dst, int row, int half, const HalfTable& t,
+                                           bool valid) {
+  const uint32_t base = dst + (uint32_t)half * kPPanel + (uint32_t)row * 128u;
+  // formats loaded in 16-byte pieces of two or more hold their upper part first for half 1
+  constexpr bool kSwapped = F != 3 && HalfRecord<F>::kBytes >= 32;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint4 v = chunk_of<F>(r, i, t);
+    if (!valid) v = make_uint4(0u, 0u, 0u, 0u);
+    const int c = kSwapped ? i ^ (4 * half) : i;
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(base + (uint32_t)((c ^ (row & 7)) << 4)), "r"(v.x),
+                 "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_b2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A warp's row of Q' (lane: coordinates 4 lane .. 4 lane + 3) to the operand tile at `dst`.
+__device__ __forceinline__ void store_q(uint32_t dst, int row, int lane, uint32_t w0, uint32_t w1) {
+  const uint32_t addr = dst + (uint32_t)(lane >> 4) * kPPanel + (uint32_t)row * 128u +
+                        (uint32_t)((((lane & 15) >> 1) ^ (row & 7)) << 4) + (uint32_t)(lane & 1) * 8u;
+  asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(addr), "r"(w0), "r"(w1) : "memory");
+}
+
+// The CTA's rows of Q: rotated for packed keys, scaled by a power of two to fp16 (bf16
+// layers: bf16 parts as they are); scale_s[row] gives log2-logits from S.
+template <int KF>
+__device__ __forceinline__ void stage_q(const PrefixArgs& a, int kvh, int r0, uint32_t qdst, float* scale_s, int warp,
+                                        int lane) {
+  constexpr int kWarps = kPSoftWarps + kPProdWarps;
+  const int rows = a.pair ? 2 * kPTile : kPTile;
+  float sg[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+  if (KF >= 2 && KF <= 4) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sg[k] = __ldg(a.rot + 4 * lane + k) * 0.08838834764831845f;
+  }
+  const float flip = a.scale < 0.0f ? -1.0f : 1.0f;  // the rows' scales are positive
+#pragma unroll 4
+  for (int r = warp; r < rows; r += kWarps) {
+    float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (r0 + r < a.rows) {
       const int64_t row = (int64_t)((r0 + r) / a.g) * a.Hq + kvh * a.g + (r0 + r) % a.g;
-      v = a.q_bf16 ? load_elem(reinterpret_cast<const __nv_bfloat16*>(a.q) + row * kD + t)
-                   : load_elem(reinterpret_cast<const float*>(a.q) + row * kD + t);
-      if (a.fmt == TQ_KV_PACKED) v *= a.rot[t] * 0.08838834764831845f;
-    }
-    qs[r][t] = v * a.scale;
-  }
-  __syncthreads();
-  if (a.fmt == TQ_KV_PACKED) {
-    for (int h = 1; h < kD; h <<= 1) {
-      for (int p = t; p < kPRows * kD / 2; p += kD) {
-        const int r = p / (kD / 2), i = p % (kD / 2);
-        const int j = (i / h) * 2 * h + i % h;
-        const float x = qs[r][j], y = qs[r][j + h];
-        qs[r][j] = x + y;
-        qs[r][j + h] = x - y;
-      }
-      __syncthreads();
-    }
-  }
-  float acc[kPRows];
-#pragma unroll
-  for (int r = 0; r < kPRows; ++r) acc[r] = 0.0f;
-  const int nblk = (a.len + kBlock - 1) / kBlock;
-  const int b0 = blockIdx.y * a.blocks_per_split, b1 = min(b0 + a.blocks_per_split, nblk);
-  for (int b = b0; b < b1; ++b) {
-    const int id = a.table[b];
-    if (id < 0 || id >= a.num_blocks) {
-      if (t == 0) flag_status(a.status, TQ_DEV_BAD_BLOCK);
-      continue;  // uniform
-    }
-    const int nt = min(kBlock, a.len - b * kBlock);
-    const uint8_t* kp = a.kpool + ((int64_t)id * a.Hkv + kvh) * a.kpage;
-    const uint8_t* vp = a.vpool + ((int64_t)id * a.Hkv + kvh) * a.vpage;
-    __syncthreads();
-    for (int i = 0; i < nt; ++i) {
-      if (a.fmt == TQ_KV_BF16) {
-        ks[i][t] = load_elem(reinterpret_cast<const __nv_bfloat16*>(kp) + i * kD + t);
-        vs[i][t] = load_elem(reinterpret_cast<const __nv_bfloat16*>(vp) + i * kD + t);
+      if (a.q_bf16) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(a.q) + row * kD) + lane);
+        x[0] = __uint_as_float(v.x << 16);
+        x[1] = __uint_as_float(v.x & 0xFFFF0000u);
+        x[2] = __uint_as_float(v.y << 16);
+        x[3] = __uint_as_float(v.y & 0xFFFF0000u);
       } else {
-        ks[i][t] = a.fmt == TQ_KV_K8V4 ? __half2float(__half(__nv_cvt_fp8_to_halfraw(kp[i * kD + t], __NV_E4M3)))
-                                       : coded_at(kp, a.bits_k, i, t, tk);
-        vs[i][t] = coded_at(vp, a.bits_v, i, t, tv);
+        const float4 v = __ldg(reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.q) + row * kD) + lane);
+        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
       }
     }
-    __syncthreads();
-    for (int p = t; p < kPRows * kBlock; p += kD) {
-      const int r = p / kBlock, i = p % kBlock;
-      float s = -INFINITY;
-      if (i < nt) {
-        s = 0.0f;
-        for (int j = 0; j < kD; ++j) s = fmaf(qs[r][j], ks[i][j], s);
-      }
-      ps[r][i] = s;
-    }
-    __syncthreads();
-    if (t < kPRows) {
-      float m = rm[t];
-      for (int i = 0; i < nt; ++i) m = fmaxf(m, ps[t][i]);
-      const float f = m == -INFINITY ? 1.0f : exp2f(rm[t] - m);
-      float l = rl[t] * f;
-      for (int i = 0; i < nt; ++i) {
-        const float p = m == -INFINITY ? 0.0f : exp2f(ps[t][i] - m);
-        ps[t][i] = p;
-        l += p;
-      }
-      rm[t] = m;
-      rl[t] = l;
-      ra[t] = f;
-    }
-    __syncthreads();
 #pragma unroll
-    for (int r = 0; r < kPRows; ++r) {
-      float s = acc[r] * ra[r];
-      for (int i = 0; i < nt; ++i) s = fmaf(ps[r][i], vs[i][t], s);
-      acc[r] = s;
+    for (int k = 0; k < 4; ++k) x[k] *= flip;
+    const uint32_t tile = qdst + (uint32_t)(r / kPTile) * kPOperand;
+    const int tr = r % kPTile;
+    if constexpr (KF == 0) {
+      const uint32_t w0 = pack_b2(x[0], x[1]), w1 = pack_b2(x[2], x[3]);
+      store_q(tile, tr, lane, w0, w1);
+      if (a.split_q)
+        store_q(tile + kPOperand, tr, lane,
+                pack_b2(x[0] - __uint_as_float(w0 << 16), x[1] - __uint_as_float(w0 & 0xFFFF0000u)),
+                pack_b2(x[2] - __uint_as_float(w1 << 16), x[3] - __uint_as_float(w1 & 0xFFFF0000u)));
+      if (lane == 0) scale_s[r] = fmaxf(fabsf(a.scale), 1e-30f);
+    } else {
+      if constexpr (KF >= 2 && KF <= 4) {  // H D x / sqrt(d): bits 0, 1 in the lane, bits 2..6 across lanes
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] *= sg[k];
+        const float t0 = x[0] + x[1], t1 = x[0] - x[1], t2 = x[2] + x[3], t3 = x[2] - x[3];
+        x[0] = t0 + t2; x[2] = t0 - t2; x[1] = t1 + t3; x[3] = t1 - t3;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+          const bool upper = (lane & m) != 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float o = __shfl_xor_sync(0xffffffffu, x[k], m);
+            x[k] = upper ? (o - x[k]) : (x[k] + o);
+          }
+        }
+      }
+      float mx = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+#pragma unroll
+      for (int m = 16; m > 0; m >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
+      // 2^e <= largest coordinate < 2^(e + 1); products with the inverse power are exact
+      const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100);
+      const float inv = __uint_as_float((uint32_t)(127 - e) << 23), pw = __uint_as_float((uint32_t)(127 + e) << 23);
+      store_q(tile, tr, lane, pack_h2(x[0] * inv, x[1] * inv), pack_h2(x[2] * inv, x[3] * inv));
+      if (lane == 0) scale_s[r] = fmaxf(fabsf(a.scale) * pw, 1e-30f);
     }
   }
-  __syncthreads();
-#pragma unroll
-  for (int r = 0; r < kPRows; ++r) {
-    if (r < nr) {
-      const int64_t row = (int64_t)blockIdx.y * a.batch * a.Hq + (int64_t)((r0 + r) / a.g) * a.Hq + kvh * a.g + (r0 + r) % a.g;
-      a.part[row * kD + t] = acc[r];
-      if (t < 2) a.ml[row * 2 + t] = t == 0 ? rm[r] : rl[r];
+}
+
+// --------------------------------------------------------------- the kernel
+
+template <int KF, int VF>
+__global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__ PrefixArgs a) {
+  constexpr bool kCodedK = KF >= 2 && KF <= 4, kCodedV = VF != 0;
+  constexpr int kpage = KF == 0 ? kBlock * kD * 2 : (KF == 8 ? kBlock * kD : kBlock * (kD * KF / 8 + 4));
+  constexpr int vpage = VF == 0 ? kBlock * kD * 2 : kBlock * (kD * VF / 8 + 4);
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  unsigned char* const gen = smem_raw + (base - raw);
+  float* const gk = reinterpret_cast<float*>(gen + kPOffGk);
+  float* const gv = reinterpret_cast<float*>(gen + kPOffGv);
+  float* const scale_s = reinterpret_cast<float*>(gen + kPOffScale);
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(gen + kPOffBar);
+  uint64_t *const kfull = bars, *const kempty = bars + 2, *const vfull = bars + 4, *const vempty = bars + 6;
+  uint64_t* const gfull = bars + 8;                 // [kPNormSlots]
+  uint64_t* const sfull = gfull + kPNormSlots;      // [2] logits of a stream are in tensor memory
+  uint64_t* const pfull = sfull + 2;                // [2] weights of a stream are in tensor memory
+  uint64_t* const odone = pfull + 2;                // [2] a stream's accumulator is complete
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  const int kvh = blockIdx.x / a.row_blocks;
+  const int r0 = (blockIdx.x % a.row_blocks) * (a.pair ? 2 * kPTile : kPTile);
+  const int all_tiles = (a.len + kPTile - 1) / kPTile;
+  const int tile0 = blockIdx.y * a.tiles_per_split;
+  const int n = max(0, min(a.tiles_per_split, all_tiles - tile0));  // the CTA's tiles of tokens
+  // stream s: tiles i (pair) or 2 i + s, i < count(s)
+  const int count0 = a.pair ? n : (n + 1) / 2, count1 = a.pair ? n : n / 2;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(kfull + i, kPProdWarps);
+      mbar_init(kempty + i, 1);
+      mbar_init(vfull + i, kPProdWarps);
+      mbar_init(vempty + i, 1);
+      mbar_init(sfull + i, 1);
+      mbar_init(pfull + i, 4);
+      mbar_init(odone + i, 1);
     }
+    for (int i = 0; i < kPNormSlots; ++i) mbar_init(gfull + i, kPProdWarps);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kPSoftWarps + kPProdWarps) tmem_alloc(base + kPOffTmem, 512);
+  else stage_q<KF>(a, kvh, r0, base + kPOffQ, scale_s, warp, lane);
+  fence_proxy_async();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<const uint32_t*>(gen + kPOffTmem);
+  bool ok = true;  // no wait gave up
+
+  if (warp < kPSoftWarps) {
+    // ------------------------------------------------------------- softmax
+    const int s = warp >> 2, w = warp & 3;
+    const uint32_t ts = tmem + (uint32_t)(s * kPTile) + ((uint32_t)(32 * w) << 16);
+    const uint32_t to = tmem + (uint32_t)((2 + s) * kPTile) + ((uint32_t)(32 * w) << 16);
+    const int count = s ? count1 : count0;
+    const int trow = a.pair ? s * kPTile + 32 * w : 32 * w;  // the warp's first row of the CTA's rows
+    const bool live = r0 + trow < a.rows;  // (whole warps of padding rows only take part in the barriers)
+    const float rs = scale_s[trow + lane];
+    float M = -INFINITY, l = 0.0f;  // reference in log2 units; sum of weights 2^(s - M + kPShift - E)
+    int E = -1000;                  // power of two of the norms' reference
+    for (int i = 0; i < count && ok; ++i) {
+      const int t = a.pair ? i : 2 * i + s, slot = t & (kPNormSlots - 1);
+      ok = mbar_wait(gfull + slot, (t / kPNormSlots) & 1) && mbar_wait(sfull + s, i & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      if (live) {
+        const uint4 mw = *reinterpret_cast<const uint4*>(gen + kPOffMask + slot * 16);
+        const bool whole = (mw.x & mw.y & mw.z & mw.w) == 0xFFFFFFFFu;  // no masked token in the tile
+        const uint32_t mword[4] = {mw.x, mw.y, mw.z, mw.w};
+        const float4* gk4 = reinterpret_cast<const float4*>(gk + slot * kPTile);
+        const float4* gv4 = reinterpret_cast<const float4*>(gv + slot * kPTile);
+        uint32_t ra[32], rb[32];
+        float mx = -INFINITY;
+        auto pass1 = [&](uint32_t(&r)[32], int c) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float v[4] = {__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]), __uint_as_float(r[4 * k + 2]),
+                          __uint_as_float(r[4 * k + 3])};
+            if constexpr (kCodedK) {
+              const float4 g = gk4[8 * c + k];
+              v[0] *= g.x; v[1] *= g.y; v[2] *= g.z; v[3] *= g.w;
+            }
+            if (!whole) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) v[j] = (mword[c] >> (4 * k + j)) & 1u ? v[j] : -INFINITY;
+            }
+            mx = fmaxf(fmaxf(mx, fmaxf(v[0], v[1])), fmaxf(v[2], v[3]));
+          }
+        };
+        tmem_ld32_async(ts, ra);
+        tmem_wait_ld32(ra);
+        tmem_ld32_async(ts + 32, rb);
+        pass1(ra, 0);
+        tmem_wait_ld32(rb);
+        tmem_ld32_async(ts + 64, ra);
+        pass1(rb, 1);
+        tmem_wait_ld32(ra);
+        tmem_ld32_async(ts + 96, rb);
+        pass1(ra, 2);
+        tmem_wait_ld32(rb);
+        pass1(rb, 3);
+        // move the reference where a logit or a norm outgrew it
+        const float m = mx * rs;
+        int e = E;
+        if constexpr (kCodedV) {
+          const int4 e0 = reinterpret_cast<const int4*>(gen + kPOffExp + slot * 32)[0];
+          const int4 e1 = reinterpret_cast<const int4*>(gen + kPOffExp + slot * 32)[1];
+          const int et = max(max(max(e0.x, e0.y), max(e0.z, e0.w)), max(max(e1.x, e1.y), max(e1.z, e1.w)));
+          if (et > E + kPNormSlack) e = et;
+        } else {
+          e = 0;
+        }
+        const bool move = m > M + kPSlack || (M == -INFINITY && m > -INFINITY);
+        if (__any_sync(0xffffffffu, move || e != E)) {
+          const float nm = move ? m : M;
+          const float f = M == -INFINITY ? 0.0f : exp2f(M - nm + (float)(E - e));
+          l *= f;
+          if (i > 0) {  // rescale the accumulator (the last product into it is complete: it precedes S)
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              tmem_ld32_async(to + 32 * c, ra);
+              tmem_wait_ld32(ra);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) ra[k] = __float_as_uint(__uint_as_float(ra[k]) * f);
+              tmem_st32(to + 32 * c, ra);
+            }
+          }
+          M = nm;
+          E = e;
+        }
+        // weights: 2^(u - M + kPShift - E), u = rs gamma s
+        const float off = (M == -INFINITY ? 0.0f : M) - (kCodedV ? (float)(kPShift - E) : 0.0f);
+        float2 sum = make_float2(0.0f, 0.0f);
+        auto pass2 = [&](uint32_t(&r)[32], int c) {
+          uint32_t p[16];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float2 u0 = make_float2(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]));
+            float2 u1 = make_float2(__uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3]));
+            if constexpr (kCodedK) {
+              const float4 g = gk4[8 * c + k];
+              u0 = __fmul2_rn(u0, make_float2(g.x, g.y));
+              u1 = __fmul2_rn(u1, make_float2(g.z, g.w));
+            }
+            u0 = __ffma2_rn(u0, make_float2(rs, rs), make_float2(-off, -off));
+            u1 = __ffma2_rn(u1, make_float2(rs, rs), make_float2(-off, -off));
+            if (!whole) {
+              const uint32_t b = mword[c] >> (4 * k);
+              u0.x = b & 1u ? u0.x : -INFINITY;
+              u0.y = b & 2u ? u0.y : -INFINITY;
+              u1.x = b & 4u ? u1.x : -INFINITY;
+              u1.y = b & 8u ? u1.y : -INFINITY;
+            }
+            u0 = make_float2(ex2(u0.x), ex2(u0.y));
+            u1 = make_float2(ex2(u1.x), ex2(u1.y));
+            sum = __fadd2_rn(sum, __fadd2_rn(u0, u1));
+            if constexpr (kCodedV) {
+              const float4 g = gv4[8 * c + k];
+              u0 = __fmul2_rn(u0, make_float2(g.x, g.y));
+              u1 = __fmul2_rn(u1, make_float2(g.z, g.w));
+              p[2 * k] = pack_h2(u0.x, u0.y);
+              p[2 * k + 1] = pack_h2(u1.x, u1.y);
+            } else {
+              p[2 * k] = pack_b2(u0.x, u0.y);
+              p[2 * k + 1] = pack_b2(u1.x, u1.y);
+            }
+          }
+          tmem_st16(ts + 16 * c, p);  // over logits that have been read
+        };
+        tmem_ld32_async(ts, ra);
+        tmem_wait_ld32(ra);
+        tmem_ld32_async(ts + 32, rb);
+        pass2(ra, 0);
+        tmem_wait_ld32(rb);
+        tmem_ld32_async(ts + 64, ra);
+        pass2(rb, 1);
+        tmem_wait_ld32(ra);
+        tmem_ld32_async(ts + 96, rb);
+        pass2(ra, 2);
+        tmem_wait_ld32(rb);
+        pass2(rb, 3);
+        l += sum.x + sum.y;
+        tmem_wait_st();
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pfull + s);
+    }
+    // ---- the stream's partial: (accumulator, reference, denominator) of each row
+    if (ok && count > 0) ok = __all_sync(0xffffffffu, mbar_wait(odone + s, 0));
+    tc_fence_after();
+    if (live) {
+      const int r = r0 + trow + lane;
+      const int64_t pi = a.pair ? blockIdx.y : 2 * blockIdx.y + s;
+      const int64_t row = pi * a.all_rows + (int64_t)(r / a.g) * a.Hq + kvh * a.g + r % a.g;
+      const bool any = ok && M != -INFINITY;
+      if (r < a.rows) {
+        a.ml[2 * row] = any ? M - (kCodedV ? (float)(kPShift - E) : 0.0f) : -INFINITY;
+        a.ml[2 * row + 1] = any ? l : 0.0f;
+      }
+      if (ok && count > 0) {
+        uint32_t ra[32];
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld32_async(to + 32 * c, ra);
+          tmem_wait_ld32(ra);
+          if (r < a.rows) {
+            uint4* o = reinterpret_cast<uint4*>(a.part + row * kD + 32 * c);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = make_uint4(ra[4 * k], ra[4 * k + 1], ra[4 * k + 2], ra[4 * k + 3]);
+          }
+        }
+      }
+    }
+  } else if (warp < kPSoftWarps + kPProdWarps) {
+    // ------------------------------------------------------------ producers
+    const int w = warp - kPSoftWarps, tok = lane >> 1, half = lane & 1;
+    const int row = w * kBlock + tok;
+    HalfTable tk = {}, tv = {};
+    if constexpr (kCodedK) tk = half_table<(kCodedK ? KF : 4)>(a.cbk);
+    if constexpr (kCodedV) tv = half_table<(kCodedV ? VF : 4)>(a.cbv);
+    const int blocks = (a.len + kBlock - 1) / kBlock;
+    auto block_id = [&](int t) {  // the warp's block of the CTA's tile t: its id, -1 past the end
+      const int b = (tile0 + t) * kPBlocks + w;
+      return t < n && b < blocks ? __ldg(a.table + b) : -1;
+    };
+    auto valid_token = [&](int t, int id) {
+      const int b = (tile0 + t) * kPBlocks + w;
+      return id >= 0 && id < a.num_blocks && b * kBlock + tok < a.len;
+    };
+    HalfRecord<KF> rk;
+    HalfRecord<VF> rv;
+    int id = block_id(0), id_next = block_id(1);
+    auto fetch_k = [&](int t, int blk) {
+      if (valid_token(t, blk)) load_half<KF>(rk, a.kpool + ((int64_t)blk * a.Hkv + kvh) * kpage, tok, half);
+      else zero_half<KF>(rk);
+    };
+    auto fetch_v = [&](int t, int blk) {
+      if (valid_token(t, blk)) load_half<VF>(rv, a.vpool + ((int64_t)blk * a.Hkv + kvh) * vpage, tok, half);
+      else zero_half<VF>(rv);
+    };
+    if (n > 0) {
+      fetch_k(0, id);
+      fetch_v(0, id);
+    }
+    for (int t = 0; t < n && ok; ++t) {
+      const int st = t & 1, slot = t & (kPNormSlots - 1);
+      const bool valid = valid_token(t, id);
+      if (lane == 0 && (id < 0 || id >= a.num_blocks) && (tile0 + t) * kPBlocks + w < blocks)
+        flag_status(a.status, TQ_DEV_BAD_BLOCK);
+      const int id_after = block_id(t + 2);
+      if (t >= 2) ok = mbar_wait(kempty + st, ((t >> 1) - 1) & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      // norms, mask and the norms' largest exponent of the block
+      if (half == 0) {
+        gk[slot * kPTile + row] = rk.gamma;
+        gv[slot * kPTile + row] = rv.gamma;
+      }
+      const uint32_t vb = __ballot_sync(0xffffffffu, valid && half == 0);  // bit 2 tok
+      if constexpr (kCodedV) {
+        int e = valid ? (int)((__float_as_uint(rv.gamma) >> 23) & 255u) - 126 : -126;  // gamma < 2^e
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, m));
+        if (lane == 0) reinterpret_cast<int*>(gen + kPOffExp)[slot * 8 + w] = e;
+      }
+      if (lane == 0) {
+        uint32_t x = vb & 0x55555555u;  // every other bit together
+        x = (x | x >> 1) & 0x33333333u;
+        x = (x | x >> 2) & 0x0F0F0F0Fu;
+        x = (x | x >> 4) & 0x00FF00FFu;
+        x = (x | x >> 8) & 0x0000FFFFu;
+        reinterpret_cast<uint16_t*>(gen + kPOffMask)[slot * 8 + w] = (uint16_t)x;
+      }
+      store_half<KF>(rk, base + kPOffK + (uint32_t)st * kPOperand, row, half, tk, valid);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(gfull + slot);
+        mbar_arrive(kfull + st);
+      }
+      if (t + 1 < n) fetch_k(t + 1, id_next);
+      if (t >= 2) ok = mbar_wait(vempty + st, ((t >> 1) - 1) & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      store_half<VF>(rv, base + kPOffV + (uint32_t)st * kPOperand, row, half, tv, valid);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(vfull + st);
+      if (t + 1 < n) fetch_v(t + 1, id_next);
+      id = id_next;
+      id_next = id_after;
+    }
+  } else if (lane == 0) {
+    // ------------------------------------------------------------------ MMA
+    constexpr bool kBf16K = KF == 0, kBf16V = VF == 0;
+    constexpr uint32_t idesc_s = umma_idesc_16(kBf16K, false, kPTile, kPTile);
+    constexpr uint32_t idesc_o = umma_idesc_16(kBf16V, true, kPTile, kPTile);
+    const uint64_t dq = umma_desc_sw128(base + kPOffQ), dk = umma_desc_sw128(base + kPOffK);
+    const uint64_t dv = umma_desc_sw128_mn(base + kPOffV, kPPanel);
+    auto tile_of = [&](int i, int s) { return a.pair ? i : 2 * i + s; };
+    auto logits = [&](int i, int s) {  // S_s = Q_s K^T
+      const int t = tile_of(i, s), st = t & 1;
+      if (!mbar_wait(kfull + st, (t >> 1) & 1)) return false;
+      tc_fence_after();
+      const uint64_t q = dq + (uint64_t)((a.pair ? s : 0) * (kPOperand >> 4));
+      const uint64_t k = dk + (uint64_t)(st * (kPOperand >> 4));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint64_t off = (uint64_t)((j >> 2) * (kPPanel >> 4) + (j & 3) * 2);
+        umma_bf16(tmem + (uint32_t)(s * kPTile), q + off, k + off, idesc_s, j > 0);
+      }
+      if (KF == 0 && a.split_q) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint64_t off = (uint64_t)((j >> 2) * (kPPanel >> 4) + (j & 3) * 2);
+          umma_bf16(tmem + (uint32_t)(s * kPTile), q + (kPOperand >> 4) + off, k + off, idesc_s, true);
+        }
+      }
+      umma_commit(smem_u32(sfull + s));
+      if (!a.pair || s == 1) umma_commit(smem_u32(kempty + st));
+      return true;
+    };
+    auto values = [&](int i, int s) {  // O_s += P_s V
+      const int t = tile_of(i, s), st = t & 1;
+      if (!mbar_wait(pfull + s, i & 1) || !mbar_wait(vfull + st, (t >> 1) & 1)) return false;
+      tc_fence_after();
+      const uint64_t v = dv + (uint64_t)(st * (kPOperand >> 4));
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        umma_16_ts(tmem + (uint32_t)((2 + s) * kPTile), tmem + (uint32_t)(s * kPTile + 8 * j), v + (uint64_t)(j * (16 * 128 >> 4)),
+                   idesc_o, i > 0 || j > 0);
+      if (!a.pair || s == 1) umma_commit(smem_u32(vempty + st));
+      if (i + 1 == (s ? count1 : count0)) umma_commit(smem_u32(odone + s));
+      return true;
+    };
+    if (count0 > 0) ok = logits(0, 0);
+    if (ok && count1 > 0) ok = logits(0, 1);
+    for (int i = 0; i < count0 && ok; ++i) {
+      ok = values(i, 0);
+      if (ok && i + 1 < count0) ok = logits(i + 1, 0);
+      if (ok && i < count1) ok = values(i, 1);
+      if (ok && i + 1 < count1) ok = logits(i + 1, 1);
+    }
+  }
+  if (!ok && lane == 0) flag_status(a.status, TQ_DEV_WAIT_TIMEOUT);
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kPSoftWarps + kPProdWarps) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
 }
 
@@ -226,21 +740,65 @@ __global__ void __launch_bounds__(128) k_prefix_merge(const MergeArgs a) {
   }
 }
 
-// Splits of the prefix: about four CTAs an SM, a block each at least.
-static int prefix_splits(const tq_cache_desc& d, int batch, int num_q_heads, int64_t len, int num_sms) {
-  if (len < 1) return 0;
-  const int64_t blocks = (len + kBlock - 1) / kBlock;
+// How the prefix is cut: streams over two tiles of rows (pair) or over tiles of tokens,
+// CTAs over the rows and splits of the tokens.  The splits are chosen so that the CTAs,
+// one an SM, fill whole waves: the fewest tiles in a row over one to four waves, a CTA's
+// start and end counted as three tiles.
+struct PrefixPlan {
+  int pair, row_blocks, splits, tiles_per_split, partials;
+};
+static PrefixPlan prefix_plan(const tq_cache_desc& d, int batch, int num_q_heads, int64_t len, int num_sms,
+                              bool split_q) {
+  PrefixPlan p = {};
+  if (len < 1) return p;
   const int64_t rows = (int64_t)batch * (num_q_heads / d.num_kv_heads);
-  const int64_t tiles = (rows + kPRows - 1) / kPRows * d.num_kv_heads;
-  int64_t s = (4 * (int64_t)num_sms + tiles - 1) / tiles;
-  s = s < 1 ? 1 : (s > blocks ? blocks : s);
-  const int64_t per = (blocks + s - 1) / s;
-  return (int)((blocks + per - 1) / per);
+  p.pair = rows > kPTile && !split_q ? 1 : 0;
+  const int per_cta = p.pair ? 2 * kPTile : kPTile;
+  p.row_blocks = (int)((rows + per_cta - 1) / per_cta);
+  const int64_t units = (int64_t)p.row_blocks * d.num_kv_heads;
+  const int64_t tiles = (len + kPTile - 1) / kPTile;
+  int64_t best = INT64_MAX;
+  for (int waves = 1; waves <= 4; ++waves) {
+    int64_t s = (int64_t)waves * num_sms / units;
+    s = s < 1 ? 1 : (s > tiles ? tiles : s);
+    const int64_t per = (tiles + s - 1) / s;
+    s = (tiles + per - 1) / per;
+    const int64_t w = (units * s + num_sms - 1) / num_sms;
+    if (w * (per + 3) < best) {
+      best = w * (per + 3);
+      p.splits = (int)s;
+      p.tiles_per_split = (int)per;
+    }
+  }
+  p.partials = p.splits * (p.pair ? 1 : 2);
+  return p;
 }
 
 size_t prefix_partial_bytes(const tq_cache_desc& d, int batch, int num_q_heads, int64_t prefix_len, int num_sms) {
   const size_t rows = (size_t)batch * num_q_heads;
-  return (size_t)prefix_splits(d, batch, num_q_heads, prefix_len, num_sms) * rows * (kD + 2) * sizeof(float);
+  // (the type of q is not known here: the larger of the two plans)
+  const int a = prefix_plan(d, batch, num_q_heads, prefix_len, num_sms, false).partials;
+  const int b = d.fmt.kv_format == TQ_KV_BF16 ? prefix_plan(d, batch, num_q_heads, prefix_len, num_sms, true).partials : 0;
+  return (size_t)(a > b ? a : b) * rows * (kD + 2) * sizeof(float);
+}
+
+template <int KF, int VF>
+static cudaError_t run_prefix(const PrefixArgs& a, int splits, cudaStream_t st) {
+  auto kern = k_prefix<KF, VF>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPSmem);
+  if (e != cudaSuccess) return e;
+  kern<<<dim3((unsigned)(a.row_blocks * a.Hkv), (unsigned)splits), kPThreads, kPSmem, st>>>(a);
+  count_launch();
+  return cudaGetLastError();
+}
+
+template <int KF>
+static cudaError_t run_prefix_v(const PrefixArgs& a, int bits_v, int splits, cudaStream_t st) {
+  switch (bits_v) {
+    case 2: return run_prefix<KF, 2>(a, splits, st);
+    case 3: return run_prefix<KF, 3>(a, splits, st);
+    default: return run_prefix<KF, 4>(a, splits, st);
+  }
 }
 
 cudaError_t launch_prefix_decode(const PrefixCall& c, cudaStream_t st) {
@@ -263,40 +821,45 @@ cudaError_t launch_prefix_decode(const PrefixCall& c, cudaStream_t st) {
   }
   if (c.prefix_len > 0) {
     PrefixArgs a = {};
+    a.split_q = d.fmt.kv_format == TQ_KV_BF16 && c.own.q_dtype == TQ_F32 ? 1 : 0;
+    const PrefixPlan p = prefix_plan(d, c.own.batch, c.own.num_q_heads, c.prefix_len, c.num_sms, a.split_q != 0);
     a.kpool = reinterpret_cast<const uint8_t*>(d.k_cache);
     a.vpool = reinterpret_cast<const uint8_t*>(d.v_cache);
-    a.kpage = (int)page_bytes_of(d, 0);
-    a.vpage = (int)page_bytes_of(d, 1);
     a.num_blocks = d.num_blocks;
     a.table = c.prefix_table;
     a.len = (int)c.prefix_len;
     a.q = c.own.q;
     a.q_bf16 = c.own.q_dtype == TQ_BF16 ? 1 : 0;
-    a.batch = c.own.batch;
     a.Hq = c.own.num_q_heads;
     a.Hkv = d.num_kv_heads;
     a.g = a.Hq / a.Hkv;
-    a.fmt = d.fmt.kv_format;
-    a.bits_k = d.fmt.bits_k;
-    a.bits_v = d.fmt.bits_v;
+    a.rows = c.own.batch * a.g;
+    a.row_blocks = p.row_blocks;
+    a.pair = p.pair;
+    a.tiles_per_split = p.tiles_per_split;
     a.scale = c.own.sm_scale * 1.4426950408889634f;
     a.rot = d.rotation;
-    a.splits = prefix_splits(d, a.batch, a.Hq, c.prefix_len, c.num_sms);
-    const int blocks = (a.len - 1) / kBlock + 1;
-    a.blocks_per_split = (blocks + a.splits - 1) / a.splits;
+    a.all_rows = rows;
     a.part = reinterpret_cast<float*>(c.own.workspace + off);
-    a.ml = a.part + (size_t)a.splits * rows * kD;
+    a.ml = a.part + (size_t)p.partials * rows * kD;
     a.cbk = codebook_of(d, 0);
     a.cbv = codebook_of(d, 1);
     a.status = c.own.status;
-    const int tiles = (a.batch * a.g + kPRows - 1) / kPRows;
-    k_prefix<<<dim3((unsigned)(tiles * a.Hkv), (unsigned)a.splits), kD, 0, st>>>(a);
-    count_launch();
-    const cudaError_t e = cudaGetLastError();
+    cudaError_t e;
+    if (d.fmt.kv_format == TQ_KV_BF16) {
+      e = run_prefix<0, 0>(a, p.splits, st);
+    } else {
+      switch (d.fmt.kv_format == TQ_KV_K8V4 ? 8 : d.fmt.bits_k) {
+        case 8: e = run_prefix_v<8>(a, d.fmt.bits_v, p.splits, st); break;
+        case 2: e = run_prefix_v<2>(a, d.fmt.bits_v, p.splits, st); break;
+        case 3: e = run_prefix_v<3>(a, d.fmt.bits_v, p.splits, st); break;
+        default: e = run_prefix_v<4>(a, d.fmt.bits_v, p.splits, st); break;
+      }
+    }
     if (e != cudaSuccess) return e;
     m.part = a.part;
     m.ml = a.ml;
-    m.splits = a.splits;
+    m.splits = p.partials;
   }
   if (c.own.max_blocks > 0) {
     DecodeCall own = c.own;
