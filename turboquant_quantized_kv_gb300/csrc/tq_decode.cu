@@ -1738,7 +1738,7 @@ cudaError_t launch_decode(const DecodeCall& c, cudaStream_t st) {
   const int kind = bf16 ? ROTQ_IDENTITY : (d.fmt.rot_kind == TQ_ROT_DENSE ? ROTQ_DENSE : ROTQ_HADAMARD);
   const int kind_q = k8 ? ROTQ_IDENTITY : kind;
   const int64_t rows = (int64_t)c.batch * c.num_q_heads;
-  const float scale = c.sm_scale * kLog2e;
+  const float scale = c.sm_scale * kLog2e / c.factor_k;
   int* counters = reinterpret_cast<int*>(c.workspace + ws.cnt_off);
   // Hadamard and unrotated layers without QJL rotate q inside the decode kernel;
   // dense rotations and S q' (QJL) take a separate mat-vec pass first
@@ -1821,6 +1821,10 @@ cudaError_t launch_decode(const DecodeCall& c, cudaStream_t st) {
   a.ml = reinterpret_cast<float*>(c.workspace + ws.ml_off);
   a.cbk = codebook_of(d, 0);
   a.cbv = codebook_of(d, 1);
+  for (int i = 0; i < 16; ++i) {  // (times one outside tq_prefix_decode)
+    a.cbk.c[i] *= c.factor_k;
+    a.cbv.c[i] *= c.factor_v;
+  }
   a.qjl_coef = 1.2533141373155003f / (float)kD;  // sqrt(pi/2) / m
   a.status = c.status;
   // the decode kernel finishes the job itself (merge and inverse rotation) unless the

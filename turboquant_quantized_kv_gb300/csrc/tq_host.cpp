@@ -370,6 +370,33 @@ size_t page_bytes_of(const tq_cache_desc& d, int which) {
   return n;
 }
 
+float table_factor(const float* centroids, int bits) {
+  constexpr int kCandidates = 512;  // 1 + i / 512; about a microsecond for the 8 magnitudes of 4 bits
+  const int half = 1 << (bits - 1);
+  float best_err = 1.0f, best = 1.0f;
+  float err[kCandidates] = {};
+  for (int j = 0; j < half; ++j) {
+    const float c = centroids[half + j];
+    if (!(c > 0.0f)) continue;
+    for (int i = 0; i < kCandidates; ++i) {  // 11 significant bits, nearest even
+      const float x = c * (1.0f + (float)i / kCandidates);
+      uint32_t u;
+      std::memcpy(&u, &x, 4);
+      u = (u + 0xFFFu + ((u >> 13) & 1u)) & ~0x1FFFu;
+      float r;
+      std::memcpy(&r, &u, 4);
+      const float e = std::fabs(r - x) / x;
+      err[i] = e > err[i] ? e : err[i];
+    }
+  }
+  for (int i = 0; i < kCandidates; ++i)
+    if (err[i] < best_err) {
+      best_err = err[i];
+      best = 1.0f + (float)i / kCandidates;
+    }
+  return best;
+}
+
 static bool table_ok(const float* c, const float* b, int bits) {
   const int k = 1 << bits;
   for (int i = 0; i + 1 < k; ++i)

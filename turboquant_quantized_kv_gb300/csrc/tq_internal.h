@@ -71,6 +71,9 @@ struct DecodeCall {
   // the chunks' partials stay in the workspace for the caller to merge (live slots as
   // slot_live says); out is not written
   bool partials_only = false;
+  // factors of the centroid tables (table_factor); the scale of q undoes the keys' one, the
+  // caller the values'
+  float factor_k = 1.0f, factor_v = 1.0f;
 };
 
 // One validated call of tq_rope_apply or tq_rope_append, as the launchers see it.
@@ -96,6 +99,10 @@ struct PrefixCall {
 };
 // Bytes of the prefix's partials, which follow the workspace of the own tokens' decode.
 size_t prefix_partial_bytes(const tq_cache_desc& d, int batch, int num_q_heads, int64_t prefix_len, int num_sms);
+
+// The factor in [1, 2) that leaves the centroids (2^bits, antisymmetric) with the smallest
+// largest relative error when they are rounded to fp16.
+float table_factor(const float* centroids, int bits);
 
 // True if the append quantizer's cell table can hold these (ascending) boundaries:
 // each boundary in a cell of its own (cells are 1/63 wide on [-1, 1]).

@@ -30,10 +30,15 @@
 // tokens; with fewer they share the rows and take every other tile of tokens, each with an
 // accumulator of its own (two partials).
 //
-// Roundings: Q' and the centroids to fp16 (half a step 2^-12; a row of Q' is first scaled by
-// a power of two), weights to fp16 (2^-12) with coded values and to bf16 (2^-9) in bf16
-// layers, whose q and K stay exact (an fp32 q is split in two bf16 parts); sums, maxima and
-// denominators are fp32, the denominator of the unrounded weights.
+// Roundings.  A query that is not exact in 16 bits (a rotated one, an fp32 one) goes in as two
+// parts, high and low, by a second product on the same K.  Centroids are rounded to fp16
+// after a common factor in [1, 2) that the host chooses so that the table's few magnitudes
+// lie next to fp16 values (largest relative error of a 4-bit table 3.0e-4 -> 1.2e-4, of a
+// 3-bit one 2.3e-4 -> 1.0e-4); the logits' scale and the merge undo it.  The own tokens'
+// decode gets the same tables.  Weights go to
+// fp16 (half a step 2^-11); bf16 values are held as fp16 below a power of two of the token,
+// which takes the place of gamma', because bf16 weights would cost a result up to 6e-3 of its
+// row's largest value.  Sums, maxima and denominators are fp32.
 #include <cuda_fp8.h>
 
 #include "tq_async.cuh"
@@ -58,6 +63,9 @@ constexpr int kPNormSlack = 4;                   // log2 units a norm may exceed
 constexpr int kPShift = 3;                       // weights are scaled by 2^3: at most 2^15 in fp16
 
 // Shared memory past the operands (byte offsets from its 1024-aligned start).
+// Operands: 0, 1 the streams' Q (one tile of rows: 1 holds its low part); K in 2 and 3, V in
+// 4 and 5 in two stages, or, when two tiles of rows have low parts, K in 2 and V in 4 in
+// one stage and the low parts in 3 and 5.
 constexpr uint32_t kPOffQ = 0, kPOffK = 2 * kPOperand, kPOffV = 4 * kPOperand, kPOffGk = 6 * kPOperand;
 constexpr uint32_t kPOffGv = kPOffGk + kPNormSlots * kPTile * 4;
 constexpr uint32_t kPOffMask = kPOffGv + kPNormSlots * kPTile * 4;       // u16 [slots][8]
@@ -80,18 +88,33 @@ struct PrefixArgs {
   int rows;        // batch * g: rows of a KV head
   int row_blocks;  // CTAs over the rows of a KV head
   int pair;        // 1: the streams are two tiles of rows; 0: two sets of tiles of tokens
-  int split_q;     // bf16 layers with an fp32 q: the second tile of Q holds its low parts
+  int split_q;     // Q in two parts
+  int stages;      // of K and of V
   int tiles_per_split;
   float scale;     // sm_scale * log2 e
   const float* rot;  // signs, for packed keys (null: q is not rotated)
   int64_t all_rows;  // batch * Hq
   float* part;     // [partials][B * Hq][d]
   float* ml;       // [partials][B * Hq][2]
-  Codebook cbk, cbv;
+  Codebook cbk, cbv;  // centroids times the tables' factors
   unsigned* status;
 };
 
 // ------------------------------------------------------------------ operands
+
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_b2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // fp16 centroids of the upper half of a codebook as byte tables for permutes: entry i < 8,
 // low bytes and high bytes apart.
@@ -202,9 +225,33 @@ __device__ __forceinline__ uint4 chunk_of(const HalfRecord<F>& r, int i, const H
   }
 }
 
+// A power of two above every magnitude of a bf16 token (both lanes of its halves return it):
+// the token is then gamma times fp16 values below 1, exact but for elements under
+// 2^-14 of the largest.
+__device__ __forceinline__ float range_of(const HalfRecord<0>& r) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < HalfRecord<0>::kWords; ++i) m = __vmaxu2(m, r.w[i] & 0x7FFF7FFFu);
+  m = max(m & 0xFFFFu, m >> 16);
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  return __uint_as_float(min(max((m >> 7) + 1u, 1u), 253u) << 23);
+}
+// Eight bf16 values times a power of two, as fp16.
+__device__ __forceinline__ uint4 scaled_half8(const uint4& v, float inv) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 f = __fmul2_rn(make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u)),
+                                make_float2(inv, inv));
+    o[k] = pack_h2(f.x, f.y);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 // The token's half row to the operand at `dst`: panel = half, row = token of the tile,
 // 16-byte chunk c at c ^ (row & 7).
-template <int F>
+template <int F, bool SCALED = false>
 __device__ __forceinline__ void store_half(const HalfRecord<F>& r, uint32_t dst, int row, int half, const HalfTable& t,
                                            bool valid) {
   const uint32_t base = dst + (uint32_t)half * kPPanel + (uint32_t)row * 128u;
@@ -213,26 +260,13 @@ __device__ __forceinline__ void store_half(const HalfRecord<F>& r, uint32_t dst,
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     uint4 v = chunk_of<F>(r, i, t);
+    if constexpr (SCALED) v = scaled_half8(v, __uint_as_float(0x7F000000u - __float_as_uint(r.gamma)));  // 1 / gamma
     if (!valid) v = make_uint4(0u, 0u, 0u, 0u);
     const int c = kSwapped ? i ^ (4 * half) : i;
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(base + (uint32_t)((c ^ (row & 7)) << 4)), "r"(v.x),
                  "r"(v.y), "r"(v.z), "r"(v.w)
                  : "memory");
   }
-}
-
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t pack_b2(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 // A warp's row of Q' (lane: coordinates 4 lane .. 4 lane + 3) to the operand tile at `dst`.
@@ -243,7 +277,8 @@ __device__ __forceinline__ void store_q(uint32_t dst, int row, int lane, uint32_
 }
 
 // The CTA's rows of Q: rotated for packed keys, scaled by a power of two to fp16 (bf16
-// layers: bf16 parts as they are); scale_s[row] gives log2-logits from S.
+// layers: bf16 as they are), the low parts of a split query in a second operand;
+// scale_s[row] gives log2-logits from S.
 template <int KF>
 __device__ __forceinline__ void stage_q(const PrefixArgs& a, int kvh, int r0, uint32_t qdst, float* scale_s, int warp,
                                         int lane) {
@@ -274,12 +309,13 @@ __device__ __forceinline__ void stage_q(const PrefixArgs& a, int kvh, int r0, ui
 #pragma unroll
     for (int k = 0; k < 4; ++k) x[k] *= flip;
     const uint32_t tile = qdst + (uint32_t)(r / kPTile) * kPOperand;
+    const uint32_t low = qdst + (uint32_t)(a.pair ? 3 + 2 * (r / kPTile) : 1) * kPOperand;
     const int tr = r % kPTile;
     if constexpr (KF == 0) {
       const uint32_t w0 = pack_b2(x[0], x[1]), w1 = pack_b2(x[2], x[3]);
       store_q(tile, tr, lane, w0, w1);
       if (a.split_q)
-        store_q(tile + kPOperand, tr, lane,
+        store_q(low, tr, lane,
                 pack_b2(x[0] - __uint_as_float(w0 << 16), x[1] - __uint_as_float(w0 & 0xFFFF0000u)),
                 pack_b2(x[2] - __uint_as_float(w1 << 16), x[3] - __uint_as_float(w1 & 0xFFFF0000u)));
       if (lane == 0) scale_s[r] = fmaxf(fabsf(a.scale), 1e-30f);
@@ -305,7 +341,15 @@ __device__ __forceinline__ void stage_q(const PrefixArgs& a, int kvh, int r0, ui
       // 2^e <= largest coordinate < 2^(e + 1); products with the inverse power are exact
       const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100);
       const float inv = __uint_as_float((uint32_t)(127 - e) << 23), pw = __uint_as_float((uint32_t)(127 + e) << 23);
-      store_q(tile, tr, lane, pack_h2(x[0] * inv, x[1] * inv), pack_h2(x[2] * inv, x[3] * inv));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] *= inv;
+      const uint32_t w0 = pack_h2(x[0], x[1]), w1 = pack_h2(x[2], x[3]);
+      store_q(tile, tr, lane, w0, w1);
+      if (a.split_q) {
+        const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&w0));
+        const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&w1));
+        store_q(low, tr, lane, pack_h2(x[0] - f0.x, x[1] - f0.y), pack_h2(x[2] - f1.x, x[3] - f1.y));
+      }
       if (lane == 0) scale_s[r] = fmaxf(fabsf(a.scale) * pw, 1e-30f);
     }
   }
@@ -354,14 +398,21 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
     for (int i = 0; i < kPNormSlots; ++i) mbar_init(gfull + i, kPProdWarps);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kPSoftWarps + kPProdWarps) tmem_alloc(base + kPOffTmem, 512);
-  else stage_q<KF>(a, kvh, r0, base + kPOffQ, scale_s, warp, lane);
+  if (warp == kPSoftWarps + kPProdWarps) {
+    tmem_alloc(base + kPOffTmem, 512);
+  } else {
+    stage_q<KF>(a, kvh, r0, base + kPOffQ, scale_s, warp, lane);
+  }
   fence_proxy_async();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<const uint32_t*>(gen + kPOffTmem);
   bool ok = true;  // no wait gave up
+  // tile t's stage, and the parity of its use
+  const int two = a.stages - 1;  // 0 or 1
+  auto stage = [&](int t) { return t & two; };
+  auto turn = [&](int t) { return (t >> two) & 1; };
 
   if (warp < kPSoftWarps) {
     // ------------------------------------------------------------- softmax
@@ -419,13 +470,11 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
         // move the reference where a logit or a norm outgrew it
         const float m = mx * rs;
         int e = E;
-        if constexpr (kCodedV) {
+        {
           const int4 e0 = reinterpret_cast<const int4*>(gen + kPOffExp + slot * 32)[0];
           const int4 e1 = reinterpret_cast<const int4*>(gen + kPOffExp + slot * 32)[1];
           const int et = max(max(max(e0.x, e0.y), max(e0.z, e0.w)), max(max(e1.x, e1.y), max(e1.z, e1.w)));
           if (et > E + kPNormSlack) e = et;
-        } else {
-          e = 0;
         }
         const bool move = m > M + kPSlack || (M == -INFINITY && m > -INFINITY);
         if (__any_sync(0xffffffffu, move || e != E)) {
@@ -446,7 +495,7 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
           E = e;
         }
         // weights: 2^(u - M + kPShift - E), u = rs gamma s
-        const float off = (M == -INFINITY ? 0.0f : M) - (kCodedV ? (float)(kPShift - E) : 0.0f);
+        const float off = (M == -INFINITY ? 0.0f : M) - (float)(kPShift - E);
         float2 sum = make_float2(0.0f, 0.0f);
         auto pass2 = [&](uint32_t(&r)[32], int c) {
           uint32_t p[16];
@@ -471,16 +520,11 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
             u0 = make_float2(ex2(u0.x), ex2(u0.y));
             u1 = make_float2(ex2(u1.x), ex2(u1.y));
             sum = __fadd2_rn(sum, __fadd2_rn(u0, u1));
-            if constexpr (kCodedV) {
-              const float4 g = gv4[8 * c + k];
-              u0 = __fmul2_rn(u0, make_float2(g.x, g.y));
-              u1 = __fmul2_rn(u1, make_float2(g.z, g.w));
-              p[2 * k] = pack_h2(u0.x, u0.y);
-              p[2 * k + 1] = pack_h2(u1.x, u1.y);
-            } else {
-              p[2 * k] = pack_b2(u0.x, u0.y);
-              p[2 * k + 1] = pack_b2(u1.x, u1.y);
-            }
+            const float4 g = gv4[8 * c + k];
+            u0 = __fmul2_rn(u0, make_float2(g.x, g.y));
+            u1 = __fmul2_rn(u1, make_float2(g.z, g.w));
+            p[2 * k] = pack_h2(u0.x, u0.y);
+            p[2 * k + 1] = pack_h2(u1.x, u1.y);
           }
           tmem_st16(ts + 16 * c, p);  // over logits that have been read
         };
@@ -512,7 +556,7 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
       const int64_t row = pi * a.all_rows + (int64_t)(r / a.g) * a.Hq + kvh * a.g + r % a.g;
       const bool any = ok && M != -INFINITY;
       if (r < a.rows) {
-        a.ml[2 * row] = any ? M - (kCodedV ? (float)(kPShift - E) : 0.0f) : -INFINITY;
+        a.ml[2 * row] = any ? M - (float)(kPShift - E) : -INFINITY;
         a.ml[2 * row + 1] = any ? l : 0.0f;
       }
       if (ok && count > 0) {
@@ -561,21 +605,22 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
       fetch_v(0, id);
     }
     for (int t = 0; t < n && ok; ++t) {
-      const int st = t & 1, slot = t & (kPNormSlots - 1);
+      const int st = stage(t), slot = t & (kPNormSlots - 1);
       const bool valid = valid_token(t, id);
       if (lane == 0 && (id < 0 || id >= a.num_blocks) && (tile0 + t) * kPBlocks + w < blocks)
         flag_status(a.status, TQ_DEV_BAD_BLOCK);
       const int id_after = block_id(t + 2);
-      if (t >= 2) ok = mbar_wait(kempty + st, ((t >> 1) - 1) & 1);
+      if (t >= a.stages) ok = mbar_wait(kempty + st, turn(t) ^ 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
+      if constexpr (VF == 0) rv.gamma = range_of(rv);
       // norms, mask and the norms' largest exponent of the block
       if (half == 0) {
         gk[slot * kPTile + row] = rk.gamma;
         gv[slot * kPTile + row] = rv.gamma;
       }
       const uint32_t vb = __ballot_sync(0xffffffffu, valid && half == 0);  // bit 2 tok
-      if constexpr (kCodedV) {
+      {
         int e = valid ? (int)((__float_as_uint(rv.gamma) >> 23) & 255u) - 126 : -126;  // gamma < 2^e
 #pragma unroll
         for (int m = 16; m > 0; m >>= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, m));
@@ -597,10 +642,10 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
         mbar_arrive(kfull + st);
       }
       if (t + 1 < n) fetch_k(t + 1, id_next);
-      if (t >= 2) ok = mbar_wait(vempty + st, ((t >> 1) - 1) & 1);
+      if (t >= a.stages) ok = mbar_wait(vempty + st, turn(t) ^ 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      store_half<VF>(rv, base + kPOffV + (uint32_t)st * kPOperand, row, half, tv, valid);
+      store_half<VF, VF == 0>(rv, base + kPOffV + (uint32_t)st * kPOperand, row, half, tv, valid);
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(vfull + st);
@@ -610,15 +655,14 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
     }
   } else if (lane == 0) {
     // ------------------------------------------------------------------ MMA
-    constexpr bool kBf16K = KF == 0, kBf16V = VF == 0;
-    constexpr uint32_t idesc_s = umma_idesc_16(kBf16K, false, kPTile, kPTile);
-    constexpr uint32_t idesc_o = umma_idesc_16(kBf16V, true, kPTile, kPTile);
+    constexpr uint32_t idesc_s = umma_idesc_16(KF == 0, false, kPTile, kPTile);
+    constexpr uint32_t idesc_o = umma_idesc_16(false, true, kPTile, kPTile);
     const uint64_t dq = umma_desc_sw128(base + kPOffQ), dk = umma_desc_sw128(base + kPOffK);
     const uint64_t dv = umma_desc_sw128_mn(base + kPOffV, kPPanel);
     auto tile_of = [&](int i, int s) { return a.pair ? i : 2 * i + s; };
     auto logits = [&](int i, int s) {  // S_s = Q_s K^T
-      const int t = tile_of(i, s), st = t & 1;
-      if (!mbar_wait(kfull + st, (t >> 1) & 1)) return false;
+      const int t = tile_of(i, s), st = stage(t);
+      if (!mbar_wait(kfull + st, turn(t))) return false;
       tc_fence_after();
       const uint64_t q = dq + (uint64_t)((a.pair ? s : 0) * (kPOperand >> 4));
       const uint64_t k = dk + (uint64_t)(st * (kPOperand >> 4));
@@ -627,11 +671,12 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
         const uint64_t off = (uint64_t)((j >> 2) * (kPPanel >> 4) + (j & 3) * 2);
         umma_bf16(tmem + (uint32_t)(s * kPTile), q + off, k + off, idesc_s, j > 0);
       }
-      if (KF == 0 && a.split_q) {
+      if (a.split_q) {
+        const uint64_t low = dq + (uint64_t)((a.pair ? 3 + 2 * s : 1) * (kPOperand >> 4));
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const uint64_t off = (uint64_t)((j >> 2) * (kPPanel >> 4) + (j & 3) * 2);
-          umma_bf16(tmem + (uint32_t)(s * kPTile), q + (kPOperand >> 4) + off, k + off, idesc_s, true);
+          umma_bf16(tmem + (uint32_t)(s * kPTile), low + off, k + off, idesc_s, true);
         }
       }
       umma_commit(smem_u32(sfull + s));
@@ -639,8 +684,8 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
       return true;
     };
     auto values = [&](int i, int s) {  // O_s += P_s V
-      const int t = tile_of(i, s), st = t & 1;
-      if (!mbar_wait(pfull + s, i & 1) || !mbar_wait(vfull + st, (t >> 1) & 1)) return false;
+      const int t = tile_of(i, s), st = stage(t);
+      if (!mbar_wait(pfull + s, i & 1) || !mbar_wait(vfull + st, turn(t))) return false;
       tc_fence_after();
       const uint64_t v = dv + (uint64_t)(st * (kPOperand >> 4));
 #pragma unroll
@@ -680,6 +725,7 @@ struct MergeArgs {
   UnitMap um;
   int64_t rows;      // B * Hq
   const float* rot;  // signs of the inverse rotation (null: none)
+  float value_scale; // 1 / the factor of the values' table
   void* out;
   int out_bf16;
 };
@@ -715,7 +761,7 @@ __global__ void __launch_bounds__(128) k_prefix_merge(const MergeArgs a) {
   for (int s = 0; s < a.own_splits; ++s)
     if (slot_live(unit, a.own_splits, s, a.um.nw))
       join(a.own_part + (row * a.own_splits + s) * kD, a.own_ml + (row * a.own_splits + s) * 2);
-  const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+  const float inv = L > 0.0f ? a.value_scale / L : 0.0f;
 #pragma unroll
   for (int k = 0; k < 4; ++k) y[k] *= inv;
   if (a.rot) {  // Pi^T y = D H y / sqrt(d): bits 0, 1 in the lane, bits 2..6 across lanes
@@ -747,12 +793,11 @@ __global__ void __launch_bounds__(128) k_prefix_merge(const MergeArgs a) {
 struct PrefixPlan {
   int pair, row_blocks, splits, tiles_per_split, partials;
 };
-static PrefixPlan prefix_plan(const tq_cache_desc& d, int batch, int num_q_heads, int64_t len, int num_sms,
-                              bool split_q) {
+static PrefixPlan prefix_plan(const tq_cache_desc& d, int batch, int num_q_heads, int64_t len, int num_sms) {
   PrefixPlan p = {};
   if (len < 1) return p;
   const int64_t rows = (int64_t)batch * (num_q_heads / d.num_kv_heads);
-  p.pair = rows > kPTile && !split_q ? 1 : 0;
+  p.pair = rows > kPTile ? 1 : 0;
   const int per_cta = p.pair ? 2 * kPTile : kPTile;
   p.row_blocks = (int)((rows + per_cta - 1) / per_cta);
   const int64_t units = (int64_t)p.row_blocks * d.num_kv_heads;
@@ -776,10 +821,7 @@ static PrefixPlan prefix_plan(const tq_cache_desc& d, int batch, int num_q_heads
 
 size_t prefix_partial_bytes(const tq_cache_desc& d, int batch, int num_q_heads, int64_t prefix_len, int num_sms) {
   const size_t rows = (size_t)batch * num_q_heads;
-  // (the type of q is not known here: the larger of the two plans)
-  const int a = prefix_plan(d, batch, num_q_heads, prefix_len, num_sms, false).partials;
-  const int b = d.fmt.kv_format == TQ_KV_BF16 ? prefix_plan(d, batch, num_q_heads, prefix_len, num_sms, true).partials : 0;
-  return (size_t)(a > b ? a : b) * rows * (kD + 2) * sizeof(float);
+  return (size_t)prefix_plan(d, batch, num_q_heads, prefix_len, num_sms).partials * rows * (kD + 2) * sizeof(float);
 }
 
 template <int KF, int VF>
@@ -809,6 +851,9 @@ cudaError_t launch_prefix_decode(const PrefixCall& c, cudaStream_t st) {
   m.um = unit_map(d, c.own.num_q_heads);
   m.rows = rows;
   m.rot = coded ? d.rotation : nullptr;
+  const float fk = d.fmt.kv_format == TQ_KV_PACKED ? table_factor(d.centroids_k, d.fmt.bits_k) : 1.0f;
+  const float fv = coded ? table_factor(d.centroids_v, d.fmt.bits_v) : 1.0f;
+  m.value_scale = 1.0f / fv;
   m.out = c.own.out;
   m.out_bf16 = c.own.out_dtype == TQ_BF16 ? 1 : 0;
   size_t off = kCounterRegionBytes;
@@ -821,8 +866,9 @@ cudaError_t launch_prefix_decode(const PrefixCall& c, cudaStream_t st) {
   }
   if (c.prefix_len > 0) {
     PrefixArgs a = {};
-    a.split_q = d.fmt.kv_format == TQ_KV_BF16 && c.own.q_dtype == TQ_F32 ? 1 : 0;
-    const PrefixPlan p = prefix_plan(d, c.own.batch, c.own.num_q_heads, c.prefix_len, c.num_sms, a.split_q != 0);
+    const PrefixPlan p = prefix_plan(d, c.own.batch, c.own.num_q_heads, c.prefix_len, c.num_sms);
+    a.split_q = d.fmt.kv_format == TQ_KV_PACKED || c.own.q_dtype == TQ_F32 ? 1 : 0;
+    a.stages = p.pair && a.split_q ? 1 : 2;
     a.kpool = reinterpret_cast<const uint8_t*>(d.k_cache);
     a.vpool = reinterpret_cast<const uint8_t*>(d.v_cache);
     a.num_blocks = d.num_blocks;
@@ -837,13 +883,17 @@ cudaError_t launch_prefix_decode(const PrefixCall& c, cudaStream_t st) {
     a.row_blocks = p.row_blocks;
     a.pair = p.pair;
     a.tiles_per_split = p.tiles_per_split;
-    a.scale = c.own.sm_scale * 1.4426950408889634f;
+    a.scale = c.own.sm_scale * 1.4426950408889634f / fk;
     a.rot = d.rotation;
     a.all_rows = rows;
     a.part = reinterpret_cast<float*>(c.own.workspace + off);
     a.ml = a.part + (size_t)p.partials * rows * kD;
     a.cbk = codebook_of(d, 0);
     a.cbv = codebook_of(d, 1);
+    for (int i = 0; i < 16; ++i) {
+      a.cbk.c[i] *= fk;
+      a.cbv.c[i] *= fv;
+    }
     a.status = c.own.status;
     cudaError_t e;
     if (d.fmt.kv_format == TQ_KV_BF16) {
@@ -864,6 +914,8 @@ cudaError_t launch_prefix_decode(const PrefixCall& c, cudaStream_t st) {
   if (c.own.max_blocks > 0) {
     DecodeCall own = c.own;
     own.partials_only = true;
+    own.factor_k = fk;
+    own.factor_v = fv;
     const cudaError_t e = launch_decode(own, st);
     if (e != cudaSuccess) return e;
   }
