@@ -13,19 +13,21 @@
 // k_prefix: one CTA per SM, two "streams" of 128 rows x 128 tokens through the
 // fifth-generation tensor cores.
 //   8 producer warps  turn 8 blocks (128 tokens) of K and V pages into 16-bit operands in
-//                     shared memory, two stages each: bf16 pages as they are, codes as
-//                     fp16 centroids by byte permutes from tables in registers (a centroid
-//                     table is antisymmetric: magnitude lookup, then the sign bit), FP8
-//                     keys as fp16.  The norms gamma stay fp32 and are applied to the
-//                     logits and to the weights.
+//                     shared memory: bf16 keys as they are, codes as fp16 centroids by
+//                     byte permutes from tables in registers (a centroid table is
+//                     antisymmetric: magnitude lookup, then the sign bit), FP8 keys as
+//                     fp16.  Key norms stay fp32 and scale the logits; value norms go into
+//                     V's operand.
 //   1 MMA warp        S = Q' K^T (A, B in shared memory), O += P V (A = P in tensor
 //                     memory), one elected thread.
-//   8 softmax warps   a thread a row: two passes over the row's 128 logits in tensor memory
-//                     (the maximum; then base-2 weights, written back as 16-bit P over S).
-//                     The reference moves only when a logit exceeds it by 2^8, so the
-//                     accumulator is rarely rescaled; the weights gamma' 2^(s - M) carry a
-//                     common power of two that keeps them in fp16's range whatever the
-//                     values' norms.
+//   8 softmax warps   a thread a row: the maximum of its 128 logits from tensor memory, then
+//                     base-2 weights, written back as 16-bit P over S.
+// Scales.  A tile's values are normalised by a power of two 2^et above its norms, so that V's
+// operand and P both fit fp16 whatever the norms are; a row keeps one reference C for
+// weight times value, and P = 2^(u + et - C + shift) for a log2-logit u = g_t s_t, where g_t
+// holds the key's norm and every scale.  C moves, and the accumulator is rescaled, only when
+// a row's largest u + et exceeds it by 8; whether it may is decided from the largest raw
+// logit and the tile's largest and smallest g, the exact maximum being taken only then.
 // With more than 128 rows a KV head the streams are two tiles of rows over the same
 // tokens; with fewer they share the rows and take every other tile of tokens, each with an
 // accumulator of its own (two partials).
@@ -35,10 +37,9 @@
 // after a common factor in [1, 2) that the host chooses so that the table's few magnitudes
 // lie next to fp16 values (largest relative error of a 4-bit table 3.0e-4 -> 1.2e-4, of a
 // 3-bit one 2.3e-4 -> 1.0e-4); the logits' scale and the merge undo it.  The own tokens'
-// decode gets the same tables.  Weights go to
-// fp16 (half a step 2^-11); bf16 values are held as fp16 below a power of two of the token,
-// which takes the place of gamma', because bf16 weights would cost a result up to 6e-3 of its
-// row's largest value.  Sums, maxima and denominators are fp32.
+// decode gets the same tables.  Weights and values go to fp16 (half a step 2^-11 each), also
+// in bf16 layers, where bf16 weights would cost a result up to 6e-3 of its row's largest
+// value.  Sums, maxima and denominators are fp32.
 #include <cuda_fp8.h>
 
 #include "tq_async.cuh"
@@ -58,23 +59,25 @@ constexpr int kPThreads = (kPSoftWarps + kPProdWarps + 1) * 32;
 constexpr uint32_t kPPanel = kPTile * 128;       // 128 rows of 64 16-bit elements, swizzled
 constexpr uint32_t kPOperand = 2 * kPPanel;      // a 128 x 128 operand
 constexpr int kPNormSlots = 4;                   // tiles whose norms and masks are kept
-constexpr float kPSlack = 8.0f;                  // log2 units a logit may exceed the reference
-constexpr int kPNormSlack = 4;                   // log2 units a norm may exceed its reference
-constexpr int kPShift = 3;                       // weights are scaled by 2^3: at most 2^15 in fp16
+constexpr float kPSlack = 8.0f;                  // log2 units u + et may exceed a row's reference
+constexpr float kPShift = 6.0f;                  // P is at most 2^14
+constexpr int kPMinExp = -60;                    // smallest et: values below are as good as zero
 
-// Shared memory past the operands (byte offsets from its 1024-aligned start).
-// Operands: 0, 1 the streams' Q (one tile of rows: 1 holds its low part); K in 2 and 3, V in
-// 4 and 5 in two stages, or, when two tiles of rows have low parts, K in 2 and V in 4 in
-// one stage and the low parts in 3 and 5.
-constexpr uint32_t kPOffQ = 0, kPOffK = 2 * kPOperand, kPOffV = 4 * kPOperand, kPOffGk = 6 * kPOperand;
-constexpr uint32_t kPOffGv = kPOffGk + kPNormSlots * kPTile * 4;
-constexpr uint32_t kPOffMask = kPOffGv + kPNormSlots * kPTile * 4;       // u16 [slots][8]
-constexpr uint32_t kPOffExp = kPOffMask + kPNormSlots * 16;              // int [slots][8]
-constexpr uint32_t kPOffScale = kPOffExp + kPNormSlots * 32;             // float [256]
-constexpr uint32_t kPOffBar = kPOffScale + 2 * kPTile * 4;
+// Shared memory (byte offsets): operands of 32 KB -- the streams' Q in 0 and 1; low parts of
+// Q in 2 and 3 when two tiles of rows have them (of one tile: in 1); K in two stages; V in
+// what is left, two stages or, with two tiles of low parts, one -- then the rest.
+constexpr int kPOperands = 7;
+constexpr uint32_t kPOffG = kPOperands * kPOperand;                  // float [slots][128]: g_t
+constexpr uint32_t kPOffMask = kPOffG + kPNormSlots * kPTile * 4;    // u16 [slots][8]
+constexpr uint32_t kPOffExp = kPOffMask + kPNormSlots * 16;          // s8 [slots][8]: et of each block
+constexpr uint32_t kPOffHi = kPOffExp + kPNormSlots * 8;             // bf16 [slots][8]: upper bounds of g
+constexpr uint32_t kPOffLo = kPOffHi + kPNormSlots * 16;             // bf16 [slots][8]: lower bounds of g
+constexpr uint32_t kPOffBar = kPOffLo + kPNormSlots * 16;
 constexpr int kPBars = 2 + 2 + 2 + 2 + kPNormSlots + 2 + 2 + 2;
 constexpr uint32_t kPOffTmem = kPOffBar + kPBars * 8;
-constexpr uint32_t kPSmem = kPOffTmem + 16 + 1024;  // 1024: alignment of the start
+constexpr uint32_t kPOffMax = kPOffTmem + 4;                         // u32: largest |q|
+constexpr uint32_t kPSmem = kPOffTmem + 8;
+static_assert(kPSmem <= 232448, "the shared memory of one CTA an SM");
 
 struct PrefixArgs {
   const uint8_t* kpool;
@@ -89,10 +92,10 @@ struct PrefixArgs {
   int row_blocks;  // CTAs over the rows of a KV head
   int pair;        // 1: the streams are two tiles of rows; 0: two sets of tiles of tokens
   int split_q;     // Q in two parts
-  int stages;      // of K and of V
+  int v_stages;    // 2 or 1
   int tiles_per_split;
   float scale;     // sm_scale * log2 e
-  const float* rot;  // signs, for packed keys (null: q is not rotated)
+  const float* rot;  // signs, for packed keys
   int64_t all_rows;  // batch * Hq
   float* part;     // [partials][B * Hq][d]
   float* ml;       // [partials][B * Hq][2]
@@ -109,11 +112,6 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
 __device__ __forceinline__ uint32_t pack_b2(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 // fp16 centroids of the upper half of a codebook as byte tables for permutes: entry i < 8,
@@ -225,16 +223,12 @@ __device__ __forceinline__ uint4 chunk_of(const HalfRecord<F>& r, int i, const H
   }
 }
 
-// A power of two above every magnitude of a bf16 token (both lanes of its halves return it):
-// the token is then gamma times fp16 values below 1, exact but for elements under
-// 2^-14 of the largest.
-__device__ __forceinline__ float range_of(const HalfRecord<0>& r) {
+// Exponent e with every magnitude of the lane's half of a bf16 token below 2^e.
+__device__ __forceinline__ int range_of(const HalfRecord<0>& r) {
   uint32_t m = 0u;
 #pragma unroll
   for (int i = 0; i < HalfRecord<0>::kWords; ++i) m = __vmaxu2(m, r.w[i] & 0x7FFF7FFFu);
-  m = max(m & 0xFFFFu, m >> 16);
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  return __uint_as_float(min(max((m >> 7) + 1u, 1u), 253u) << 23);
+  return (int)(max(m & 0xFFFFu, m >> 16) >> 7) - 126;
 }
 // Eight bf16 values times a power of two, as fp16.
 __device__ __forceinline__ uint4 scaled_half8(const uint4& v, float inv) {
@@ -250,18 +244,30 @@ __device__ __forceinline__ uint4 scaled_half8(const uint4& v, float inv) {
 }
 
 // The token's half row to the operand at `dst`: panel = half, row = token of the tile,
-// 16-byte chunk c at c ^ (row & 7).
-template <int F, bool SCALED = false>
+// 16-byte chunk c at c ^ (row & 7).  Values (VALUES) times `scale`: codes by the token's
+// scaled norm in fp16, bf16 values by a power of two.
+template <int F, bool VALUES>
 __device__ __forceinline__ void store_half(const HalfRecord<F>& r, uint32_t dst, int row, int half, const HalfTable& t,
-                                           bool valid) {
+                                           float scale) {
   const uint32_t base = dst + (uint32_t)half * kPPanel + (uint32_t)row * 128u;
   // formats loaded in 16-byte pieces of two or more hold their upper part first for half 1
   constexpr bool kSwapped = F != 3 && HalfRecord<F>::kBytes >= 32;
+  // a norm in two fp16 parts, so that a centroid times it is rounded once
+  const __half2 s2 = __float2half2_rn(scale), s2l = __float2half2_rn(scale - __low2float(s2));
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     uint4 v = chunk_of<F>(r, i, t);
-    if constexpr (SCALED) v = scaled_half8(v, __uint_as_float(0x7F000000u - __float_as_uint(r.gamma)));  // 1 / gamma
-    if (!valid) v = make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (VALUES && F == 0) {
+      v = scaled_half8(v, scale);
+    } else if constexpr (VALUES) {
+      uint32_t* w = &v.x;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const __half2 c2 = *reinterpret_cast<const __half2*>(w + k);
+        const __half2 h = __hfma2(c2, s2, __hmul2(c2, s2l));
+        w[k] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
     const int c = kSwapped ? i ^ (4 * half) : i;
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(base + (uint32_t)((c ^ (row & 7)) << 4)), "r"(v.x),
                  "r"(v.y), "r"(v.z), "r"(v.w)
@@ -269,90 +275,102 @@ __device__ __forceinline__ void store_half(const HalfRecord<F>& r, uint32_t dst,
   }
 }
 
-// A warp's row of Q' (lane: coordinates 4 lane .. 4 lane + 3) to the operand tile at `dst`.
-__device__ __forceinline__ void store_q(uint32_t dst, int row, int lane, uint32_t w0, uint32_t w1) {
-  const uint32_t addr = dst + (uint32_t)(lane >> 4) * kPPanel + (uint32_t)row * 128u +
-                        (uint32_t)((((lane & 15) >> 1) ^ (row & 7)) << 4) + (uint32_t)(lane & 1) * 8u;
-  asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(addr), "r"(w0), "r"(w1) : "memory");
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
-// The CTA's rows of Q: rotated for packed keys, scaled by a power of two to fp16 (bf16
-// layers: bf16 as they are), the low parts of a split query in a second operand;
-// scale_s[row] gives log2-logits from S.
-template <int KF>
-__device__ __forceinline__ void stage_q(const PrefixArgs& a, int kvh, int r0, uint32_t qdst, float* scale_s, int warp,
-                                        int lane) {
-  constexpr int kWarps = kPSoftWarps + kPProdWarps;
-  const int rows = a.pair ? 2 * kPTile : kPTile;
-  float sg[4] = {1.0f, 1.0f, 1.0f, 1.0f};
-  if (KF >= 2 && KF <= 4) {
+// Rows of Q, a quad of lanes a row, lane q holding coordinates [32 q, 32 q + 32).  load_q
+// keeps the CTA's rows as loaded and returns the largest magnitude; place_q rotates them for
+// packed keys, scales them by `inv` (a power of two) and writes fp16 parts (bf16 layers:
+// bf16 as they are) to the operands.
+template <bool BF16>
+struct QRows {
+  uint32_t w[2][BF16 ? 16 : 32];
+};
+template <bool BF16>
+__device__ __forceinline__ float load_q(QRows<BF16>& x, const PrefixArgs& a, int kvh, int r0, int warp, int lane) {
+  uint32_t mx = 0u;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) sg[k] = __ldg(a.rot + 4 * lane + k) * 0.08838834764831845f;
-  }
-  const float flip = a.scale < 0.0f ? -1.0f : 1.0f;  // the rows' scales are positive
-#pragma unroll 4
-  for (int r = warp; r < rows; r += kWarps) {
-    float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (r0 + r < a.rows) {
-      const int64_t row = (int64_t)((r0 + r) / a.g) * a.Hq + kvh * a.g + (r0 + r) % a.g;
-      if (a.q_bf16) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(a.q) + row * kD) + lane);
-        x[0] = __uint_as_float(v.x << 16);
-        x[1] = __uint_as_float(v.x & 0xFFFF0000u);
-        x[2] = __uint_as_float(v.y << 16);
-        x[3] = __uint_as_float(v.y & 0xFFFF0000u);
-      } else {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.q) + row * kD) + lane);
-        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-      }
+  for (int h = 0; h < 2; ++h) {
+    if (h == 1 && !a.pair) break;
+    const int r = r0 + h * kPTile + 8 * warp + (lane >> 2);
+    const int rr = min(r, a.rows - 1), b = rr / a.g;
+    const int64_t row = (int64_t)b * a.Hq + kvh * a.g + (rr - b * a.g);
+    const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(a.q) + (row * kD + 32 * (lane & 3)) * (BF16 ? 2 : 4));
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 4 : 8); ++i) {
+      const uint4 v = __ldg(src + i);
+      x.w[h][4 * i] = v.x; x.w[h][4 * i + 1] = v.y; x.w[h][4 * i + 2] = v.z; x.w[h][4 * i + 3] = v.w;
     }
+  }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) x[k] *= flip;
-    const uint32_t tile = qdst + (uint32_t)(r / kPTile) * kPOperand;
-    const uint32_t low = qdst + (uint32_t)(a.pair ? 3 + 2 * (r / kPTile) : 1) * kPOperand;
-    const int tr = r % kPTile;
-    if constexpr (KF == 0) {
-      const uint32_t w0 = pack_b2(x[0], x[1]), w1 = pack_b2(x[2], x[3]);
-      store_q(tile, tr, lane, w0, w1);
-      if (a.split_q)
-        store_q(low, tr, lane,
-                pack_b2(x[0] - __uint_as_float(w0 << 16), x[1] - __uint_as_float(w0 & 0xFFFF0000u)),
-                pack_b2(x[2] - __uint_as_float(w1 << 16), x[3] - __uint_as_float(w1 & 0xFFFF0000u)));
-      if (lane == 0) scale_s[r] = fmaxf(fabsf(a.scale), 1e-30f);
-    } else {
-      if constexpr (KF >= 2 && KF <= 4) {  // H D x / sqrt(d): bits 0, 1 in the lane, bits 2..6 across lanes
+  for (int h = 0; h < 2; ++h) {
+    if (h == 1 && !a.pair) break;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] *= sg[k];
-        const float t0 = x[0] + x[1], t1 = x[0] - x[1], t2 = x[2] + x[3], t3 = x[2] - x[3];
-        x[0] = t0 + t2; x[2] = t0 - t2; x[1] = t1 + t3; x[3] = t1 - t3;
+    for (int i = 0; i < (BF16 ? 16 : 32); ++i) {
+      if (BF16) mx = max(mx, max(x.w[h][i] << 16 & 0x7FFF0000u, x.w[h][i] & 0x7FFF0000u));
+      else mx = max(mx, x.w[h][i] & 0x7FFFFFFFu);
+    }
+  }
+  return __uint_as_float(mx);
+}
+template <int KF, bool BF16>
+__device__ __forceinline__ void place_q(const QRows<BF16>& q, const PrefixArgs& a, int r0, uint32_t base, float inv,
+                                        uint32_t signs, int warp, int lane) {
+  const int quad = lane & 3;
 #pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-          const bool upper = (lane & m) != 0;
+  for (int h = 0; h < 2; ++h) {
+    if (h == 1 && !a.pair) break;
+    const int tr = 8 * warp + (lane >> 2);
+    const bool live = r0 + h * kPTile + tr < a.rows;
+    float x[32];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float o = __shfl_xor_sync(0xffffffffu, x[k], m);
-            x[k] = upper ? (o - x[k]) : (x[k] + o);
-          }
+    for (int i = 0; i < 32; ++i) {
+      const uint32_t w = BF16 ? (i & 1 ? q.w[h][i >> 1] & 0xFFFF0000u : q.w[h][i >> 1] << 16) : q.w[h][BF16 ? 0 : i];
+      x[i] = live ? __uint_as_float(w) * inv : 0.0f;
+      if (KF >= 2 && KF <= 4) x[i] = __uint_as_float(__float_as_uint(x[i]) ^ ((signs << (31 - i)) & 0x80000000u));
+    }
+    if (KF >= 2 && KF <= 4) {
+      fwht128_quad_f2(x, quad);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] *= 0.08838834764831845f;  // 1 / sqrt(128)
+    }
+    const uint32_t row = (uint32_t)(quad >> 1) * kPPanel + (uint32_t)tr * 128u;
+    const uint32_t hi = base + (uint32_t)h * kPOperand + row;
+    const uint32_t lo = base + (uint32_t)(a.pair ? 2 + h : 1) * kPOperand + row;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t w[4], v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float x0 = x[8 * c + 2 * k], x1 = x[8 * c + 2 * k + 1];
+        if (KF == 0) {
+          w[k] = pack_b2(x0, x1);
+          v[k] = pack_b2(x0 - __uint_as_float(w[k] << 16), x1 - __uint_as_float(w[k] & 0xFFFF0000u));
+        } else {
+          w[k] = pack_h2(x0, x1);
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+          v[k] = pack_h2(x0 - f.x, x1 - f.y);
         }
       }
-      float mx = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-#pragma unroll
-      for (int m = 16; m > 0; m >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
-      // 2^e <= largest coordinate < 2^(e + 1); products with the inverse power are exact
-      const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100);
-      const float inv = __uint_as_float((uint32_t)(127 - e) << 23), pw = __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] *= inv;
-      const uint32_t w0 = pack_h2(x[0], x[1]), w1 = pack_h2(x[2], x[3]);
-      store_q(tile, tr, lane, w0, w1);
-      if (a.split_q) {
-        const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&w0));
-        const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&w1));
-        store_q(low, tr, lane, pack_h2(x[0] - f0.x, x[1] - f0.y), pack_h2(x[2] - f1.x, x[3] - f1.y));
-      }
-      if (lane == 0) scale_s[r] = fmaxf(fabsf(a.scale) * pw, 1e-30f);
+      const uint32_t off = (uint32_t)(((4 * (quad & 1) + c) ^ (tr & 7)) << 4);
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(hi + off), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                   : "memory");
+      if (a.split_q)
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(lo + off), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                     : "memory");
     }
   }
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
 }
 
 // --------------------------------------------------------------- the kernel
@@ -362,13 +380,13 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
   constexpr bool kCodedK = KF >= 2 && KF <= 4, kCodedV = VF != 0;
   constexpr int kpage = KF == 0 ? kBlock * kD * 2 : (KF == 8 ? kBlock * kD : kBlock * (kD * KF / 8 + 4));
   constexpr int vpage = VF == 0 ? kBlock * kD * 2 : kBlock * (kD * VF / 8 + 4);
-  extern __shared__ unsigned char smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  unsigned char* const gen = smem_raw + (base - raw);
-  float* const gk = reinterpret_cast<float*>(gen + kPOffGk);
-  float* const gv = reinterpret_cast<float*>(gen + kPOffGv);
-  float* const scale_s = reinterpret_cast<float*>(gen + kPOffScale);
+  extern __shared__ __align__(128) unsigned char gen[];
+  const uint32_t base = smem_u32(gen);
+  if (base & 1023u) {  // (uniform) the swizzled operands need it; the window starts so on sm_103a
+    if (threadIdx.x == 0) flag_status(a.status, TQ_DEV_LAYOUT);
+    return;
+  }
+  float* const gs = reinterpret_cast<float*>(gen + kPOffG);
   uint64_t* const bars = reinterpret_cast<uint64_t*>(gen + kPOffBar);
   uint64_t *const kfull = bars, *const kempty = bars + 2, *const vfull = bars + 4, *const vempty = bars + 6;
   uint64_t* const gfull = bars + 8;                 // [kPNormSlots]
@@ -385,6 +403,9 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
   // stream s: tiles i (pair) or 2 i + s, i < count(s)
   const int count0 = a.pair ? n : (n + 1) / 2, count1 = a.pair ? n : n / 2;
 
+  // operands: K stage s at k_op + s, V stage s at v_op + s
+  const uint32_t k_op = base + (uint32_t)(a.v_stages == 1 ? 4 : 2) * kPOperand, v_op = k_op + 2 * kPOperand;
+  uint32_t* const qmax = reinterpret_cast<uint32_t*>(gen + kPOffMax);
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(kfull + i, kPProdWarps);
@@ -397,22 +418,52 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
     }
     for (int i = 0; i < kPNormSlots; ++i) mbar_init(gfull + i, kPProdWarps);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    *qmax = 0u;
   }
-  if (warp == kPSoftWarps + kPProdWarps) {
-    tmem_alloc(base + kPOffTmem, 512);
-  } else {
-    stage_q<KF>(a, kvh, r0, base + kPOffQ, scale_s, warp, lane);
+  __syncthreads();
+  // the CTA's rows of Q, by one power of two (2^qe > largest |q|; |Pi q| may be 11.4 times it)
+  float qscale = 1.0f;
+  {
+    constexpr int kSpare = KF >= 2 && KF <= 4 ? 4 : 0;
+    const bool mma_warp = warp == kPSoftWarps + kPProdWarps;
+    QRows<true> q16;
+    QRows<false> q32;
+    uint32_t signs = 0u;
+    if (mma_warp) {
+      tmem_alloc(base + kPOffTmem, 512);
+    } else {
+      if (KF >= 2 && KF <= 4) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t m = __ballot_sync(0xffffffffu, __ldg(a.rot + 32 * k + lane) < 0.0f);
+          if ((lane & 3) == k) signs = m;
+        }
+      }
+      const float mx = a.q_bf16 ? load_q<true>(q16, a, kvh, r0, warp, lane) : load_q<false>(q32, a, kvh, r0, warp, lane);
+      const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
+      if (lane == 0) atomicMax(qmax, m);
+    }
+    __syncthreads();
+    const int qe = KF == 0 ? 0 : min(max((int)(*qmax >> 23) - 126 + kSpare, -100), 100);
+    qscale = __uint_as_float((uint32_t)(127 + qe) << 23);
+    // (a negative sm_scale turns the queries, so that every g is positive)
+    const float inv = (a.scale < 0.0f ? -1.0f : 1.0f) * __uint_as_float((uint32_t)(127 - qe) << 23);
+    if (!mma_warp) {
+      if (a.q_bf16) place_q<KF, true>(q16, a, r0, base, inv, signs, warp, lane);
+      else place_q<KF, false>(q32, a, r0, base, inv, signs, warp, lane);
+    }
   }
+  const float rs = fmaxf(fabsf(a.scale) * qscale, 1e-30f);  // log2-logit of an S of one
   fence_proxy_async();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<const uint32_t*>(gen + kPOffTmem);
   bool ok = true;  // no wait gave up
-  // tile t's stage, and the parity of its use
-  const int two = a.stages - 1;  // 0 or 1
-  auto stage = [&](int t) { return t & two; };
-  auto turn = [&](int t) { return (t >> two) & 1; };
+  // a tile's stage of V, and the parity of its use (of K: t & 1 and (t >> 1) & 1)
+  const int vbit = a.v_stages - 1;
+  auto vstage = [&](int t) { return t & vbit; };
+  auto vturn = [&](int t) { return (t >> vbit) & 1; };
 
   if (warp < kPSoftWarps) {
     // ------------------------------------------------------------- softmax
@@ -422,9 +473,7 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
     const int count = s ? count1 : count0;
     const int trow = a.pair ? s * kPTile + 32 * w : 32 * w;  // the warp's first row of the CTA's rows
     const bool live = r0 + trow < a.rows;  // (whole warps of padding rows only take part in the barriers)
-    const float rs = scale_s[trow + lane];
-    float M = -INFINITY, l = 0.0f;  // reference in log2 units; sum of weights 2^(s - M + kPShift - E)
-    int E = -1000;                  // power of two of the norms' reference
+    float C = -INFINITY, l = 0.0f;  // reference of u + et; sum of 2^(u - C + shift)
     for (int i = 0; i < count && ok; ++i) {
       const int t = a.pair ? i : 2 * i + s, slot = t & (kPNormSlots - 1);
       ok = mbar_wait(gfull + slot, (t / kPNormSlots) & 1) && mbar_wait(sfull + s, i & 1);
@@ -433,96 +482,102 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
       tc_fence_after();
       if (live) {
         const uint4 mw = *reinterpret_cast<const uint4*>(gen + kPOffMask + slot * 16);
-        const bool whole = (mw.x & mw.y & mw.z & mw.w) == 0xFFFFFFFFu;  // no masked token in the tile
-        const uint32_t mword[4] = {mw.x, mw.y, mw.z, mw.w};
-        const float4* gk4 = reinterpret_cast<const float4*>(gk + slot * kPTile);
-        const float4* gv4 = reinterpret_cast<const float4*>(gv + slot * kPTile);
+        const float4* g4 = reinterpret_cast<const float4*>(gs + slot * kPTile);
+        const uint2 ew = *reinterpret_cast<const uint2*>(gen + kPOffExp + slot * 8);
+        const uint32_t em = __vmaxs4(ew.x, ew.y);
+        const uint32_t em2 = __vmaxs4(em, em >> 16), em3 = __vmaxs4(em2, em2 >> 8);
+        const int et = (int)(int8_t)(em3 & 255u);
         uint32_t ra[32], rb[32];
-        float mx = -INFINITY;
-        auto pass1 = [&](uint32_t(&r)[32], int c) {
+        if ((mw.x & mw.y & mw.z & mw.w) != 0xFFFFFFFFu) {  // logits of the tile's masked tokens to -inf
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t bits = c == 0 ? mw.x : (c == 1 ? mw.y : (c == 2 ? mw.z : mw.w));
+            tmem_ld32_async(ts + 32 * c, ra);
+            tmem_wait_ld32(ra);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) ra[k] = (bits >> k) & 1u ? ra[k] : 0xFF800000u;
+            tmem_st32(ts + 32 * c, ra);
+          }
+          tmem_wait_st();
+        }
+        float m0 = -INFINITY, m1 = -INFINITY;
+        auto raw_max = [&](const uint32_t(&r)[32]) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            float v[4] = {__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]), __uint_as_float(r[4 * k + 2]),
-                          __uint_as_float(r[4 * k + 3])};
-            if constexpr (kCodedK) {
-              const float4 g = gk4[8 * c + k];
-              v[0] *= g.x; v[1] *= g.y; v[2] *= g.z; v[3] *= g.w;
-            }
-            if (!whole) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) v[j] = (mword[c] >> (4 * k + j)) & 1u ? v[j] : -INFINITY;
-            }
-            mx = fmaxf(fmaxf(mx, fmaxf(v[0], v[1])), fmaxf(v[2], v[3]));
+            m0 = max3(m0, __uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]));
+            m1 = max3(m1, __uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3]));
           }
         };
         tmem_ld32_async(ts, ra);
         tmem_wait_ld32(ra);
         tmem_ld32_async(ts + 32, rb);
-        pass1(ra, 0);
+        raw_max(ra);
         tmem_wait_ld32(rb);
         tmem_ld32_async(ts + 64, ra);
-        pass1(rb, 1);
+        raw_max(rb);
         tmem_wait_ld32(ra);
         tmem_ld32_async(ts + 96, rb);
-        pass1(ra, 2);
+        raw_max(ra);
         tmem_wait_ld32(rb);
-        pass1(rb, 3);
-        // move the reference where a logit or a norm outgrew it
-        const float m = mx * rs;
-        int e = E;
-        {
-          const int4 e0 = reinterpret_cast<const int4*>(gen + kPOffExp + slot * 32)[0];
-          const int4 e1 = reinterpret_cast<const int4*>(gen + kPOffExp + slot * 32)[1];
-          const int et = max(max(max(e0.x, e0.y), max(e0.z, e0.w)), max(max(e1.x, e1.y), max(e1.z, e1.w)));
-          if (et > E + kPNormSlack) e = et;
+        raw_max(rb);
+        float m = fmaxf(m0, m1);
+        if constexpr (kCodedK) {  // no u of the row exceeds this
+          const uint4 h = *reinterpret_cast<const uint4*>(gen + (m > 0.0f ? kPOffHi : kPOffLo) + slot * 16);
+          const uint32_t hm = m > 0.0f ? __vmaxu2(__vmaxu2(h.x, h.y), __vmaxu2(h.z, h.w))
+                                       : __vminu2(__vminu2(h.x, h.y), __vminu2(h.z, h.w));
+          const uint32_t g16 = m > 0.0f ? max(hm & 0xFFFFu, hm >> 16) : min(hm & 0xFFFFu, hm >> 16);
+          m = m == -INFINITY ? m : m * __uint_as_float(g16 << 16);
+        } else {
+          m *= rs;
         }
-        const bool move = m > M + kPSlack || (M == -INFINITY && m > -INFINITY);
-        if (__any_sync(0xffffffffu, move || e != E)) {
-          const float nm = move ? m : M;
-          const float f = M == -INFINITY ? 0.0f : exp2f(M - nm + (float)(E - e));
-          l *= f;
-          if (i > 0) {  // rescale the accumulator (the last product into it is complete: it precedes S)
+        if (__any_sync(0xffffffffu, m + (float)et > C + kPSlack)) {
+          if constexpr (kCodedK) {  // the exact maximum
+            m = -INFINITY;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
-              tmem_ld32_async(to + 32 * c, ra);
+              tmem_ld32_async(ts + 32 * c, ra);
               tmem_wait_ld32(ra);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) ra[k] = __float_as_uint(__uint_as_float(ra[k]) * f);
-              tmem_st32(to + 32 * c, ra);
+              for (int k = 0; k < 8; ++k) {
+                const float4 g = g4[8 * c + k];
+                m = max3(m, __uint_as_float(ra[4 * k]) * g.x, __uint_as_float(ra[4 * k + 1]) * g.y);
+                m = max3(m, __uint_as_float(ra[4 * k + 2]) * g.z, __uint_as_float(ra[4 * k + 3]) * g.w);
+              }
             }
           }
-          M = nm;
-          E = e;
+          const float nc = m + (float)et > C + kPSlack ? m + (float)et : C;
+          const float f = C == -INFINITY ? 0.0f : exp2f(C - nc);
+          if (__any_sync(0xffffffffu, nc != C)) {
+            l *= f;
+            if (i > 0) {  // rescale the accumulator (the last product into it is complete: it precedes S)
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                tmem_ld32_async(to + 32 * c, ra);
+                tmem_wait_ld32(ra);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) ra[k] = __float_as_uint(__uint_as_float(ra[k]) * f);
+                tmem_st32(to + 32 * c, ra);
+              }
+            }
+            C = nc;
+          }
         }
-        // weights: 2^(u - M + kPShift - E), u = rs gamma s
-        const float off = (M == -INFINITY ? 0.0f : M) - (float)(kPShift - E);
-        float2 sum = make_float2(0.0f, 0.0f);
-        auto pass2 = [&](uint32_t(&r)[32], int c) {
+        // P = 2^(u + et - C + shift); the denominator's terms are P 2^-et
+        const float off = (C == -INFINITY ? 0.0f : C) - kPShift - (float)et;
+        float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
+        auto weights = [&](uint32_t(&r)[32], int c) {
           uint32_t p[16];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             float2 u0 = make_float2(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]));
             float2 u1 = make_float2(__uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3]));
-            if constexpr (kCodedK) {
-              const float4 g = gk4[8 * c + k];
-              u0 = __fmul2_rn(u0, make_float2(g.x, g.y));
-              u1 = __fmul2_rn(u1, make_float2(g.z, g.w));
-            }
-            u0 = __ffma2_rn(u0, make_float2(rs, rs), make_float2(-off, -off));
-            u1 = __ffma2_rn(u1, make_float2(rs, rs), make_float2(-off, -off));
-            if (!whole) {
-              const uint32_t b = mword[c] >> (4 * k);
-              u0.x = b & 1u ? u0.x : -INFINITY;
-              u0.y = b & 2u ? u0.y : -INFINITY;
-              u1.x = b & 4u ? u1.x : -INFINITY;
-              u1.y = b & 8u ? u1.y : -INFINITY;
-            }
+            const float4 g = kCodedK ? g4[8 * c + k] : make_float4(rs, rs, rs, rs);
+            u0 = __ffma2_rn(u0, make_float2(g.x, g.y), make_float2(-off, -off));
+            u1 = __ffma2_rn(u1, make_float2(g.z, g.w), make_float2(-off, -off));
             u0 = make_float2(ex2(u0.x), ex2(u0.y));
             u1 = make_float2(ex2(u1.x), ex2(u1.y));
-            sum = __fadd2_rn(sum, __fadd2_rn(u0, u1));
-            const float4 g = gv4[8 * c + k];
-            u0 = __fmul2_rn(u0, make_float2(g.x, g.y));
-            u1 = __fmul2_rn(u1, make_float2(g.z, g.w));
+            sum0 = __fadd2_rn(sum0, u0);
+            sum1 = __fadd2_rn(sum1, u1);
             p[2 * k] = pack_h2(u0.x, u0.y);
             p[2 * k + 1] = pack_h2(u1.x, u1.y);
           }
@@ -531,16 +586,16 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
         tmem_ld32_async(ts, ra);
         tmem_wait_ld32(ra);
         tmem_ld32_async(ts + 32, rb);
-        pass2(ra, 0);
+        weights(ra, 0);
         tmem_wait_ld32(rb);
         tmem_ld32_async(ts + 64, ra);
-        pass2(rb, 1);
+        weights(rb, 1);
         tmem_wait_ld32(ra);
         tmem_ld32_async(ts + 96, rb);
-        pass2(ra, 2);
+        weights(ra, 2);
         tmem_wait_ld32(rb);
-        pass2(rb, 3);
-        l += sum.x + sum.y;
+        weights(rb, 3);
+        l = fmaf((sum0.x + sum0.y) + (sum1.x + sum1.y), __uint_as_float((uint32_t)(127 - et) << 23), l);
         tmem_wait_st();
         tc_fence_before();
       }
@@ -554,22 +609,32 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
       const int r = r0 + trow + lane;
       const int64_t pi = a.pair ? blockIdx.y : 2 * blockIdx.y + s;
       const int64_t row = pi * a.all_rows + (int64_t)(r / a.g) * a.Hq + kvh * a.g + r % a.g;
-      const bool any = ok && M != -INFINITY;
+      const bool any = ok && C != -INFINITY;
       if (r < a.rows) {
-        a.ml[2 * row] = any ? M - (float)(kPShift - E) : -INFINITY;
+        a.ml[2 * row] = any ? C - kPShift : -INFINITY;
         a.ml[2 * row + 1] = any ? l : 0.0f;
       }
       if (ok && count > 0) {
+        // through shared memory (the first four operands, Q and K: the last logits have read them),
+        // so that a warp's store is one row: 16-byte piece c of row i lies at piece c ^ i
+        unsigned char* const mine = gen + warp * (32 * kD * 4);
         uint32_t ra[32];
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           tmem_ld32_async(to + 32 * c, ra);
           tmem_wait_ld32(ra);
-          if (r < a.rows) {
-            uint4* o = reinterpret_cast<uint4*>(a.part + row * kD + 32 * c);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) o[k] = make_uint4(ra[4 * k], ra[4 * k + 1], ra[4 * k + 2], ra[4 * k + 3]);
-          }
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4*>(mine + lane * (kD * 4) + (((8 * c + k) ^ lane) << 4)) =
+                make_uint4(ra[4 * k], ra[4 * k + 1], ra[4 * k + 2], ra[4 * k + 3]);
+        }
+        __syncwarp();
+        const int last = min(32, a.rows - (r0 + trow));
+#pragma unroll 4
+        for (int i = 0; i < last; ++i) {
+          const int64_t ri = __shfl_sync(0xffffffffu, row, i);
+          reinterpret_cast<uint4*>(a.part + ri * kD)[lane] =
+              *reinterpret_cast<const uint4*>(mine + i * (kD * 4) + ((lane ^ i) << 4));
         }
       }
     }
@@ -605,26 +670,31 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
       fetch_v(0, id);
     }
     for (int t = 0; t < n && ok; ++t) {
-      const int st = stage(t), slot = t & (kPNormSlots - 1);
+      const int st = t & 1, slot = t & (kPNormSlots - 1);
       const bool valid = valid_token(t, id);
       if (lane == 0 && (id < 0 || id >= a.num_blocks) && (tile0 + t) * kPBlocks + w < blocks)
         flag_status(a.status, TQ_DEV_BAD_BLOCK);
       const int id_after = block_id(t + 2);
-      if (t >= a.stages) ok = mbar_wait(kempty + st, turn(t) ^ 1);
+      if (t >= 2) ok = mbar_wait(kempty + st, ((t >> 1) & 1) ^ 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      if constexpr (VF == 0) rv.gamma = range_of(rv);
-      // norms, mask and the norms' largest exponent of the block
-      if (half == 0) {
-        gk[slot * kPTile + row] = rk.gamma;
-        gv[slot * kPTile + row] = rv.gamma;
-      }
+      // g, mask, exponent of the values and bounds of g of the block
+      const float g = valid ? rs * rk.gamma : 1.0f;  // (a masked logit is -inf: not times zero)
+      if (kCodedK && half == 0) gs[slot * kPTile + row] = g;
       const uint32_t vb = __ballot_sync(0xffffffffu, valid && half == 0);  // bit 2 tok
-      {
-        int e = valid ? (int)((__float_as_uint(rv.gamma) >> 23) & 255u) - 126 : -126;  // gamma < 2^e
-#pragma unroll
-        for (int m = 16; m > 0; m >>= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, m));
-        if (lane == 0) reinterpret_cast<int*>(gen + kPOffExp)[slot * 8 + w] = e;
+      int e = kPMinExp;
+      if (valid) {
+        if constexpr (VF == 0) e = range_of(rv);
+        else e = (int)((__float_as_uint(rv.gamma) >> 23) & 255u) - 126;  // gamma < 2^e
+      }
+      e = __reduce_max_sync(0xffffffffu, min(max(e, kPMinExp), 126));
+      if constexpr (kCodedK) {  // bf16 above and below (norms are not negative)
+        const uint32_t hi = __reduce_max_sync(0xffffffffu, valid ? __float_as_uint(g) : 0u);
+        const uint32_t lo = __reduce_min_sync(0xffffffffu, valid ? __float_as_uint(g) : 0x7F7FFFFFu);
+        if (lane == 0) {
+          reinterpret_cast<uint16_t*>(gen + kPOffHi)[slot * 8 + w] = (uint16_t)((hi >> 16) + 1u);
+          reinterpret_cast<uint16_t*>(gen + kPOffLo)[slot * 8 + w] = (uint16_t)(lo >> 16);
+        }
       }
       if (lane == 0) {
         uint32_t x = vb & 0x55555555u;  // every other bit together
@@ -633,67 +703,81 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
         x = (x | x >> 4) & 0x00FF00FFu;
         x = (x | x >> 8) & 0x0000FFFFu;
         reinterpret_cast<uint16_t*>(gen + kPOffMask)[slot * 8 + w] = (uint16_t)x;
+        reinterpret_cast<int8_t*>(gen + kPOffExp)[slot * 8 + w] = (int8_t)e;
       }
-      store_half<KF>(rk, base + kPOffK + (uint32_t)st * kPOperand, row, half, tk, valid);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(gfull + slot);
+      store_half<KF, false>(rk, k_op + (uint32_t)st * kPOperand, row, half, tk, 1.0f);
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(gfull + slot);
-        mbar_arrive(kfull + st);
-      }
+      if (lane == 0) mbar_arrive(kfull + st);
       if (t + 1 < n) fetch_k(t + 1, id_next);
-      if (t >= a.stages) ok = mbar_wait(vempty + st, turn(t) ^ 1);
-      ok = __all_sync(0xffffffffu, ok);
+      if (t >= a.v_stages) ok = mbar_wait(vempty + vstage(t), vturn(t) ^ 1);
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(gfull + slot, (t / kPNormSlots) & 1));
       if (!ok) break;
-      store_half<VF, VF == 0>(rv, base + kPOffV + (uint32_t)st * kPOperand, row, half, tv, valid);
+      const uint2 ew = *reinterpret_cast<const uint2*>(gen + kPOffExp + slot * 8);
+      const uint32_t em = __vmaxs4(ew.x, ew.y);
+      const uint32_t em2 = __vmaxs4(em, em >> 16), em3 = __vmaxs4(em2, em2 >> 8);
+      const float down = __uint_as_float((uint32_t)(127 - (int)(int8_t)(em3 & 255u)) << 23);  // 2^-et
+      store_half<VF, true>(rv, v_op + (uint32_t)vstage(t) * kPOperand, row, half, tv, VF == 0 ? down : down * rv.gamma);
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(vfull + st);
+      if (lane == 0) mbar_arrive(vfull + vstage(t));
       if (t + 1 < n) fetch_v(t + 1, id_next);
       id = id_next;
       id_next = id_after;
     }
-  } else if (lane == 0) {
+  } else {
     // ------------------------------------------------------------------ MMA
+    // (the whole warp runs the loop, so that descriptors stay in uniform registers; one lane issues)
+    const bool issue = elect_one();
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     constexpr uint32_t idesc_s = umma_idesc_16(KF == 0, false, kPTile, kPTile);
     constexpr uint32_t idesc_o = umma_idesc_16(false, true, kPTile, kPTile);
-    const uint64_t dq = umma_desc_sw128(base + kPOffQ), dk = umma_desc_sw128(base + kPOffK);
-    const uint64_t dv = umma_desc_sw128_mn(base + kPOffV, kPPanel);
+    const uint64_t dq = umma_desc_sw128(base), dk = umma_desc_sw128(k_op);
+    const uint64_t dv = umma_desc_sw128_mn(v_op, kPPanel);
     auto tile_of = [&](int i, int s) { return a.pair ? i : 2 * i + s; };
     auto logits = [&](int i, int s) {  // S_s = Q_s K^T
-      const int t = tile_of(i, s), st = stage(t);
-      if (!mbar_wait(kfull + st, turn(t))) return false;
+      const int t = tile_of(i, s), st = t & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(kfull + st, (t >> 1) & 1))) return false;
       tc_fence_after();
       const uint64_t q = dq + (uint64_t)((a.pair ? s : 0) * (kPOperand >> 4));
       const uint64_t k = dk + (uint64_t)(st * (kPOperand >> 4));
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint64_t off = (uint64_t)((j >> 2) * (kPPanel >> 4) + (j & 3) * 2);
-        umma_bf16(tmem + (uint32_t)(s * kPTile), q + off, k + off, idesc_s, j > 0);
-      }
-      if (a.split_q) {
-        const uint64_t low = dq + (uint64_t)((a.pair ? 3 + 2 * s : 1) * (kPOperand >> 4));
+      const uint64_t low = dq + (uint64_t)((a.pair ? 2 + s : 1) * (kPOperand >> 4));
+      const uint32_t d = tm + (uint32_t)(s * kPTile);
+      if (issue) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const uint64_t off = (uint64_t)((j >> 2) * (kPPanel >> 4) + (j & 3) * 2);
-          umma_bf16(tmem + (uint32_t)(s * kPTile), low + off, k + off, idesc_s, true);
+          umma_bf16(d, q + off, k + off, idesc_s, j > 0);
         }
+        if (a.split_q) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint64_t off = (uint64_t)((j >> 2) * (kPPanel >> 4) + (j & 3) * 2);
+            umma_bf16(d, low + off, k + off, idesc_s, true);
+          }
+        }
+        umma_commit(smem_u32(sfull + s));
+        if (!a.pair || s == 1) umma_commit(smem_u32(kempty + st));
       }
-      umma_commit(smem_u32(sfull + s));
-      if (!a.pair || s == 1) umma_commit(smem_u32(kempty + st));
+      __syncwarp();
       return true;
     };
     auto values = [&](int i, int s) {  // O_s += P_s V
-      const int t = tile_of(i, s), st = stage(t);
-      if (!mbar_wait(pfull + s, i & 1) || !mbar_wait(vfull + st, turn(t))) return false;
+      const int t = tile_of(i, s), st = vstage(t);
+      if (!__all_sync(0xffffffffu, mbar_wait(pfull + s, i & 1) && mbar_wait(vfull + st, vturn(t)))) return false;
       tc_fence_after();
       const uint64_t v = dv + (uint64_t)(st * (kPOperand >> 4));
+      const uint32_t d = tm + (uint32_t)((2 + s) * kPTile), p = tm + (uint32_t)(s * kPTile);
+      if (issue) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        umma_16_ts(tmem + (uint32_t)((2 + s) * kPTile), tmem + (uint32_t)(s * kPTile + 8 * j), v + (uint64_t)(j * (16 * 128 >> 4)),
-                   idesc_o, i > 0 || j > 0);
-      if (!a.pair || s == 1) umma_commit(smem_u32(vempty + st));
-      if (i + 1 == (s ? count1 : count0)) umma_commit(smem_u32(odone + s));
+        for (int j = 0; j < 8; ++j)
+          umma_16_ts(d, p + (uint32_t)(8 * j), v + (uint64_t)(j * (16 * 128 >> 4)), idesc_o, i > 0 || j > 0);
+        if (!a.pair || s == 1) umma_commit(smem_u32(vempty + st));
+        if (i + 1 == (s ? count1 : count0)) umma_commit(smem_u32(odone + s));
+      }
+      __syncwarp();
       return true;
     };
     if (count0 > 0) ok = logits(0, 0);
@@ -738,29 +822,52 @@ __global__ void __launch_bounds__(128) k_prefix_merge(const MergeArgs a) {
   if (row >= a.rows) return;
   const int b = (int)(row / a.um.Hq), head = (int)(row - (int64_t)b * a.um.Hq);
   const int unit = (b * a.um.Hkv + head / a.um.g) * a.um.ngroups + (head % a.um.g) / a.um.hpw;
+  // reference of all partials
+  auto own_live = [&](int s) { return s < a.own_splits && slot_live(unit, a.own_splits, s, a.um.nw); };
   float M = -INFINITY;
-  for (int s = lane; s < a.splits; s += 32) M = fmaxf(M, a.ml[(s * a.rows + row) * 2]);
+  for (int s = lane; s < a.splits; s += 32) M = fmaxf(M, __ldg(a.ml + (s * a.rows + row) * 2));
   for (int s = lane; s < a.own_splits; s += 32)
-    if (slot_live(unit, a.own_splits, s, a.um.nw)) M = fmaxf(M, a.own_ml[(row * a.own_splits + s) * 2]);
+    if (own_live(s)) M = fmaxf(M, __ldg(a.own_ml + (row * a.own_splits + s) * 2));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   float L = 0.0f;
-  auto join = [&](const float* part, const float* ml) {
-    const float m = ml[0];
-    if (m == -INFINITY) return;  // nothing in this partial
-    const float f = exp2f(m - M);
-    const float4 v = reinterpret_cast<const float4*>(part)[lane];
-    y[0] = fmaf(v.x, f, y[0]);
-    y[1] = fmaf(v.y, f, y[1]);
-    y[2] = fmaf(v.z, f, y[2]);
-    y[3] = fmaf(v.w, f, y[3]);
-    L = fmaf(ml[1], f, L);
+  // 32 partials a round: lane s holds partial s's factor, eight loads of values in flight
+  auto join = [&](const float* part, int64_t step, float m, float l, int count) {
+    const float f = m == -INFINITY ? 0.0f : exp2f(m - M);
+    L = fmaf(l, f, L);
+    for (int s0 = 0; s0 < count; s0 += 8) {
+      float4 v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float fk = __shfl_sync(0xffffffffu, f, (s0 + k) & 31);
+        v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (s0 + k < count && fk != 0.0f) v[k] = __ldg(reinterpret_cast<const float4*>(part + (s0 + k) * step) + lane);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float fk = __shfl_sync(0xffffffffu, f, (s0 + k) & 31);
+        y[0] = fmaf(v[k].x, fk, y[0]);
+        y[1] = fmaf(v[k].y, fk, y[1]);
+        y[2] = fmaf(v[k].z, fk, y[2]);
+        y[3] = fmaf(v[k].w, fk, y[3]);
+      }
+    }
   };
-  for (int s = 0; s < a.splits; ++s) join(a.part + (s * a.rows + row) * kD, a.ml + (s * a.rows + row) * 2);
-  for (int s = 0; s < a.own_splits; ++s)
-    if (slot_live(unit, a.own_splits, s, a.um.nw))
-      join(a.own_part + (row * a.own_splits + s) * kD, a.own_ml + (row * a.own_splits + s) * 2);
+  for (int s0 = 0; s0 < a.splits; s0 += 32) {
+    const int s = s0 + lane;
+    const bool in = s < a.splits;
+    const float2 ml = in ? __ldg(reinterpret_cast<const float2*>(a.ml) + s * a.rows + row) : make_float2(-INFINITY, 0.0f);
+    join(a.part + (s0 * a.rows + row) * kD, a.rows * kD, ml.x, ml.y, min(32, a.splits - s0));
+  }
+  for (int s0 = 0; s0 < a.own_splits; s0 += 32) {
+    const int s = s0 + lane;
+    const float2 ml = own_live(s) ? __ldg(reinterpret_cast<const float2*>(a.own_ml) + row * a.own_splits + s)
+                                  : make_float2(-INFINITY, 0.0f);
+    join(a.own_part + (row * a.own_splits + s0) * kD, kD, ml.x, ml.y, min(32, a.own_splits - s0));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
   const float inv = L > 0.0f ? a.value_scale / L : 0.0f;
 #pragma unroll
   for (int k = 0; k < 4; ++k) y[k] *= inv;
@@ -868,7 +975,7 @@ cudaError_t launch_prefix_decode(const PrefixCall& c, cudaStream_t st) {
     PrefixArgs a = {};
     const PrefixPlan p = prefix_plan(d, c.own.batch, c.own.num_q_heads, c.prefix_len, c.num_sms);
     a.split_q = d.fmt.kv_format == TQ_KV_PACKED || c.own.q_dtype == TQ_F32 ? 1 : 0;
-    a.stages = p.pair && a.split_q ? 1 : 2;
+    a.v_stages = p.pair && a.split_q ? 1 : 2;
     a.kpool = reinterpret_cast<const uint8_t*>(d.k_cache);
     a.vpool = reinterpret_cast<const uint8_t*>(d.v_cache);
     a.num_blocks = d.num_blocks;
