@@ -26,7 +26,7 @@
 // operand and P both fit fp16 whatever the norms are; a row keeps one reference C for
 // weight times value, and P = 2^(u + et - C + shift) for a log2-logit u = g_t s_t, where g_t
 // holds the key's norm and every scale.  C moves, and the accumulator is rescaled, only when
-// a row's largest u + et exceeds it by 8; whether it may is decided from the largest raw
+// a row's largest u + et exceeds it by 14; whether it may is decided from the largest raw
 // logit and the tile's largest and smallest g, the exact maximum being taken only then.
 // With more than 128 rows a KV head the streams are two tiles of rows over the same
 // tokens; with fewer they share the rows and take every other tile of tokens, each with an
@@ -59,8 +59,8 @@ constexpr int kPThreads = (kPSoftWarps + kPProdWarps + 1) * 32;
 constexpr uint32_t kPPanel = kPTile * 128;       // 128 rows of 64 16-bit elements, swizzled
 constexpr uint32_t kPOperand = 2 * kPPanel;      // a 128 x 128 operand
 constexpr int kPNormSlots = 4;                   // tiles whose norms and masks are kept
-constexpr float kPSlack = 8.0f;                  // log2 units u + et may exceed a row's reference
-constexpr float kPShift = 6.0f;                  // P is at most 2^14
+constexpr float kPSlack = 14.0f;                 // log2 units u + et may exceed a row's reference
+constexpr float kPShift = 1.0f;                  // P is at most 2^15
 constexpr int kPMinExp = -60;                    // smallest et: values below are as good as zero
 
 // Shared memory (byte offsets): operands of 32 KB -- the streams' Q in 0 and 1; low parts of
@@ -73,7 +73,7 @@ constexpr uint32_t kPOffExp = kPOffMask + kPNormSlots * 16;          // s8 [slot
 constexpr uint32_t kPOffHi = kPOffExp + kPNormSlots * 8;             // bf16 [slots][8]: upper bounds of g
 constexpr uint32_t kPOffLo = kPOffHi + kPNormSlots * 16;             // bf16 [slots][8]: lower bounds of g
 constexpr uint32_t kPOffBar = kPOffLo + kPNormSlots * 16;
-constexpr int kPBars = 2 + 2 + 2 + 2 + kPNormSlots + 2 + 2 + 2;
+constexpr int kPBars = 2 + 2 + 2 + 2 + 2 * kPNormSlots + 2 + 2 + 2;
 constexpr uint32_t kPOffTmem = kPOffBar + kPBars * 8;
 constexpr uint32_t kPOffMax = kPOffTmem + 4;                         // u32: largest |q|
 constexpr uint32_t kPSmem = kPOffTmem + 8;
@@ -148,8 +148,9 @@ __device__ __forceinline__ uint4 centroids8(uint32_t v, const HalfTable& t) {
   return make_uint4(prmt(l0, h0, 0x5140u), prmt(l0, h0, 0x7362u), prmt(l1, h1, 0x5140u), prmt(l1, h1, 0x7362u));
 }
 
-// A lane's half record (64 coordinates of one token) of a page of format F (0: bf16, 8: FP8,
-// else code bits), as loaded.
+// A lane's share of a page of format F (0: bf16, 8: FP8, else code bits), as loaded.  Coded
+// pages: half a record (64 coordinates) of token lane / 2; bf16 and FP8 pages: 16-byte
+// pieces lane, lane + 32, ... of the page, so that a warp's load is 512 bytes in a row.
 template <int F>
 struct HalfRecord {
   static constexpr int kBytes = F == 0 ? 128 : 8 * F;
@@ -157,12 +158,39 @@ struct HalfRecord {
   uint32_t w[kWords];
   float gamma;
 };
-
-// Chunk order: lane half h visits chunk i ^ (4 h) in step i, so that the eight lanes of a
-// 128-bit store phase (four tokens, two halves) hit eight different 16-byte columns.
 template <int F>
-__device__ __forceinline__ void load_half(HalfRecord<F>& r, const uint8_t* page, int tok, int half) {
+__device__ __forceinline__ constexpr bool by_pieces() { return F == 0 || F == 8; }
+template <int F>  // token of piece i
+__device__ __forceinline__ int piece_token(int i, int lane) { return F == 0 ? 2 * i + (lane >> 4) : 4 * i + (lane >> 3); }
+
+// (`live`: tokens of the block; what lies past them reads as zero)
+template <int F>
+__device__ __forceinline__ void load_half(HalfRecord<F>& r, const uint8_t* page, int lane, int live) {
   constexpr int B = HalfRecord<F>::kBytes;
+  const int tok = lane >> 1, half = lane & 1;
+  if constexpr (by_pieces<F>()) {
+#pragma unroll
+    for (int i = 0; i < B / 16; ++i) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(page) + 32 * i + lane);
+      r.w[4 * i] = v.x;
+      r.w[4 * i + 1] = v.y;
+      r.w[4 * i + 2] = v.z;
+      r.w[4 * i + 3] = v.w;
+    }
+    if (live < kBlock) {
+#pragma unroll
+      for (int i = 0; i < B / 16; ++i)
+        if (piece_token<F>(i, lane) >= live) r.w[4 * i] = r.w[4 * i + 1] = r.w[4 * i + 2] = r.w[4 * i + 3] = 0u;
+    }
+    r.gamma = 1.0f;
+    return;
+  }
+  if (tok >= live) {
+#pragma unroll
+    for (int i = 0; i < HalfRecord<F>::kWords; ++i) r.w[i] = 0u;
+    r.gamma = 0.0f;
+    return;
+  }
   const uint8_t* p = page + tok * 2 * B + half * B;
   if constexpr (F == 3) {
 #pragma unroll
@@ -171,28 +199,22 @@ __device__ __forceinline__ void load_half(HalfRecord<F>& r, const uint8_t* page,
       r.w[2 * i] = v.x;
       r.w[2 * i + 1] = v.y;
     }
-  } else {
+  } else if constexpr (!by_pieces<F>()) {
 #pragma unroll
     for (int i = 0; i < B / 16; ++i) {
-      const int c = B >= 32 ? i ^ (half * (B / 32)) : i;  // (the upper half of the record's half first for h = 1)
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + c);
+      // chunk order of 4-bit records: lane half h visits chunk i ^ (4 h) in step i, so that the
+      // eight lanes of a 128-bit store phase hit eight different 16-byte columns
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + (B >= 32 ? i ^ half : i));
       r.w[4 * i] = v.x;
       r.w[4 * i + 1] = v.y;
       r.w[4 * i + 2] = v.z;
       r.w[4 * i + 3] = v.w;
     }
   }
-  r.gamma = (F >= 2 && F <= 4) ? __ldg(reinterpret_cast<const float*>(page + kBlock * 2 * B) + tok) : 1.0f;
+  r.gamma = __ldg(reinterpret_cast<const float*>(page + kBlock * 2 * B) + tok);
 }
 
-template <int F>
-__device__ __forceinline__ void zero_half(HalfRecord<F>& r) {
-#pragma unroll
-  for (int i = 0; i < HalfRecord<F>::kWords; ++i) r.w[i] = 0u;
-  r.gamma = 0.0f;
-}
-
-// Step i of the half record: its chunk's place (0..7) and its eight 16-bit values.
+// Eight 16-bit values: chunk i of the lane's share.
 template <int F>
 __device__ __forceinline__ uint4 chunk_of(const HalfRecord<F>& r, int i, const HalfTable& t) {
   if constexpr (F == 0) {
@@ -243,35 +265,47 @@ __device__ __forceinline__ uint4 scaled_half8(const uint4& v, float inv) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// The token's half row to the operand at `dst`: panel = half, row = token of the tile,
-// 16-byte chunk c at c ^ (row & 7).  Values (VALUES) times `scale`: codes by the token's
-// scaled norm in fp16, bf16 values by a power of two.
+// The lane's share of block w to the operand at `dst`: panel = half of the head, row = token
+// of the tile, 16-byte chunk c at c ^ (row & 7).  Values (VALUES) times `scale`: codes by
+// the token's scaled norm, bf16 values by a power of two.
 template <int F, bool VALUES>
-__device__ __forceinline__ void store_half(const HalfRecord<F>& r, uint32_t dst, int row, int half, const HalfTable& t,
+__device__ __forceinline__ void store_half(const HalfRecord<F>& r, uint32_t dst, int w, int lane, const HalfTable& t,
                                            float scale) {
-  const uint32_t base = dst + (uint32_t)half * kPPanel + (uint32_t)row * 128u;
-  // formats loaded in 16-byte pieces of two or more hold their upper part first for half 1
-  constexpr bool kSwapped = F != 3 && HalfRecord<F>::kBytes >= 32;
-  // a norm in two fp16 parts, so that a centroid times it is rounded once
-  const __half2 s2 = __float2half2_rn(scale), s2l = __float2half2_rn(scale - __low2float(s2));
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    uint4 v = chunk_of<F>(r, i, t);
-    if constexpr (VALUES && F == 0) {
-      v = scaled_half8(v, scale);
-    } else if constexpr (VALUES) {
-      uint32_t* w = &v.x;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const __half2 c2 = *reinterpret_cast<const __half2*>(w + k);
-        const __half2 h = __hfma2(c2, s2, __hmul2(c2, s2l));
-        w[k] = *reinterpret_cast<const uint32_t*>(&h);
-      }
-    }
-    const int c = kSwapped ? i ^ (4 * half) : i;
-    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(base + (uint32_t)((c ^ (row & 7)) << 4)), "r"(v.x),
-                 "r"(v.y), "r"(v.z), "r"(v.w)
+  auto put = [&](const uint4& v, int row, int panel, int c) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst + (uint32_t)panel * kPPanel + (uint32_t)row * 128u +
+                                                               (uint32_t)((c ^ (row & 7)) << 4)),
+                 "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                  : "memory");
+  };
+  if constexpr (F == 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint4 v = chunk_of<F>(r, i, t);
+      if constexpr (VALUES) v = scaled_half8(v, scale);
+      put(v, w * kBlock + piece_token<F>(i, lane), (lane >> 3) & 1, lane & 7);
+    }
+  } else if constexpr (F == 8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      put(chunk_of<F>(r, i, t), w * kBlock + piece_token<F>(i >> 1, lane), (lane >> 2) & 1, 2 * (lane & 3) + (i & 1));
+  } else {
+    // a norm in two fp16 parts, so that a centroid times it is rounded once
+    const __half2 s2 = __float2half2_rn(scale), s2l = __float2half2_rn(scale - __low2float(s2));
+    const int row = w * kBlock + (lane >> 1), half = lane & 1;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint4 v = chunk_of<F>(r, i, t);
+      if constexpr (VALUES) {
+        uint32_t* x = &v.x;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const __half2 c2 = *reinterpret_cast<const __half2*>(x + k);
+          const __half2 h = __hfma2(c2, s2, __hmul2(c2, s2l));
+          x[k] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      }
+      put(v, row, half, F == 4 ? i ^ (4 * half) : i);
+    }
   }
 }
 
@@ -389,8 +423,9 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
   float* const gs = reinterpret_cast<float*>(gen + kPOffG);
   uint64_t* const bars = reinterpret_cast<uint64_t*>(gen + kPOffBar);
   uint64_t *const kfull = bars, *const kempty = bars + 2, *const vfull = bars + 4, *const vempty = bars + 6;
-  uint64_t* const gfull = bars + 8;                 // [kPNormSlots]
-  uint64_t* const sfull = gfull + kPNormSlots;      // [2] logits of a stream are in tensor memory
+  uint64_t* const gfull = bars + 8;                 // [kPNormSlots] g, its bounds and the mask of a tile
+  uint64_t* const efull = gfull + kPNormSlots;      // [kPNormSlots] exponents of a tile's values
+  uint64_t* const sfull = efull + kPNormSlots;      // [2] logits of a stream are in tensor memory
   uint64_t* const pfull = sfull + 2;                // [2] weights of a stream are in tensor memory
   uint64_t* const odone = pfull + 2;                // [2] a stream's accumulator is complete
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -416,7 +451,7 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
       mbar_init(pfull + i, 4);
       mbar_init(odone + i, 1);
     }
-    for (int i = 0; i < kPNormSlots; ++i) mbar_init(gfull + i, kPProdWarps);
+    for (int i = 0; i < 2 * kPNormSlots; ++i) mbar_init(gfull + i, kPProdWarps);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     *qmax = 0u;
   }
@@ -476,7 +511,8 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
     float C = -INFINITY, l = 0.0f;  // reference of u + et; sum of 2^(u - C + shift)
     for (int i = 0; i < count && ok; ++i) {
       const int t = a.pair ? i : 2 * i + s, slot = t & (kPNormSlots - 1);
-      ok = mbar_wait(gfull + slot, (t / kPNormSlots) & 1) && mbar_wait(sfull + s, i & 1);
+      ok = mbar_wait(gfull + slot, (t / kPNormSlots) & 1) && mbar_wait(efull + slot, (t / kPNormSlots) & 1) &&
+           mbar_wait(sfull + s, i & 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
@@ -545,7 +581,7 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
               }
             }
           }
-          const float nc = m + (float)et > C + kPSlack ? m + (float)et : C;
+          const float nc = fmaxf(C, m + (float)et);
           const float f = C == -INFINITY ? 0.0f : exp2f(C - nc);
           if (__any_sync(0xffffffffu, nc != C)) {
             l *= f;
@@ -641,7 +677,6 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
   } else if (warp < kPSoftWarps + kPProdWarps) {
     // ------------------------------------------------------------ producers
     const int w = warp - kPSoftWarps, tok = lane >> 1, half = lane & 1;
-    const int row = w * kBlock + tok;
     HalfTable tk = {}, tv = {};
     if constexpr (kCodedK) tk = half_table<(kCodedK ? KF : 4)>(a.cbk);
     if constexpr (kCodedV) tv = half_table<(kCodedV ? VF : 4)>(a.cbv);
@@ -650,45 +685,33 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
       const int b = (tile0 + t) * kPBlocks + w;
       return t < n && b < blocks ? __ldg(a.table + b) : -1;
     };
-    auto valid_token = [&](int t, int id) {
-      const int b = (tile0 + t) * kPBlocks + w;
-      return id >= 0 && id < a.num_blocks && b * kBlock + tok < a.len;
+    auto tokens = [&](int t, int id) {  // tokens of it (none of a bad block)
+      return id >= 0 && id < a.num_blocks ? min(kBlock, a.len - ((tile0 + t) * kPBlocks + w) * kBlock) : 0;
     };
     HalfRecord<KF> rk;
     HalfRecord<VF> rv;
-    int id = block_id(0), id_next = block_id(1);
-    auto fetch_k = [&](int t, int blk) {
-      if (valid_token(t, blk)) load_half<KF>(rk, a.kpool + ((int64_t)blk * a.Hkv + kvh) * kpage, tok, half);
-      else zero_half<KF>(rk);
+    // (a block without tokens reads as zeros: no page is touched)
+    auto fetch_k = [&](int t, int id) {
+      const int live = tokens(t, id);
+      if (live > 0) load_half<KF>(rk, a.kpool + ((int64_t)id * a.Hkv + kvh) * kpage, lane, live);
+      else rk = HalfRecord<KF>{};
     };
-    auto fetch_v = [&](int t, int blk) {
-      if (valid_token(t, blk)) load_half<VF>(rv, a.vpool + ((int64_t)blk * a.Hkv + kvh) * vpage, tok, half);
-      else zero_half<VF>(rv);
+    auto fetch_v = [&](int t, int id) {
+      const int live = tokens(t, id);
+      if (live > 0) load_half<VF>(rv, a.vpool + ((int64_t)id * a.Hkv + kvh) * vpage, lane, live);
+      else rv = HalfRecord<VF>{};
     };
-    if (n > 0) {
-      fetch_k(0, id);
-      fetch_v(0, id);
-    }
-    for (int t = 0; t < n && ok; ++t) {
-      const int st = t & 1, slot = t & (kPNormSlots - 1);
-      const bool valid = valid_token(t, id);
+    // K of tile t, with its g and mask
+    auto put_k = [&](int t, int id) {
+      const int st = t & 1, slot = t & (kPNormSlots - 1), live = tokens(t, id);
       if (lane == 0 && (id < 0 || id >= a.num_blocks) && (tile0 + t) * kPBlocks + w < blocks)
         flag_status(a.status, TQ_DEV_BAD_BLOCK);
-      const int id_after = block_id(t + 2);
-      if (t >= 2) ok = mbar_wait(kempty + st, ((t >> 1) & 1) ^ 1);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      // g, mask, exponent of the values and bounds of g of the block
-      const float g = valid ? rs * rk.gamma : 1.0f;  // (a masked logit is -inf: not times zero)
-      if (kCodedK && half == 0) gs[slot * kPTile + row] = g;
-      const uint32_t vb = __ballot_sync(0xffffffffu, valid && half == 0);  // bit 2 tok
-      int e = kPMinExp;
-      if (valid) {
-        if constexpr (VF == 0) e = range_of(rv);
-        else e = (int)((__float_as_uint(rv.gamma) >> 23) & 255u) - 126;  // gamma < 2^e
-      }
-      e = __reduce_max_sync(0xffffffffu, min(max(e, kPMinExp), 126));
-      if constexpr (kCodedK) {  // bf16 above and below (norms are not negative)
+      if (t >= 2 && !__all_sync(0xffffffffu, mbar_wait(kempty + st, ((t >> 1) & 1) ^ 1))) return false;
+      if constexpr (kCodedK) {
+        const bool valid = tok < live;
+        const float g = valid ? rs * rk.gamma : 1.0f;  // (a masked logit is -inf: not times zero)
+        if (half == 0) gs[slot * kPTile + w * kBlock + tok] = g;
+        // bounds, in bf16 above and below (norms are not negative)
         const uint32_t hi = __reduce_max_sync(0xffffffffu, valid ? __float_as_uint(g) : 0u);
         const uint32_t lo = __reduce_min_sync(0xffffffffu, valid ? __float_as_uint(g) : 0x7F7FFFFFu);
         if (lane == 0) {
@@ -696,36 +719,50 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
           reinterpret_cast<uint16_t*>(gen + kPOffLo)[slot * 8 + w] = (uint16_t)(lo >> 16);
         }
       }
-      if (lane == 0) {
-        uint32_t x = vb & 0x55555555u;  // every other bit together
-        x = (x | x >> 1) & 0x33333333u;
-        x = (x | x >> 2) & 0x0F0F0F0Fu;
-        x = (x | x >> 4) & 0x00FF00FFu;
-        x = (x | x >> 8) & 0x0000FFFFu;
-        reinterpret_cast<uint16_t*>(gen + kPOffMask)[slot * 8 + w] = (uint16_t)x;
-        reinterpret_cast<int8_t*>(gen + kPOffExp)[slot * 8 + w] = (int8_t)e;
-      }
+      if (lane == 0) reinterpret_cast<uint16_t*>(gen + kPOffMask)[slot * 8 + w] = (uint16_t)((1u << live) - 1u);
       __syncwarp();
       if (lane == 0) mbar_arrive(gfull + slot);
-      store_half<KF, false>(rk, k_op + (uint32_t)st * kPOperand, row, half, tk, 1.0f);
+      store_half<KF, false>(rk, k_op + (uint32_t)st * kPOperand, w, lane, tk, 1.0f);
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(kfull + st);
-      if (t + 1 < n) fetch_k(t + 1, id_next);
+      return true;
+    };
+    int id = block_id(0), id1 = block_id(1);
+    if (n > 0) {
+      fetch_k(0, id);
+      fetch_v(0, id);
+      ok = put_k(0, id);
+      if (n > 1) fetch_k(1, id1);
+    }
+    for (int t = 0; t < n && ok; ++t) {
+      const int slot = t & (kPNormSlots - 1);
+      const int id2 = block_id(t + 2);
+      // the exponent of the block's values: all tokens of the tile get the largest
+      int e = kPMinExp;
+      if constexpr (VF == 0) e = range_of(rv);
+      else if (tok < tokens(t, id)) e = (int)((__float_as_uint(rv.gamma) >> 23) & 255u) - 126;  // gamma < 2^e
+      e = __reduce_max_sync(0xffffffffu, min(max(e, kPMinExp), 126));
+      if (lane == 0) reinterpret_cast<int8_t*>(gen + kPOffExp)[slot * 8 + w] = (int8_t)e;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(efull + slot);
+      // the next tile's K goes ahead of this tile's V: the tensor cores want it first
+      if (t + 1 < n && !(ok = put_k(t + 1, id1))) break;
+      if (t + 2 < n) fetch_k(t + 2, id2);
       if (t >= a.v_stages) ok = mbar_wait(vempty + vstage(t), vturn(t) ^ 1);
-      ok = __all_sync(0xffffffffu, ok && mbar_wait(gfull + slot, (t / kPNormSlots) & 1));
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(efull + slot, (t / kPNormSlots) & 1));
       if (!ok) break;
       const uint2 ew = *reinterpret_cast<const uint2*>(gen + kPOffExp + slot * 8);
       const uint32_t em = __vmaxs4(ew.x, ew.y);
       const uint32_t em2 = __vmaxs4(em, em >> 16), em3 = __vmaxs4(em2, em2 >> 8);
       const float down = __uint_as_float((uint32_t)(127 - (int)(int8_t)(em3 & 255u)) << 23);  // 2^-et
-      store_half<VF, true>(rv, v_op + (uint32_t)vstage(t) * kPOperand, row, half, tv, VF == 0 ? down : down * rv.gamma);
+      store_half<VF, true>(rv, v_op + (uint32_t)vstage(t) * kPOperand, w, lane, tv, VF == 0 ? down : down * rv.gamma);
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(vfull + vstage(t));
-      if (t + 1 < n) fetch_v(t + 1, id_next);
-      id = id_next;
-      id_next = id_after;
+      if (t + 1 < n) fetch_v(t + 1, id1);
+      id = id1;
+      id1 = id2;
     }
   } else {
     // ------------------------------------------------------------------ MMA
