@@ -179,8 +179,8 @@ tq_status check_heads(const tq_heads& h, int dtype, int64_t n_tokens, bool need_
 // counter region alone, so that it stays zero for later decode calls.
 size_t own_workspace(const tq_cache_desc* desc, int batch, int num_q_heads, int max_blocks) {
   if (max_blocks < 1) return kCounterRegionBytes;
-  return decode_workspace(batch, num_q_heads, resolve_splits(desc, batch, num_q_heads, max_blocks, 0), desc->head_dim,
-                          false).total;
+  return decode_workspace(batch, num_q_heads, resolve_splits(desc, batch, num_q_heads, max_blocks, own_splits(max_blocks)),
+                          desc->head_dim, false).total;
 }
 
 }  // namespace
@@ -460,7 +460,7 @@ tq_status tq_prefix_decode(const tq_cache_desc* desc, const void* q, int q_dtype
   PrefixCall c = {};
   if (max_blocks_per_seq > 0) {
     s = prepare_decode(desc, q, q_dtype, batch, num_q_heads, block_table, max_blocks_per_seq, context_lens, sm_scale,
-                       out, out_dtype, workspace, own, 0, fn, &c.own);
+                       out, out_dtype, workspace, own, own_splits(max_blocks_per_seq), fn, &c.own);
     if (s != TQ_OK) return s;
   } else {
     c.own.desc = desc;

@@ -97,6 +97,9 @@ struct PrefixCall {
   int64_t prefix_len;
   int num_sms;
 };
+// Splits of the own tokens' decode for prepare_decode (0: the automatic choice): short block
+// tables take CTAs of 16 blocks (k_own), longer ones the decode kernel.
+int own_splits(int max_blocks);
 // Bytes of the prefix's partials, which follow the workspace of the own tokens' decode.
 size_t prefix_partial_bytes(const tq_cache_desc& d, int batch, int num_q_heads, int64_t prefix_len, int num_sms);
 

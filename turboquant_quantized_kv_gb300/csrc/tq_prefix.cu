@@ -45,6 +45,7 @@
 #include "tq_async.cuh"
 #include "tq_device.cuh"
 #include "tq_internal.h"
+#include "tq_prefix.cuh"
 #include "tq_tcgen05.cuh"
 
 namespace tq {
@@ -96,57 +97,14 @@ struct PrefixArgs {
   int tiles_per_split;
   float scale;     // sm_scale * log2 e
   const float* rot;  // signs, for packed keys
-  int64_t all_rows;  // batch * Hq
-  float* part;     // [partials][B * Hq][d]
-  float* ml;       // [partials][B * Hq][2]
+  int row_tiles;     // tiles of 32 rows of a KV head
+  float* part;       // [partials][Hkv][row_tiles][d / 4][32 rows][4]
+  float2* ml;        // [partials][Hkv][row_tiles][32 rows]
   Codebook cbk, cbv;  // centroids times the tables' factors
   unsigned* status;
 };
 
 // ------------------------------------------------------------------ operands
-
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t pack_b2(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// fp16 centroids of the upper half of a codebook as byte tables for permutes: entry i < 8,
-// low bytes and high bytes apart.
-struct HalfTable {
-  uint32_t lo0, lo1, hi0, hi1;
-};
-template <int BITS>
-__device__ __forceinline__ HalfTable half_table(const Codebook& cb) {
-  constexpr int H = 1 << (BITS - 1);
-  uint32_t h[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) h[i] = (uint32_t)__half_as_ushort(__float2half_rn(cb.c[H + (i & (H - 1))]));
-  HalfTable t;
-  t.lo0 = (h[0] & 255u) | (h[1] & 255u) << 8 | (h[2] & 255u) << 16 | (h[3] & 255u) << 24;
-  t.lo1 = (h[4] & 255u) | (h[5] & 255u) << 8 | (h[6] & 255u) << 16 | (h[7] & 255u) << 24;
-  t.hi0 = h[0] >> 8 | (h[1] >> 8) << 8 | (h[2] >> 8) << 16 | (h[3] >> 8) << 24;
-  t.hi1 = h[4] >> 8 | (h[5] >> 8) << 8 | (h[6] >> 8) << 16 | (h[7] >> 8) << 24;
-  return t;
-}
-
-// Eight codes, one in each nibble of v, to eight fp16 centroids.
-template <int BITS>
-__device__ __forceinline__ uint4 centroids8(uint32_t v, const HalfTable& t) {
-  constexpr uint32_t top = 0x11111111u << (BITS - 1);
-  const uint32_t n = ~v & top;                       // negative: the top bit of a code is clear
-  const uint32_t m = n - (n >> (BITS - 1));          // the low bits of the negative ones
-  const uint32_t sel = (v ^ m) & (top - 0x11111111u);  // magnitude index
-  const uint32_t l0 = prmt(t.lo0, t.lo1, sel), l1 = prmt(t.lo0, t.lo1, sel >> 16);
-  uint32_t h0 = prmt(t.hi0, t.hi1, sel), h1 = prmt(t.hi0, t.hi1, sel >> 16);
-  const uint32_t ne = n << (8 - BITS), no = n << (4 - BITS);  // signs of even and odd codes at the tops of bytes
-  h0 ^= prmt(ne, no, 0x5140u) & 0x80808080u;
-  h1 ^= prmt(ne, no, 0x7362u) & 0x80808080u;
-  return make_uint4(prmt(l0, h0, 0x5140u), prmt(l0, h0, 0x7362u), prmt(l1, h1, 0x5140u), prmt(l1, h1, 0x7362u));
-}
 
 // A lane's share of a page of format F (0: bf16, 8: FP8, else code bits), as loaded.  Coded
 // pages: half a record (64 coordinates) of token lane / 2; bf16 and FP8 pages: 16-byte
@@ -214,37 +172,6 @@ __device__ __forceinline__ void load_half(HalfRecord<F>& r, const uint8_t* page,
   r.gamma = __ldg(reinterpret_cast<const float*>(page + kBlock * 2 * B) + tok);
 }
 
-// Eight 16-bit values: chunk i of the lane's share.
-template <int F>
-__device__ __forceinline__ uint4 chunk_of(const HalfRecord<F>& r, int i, const HalfTable& t) {
-  if constexpr (F == 0) {
-    return make_uint4(r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]);
-  } else if constexpr (F == 8) {
-    uint32_t o[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t w = r.w[2 * i + (k >> 1)];
-      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((k & 1) ? w >> 16 : w & 0xFFFFu), __NV_E4M3);
-      o[k] = (uint32_t)h.x | ((uint32_t)h.y << 16);
-    }
-    return make_uint4(o[0], o[1], o[2], o[3]);
-  } else if constexpr (F == 4) {
-    return centroids8<4>(r.w[i], t);
-  } else if constexpr (F == 3) {  // 24 bits to nibbles
-    const int bit = 24 * i;
-    uint32_t x = r.w[bit >> 5] >> (bit & 31);
-    if ((bit & 31) > 8) x |= r.w[(bit >> 5) + 1] << (32 - (bit & 31));
-    const uint32_t u = (x & 0x00000FFFu) | ((x & 0x00FFF000u) << 4);
-    const uint32_t v = (u & 0x003F003Fu) | ((u & 0x0FC00FC0u) << 2);
-    return centroids8<3>((v & 0x07070707u) | ((v & 0x38383838u) << 1), t);
-  } else {  // 16 bits to nibbles
-    const uint32_t x = (r.w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu;
-    uint32_t u = (x | x << 8) & 0x00FF00FFu;
-    u = (u | u << 4) & 0x0F0F0F0Fu;
-    return centroids8<2>((u | u << 2) & 0x33333333u, t);
-  }
-}
-
 // Exponent e with every magnitude of the lane's half of a bf16 token below 2^e.
 __device__ __forceinline__ int range_of(const HalfRecord<0>& r) {
   uint32_t m = 0u;
@@ -309,11 +236,6 @@ __device__ __forceinline__ void store_half(const HalfRecord<F>& r, uint32_t dst,
   }
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
 // Rows of Q, a quad of lanes a row, lane q holding coordinates [32 q, 32 q + 32).  load_q
@@ -415,6 +337,7 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
   constexpr int kpage = KF == 0 ? kBlock * kD * 2 : (KF == 8 ? kBlock * kD : kBlock * (kD * KF / 8 + 4));
   constexpr int vpage = VF == 0 ? kBlock * kD * 2 : kBlock * (kD * VF / 8 + 4);
   extern __shared__ __align__(128) unsigned char gen[];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the own tokens' kernel needs nothing of this one
   const uint32_t base = smem_u32(gen);
   if (base & 1023u) {  // (uniform) the swizzled operands need it; the window starts so on sm_103a
     if (threadIdx.x == 0) flag_status(a.status, TQ_DEV_LAYOUT);
@@ -441,6 +364,14 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
   // operands: K stage s at k_op + s, V stage s at v_op + s
   const uint32_t k_op = base + (uint32_t)(a.v_stages == 1 ? 4 : 2) * kPOperand, v_op = k_op + 2 * kPOperand;
   uint32_t* const qmax = reinterpret_cast<uint32_t*>(gen + kPOffMax);
+  // the producers' first pages on their way to L2 while Q is staged
+  int early[2] = {-1, -1};
+  const int pw = warp - kPSoftWarps, pblocks = (a.len + kBlock - 1) / kBlock;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int blk = (tile0 + t) * kPBlocks + pw;
+    if (pw >= 0 && pw < kPProdWarps && t < n && blk < pblocks) early[t] = __ldg(a.table + blk);
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(kfull + i, kPProdWarps);
@@ -477,6 +408,13 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
       const float mx = a.q_bf16 ? load_q<true>(q16, a, kvh, r0, warp, lane) : load_q<false>(q32, a, kvh, r0, warp, lane);
       const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
       if (lane == 0) atomicMax(qmax, m);
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      if (early[t] < 0 || early[t] >= a.num_blocks) continue;
+      const int64_t page = (int64_t)early[t] * a.Hkv + kvh;
+      if (128 * lane < kpage) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.kpool + page * kpage + 128 * lane));
+      if (128 * lane < vpage) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.vpool + page * vpage + 128 * lane));
     }
     __syncthreads();
     const int qe = KF == 0 ? 0 : min(max((int)(*qmax >> 23) - 126 + kSpare, -100), 100);
@@ -641,36 +579,20 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
     // ---- the stream's partial: (accumulator, reference, denominator) of each row
     if (ok && count > 0) ok = __all_sync(0xffffffffu, mbar_wait(odone + s, 0));
     tc_fence_after();
-    if (live) {
-      const int r = r0 + trow + lane;
+    if (live) {  // a lane a row: 16-byte pieces of 32 rows next to each other, one warp store 512 bytes
       const int64_t pi = a.pair ? blockIdx.y : 2 * blockIdx.y + s;
-      const int64_t row = pi * a.all_rows + (int64_t)(r / a.g) * a.Hq + kvh * a.g + r % a.g;
+      const int64_t tile = (pi * a.Hkv + kvh) * a.row_tiles + (r0 + trow) / 32;
       const bool any = ok && C != -INFINITY;
-      if (r < a.rows) {
-        a.ml[2 * row] = any ? C - kPShift : -INFINITY;
-        a.ml[2 * row + 1] = any ? l : 0.0f;
-      }
+      a.ml[tile * 32 + lane] = any ? make_float2(C - kPShift, l) : make_float2(-INFINITY, 0.0f);
       if (ok && count > 0) {
-        // through shared memory (the first four operands, Q and K: the last logits have read them),
-        // so that a warp's store is one row: 16-byte piece c of row i lies at piece c ^ i
-        unsigned char* const mine = gen + warp * (32 * kD * 4);
+        uint4* const o = reinterpret_cast<uint4*>(a.part + tile * (32 * kD)) + lane;
         uint32_t ra[32];
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           tmem_ld32_async(to + 32 * c, ra);
           tmem_wait_ld32(ra);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<uint4*>(mine + lane * (kD * 4) + (((8 * c + k) ^ lane) << 4)) =
-                make_uint4(ra[4 * k], ra[4 * k + 1], ra[4 * k + 2], ra[4 * k + 3]);
-        }
-        __syncwarp();
-        const int last = min(32, a.rows - (r0 + trow));
-#pragma unroll 4
-        for (int i = 0; i < last; ++i) {
-          const int64_t ri = __shfl_sync(0xffffffffu, row, i);
-          reinterpret_cast<uint4*>(a.part + ri * kD)[lane] =
-              *reinterpret_cast<const uint4*>(mine + i * (kD * 4) + ((lane ^ i) << 4));
+          for (int k = 0; k < 8; ++k) o[(8 * c + k) * 32] = make_uint4(ra[4 * k], ra[4 * k + 1], ra[4 * k + 2], ra[4 * k + 3]);
         }
       }
     }
@@ -837,98 +759,162 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
 }
 
 struct MergeArgs {
-  const float* part;  // the prefix's
-  const float* ml;
-  int splits;
-  const float* own_part;  // the decode's [B][Hq][own_splits][d]
-  const float* own_ml;
+  const float* part;  // the prefix's (layout at PrefixArgs)
+  const float2* ml;
+  int partials, row_tiles;
+  const float* own_part;  // [B][Hq][own_splits][d]
+  const float2* own_ml;   // [B][Hq][own_splits]
   int own_splits;  // 0: none
   UnitMap um;
-  int64_t rows;      // B * Hq
+  int rows;          // rows of a KV head
   const float* rot;  // signs of the inverse rotation (null: none)
   float value_scale; // 1 / the factor of the values' table
   void* out;
   int out_bf16;
 };
 
-// A warp per (sequence, query head), lane l holding coordinates 4 l .. 4 l + 3: joins the
-// partials at their common maximum in a fixed order, divides, applies Pi^T.
-__global__ void __launch_bounds__(128) k_prefix_merge(const MergeArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (row >= a.rows) return;
-  const int b = (int)(row / a.um.Hq), head = (int)(row - (int64_t)b * a.um.Hq);
-  const int unit = (b * a.um.Hkv + head / a.um.g) * a.um.ngroups + (head % a.um.g) / a.um.hpw;
-  // reference of all partials
-  auto own_live = [&](int s) { return s < a.own_splits && slot_live(unit, a.own_splits, s, a.um.nw); };
-  float M = -INFINITY;
-  for (int s = lane; s < a.splits; s += 32) M = fmaxf(M, __ldg(a.ml + (s * a.rows + row) * 2));
-  for (int s = lane; s < a.own_splits; s += 32)
-    if (own_live(s)) M = fmaxf(M, __ldg(a.own_ml + (row * a.own_splits + s) * 2));
+// A CTA: 8 rows of one KV head; thread (w, lane) holds two 16-byte pieces, coordinates
+// 4 c .. 4 c + 3 for c = 8 w + 4 k + lane / 8, of row lane % 8, so that a warp's load is four
+// runs of 128 bytes.  Joins the partials at their common reference in a fixed order, divides,
+// applies Pi^T (coordinate bits 0, 1 and 4 in the thread, 2 and 3 across lanes, 5 and 6 across
+// warps).
+constexpr int kMergeRound = 64;  // partials a round
+__global__ void __launch_bounds__(128) k_prefix_merge(const __grid_constant__ MergeArgs a) {
+  __shared__ float4 sm[4][2][32];
+  __shared__ float2 fl[kMergeRound][8];  // a round's references, then factors, and denominators
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int tiles8 = (a.rows + 7) / 8;
+  const int kvh = blockIdx.x / tiles8;
+  const int r = (blockIdx.x - kvh * tiles8) * 8 + (lane & 7);
+  const bool live = r < a.rows;
+  const int b = (live ? r : 0) / a.um.g, hh = (live ? r : 0) - b * a.um.g;
+  const int64_t row = (int64_t)b * a.um.Hq + kvh * a.um.g + hh;
+  const int unit = (b * a.um.Hkv + kvh) * a.um.ngroups + hh / a.um.hpw;
+  const int64_t step = (int64_t)a.um.Hkv * a.row_tiles * 32;  // rows between partials
+  const int64_t prow = (int64_t)kvh * a.row_tiles * 32 + (live ? r : 0);
+  const int c0 = 8 * w + (lane >> 3);  // and c0 + 4
+  const float2* const ml = a.ml + prow;
+  const float2* const own_ml = a.own_ml + row * a.own_splits;
+  const float4* const part =
+      reinterpret_cast<const float4*>(a.part) + (prow & ~(int64_t)31) * (kD / 4) + c0 * 32 + (prow & 31);
+  const float4* const own = reinterpret_cast<const float4*>(a.own_part + row * a.own_splits * kD) + c0;
+  float sgn[8];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  float L = 0.0f;
-  // 32 partials a round: lane s holds partial s's factor, eight loads of values in flight
-  auto join = [&](const float* part, int64_t step, float m, float l, int count) {
-    const float f = m == -INFINITY ? 0.0f : exp2f(m - M);
-    L = fmaf(l, f, L);
-    for (int s0 = 0; s0 < count; s0 += 8) {
-      float4 v[8];
+  for (int i = 0; i < 8; ++i) sgn[i] = a.rot ? __ldg(a.rot + 4 * (c0 + 4 * (i >> 2)) + (i & 3)) * 0.08838834764831845f : 1.0f;
+  grid_dep_wait();  // both kernels' partials
+  float y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  float M = -INFINITY, L = 0.0f;
+  const int total = a.partials + a.own_splits;  // the prefix's partials, then the own tokens' slots
+  for (int p0 = 0; p0 < total; p0 += kMergeRound) {
+    const int n = min(kMergeRound, total - p0);
+    // (references and denominators of the round's partials: 16 threads a row)
+    for (int k = threadIdx.x >> 3; k < n; k += 16) {
+      const int s = p0 + k - a.partials;
+      float2 e = make_float2(-INFINITY, 0.0f);
+      if (s < 0) e = __ldcg(ml + (p0 + k) * step);
+      else if (slot_live(unit, a.own_splits, s, a.um.nw)) e = __ldcg(own_ml + s);
+      fl[k][lane & 7] = e;
+    }
+    __syncthreads();
+    float nm = M;
+    for (int k = 0; k < n; ++k) nm = fmaxf(nm, fl[k][lane & 7].x);
+    const float f0 = M == -INFINITY ? 0.0f : exp2f(M - nm);
+    L *= f0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float fk = __shfl_sync(0xffffffffu, f, (s0 + k) & 31);
-        v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (s0 + k < count && fk != 0.0f) v[k] = __ldg(reinterpret_cast<const float4*>(part + (s0 + k) * step) + lane);
+    for (int i = 0; i < 8; ++i) y[i] *= f0;
+    M = nm;
+    constexpr int kBatch = 8;  // partials whose loads are in flight; an empty one is not read
+    for (int k0 = 0; k0 < n; k0 += kBatch) {
+      float4 t[kBatch][2];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        t[k][0] = t[k][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (k0 + k < n && fl[k0 + k][lane & 7].x != -INFINITY) {
+          const int q = p0 + k0 + k, s = q - a.partials;
+          const float4* v = s < 0 ? part + q * step * (kD / 4) : own + s * (kD / 4);
+          t[k][0] = __ldcg(v);
+          t[k][1] = __ldcg(v + (s < 0 ? 4 * 32 : 4));
+        }
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float fk = __shfl_sync(0xffffffffu, f, (s0 + k) & 31);
-        y[0] = fmaf(v[k].x, fk, y[0]);
-        y[1] = fmaf(v[k].y, fk, y[1]);
-        y[2] = fmaf(v[k].z, fk, y[2]);
-        y[3] = fmaf(v[k].w, fk, y[3]);
+      for (int k = 0; k < kBatch; ++k) {
+        if (k0 + k >= n) break;
+        const float2 e = fl[k0 + k][lane & 7];
+        const float f = e.x == -INFINITY ? 0.0f : exp2f(e.x - M);
+        L = fmaf(e.y, f, L);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          y[4 * i] = fmaf(t[k][i].x, f, y[4 * i]);
+          y[4 * i + 1] = fmaf(t[k][i].y, f, y[4 * i + 1]);
+          y[4 * i + 2] = fmaf(t[k][i].z, f, y[4 * i + 2]);
+          y[4 * i + 3] = fmaf(t[k][i].w, f, y[4 * i + 3]);
+        }
       }
     }
-  };
-  for (int s0 = 0; s0 < a.splits; s0 += 32) {
-    const int s = s0 + lane;
-    const bool in = s < a.splits;
-    const float2 ml = in ? __ldg(reinterpret_cast<const float2*>(a.ml) + s * a.rows + row) : make_float2(-INFINITY, 0.0f);
-    join(a.part + (s0 * a.rows + row) * kD, a.rows * kD, ml.x, ml.y, min(32, a.splits - s0));
+    __syncthreads();
   }
-  for (int s0 = 0; s0 < a.own_splits; s0 += 32) {
-    const int s = s0 + lane;
-    const float2 ml = own_live(s) ? __ldg(reinterpret_cast<const float2*>(a.own_ml) + row * a.own_splits + s)
-                                  : make_float2(-INFINITY, 0.0f);
-    join(a.own_part + (row * a.own_splits + s0) * kD, kD, ml.x, ml.y, min(32, a.own_splits - s0));
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
   const float inv = L > 0.0f ? a.value_scale / L : 0.0f;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) y[k] *= inv;
-  if (a.rot) {  // Pi^T y = D H y / sqrt(d): bits 0, 1 in the lane, bits 2..6 across lanes
-    const float t0 = y[0] + y[1], t1 = y[0] - y[1], t2 = y[2] + y[3], t3 = y[2] - y[3];
-    y[0] = t0 + t2; y[2] = t0 - t2; y[1] = t1 + t3; y[3] = t1 - t3;
+  for (int i = 0; i < 8; ++i) y[i] *= inv;
+  if (a.rot) {  // Pi^T y = D H y / sqrt(d)
 #pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-      const bool upper = (lane & m) != 0;
+    for (int h = 1; h < 8; h <<= 1) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float o = __shfl_xor_sync(0xffffffffu, y[k], m);
-        y[k] = upper ? (o - y[k]) : (y[k] + o);
+      for (int i = 0; i < 8; ++i) {
+        if ((i & h) == 0) {
+          const float u = y[i], v = y[i + h];
+          y[i] = u + v;
+          y[i + h] = u - v;
+        }
       }
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) y[k] *= 0.08838834764831845f * __ldg(a.rot + 4 * lane + k);
-  }
+    for (int m = 8; m < 32; m <<= 1) {
+      const bool upper = (lane & m) != 0;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if (a.out_bf16) store_elem(reinterpret_cast<__nv_bfloat16*>(a.out) + row * kD + 4 * lane + k, y[k]);
-    else store_elem(reinterpret_cast<float*>(a.out) + row * kD + 4 * lane + k, y[k]);
+      for (int i = 0; i < 8; ++i) {
+        const float o = __shfl_xor_sync(0xffffffffu, y[i], m);
+        y[i] = upper ? (o - y[i]) : (y[i] + o);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) sm[w][i][lane] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+    __syncthreads();
+    const float s0 = w & 1 ? -1.0f : 1.0f, s1 = w & 2 ? -1.0f : 1.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float4 p = sm[0][i][lane], q = sm[1][i][lane], u = sm[2][i][lane], v = sm[3][i][lane];
+      y[4 * i] = ((p.x + s0 * q.x) + s1 * (u.x + s0 * v.x)) * sgn[4 * i];
+      y[4 * i + 1] = ((p.y + s0 * q.y) + s1 * (u.y + s0 * v.y)) * sgn[4 * i + 1];
+      y[4 * i + 2] = ((p.z + s0 * q.z) + s1 * (u.z + s0 * v.z)) * sgn[4 * i + 2];
+      y[4 * i + 3] = ((p.w + s0 * q.w) + s1 * (u.w + s0 * v.w)) * sgn[4 * i + 3];
+    }
+  }
+  if (!live) return;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t at = row * kD + 4 * (c0 + 4 * i);
+    if (a.out_bf16) {
+      __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.out) + at;
+      if ((reinterpret_cast<uintptr_t>(a.out) & 7u) == 0u) {
+        *reinterpret_cast<uint2*>(o) = make_uint2(pack_b2(y[4 * i], y[4 * i + 1]), pack_b2(y[4 * i + 2], y[4 * i + 3]));
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = __float2bfloat16_rn(y[4 * i + k]);
+      }
+    } else {
+      float* o = reinterpret_cast<float*>(a.out) + at;
+      if ((reinterpret_cast<uintptr_t>(a.out) & 15u) == 0u) {
+        *reinterpret_cast<float4*>(o) = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = y[4 * i + k];
+      }
+    }
   }
 }
+
+int own_splits(int max_blocks) { return max_blocks <= kOwnMaxBlocks ? (max_blocks + kOwnChunk - 1) / kOwnChunk : 0; }
 
 // How the prefix is cut: streams over two tiles of rows (pair) or over tiles of tokens,
 // CTAs over the rows and splits of the tokens.  The splits are chosen so that the CTAs,
@@ -964,8 +950,8 @@ static PrefixPlan prefix_plan(const tq_cache_desc& d, int batch, int num_q_heads
 }
 
 size_t prefix_partial_bytes(const tq_cache_desc& d, int batch, int num_q_heads, int64_t prefix_len, int num_sms) {
-  const size_t rows = (size_t)batch * num_q_heads;
-  return (size_t)prefix_plan(d, batch, num_q_heads, prefix_len, num_sms).partials * rows * (kD + 2) * sizeof(float);
+  const size_t tiles = ((size_t)batch * (num_q_heads / d.num_kv_heads) + 31) / 32 * d.num_kv_heads;
+  return (size_t)prefix_plan(d, batch, num_q_heads, prefix_len, num_sms).partials * tiles * 32 * (kD + 2) * sizeof(float);
 }
 
 template <int KF, int VF>
@@ -989,11 +975,11 @@ static cudaError_t run_prefix_v(const PrefixArgs& a, int bits_v, int splits, cud
 
 cudaError_t launch_prefix_decode(const PrefixCall& c, cudaStream_t st) {
   const tq_cache_desc& d = *c.own.desc;
-  const int64_t rows = (int64_t)c.own.batch * c.own.num_q_heads;
   const bool coded = d.fmt.kv_format != TQ_KV_BF16;
   MergeArgs m = {};
   m.um = unit_map(d, c.own.num_q_heads);
-  m.rows = rows;
+  m.rows = c.own.batch * m.um.g;
+  m.row_tiles = (m.rows + 31) / 32;
   m.rot = coded ? d.rotation : nullptr;
   const float fk = d.fmt.kv_format == TQ_KV_PACKED ? table_factor(d.centroids_k, d.fmt.bits_k) : 1.0f;
   const float fv = coded ? table_factor(d.centroids_v, d.fmt.bits_v) : 1.0f;
@@ -1004,7 +990,7 @@ cudaError_t launch_prefix_decode(const PrefixCall& c, cudaStream_t st) {
   if (c.own.max_blocks > 0) {
     const DecodeWorkspace ws = decode_workspace(c.own.batch, c.own.num_q_heads, c.own.splits, kD, false);
     m.own_part = reinterpret_cast<const float*>(c.own.workspace + ws.part_off);
-    m.own_ml = reinterpret_cast<const float*>(c.own.workspace + ws.ml_off);
+    m.own_ml = reinterpret_cast<const float2*>(c.own.workspace + ws.ml_off);
     m.own_splits = c.own.splits;
     off = ws.total;
   }
@@ -1029,9 +1015,9 @@ cudaError_t launch_prefix_decode(const PrefixCall& c, cudaStream_t st) {
     a.tiles_per_split = p.tiles_per_split;
     a.scale = c.own.sm_scale * 1.4426950408889634f / fk;
     a.rot = d.rotation;
-    a.all_rows = rows;
+    a.row_tiles = m.row_tiles;
     a.part = reinterpret_cast<float*>(c.own.workspace + off);
-    a.ml = a.part + (size_t)p.partials * rows * kD;
+    a.ml = reinterpret_cast<float2*>(a.part + (size_t)p.partials * a.Hkv * a.row_tiles * 32 * kD);
     a.cbk = codebook_of(d, 0);
     a.cbv = codebook_of(d, 1);
     for (int i = 0; i < 16; ++i) {
@@ -1053,18 +1039,35 @@ cudaError_t launch_prefix_decode(const PrefixCall& c, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     m.part = a.part;
     m.ml = a.ml;
-    m.splits = p.partials;
+    m.partials = p.partials;
   }
   if (c.own.max_blocks > 0) {
     DecodeCall own = c.own;
     own.partials_only = true;
     own.factor_k = fk;
     own.factor_v = fv;
-    const cudaError_t e = launch_decode(own, st);
+    cudaError_t e;
+    if (own_splits(own.max_blocks) > 0) {  // short contexts
+      m.um.nw = 1;  // (every slot is written)
+      e = launch_own(own, c.prefix_len > 0, st);
+    } else {
+      e = launch_decode(own, st);
+    }
     if (e != cudaSuccess) return e;
   }
-  k_prefix_merge<<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(m);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(m.um.Hkv * ((m.rows + 7) / 8)));
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;  // a dependent of this call's own kernels; without any it waits for nothing it needs
+  if (c.prefix_len < 1 && c.own.max_blocks < 1) cfg.numAttrs = 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_prefix_merge, m);
   count_launch();
+  if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 
