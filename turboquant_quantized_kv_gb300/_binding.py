@@ -202,42 +202,49 @@ def _ptr(t, name):
 
 def _stream(stream):
     torch = _torch()
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return ctypes.c_void_p(stream.cuda_stream)
+    # the current stream of the current device, without building a Stream object
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
-def _heads(t, out, name, positions):
-    """A tq_heads of t [n_tokens, heads, d] (any token and head strides) and its output rows."""
+def _check_rows(x, what, n):
+    """Raises for rows that are not [n, heads, d] on the device with a contiguous last dimension."""
+    if not x.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % what)
+    if x.dim() != 3 or x.shape[2] != TQ_HEAD_DIM or x.shape[0] != n:
+        raise ValueError("%s must be [%d, heads, %d], got %s" % (what, n, TQ_HEAD_DIM, tuple(x.shape)))
+    if x.numel() > 0 and x.stride(2) != 1:
+        raise ValueError("%s must be contiguous in its last dimension" % what)
+
+
+def _heads(t, out, name, n):
+    """A tq_heads of t [n, heads, d] (any token and head strides) and its output rows."""
     if t is None:
         return None
-    h = Heads()
-    for x, what in ((t, name), (out, name + "_out")):
-        if x is None:
-            continue
-        if not x.is_cuda:
-            raise ValueError("%s must be a CUDA tensor" % what)
-        if x.dim() != 3 or x.shape[2] != TQ_HEAD_DIM or x.shape[0] != positions.shape[0]:
-            raise ValueError("%s must be [%d, heads, %d], got %s" % (what, positions.shape[0], TQ_HEAD_DIM,
-                                                                     tuple(x.shape)))
-        if x.numel() > 0 and x.stride(2) != 1:
-            raise ValueError("%s must be contiguous in its last dimension" % what)
-    if out is not None and (out.shape != t.shape or out.dtype != t.dtype):
-        raise ValueError("%s_out must have %s's shape and type" % (name, name))
-    h.inp, h.num_heads = t.data_ptr(), t.shape[1]
-    h.in_token_stride, h.in_head_stride = t.stride(0), t.stride(1)
-    if out is not None:
-        h.out = out.data_ptr()
-        h.out_token_stride, h.out_head_stride = out.stride(0), out.stride(1)
-    return h
+    _check_rows(t, name, n)
+    s0, s1, _ = t.stride()
+    if out is None:
+        return Heads(t.data_ptr(), None, t.shape[1], s0, s1, 0, 0)
+    if out is not t:
+        if out.shape != t.shape or out.dtype != t.dtype:
+            raise ValueError("%s_out must have %s's shape and type" % (name, name))
+        _check_rows(out, name + "_out", n)
+    o0, o1, _ = out.stride()
+    return Heads(t.data_ptr(), out.data_ptr(), t.shape[1], s0, s1, o0, o1)
 
 
 def _index_ptr(t, name, dtype, shape):
     """Device pointer of an index tensor after checking its type and shape."""
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    return _ptr(t, name)
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
 
 
 def _ref(struct):
@@ -298,7 +305,7 @@ def apply_rope(rope, positions, q, k=None, q_out=None, k_out=None, transpose=Fal
         k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
     n = int(ref.shape[0])
     pos = _index_ptr(positions, "positions", torch.int64, (n,))
-    hq, hk = _heads(q, q_out, "q", positions), _heads(k, k_out, "k", positions)
+    hq, hk = _heads(q, q_out, "q", n), _heads(k, k_out, "k", n)
     _check(lib().tq_rope_apply(ctypes.byref(rope.desc), 1 if transpose else 0, _ref(hq), _ref(hk), _dtype_code(ref),
                                pos, n, _stream(stream)))
     return q_out, k_out
@@ -493,8 +500,8 @@ class Layer:
         slots = _index_ptr(slot_mapping, "slot_mapping", torch.int64, (n,))
         if q is not None and q_out is None:
             q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        hq, hk = _heads(q, q_out, "q", positions), _heads(k, k_out, "k", positions)
-        hv = _heads(v, None, "v", positions)
+        hq, hk = _heads(q, q_out, "q", n), _heads(k, k_out, "k", n)
+        hv = _heads(v, None, "v", n)
         _check(lib().tq_rope_append(ctypes.byref(self.desc), ctypes.byref(rope.desc), _ref(hq), _ref(hk), _ref(hv),
                                     _dtype_code(ref), pos, slots, n, _stream(stream)))
         return q_out

@@ -102,7 +102,7 @@ __device__ __forceinline__ void load_run(Run<F, N>& r, const uint8_t* page, int 
 }
 
 template <int KF, int VF>
-__global__ void __launch_bounds__(kOwnWarps * 32, KF == 0 ? 2 : 3) k_own(const __grid_constant__ OwnArgs a) {
+__global__ void __launch_bounds__(kOwnWarps * 32, 3) k_own(const __grid_constant__ OwnArgs a) {
   constexpr bool kCodedK = KF >= 2 && KF <= 4, kCodedV = VF != 0;
   constexpr int kpage = KF == 0 ? kBlock * kD * 2 : (KF == 8 ? kBlock * kD : kBlock * (kD * KF / 8 + 4));
   constexpr int vpage = VF == 0 ? kBlock * kD * 2 : kBlock * (kD * VF / 8 + 4);
@@ -113,13 +113,48 @@ __global__ void __launch_bounds__(kOwnWarps * 32, KF == 0 ? 2 : 3) k_own(const _
   const int unit = blockIdx.x, hg = unit % a.ngroups, kvh = (unit / a.ngroups) % a.Hkv, b = unit / (a.ngroups * a.Hkv);
   const int rows = min(8, a.g - 8 * hg);
   const int64_t row0 = (int64_t)b * a.Hq + kvh * a.g + 8 * hg;
-  int ctx = __ldg(a.ctx_lens + b);
+  // context length, block ids (lane k: the warp's k-th) and queries are requested together
+  const int ctx_raw = __ldg(a.ctx_lens + b);
+  const int j0 = blockIdx.y * kOwnChunk;
+  static_assert(kOwnChunk == 4 * kOwnWarps, "four blocks a warp");
+  const int jm = j0 + warp + kOwnWarps * (lane & 3);
+  const int idm = jm < a.max_blocks ? __ldg(a.table + (int64_t)b * a.max_blocks + jm) : -1;
+  const bool rlive = g_ < rows;
+  const int64_t qrow = row0 + (rlive ? g_ : 0);
+  float x[32], rot4[4];
+  if constexpr (kCodedK) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) rot4[k] = __ldg(a.rot + 32 * k + lane);
+    if (a.q_bf16) load32<__nv_bfloat16>(reinterpret_cast<const __nv_bfloat16*>(a.q) + qrow * kD + 32 * tig, x);
+    else load32<float>(reinterpret_cast<const float*>(a.q) + qrow * kD + 32 * tig, x);
+  } else {  // the coordinates of the keys' pieces
+    constexpr int E = KF == 0 ? 8 : 16;  // of a piece
+#pragma unroll
+    for (int i = 0; i < 32; i += 8) {
+      const int64_t at = qrow * kD + 4 * E * (i / E) + E * tig + i % E;
+      if (a.q_bf16) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) + at));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          x[i + 2 * k] = __uint_as_float(w[k] << 16);
+          x[i + 2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; k += 4) {
+          const float4 v = __ldg(reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.q) + at + k));
+          x[i + k] = v.x; x[i + k + 1] = v.y; x[i + k + 2] = v.z; x[i + k + 3] = v.w;
+        }
+      }
+    }
+  }
+  int ctx = ctx_raw;
   if (ctx < 0 || ctx > a.max_blocks * kBlock) {
     if (threadIdx.x == 0 && blockIdx.y == 0 && hg == 0 && kvh == 0) flag_status(a.status, TQ_DEV_BAD_CONTEXT);
     ctx = ctx < 0 ? 0 : a.max_blocks * kBlock;
   }
   const int j1 = min((ctx + kBlock - 1) / kBlock, (int)(blockIdx.y + 1) * kOwnChunk);
-  const int j0 = blockIdx.y * kOwnChunk;
   if (j0 >= j1) {  // nothing of the context here
     if (threadIdx.x < rows) {
       float* ml = a.ml + 2 * ((row0 + threadIdx.x) * a.splits + blockIdx.y);
@@ -129,10 +164,8 @@ __global__ void __launch_bounds__(kOwnWarps * 32, KF == 0 ? 2 : 3) k_own(const _
     grid_dep_wait();
     return;
   }
-  const int32_t* ids = a.table + (int64_t)b * a.max_blocks;
-  // the warp's blocks: lane k holds the id of the k-th, and their pages start towards L2
-  static_assert(kOwnChunk == 4 * kOwnWarps, "four blocks a warp");
-  const int mine = lane < 4 && j0 + warp + kOwnWarps * lane < j1 ? __ldg(ids + j0 + warp + kOwnWarps * lane) : -1;
+  // the warp's blocks start towards L2
+  const int mine = jm < j1 ? idm : -1;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int id = __shfl_sync(0xffffffffu, mine, k);
@@ -147,42 +180,14 @@ __global__ void __launch_bounds__(kOwnWarps * 32, KF == 0 ? 2 : 3) k_own(const _
   uint32_t qf[8][4];
   float rs;
   {
-    float x[32];
-    const bool live = g_ < rows;
-    const int64_t row = row0 + (live ? g_ : 0);
-    if constexpr (kCodedK) {
-      if (a.q_bf16) load32<__nv_bfloat16>(reinterpret_cast<const __nv_bfloat16*>(a.q) + row * kD + 32 * tig, x);
-      else load32<float>(reinterpret_cast<const float*>(a.q) + row * kD + 32 * tig, x);
-    } else {  // the coordinates of the keys' pieces
-      constexpr int E = KF == 0 ? 8 : 16;  // of a piece
-#pragma unroll
-      for (int i = 0; i < 32; i += 8) {
-        const int64_t at = row * kD + 4 * E * (i / E) + E * tig + i % E;
-        if (a.q_bf16) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) + at));
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            x[i + 2 * k] = __uint_as_float(w[k] << 16);
-            x[i + 2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; k += 4) {
-            const float4 v = __ldg(reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.q) + at + k));
-            x[i + k] = v.x; x[i + k + 1] = v.y; x[i + k + 2] = v.z; x[i + k + 3] = v.w;
-          }
-        }
-      }
-    }
-    const float flip = live ? (a.scale < 0.0f ? -1.0f : 1.0f) : 0.0f;
+    const float flip = rlive ? (a.scale < 0.0f ? -1.0f : 1.0f) : 0.0f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) x[i] *= flip;
     if constexpr (kCodedK) {
       uint32_t signs = 0u;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint32_t m = __ballot_sync(0xffffffffu, __ldg(a.rot + 32 * k + lane) < 0.0f);
+        const uint32_t m = __ballot_sync(0xffffffffu, rot4[k] < 0.0f);
         if (tig == k) signs = m;
       }
 #pragma unroll
