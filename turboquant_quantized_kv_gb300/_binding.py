@@ -209,29 +209,30 @@ def _stream(stream):
 
 
 def _check_rows(x, what, n):
-    """Raises for rows that are not [n, heads, d] on the device with a contiguous last dimension."""
+    """Strides of rows [n, heads, d] on the device with a contiguous last dimension; raises for others."""
     if not x.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % what)
-    if x.dim() != 3 or x.shape[2] != TQ_HEAD_DIM or x.shape[0] != n:
-        raise ValueError("%s must be [%d, heads, %d], got %s" % (what, n, TQ_HEAD_DIM, tuple(x.shape)))
-    if x.numel() > 0 and x.stride(2) != 1:
+    shape = x.shape
+    if len(shape) != 3 or shape[2] != TQ_HEAD_DIM or shape[0] != n:
+        raise ValueError("%s must be [%d, heads, %d], got %s" % (what, n, TQ_HEAD_DIM, tuple(shape)))
+    strides = x.stride()
+    if strides[2] != 1 and x.numel() > 0:
         raise ValueError("%s must be contiguous in its last dimension" % what)
+    return strides
 
 
 def _heads(t, out, name, n):
     """A tq_heads of t [n, heads, d] (any token and head strides) and its output rows."""
     if t is None:
         return None
-    _check_rows(t, name, n)
-    s0, s1, _ = t.stride()
+    st = so = _check_rows(t, name, n)
     if out is None:
-        return Heads(t.data_ptr(), None, t.shape[1], s0, s1, 0, 0)
+        return Heads(t.data_ptr(), None, t.shape[1], st[0], st[1], 0, 0)
     if out is not t:
         if out.shape != t.shape or out.dtype != t.dtype:
             raise ValueError("%s_out must have %s's shape and type" % (name, name))
-        _check_rows(out, name + "_out", n)
-    o0, o1, _ = out.stride()
-    return Heads(t.data_ptr(), out.data_ptr(), t.shape[1], s0, s1, o0, o1)
+        so = _check_rows(out, name + "_out", n)
+    return Heads(t.data_ptr(), out.data_ptr(), t.shape[1], st[0], st[1], so[0], so[1])
 
 
 def _index_ptr(t, name, dtype, shape):

@@ -378,6 +378,7 @@ float table_factor(const float* centroids, int bits) {
   for (int j = 0; j < half; ++j) {
     const float c = centroids[half + j];
     if (!(c > 0.0f)) continue;
+    const float inv = 1.0f / c;
     for (int i = 0; i < kCandidates; ++i) {  // 11 significant bits, nearest even
       const float x = c * (1.0f + (float)i / kCandidates);
       uint32_t u;
@@ -385,15 +386,17 @@ float table_factor(const float* centroids, int bits) {
       u = (u + 0xFFFu + ((u >> 13) & 1u)) & ~0x1FFFu;
       float r;
       std::memcpy(&r, &u, 4);
-      const float e = std::fabs(r - x) / x;
+      const float e = std::fabs(r - x) * inv;
       err[i] = e > err[i] ? e : err[i];
     }
   }
-  for (int i = 0; i < kCandidates; ++i)
-    if (err[i] < best_err) {
-      best_err = err[i];
-      best = 1.0f + (float)i / kCandidates;
+  for (int i = 0; i < kCandidates; ++i) {
+    const float f = 1.0f + (float)i / kCandidates, e = err[i] / f;
+    if (e < best_err) {
+      best_err = e;
+      best = f;
     }
+  }
   return best;
 }
 

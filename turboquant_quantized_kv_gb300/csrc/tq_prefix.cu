@@ -42,6 +42,8 @@
 // value.  Sums, maxima and denominators are fp32.
 #include <cuda_fp8.h>
 
+#include <atomic>
+
 #include "tq_async.cuh"
 #include "tq_device.cuh"
 #include "tq_internal.h"
@@ -957,8 +959,16 @@ size_t prefix_partial_bytes(const tq_cache_desc& d, int batch, int num_q_heads, 
 template <int KF, int VF>
 static cudaError_t run_prefix(const PrefixArgs& a, int splits, cudaStream_t st) {
   auto kern = k_prefix<KF, VF>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPSmem);
+  static std::atomic<uint64_t> ready{0};  // devices (up to 64) whose kernel has its shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(ready.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPSmem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_release);
+  }
   kern<<<dim3((unsigned)(a.row_blocks * a.Hkv), (unsigned)splits), kPThreads, kPSmem, st>>>(a);
   count_launch();
   return cudaGetLastError();

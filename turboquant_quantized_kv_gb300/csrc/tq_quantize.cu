@@ -1083,8 +1083,27 @@ __global__ void __launch_bounds__(kThreads) k_dequant(const uint8_t* __restrict_
     }
     if (valid) {
       TOut* o = out + vec * kD + 32 * q;
+      if ((reinterpret_cast<uintptr_t>(out) & 15u) == 0u) {  // 16-byte stores
+        if constexpr (sizeof(TOut) == 2) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) store_elem<TOut>(o + i, v[i]);
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(v[8 * i + 2 * k], v[8 * i + 2 * k + 1]);
+              w[k] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+            reinterpret_cast<uint4*>(o)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            reinterpret_cast<float4*>(o)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) store_elem<TOut>(o + i, v[i]);
+      }
     }
   }
 }

@@ -59,7 +59,7 @@ struct RopeArgs {
   int n_rows;       // tensors
   int heads;        // of all of them
   int tile_tok;     // tokens a tile
-  unsigned row_blocks;  // CTAs of the rows part, after the coded part's
+  int64_t row_tiles;
   // coded part: keys (0) and values (1)
   const int64_t* slots;
   int64_t max_slot;
@@ -72,7 +72,7 @@ struct RopeArgs {
     int page_bytes;
     int bits;
     int rotate;
-    unsigned blocks;  // CTAs
+    int64_t tiles;  // of 64 vectors
     Codebook cb;
   } coded[2];
   int coded_tok;  // tokens a tile of coded vectors can touch
@@ -136,42 +136,58 @@ __device__ __forceinline__ uint32_t fp8_pair(float lo, float hi) {
   return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
 
-// One item of the rows part: W = 8 pairs (16 coordinates in two runs of eight, aligned) or
+// One item of the rows part: W = 8 pairs (16 coordinates in two aligned runs of eight) or
 // one pair, of one head of one token.
 template <typename T, int W>
 struct RowItem {
-  float a[W], b[W];  // the pairs' coordinates (or 2 W coordinates that pass through)
-  int oa, ob;        // their places in the head (interleaved: run starts, W = 8)
-  int pair;          // first pair, or -1: not rotated
+  static constexpr int kWords = W == 8 ? (int)sizeof(T) * 2 : 1;  // 32-bit words of a run (W = 1: one element)
+  uint32_t ra[kWords], rb[kWords];  // as loaded
+  float a[W], b[W];                 // the pairs' coordinates (or 2 W coordinates that pass through)
+  int oa, ob;                       // their places in the head (interleaved: run starts, W = 8)
+  int pair;                         // first pair, or -1: not rotated
 };
 
 template <typename T, int W>
-__device__ __forceinline__ void item_load(RowItem<T, W>& it, const T* head, int c, int pairs, bool interleaved) {
+__device__ __forceinline__ void item_place(RowItem<T, W>& it, int c, int pairs, bool interleaved) {
   if (W == 8) {
-    if (interleaved) {
-      it.oa = 16 * c;
-      it.ob = 16 * c + 8;
-      it.pair = 8 * c < pairs ? 8 * c : -1;
-    } else if (8 * c < pairs) {
-      it.oa = 8 * c;
-      it.ob = pairs + 8 * c;
-      it.pair = 8 * c;
-    } else {
-      it.oa = 16 * c;  // the head's coordinates from 2 pairs on, 16 an item
-      it.ob = 16 * c + 8;
-      it.pair = -1;
-    }
-    if constexpr (W == 8) {
-      load8<T>(head + it.oa, it.a);
-      load8<T>(head + it.ob, it.b);
-    }
+    const bool low = !interleaved && 8 * c < pairs;  // else 16 coordinates from 16 c on
+    it.oa = low ? 8 * c : 16 * c;
+    it.ob = low ? pairs + 8 * c : 16 * c + 8;
+    it.pair = 8 * c < pairs ? 8 * c : -1;
   } else {
     const bool live = c < pairs;
     it.oa = (interleaved || !live) ? 2 * c : c;
     it.ob = (interleaved || !live) ? 2 * c + 1 : c + pairs;
     it.pair = live ? c : -1;
-    it.a[0] = load_elem<T>(head + it.oa);
-    it.b[0] = load_elem<T>(head + it.ob);
+  }
+}
+
+template <typename T, int W>
+__device__ __forceinline__ void item_load(RowItem<T, W>& it, const T* head) {
+  if constexpr (W == 8) {
+#pragma unroll
+    for (int i = 0; i < RowItem<T, W>::kWords / 4; ++i) {
+      const uint4 u = reinterpret_cast<const uint4*>(head + it.oa)[i], v = reinterpret_cast<const uint4*>(head + it.ob)[i];
+      it.ra[4 * i] = u.x; it.ra[4 * i + 1] = u.y; it.ra[4 * i + 2] = u.z; it.ra[4 * i + 3] = u.w;
+      it.rb[4 * i] = v.x; it.rb[4 * i + 1] = v.y; it.rb[4 * i + 2] = v.z; it.rb[4 * i + 3] = v.w;
+    }
+  } else {
+    it.ra[0] = __float_as_uint(load_elem<T>(head + it.oa));
+    it.rb[0] = __float_as_uint(load_elem<T>(head + it.ob));
+  }
+}
+
+template <typename T, int W>
+__device__ __forceinline__ void item_widen(RowItem<T, W>& it) {
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    if (W == 8 && sizeof(T) == 2) {
+      it.a[i] = __uint_as_float(i & 1 ? it.ra[i >> 1] & 0xFFFF0000u : it.ra[i >> 1] << 16);
+      it.b[i] = __uint_as_float(i & 1 ? it.rb[i >> 1] & 0xFFFF0000u : it.rb[i >> 1] << 16);
+    } else {
+      it.a[i] = __uint_as_float(it.ra[i % RowItem<T, W>::kWords]);
+      it.b[i] = __uint_as_float(it.rb[i % RowItem<T, W>::kWords]);
+    }
   }
 }
 
@@ -238,15 +254,14 @@ __device__ __forceinline__ void item_store_page(const RowItem<T, W>& it, uint8_t
   }
 }
 
-// Tiles of tokens: cosines and sines to shared memory, then the items of all heads.
-template <typename T, int W>
-__device__ __forceinline__ void rope_rows(const RopeArgs& a, unsigned block, unsigned blocks, float2* cs,
-                                          const uint64_t* turns) {
+// One tile of tokens: cosines and sines to shared memory, then the items of all heads, AHEAD
+// of a thread's at a time.
+template <typename T, int W, int AHEAD>
+__device__ __forceinline__ void rope_rows(const RopeArgs& a, int64_t tile, float2* cs, const uint64_t* turns) {
   constexpr int PER = kPairs / W;  // items per head
   const int tid = threadIdx.x;
-  const int64_t tiles = (a.n_tok + a.tile_tok - 1) / a.tile_tok;
   const bool inter = a.interleaved != 0;
-  for (int64_t tile = block; tile < tiles; tile += blocks) {
+  {
     const int64_t t0 = tile * a.tile_tok;
     const int nt = (int)min((int64_t)a.tile_tok, a.n_tok - t0);
     __syncthreads();  // the table of the previous tile is no longer read
@@ -256,36 +271,52 @@ __device__ __forceinline__ void rope_rows(const RopeArgs& a, unsigned block, uns
     }
     __syncthreads();
     const int items = nt * a.heads * PER;
-    for (int i = tid; i < items; i += kRThreads) {
-      const int c = i % PER, th = i / PER;
-      const int lt = th / a.heads;
-      int h = th - lt * a.heads, s = 0;
-      while (s + 1 < a.n_rows && h >= a.rows[s].heads) h -= a.rows[s++].heads;
-      const RopeRows& r = a.rows[s];
-      const int64_t tok = t0 + lt;
-      RowItem<T, W> it;
-      item_load<T, W>(it, reinterpret_cast<const T*>(r.in) + tok * r.in_tok + h * r.in_head, c, r.rotate ? a.pairs : 0,
-                      inter);
-      item_rotate<T, W>(it, cs + lt * kPairs, a.pairs, inter);
-      if (r.out) item_store<T, W>(it, reinterpret_cast<T*>(r.out) + tok * r.out_tok + h * r.out_head);
-      if (r.page) {
-        const int64_t slot = __ldg(a.slots + tok);
-        if (slot >= a.max_slot) {
-          if (c == 0) flag_status(a.status, TQ_DEV_BAD_SLOT);
-        } else if (slot >= 0) {
-          item_store_page<T, W>(it, r.pool, r.page, slot, h, a.kv_heads);
+    const float inv_heads = 1.0f / (float)a.heads;  // (quotients below 2^13 of a few: exact)
+    for (int i0 = tid; i0 < items; i0 += AHEAD * kRThreads) {
+      RowItem<T, W> it[AHEAD];
+      int tok[AHEAD], head[AHEAD];
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        const int i = i0 + k * kRThreads;
+        if (i >= items) break;
+        const int c = i % PER, th = i / PER;
+        tok[k] = (int)(((float)th + 0.5f) * inv_heads);
+        head[k] = th - tok[k] * a.heads;
+        int h = head[k], s = 0;
+        while (s + 1 < a.n_rows && h >= a.rows[s].heads) h -= a.rows[s++].heads;
+        const RopeRows& r = a.rows[s];
+        item_place<T, W>(it[k], c, r.rotate ? a.pairs : 0, inter);
+        item_load<T, W>(it[k], reinterpret_cast<const T*>(r.in) + (t0 + tok[k]) * r.in_tok + h * r.in_head);
+      }
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        const int i = i0 + k * kRThreads;
+        if (i >= items) break;
+        int h = head[k], s = 0;
+        while (s + 1 < a.n_rows && h >= a.rows[s].heads) h -= a.rows[s++].heads;
+        const RopeRows& r = a.rows[s];
+        item_widen<T, W>(it[k]);
+        item_rotate<T, W>(it[k], cs + tok[k] * kPairs, a.pairs, inter);
+        if (r.out) item_store<T, W>(it[k], reinterpret_cast<T*>(r.out) + (t0 + tok[k]) * r.out_tok + h * r.out_head);
+        if (r.page) {
+          const int64_t slot = __ldg(a.slots + t0 + tok[k]);
+          if (slot >= a.max_slot) {
+            if (i % PER == 0) flag_status(a.status, TQ_DEV_BAD_SLOT);
+          } else if (slot >= 0) {
+            item_store_page<T, W>(it[k], r.pool, r.page, slot, h, a.kv_heads);
+          }
         }
       }
     }
   }
 }
 
-// One coded tensor: a quad of lanes a vector.  Lane q holds coordinates [16 q, 16 q + 16)
+// One tile of 64 vectors of a coded tensor: a quad of lanes a vector.  Lane q holds coordinates [16 q, 16 q + 16)
 // and [64 + 16 q, 64 + 16 q + 16): the pairs of a full rotation in either layout lie in
 // one lane, and the butterfly over them is the quad transform with the coordinate's bits
 // 0..3 and 6 inside the lane and bits 4 and 5 across lanes.
 template <typename T, int BITS>
-__device__ __forceinline__ void rope_coded(const RopeArgs& a, const RopeArgs::Coded& t, unsigned block, float2* cs,
+__device__ __forceinline__ void rope_coded(const RopeArgs& a, const RopeArgs::Coded& t, int64_t tile, float2* cs,
                                            const uint64_t* turns, const uint32_t* signw, uint32_t qtab_addr) {
   constexpr int R = 16 * BITS;
   const int tid = threadIdx.x, lane = tid & 31, q = tid & 3, vl = tid >> 2;
@@ -293,16 +324,14 @@ __device__ __forceinline__ void rope_coded(const RopeArgs& a, const RopeArgs::Co
   const uint32_t qrow_addr = qtab_addr | (16u * (uint32_t)(lane & 7));
   const uint32_t sw = ((signw[q >> 1] >> (16 * (q & 1))) & 0xFFFFu) | ((signw[2 + (q >> 1)] >> (16 * (q & 1))) << 16);
   const int64_t n_vec = a.n_tok * H;
-  const int64_t tiles = (n_vec + kVecTile - 1) / kVecTile;
   const bool aligned = ((reinterpret_cast<uintptr_t>(t.in) | (t.in_tok * sizeof(T)) | (t.in_head * sizeof(T))) & 15) == 0;
   const bool out_aligned =
       ((reinterpret_cast<uintptr_t>(t.out) | (t.out_tok * sizeof(T)) | (t.out_head * sizeof(T))) & 15) == 0;
-  for (int64_t tile = block; tile < tiles; tile += t.blocks) {
+  {
     const int64_t v0 = tile * kVecTile;
     const int64_t t0 = v0 / H;  // first token of the tile
-    const int64_t vec_raw = v0 + vl;
-    const bool valid = vec_raw < n_vec;
-    const int64_t vec = valid ? vec_raw : n_vec - 1;
+    const bool valid = v0 + vl < n_vec;
+    const int64_t vec = min(v0 + vl, n_vec - 1);
     const int64_t tok = vec / H;
     const int head = (int)(vec - tok * H);
     const T* src = reinterpret_cast<const T*>(t.in) + tok * t.in_tok + head * t.in_head;
@@ -425,10 +454,14 @@ __global__ void __launch_bounds__(kRThreads) k_rope_apply(const __grid_constant_
   extern __shared__ __align__(16) unsigned char smem_raw[];
   uint64_t* turns = reinterpret_cast<uint64_t*>(smem_raw);
   if (threadIdx.x < kPairs) turns[threadIdx.x] = a.turns[threadIdx.x];
-  rope_rows<T, W>(a, blockIdx.x, gridDim.x, reinterpret_cast<float2*>(smem_raw + kPairs * 8), turns);
+  for (int64_t t = blockIdx.x; t < a.row_tiles; t += gridDim.x)
+    rope_rows<T, W, 1>(a, t, reinterpret_cast<float2*>(smem_raw + kPairs * 8), turns);
 }
 
-// CTAs [0, coded[0].blocks): coded keys; then coded[1].blocks of coded values; then the rows.
+// Tiles of coded keys, of coded values and of rows in one sequence, dealt out to the CTAs in
+// turn: position p is a coded tile where floor(p coded / all) steps, so that a CTA's neighbours
+// are busy with the other kind (codes keep the arithmetic busy, rows the memory), and every CTA
+// gets as many of each.  The cell tables of both tensors stay in shared memory.
 template <typename T, int W>
 __global__ void __launch_bounds__(kRThreads, 3) k_rope_append(const __grid_constant__ RopeArgs a, int cs_tokens) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // a dependent decode may start its prologue
@@ -436,37 +469,49 @@ __global__ void __launch_bounds__(kRThreads, 3) k_rope_append(const __grid_const
   __shared__ uint32_t signw[4];
   uint64_t* turns = reinterpret_cast<uint64_t*>(smem_raw);
   float2* cs = reinterpret_cast<float2*>(smem_raw + kPairs * 8);
-  if (threadIdx.x < kPairs) turns[threadIdx.x] = a.turns[threadIdx.x];
-  unsigned block = blockIdx.x;
-  int which = 0;
-  if (block >= a.coded[0].blocks) {
-    block -= a.coded[0].blocks;
-    which = 1;
-    if (block >= a.coded[1].blocks) {
-      rope_rows<T, W>(a, block - a.coded[1].blocks, a.row_blocks, cs, turns);
-      return;
-    }
-  }
-  const RopeArgs::Coded& t = a.coded[which];
-  // the cell table at the first 16 KB aligned shared address past the cosines
+  const int tid = threadIdx.x;
+  if (tid < kPairs) turns[tid] = a.turns[tid];
+  // the cell tables at the first 16 KB aligned shared address past the cosines
   const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem_raw);
   const uint32_t qtab_addr = (base + kPairs * 8 + (uint32_t)cs_tokens * kPairs * 8 + 16383u) & ~16383u;
-  float4* qtab = reinterpret_cast<float4*>(smem_raw + (qtab_addr - base));
-  const int tid = threadIdx.x;
-  if (tid < 32) {
+  const int64_t coded = a.coded[0].tiles + a.coded[1].tiles, all = coded + a.row_tiles;
+  if (coded > 0) {
+    if (tid < 32) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t m = __ballot_sync(0xffffffffu, __ldg(a.signs + 32 * k + tid) < 0.0f);
-      if (tid == 0) signw[k] = m;
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t m = __ballot_sync(0xffffffffu, __ldg(a.signs + 32 * k + tid) < 0.0f);
+        if (tid == 0) signw[k] = m;
+      }
+    }
+    uint32_t at = qtab_addr;
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+      const RopeArgs::Coded& t = a.coded[which];
+      if (t.tiles == 0) continue;
+      float4* qtab = reinterpret_cast<float4*>(smem_raw + (at - base));
+      if (t.bits == 4) build_cell_table<4>(t.cb, qtab, tid);
+      else if (t.bits == 3) build_cell_table<3>(t.cb, qtab, tid);
+      else build_cell_table<2>(t.cb, qtab, tid);
+      at += (uint32_t)kLutQBytes;
     }
   }
-  if (t.bits == 4) build_cell_table<4>(t.cb, qtab, tid);
-  else if (t.bits == 3) build_cell_table<3>(t.cb, qtab, tid);
-  else build_cell_table<2>(t.cb, qtab, tid);
   __syncthreads();
-  if (t.bits == 4) rope_coded<T, 4>(a, t, block, cs, turns, signw, qtab_addr);
-  else if (t.bits == 3) rope_coded<T, 3>(a, t, block, cs, turns, signw, qtab_addr);
-  else rope_coded<T, 2>(a, t, block, cs, turns, signw, qtab_addr);
+  for (int64_t p = blockIdx.x; p < all; p += gridDim.x) {
+    const int64_t c = p * coded / all;
+    if ((p + 1) * coded / all == c) {
+      rope_rows<T, W, 2>(a, p - c, cs, turns);
+      continue;
+    }
+    // coded tile c: keys and values in turn (their tiles are as many where both are coded)
+    const bool both = a.coded[0].tiles > 0 && a.coded[1].tiles > 0;
+    const int which = both ? (int)(c & 1) : (a.coded[0].tiles > 0 ? 0 : 1);
+    const int64_t tile = both ? c >> 1 : c;
+    const RopeArgs::Coded& t = a.coded[which];
+    const uint32_t tab = qtab_addr + (both && which ? (uint32_t)kLutQBytes : 0u);
+    if (t.bits == 4) rope_coded<T, 4>(a, t, tile, cs, turns, signw, tab);
+    else if (t.bits == 3) rope_coded<T, 3>(a, t, tile, cs, turns, signw, tab);
+    else rope_coded<T, 2>(a, t, tile, cs, turns, signw, tab);
+  }
 }
 
 // ----------------------------------------------------------------- launchers
@@ -525,7 +570,8 @@ static cudaError_t run_apply(const RopeArgs& a, int num_sms, cudaStream_t st) {
   const bool wide = wide_rows(a, (int)sizeof(T));
   auto kern = wide ? k_rope_apply<T, 8> : k_rope_apply<T, 1>;
   const size_t smem = kPairs * 8 + (size_t)a.tile_tok * kPairs * 8;
-  kern<<<a.row_blocks, kRThreads, smem, st>>>(a);
+  const int64_t cap = (int64_t)num_sms * 8;
+  kern<<<(unsigned)(a.row_tiles < cap ? a.row_tiles : cap), kRThreads, smem, st>>>(a);
   count_launch();
   return cudaGetLastError();
 }
@@ -539,9 +585,7 @@ cudaError_t launch_rope_apply(const RopeCall& c, cudaStream_t st) {
       a.heads += c.heads[s]->num_heads;
     }
   a.tile_tok = rows_tile(a, c.num_sms);
-  const int64_t tiles = (a.n_tok + a.tile_tok - 1) / a.tile_tok;
-  const int64_t cap = (int64_t)c.num_sms * 8;
-  a.row_blocks = (unsigned)(tiles < cap ? tiles : cap);
+  a.row_tiles = (a.n_tok + a.tile_tok - 1) / a.tile_tok;
   return c.dtype == TQ_F32 ? run_apply<float>(a, c.num_sms, st) : run_apply<__nv_bfloat16>(a, c.num_sms, st);
 }
 
@@ -549,11 +593,13 @@ template <typename T>
 static cudaError_t run_append(const RopeArgs& a, unsigned grid, cudaStream_t st) {
   const bool wide = wide_rows(a, (int)sizeof(T));
   auto kern = wide ? k_rope_append<T, 8> : k_rope_append<T, 1>;
-  const bool coded = a.coded[0].blocks + a.coded[1].blocks > 0;
+  const int coded = (a.coded[0].tiles > 0) + (a.coded[1].tiles > 0);
   const int tok = (coded && a.coded_tok > a.tile_tok) ? a.coded_tok : a.tile_tok;
-  const size_t smem = kPairs * 8 + (size_t)tok * kPairs * 8 + (coded ? 16384 + kLutQBytes : 0);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
+  const size_t smem = kPairs * 8 + (size_t)tok * kPairs * 8 + (coded ? 16384 + coded * kLutQBytes : 0);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   kern<<<grid, kRThreads, smem, st>>>(a, tok);
   count_launch();
   return cudaGetLastError();
@@ -571,7 +617,6 @@ cudaError_t launch_rope_append(const RopeCall& c, const tq_cache_desc& d, cudaSt
     a.rows[a.n_rows++] = rows_of(*c.heads[0], true);
     a.heads += c.heads[0]->num_heads;
   }
-  int64_t coded_tensors = 0;
   for (int which = 0; which < 2; ++which) {
     const tq_heads* h = c.heads[1 + which];
     if (!h) continue;
@@ -589,8 +634,7 @@ cudaError_t launch_rope_append(const RopeCall& c, const tq_cache_desc& d, cudaSt
       t.bits = which == 0 ? d.fmt.bits_k : d.fmt.bits_v;
       t.rotate = which == 0 ? 1 : 0;
       t.cb = codebook_of(d, which);
-      t.blocks = 1;
-      ++coded_tensors;
+      t.tiles = (c.n_tokens * d.num_kv_heads + kVecTile - 1) / kVecTile;
     } else {
       RopeRows r = rows_of(*h, which == 0);
       if (which == 1) r.out = nullptr;
@@ -601,31 +645,9 @@ cudaError_t launch_rope_append(const RopeCall& c, const tq_cache_desc& d, cudaSt
     }
   }
   a.tile_tok = a.n_rows ? rows_tile(a, c.num_sms) : 1;
-  const int64_t n_vec = c.n_tokens * d.num_kv_heads;
-  const int64_t vec_tiles = (n_vec + kVecTile - 1) / kVecTile;
-  const int64_t row_tiles = a.n_rows ? (c.n_tokens + a.tile_tok - 1) / a.tile_tok : 0;
-  // three CTAs an SM; when there are more tiles than that, the CTAs are shared out by
-  // estimated time: a coded vector about as long as one and a half rows of a query
-  const int64_t cap = (int64_t)c.num_sms * 3;
-  int64_t coded_blocks = vec_tiles, row_blocks = row_tiles;
-  if (coded_tensors * vec_tiles + row_tiles > cap) {
-    const double wc = 1.5 * (double)coded_tensors * d.num_kv_heads, wr = a.heads;
-    const double share = wc / (wc + wr);
-    if (coded_tensors) {
-      coded_blocks = (int64_t)(share * (double)cap / (double)coded_tensors);
-      if (coded_blocks < 1) coded_blocks = 1;
-      if (coded_blocks > vec_tiles) coded_blocks = vec_tiles;
-    }
-    if (a.n_rows) {
-      row_blocks = cap - coded_blocks * coded_tensors;
-      if (row_blocks < 1) row_blocks = 1;
-      if (row_blocks > row_tiles) row_blocks = row_tiles;
-    }
-  }
-  for (int which = 0; which < 2; ++which)
-    if (a.coded[which].blocks) a.coded[which].blocks = (unsigned)coded_blocks;
-  a.row_blocks = (unsigned)row_blocks;
-  const unsigned grid = a.coded[0].blocks + a.coded[1].blocks + a.row_blocks;
+  a.row_tiles = a.n_rows ? (c.n_tokens + a.tile_tok - 1) / a.tile_tok : 0;
+  const int64_t all = a.coded[0].tiles + a.coded[1].tiles + a.row_tiles, cap = (int64_t)c.num_sms * 3;
+  const unsigned grid = (unsigned)(all < cap ? all : cap);
   // tokens a tile of coded vectors can touch
   const int64_t touch = (kVecTile - 1) / d.num_kv_heads + 2;
   a.coded_tok = (int)(touch < kVecTile ? touch : kVecTile);
