@@ -33,6 +33,10 @@ namespace tq {
 
 constexpr int kRThreads = 256;
 constexpr int kPairs = kD / 2;
+// A token's cosines and sines in shared memory: a gap after every 16 pairs, so that lanes 8 or 16
+// pairs apart read different banks.
+constexpr int kCsRow = kPairs + kPairs / 16;
+__host__ __device__ __forceinline__ constexpr int cs_at(int pair) { return pair + (pair >> 4); }
 constexpr int kVecTile = kRThreads / 4;  // coded vectors per tile: four lanes each
 
 // Where rows of one tensor come from and go to.
@@ -198,7 +202,7 @@ __device__ __forceinline__ void item_rotate(RowItem<T, W>& it, const float2* cs,
 #pragma unroll
     for (int k = 0; k < W; ++k) {
       if (it.pair + k < pairs) {
-        const float2 t = cs[it.pair + k];
+        const float2 t = cs[cs_at(it.pair) + k];  // (a gap never lies inside eight pairs)
         float& x0 = k < 4 ? it.a[(2 * k) % W] : it.b[(2 * k) % W];
         float& x1 = k < 4 ? it.a[(2 * k + 1) % W] : it.b[(2 * k + 1) % W];
         turn_pair(x0, x1, t);
@@ -207,7 +211,7 @@ __device__ __forceinline__ void item_rotate(RowItem<T, W>& it, const float2* cs,
   } else {
 #pragma unroll
     for (int k = 0; k < W; ++k) {
-      turn_pair(it.a[k], it.b[k], cs[it.pair + k]);
+      turn_pair(it.a[k], it.b[k], cs[cs_at(it.pair) + k]);
     }
   }
 }
@@ -267,41 +271,43 @@ __device__ __forceinline__ void rope_rows(const RopeArgs& a, int64_t tile, float
     __syncthreads();  // the table of the previous tile is no longer read
     for (int i = tid; i < nt * kPairs; i += kRThreads) {
       const int p = i & (kPairs - 1);
-      if (p < a.pairs) cs[i] = turn_of(turns[p], __ldg(a.positions + t0 + i / kPairs), a.amplitude, a.transpose);
+      if (p < a.pairs)
+        cs[i / kPairs * kCsRow + cs_at(p)] = turn_of(turns[p], __ldg(a.positions + t0 + i / kPairs), a.amplitude, a.transpose);
     }
     __syncthreads();
-    const int items = nt * a.heads * PER;
+    // a thread always has item c of a head; heads of the tile's tokens in steps of the CTA
+    constexpr int STEP = kRThreads / PER;
+    const int c = tid % PER, heads = nt * a.heads;
     const float inv_heads = 1.0f / (float)a.heads;  // (quotients below 2^13 of a few: exact)
-    for (int i0 = tid; i0 < items; i0 += AHEAD * kRThreads) {
+    auto rows_of_head = [&](int& h) -> const RopeRows& {  // the tensor of head h, h its head there
+      int s = 0;
+      while (s + 1 < a.n_rows && h >= a.rows[s].heads) h -= a.rows[s++].heads;
+      return a.rows[s];
+    };
+    for (int th = tid / PER; th < heads; th += AHEAD * STEP) {
       RowItem<T, W> it[AHEAD];
-      int tok[AHEAD], head[AHEAD];
 #pragma unroll
       for (int k = 0; k < AHEAD; ++k) {
-        const int i = i0 + k * kRThreads;
-        if (i >= items) break;
-        const int c = i % PER, th = i / PER;
-        tok[k] = (int)(((float)th + 0.5f) * inv_heads);
-        head[k] = th - tok[k] * a.heads;
-        int h = head[k], s = 0;
-        while (s + 1 < a.n_rows && h >= a.rows[s].heads) h -= a.rows[s++].heads;
-        const RopeRows& r = a.rows[s];
+        if (th + k * STEP >= heads) break;
+        const int tok = (int)(((float)(th + k * STEP) + 0.5f) * inv_heads);
+        int h = th + k * STEP - tok * a.heads;
+        const RopeRows& r = rows_of_head(h);
         item_place<T, W>(it[k], c, r.rotate ? a.pairs : 0, inter);
-        item_load<T, W>(it[k], reinterpret_cast<const T*>(r.in) + (t0 + tok[k]) * r.in_tok + h * r.in_head);
+        item_load<T, W>(it[k], reinterpret_cast<const T*>(r.in) + (t0 + tok) * r.in_tok + h * r.in_head);
       }
 #pragma unroll
       for (int k = 0; k < AHEAD; ++k) {
-        const int i = i0 + k * kRThreads;
-        if (i >= items) break;
-        int h = head[k], s = 0;
-        while (s + 1 < a.n_rows && h >= a.rows[s].heads) h -= a.rows[s++].heads;
-        const RopeRows& r = a.rows[s];
+        if (th + k * STEP >= heads) break;
+        const int tok = (int)(((float)(th + k * STEP) + 0.5f) * inv_heads);
+        int h = th + k * STEP - tok * a.heads;
+        const RopeRows& r = rows_of_head(h);
         item_widen<T, W>(it[k]);
-        item_rotate<T, W>(it[k], cs + tok[k] * kPairs, a.pairs, inter);
-        if (r.out) item_store<T, W>(it[k], reinterpret_cast<T*>(r.out) + (t0 + tok[k]) * r.out_tok + h * r.out_head);
+        item_rotate<T, W>(it[k], cs + tok * kCsRow, a.pairs, inter);
+        if (r.out) item_store<T, W>(it[k], reinterpret_cast<T*>(r.out) + (t0 + tok) * r.out_tok + h * r.out_head);
         if (r.page) {
-          const int64_t slot = __ldg(a.slots + t0 + tok[k]);
+          const int64_t slot = __ldg(a.slots + t0 + tok);
           if (slot >= a.max_slot) {
-            if (i % PER == 0) flag_status(a.status, TQ_DEV_BAD_SLOT);
+            if (c == 0) flag_status(a.status, TQ_DEV_BAD_SLOT);
           } else if (slot >= 0) {
             item_store_page<T, W>(it[k], r.pool, r.page, slot, h, a.kv_heads);
           }
@@ -354,20 +360,21 @@ __device__ __forceinline__ void rope_coded(const RopeArgs& a, const RopeArgs::Co
       const int nt = (int)min((int64_t)a.coded_tok, a.n_tok - t0);
       for (int i = tid; i < nt * kPairs; i += kRThreads) {
         const int p = i & (kPairs - 1);
-        if (p < a.pairs) cs[i] = turn_of(turns[p], __ldg(a.positions + t0 + i / kPairs), a.amplitude, a.transpose);
+        if (p < a.pairs)
+          cs[i / kPairs * kCsRow + cs_at(p)] = turn_of(turns[p], __ldg(a.positions + t0 + i / kPairs), a.amplitude, a.transpose);
       }
       __syncthreads();
-      const float2* ct = cs + (tok - t0) * kPairs;
+      const float2* ct = cs + (tok - t0) * kCsRow;
       if (a.interleaved) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int p = 32 * (i >> 3) + 8 * q + (i & 7);
-          if (p < a.pairs) turn_pair(x[2 * i], x[2 * i + 1], ct[p]);
+          if (p < a.pairs) turn_pair(x[2 * i], x[2 * i + 1], ct[cs_at(p)]);
         }
       } else if (a.pairs == kPairs) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          turn_pair(x[i], x[16 + i], ct[16 * q + i]);
+          turn_pair(x[i], x[16 + i], ct[17 * q + i]);
         }
       } else {  // part of the head: a coordinate's partner may be another lane's; read again (from L1)
         const int rot = 2 * a.pairs;
@@ -376,7 +383,7 @@ __device__ __forceinline__ void rope_coded(const RopeArgs& a, const RopeArgs::Co
           const int j = 64 * (i >> 4) + 16 * q + (i & 15);
           if (j < rot) {
             const bool low = j < a.pairs;
-            const float2 c = ct[low ? j : j - a.pairs];
+            const float2 c = ct[cs_at(low ? j : j - a.pairs)];
             const float o = load_elem<T>(src + (low ? j + a.pairs : j - a.pairs));
             x[i] = __fmaf_rn(x[i], c.x, low ? -__fmul_rn(o, c.y) : __fmul_rn(o, c.y));
           }
@@ -458,10 +465,10 @@ __global__ void __launch_bounds__(kRThreads) k_rope_apply(const __grid_constant_
     rope_rows<T, W, 1>(a, t, reinterpret_cast<float2*>(smem_raw + kPairs * 8), turns);
 }
 
-// Tiles of coded keys, of coded values and of rows in one sequence, dealt out to the CTAs in
-// turn: position p is a coded tile where floor(p coded / all) steps, so that a CTA's neighbours
-// are busy with the other kind (codes keep the arithmetic busy, rows the memory), and every CTA
-// gets as many of each.  The cell tables of both tensors stay in shared memory.
+// Tiles of coded keys, of coded values and of rows: every CTA takes every gridDim-th tile of codes
+// and every gridDim-th of rows (starting where the codes end, for a call with fewer tiles than
+// CTAs), and goes through both in proportion: codes keep the arithmetic busy, rows the memory.
+// The cell tables of both tensors stay in shared memory.
 template <typename T, int W>
 __global__ void __launch_bounds__(kRThreads, 3) k_rope_append(const __grid_constant__ RopeArgs a, int cs_tokens) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // a dependent decode may start its prologue
@@ -473,8 +480,8 @@ __global__ void __launch_bounds__(kRThreads, 3) k_rope_append(const __grid_const
   if (tid < kPairs) turns[tid] = a.turns[tid];
   // the cell tables at the first 16 KB aligned shared address past the cosines
   const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem_raw);
-  const uint32_t qtab_addr = (base + kPairs * 8 + (uint32_t)cs_tokens * kPairs * 8 + 16383u) & ~16383u;
-  const int64_t coded = a.coded[0].tiles + a.coded[1].tiles, all = coded + a.row_tiles;
+  const uint32_t qtab_addr = (base + kPairs * 8 + (uint32_t)cs_tokens * kCsRow * 8 + 16383u) & ~16383u;
+  const int64_t coded = a.coded[0].tiles + a.coded[1].tiles;
   if (coded > 0) {
     if (tid < 32) {
 #pragma unroll
@@ -496,12 +503,23 @@ __global__ void __launch_bounds__(kRThreads, 3) k_rope_append(const __grid_const
     }
   }
   __syncthreads();
-  for (int64_t p = blockIdx.x; p < all; p += gridDim.x) {
-    const int64_t c = p * coded / all;
-    if ((p + 1) * coded / all == c) {
-      rope_rows<T, W, 2>(a, p - c, cs, turns);
+  const int64_t G = gridDim.x;
+  int64_t c_next = blockIdx.x, r_next = (blockIdx.x + G - coded % G) % G;
+  const int64_t nc = c_next < coded ? (coded - 1 - c_next) / G + 1 : 0;
+  const int64_t nr = r_next < a.row_tiles ? (a.row_tiles - 1 - r_next) / G + 1 : 0;
+  // (a CTA starts somewhere else in the mixture than its neighbour)
+  int64_t debt = (nc + nr) * (blockIdx.x & 7) / 8;
+  for (int64_t i = 0; i < nc + nr; ++i) {
+    debt += nc;
+    const bool code = r_next >= a.row_tiles || (debt >= nc + nr && c_next < coded);
+    if (!code) {
+      rope_rows<T, W, 2>(a, r_next, cs, turns);
+      r_next += G;
       continue;
     }
+    debt -= nc + nr;
+    const int64_t c = c_next;
+    c_next += G;
     // coded tile c: keys and values in turn (their tiles are as many where both are coded)
     const bool both = a.coded[0].tiles > 0 && a.coded[1].tiles > 0;
     const int which = both ? (int)(c & 1) : (a.coded[0].tiles > 0 ? 0 : 1);
@@ -569,7 +587,7 @@ template <typename T>
 static cudaError_t run_apply(const RopeArgs& a, int num_sms, cudaStream_t st) {
   const bool wide = wide_rows(a, (int)sizeof(T));
   auto kern = wide ? k_rope_apply<T, 8> : k_rope_apply<T, 1>;
-  const size_t smem = kPairs * 8 + (size_t)a.tile_tok * kPairs * 8;
+  const size_t smem = kPairs * 8 + (size_t)a.tile_tok * kCsRow * 8;
   const int64_t cap = (int64_t)num_sms * 8;
   kern<<<(unsigned)(a.row_tiles < cap ? a.row_tiles : cap), kRThreads, smem, st>>>(a);
   count_launch();
@@ -595,7 +613,7 @@ static cudaError_t run_append(const RopeArgs& a, unsigned grid, cudaStream_t st)
   auto kern = wide ? k_rope_append<T, 8> : k_rope_append<T, 1>;
   const int coded = (a.coded[0].tiles > 0) + (a.coded[1].tiles > 0);
   const int tok = (coded && a.coded_tok > a.tile_tok) ? a.coded_tok : a.tile_tok;
-  const size_t smem = kPairs * 8 + (size_t)tok * kPairs * 8 + (coded ? 16384 + coded * kLutQBytes : 0);
+  const size_t smem = kPairs * 8 + (size_t)tok * kCsRow * 8 + (coded ? 16384 + coded * kLutQBytes : 0);
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
