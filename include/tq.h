@@ -404,7 +404,7 @@ tq_status tq_decode_step(const tq_cache_desc* desc, const void* k_new, const voi
 tq_status tq_rope_apply(const tq_rope* rope, int transpose, const tq_heads* q, const tq_heads* k, int dtype,
                         const int64_t* positions, int64_t n_tokens, void* stream);
 
-/* Append with the rotation applied on the way, in one kernel: the keys of token t
+/* Append with the rotation applied on the way, in one kernel (two for a large call): the keys of token t
  * are rotated to positions[t] in fp32 and stored, with the values, in slot
  * slot_mapping[t] in the layer's format ("Memory layout"; skipped if the slot is
  * negative); the keys are not rounded between the rotation and the quantizer.  q

@@ -25,6 +25,7 @@
 
 #include <cmath>
 
+#include "tq_async.cuh"
 #include "tq_cells.cuh"
 #include "tq_device.cuh"
 #include "tq_internal.h"
@@ -79,7 +80,7 @@ struct RopeArgs {
     int64_t tiles;  // of 64 vectors
     Codebook cb;
   } coded[2];
-  int coded_tok;  // tokens a tile of coded vectors can touch
+  int coded_tok;  // tokens eight coded vectors can touch
   int kv_heads;
   const float* signs;
   int norm_raw;
@@ -265,54 +266,100 @@ __device__ __forceinline__ void rope_rows(const RopeArgs& a, int64_t tile, float
   constexpr int PER = kPairs / W;  // items per head
   const int tid = threadIdx.x;
   const bool inter = a.interleaved != 0;
-  {
-    const int64_t t0 = tile * a.tile_tok;
-    const int nt = (int)min((int64_t)a.tile_tok, a.n_tok - t0);
-    __syncthreads();  // the table of the previous tile is no longer read
-    for (int i = tid; i < nt * kPairs; i += kRThreads) {
-      const int p = i & (kPairs - 1);
-      if (p < a.pairs)
-        cs[i / kPairs * kCsRow + cs_at(p)] = turn_of(turns[p], __ldg(a.positions + t0 + i / kPairs), a.amplitude, a.transpose);
+  const int64_t t0 = tile * a.tile_tok;
+  const int nt = (int)min((int64_t)a.tile_tok, a.n_tok - t0);
+  // a thread always has item c of a head; heads of the tile's tokens in steps of the CTA
+  constexpr int STEP = kRThreads / PER;
+  const int c = tid % PER, heads = nt * a.heads;
+  const float inv_heads = 1.0f / (float)a.heads;  // (quotients below 2^13 of a few: exact)
+  auto rows_of_head = [&](int& h) -> const RopeRows& {  // the tensor of head h, h its head there
+    int s = 0;
+    while (s + 1 < a.n_rows && h >= a.rows[s].heads) h -= a.rows[s++].heads;
+    return a.rows[s];
+  };
+  RowItem<T, W> it[AHEAD];
+  auto request = [&](int th) {
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      if (th + k * STEP >= heads) break;
+      const int tok = (int)(((float)(th + k * STEP) + 0.5f) * inv_heads);
+      int h = th + k * STEP - tok * a.heads;
+      const RopeRows& r = rows_of_head(h);
+      item_place<T, W>(it[k], c, r.rotate ? a.pairs : 0, inter);
+      item_load<T, W>(it[k], reinterpret_cast<const T*>(r.in) + (t0 + tok) * r.in_tok + h * r.in_head);
     }
-    __syncthreads();
-    // a thread always has item c of a head; heads of the tile's tokens in steps of the CTA
-    constexpr int STEP = kRThreads / PER;
-    const int c = tid % PER, heads = nt * a.heads;
-    const float inv_heads = 1.0f / (float)a.heads;  // (quotients below 2^13 of a few: exact)
-    auto rows_of_head = [&](int& h) -> const RopeRows& {  // the tensor of head h, h its head there
-      int s = 0;
-      while (s + 1 < a.n_rows && h >= a.rows[s].heads) h -= a.rows[s++].heads;
-      return a.rows[s];
-    };
-    for (int th = tid / PER; th < heads; th += AHEAD * STEP) {
-      RowItem<T, W> it[AHEAD];
+  };
+  request(tid / PER);  // on their way while the angles are formed
+  __syncthreads();  // the table of the previous tile is no longer read
+  for (int i = tid; i < nt * kPairs; i += kRThreads) {
+    const int p = i & (kPairs - 1);
+    if (p < a.pairs)
+      cs[i / kPairs * kCsRow + cs_at(p)] = turn_of(turns[p], __ldg(a.positions + t0 + i / kPairs), a.amplitude, a.transpose);
+  }
+  __syncthreads();
+  for (int th = tid / PER; th < heads; th += AHEAD * STEP) {
+    if (th != tid / PER) request(th);
 #pragma unroll
-      for (int k = 0; k < AHEAD; ++k) {
-        if (th + k * STEP >= heads) break;
-        const int tok = (int)(((float)(th + k * STEP) + 0.5f) * inv_heads);
-        int h = th + k * STEP - tok * a.heads;
-        const RopeRows& r = rows_of_head(h);
-        item_place<T, W>(it[k], c, r.rotate ? a.pairs : 0, inter);
-        item_load<T, W>(it[k], reinterpret_cast<const T*>(r.in) + (t0 + tok) * r.in_tok + h * r.in_head);
-      }
-#pragma unroll
-      for (int k = 0; k < AHEAD; ++k) {
-        if (th + k * STEP >= heads) break;
-        const int tok = (int)(((float)(th + k * STEP) + 0.5f) * inv_heads);
-        int h = th + k * STEP - tok * a.heads;
-        const RopeRows& r = rows_of_head(h);
-        item_widen<T, W>(it[k]);
-        item_rotate<T, W>(it[k], cs + tok * kCsRow, a.pairs, inter);
-        if (r.out) item_store<T, W>(it[k], reinterpret_cast<T*>(r.out) + (t0 + tok) * r.out_tok + h * r.out_head);
-        if (r.page) {
-          const int64_t slot = __ldg(a.slots + t0 + tok);
-          if (slot >= a.max_slot) {
-            if (c == 0) flag_status(a.status, TQ_DEV_BAD_SLOT);
-          } else if (slot >= 0) {
-            item_store_page<T, W>(it[k], r.pool, r.page, slot, h, a.kv_heads);
-          }
+    for (int k = 0; k < AHEAD; ++k) {
+      if (th + k * STEP >= heads) break;
+      const int tok = (int)(((float)(th + k * STEP) + 0.5f) * inv_heads);
+      int h = th + k * STEP - tok * a.heads;
+      const RopeRows& r = rows_of_head(h);
+      item_widen<T, W>(it[k]);
+      item_rotate<T, W>(it[k], cs + tok * kCsRow, a.pairs, inter);
+      if (r.out) item_store<T, W>(it[k], reinterpret_cast<T*>(r.out) + (t0 + tok) * r.out_tok + h * r.out_head);
+      if (r.page) {
+        const int64_t slot = __ldg(a.slots + t0 + tok);
+        if (slot >= a.max_slot) {
+          if (c == 0) flag_status(a.status, TQ_DEV_BAD_SLOT);
+        } else if (slot >= 0) {
+          item_store_page<T, W>(it[k], r.pool, r.page, slot, h, a.kv_heads);
         }
       }
+    }
+  }
+}
+
+// v / h; a 64-bit division is long, and few calls need it.
+__device__ __forceinline__ int64_t over(int64_t v, int h) {
+  return v < (1ll << 32) ? (int64_t)((uint32_t)v / (uint32_t)h) : v / h;
+}
+
+// What a lane needs of its vector of the next coded tile, requested while the CTA is still at
+// the tile before: its quarter of the vector as loaded, its token's slot and position.
+template <typename T>
+struct CodedNext {
+  static constexpr int kLoads = (int)sizeof(T) * 2;
+  uint4 raw[kLoads];
+  int64_t tok, slot, pos;
+  int head;
+};
+template <typename T>
+__device__ __forceinline__ void request_coded(CodedNext<T>& r, const RopeArgs& a, const RopeArgs::Coded& t, int64_t tile) {
+  const int64_t vec = min(tile * kVecTile + (threadIdx.x >> 2), a.n_tok * a.kv_heads - 1);
+  r.tok = over(vec, a.kv_heads);
+  r.head = (int)(vec - r.tok * a.kv_heads);
+  r.slot = __ldg(a.slots + r.tok);
+  if (t.rotate) r.pos = __ldg(a.positions + r.tok);
+  const T* src = reinterpret_cast<const T*>(t.in) + r.tok * t.in_tok + r.head * t.in_head + 16 * (threadIdx.x & 3);
+  if (((reinterpret_cast<uintptr_t>(t.in) | (t.in_tok * sizeof(T)) | (t.in_head * sizeof(T))) & 15) == 0) {
+#pragma unroll
+    for (int k = 0; k < CodedNext<T>::kLoads; ++k)
+      r.raw[k] = reinterpret_cast<const uint4*>(src + 64 * (2 * k / CodedNext<T>::kLoads))[k % (CodedNext<T>::kLoads / 2)];
+  } else {
+#pragma unroll
+    for (int k = 0; k < CodedNext<T>::kLoads; ++k) {
+      constexpr int N = 16 / (int)sizeof(T);  // elements of a load
+      const T* e = src + 64 * (2 * k / CodedNext<T>::kLoads) + N * (k % (CodedNext<T>::kLoads / 2));
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 2)
+          w[i] = (uint32_t)reinterpret_cast<const uint16_t*>(e)[2 * i] | ((uint32_t)reinterpret_cast<const uint16_t*>(e)[2 * i + 1] << 16);
+        else
+          w[i] = reinterpret_cast<const uint32_t*>(e)[i];
+      }
+      r.raw[k] = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
@@ -322,7 +369,8 @@ __device__ __forceinline__ void rope_rows(const RopeArgs& a, int64_t tile, float
 // one lane, and the butterfly over them is the quad transform with the coordinate's bits
 // 0..3 and 6 inside the lane and bits 4 and 5 across lanes.
 template <typename T, int BITS>
-__device__ __forceinline__ void rope_coded(const RopeArgs& a, const RopeArgs::Coded& t, int64_t tile, float2* cs,
+__device__ __forceinline__ void rope_coded(const RopeArgs& a, const RopeArgs::Coded& t, int64_t tile,
+                                           const CodedNext<T>& in, float2* cs,
                                            const uint64_t* turns, const uint32_t* signw, uint32_t qtab_addr) {
   constexpr int R = 16 * BITS;
   const int tid = threadIdx.x, lane = tid & 31, q = tid & 3, vl = tid >> 2;
@@ -330,40 +378,45 @@ __device__ __forceinline__ void rope_coded(const RopeArgs& a, const RopeArgs::Co
   const uint32_t qrow_addr = qtab_addr | (16u * (uint32_t)(lane & 7));
   const uint32_t sw = ((signw[q >> 1] >> (16 * (q & 1))) & 0xFFFFu) | ((signw[2 + (q >> 1)] >> (16 * (q & 1))) << 16);
   const int64_t n_vec = a.n_tok * H;
-  const bool aligned = ((reinterpret_cast<uintptr_t>(t.in) | (t.in_tok * sizeof(T)) | (t.in_head * sizeof(T))) & 15) == 0;
   const bool out_aligned =
       ((reinterpret_cast<uintptr_t>(t.out) | (t.out_tok * sizeof(T)) | (t.out_head * sizeof(T))) & 15) == 0;
   {
     const int64_t v0 = tile * kVecTile;
-    const int64_t t0 = v0 / H;  // first token of the tile
     const bool valid = v0 + vl < n_vec;
-    const int64_t vec = min(v0 + vl, n_vec - 1);
-    const int64_t tok = vec / H;
-    const int head = (int)(vec - tok * H);
+    const int64_t tok = in.tok, slot = in.slot;
+    const int head = in.head;
     const T* src = reinterpret_cast<const T*>(t.in) + tok * t.in_tok + head * t.in_head;
     float x[32];
-    if (aligned) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        float v[8];
-        load8<T>(src + 64 * (r >> 1) + 16 * q + 8 * (r & 1), v);
+    for (int r = 0; r < CodedNext<T>::kLoads; ++r) {
+      const uint32_t w[4] = {in.raw[r].x, in.raw[r].y, in.raw[r].z, in.raw[r].w};
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[8 * r + k] = v[k];
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (sizeof(T) == 2) {
+          x[8 * r + 2 * k] = __uint_as_float(w[k] << 16);
+          x[8 * r + 2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+        } else {
+          x[4 * r + k] = __uint_as_float(w[k]);
+        }
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] = load_elem<T>(src + 64 * (i >> 4) + 16 * q + (i & 15));
     }
-    const int64_t slot = __ldg(a.slots + tok);
     if (t.rotate) {
-      __syncthreads();  // the table of the previous tile is no longer read
-      const int nt = (int)min((int64_t)a.coded_tok, a.n_tok - t0);
-      for (int i = tid; i < nt * kPairs; i += kRThreads) {
-        const int p = i & (kPairs - 1);
-        if (p < a.pairs)
-          cs[i / kPairs * kCsRow + cs_at(p)] = turn_of(turns[p], __ldg(a.positions + t0 + i / kPairs), a.amplitude, a.transpose);
+      // the warp's eight vectors touch a.coded_tok tokens at most; its cosines are its own (past the
+      // last vector, lanes repeat it: tokens do not decrease)
+      const int64_t t0 = __shfl_sync(0xffffffffu, tok, 0);
+      const int nt = (int)(__shfl_sync(0xffffffffu, tok, 31) - t0) + 1;
+      __syncwarp();  // (those of the warp's last tile are no longer read)
+      for (int k = 0; k < nt; ++k) {
+        // the position of token t0 + k from the first of the warp's vectors that has it
+        const int64_t first = (t0 + k) * H - (v0 + (vl & ~7));
+        const int64_t pos = __shfl_sync(0xffffffffu, in.pos, first > 0 ? 4 * (int)first : 0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int p = lane + 32 * h;
+          if (p < a.pairs) cs[k * kCsRow + cs_at(p)] = turn_of(turns[p], pos, a.amplitude, a.transpose);
+        }
       }
-      __syncthreads();
+      __syncwarp();
       const float2* ct = cs + (tok - t0) * kCsRow;
       if (a.interleaved) {
 #pragma unroll
@@ -417,17 +470,32 @@ __device__ __forceinline__ void rope_coded(const RopeArgs& a, const RopeArgs::Co
     for (int i = 0; i < 32; ++i) x[i] = flip_sign(x[i], sw, i);
     fwht128_quad_f2(x, q);  // H D x = sqrt(d) Pi x
     const float inv_n = n > 0.0f ? 0.08838834764831845f / n : 0.0f;  // 1 / sqrt(128) folded in
-    uint32_t code[32];
+    uint32_t w[BITS] = {};  // the low half: codes of the first run, the high half: of the second
     float2 c2v = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      const float2 y = __fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(inv_n, inv_n));
-      const float4 e0 = lds128f((qcell_bits(y.x) & kQRowMask) | qrow_addr);
-      const float4 e1 = lds128f((qcell_bits(y.y) & kQRowMask) | qrow_addr);
-      const bool up0 = y.x >= e0.x, up1 = y.y >= e1.x;
-      code[i] = __float_as_uint(e0.w) + (up0 ? 1u : 0u);
-      code[i + 1] = __float_as_uint(e1.w) + (up1 ? 1u : 0u);
-      c2v = __fadd2_rn(c2v, make_float2(up0 ? e0.z : e0.y, up1 ? e1.z : e1.y));
+    for (int g = 0; g < 4; ++g) {  // eight codes at a time
+      uint32_t code[8];
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const float2 y = __fmul2_rn(make_float2(x[8 * g + i], x[8 * g + i + 1]), make_float2(inv_n, inv_n));
+        const float4 e0 = lds128f((qcell_bits(y.x) & kQRowMask) | qrow_addr);
+        const float4 e1 = lds128f((qcell_bits(y.y) & kQRowMask) | qrow_addr);
+        const bool up0 = y.x >= e0.x, up1 = y.y >= e1.x;
+        code[i] = __float_as_uint(e0.w) + (up0 ? 1u : 0u);
+        code[i + 1] = __float_as_uint(e1.w) + (up1 ? 1u : 0u);
+        c2v = __fadd2_rn(c2v, make_float2(up0 ? e0.z : e0.y, up1 ? e1.z : e1.y));
+      }
+      uint32_t by[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) by[k] = code[2 * k] + (code[2 * k + 1] << BITS);
+      if constexpr (BITS == 4) {
+        w[g] = __byte_perm(__byte_perm(by[0], by[1], 0x0040u), __byte_perm(by[2], by[3], 0x0040u), 0x5410u);
+      } else {
+        const uint32_t v = (by[0] + (by[1] << 2 * BITS)) + ((by[2] + (by[3] << 2 * BITS)) << 4 * BITS);
+        const int bit = 8 * BITS * g;
+        w[bit >> 5] |= v << (bit & 31);
+        if ((bit & 31) + 8 * BITS > 32) w[(bit >> 5) + 1] |= v >> (32 - (bit & 31));
+      }
     }
     const float c2 = quad_sum(c2v.x + c2v.y);
     const float gamma = a.norm_raw ? n : ((n > 0.0f && c2 > 0.0f) ? n / sqrtf(c2) : 0.0f);
@@ -436,8 +504,6 @@ __device__ __forceinline__ void rope_coded(const RopeArgs& a, const RopeArgs::Co
     } else if (valid && slot >= 0) {
       uint8_t* page = t.pool + ((slot >> 4) * H + head) * (int64_t)t.page_bytes;
       const int off = (int)(slot & 15);
-      uint32_t w[BITS];
-      pack32<BITS>(code, w);  // the low half: codes of the first run, the high half: of the second
       uint8_t* rec = page + off * R + 2 * BITS * q;
       if constexpr (BITS == 4) {
         *reinterpret_cast<uint2*>(rec) = make_uint2(w[0], w[1]);
@@ -458,6 +524,7 @@ __device__ __forceinline__ void rope_coded(const RopeArgs& a, const RopeArgs::Co
 
 template <typename T, int W>
 __global__ void __launch_bounds__(kRThreads) k_rope_apply(const __grid_constant__ RopeArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (a large append's codes follow its rows)
   extern __shared__ __align__(16) unsigned char smem_raw[];
   uint64_t* turns = reinterpret_cast<uint64_t*>(smem_raw);
   if (threadIdx.x < kPairs) turns[threadIdx.x] = a.turns[threadIdx.x];
@@ -470,7 +537,7 @@ __global__ void __launch_bounds__(kRThreads) k_rope_apply(const __grid_constant_
 // CTAs), and goes through both in proportion: codes keep the arithmetic busy, rows the memory.
 // The cell tables of both tensors stay in shared memory.
 template <typename T, int W>
-__global__ void __launch_bounds__(kRThreads, 3) k_rope_append(const __grid_constant__ RopeArgs a, int cs_tokens) {
+__global__ void __launch_bounds__(kRThreads, 2) k_rope_append(const __grid_constant__ RopeArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // a dependent decode may start its prologue
   extern __shared__ __align__(16) unsigned char smem_raw[];
   __shared__ uint32_t signw[4];
@@ -480,7 +547,10 @@ __global__ void __launch_bounds__(kRThreads, 3) k_rope_append(const __grid_const
   if (tid < kPairs) turns[tid] = a.turns[tid];
   // the cell tables at the first 16 KB aligned shared address past the cosines
   const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem_raw);
-  const uint32_t qtab_addr = (base + kPairs * 8 + (uint32_t)cs_tokens * kCsRow * 8 + 16383u) & ~16383u;
+  // cosines of the rows' tile, then of each warp's coded vectors
+  float2* const cs_warp = cs + (a.tile_tok + (tid >> 5) * a.coded_tok) * kCsRow;
+  const uint32_t qtab_addr =
+      (base + kPairs * 8 + (uint32_t)(a.tile_tok + kRThreads / 32 * a.coded_tok) * kCsRow * 8 + 16383u) & ~16383u;
   const int64_t coded = a.coded[0].tiles + a.coded[1].tiles;
   if (coded > 0) {
     if (tid < 32) {
@@ -509,6 +579,13 @@ __global__ void __launch_bounds__(kRThreads, 3) k_rope_append(const __grid_const
   const int64_t nr = r_next < a.row_tiles ? (a.row_tiles - 1 - r_next) / G + 1 : 0;
   // (a CTA starts somewhere else in the mixture than its neighbour)
   int64_t debt = (nc + nr) * (blockIdx.x & 7) / 8;
+  CodedNext<T> next;
+  auto ask = [&]() {
+    if (c_next >= coded) return;
+    const int which = c_next >= a.coded[0].tiles ? 1 : 0;
+    request_coded<T>(next, a, a.coded[which], c_next - (which ? a.coded[0].tiles : 0));
+  };
+  ask();
   for (int64_t i = 0; i < nc + nr; ++i) {
     debt += nc;
     const bool code = r_next >= a.row_tiles || (debt >= nc + nr && c_next < coded);
@@ -518,18 +595,18 @@ __global__ void __launch_bounds__(kRThreads, 3) k_rope_append(const __grid_const
       continue;
     }
     debt -= nc + nr;
-    const int64_t c = c_next;
+    const int which = c_next >= a.coded[0].tiles ? 1 : 0;
+    const int64_t tile = c_next - (which ? a.coded[0].tiles : 0);
+    const CodedNext<T> in = next;
     c_next += G;
-    // coded tile c: keys and values in turn (their tiles are as many where both are coded)
-    const bool both = a.coded[0].tiles > 0 && a.coded[1].tiles > 0;
-    const int which = both ? (int)(c & 1) : (a.coded[0].tiles > 0 ? 0 : 1);
-    const int64_t tile = both ? c >> 1 : c;
+    ask();
     const RopeArgs::Coded& t = a.coded[which];
-    const uint32_t tab = qtab_addr + (both && which ? (uint32_t)kLutQBytes : 0u);
-    if (t.bits == 4) rope_coded<T, 4>(a, t, tile, cs, turns, signw, tab);
-    else if (t.bits == 3) rope_coded<T, 3>(a, t, tile, cs, turns, signw, tab);
-    else rope_coded<T, 2>(a, t, tile, cs, turns, signw, tab);
+    const uint32_t tab = qtab_addr + (which && a.coded[0].tiles > 0 ? (uint32_t)kLutQBytes : 0u);
+    if (t.bits == 4) rope_coded<T, 4>(a, t, tile, in, cs_warp, turns, signw, tab);
+    else if (t.bits == 3) rope_coded<T, 3>(a, t, tile, in, cs_warp, turns, signw, tab);
+    else rope_coded<T, 2>(a, t, tile, in, cs_warp, turns, signw, tab);
   }
+  grid_dep_wait();  // (after the rows of a large append: complete only when they are)
 }
 
 // ----------------------------------------------------------------- launchers
@@ -575,11 +652,12 @@ static void fill_common(RopeArgs& a, const RopeCall& c) {
   a.status = c.status;
 }
 
-// Tokens a tile of the rows part: enough items for the CTA's threads to have four each,
-// one token while the tiles would not fill the GPU.
+// Tokens a tile of the rows part: enough items for the CTA's threads to have sixteen each,
+// so that forming the angles and the two barriers weigh little; fewer while the tiles would
+// not fill the GPU.
 static int rows_tile(const RopeArgs& a, int num_sms) {
   int t = 1;
-  while (t < 8 && t * a.heads * (kPairs / 8) < 4 * kRThreads && a.n_tok / (2 * t) >= 8 * (int64_t)num_sms) t *= 2;
+  while (t < 8 && t * a.heads * (kPairs / 8) < 16 * kRThreads && a.n_tok / (2 * t) >= 8 * (int64_t)num_sms) t *= 2;
   return t;
 }
 
@@ -608,19 +686,29 @@ cudaError_t launch_rope_apply(const RopeCall& c, cudaStream_t st) {
 }
 
 template <typename T>
-static cudaError_t run_append(const RopeArgs& a, unsigned grid, cudaStream_t st) {
+static cudaError_t run_append(const RopeArgs& a, unsigned grid, bool pdl, cudaStream_t st) {
   const bool wide = wide_rows(a, (int)sizeof(T));
   auto kern = wide ? k_rope_append<T, 8> : k_rope_append<T, 1>;
   const int coded = (a.coded[0].tiles > 0) + (a.coded[1].tiles > 0);
-  const int tok = (coded && a.coded_tok > a.tile_tok) ? a.coded_tok : a.tile_tok;
-  const size_t smem = kPairs * 8 + (size_t)tok * kCsRow * 8 + (coded ? 16384 + coded * kLutQBytes : 0);
+  const size_t tok = (size_t)a.tile_tok + (coded ? kRThreads / 32 * (size_t)a.coded_tok : 0);
+  const size_t smem = kPairs * 8 + tok * kCsRow * 8 + (coded ? 16384 + coded * kLutQBytes : 0);
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  kern<<<grid, kRThreads, smem, st>>>(a, tok);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kRThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
   count_launch();
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_rope_append(const RopeCall& c, const tq_cache_desc& d, cudaStream_t st) {
@@ -664,12 +752,23 @@ cudaError_t launch_rope_append(const RopeCall& c, const tq_cache_desc& d, cudaSt
   }
   a.tile_tok = a.n_rows ? rows_tile(a, c.num_sms) : 1;
   a.row_tiles = a.n_rows ? (c.n_tokens + a.tile_tok - 1) / a.tile_tok : 0;
-  const int64_t all = a.coded[0].tiles + a.coded[1].tiles + a.row_tiles, cap = (int64_t)c.num_sms * 3;
+  const int touch = 7 / d.num_kv_heads + 2;
+  a.coded_tok = touch < 8 ? touch : 8;
+  // Many rows beside codes: the rows go first in a kernel of their own, at eight CTAs an SM
+  // instead of the two that the quantizer's registers leave (65,536 tokens, 64 query and 8 KV
+  // heads: 341 + 200 us apart, 588 us together; 11,000 tokens, 32 heads: 41 + 37 apart, 77
+  // together).
+  const int64_t coded = a.coded[0].tiles + a.coded[1].tiles;
+  bool apart = false;
+  if (coded > 0 && a.row_tiles > 0 && c.n_tokens * a.heads >= (1 << 20)) {
+    const cudaError_t e = c.dtype == TQ_F32 ? run_apply<float>(a, c.num_sms, st) : run_apply<__nv_bfloat16>(a, c.num_sms, st);
+    if (e != cudaSuccess) return e;
+    a.row_tiles = 0;
+    apart = true;
+  }
+  const int64_t all = coded + a.row_tiles, cap = (int64_t)c.num_sms * 2;
   const unsigned grid = (unsigned)(all < cap ? all : cap);
-  // tokens a tile of coded vectors can touch
-  const int64_t touch = (kVecTile - 1) / d.num_kv_heads + 2;
-  a.coded_tok = (int)(touch < kVecTile ? touch : kVecTile);
-  return c.dtype == TQ_F32 ? run_append<float>(a, grid, st) : run_append<__nv_bfloat16>(a, grid, st);
+  return c.dtype == TQ_F32 ? run_append<float>(a, grid, apart, st) : run_append<__nv_bfloat16>(a, grid, apart, st);
 }
 
 }  // namespace tq
