@@ -8,7 +8,7 @@
 // 128 rows would be empty but for 4 to 8 of them --
 //     S [rows x 8 tokens] = Q' K^T: rows 0..7 the heads' high parts, rows 8..15 their low
 //                           parts, whose results are added;
-//     O [rows x 128]     += P V: P's high and low parts in the same places.
+//     O^T [128 x rows]   += V^T P^T, once for P's high parts and once for its low ones.
 // A logit's lane is the lane that P needs it in.  What bounds it is the latency of a warp's few
 // blocks, so small CTAs, several an SM, take the place of one large one: own contexts of 0 to
 // 256 tokens of 128 sequences (32/8 heads, bf16) took the decode kernel 33 us.
@@ -102,7 +102,7 @@ __device__ __forceinline__ void load_run(Run<F, N>& r, const uint8_t* page, int 
 }
 
 template <int KF, int VF>
-__global__ void __launch_bounds__(kOwnWarps * 32, 3) k_own(const __grid_constant__ OwnArgs a) {
+__global__ void __launch_bounds__(kOwnWarps * 32, KF == 0 ? 3 : 4) k_own(const __grid_constant__ OwnArgs a) {
   constexpr bool kCodedK = KF >= 2 && KF <= 4, kCodedV = VF != 0;
   constexpr int kpage = KF == 0 ? kBlock * kD * 2 : (KF == 8 ? kBlock * kD : kBlock * (kD * KF / 8 + 4));
   constexpr int vpage = VF == 0 ? kBlock * kD * 2 : kBlock * (kD * VF / 8 + 4);
@@ -227,9 +227,11 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 3) k_own(const __grid_constant
   if constexpr (kCodedV) tv = half_table<(kCodedV ? VF : 4)>(a.cbv);
 
   float C = -INFINITY, l = 0.0f;  // reference of log2 weight plus the norms' exponent; sum of 2^(u - C + shift)
-  float acc[16][4];
+  // tile i holds rows 2 tig and 2 tig + 1 of coordinates 16 g_ + 2 i and 16 g_ + 2 i + 1 (bf16 pieces:
+  // 8 g_ + 2 i for i < 4, 64 + 8 g_ + 2 i - 8 from there)
+  float acc[8][4];
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
+  for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int k = 0; k < 4; ++k) acc[i][k] = 0.0f;
 
@@ -299,14 +301,18 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 3) k_own(const __grid_constant
     if (__any_sync(0xffffffffu, nc > C)) {
       const float f = C == -INFINITY ? 0.0f : ex2(C - nc);
       l *= f;
+      const float f0 = __shfl_sync(0xffffffffu, f, 8 * tig), f1 = __shfl_sync(0xffffffffu, f, 8 * tig + 4);
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) acc[i][k] *= f;
+      for (int i = 0; i < 8; ++i) {
+        acc[i][0] *= f0;
+        acc[i][1] *= f1;
+        acc[i][2] *= f0;
+        acc[i][3] *= f1;
+      }
       C = nc;
     }
     const float off = (C == -INFINITY ? 0.0f : C) - kOwnShift;
-    uint32_t pf[4];  // high parts of rows g_, low parts in the places of rows g_ + 8
+    uint32_t ph[2], pl[2];  // high and low parts of row g_ at tokens 2 tig, 2 tig + 1 (and 8 further)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float2 p = make_float2(ex2(u[h].x - off), ex2(u[h].y - off));
@@ -314,16 +320,15 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 3) k_own(const __grid_constant
       p.x *= gv[h].x;
       p.y *= gv[h].y;
       if constexpr (VF == 0) {
-        pf[2 * h] = pack_b2(p.x, p.y);
-        pf[2 * h + 1] = pack_b2(p.x - __uint_as_float(pf[2 * h] << 16), p.y - __uint_as_float(pf[2 * h] & 0xFFFF0000u));
+        ph[h] = pack_b2(p.x, p.y);
+        pl[h] = pack_b2(p.x - __uint_as_float(ph[h] << 16), p.y - __uint_as_float(ph[h] & 0xFFFF0000u));
       } else {
-        pf[2 * h] = pack_h2(p.x, p.y);
-        const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&pf[2 * h]));
-        pf[2 * h + 1] = pack_h2(p.x - r.x, p.y - r.y);
+        ph[h] = pack_h2(p.x, p.y);
+        const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&ph[h]));
+        pl[h] = pack_h2(p.x - r.x, p.y - r.y);
       }
     }
-    // ---- values: tile i holds coordinates 16 n + i, n = 0..7, so a lane's result is 32 in a row
-    // (bf16 pieces: 8 n + i for i < 8 and 64 + 8 n + i - 8 from there, two runs of 16)
+    // ---- values
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const uint4 x0 = chunk_of<VF>(v0[0], c, tv), x1 = chunk_of<VF>(v1[0], c, tv);
@@ -332,8 +337,10 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 3) k_own(const __grid_constant
       const uint32_t c0[4] = {y0.x, y0.y, y0.z, y0.w}, c1[4] = {y1.x, y1.y, y1.z, y1.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        mma_16n8k16<VF == 0>(acc[8 * c + 2 * k], pf, prmt(a0[k], a1[k], 0x5410u), prmt(c0[k], c1[k], 0x5410u));
-        mma_16n8k16<VF == 0>(acc[8 * c + 2 * k + 1], pf, prmt(a0[k], a1[k], 0x7632u), prmt(c0[k], c1[k], 0x7632u));
+        const uint32_t v[4] = {prmt(a0[k], a1[k], 0x5410u), prmt(a0[k], a1[k], 0x7632u), prmt(c0[k], c1[k], 0x5410u),
+                               prmt(c0[k], c1[k], 0x7632u)};
+        mma_16n8k16<VF == 0>(acc[4 * c + k], v, ph[0], ph[1]);
+        mma_16n8k16<VF == 0>(acc[4 * c + k], v, pl[0], pl[1]);
       }
     }
   }
@@ -342,10 +349,9 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 3) k_own(const __grid_constant
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<float4*>(&red[warp][g_][VF == 0 ? 64 * (i >> 1) + 16 * tig + 8 * h + 4 * (i & 1) : 32 * tig + 16 * h + 4 * i]) =
-          make_float4(acc[4 * i][h] + acc[4 * i][2 + h], acc[4 * i + 1][h] + acc[4 * i + 1][2 + h],
-                      acc[4 * i + 2][h] + acc[4 * i + 2][2 + h], acc[4 * i + 3][h] + acc[4 * i + 3][2 + h]);
+    for (int i = 0; i < 4; ++i)  // (a row's 16 coordinates, four at a time)
+      *reinterpret_cast<float4*>(&red[warp][2 * tig + h][VF == 0 ? 64 * (i >> 1) + 8 * g_ + 4 * (i & 1) : 16 * g_ + 4 * i]) =
+          make_float4(acc[2 * i][h], acc[2 * i][2 + h], acc[2 * i + 1][h], acc[2 * i + 1][2 + h]);
   if (tig == 0) {
     redc[warp][g_] = C;
     redl[warp][g_] = l;
