@@ -76,6 +76,16 @@ __device__ __forceinline__ void tensor_copy_2d(uint32_t dst, const CUtensorMap* 
       : "memory");
 }
 
+// The 3-D form: one box at element coordinates (c0 inner, c1, c2 outer).
+__device__ __forceinline__ void tensor_copy_3d(uint32_t dst, const CUtensorMap* tmap, int c0, int c1, int c2,
+                                               uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+          "r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // Orders this thread's earlier shared-memory accesses (and those it has seen
 // through a warp or CTA barrier) before its later asynchronous-proxy copies.
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }

@@ -13,7 +13,7 @@
 // k_prefix: one CTA per SM, two "streams" of 128 rows x 128 tokens through the
 // fifth-generation tensor cores.
 //   8 producer warps  turn 8 blocks (128 tokens) of K and V pages into 16-bit operands in
-//                     shared memory: bf16 keys as they are, codes as fp16 centroids by
+//                     shared memory (bf16 keys come by tensor copies of a copy warp): codes as fp16 centroids by
 //                     byte permutes from tables in registers (a centroid table is
 //                     antisymmetric: magnitude lookup, then the sign bit), FP8 keys as
 //                     fp16.  Key norms stay fp32 and scale the logits; value norms go into
@@ -54,11 +54,15 @@ namespace tq {
 
 Codebook codebook_of(const tq_cache_desc& d, int which);
 UnitMap unit_map(const tq_cache_desc& d, int num_q_heads);
+bool bf16_page_map(CUtensorMap* m, const void* pool, int64_t pages);
 
 constexpr int kPTile = 128;            // tokens a tile, rows a stream
 constexpr int kPBlocks = kPTile / kBlock;
 constexpr int kPSoftWarps = 8, kPProdWarps = 8;
-constexpr int kPThreads = (kPSoftWarps + kPProdWarps + 1) * 32;
+constexpr int kPMmaWarp = kPSoftWarps + kPProdWarps, kPCopyWarp = kPMmaWarp + 1;
+// (bf16 keys have a copy warp; the register file holds 20 warps' worth either way)
+template <int KF>
+constexpr int kPThreads = (kPMmaWarp + (KF == 0 ? 2 : 1)) * 32;
 constexpr uint32_t kPPanel = kPTile * 128;       // 128 rows of 64 16-bit elements, swizzled
 constexpr uint32_t kPOperand = 2 * kPPanel;      // a 128 x 128 operand
 constexpr int kPNormSlots = 4;                   // tiles whose norms and masks are kept
@@ -83,6 +87,7 @@ constexpr uint32_t kPSmem = kPOffTmem + 8;
 static_assert(kPSmem <= 232448, "the shared memory of one CTA an SM");
 
 struct PrefixArgs {
+  CUtensorMap kmap;  // the pool of keys of a bf16 layer
   const uint8_t* kpool;
   const uint8_t* vpool;
   int64_t num_blocks;
@@ -334,7 +339,7 @@ __device__ __forceinline__ bool elect_one() {
 // --------------------------------------------------------------- the kernel
 
 template <int KF, int VF>
-__global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__ PrefixArgs a) {
+__global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_constant__ PrefixArgs a) {
   constexpr bool kCodedK = KF >= 2 && KF <= 4, kCodedV = VF != 0;
   constexpr int kpage = KF == 0 ? kBlock * kD * 2 : (KF == 8 ? kBlock * kD : kBlock * (kD * KF / 8 + 4));
   constexpr int vpage = VF == 0 ? kBlock * kD * 2 : kBlock * (kD * VF / 8 + 4);
@@ -376,7 +381,7 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(kfull + i, kPProdWarps);
+      mbar_init(kfull + i, KF == 0 ? 1 : kPProdWarps);
       mbar_init(kempty + i, 1);
       mbar_init(vfull + i, kPProdWarps);
       mbar_init(vempty + i, 1);
@@ -384,7 +389,10 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
       mbar_init(pfull + i, 4);
       mbar_init(odone + i, 1);
     }
-    for (int i = 0; i < 2 * kPNormSlots; ++i) mbar_init(gfull + i, kPProdWarps);
+    for (int i = 0; i < kPNormSlots; ++i) {
+      mbar_init(gfull + i, KF == 0 ? 1 : kPProdWarps);
+      mbar_init(efull + i, kPProdWarps);
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     *qmax = 0u;
   }
@@ -393,13 +401,12 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
   float qscale = 1.0f;
   {
     constexpr int kSpare = KF >= 2 && KF <= 4 ? 4 : 0;
-    const bool mma_warp = warp == kPSoftWarps + kPProdWarps;
+    const bool stages = warp < kPMmaWarp;
     QRows<true> q16;
     QRows<false> q32;
     uint32_t signs = 0u;
-    if (mma_warp) {
-      tmem_alloc(base + kPOffTmem, 512);
-    } else {
+    if (warp == kPMmaWarp) tmem_alloc(base + kPOffTmem, 512);
+    if (stages) {
       if (KF >= 2 && KF <= 4) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -415,7 +422,7 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
     for (int t = 0; t < 2; ++t) {
       if (early[t] < 0 || early[t] >= a.num_blocks) continue;
       const int64_t page = (int64_t)early[t] * a.Hkv + kvh;
-      if (128 * lane < kpage) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.kpool + page * kpage + 128 * lane));
+      if (KF != 0 && 128 * lane < kpage) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.kpool + page * kpage + 128 * lane));
       if (128 * lane < vpage) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.vpool + page * vpage + 128 * lane));
     }
     __syncthreads();
@@ -423,7 +430,7 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
     qscale = __uint_as_float((uint32_t)(127 + qe) << 23);
     // (a negative sm_scale turns the queries, so that every g is positive)
     const float inv = (a.scale < 0.0f ? -1.0f : 1.0f) * __uint_as_float((uint32_t)(127 - qe) << 23);
-    if (!mma_warp) {
+    if (stages) {
       if (a.q_bf16) place_q<KF, true>(q16, a, r0, base, inv, signs, warp, lane);
       else place_q<KF, false>(q32, a, r0, base, inv, signs, warp, lane);
     }
@@ -598,7 +605,7 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
         }
       }
     }
-  } else if (warp < kPSoftWarps + kPProdWarps) {
+  } else if (warp < kPMmaWarp) {
     // ------------------------------------------------------------ producers
     const int w = warp - kPSoftWarps, tok = lane >> 1, half = lane & 1;
     HalfTable tk = {}, tv = {};
@@ -616,6 +623,7 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
     HalfRecord<VF> rv;
     // (a block without tokens reads as zeros: no page is touched)
     auto fetch_k = [&](int t, int id) {
+      if (KF == 0) return;
       const int live = tokens(t, id);
       if (live > 0) load_half<KF>(rk, a.kpool + ((int64_t)id * a.Hkv + kvh) * kpage, lane, live);
       else rk = HalfRecord<KF>{};
@@ -628,6 +636,7 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
     // K of tile t, with its g and mask
     auto put_k = [&](int t, int id) {
       const int st = t & 1, slot = t & (kPNormSlots - 1), live = tokens(t, id);
+      if (KF == 0) return true;  // (the copy warp's)
       if (lane == 0 && (id < 0 || id >= a.num_blocks) && (tile0 + t) * kPBlocks + w < blocks)
         flag_status(a.status, TQ_DEV_BAD_BLOCK);
       if (t >= 2 && !__all_sync(0xffffffffu, mbar_wait(kempty + st, ((t >> 1) & 1) ^ 1))) return false;
@@ -687,6 +696,40 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
       if (t + 1 < n) fetch_v(t + 1, id1);
       id = id1;
       id1 = id2;
+    }
+  } else if (KF == 0 && warp == kPCopyWarp) {
+    // ------------------------------------------------- bf16 keys: tensor copies
+    // lane i < 8 has block i of the tile: its mask, and its page in two swizzled boxes
+    const int blocks = (a.len + kBlock - 1) / kBlock;
+    auto block_id = [&](int t) {
+      const int b = (tile0 + t) * kPBlocks + lane;
+      return lane < kPBlocks && t < n && b < blocks ? __ldg(a.table + b) : -1;
+    };
+    int id = block_id(0);
+    for (int t = 0; t < n && ok; ++t) {
+      const int st = t & 1, slot = t & (kPNormSlots - 1), b = (tile0 + t) * kPBlocks + lane;
+      const int id1 = block_id(t + 1);
+      const bool valid = id >= 0 && id < a.num_blocks;
+      if (!valid && lane < kPBlocks && b < blocks) flag_status(a.status, TQ_DEV_BAD_BLOCK);
+      if (t >= 2) ok = __all_sync(0xffffffffu, mbar_wait(kempty + st, ((t >> 1) & 1) ^ 1));
+      if (!ok) break;
+      if (lane < kPBlocks) {
+        const int live = valid ? min(kBlock, a.len - b * kBlock) : 0;
+        reinterpret_cast<uint16_t*>(gen + kPOffMask)[slot * 8 + lane] = (uint16_t)((1u << live) - 1u);
+      }
+      const uint32_t pages = __popc(__ballot_sync(0xffffffffu, valid));
+      if (lane == 0) {
+        mbar_arrive(gfull + slot);
+        mbar_arrive_expect_tx(kfull + st, pages * (uint32_t)(kBlock * kD * 2));
+      }
+      __syncwarp();
+      if (valid) {
+        const uint32_t dst = k_op + (uint32_t)st * kPOperand + (uint32_t)lane * (kBlock * 128);
+        const int page = id * a.Hkv + kvh;
+        tensor_copy_3d(dst, &a.kmap, 0, 0, page, kfull + st);
+        tensor_copy_3d(dst + kPPanel, &a.kmap, 64, 0, page, kfull + st);
+      }
+      id = id1;
     }
   } else {
     // ------------------------------------------------------------------ MMA
@@ -754,7 +797,7 @@ __global__ void __launch_bounds__(kPThreads, 1) k_prefix(const __grid_constant__
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == kPSoftWarps + kPProdWarps) {
+  if (warp == kPMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -991,7 +1034,7 @@ static cudaError_t run_prefix(const PrefixArgs& a, int splits, cudaStream_t st) 
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_release);
   }
-  kern<<<dim3((unsigned)(a.row_blocks * a.Hkv), (unsigned)splits), kPThreads, kPSmem, st>>>(a);
+  kern<<<dim3((unsigned)(a.row_blocks * a.Hkv), (unsigned)splits), kPThreads<KF>, kPSmem, st>>>(a);
   count_launch();
   return cudaGetLastError();
 }
@@ -1059,6 +1102,7 @@ cudaError_t launch_prefix_decode(const PrefixCall& c, cudaStream_t st) {
     a.status = c.own.status;
     cudaError_t e;
     if (d.fmt.kv_format == TQ_KV_BF16) {
+      if (!bf16_page_map(&a.kmap, d.k_cache, d.num_blocks * d.num_kv_heads)) return cudaErrorNotSupported;
       e = run_prefix<0, 0>(a, p.splits, st);
     } else {
       switch (d.fmt.kv_format == TQ_KV_K8V4 ? 8 : d.fmt.bits_k) {

@@ -1201,6 +1201,19 @@ static bool vec_tensor_map(CUtensorMap* m, const void* x, uint32_t n_vec, uint32
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A pool of bf16 pages [pages][16][128]: boxes of one page and half its columns, 128-byte swizzle.
+bool bf16_page_map(CUtensorMap* m, const void* pool, int64_t pages) {
+  const EncodeTiledFn enc = encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)kBlock, (cuuint64_t)pages};
+  const cuuint64_t strides[2] = {(cuuint64_t)kD * 2, (cuuint64_t)kBlock * kD * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)kBlock, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(pool), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Launches kern<<<grid, block, smem, st>>>(args); with pdl, as a programmatic dependent
 // of the kernel before it on the stream (it may start while that kernel finishes).
 template <typename Args>
