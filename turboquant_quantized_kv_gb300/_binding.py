@@ -176,18 +176,27 @@ def make_rotation(kind, seed, layer=0, head_dim=TQ_HEAD_DIM):
 
 # ------------------------------------------------------------ tensor glue
 
+_torch_module = None
+_dtype_codes = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t):
-    torch = _torch()
-    if t.dtype == torch.float32:
-        return TQ_F32
-    if t.dtype == torch.bfloat16:
-        return TQ_BF16
-    raise TypeError("unsupported dtype %s (float32 or bfloat16)" % t.dtype)
+    global _dtype_codes
+    if _dtype_codes is None:
+        torch = _torch()
+        _dtype_codes = {torch.float32: TQ_F32, torch.bfloat16: TQ_BF16}
+    code = _dtype_codes.get(t.dtype)
+    if code is None:
+        raise TypeError("unsupported dtype %s (float32 or bfloat16)" % t.dtype)
+    return code
 
 
 def _ptr(t, name):
@@ -208,6 +217,9 @@ def _stream(stream):
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
+_byref = ctypes.byref
+
+
 def _check_rows(x, what, n):
     """Strides of rows [n, heads, d] on the device with a contiguous last dimension; raises for others."""
     if not x.is_cuda:
@@ -222,17 +234,17 @@ def _check_rows(x, what, n):
 
 
 def _heads(t, out, name, n):
-    """A tq_heads of t [n, heads, d] (any token and head strides) and its output rows."""
+    """Reference to a tq_heads of t [n, heads, d] (any token and head strides) and its output rows."""
     if t is None:
         return None
     st = so = _check_rows(t, name, n)
     if out is None:
-        return Heads(t.data_ptr(), None, t.shape[1], st[0], st[1], 0, 0)
+        return _byref(Heads(t.data_ptr(), None, t.shape[1], st[0], st[1], 0, 0))
     if out is not t:
         if out.shape != t.shape or out.dtype != t.dtype:
             raise ValueError("%s_out must have %s's shape and type" % (name, name))
         so = _check_rows(out, name + "_out", n)
-    return Heads(t.data_ptr(), out.data_ptr(), t.shape[1], st[0], st[1], so[0], so[1])
+    return _byref(Heads(t.data_ptr(), out.data_ptr(), t.shape[1], st[0], st[1], so[0], so[1]))
 
 
 def _index_ptr(t, name, dtype, shape):
@@ -281,7 +293,8 @@ class Rope:
                 raise ValueError("inv_freq must hold rotary_dim / 2 frequencies")
             freqs = (ctypes.c_double * values.size)(*values)
         self.desc = RopeDesc()
-        _check(lib().tq_make_rope(self._LAYOUTS[layout], rotary_dim, base, _ref(s), freqs, ctypes.byref(self.desc)))
+        self.ref = ctypes.byref(self.desc)
+        _check(lib().tq_make_rope(self._LAYOUTS[layout], rotary_dim, base, _ref(s), freqs, self.ref))
         self.layout, self.rotary_dim = layout, int(rotary_dim)
         self.amplitude = float(self.desc.amplitude)
 
@@ -295,20 +308,19 @@ def apply_rope(rope, positions, q, k=None, q_out=None, k_out=None, transpose=Fal
     [n_tokens].  transpose: the transposed rotation (the gradient).  q_out / k_out may be
     q / k (in place).  Returns (q_out, k_out), contiguous where they were not given."""
     torch = _torch()
-    if q is None and k is None:
-        raise ValueError("q or k is needed")
     ref = q if q is not None else k
-    if q is not None and k is not None and q.dtype != k.dtype:
+    if ref is None:
+        raise ValueError("q or k is needed")
+    dtype, device, n = ref.dtype, ref.device, ref.shape[0]
+    if k is not None and k.dtype != dtype:
         raise TypeError("q and k must have one type")
     if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = torch.empty(q.shape, dtype=dtype, device=device)
     if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    n = int(ref.shape[0])
+        k_out = torch.empty(k.shape, dtype=dtype, device=device)
     pos = _index_ptr(positions, "positions", torch.int64, (n,))
-    hq, hk = _heads(q, q_out, "q", n), _heads(k, k_out, "k", n)
-    _check(lib().tq_rope_apply(ctypes.byref(rope.desc), 1 if transpose else 0, _ref(hq), _ref(hk), _dtype_code(ref),
-                               pos, n, _stream(stream)))
+    _check(lib().tq_rope_apply(rope.ref, 1 if transpose else 0, _heads(q, q_out, "q", n), _heads(k, k_out, "k", n),
+                               _dtype_code(ref), pos, n, _stream(stream)))
     return q_out, k_out
 
 
@@ -494,17 +506,15 @@ class Layer:
         ref = k if k is not None else v
         if ref is None:
             raise ValueError("k or v is needed")
-        if any(t is not None and t.dtype != ref.dtype for t in (q, v)):
+        dtype, n = ref.dtype, ref.shape[0]
+        if (q is not None and q.dtype != dtype) or (v is not None and v.dtype != dtype):
             raise TypeError("q, k and v must have one type")
-        n = int(ref.shape[0])
         pos = _index_ptr(positions, "positions", torch.int64, (n,))
         slots = _index_ptr(slot_mapping, "slot_mapping", torch.int64, (n,))
         if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        hq, hk = _heads(q, q_out, "q", n), _heads(k, k_out, "k", n)
-        hv = _heads(v, None, "v", n)
-        _check(lib().tq_rope_append(ctypes.byref(self.desc), ctypes.byref(rope.desc), _ref(hq), _ref(hk), _ref(hv),
-                                    _dtype_code(ref), pos, slots, n, _stream(stream)))
+            q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
+        _check(lib().tq_rope_append(_byref(self.desc), rope.ref, _heads(q, q_out, "q", n), _heads(k, k_out, "k", n),
+                                    _heads(v, None, "v", n), _dtype_code(ref), pos, slots, n, _stream(stream)))
         return q_out
 
     def prefix_workspace_bytes(self, batch, num_q_heads, prefix_len, max_blocks_per_seq):

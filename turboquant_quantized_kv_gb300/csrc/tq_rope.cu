@@ -760,7 +760,7 @@ cudaError_t launch_rope_append(const RopeCall& c, const tq_cache_desc& d, cudaSt
   // together).
   const int64_t coded = a.coded[0].tiles + a.coded[1].tiles;
   bool apart = false;
-  if (coded > 0 && a.row_tiles > 0 && c.n_tokens * a.heads >= (1 << 20)) {
+  if (coded > 0 && a.row_tiles > 0 && c.n_tokens * a.heads >= (1 << 18)) {
     const cudaError_t e = c.dtype == TQ_F32 ? run_apply<float>(a, c.num_sms, st) : run_apply<__nv_bfloat16>(a, c.num_sms, st);
     if (e != cudaSuccess) return e;
     a.row_tiles = 0;
