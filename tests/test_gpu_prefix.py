@@ -175,6 +175,84 @@ def test_workspace_serves_both_calls_and_repeats(cuda, tqlib):
             assert cuda.equal(layer.decode(*args, workspace=big), layer.decode(*args))
 
 
+@pytest.mark.parametrize("fmt,bk,bv", [("bf16", 4, 4), ("k8v4", 8, 4), ("packed", 4, 4), ("packed", 3, 4)])
+@pytest.mark.parametrize("width", [127, 128, 129, 200])
+def test_wide_block_tables(cuda, tqlib, fmt, bk, bv, width):
+    """Block tables around the width from which the decode kernel takes the own tokens, with a full, a
+    short and an empty sequence."""
+    case = build(cuda, tqlib, fmt, bk, bv, B=3, hq=8, hkv=1, P=150, lens=[16 * width - 3, 20, 0], seed=width,
+                 width=width)
+    check(cuda, tqlib, case, 150)
+
+
+@pytest.mark.parametrize("fmt,bk,bv", [("bf16", 4, 4), ("k8v4", 8, 4), ("packed", 4, 4)])
+@pytest.mark.parametrize("scale", [-0.05, 0.0, 0.3])
+def test_scales_of_any_sign(cuda, tqlib, fmt, bk, bv, scale):
+    P = 200
+    case = build(cuda, tqlib, fmt, bk, bv, B=3, hq=8, hkv=2, P=P, lens=[20, 0, 33], seed=3, heavy=True)
+    layer, q, ptab, table, lens = case
+    out = run(cuda, tqlib, case, P, cuda.float32, sm_scale=scale)
+    ref = prefix_attention(q.double().cpu().numpy(), *stands_for(layer), ptab, P, table, lens, scale)
+    assert max_rel_err(out.cpu().numpy(), ref) <= TOL
+
+
+def test_bad_context_lengths_are_clamped_and_flagged(cuda, tqlib):
+    """As in decode: a negative length counts as none, one past the table as the whole table."""
+    tq = tqlib
+    for fmt, bk, bv in FORMATS:
+        layer, q, ptab, table, lens = build(cuda, tq, fmt, bk, bv, B=3, hq=4, hkv=2, P=40, lens=[32, 32, 5], seed=8)
+        out = layer.prefix_decode(q, cuda.from_numpy(ptab).cuda(), 40, cuda.from_numpy(table).cuda(),
+                                  cuda.tensor([-4, 1000, 5], dtype=cuda.int32, device="cuda"), out_dtype=cuda.float32)
+        cuda.cuda.synchronize()
+        assert tq.get_device_status() == tq.TQ_DEV_BAD_CONTEXT
+        ref = prefix_attention(q.double().cpu().numpy(), *stands_for(layer), ptab, 40, table, np.array([0, 32, 5]),
+                               1 / math.sqrt(D))
+        assert max_rel_err(out.cpu().numpy(), ref) <= TOL
+
+
+def test_bad_own_blocks_are_skipped_and_flagged(cuda, tqlib):
+    tq = tqlib
+    for fmt, bk, bv in FORMATS:
+        layer, q, ptab, table, lens = build(cuda, tq, fmt, bk, bv, B=2, hq=4, hkv=2, P=40, lens=[48, 20], seed=8)
+        bad = table.copy()
+        bad[0, 1], bad[1, 0] = layer.num_blocks + 7, -2
+        out = layer.prefix_decode(q, cuda.from_numpy(ptab).cuda(), 40, cuda.from_numpy(bad).cuda(),
+                                  cuda.from_numpy(lens).cuda(), out_dtype=cuda.float32)
+        cuda.cuda.synchronize()
+        assert tq.get_device_status() == tq.TQ_DEV_BAD_BLOCK
+        left = np.stack([table[0, [0, 2, 2]], table[1, [1, 1, 1]]])
+        ref = prefix_attention(q.double().cpu().numpy(), *stands_for(layer), ptab, 40, left, np.array([32, 4]),
+                               1 / math.sqrt(D))
+        assert max_rel_err(out.cpu().numpy(), ref) <= TOL
+
+
+def test_unaligned_output_and_raw_norms(cuda, tqlib):
+    tq = tqlib
+    P = 100
+    layer, q, ptab, table, lens = case = build(cuda, tq, "packed", 4, 4, B=3, hq=4, hkv=2, P=P, lens=[9, 0, 17], seed=2)
+    for dtype in (cuda.bfloat16, cuda.float32):
+        want = run(cuda, tq, case, P, dtype)
+        flat = cuda.zeros(q.numel() + 1, dtype=dtype, device="cuda")
+        out = flat[1:].view(q.shape)
+        run(cuda, tq, case, P, out=out)
+        assert cuda.equal(out, want)
+    raw = tq.Layer(10, 1, bits_k=3, bits_v=2, norm_mode=tq.TQ_NORM_RAW, seed=4, fill=0xFF)
+    k, v = (cuda.from_numpy(x.view(np.int16)).cuda().view(cuda.bfloat16) for x in workloads.lognormal_channel_kv(3, 70, 1, D))
+    pos = cuda.arange(70, device="cuda")
+    raw.rope_append(tq.Rope(), k, v, pos, pos)
+    q1 = cuda.from_numpy(workloads.queries(5, 2, 3, D, dtype="f32")).cuda()
+    ids = cuda.arange(5, dtype=cuda.int32, device="cuda")
+    out = raw.prefix_decode(q1, ids, 70)
+    ref = prefix_attention(q1.double().cpu().numpy(), *stands_for(raw), np.arange(5), 70, np.zeros((2, 0), np.int32),
+                           np.zeros(2, np.int32), 1 / math.sqrt(D))
+    assert max_rel_err(out.cpu().numpy(), ref) <= TOL
+
+
+def test_example_runs_the_operators_together(cuda, tqlib):
+    from examples import shared_prefix
+    assert shared_prefix.main(batch=3, prompt=120, steps=3, verbose=False) <= 2 * TOL
+
+
 def test_bad_prefix_blocks_are_skipped_and_flagged(cuda, tqlib):
     tq = tqlib
     for fmt, bk, bv in FORMATS:
