@@ -86,37 +86,9 @@ __device__ __forceinline__ void load32<__nv_bfloat16>(const __nv_bfloat16* p, fl
   }
 }
 
-// Unnormalised Walsh-Hadamard transform of 128 values spread over the 4
-// consecutive lanes of a quad (lane q holds coordinates [32q, 32q + 32)):
-// 5 butterfly stages inside the registers, 2 across lanes.
-__device__ __forceinline__ void fwht128_quad(float (&x)[32], int q) {
-#pragma unroll
-  for (int h = 1; h < 32; h <<= 1) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      if ((i & h) == 0) {
-        float a = x[i], b = x[i + h];
-        x[i] = a + b;
-        x[i + h] = a - b;
-      }
-    }
-  }
-#pragma unroll
-  for (int m = 1; m <= 2; m <<= 1) {
-    const bool upper = (q & m) != 0;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      float o = __shfl_xor_sync(0xffffffffu, x[i], m);
-      x[i] = upper ? (o - x[i]) : (x[i] + o);
-    }
-  }
-}
-
-// The same transform with packed fp32 pairs (sm_100+ f32x2 arithmetic): bit 0 of
-// the coordinate inside each pair, bits 1..4 as pair butterflies, bits 5 and 6
-// across the quad as x <- partner + s x with s = -1 on the upper lane.
-__device__ __forceinline__ void fwht128_quad_f2(float (&x)[32], int q) {
-  float2 v[16];
+// The five in-lane stages of the quad transforms below, with packed fp32 pairs (sm_100+ f32x2
+// arithmetic): bit 0 of the coordinate inside each pair, bits 1..4 as pair butterflies.
+__device__ __forceinline__ void fwht32_pairs(const float (&x)[32], float2 (&v)[16]) {
 #pragma unroll
   for (int j = 0; j < 16; ++j) v[j] = make_float2(x[2 * j] + x[2 * j + 1], x[2 * j] - x[2 * j + 1]);
   const float2 m1 = make_float2(-1.0f, -1.0f);
@@ -131,6 +103,14 @@ __device__ __forceinline__ void fwht128_quad_f2(float (&x)[32], int q) {
       }
     }
   }
+}
+
+// Unnormalised Walsh-Hadamard transform of 128 values spread over the 4 consecutive lanes of a
+// quad (lane q holds coordinates [32q, 32q + 32)): 5 butterfly stages inside the registers, then
+// bits 5 and 6 across the quad as x <- partner + s x with s = -1 on the upper lane.
+__device__ __forceinline__ void fwht128_quad_f2(float (&x)[32], int q) {
+  float2 v[16];
+  fwht32_pairs(x, v);
 #pragma unroll
   for (int m = 1; m <= 2; m <<= 1) {
     const float sgn = (q & m) ? -1.0f : 1.0f;
@@ -139,6 +119,39 @@ __device__ __forceinline__ void fwht128_quad_f2(float (&x)[32], int q) {
     for (int j = 0; j < 16; ++j) {
       const float2 o = make_float2(__shfl_xor_sync(0xffffffffu, v[j].x, m), __shfl_xor_sync(0xffffffffu, v[j].y, m));
       v[j] = __ffma2_rn(v[j], s2, o);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    x[2 * j] = v[j].x;
+    x[2 * j + 1] = v[j].y;
+  }
+}
+
+// The same transform (same additions in the same order) for a kernel that may take its values
+// dealt out otherwise afterwards: x[8 b + c] is coordinate 32 q + 8 b + c of lane q on entry and
+// coordinate 32 b + 8 q + c at the end.  The two stages across lanes exchange the half of the
+// values that changes lanes instead of all of them: 32 shuffles for 64.
+__device__ __forceinline__ void fwht128_quad_swap(float (&x)[32], int q) {
+  float2 v[16];
+  fwht32_pairs(x, v);
+  // v[4 b + c / 2].  Lane bit 0 against bit 0 of b, then lane bit 1 against bit 1 of b: a lane
+  // keeps the values whose bit is its own, sends the others, and forms sum and difference in the
+  // order of the lanes (the lower lane's value first).
+#pragma unroll
+  for (int m = 1; m <= 2; m <<= 1) {
+    const bool up = (q & m) != 0;
+    const float sgn = up ? -1.0f : 1.0f;
+    const float2 s2 = make_float2(sgn, sgn), n2 = make_float2(-sgn, -sgn);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      if (((j >> 2) & m) == 0) {
+        const float2 lo = v[j], hi = v[j + 4 * m];
+        const float2 keep = up ? hi : lo, send = up ? lo : hi;
+        const float2 got = make_float2(__shfl_xor_sync(0xffffffffu, send.x, m), __shfl_xor_sync(0xffffffffu, send.y, m));
+        v[j] = __fadd2_rn(keep, got);
+        v[j + 4 * m] = __ffma2_rn(keep, s2, __fmul2_rn(got, n2));
+      }
     }
   }
 #pragma unroll

@@ -1038,13 +1038,18 @@ __global__ void __launch_bounds__(kThreads) k_dequant(const uint8_t* __restrict_
   }
   if (DENSE) stage_matrix(rot, matP, /*transpose=*/false);  // out = Pi^T v
   __syncthreads();
-  const uint32_t sw = DENSE ? 0u : signw[q];
+  // Hadamard layers end with coordinates 32 r + 8 q + c at v[8 r + c], dense ones with 32 q + i
+  uint32_t sw = 0u;
+  if (!DENSE) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) sw |= ((signw[r] >> (8 * q)) & 0xFFu) << (8 * r);
+  }
   const int64_t n_tiles = (n_vec + kTile - 1) / kTile;
   for (int64_t t = blockIdx.x; t < n_tiles; t += gridDim.x) {
     const int64_t vec_raw = t * kTile + vl;
     const bool valid = vec_raw < n_vec;
     const int64_t vec = valid ? vec_raw : (n_vec - 1);
-    const int64_t tok = vec / H;
+    const int64_t tok = n_vec < (1ll << 32) ? (int64_t)((uint32_t)vec / (uint32_t)H) : vec / H;
     const int head = (int)(vec - tok * H);
     const int64_t slot = __ldg(slots + tok);
     const bool ok = slot >= 0 && slot < max_slot;
@@ -1077,32 +1082,34 @@ __global__ void __launch_bounds__(kThreads) k_dequant(const uint8_t* __restrict_
       __syncthreads();
       matvec_padded(matP, tile + vl * kTileStride, q, v);
     } else {
-      fwht128_quad(v, q);  // Pi^T v = D H v / sqrt(d)
+      fwht128_quad_swap(v, q);  // Pi^T v = D H v / sqrt(d)
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = flip_sign(v[i] * 0.08838834764831845f, sw, i);
     }
     if (valid) {
-      TOut* o = out + vec * kD + 32 * q;
+      TOut* o = out + vec * kD + (DENSE ? 32 : 8) * q;
+      constexpr int kRun = DENSE ? 8 : 32;  // from one eight to the next
       if ((reinterpret_cast<uintptr_t>(out) & 15u) == 0u) {  // 16-byte stores
-        if constexpr (sizeof(TOut) == 2) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (sizeof(TOut) == 2) {
             uint32_t w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const __nv_bfloat162 b = __floats2bfloat162_rn(v[8 * i + 2 * k], v[8 * i + 2 * k + 1]);
               w[k] = *reinterpret_cast<const uint32_t*>(&b);
             }
-            reinterpret_cast<uint4*>(o)[i] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        } else {
+            *reinterpret_cast<uint4*>(o + kRun * i) = make_uint4(w[0], w[1], w[2], w[3]);
+          } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            reinterpret_cast<float4*>(o)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            for (int k = 0; k < 8; k += 4)
+              *reinterpret_cast<float4*>(o + kRun * i + k) =
+                  make_float4(v[8 * i + k], v[8 * i + k + 1], v[8 * i + k + 2], v[8 * i + k + 3]);
+          }
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) store_elem<TOut>(o + i, v[i]);
+        for (int i = 0; i < 32; ++i) store_elem<TOut>(o + kRun * (i >> 3) + (i & 7), v[i]);
       }
     }
   }

@@ -652,12 +652,12 @@ static void fill_common(RopeArgs& a, const RopeCall& c) {
   a.status = c.status;
 }
 
-// Tokens a tile of the rows part: enough items for the CTA's threads to have sixteen each,
-// so that forming the angles and the two barriers weigh little; fewer while the tiles would
-// not fill the GPU.
+// Tokens a tile of the rows part: enough items for the CTA's threads to have four each, fewer
+// while the tiles would not fill the GPU.  (Sixteen items a thread leave too few tiles to
+// spread: 12,345 tokens of 40 heads 51 us, with four 48.)
 static int rows_tile(const RopeArgs& a, int num_sms) {
   int t = 1;
-  while (t < 8 && t * a.heads * (kPairs / 8) < 16 * kRThreads && a.n_tok / (2 * t) >= 8 * (int64_t)num_sms) t *= 2;
+  while (t < 8 && t * a.heads * (kPairs / 8) < 4 * kRThreads && a.n_tok / (2 * t) >= 8 * (int64_t)num_sms) t *= 2;
   return t;
 }
 
