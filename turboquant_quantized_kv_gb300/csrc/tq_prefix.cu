@@ -287,6 +287,8 @@ __device__ __forceinline__ void place_q(const QRows<BF16>& q, const PrefixArgs& 
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     if (h == 1 && !a.pair) break;
+    // (a group of eight rows past the end stays unwritten: a row's products meet no other row)
+    if (r0 + h * kPTile + 8 * warp >= a.rows) break;
     const int tr = 8 * warp + (lane >> 2);
     const bool live = r0 + h * kPTile + tr < a.rows;
     float x[32];
@@ -297,13 +299,12 @@ __device__ __forceinline__ void place_q(const QRows<BF16>& q, const PrefixArgs& 
       if (KF >= 2 && KF <= 4) x[i] = __uint_as_float(__float_as_uint(x[i]) ^ ((signs << (31 - i)) & 0x80000000u));
     }
     if (KF >= 2 && KF <= 4) {
-      fwht128_quad_f2(x, quad);
+      fwht128_quad_swap(x, quad);
 #pragma unroll
       for (int i = 0; i < 32; ++i) x[i] *= 0.08838834764831845f;  // 1 / sqrt(128)
     }
-    const uint32_t row = (uint32_t)(quad >> 1) * kPPanel + (uint32_t)tr * 128u;
-    const uint32_t hi = base + (uint32_t)h * kPOperand + row;
-    const uint32_t lo = base + (uint32_t)(a.pair ? 2 + h : 1) * kPOperand + row;
+    const uint32_t hi = base + (uint32_t)h * kPOperand + (uint32_t)tr * 128u;
+    const uint32_t lo = base + (uint32_t)(a.pair ? 2 + h : 1) * kPOperand + (uint32_t)tr * 128u;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       uint32_t w[4], v[4];
@@ -319,7 +320,9 @@ __device__ __forceinline__ void place_q(const QRows<BF16>& q, const PrefixArgs& 
           v[k] = pack_h2(x0 - f.x, x1 - f.y);
         }
       }
-      const uint32_t off = (uint32_t)(((4 * (quad & 1) + c) ^ (tr & 7)) << 4);
+      // eight coordinates: from 32 c + 8 quad on after the transform, from 32 quad + 8 c on without
+      const int at = KF >= 2 && KF <= 4 ? 4 * c + quad : 4 * quad + c;
+      const uint32_t off = (uint32_t)(at >> 3) * kPPanel + (uint32_t)(((at & 7) ^ (tr & 7)) << 4);
       asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(hi + off), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
                    : "memory");
       if (a.split_q)
@@ -407,16 +410,21 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
     uint32_t signs = 0u;
     if (warp == kPMmaWarp) tmem_alloc(base + kPOffTmem, 512);
     if (stages) {
+      float sv[4] = {};
       if (KF >= 2 && KF <= 4) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t m = __ballot_sync(0xffffffffu, __ldg(a.rot + 32 * k + lane) < 0.0f);
-          if ((lane & 3) == k) signs = m;
-        }
+        for (int k = 0; k < 4; ++k) sv[k] = __ldg(a.rot + 32 * k + lane);
       }
       const float mx = a.q_bf16 ? load_q<true>(q16, a, kvh, r0, warp, lane) : load_q<false>(q32, a, kvh, r0, warp, lane);
       const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
       if (lane == 0) atomicMax(qmax, m);
+      if (KF >= 2 && KF <= 4) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t b = __ballot_sync(0xffffffffu, sv[k] < 0.0f);
+          if ((lane & 3) == k) signs = b;
+        }
+      }
     }
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -987,10 +995,18 @@ int own_splits(int max_blocks) { return max_blocks <= kOwnMaxBlocks ? (max_block
 // CTAs over the rows and splits of the tokens.  The splits are chosen so that the CTAs,
 // one an SM, fill whole waves: the fewest tiles in a row over one to four waves, a CTA's
 // start and end counted as three tiles.
+//
+// The own tokens' CTAs (own_ctas of them, a few an SM) run next to the prefix kernel on the SMs
+// that it leaves free.  When some of them would have to follow it, fewer splits may be better:
+// the times below are in us, of a tile, of the prefix kernel's start and end, and of a CTA of
+// k_own.  (64 rows, 8192 tokens, 512 CTAs of own tokens: 16 splits 37.4 us, 13 31.0, 11 29.0,
+// 10 31.0.)  Never more splits than without own tokens, so that a workspace made for them
+// serves calls that have none.
 struct PrefixPlan {
   int pair, row_blocks, splits, tiles_per_split, partials;
 };
-static PrefixPlan prefix_plan(const tq_cache_desc& d, int batch, int num_q_heads, int64_t len, int num_sms) {
+static PrefixPlan prefix_plan(const tq_cache_desc& d, int batch, int num_q_heads, int64_t len, int64_t own_ctas,
+                              int num_sms) {
   PrefixPlan p = {};
   if (len < 1) return p;
   const int64_t rows = (int64_t)batch * (num_q_heads / d.num_kv_heads);
@@ -1012,13 +1028,31 @@ static PrefixPlan prefix_plan(const tq_cache_desc& d, int batch, int num_q_heads
       p.tiles_per_split = (int)per;
     }
   }
+  if (own_ctas > 0 && units * p.splits <= num_sms) {
+    const float tile_us = p.pair ? 2.9f : 1.3f, ends_us = p.pair ? 8.7f : 10.4f, own_us = 7.0f;
+    const int64_t per_sm = d.fmt.kv_format == TQ_KV_BF16 ? 3 : 4;
+    float least = INFINITY;
+    for (int64_t s = p.splits; s >= 1; --s) {
+      const int64_t per = (tiles + s - 1) / s;
+      s = (tiles + per - 1) / per;
+      const float t = tile_us * (float)per + ends_us;
+      const int64_t beside = (num_sms - units * s) * per_sm * (int64_t)(t / own_us);
+      const int64_t left = own_ctas > beside ? own_ctas - beside : 0;
+      const float all = t + own_us * (float)((left + num_sms * per_sm - 1) / (num_sms * per_sm));
+      if (all < least) {
+        least = all;
+        p.splits = (int)s;
+        p.tiles_per_split = (int)per;
+      }
+    }
+  }
   p.partials = p.splits * (p.pair ? 1 : 2);
   return p;
 }
 
 size_t prefix_partial_bytes(const tq_cache_desc& d, int batch, int num_q_heads, int64_t prefix_len, int num_sms) {
   const size_t tiles = ((size_t)batch * (num_q_heads / d.num_kv_heads) + 31) / 32 * d.num_kv_heads;
-  return (size_t)prefix_plan(d, batch, num_q_heads, prefix_len, num_sms).partials * tiles * 32 * (kD + 2) * sizeof(float);
+  return (size_t)prefix_plan(d, batch, num_q_heads, prefix_len, 0, num_sms).partials * tiles * 32 * (kD + 2) * sizeof(float);
 }
 
 template <int KF, int VF>
@@ -1071,7 +1105,10 @@ cudaError_t launch_prefix_decode(const PrefixCall& c, cudaStream_t st) {
   }
   if (c.prefix_len > 0) {
     PrefixArgs a = {};
-    const PrefixPlan p = prefix_plan(d, c.own.batch, c.own.num_q_heads, c.prefix_len, c.num_sms);
+    const int64_t own_ctas = c.own.max_blocks > 0 ? (int64_t)own_splits(c.own.max_blocks) * c.own.batch * d.num_kv_heads *
+                                                        ((c.own.num_q_heads / d.num_kv_heads + 7) / 8)
+                                                  : 0;
+    const PrefixPlan p = prefix_plan(d, c.own.batch, c.own.num_q_heads, c.prefix_len, own_ctas, c.num_sms);
     a.split_q = d.fmt.kv_format == TQ_KV_PACKED || c.own.q_dtype == TQ_F32 ? 1 : 0;
     a.v_stages = p.pair && a.split_q ? 1 : 2;
     a.kpool = reinterpret_cast<const uint8_t*>(d.k_cache);

@@ -109,6 +109,12 @@ __global__ void __launch_bounds__(kOwnWarps * 32, KF == 0 ? 3 : 4) k_own(const _
   __shared__ float red[kOwnWarps][8][kD + 4];
   __shared__ float redc[kOwnWarps][8], redl[kOwnWarps][8];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // The grid completes only after the prefix kernel, so that what follows finds both kernels'
+  // partials: its last CTA waits for it.  (Were all to wait, the few that find room next to the
+  // prefix kernel would keep it until that ends, and the rest would start only then.)
+  auto finish = [&] {
+    if (blockIdx.x + 1 == gridDim.x && blockIdx.y + 1 == gridDim.y) grid_dep_wait();
+  };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g_ = lane >> 2, tig = lane & 3;
   const int unit = blockIdx.x, hg = unit % a.ngroups, kvh = (unit / a.ngroups) % a.Hkv, b = unit / (a.ngroups * a.Hkv);
   const int rows = min(8, a.g - 8 * hg);
@@ -161,7 +167,7 @@ __global__ void __launch_bounds__(kOwnWarps * 32, KF == 0 ? 3 : 4) k_own(const _
       ml[0] = -INFINITY;
       ml[1] = 0.0f;
     }
-    grid_dep_wait();
+    finish();
     return;
   }
   // the warp's blocks start towards L2
@@ -380,7 +386,7 @@ __global__ void __launch_bounds__(kOwnWarps * 32, KF == 0 ? 3 : 4) k_own(const _
       a.ml[2 * slot + 1] = L;
     }
   }
-  grid_dep_wait();  // (completes only after the prefix kernel, so that what follows finds both)
+  finish();
 }
 
 template <int KF, int VF>
