@@ -2,9 +2,10 @@
 values the cache stands for.
 
 Tolerance: max over rows of the largest error over the row's largest value, 5e-3, the
-bound of the decode kernels with bf16 data: the code tables and the scaled query are held
-in fp16 (2^-11 of a value, half a step 2^-12), the weights in fp16 or bf16 (half a step
-2^-9 of a weight, with random signs over the tokens), the output in bf16 (2^-9)."""
+bound of the decode kernels with bf16 data: the output is rounded to bf16 (half a step, 2^-8 of
+the value, 3.9e-3); the code tables and the values are held in fp16 (half a step 2^-11 each,
+with random signs over coordinates and tokens), and so are the weights; the queries in two
+fp16 parts (2^-22)."""
 import math
 
 import numpy as np

@@ -11,7 +11,9 @@
 //     O^T [128 x rows]   += V^T P^T, once for P's high parts and once for its low ones.
 // A logit's lane is the lane that P needs it in.  What bounds it is the latency of a warp's few
 // blocks, so small CTAs, several an SM, take the place of one large one: own contexts of 0 to
-// 256 tokens of 128 sequences (32/8 heads, bf16) took the decode kernel 33 us.
+// 256 tokens of 128 sequences (32/8 heads, bf16) take 20 us alone, with the decode kernel 33.
+// Next to the prefix kernel most of it is hidden (64 sequences of up to 500 tokens, 64/8 heads:
+// 18 us alone, the call 5 longer than without own tokens).
 #include <cuda_fp8.h>
 
 #include "tq_async.cuh"
