@@ -269,6 +269,31 @@ def test_bad_prefix_blocks_are_skipped_and_flagged(cuda, tqlib):
         assert max_rel_err(out.cpu().numpy(), ref) <= TOL
 
 
+@pytest.mark.parametrize("fmt,bk,bv", [("bf16", 4, 4), ("k8v4", 8, 4), ("packed", 4, 4), ("packed", 3, 2)])
+@pytest.mark.parametrize("B,P", [(24, 3000), (80, 900)])
+def test_many_own_tokens_beside_the_prefix(cuda, tqlib, fmt, bk, bv, B, P):
+    """Enough CTAs of own tokens that the prefix is cut into fewer splits and both kernels run at
+    once: right, the same bits in calls that follow one another without a pause, and the
+    workspace serves the call without own tokens."""
+    tq = tqlib
+    lens = workloads.rng(B).integers(0, 1500, B)
+    lens[:3] = 0, 1500, 1
+    case = build(cuda, tq, fmt, bk, bv, B=B, hq=16, hkv=4, P=P, lens=lens, seed=B)
+    check(cuda, tq, case, P)
+    layer, q, ptab, table, lens = case
+    p, t, n = (cuda.from_numpy(x).cuda() for x in (ptab, table, lens))
+    ws = cuda.zeros(layer.prefix_workspace_bytes(B, 16, P, table.shape[1]), dtype=cuda.uint8, device="cuda")
+    outs = [layer.prefix_decode(q, p, P, t, n, workspace=ws) for _ in range(20)]
+    alone = layer.prefix_decode(q, p, P, workspace=ws)
+    cuda.cuda.synchronize()
+    assert tq.get_device_status() == 0
+    assert all(cuda.equal(o, outs[0]) for o in outs[1:])
+    none = np.zeros((B, 0), np.int32)
+    ref = prefix_attention(q.double().cpu().numpy(), *stands_for(layer), ptab, P, none, np.zeros(B, np.int32),
+                           1 / math.sqrt(D))
+    assert max_rel_err(alone.float().cpu().numpy(), ref) <= TOL
+
+
 def test_capture_on_a_side_stream(cuda, tqlib):
     tq = tqlib
     case = build(cuda, tq, "packed", 4, 4, B=6, hq=8, hkv=2, P=333, lens=[1, 2, 3, 40, 0, 9], seed=21)
