@@ -835,18 +835,19 @@ struct MergeArgs {
   int out_bf16;
 };
 
-// A CTA: 8 rows of one KV head, four warps (or twice four, see launch); thread (w, lane) holds two 16-byte pieces, coordinates
+// A CTA: 8 rows of one KV head, one to four sets of four warps (see launch); thread (w, lane) holds two 16-byte pieces, coordinates
 // 4 c .. 4 c + 3 for c = 8 w + 4 k + lane / 8, of row lane % 8, so that a warp's load is four
 // runs of 128 bytes.  Joins the partials at their common reference in a fixed order, divides,
 // applies Pi^T (coordinate bits 0, 1 and 4 in the thread, 2 and 3 across lanes, 5 and 6 across
 // warps).
 constexpr int kMergeRound = 64;  // partials a round
-template <int HALVES>
-__global__ void __launch_bounds__(HALVES * 128) k_prefix_merge(const __grid_constant__ MergeArgs a) {
-  __shared__ float4 sm[4][2][32], half[4][2][32];
+template <int SETS>
+__global__ void __launch_bounds__(SETS * 128) k_prefix_merge(const __grid_constant__ MergeArgs a) {
+  __shared__ float4 sm[4][2][32], sums[SETS > 1 ? SETS - 1 : 1][4][2][32];
+  __shared__ float lsum[SETS][32];
   __shared__ float2 fl[kMergeRound][8];  // a round's references, then factors, and denominators
-  // warps 4 to 7 take every other batch of partials and hand their sums to warps 0 to 3
-  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3, hi = HALVES == 2 ? threadIdx.x >> 7 : 0;
+  // warps 4 h to 4 h + 3 take every SETS-th batch of partials and hand their sums to warps 0 to 3
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3, hi = threadIdx.x >> 7;
   const int tiles8 = (a.rows + 7) / 8;
   const int kvh = blockIdx.x / tiles8;
   const int r = (blockIdx.x - kvh * tiles8) * 8 + (lane & 7);
@@ -872,7 +873,7 @@ __global__ void __launch_bounds__(HALVES * 128) k_prefix_merge(const __grid_cons
   for (int p0 = 0; p0 < total; p0 += kMergeRound) {
     const int n = min(kMergeRound, total - p0);
     // (references and denominators of the round's partials: 16 or 32 threads a row)
-    for (int k = threadIdx.x >> 3; k < n; k += 16 * HALVES) {
+    for (int k = threadIdx.x >> 3; k < n; k += 16 * SETS) {
       const int s = p0 + k - a.partials;
       float2 e = make_float2(-INFINITY, 0.0f);
       if (s < 0) e = __ldcg(ml + (p0 + k) * step);
@@ -888,7 +889,7 @@ __global__ void __launch_bounds__(HALVES * 128) k_prefix_merge(const __grid_cons
     for (int i = 0; i < 8; ++i) y[i] *= f0;
     M = nm;
     constexpr int kBatch = 8;  // partials whose loads are in flight; an empty one is not read
-    for (int k0 = hi * kBatch; k0 < n; k0 += HALVES * kBatch) {
+    for (int k0 = hi * kBatch; k0 < n; k0 += SETS * kBatch) {
       float4 t[kBatch][2];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
@@ -917,24 +918,28 @@ __global__ void __launch_bounds__(HALVES * 128) k_prefix_merge(const __grid_cons
     }
     __syncthreads();
   }
-  if constexpr (HALVES == 2) {
-    // (both halves scaled to the same reference)
+  if constexpr (SETS > 1) {
+    // (all scaled to the same reference)
     if (hi) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) half[w][i][lane] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-      if (w == 0) sm[0][0][lane].x = L;
+      for (int i = 0; i < 2; ++i)
+        sums[hi - 1][w][i][lane] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+      if (w == 0) lsum[hi][lane] = L;
     }
     __syncthreads();
     if (hi) return;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float4 v = half[w][i][lane];
-      y[4 * i] += v.x;
-      y[4 * i + 1] += v.y;
-      y[4 * i + 2] += v.z;
-      y[4 * i + 3] += v.w;
+    for (int h = 1; h < SETS; ++h) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float4 v = sums[h - 1][w][i][lane];
+        y[4 * i] += v.x;
+        y[4 * i + 1] += v.y;
+        y[4 * i + 2] += v.z;
+        y[4 * i + 3] += v.w;
+      }
+      L += lsum[h][lane];
     }
-    L += sm[0][0][lane].x;
   }
   const float inv = L > 0.0f ? a.value_scale / L : 0.0f;
 #pragma unroll
@@ -1179,10 +1184,13 @@ cudaError_t launch_prefix_decode(const PrefixCall& c, cudaStream_t st) {
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(m.um.Hkv * ((m.rows + 7) / 8)));
-  // past 16 partials a second set of warps shares them (36 partials, 512 rows: 9.9 -> 8.0 us; with 10
-  // it would cost 7.3 -> 10.0)
-  const bool two = m.partials + m.own_splits > 16;
-  cfg.blockDim = dim3(two ? 256 : 128);
+  // Sets of warps that share a row's partials: more where there are many partials or the CTAs are
+  // few.  Calls of 64 CTAs with 26 partials take 28.5 us with four sets, 28.9 with two; of 192 CTAs
+  // with 13 partials 24.8 with two, 26.8 with one; of 512 CTAs with 9 partials 51.3 with two,
+  // 49.2 with one.
+  const int all = m.partials + m.own_splits, ctas = (int)cfg.gridDim.x;
+  const int sets = all > 16 ? (ctas <= c.num_sms ? 4 : 2) : (all > 8 && ctas <= 2 * c.num_sms ? 2 : 1);
+  cfg.blockDim = dim3(128 * sets);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1190,7 +1198,7 @@ cudaError_t launch_prefix_decode(const PrefixCall& c, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;  // a dependent of this call's own kernels; without any it waits for nothing it needs
   if (c.prefix_len < 1 && c.own.max_blocks < 1) cfg.numAttrs = 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, two ? k_prefix_merge<2> : k_prefix_merge<1>, m);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, sets == 4 ? k_prefix_merge<4> : sets == 2 ? k_prefix_merge<2> : k_prefix_merge<1>, m);
   count_launch();
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
