@@ -78,6 +78,8 @@ constexpr int kPNormSlots = 4;                   // tiles whose norms and masks 
 constexpr float kPSlack = 14.0f;                 // log2 units u + et may exceed a row's reference
 constexpr float kPShift = 1.0f;                  // P is at most 2^15
 constexpr int kPMinExp = -60;                    // smallest et: values below are as good as zero
+constexpr int kPRowSpread = 6;                   // rows of Q this much (log2) below the CTA's largest share its exponent
+constexpr int kPRowMin = -120;                   // the least difference that is told apart
 
 // Shared memory (byte offsets): operands of 32 KB -- the streams' Q in 0 and 1; low parts of
 // Q in 2 and 3 when two tiles of rows have them (of one tile: in 1); K in two stages; V in
@@ -91,8 +93,9 @@ constexpr uint32_t kPOffLo = kPOffHi + kPNormSlots * 16;             // bf16 [sl
 constexpr uint32_t kPOffBar = kPOffLo + kPNormSlots * 16;
 constexpr int kPBars = 2 + 2 + 2 + 2 + 2 * kPNormSlots + 2 + 2 + 2;
 constexpr uint32_t kPOffTmem = kPOffBar + kPBars * 8;
-constexpr uint32_t kPOffMax = kPOffTmem + 4;                         // u32: largest |q|
-constexpr uint32_t kPSmem = kPOffTmem + 8;
+constexpr uint32_t kPOffMax = kPOffTmem + 4;                         // u32: largest finite |q|
+constexpr uint32_t kPOffRow = kPOffMax + 4;                          // s8 [256]: a row's exponent less the CTA's
+constexpr uint32_t kPSmem = kPOffRow + 2 * kPTile;
 static_assert(kPSmem <= 232448, "the shared memory of one CTA an SM");
 
 struct PrefixArgs {
@@ -254,17 +257,21 @@ __device__ __forceinline__ void store_half(const HalfRecord<F>& r, uint32_t dst,
 
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
+// 2^e, -126 <= e <= 127.
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
 // Rows of Q, a quad of lanes a row, lane q holding coordinates [32 q, 32 q + 32).  load_q
-// keeps the CTA's rows as loaded and returns the largest magnitude; place_q rotates them for
-// packed keys, scales them by `inv` (a power of two) and writes fp16 parts (bf16 layers:
-// bf16 as they are) to the operands.
+// keeps the CTA's rows as loaded, each with its largest magnitude (of a row that is not finite:
+// zero), and returns the largest of all; place_q rotates them for packed keys, scales them by a
+// power of two and writes fp16 parts (bf16 layers: bf16 as they are) to the operands.
 template <bool BF16>
 struct QRows {
   uint32_t w[2][BF16 ? 16 : 32];
+  uint32_t top[2];  // bits of the row's largest magnitude
 };
 template <bool BF16>
-__device__ __forceinline__ float load_q(QRows<BF16>& x, const PrefixArgs& a, int kvh, int r0, int warp, int lane) {
-  uint32_t mx = 0u;
+__device__ __forceinline__ uint32_t load_q(QRows<BF16>& x, const PrefixArgs& a, int kvh, int r0, int warp, int lane) {
+  uint32_t all = 0u;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     if (h == 1 && !a.pair) break;
@@ -281,17 +288,30 @@ __device__ __forceinline__ float load_q(QRows<BF16>& x, const PrefixArgs& a, int
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     if (h == 1 && !a.pair) break;
+    uint32_t mx = 0u;
 #pragma unroll
     for (int i = 0; i < (BF16 ? 16 : 32); ++i) {
       if (BF16) mx = max(mx, max(x.w[h][i] << 16 & 0x7FFF0000u, x.w[h][i] & 0x7FFF0000u));
       else mx = max(mx, x.w[h][i] & 0x7FFFFFFFu);
     }
+    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    x.top[h] = mx < 0x7F800000u ? mx : 0u;
+    all = max(all, x.top[h]);
   }
-  return __uint_as_float(mx);
+  return all;
 }
+// Exponent e of a power of two above a row's largest magnitude, with `spare` bits to grow.
+__device__ __forceinline__ int row_exponent(uint32_t top, int spare) {
+  return min(max((int)(top >> 23) - 126 + spare, -120), 120);
+}
+// `qe`: the exponent of the CTA's largest row.  Rows up to kPRowSpread below share it (their parts
+// keep 2^-14 of the row's largest value or better); one far below takes its own, and the softmax
+// scales its logits back (`down`: its exponent less qe).  A row that is not finite stays by itself:
+// its products meet no other row.
 template <int KF, bool BF16>
-__device__ __forceinline__ void place_q(const QRows<BF16>& q, const PrefixArgs& a, int r0, uint32_t base, float inv,
-                                        uint32_t signs, int warp, int lane) {
+__device__ __forceinline__ void place_q(const QRows<BF16>& q, const PrefixArgs& a, int r0, uint32_t base, int qe, int spare,
+                                        int8_t* down, uint32_t signs, int warp, int lane) {
   const int quad = lane & 3;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -300,6 +320,14 @@ __device__ __forceinline__ void place_q(const QRows<BF16>& q, const PrefixArgs& 
     if (r0 + h * kPTile + 8 * warp >= a.rows) break;
     const int tr = 8 * warp + (lane >> 2);
     const bool live = r0 + h * kPTile + tr < a.rows;
+    int d = 0;
+    if (KF != 0) {
+      if (live && q.top[h] != 0u) d = max(row_exponent(q.top[h], spare) - qe, kPRowMin);
+      if (d >= -kPRowSpread) d = 0;
+      if (quad == 0) down[h * kPTile + tr] = (int8_t)d;
+    }
+    // (a negative sm_scale turns the queries, so that every g is positive)
+    const float inv = (a.scale < 0.0f ? -1.0f : 1.0f) * exp2i(-(qe + d));
     float x[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
@@ -409,7 +437,8 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
     *qmax = 0u;
   }
   __syncthreads();
-  // the CTA's rows of Q, by one power of two (2^qe > largest |q|; |Pi q| may be 11.4 times it)
+  // the CTA's rows of Q by powers of two (2^qe > largest |q|; |Pi q| may be 11.4 times it)
+  int8_t* const down = reinterpret_cast<int8_t*>(gen + kPOffRow);
   float qscale = 1.0f;
   {
     constexpr int kSpare = KF >= 2 && KF <= 4 ? 4 : 0;
@@ -424,8 +453,8 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
 #pragma unroll
         for (int k = 0; k < 4; ++k) sv[k] = __ldg(a.rot + 32 * k + lane);
       }
-      const float mx = a.q_bf16 ? load_q<true>(q16, a, kvh, r0, warp, lane) : load_q<false>(q32, a, kvh, r0, warp, lane);
-      const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
+      const uint32_t mx = a.q_bf16 ? load_q<true>(q16, a, kvh, r0, warp, lane) : load_q<false>(q32, a, kvh, r0, warp, lane);
+      const uint32_t m = __reduce_max_sync(0xffffffffu, mx);
       if (lane == 0) atomicMax(qmax, m);
       if (KF >= 2 && KF <= 4) {
 #pragma unroll
@@ -443,13 +472,11 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
       if (128 * lane < vpage) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.vpool + page * vpage + 128 * lane));
     }
     __syncthreads();
-    const int qe = KF == 0 ? 0 : min(max((int)(*qmax >> 23) - 126 + kSpare, -100), 100);
-    qscale = __uint_as_float((uint32_t)(127 + qe) << 23);
-    // (a negative sm_scale turns the queries, so that every g is positive)
-    const float inv = (a.scale < 0.0f ? -1.0f : 1.0f) * __uint_as_float((uint32_t)(127 - qe) << 23);
+    const int qe = KF == 0 ? 0 : row_exponent(*qmax, kSpare);
+    qscale = exp2i(qe);
     if (stages) {
-      if (a.q_bf16) place_q<KF, true>(q16, a, r0, base, inv, signs, warp, lane);
-      else place_q<KF, false>(q32, a, r0, base, inv, signs, warp, lane);
+      if (a.q_bf16) place_q<KF, true>(q16, a, r0, base, qe, kSpare, down, signs, warp, lane);
+      else place_q<KF, false>(q32, a, r0, base, qe, kSpare, down, signs, warp, lane);
     }
   }
   const float rs = fmaxf(fabsf(a.scale) * qscale, 1e-30f);  // log2-logit of an S of one
@@ -472,6 +499,11 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
     const int count = s ? count1 : count0;
     const int trow = a.pair ? s * kPTile + 32 * w : 32 * w;  // the warp's first row of the CTA's rows
     const bool live = r0 + trow < a.rows;  // (whole warps of padding rows only take part in the barriers)
+    // the row's power of two: FP8 keys' logits take it with their common factor, coded keys' in the
+    // pass below, which few warps need
+    const int rd = KF != 0 && r0 + trow + lane < a.rows ? (int)down[trow + lane] : 0;
+    const bool scaled = kCodedK && __any_sync(0xffffffffu, rd != 0);
+    const float rsr = KF == 8 ? fmaxf(rs * exp2i(rd), 1e-30f) : rs;
     float C = -INFINITY, l = 0.0f;  // reference of u + et; sum of 2^(u - C + shift)
     for (int i = 0; i < count && ok; ++i) {
       const int t = a.pair ? i : 2 * i + s, slot = t & (kPNormSlots - 1);
@@ -488,14 +520,16 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
         const uint32_t em2 = __vmaxs4(em, em >> 16), em3 = __vmaxs4(em2, em2 >> 8);
         const int et = (int)(int8_t)(em3 & 255u);
         uint32_t ra[32], rb[32];
-        if ((mw.x & mw.y & mw.z & mw.w) != 0xFFFFFFFFu) {  // logits of the tile's masked tokens to -inf
+        if (scaled || (mw.x & mw.y & mw.z & mw.w) != 0xFFFFFFFFu) {
+          // logits of the tile's masked tokens to -inf, of rows with an exponent of their own to the CTA's
+          const float f = kCodedK ? exp2i(rd) : 1.0f;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             const uint32_t bits = c == 0 ? mw.x : (c == 1 ? mw.y : (c == 2 ? mw.z : mw.w));
             tmem_ld32_async(ts + 32 * c, ra);
             tmem_wait_ld32(ra);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) ra[k] = (bits >> k) & 1u ? ra[k] : 0xFF800000u;
+            for (int k = 0; k < 32; ++k) ra[k] = (bits >> k) & 1u ? __float_as_uint(__uint_as_float(ra[k]) * f) : 0xFF800000u;
             tmem_st32(ts + 32 * c, ra);
           }
           tmem_wait_st();
@@ -528,7 +562,7 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
           const uint32_t g16 = m > 0.0f ? max(hm & 0xFFFFu, hm >> 16) : min(hm & 0xFFFFu, hm >> 16);
           m = m == -INFINITY ? m : m * __uint_as_float(g16 << 16);
         } else {
-          m *= rs;
+          m *= rsr;
         }
         if (__any_sync(0xffffffffu, m + (float)et > C + kPSlack)) {
           if constexpr (kCodedK) {  // the exact maximum
@@ -571,7 +605,7 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
           for (int k = 0; k < 8; ++k) {
             float2 u0 = make_float2(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]));
             float2 u1 = make_float2(__uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3]));
-            const float4 g = kCodedK ? g4[8 * c + k] : make_float4(rs, rs, rs, rs);
+            const float4 g = kCodedK ? g4[8 * c + k] : make_float4(rsr, rsr, rsr, rsr);
             u0 = __ffma2_rn(u0, make_float2(g.x, g.y), make_float2(-off, -off));
             u1 = __ffma2_rn(u1, make_float2(g.z, g.w), make_float2(-off, -off));
             u0 = make_float2(ex2(u0.x), ex2(u0.y));
