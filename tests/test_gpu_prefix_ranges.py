@@ -52,3 +52,19 @@ def test_query_rows_of_every_size(cuda, tqlib, fmt, bk, bv):
     q *= cuda.from_numpy((2.0 ** e).astype(np.float32)).cuda()
     out = run(cuda, tqlib, case, P, cuda.float32).cpu().numpy()
     assert max_rel_err(out, reference(case, P)) <= TOL
+
+
+@pytest.mark.parametrize("fmt,bk,bv", FORMATS)
+@pytest.mark.parametrize("P,width", [(300, None), (0, None), (300, 0), (300, 140)])
+def test_rows_that_are_not_finite_say_so(cuda, tqlib, fmt, bk, bv, P, width):
+    """The softmax of NaN logits is NaN, not an empty row's zeros: by the prefix kernel, the own tokens'
+    and both, next to a sequence without any token."""
+    lens = [0, 0, 0] if width == 0 else [9, 40, 0]
+    case = build(cuda, tqlib, fmt, bk, bv, B=3, hq=4, hkv=2, P=P, lens=lens, seed=4, width=width)
+    q = case[1]
+    q[0, 1], q[1, 2, 77] = float("nan"), float("inf")
+    out = run(cuda, tqlib, case, P, cuda.float32)
+    assert bool(out[0, 1].isnan().all()) and bool(out[1, 2].isnan().all())
+    out[0, 1], out[1, 2] = 0.0, 0.0
+    assert bool(out.isfinite().all())
+    assert P > 0 or bool((out[2] == 0).all())

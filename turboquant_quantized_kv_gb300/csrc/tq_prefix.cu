@@ -642,8 +642,8 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
     if (live) {  // a lane a row: 16-byte pieces of 32 rows next to each other, one warp store 512 bytes
       const int64_t pi = a.pair ? blockIdx.y : 2 * blockIdx.y + s;
       const int64_t tile = (pi * a.Hkv + kvh) * a.row_tiles + (r0 + trow) / 32;
-      const bool any = ok && C != -INFINITY;
-      a.ml[tile * 32 + lane] = any ? make_float2(C - kPShift, l) : make_float2(-INFINITY, 0.0f);
+      // (logits that are all NaN leave C where it was, and a sum that says so)
+      a.ml[tile * 32 + lane] = ok ? make_float2(C - kPShift, l) : make_float2(-INFINITY, 0.0f);
       if (ok && count > 0) {
         uint4* const o = reinterpret_cast<uint4*>(a.part + tile * (32 * kD)) + lane;
         uint32_t ra[32];
@@ -975,7 +975,7 @@ __global__ void __launch_bounds__(SETS * 128) k_prefix_merge(const __grid_consta
       L += lsum[h][lane];
     }
   }
-  const float inv = L > 0.0f ? a.value_scale / L : 0.0f;
+  const float inv = L == 0.0f ? 0.0f : a.value_scale / L;  // (zero: no token; NaN stays)
 #pragma unroll
   for (int i = 0; i < 8; ++i) y[i] *= inv;
   if (a.rot) {  // Pi^T y = D H y / sqrt(d)
