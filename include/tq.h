@@ -433,6 +433,9 @@ size_t tq_prefix_workspace_bytes(const tq_cache_desc* desc, int batch, int num_q
  * [0, num_blocks) is skipped and recorded (TQ_DEV_BAD_BLOCK).  The other arguments, the
  * workspace contract (at least tq_prefix_workspace_bytes(...), zero before the first
  * call) and errors as for tq_decode_attention; one workspace serves both calls.
+ * A row of q or a token's value that is larger than the others' by any factor, or not
+ * finite, costs no other row and no other token its precision; norms of coded values
+ * below 2^-60 may count as zero.
  * bf16, k8v4 and packed layers with a Hadamard rotation and without QJL keys
  * (TQ_ERR_UNSUPPORTED otherwise). */
 tq_status tq_prefix_decode(const tq_cache_desc* desc, const void* q, int q_dtype, int batch, int num_q_heads,

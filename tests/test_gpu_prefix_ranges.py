@@ -68,3 +68,61 @@ def test_rows_that_are_not_finite_say_so(cuda, tqlib, fmt, bk, bv, P, width):
     out[0, 1], out[1, 2] = 0.0, 0.0
     assert bool(out.isfinite().all())
     assert P > 0 or bool((out[2] == 0).all())
+
+
+def graded(cuda, tq, fmt, bk, bv, *, P, own, outlier, small=False, B=3, hq=4, seed=0):
+    """Two kinds of tokens in every block: ordinary ones, and every fifth with values `outlier` times as
+    large that no query attends (logits 60 below); small: those are the ones attended (logits 60
+    above), and the ordinary ones' values the large ones.  P prefix tokens, `own` of each sequence."""
+    g = workloads.rng(seed)
+    pb, width = -(-P // 16), -(-own // 16)
+    ids = g.permutation(pb + B * width + 1).astype(np.int32)
+    ptab, table = ids[:pb], ids[pb:pb + B * width].reshape(B, width)
+    layer = tq.Layer(len(ids), 1, kv_format=fmt, bits_k=bk, bits_v=bv, seed=seed, fill=0xFF)
+    slots = [ptab[np.arange(P) // 16].astype(np.int64) * 16 + np.arange(P) % 16]
+    slots = np.concatenate(slots + [t[np.arange(own) // 16].astype(np.int64) * 16 + np.arange(own) % 16 for t in table])
+    base = g.standard_normal(D)
+    rare = np.arange(len(slots)) % 5 == 2
+    k = 0.1 * g.standard_normal((len(slots), D)) + np.where(rare, 5.5 if small else -5.5, 0.0)[:, None] * base
+    v = g.standard_normal((len(slots), D)) * np.where(rare ^ small, outlier, 1.0)[:, None]
+    to = lambda x: cuda.from_numpy(x.astype(np.float32)).cuda()
+    layer.append(to(k[:, None]), to(v[:, None]), cuda.from_numpy(slots).cuda())
+    q = to(base + 0.1 * g.standard_normal((B, hq, D))).to(cuda.bfloat16)
+    return layer, q, ptab, table, np.full(B, own, np.int32)
+
+
+@pytest.mark.parametrize("P,own", [(300, 0), (300, 40), (0, 40)])
+@pytest.mark.parametrize("small", [False, True])
+@pytest.mark.parametrize("outlier", [2.0 ** 10, 2.0 ** 17, 2.0 ** 24, 2.0 ** 80])
+def test_bf16_values_of_every_size(cuda, tqlib, P, own, small, outlier):
+    case = graded(cuda, tqlib, "bf16", 4, 4, P=P, own=own, outlier=outlier, small=small)
+    out = run(cuda, tqlib, case, P, cuda.float32).cpu().numpy()
+    assert max_rel_err(out, reference(case, P)) <= TOL
+
+
+@pytest.mark.parametrize("B", [2, 70])
+def test_bf16_channels_of_every_size(cuda, tqlib, B):
+    """Channels from 2^-60 to 1, and one with an infinite element: each keeps its own precision."""
+    P, hq = 400, 4
+    layer, q, ptab, table, lens = case = build(cuda, tqlib, "bf16", 4, 4, B=B, hq=hq, hkv=1, P=P, lens=[0] * B, seed=8)
+    size = cuda.from_numpy(2.0 ** -workloads.rng(1).integers(0, 61, D).astype(np.float32)).cuda()
+    pool = layer.v_cache.view(cuda.bfloat16).view(-1, D)
+    pool.copy_(cuda.where(pool.isfinite(), pool * size, pool))
+    ref = reference(case, P)
+    pool[int(ptab[3]) * 16 + 2, 17] = float("inf")
+    out = run(cuda, tqlib, case, P, cuda.float32).cpu().numpy()
+    assert not np.any(np.isfinite(out[..., 17]))
+    rest = np.arange(D) != 17
+    # of a channel's largest result: weights to 2^-16, sums in fp32
+    err = np.abs(out - ref)[..., rest].max((0, 1)) / np.abs(ref)[..., rest].max((0, 1))
+    assert err.max() <= TOL
+
+
+@pytest.mark.parametrize("fmt,bk,bv", FORMATS[1:])
+@pytest.mark.parametrize("small", [False, True])
+@pytest.mark.parametrize("B", [3, 70])
+@pytest.mark.parametrize("outlier", [2.0 ** 10, 2.0 ** 17, 2.0 ** 24, 2.0 ** 60])
+def test_coded_values_of_every_size(cuda, tqlib, fmt, bk, bv, small, B, outlier):
+    case = graded(cuda, tqlib, fmt, bk, bv, P=300, own=0, outlier=outlier, small=small, B=B)
+    out = run(cuda, tqlib, case, 300, cuda.float32).cpu().numpy()
+    assert max_rel_err(out, reference(case, 300)) <= TOL

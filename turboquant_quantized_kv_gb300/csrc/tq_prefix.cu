@@ -23,8 +23,9 @@
 //   8 softmax warps   a thread a row: the maximum of its 128 logits from tensor memory, then
 //                     base-2 weights, written back as 16-bit P over S.
 // Scales.  A tile's values are normalised by a power of two 2^et above its norms, so that V's
-// operand and P both fit fp16 whatever the norms are; a row keeps one reference C for
-// weight times value, and P = 2^(u + et - C + shift) for a log2-logit u = g_t s_t, where g_t
+// operand and P both fit fp16; a tile whose norms lie far apart (wide, see TileRange) takes a power
+// of two for each coded token, or bf16 values as they are, so that a large value that nobody attends
+// costs the others nothing; a row keeps one reference C for weight times value, and P = 2^(u + et - C + shift) for a log2-logit u = g_t s_t, where g_t
 // holds the key's norm and every scale.  C moves, and the accumulator is rescaled, only when
 // a row's largest u + et exceeds it by 14; whether it may is decided from the largest raw
 // logit and the tile's largest and smallest g, the exact maximum being taken only then.
@@ -39,7 +40,7 @@
 // 3-bit one 2.3e-4 -> 1.0e-4); the logits' scale and the merge undo it.  The own tokens'
 // decode gets the same tables.  Weights and values go to fp16 (half a step 2^-11 each), also
 // in bf16 layers, where bf16 weights would cost a result up to 6e-3 of its row's largest
-// value.  Sums, maxima and denominators are fp32.
+// value (over wide tiles they go in as two bf16 parts).  Sums, maxima and denominators are fp32.
 //
 // What bounds it.  With few rows the prefix's bytes would (8192 tokens, 8 heads, 4 bits: 2.7 us),
 // but a CTA's start, first loads and end are 8 us and its chain of steps comes on top: 16 us for
@@ -77,7 +78,11 @@ constexpr uint32_t kPOperand = 2 * kPPanel;      // a 128 x 128 operand
 constexpr int kPNormSlots = 4;                   // tiles whose norms and masks are kept
 constexpr float kPSlack = 14.0f;                 // log2 units u + et may exceed a row's reference
 constexpr float kPShift = 1.0f;                  // P is at most 2^15
-constexpr int kPMinExp = -60;                    // smallest et: values below are as good as zero
+constexpr int kPMinExp = -60;                    // smallest et
+// Exponents of a tile's values may lie this far apart for them to share one (see TileRange): of the
+// tokens' norms, of bf16 values
+template <int VF>
+constexpr int kPSpread = VF == 0 ? 12 : 8;
 constexpr int kPRowSpread = 6;                   // rows of Q this much (log2) below the CTA's largest share its exponent
 constexpr int kPRowMin = -120;                   // the least difference that is told apart
 
@@ -87,8 +92,8 @@ constexpr int kPRowMin = -120;                   // the least difference that is
 constexpr int kPOperands = 7;
 constexpr uint32_t kPOffG = kPOperands * kPOperand;                  // float [slots][128]: g_t
 constexpr uint32_t kPOffMask = kPOffG + kPNormSlots * kPTile * 4;    // u16 [slots][8]
-constexpr uint32_t kPOffExp = kPOffMask + kPNormSlots * 16;          // s8 [slots][8]: et of each block
-constexpr uint32_t kPOffHi = kPOffExp + kPNormSlots * 8;             // bf16 [slots][8]: upper bounds of g
+constexpr uint32_t kPOffExp = kPOffMask + kPNormSlots * 16;          // s8 [slots][2][8]: see TileRange
+constexpr uint32_t kPOffHi = kPOffExp + kPNormSlots * 16;            // bf16 [slots][8]: upper bounds of g
 constexpr uint32_t kPOffLo = kPOffHi + kPNormSlots * 16;             // bf16 [slots][8]: lower bounds of g
 constexpr uint32_t kPOffBar = kPOffLo + kPNormSlots * 16;
 constexpr int kPBars = 2 + 2 + 2 + 2 + 2 * kPNormSlots + 2 + 2 + 2;
@@ -191,12 +196,56 @@ __device__ __forceinline__ void load_half(HalfRecord<F>& r, const uint8_t* page,
   r.gamma = __ldg(reinterpret_cast<const float*>(page + kBlock * 2 * B) + tok);
 }
 
-// Exponent e with every magnitude of the lane's half of a bf16 token below 2^e.
-__device__ __forceinline__ int range_of(const HalfRecord<0>& r) {
-  uint32_t m = 0u;
+// Exponents of the lane's part of a block of bf16 values: hi with every magnitude below 2^hi, lo the
+// least such exponent of a piece (eight channels of a token) or of a channel (of the lane's eight
+// tokens) that is not all zeros; 127 when there is none.
+__device__ __forceinline__ int2 range_of(const HalfRecord<0>& r) {
+  uint32_t ch[4] = {0u, 0u, 0u, 0u}, least = 0xFFFFFFFFu;  // (a zero wraps to the top)
 #pragma unroll
-  for (int i = 0; i < HalfRecord<0>::kWords; ++i) m = __vmaxu2(m, r.w[i] & 0x7FFF7FFFu);
-  return (int)(max(m & 0xFFFFu, m >> 16) >> 7) - 126;
+  for (int i = 0; i < 8; ++i) {
+    uint32_t x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      x[k] = r.w[4 * i + k] & 0x7FFF7FFFu;
+      ch[k] = __vmaxu2(ch[k], x[k]);
+    }
+    const uint32_t m = __vmaxu2(__vmaxu2(x[0], x[1]), __vmaxu2(x[2], x[3]));
+    least = min(least, max(m & 0xFFFFu, m >> 16) - 1u);
+  }
+  uint32_t most = 0u;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t a = ch[k] & 0xFFFFu, b = ch[k] >> 16;
+    most = max(most, max(a, b));
+    least = min(least, min(a - 1u, b - 1u));
+  }
+  return make_int2((int)(most >> 7) - 126, least == 0xFFFFFFFFu ? 127 : (int)((least + 1u) >> 7) - 126);
+}
+
+// What a tile's values have in common, from its blocks' exponents.  The exponent et lies above all of
+// them (or is kPMinExp); a tile is wide when lo, the least exponent of a token that is not zero (bf16
+// layers: of a piece or channel, see range_of), is more than kPSpread below it.  The values of a
+// tile that is not wide share et: their fp16 form is off by 2^-11 of a value or, below the normal
+// range, by 2^-25 of 2^et, 2^-16 of the token's norm (bf16: 2^-12 of the channel's and of the piece's
+// largest value).
+struct TileRange {
+  int et, lo;
+  bool wide;
+};
+template <int VF>
+__device__ __forceinline__ TileRange tile_range(const unsigned char* at) {
+  const uint4 w = *reinterpret_cast<const uint4*>(at);
+  const uint32_t a = __vmaxs4(w.x, w.y), b = __vmins4(w.z, w.w);
+  const uint32_t a2 = __vmaxs4(a, a >> 16), b2 = __vmins4(b, b >> 16);
+  TileRange r;
+  r.et = (int)(int8_t)(__vmaxs4(a2, a2 >> 8) & 255u);
+  r.lo = (int)(int8_t)(__vmins4(b2, b2 >> 8) & 255u);
+  r.wide = r.et - r.lo > kPSpread<VF>;
+  return r;
+}
+// The exponent of a norm, within what et may be: gamma < 2^e.
+__device__ __forceinline__ int norm_exponent(float gamma) {
+  return min(max((int)((__float_as_uint(gamma) >> 23) & 255u) - 126, kPMinExp), 126);
 }
 // Eight bf16 values times a power of two, as fp16.
 __device__ __forceinline__ uint4 scaled_half8(const uint4& v, float inv) {
@@ -213,10 +262,10 @@ __device__ __forceinline__ uint4 scaled_half8(const uint4& v, float inv) {
 
 // The lane's share of block w to the operand at `dst`: panel = half of the head, row = token
 // of the tile, 16-byte chunk c at c ^ (row & 7).  Values (VALUES) times `scale`: codes by
-// the token's scaled norm, bf16 values by a power of two.
+// the token's scaled norm, bf16 values by a power of two (`raw`: as they are).
 template <int F, bool VALUES>
 __device__ __forceinline__ void store_half(const HalfRecord<F>& r, uint32_t dst, int w, int lane, const HalfTable& t,
-                                           float scale) {
+                                           float scale, bool raw = false) {
   auto put = [&](const uint4& v, int row, int panel, int c) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst + (uint32_t)panel * kPPanel + (uint32_t)row * 128u +
                                                                (uint32_t)((c ^ (row & 7)) << 4)),
@@ -227,7 +276,7 @@ __device__ __forceinline__ void store_half(const HalfRecord<F>& r, uint32_t dst,
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       uint4 v = chunk_of<F>(r, i, t);
-      if constexpr (VALUES) v = scaled_half8(v, scale);
+      if (VALUES && !raw) v = scaled_half8(v, scale);
       put(v, w * kBlock + piece_token<F>(i, lane), (lane >> 3) & 1, lane & 7);
     }
   } else if constexpr (F == 8) {
@@ -376,6 +425,56 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// The softmax of one row over a wide tile of bf16 values (see TileRange), which few prefixes have: the
+// values go in as they are and P = 2^(u - C + shift) in two bf16 parts, next to each other for each
+// 16 tokens.  C lies low enough (by lo) for what the row attends.  `first`: nothing is accumulated.
+// Returns the new C and l.
+__device__ __forceinline__ float2 wide_bf16_tile(uint32_t ts, uint32_t to, float rs, int lo, bool first, float C, float l) {
+  uint32_t r[32];
+  float m = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    tmem_ld32_async(ts + 32 * c, r);
+    tmem_wait_ld32(r);
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) m = max3(m, __uint_as_float(r[k]), __uint_as_float(r[k + 1]));
+  }
+  const float nc = fmaxf(C, m * rs + (float)max(lo, kPMinExp));
+  const float f = C == -INFINITY ? 0.0f : exp2f(C - nc);
+  l *= f;
+  if (!first) {
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      tmem_ld32_async(to + 32 * c, r);
+      tmem_wait_ld32(r);
+#pragma unroll
+      for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * f);
+      tmem_st32(to + 32 * c, r);
+    }
+  }
+  const float off = (nc == -INFINITY ? 0.0f : nc) - kPShift;
+  float sum = 0.0f;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    tmem_ld32_async(ts + 32 * c, r);
+    tmem_wait_ld32(r);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t p[16];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float u0 = ex2(fmaf(__uint_as_float(r[16 * h + 2 * k]), rs, -off));
+        const float u1 = ex2(fmaf(__uint_as_float(r[16 * h + 2 * k + 1]), rs, -off));
+        sum += u0 + u1;
+        p[k] = pack_b2(u0, u1);
+        p[8 + k] = pack_b2(u0 - __uint_as_float(p[k] << 16), u1 - __uint_as_float(p[k] & 0xFFFF0000u));
+      }
+      tmem_st16(ts + 32 * c + 16 * h, p);  // over logits that have been read
+    }
+  }
+  return make_float2(nc, l + sum);
+}
+
 // --------------------------------------------------------------- the kernel
 
 template <int KF, int VF>
@@ -515,12 +614,11 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
       if (live) {
         const uint4 mw = *reinterpret_cast<const uint4*>(gen + kPOffMask + slot * 16);
         const float4* g4 = reinterpret_cast<const float4*>(gs + slot * kPTile);
-        const uint2 ew = *reinterpret_cast<const uint2*>(gen + kPOffExp + slot * 8);
-        const uint32_t em = __vmaxs4(ew.x, ew.y);
-        const uint32_t em2 = __vmaxs4(em, em >> 16), em3 = __vmaxs4(em2, em2 >> 8);
-        const int et = (int)(int8_t)(em3 & 255u);
+        const TileRange range = tile_range<VF>(gen + kPOffExp + slot * 16);
+        const int et = range.et;
+        const float to_l = VF != 0 && range.wide ? 0.0f : exp2i(-et);  // the denominator's terms of a P of one
         uint32_t ra[32], rb[32];
-        if (scaled || (mw.x & mw.y & mw.z & mw.w) != 0xFFFFFFFFu) {
+        if (scaled || (kCodedV && range.wide) || (mw.x & mw.y & mw.z & mw.w) != 0xFFFFFFFFu) {
           // logits of the tile's masked tokens to -inf, of rows with an exponent of their own to the CTA's
           const float f = kCodedK ? exp2i(rd) : 1.0f;
 #pragma unroll 1
@@ -533,103 +631,170 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
             tmem_st32(ts + 32 * c, ra);
           }
           tmem_wait_st();
-        }
-        float m0 = -INFINITY, m1 = -INFINITY;
-        auto raw_max = [&](const uint32_t(&r)[32]) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            m0 = max3(m0, __uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]));
-            m1 = max3(m1, __uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3]));
-          }
-        };
-        tmem_ld32_async(ts, ra);
-        tmem_wait_ld32(ra);
-        tmem_ld32_async(ts + 32, rb);
-        raw_max(ra);
-        tmem_wait_ld32(rb);
-        tmem_ld32_async(ts + 64, ra);
-        raw_max(rb);
-        tmem_wait_ld32(ra);
-        tmem_ld32_async(ts + 96, rb);
-        raw_max(ra);
-        tmem_wait_ld32(rb);
-        raw_max(rb);
-        float m = fmaxf(m0, m1);
-        if constexpr (kCodedK) {  // no u of the row exceeds this
-          const uint4 h = *reinterpret_cast<const uint4*>(gen + (m > 0.0f ? kPOffHi : kPOffLo) + slot * 16);
-          const uint32_t hm = m > 0.0f ? __vmaxu2(__vmaxu2(h.x, h.y), __vmaxu2(h.z, h.w))
-                                       : __vminu2(__vminu2(h.x, h.y), __vminu2(h.z, h.w));
-          const uint32_t g16 = m > 0.0f ? max(hm & 0xFFFFu, hm >> 16) : min(hm & 0xFFFFu, hm >> 16);
-          m = m == -INFINITY ? m : m * __uint_as_float(g16 << 16);
-        } else {
-          m *= rsr;
-        }
-        if (__any_sync(0xffffffffu, m + (float)et > C + kPSlack)) {
-          if constexpr (kCodedK) {  // the exact maximum
-            m = -INFINITY;
+          if (kCodedV && range.wide) {
+            // A coded token's value shares its own exponent e instead of the tile's, read again from the norms
+            // of its page.  The row's reference and denominator are brought up to date here, and a logit
+            // becomes u + e - et, for the steps below to make P = 2^(u + e - C + shift) of it.
+            auto exponents = [&](int c, int k) {  // of tokens 32 c + 4 k .. 32 c + 4 k + 3
+              float4 e = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              const int blk = (tile0 + t) * kPBlocks + 2 * c + (k >> 2), id = blk < pblocks ? __ldg(a.table + blk) : -1;
+              if (id >= 0 && id < a.num_blocks) {
+                const uint8_t* page = a.vpool + ((int64_t)id * a.Hkv + kvh) * vpage;
+                const float4 v = __ldg(reinterpret_cast<const float4*>(page + kBlock * kD * VF / 8) + (k & 3));
+                e = make_float4((float)norm_exponent(v.x), (float)norm_exponent(v.y), (float)norm_exponent(v.z),
+                                (float)norm_exponent(v.w));
+              }
+              return e;
+            };
+            float m = -INFINITY;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               tmem_ld32_async(ts + 32 * c, ra);
               tmem_wait_ld32(ra);
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
-                const float4 g = g4[8 * c + k];
-                m = max3(m, __uint_as_float(ra[4 * k]) * g.x, __uint_as_float(ra[4 * k + 1]) * g.y);
-                m = max3(m, __uint_as_float(ra[4 * k + 2]) * g.z, __uint_as_float(ra[4 * k + 3]) * g.w);
+                const float4 g = kCodedK ? g4[8 * c + k] : make_float4(rsr, rsr, rsr, rsr), e = exponents(c, k);
+                m = max3(m, fmaf(__uint_as_float(ra[4 * k]), g.x, e.x), fmaf(__uint_as_float(ra[4 * k + 1]), g.y, e.y));
+                m = max3(m, fmaf(__uint_as_float(ra[4 * k + 2]), g.z, e.z), fmaf(__uint_as_float(ra[4 * k + 3]), g.w, e.w));
               }
             }
-          }
-          const float nc = fmaxf(C, m + (float)et);
-          const float f = C == -INFINITY ? 0.0f : exp2f(C - nc);
-          if (__any_sync(0xffffffffu, nc != C)) {
-            l *= f;
-            if (i > 0) {  // rescale the accumulator (the last product into it is complete: it precedes S)
+            const float nc = fmaxf(C, m), fc = C == -INFINITY ? 0.0f : exp2f(C - nc);
+            C = nc;
+            l *= fc;
+            if (i > 0) {
 #pragma unroll 1
               for (int c = 0; c < 4; ++c) {
                 tmem_ld32_async(to + 32 * c, ra);
                 tmem_wait_ld32(ra);
 #pragma unroll
-                for (int k = 0; k < 32; ++k) ra[k] = __float_as_uint(__uint_as_float(ra[k]) * f);
+                for (int k = 0; k < 32; ++k) ra[k] = __float_as_uint(__uint_as_float(ra[k]) * fc);
                 tmem_st32(to + 32 * c, ra);
               }
             }
-            C = nc;
+            const float ref = (C == -INFINITY ? 0.0f : C) - kPShift;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              tmem_ld32_async(ts + 32 * c, ra);
+              tmem_wait_ld32(ra);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float4 g = kCodedK ? g4[8 * c + k] : make_float4(rsr, rsr, rsr, rsr), e = exponents(c, k);
+                auto turn = [&](uint32_t& x, float gx, float ex) {
+                  l += ex2(fmaf(__uint_as_float(x), gx, -ref));
+                  x = __float_as_uint(__uint_as_float(x) + (ex - (float)et) / gx);
+                };
+                turn(ra[4 * k], g.x, e.x);
+                turn(ra[4 * k + 1], g.y, e.y);
+                turn(ra[4 * k + 2], g.z, e.z);
+                turn(ra[4 * k + 3], g.w, e.w);
+              }
+              tmem_st32(ts + 32 * c, ra);
+            }
+            tmem_wait_st();
           }
         }
-        // P = 2^(u + et - C + shift); the denominator's terms are P 2^-et
-        const float off = (C == -INFINITY ? 0.0f : C) - kPShift - (float)et;
-        float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
-        auto weights = [&](uint32_t(&r)[32], int c) {
-          uint32_t p[16];
+        if (VF == 0 && range.wide) {
+          const float2 n2 = wide_bf16_tile(ts, to, rsr, range.lo, i == 0, C, l);
+          C = n2.x;
+          l = n2.y;
+        } else {
+          float m0 = -INFINITY, m1 = -INFINITY;
+          auto raw_max = [&](const uint32_t(&r)[32]) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            float2 u0 = make_float2(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]));
-            float2 u1 = make_float2(__uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3]));
-            const float4 g = kCodedK ? g4[8 * c + k] : make_float4(rsr, rsr, rsr, rsr);
-            u0 = __ffma2_rn(u0, make_float2(g.x, g.y), make_float2(-off, -off));
-            u1 = __ffma2_rn(u1, make_float2(g.z, g.w), make_float2(-off, -off));
-            u0 = make_float2(ex2(u0.x), ex2(u0.y));
-            u1 = make_float2(ex2(u1.x), ex2(u1.y));
-            sum0 = __fadd2_rn(sum0, u0);
-            sum1 = __fadd2_rn(sum1, u1);
-            p[2 * k] = pack_h2(u0.x, u0.y);
-            p[2 * k + 1] = pack_h2(u1.x, u1.y);
+            for (int k = 0; k < 8; ++k) {
+              m0 = max3(m0, __uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]));
+              m1 = max3(m1, __uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3]));
+            }
+          };
+          tmem_ld32_async(ts, ra);
+          tmem_wait_ld32(ra);
+          tmem_ld32_async(ts + 32, rb);
+          raw_max(ra);
+          tmem_wait_ld32(rb);
+          tmem_ld32_async(ts + 64, ra);
+          raw_max(rb);
+          tmem_wait_ld32(ra);
+          tmem_ld32_async(ts + 96, rb);
+          raw_max(ra);
+          tmem_wait_ld32(rb);
+          raw_max(rb);
+          float m = fmaxf(m0, m1);
+          if constexpr (kCodedK) {  // no u of the row exceeds this
+            const uint4 h = *reinterpret_cast<const uint4*>(gen + (m > 0.0f ? kPOffHi : kPOffLo) + slot * 16);
+            const uint32_t hm = m > 0.0f ? __vmaxu2(__vmaxu2(h.x, h.y), __vmaxu2(h.z, h.w))
+                                         : __vminu2(__vminu2(h.x, h.y), __vminu2(h.z, h.w));
+            const uint32_t g16 = m > 0.0f ? max(hm & 0xFFFFu, hm >> 16) : min(hm & 0xFFFFu, hm >> 16);
+            m = m == -INFINITY ? m : m * __uint_as_float(g16 << 16);
+          } else {
+            m *= rsr;
           }
-          tmem_st16(ts + 16 * c, p);  // over logits that have been read
-        };
-        tmem_ld32_async(ts, ra);
-        tmem_wait_ld32(ra);
-        tmem_ld32_async(ts + 32, rb);
-        weights(ra, 0);
-        tmem_wait_ld32(rb);
-        tmem_ld32_async(ts + 64, ra);
-        weights(rb, 1);
-        tmem_wait_ld32(ra);
-        tmem_ld32_async(ts + 96, rb);
-        weights(ra, 2);
-        tmem_wait_ld32(rb);
-        weights(rb, 3);
-        l = fmaf((sum0.x + sum0.y) + (sum1.x + sum1.y), __uint_as_float((uint32_t)(127 - et) << 23), l);
+          if (__any_sync(0xffffffffu, m + (float)et > C + kPSlack)) {
+            if constexpr (kCodedK) {  // the exact maximum
+              m = -INFINITY;
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                tmem_ld32_async(ts + 32 * c, ra);
+                tmem_wait_ld32(ra);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const float4 g = g4[8 * c + k];
+                  m = max3(m, __uint_as_float(ra[4 * k]) * g.x, __uint_as_float(ra[4 * k + 1]) * g.y);
+                  m = max3(m, __uint_as_float(ra[4 * k + 2]) * g.z, __uint_as_float(ra[4 * k + 3]) * g.w);
+                }
+              }
+            }
+            const float nc = fmaxf(C, m + (float)et);
+            const float f = C == -INFINITY ? 0.0f : exp2f(C - nc);
+            if (__any_sync(0xffffffffu, nc != C)) {
+              l *= f;
+              if (i > 0) {  // rescale the accumulator (the last product into it is complete: it precedes S)
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                  tmem_ld32_async(to + 32 * c, ra);
+                  tmem_wait_ld32(ra);
+#pragma unroll
+                  for (int k = 0; k < 32; ++k) ra[k] = __float_as_uint(__uint_as_float(ra[k]) * f);
+                  tmem_st32(to + 32 * c, ra);
+                }
+              }
+              C = nc;
+            }
+          }
+          // P = 2^(u + et - C + shift); the denominator's terms are P 2^-et
+          const float off = (C == -INFINITY ? 0.0f : C) - kPShift - (float)et;
+          float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
+          auto weights = [&](uint32_t(&r)[32], int c) {
+            uint32_t p[16];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              float2 u0 = make_float2(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]));
+              float2 u1 = make_float2(__uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3]));
+              const float4 g = kCodedK ? g4[8 * c + k] : make_float4(rsr, rsr, rsr, rsr);
+              u0 = __ffma2_rn(u0, make_float2(g.x, g.y), make_float2(-off, -off));
+              u1 = __ffma2_rn(u1, make_float2(g.z, g.w), make_float2(-off, -off));
+              u0 = make_float2(ex2(u0.x), ex2(u0.y));
+              u1 = make_float2(ex2(u1.x), ex2(u1.y));
+              sum0 = __fadd2_rn(sum0, u0);
+              sum1 = __fadd2_rn(sum1, u1);
+              p[2 * k] = pack_h2(u0.x, u0.y);
+              p[2 * k + 1] = pack_h2(u1.x, u1.y);
+            }
+            tmem_st16(ts + 16 * c, p);  // over logits that have been read
+          };
+          tmem_ld32_async(ts, ra);
+          tmem_wait_ld32(ra);
+          tmem_ld32_async(ts + 32, rb);
+          weights(ra, 0);
+          tmem_wait_ld32(rb);
+          tmem_ld32_async(ts + 64, ra);
+          weights(rb, 1);
+          tmem_wait_ld32(ra);
+          tmem_ld32_async(ts + 96, rb);
+          weights(ra, 2);
+          tmem_wait_ld32(rb);
+          weights(rb, 3);
+          l = fmaf((sum0.x + sum0.y) + (sum1.x + sum1.y), to_l, l);
+        }
         tmem_wait_st();
         tc_fence_before();
       }
@@ -693,7 +858,8 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
       if (t >= 2 && !__all_sync(0xffffffffu, mbar_wait(kempty + st, ((t >> 1) & 1) ^ 1))) return false;
       if constexpr (kCodedK) {
         const bool valid = tok < live;
-        const float g = valid ? rs * rk.gamma : 1.0f;  // (a masked logit is -inf: not times zero)
+        float g = valid ? rs * rk.gamma : 1.0f;  // (a masked logit is -inf: not times zero)
+        if (g < 1e-30f) g = 1e-30f;              // (what it scales is less than 2^13; wide tiles divide by it)
         if (half == 0) gs[slot * kPTile + w * kBlock + tok] = g;
         // bounds, in bf16 above and below (norms are not negative)
         const uint32_t hi = __reduce_max_sync(0xffffffffu, valid ? __float_as_uint(g) : 0u);
@@ -722,12 +888,17 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
     for (int t = 0; t < n && ok; ++t) {
       const int slot = t & (kPNormSlots - 1);
       const int id2 = block_id(t + 2);
-      // the exponent of the block's values: all tokens of the tile get the largest
-      int e = kPMinExp;
+      // the exponents of the block's values
+      int2 e = make_int2(kPMinExp, 127);
       if constexpr (VF == 0) e = range_of(rv);
-      else if (tok < tokens(t, id)) e = (int)((__float_as_uint(rv.gamma) >> 23) & 255u) - 126;  // gamma < 2^e
-      e = __reduce_max_sync(0xffffffffu, min(max(e, kPMinExp), 126));
-      if (lane == 0) reinterpret_cast<int8_t*>(gen + kPOffExp)[slot * 8 + w] = (int8_t)e;
+      else if (tok < tokens(t, id) && rv.gamma != 0.0f) e.x = e.y = norm_exponent(rv.gamma);
+      e.x = __reduce_max_sync(0xffffffffu, min(max(e.x, kPMinExp), 126));
+      e.y = __reduce_min_sync(0xffffffffu, e.y);
+      if (lane == 0) {
+        int8_t* const at = reinterpret_cast<int8_t*>(gen + kPOffExp) + slot * 16 + w;
+        at[0] = (int8_t)e.x;
+        at[8] = (int8_t)e.y;
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(efull + slot);
       // the next tile's K goes ahead of this tile's V: the tensor cores want it first
@@ -736,11 +907,10 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
       if (t >= a.v_stages) ok = mbar_wait(vempty + vstage(t), vturn(t) ^ 1);
       ok = __all_sync(0xffffffffu, ok && mbar_wait(efull + slot, (t / kPNormSlots) & 1));
       if (!ok) break;
-      const uint2 ew = *reinterpret_cast<const uint2*>(gen + kPOffExp + slot * 8);
-      const uint32_t em = __vmaxs4(ew.x, ew.y);
-      const uint32_t em2 = __vmaxs4(em, em >> 16), em3 = __vmaxs4(em2, em2 >> 8);
-      const float down = __uint_as_float((uint32_t)(127 - (int)(int8_t)(em3 & 255u)) << 23);  // 2^-et
-      store_half<VF, true>(rv, v_op + (uint32_t)vstage(t) * kPOperand, w, lane, tv, VF == 0 ? down : down * rv.gamma);
+      const TileRange range = tile_range<VF>(gen + kPOffExp + slot * 16);
+      const float down_by = exp2i(-(VF != 0 && range.wide ? norm_exponent(rv.gamma) : range.et));
+      store_half<VF, true>(rv, v_op + (uint32_t)vstage(t) * kPOperand, w, lane, tv, VF == 0 ? down_by : down_by * rv.gamma,
+                           VF == 0 && range.wide);
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(vfull + vstage(t));
@@ -788,7 +958,7 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
     const bool issue = elect_one();
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     constexpr uint32_t idesc_s = umma_idesc_16(KF == 0, false, kPTile, kPTile);
-    constexpr uint32_t idesc_o = umma_idesc_16(false, true, kPTile, kPTile);
+    constexpr uint32_t idesc_o = umma_idesc_16(false, true, kPTile, kPTile), idesc_raw = umma_idesc_16(true, true, kPTile, kPTile);
     const uint64_t dq = umma_desc_sw128(base), dk = umma_desc_sw128(k_op);
     const uint64_t dv = umma_desc_sw128_mn(v_op, kPPanel);
     auto tile_of = [&](int i, int s) { return a.pair ? i : 2 * i + s; };
@@ -821,14 +991,28 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
     };
     auto values = [&](int i, int s) {  // O_s += P_s V
       const int t = tile_of(i, s), st = vstage(t);
+      bool raw = false;
+      if constexpr (VF == 0) {  // (read while the weights are under way)
+        if (!__all_sync(0xffffffffu, mbar_wait(efull + (t & (kPNormSlots - 1)), (t / kPNormSlots) & 1))) return false;
+        raw = tile_range<VF>(gen + kPOffExp + (t & (kPNormSlots - 1)) * 16).wide;
+      }
       if (!__all_sync(0xffffffffu, mbar_wait(pfull + s, i & 1) && mbar_wait(vfull + st, vturn(t)))) return false;
       tc_fence_after();
       const uint64_t v = dv + (uint64_t)(st * (kPOperand >> 4));
       const uint32_t d = tm + (uint32_t)((2 + s) * kPTile), p = tm + (uint32_t)(s * kPTile);
-      if (issue) {
-#pragma unroll
+      if (issue && raw) {
+#pragma unroll 1
         for (int j = 0; j < 8; ++j)
-          umma_16_ts(d, p + (uint32_t)(8 * j), v + (uint64_t)(j * (16 * 128 >> 4)), idesc_o, i > 0 || j > 0);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            umma_16_ts(d, p + (uint32_t)(16 * j + 8 * h), v + (uint64_t)(j * (16 * 128 >> 4)), idesc_raw, i > 0 || j > 0 || h > 0);
+      }
+      if (issue) {
+        if (!raw) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            umma_16_ts(d, p + (uint32_t)(8 * j), v + (uint64_t)(j * (16 * 128 >> 4)), idesc_o, i > 0 || j > 0);
+        }
         if (!a.pair || s == 1) umma_commit(smem_u32(vempty + st));
         if (i + 1 == (s ? count1 : count0)) umma_commit(smem_u32(odone + s));
       }
