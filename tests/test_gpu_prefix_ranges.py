@@ -126,3 +126,14 @@ def test_coded_values_of_every_size(cuda, tqlib, fmt, bk, bv, small, B, outlier)
     case = graded(cuda, tqlib, fmt, bk, bv, P=300, own=0, outlier=outlier, small=small, B=B)
     out = run(cuda, tqlib, case, 300, cuda.float32).cpu().numpy()
     assert max_rel_err(out, reference(case, 300)) <= TOL
+
+
+@pytest.mark.parametrize("fmt,bk,bv", FORMATS)
+@pytest.mark.parametrize("small", [False, True])
+@pytest.mark.parametrize("P,own", [(0, 40), (300, 40), (0, 300), (20, 2100)])
+@pytest.mark.parametrize("outlier", [2.0 ** 17, 2.0 ** 60])
+def test_own_values_of_every_size(cuda, tqlib, fmt, bk, bv, small, P, own, outlier):
+    """(20, 2100): a block table for the decode kernel."""
+    case = graded(cuda, tqlib, fmt, bk, bv, P=P, own=own, outlier=outlier, small=small)
+    out = run(cuda, tqlib, case, P, cuda.float32).cpu().numpy()
+    assert max_rel_err(out, reference(case, P)) <= TOL

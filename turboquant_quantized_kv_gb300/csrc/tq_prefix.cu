@@ -78,7 +78,6 @@ constexpr uint32_t kPOperand = 2 * kPPanel;      // a 128 x 128 operand
 constexpr int kPNormSlots = 4;                   // tiles whose norms and masks are kept
 constexpr float kPSlack = 14.0f;                 // log2 units u + et may exceed a row's reference
 constexpr float kPShift = 1.0f;                  // P is at most 2^15
-constexpr int kPMinExp = -60;                    // smallest et
 // Exponents of a tile's values may lie this far apart for them to share one (see TileRange): of the
 // tokens' norms, of bf16 values
 template <int VF>
@@ -223,7 +222,7 @@ __device__ __forceinline__ int2 range_of(const HalfRecord<0>& r) {
 }
 
 // What a tile's values have in common, from its blocks' exponents.  The exponent et lies above all of
-// them (or is kPMinExp); a tile is wide when lo, the least exponent of a token that is not zero (bf16
+// them (or is kMinExp); a tile is wide when lo, the least exponent of a token that is not zero (bf16
 // layers: of a piece or channel, see range_of), is more than kPSpread below it.  The values of a
 // tile that is not wide share et: their fp16 form is off by 2^-11 of a value or, below the normal
 // range, by 2^-25 of 2^et, 2^-16 of the token's norm (bf16: 2^-12 of the channel's and of the piece's
@@ -242,10 +241,6 @@ __device__ __forceinline__ TileRange tile_range(const unsigned char* at) {
   r.lo = (int)(int8_t)(__vmins4(b2, b2 >> 8) & 255u);
   r.wide = r.et - r.lo > kPSpread<VF>;
   return r;
-}
-// The exponent of a norm, within what et may be: gamma < 2^e.
-__device__ __forceinline__ int norm_exponent(float gamma) {
-  return min(max((int)((__float_as_uint(gamma) >> 23) & 255u) - 126, kPMinExp), 126);
 }
 // Eight bf16 values times a power of two, as fp16.
 __device__ __forceinline__ uint4 scaled_half8(const uint4& v, float inv) {
@@ -439,7 +434,7 @@ __device__ __forceinline__ float2 wide_bf16_tile(uint32_t ts, uint32_t to, float
 #pragma unroll
     for (int k = 0; k < 32; k += 2) m = max3(m, __uint_as_float(r[k]), __uint_as_float(r[k + 1]));
   }
-  const float nc = fmaxf(C, m * rs + (float)max(lo, kPMinExp));
+  const float nc = fmaxf(C, m * rs + (float)max(lo, kMinExp));
   const float f = C == -INFINITY ? 0.0f : exp2f(C - nc);
   l *= f;
   if (!first) {
@@ -889,10 +884,10 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
       const int slot = t & (kPNormSlots - 1);
       const int id2 = block_id(t + 2);
       // the exponents of the block's values
-      int2 e = make_int2(kPMinExp, 127);
+      int2 e = make_int2(kMinExp, 127);
       if constexpr (VF == 0) e = range_of(rv);
       else if (tok < tokens(t, id) && rv.gamma != 0.0f) e.x = e.y = norm_exponent(rv.gamma);
-      e.x = __reduce_max_sync(0xffffffffu, min(max(e.x, kPMinExp), 126));
+      e.x = __reduce_max_sync(0xffffffffu, min(max(e.x, kMinExp), 126));
       e.y = __reduce_min_sync(0xffffffffu, e.y);
       if (lane == 0) {
         int8_t* const at = reinterpret_cast<int8_t*>(gen + kPOffExp) + slot * 16 + w;

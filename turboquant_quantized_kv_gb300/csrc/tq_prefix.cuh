@@ -89,6 +89,12 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// The exponent of a norm: gamma < 2^e, e from kMinExp on (norms below count as zero).
+constexpr int kMinExp = -60;
+__device__ __forceinline__ int norm_exponent(float gamma) {
+  return min(max((int)((__float_as_uint(gamma) >> 23) & 255u) - 126, kMinExp), 126);
+}
+
 // One validated decode over the sequences' own tokens that leaves partials (see DecodeWorkspace):
 // launched when the block table is at most kOwnMaxBlocks wide.
 constexpr int kOwnMaxBlocks = 128;

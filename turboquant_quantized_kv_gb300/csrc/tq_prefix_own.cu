@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kOwnWarps * 32, KF == 0 ? 3 : 4) k_own(const _
   if constexpr (kCodedK) tk = half_table<(kCodedK ? KF : 4)>(a.cbk);
   if constexpr (kCodedV) tv = half_table<(kCodedV ? VF : 4)>(a.cbv);
 
-  float C = -INFINITY, l = 0.0f;  // reference of log2 weight plus the norms' exponent; sum of 2^(u - C + shift)
+  float C = -INFINITY, l = 0.0f;  // reference of log2 weight plus the norm's exponent; sum of 2^(u - C + shift)
   // tile i holds rows 2 tig and 2 tig + 1 of coordinates 16 g_ + 2 i and 16 g_ + 2 i + 1 (bf16 pieces:
   // 8 g_ + 2 i for i < 4, 64 + 8 g_ + 2 i - 8 from there)
   float acc[8][4];
@@ -293,19 +293,20 @@ __global__ void __launch_bounds__(kOwnWarps * 32, KF == 0 ? 3 : 4) k_own(const _
     float2 u[2];
     u[0] = make_float2((s0[0] + s0[2]) * rs * gk[0].x, (s0[1] + s0[3]) * rs * gk[0].y);
     u[1] = make_float2((s1[0] + s1[2]) * rs * gk[1].x, (s1[1] + s1[3]) * rs * gk[1].y);
-    float et = 0.0f;
-    if constexpr (kCodedV) {
-      const float mg = fmaxf(fmaxf(gv[0].x, gv[0].y), fmaxf(gv[1].x, gv[1].y));
-      const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(mg));
-      et = (float)max((int)(m >> 23) - 126, -60);
-    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (2 * tig + 8 * h >= live) u[h].x = -INFINITY;
       if (2 * tig + 1 + 8 * h >= live) u[h].y = -INFINITY;
     }
-    const float m = quad_max(fmaxf(fmaxf(u[0].x, u[0].y), fmaxf(u[1].x, u[1].y)));
-    const float nc = fmaxf(C, m + et);
+    // (weight times norm is what the row's reference follows: a large value that it does not attend
+    // leaves the others their bits)
+    float2 e[2] = {};
+    if constexpr (kCodedV) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) e[h] = make_float2((float)norm_exponent(gv[h].x), (float)norm_exponent(gv[h].y));
+    }
+    const float m = quad_max(fmaxf(fmaxf(u[0].x + e[0].x, u[0].y + e[0].y), fmaxf(u[1].x + e[1].x, u[1].y + e[1].y)));
+    const float nc = fmaxf(C, m);
     if (__any_sync(0xffffffffu, nc > C)) {
       const float f = C == -INFINITY ? 0.0f : ex2(C - nc);
       l *= f;
