@@ -137,3 +137,22 @@ def test_own_values_of_every_size(cuda, tqlib, fmt, bk, bv, small, P, own, outli
     case = graded(cuda, tqlib, fmt, bk, bv, P=P, own=own, outlier=outlier, small=small)
     out = run(cuda, tqlib, case, P, cuda.float32).cpu().numpy()
     assert max_rel_err(out, reference(case, P)) <= TOL
+
+
+@pytest.mark.parametrize("fmt,bk,bv", FORMATS)
+@pytest.mark.parametrize("P,own,at", [(300, 0, 150), (300, 40, 150), (300, 40, 310), (0, 40, 10), (20, 2100, 100)])
+def test_logits_of_every_size(cuda, tqlib, fmt, bk, bv, P, own, at):
+    """Rows whose largest logit is from 2^6 to 2^110, more than an fp32 of the size of 2^24 can tell apart
+    in units: token `at` (of the first sequence's tokens, its own behind the prefix's) has it by far, and
+    the result is its value."""
+    B, hq = 3, 24
+    layer, q, ptab, table, lens = case = graded(cuda, tqlib, fmt, bk, bv, P=P, own=own, outlier=1.0, B=B, hq=hq)
+    q0 = q[:, :1].double().mean(0, keepdim=True)
+    slots = [int(ptab[at // 16]) * 16 + at % 16] if at < P else [int(t[(at - P) // 16]) * 16 + (at - P) % 16 for t in table]
+    k = (4.0 * q0).float().expand(len(slots), 1, D).contiguous()
+    layer.append(k, cuda.randn(len(slots), 1, D, device="cuda"), cuda.tensor(slots, device="cuda"))
+    e = np.linspace(0, 104, hq).astype(int)
+    q = (q0 * cuda.from_numpy(2.0 ** e[:, None]).cuda()).expand(B, hq, D).float().contiguous()
+    case = layer, q, ptab, table, lens
+    out = run(cuda, tqlib, case, P, cuda.float32).cpu().numpy()
+    assert max_rel_err(out, reference(case, P)) <= TOL

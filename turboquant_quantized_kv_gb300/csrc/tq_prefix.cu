@@ -78,6 +78,9 @@ constexpr uint32_t kPOperand = 2 * kPPanel;      // a 128 x 128 operand
 constexpr int kPNormSlots = 4;                   // tiles whose norms and masks are kept
 constexpr float kPSlack = 14.0f;                 // log2 units u + et may exceed a row's reference
 constexpr float kPShift = 1.0f;                  // P is at most 2^15
+// Logits of this size (log2 units) lose bits in units: the reference follows them without slack, and
+// P is formed from the rounded logit, the one that the reference is the largest of.
+constexpr float kPLarge = 1048576.0f;
 // Exponents of a tile's values may lie this far apart for them to share one (see TileRange): of the
 // tokens' norms, of bf16 values
 template <int VF>
@@ -434,7 +437,7 @@ __device__ __forceinline__ float2 wide_bf16_tile(uint32_t ts, uint32_t to, float
 #pragma unroll
     for (int k = 0; k < 32; k += 2) m = max3(m, __uint_as_float(r[k]), __uint_as_float(r[k + 1]));
   }
-  const float nc = fmaxf(C, m * rs + (float)max(lo, kMinExp));
+  const float nc = fmaxf(C, __fadd_rn(__fmul_rn(m, rs), (float)max(lo, kMinExp)));
   const float f = C == -INFINITY ? 0.0f : exp2f(C - nc);
   l *= f;
   if (!first) {
@@ -458,8 +461,8 @@ __device__ __forceinline__ float2 wide_bf16_tile(uint32_t ts, uint32_t to, float
       uint32_t p[16];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float u0 = ex2(fmaf(__uint_as_float(r[16 * h + 2 * k]), rs, -off));
-        const float u1 = ex2(fmaf(__uint_as_float(r[16 * h + 2 * k + 1]), rs, -off));
+        const float u0 = ex2(__fmul_rn(__uint_as_float(r[16 * h + 2 * k]), rs) - off);
+        const float u1 = ex2(__fmul_rn(__uint_as_float(r[16 * h + 2 * k + 1]), rs) - off);
         sum += u0 + u1;
         p[k] = pack_b2(u0, u1);
         p[8 + k] = pack_b2(u0 - __uint_as_float(p[k] << 16), u1 - __uint_as_float(p[k] & 0xFFFF0000u));
@@ -649,8 +652,9 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
                 const float4 g = kCodedK ? g4[8 * c + k] : make_float4(rsr, rsr, rsr, rsr), e = exponents(c, k);
-                m = max3(m, fmaf(__uint_as_float(ra[4 * k]), g.x, e.x), fmaf(__uint_as_float(ra[4 * k + 1]), g.y, e.y));
-                m = max3(m, fmaf(__uint_as_float(ra[4 * k + 2]), g.z, e.z), fmaf(__uint_as_float(ra[4 * k + 3]), g.w, e.w));
+                auto top = [](uint32_t x, float gx, float ex) { return __fadd_rn(__fmul_rn(__uint_as_float(x), gx), ex); };
+                m = max3(m, top(ra[4 * k], g.x, e.x), top(ra[4 * k + 1], g.y, e.y));
+                m = max3(m, top(ra[4 * k + 2], g.z, e.z), top(ra[4 * k + 3], g.w, e.w));
               }
             }
             const float nc = fmaxf(C, m), fc = C == -INFINITY ? 0.0f : exp2f(C - nc);
@@ -675,7 +679,7 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
               for (int k = 0; k < 8; ++k) {
                 const float4 g = kCodedK ? g4[8 * c + k] : make_float4(rsr, rsr, rsr, rsr), e = exponents(c, k);
                 auto turn = [&](uint32_t& x, float gx, float ex) {
-                  l += ex2(fmaf(__uint_as_float(x), gx, -ref));
+                  l += ex2(__fmul_rn(__uint_as_float(x), gx) - ref);
                   x = __float_as_uint(__uint_as_float(x) + (ex - (float)et) / gx);
                 };
                 turn(ra[4 * k], g.x, e.x);
@@ -721,9 +725,9 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
             const uint32_t g16 = m > 0.0f ? max(hm & 0xFFFFu, hm >> 16) : min(hm & 0xFFFFu, hm >> 16);
             m = m == -INFINITY ? m : m * __uint_as_float(g16 << 16);
           } else {
-            m *= rsr;
+            m = __fmul_rn(m, rsr);
           }
-          if (__any_sync(0xffffffffu, m + (float)et > C + kPSlack)) {
+          if (__any_sync(0xffffffffu, m + (float)et > C + (fabsf(C) > kPLarge ? 0.0f : kPSlack))) {
             if constexpr (kCodedK) {  // the exact maximum
               m = -INFINITY;
 #pragma unroll 1
@@ -776,18 +780,42 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
             }
             tmem_st16(ts + 16 * c, p);  // over logits that have been read
           };
-          tmem_ld32_async(ts, ra);
-          tmem_wait_ld32(ra);
-          tmem_ld32_async(ts + 32, rb);
-          weights(ra, 0);
-          tmem_wait_ld32(rb);
-          tmem_ld32_async(ts + 64, ra);
-          weights(rb, 1);
-          tmem_wait_ld32(ra);
-          tmem_ld32_async(ts + 96, rb);
-          weights(ra, 2);
-          tmem_wait_ld32(rb);
-          weights(rb, 3);
+          if (__any_sync(0xffffffffu, fabsf(C) > kPLarge && C != -INFINITY)) {
+            const float ref = (C == -INFINITY ? 0.0f : C) - kPShift;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              tmem_ld32_async(ts + 32 * c, ra);
+              tmem_wait_ld32(ra);
+              uint32_t p[16];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float4 g = kCodedK ? g4[8 * c + k] : make_float4(rsr, rsr, rsr, rsr);
+                auto weight = [&](uint32_t x, float gx) {
+                  return ex2(fminf(__fadd_rn(__fmul_rn(__uint_as_float(x), gx), (float)et) - ref, kPSlack + kPShift));
+                };
+                const float2 u0 = make_float2(weight(ra[4 * k], g.x), weight(ra[4 * k + 1], g.y));
+                const float2 u1 = make_float2(weight(ra[4 * k + 2], g.z), weight(ra[4 * k + 3], g.w));
+                sum0 = __fadd2_rn(sum0, u0);
+                sum1 = __fadd2_rn(sum1, u1);
+                p[2 * k] = pack_h2(u0.x, u0.y);
+                p[2 * k + 1] = pack_h2(u1.x, u1.y);
+              }
+              tmem_st16(ts + 16 * c, p);
+            }
+          } else {
+            tmem_ld32_async(ts, ra);
+            tmem_wait_ld32(ra);
+            tmem_ld32_async(ts + 32, rb);
+            weights(ra, 0);
+            tmem_wait_ld32(rb);
+            tmem_ld32_async(ts + 64, ra);
+            weights(rb, 1);
+            tmem_wait_ld32(ra);
+            tmem_ld32_async(ts + 96, rb);
+            weights(ra, 2);
+            tmem_wait_ld32(rb);
+            weights(rb, 3);
+          }
           l = fmaf((sum0.x + sum0.y) + (sum1.x + sum1.y), to_l, l);
         }
         tmem_wait_st();

@@ -26,7 +26,9 @@ namespace tq {
 Codebook codebook_of(const tq_cache_desc& d, int which);
 
 constexpr int kOwnWarps = 4;
-constexpr float kOwnShift = 8.0f;  // weights times norms stay below 2^8
+// Weights times norms stay below 2^7.  (Less than half of 16: the difference of a large reference, whose
+// last bit is 16 or more, and this rounds to the reference.)
+constexpr float kOwnShift = 7.0f;
 
 struct OwnArgs {
   const uint8_t* kpool;
@@ -291,8 +293,9 @@ __global__ void __launch_bounds__(kOwnWarps * 32, KF == 0 ? 3 : 4) k_own(const _
       mma_16n8k16<KF == 0>(s1, qf[2 * c + 1], y.z, y.w);
     }
     float2 u[2];
-    u[0] = make_float2((s0[0] + s0[2]) * rs * gk[0].x, (s0[1] + s0[3]) * rs * gk[0].y);
-    u[1] = make_float2((s1[0] + s1[2]) * rs * gk[1].x, (s1[1] + s1[3]) * rs * gk[1].y);
+    // (rounded, so that the weights below are formed from the values that the reference is the largest of)
+    u[0] = make_float2(__fmul_rn((s0[0] + s0[2]) * rs, gk[0].x), __fmul_rn((s0[1] + s0[3]) * rs, gk[0].y));
+    u[1] = make_float2(__fmul_rn((s1[0] + s1[2]) * rs, gk[1].x), __fmul_rn((s1[1] + s1[3]) * rs, gk[1].y));
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (2 * tig + 8 * h >= live) u[h].x = -INFINITY;
