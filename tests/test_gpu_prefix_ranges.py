@@ -156,3 +156,27 @@ def test_logits_of_every_size(cuda, tqlib, fmt, bk, bv, P, own, at):
     case = layer, q, ptab, table, lens
     out = run(cuda, tqlib, case, P, cuda.float32).cpu().numpy()
     assert max_rel_err(out, reference(case, P)) <= TOL
+
+
+def long_prefix_error(cuda, tq, fmt, P):
+    """Lengths up to the last that is accepted, by a table that names one block again and again: what the
+    block alone gives (a last, partial block changes it by 2^-20).  The values have a mean, so that an
+    accumulator that loses a little at each addition shows."""
+    layer = tq.Layer(2, 1, kv_format=fmt, bits_k=2, bits_v=2, fill=0xFF)
+    g = workloads.rng(5)
+    to = lambda x: cuda.from_numpy(x.astype(np.float32)).cuda()
+    layer.append(to(g.standard_normal((16, 1, D))), to(g.standard_normal((16, 1, D)) + 2.0), cuda.arange(16, 32, device="cuda"))
+    q = to(0.5 * g.standard_normal((1, 2, D)))
+    table = cuda.ones((P + 15) // 16, dtype=cuda.int32, device="cuda")
+    out = layer.prefix_decode(q, table, P, out_dtype=cuda.float32)
+    cuda.cuda.synchronize()
+    assert tq.get_device_status() == 0
+    ref = prefix_attention(q.double().cpu().numpy(), *stands_for(layer), np.array([1]), 16, np.zeros((1, 0), np.int32),
+                           np.zeros(1, np.int32), 1 / math.sqrt(D))
+    return max_rel_err(out.cpu().numpy(), ref)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "packed"])
+@pytest.mark.parametrize("P", [2 ** 31 - 128, 2 ** 24 + 5])
+def test_long_prefixes_keep_their_sums(cuda, tqlib, fmt, P):
+    assert long_prefix_error(cuda, tqlib, fmt, P) <= TOL

@@ -850,7 +850,7 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
     HalfTable tk = {}, tv = {};
     if constexpr (kCodedK) tk = half_table<(kCodedK ? KF : 4)>(a.cbk);
     if constexpr (kCodedV) tv = half_table<(kCodedV ? VF : 4)>(a.cbv);
-    const int blocks = (a.len + kBlock - 1) / kBlock;
+    const int blocks = pblocks;
     auto block_id = [&](int t) {  // the warp's block of the CTA's tile t: its id, -1 past the end
       const int b = (tile0 + t) * kPBlocks + w;
       return t < n && b < blocks ? __ldg(a.table + b) : -1;
@@ -944,7 +944,7 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
   } else if (KF == 0 && warp == kPCopyWarp) {
     // ------------------------------------------------- bf16 keys: tensor copies
     // lane i < 8 has block i of the tile: its mask, and its page in two swizzled boxes
-    const int blocks = (a.len + kBlock - 1) / kBlock;
+    const int blocks = pblocks;
     auto block_id = [&](int t) {
       const int b = (tile0 + t) * kPBlocks + lane;
       return lane < kPBlocks && t < n && b < blocks ? __ldg(a.table + b) : -1;
@@ -1249,7 +1249,10 @@ int own_splits(int max_blocks) { return max_blocks <= kOwnMaxBlocks ? (max_block
 // How the prefix is cut: streams over two tiles of rows (pair) or over tiles of tokens,
 // CTAs over the rows and splits of the tokens.  The splits are chosen so that the CTAs,
 // one an SM, fill whole waves: the fewest tiles in a row over one to four waves, a CTA's
-// start and end counted as three tiles.
+// start and end counted as three tiles.  No CTA takes more than kPMostTiles, though: the tensor
+// cores cut off what does not fit an accumulator, on average half of its last bit for each of
+// eight products a tile, always towards zero (one block repeated 2^27 times came out 5e-2 small
+// with 110,000 tiles a CTA, 3e-3 with 6,900, 2e-5 with 54); the merge's sums round.
 //
 // The own tokens' CTAs (own_ctas of them, a few an SM) run next to the prefix kernel on the SMs
 // that it leaves free.  When some of them would have to follow it, fewer splits may be better:
@@ -1257,6 +1260,7 @@ int own_splits(int max_blocks) { return max_blocks <= kOwnMaxBlocks ? (max_block
 // k_own.  (64 rows, 8192 tokens, 512 CTAs of own tokens: 16 splits 37.4 us, 13 31.0, 11 29.0,
 // 10 31.0.)  Never more splits than without own tokens, so that a workspace made for them
 // serves calls that have none.
+constexpr int64_t kPMostTiles = 1024;
 struct PrefixPlan {
   int pair, row_blocks, splits, tiles_per_split, partials;
 };
@@ -1274,7 +1278,8 @@ static PrefixPlan prefix_plan(const tq_cache_desc& d, int batch, int num_q_heads
   for (int waves = 1; waves <= 4; ++waves) {
     int64_t s = (int64_t)waves * num_sms / units;
     s = s < 1 ? 1 : (s > tiles ? tiles : s);
-    const int64_t per = (tiles + s - 1) / s;
+    int64_t per = (tiles + s - 1) / s;
+    per = per < kPMostTiles ? per : kPMostTiles;
     s = (tiles + per - 1) / per;
     const int64_t w = (units * s + num_sms - 1) / num_sms;
     if (w * (per + 3) < best) {
@@ -1289,6 +1294,7 @@ static PrefixPlan prefix_plan(const tq_cache_desc& d, int batch, int num_q_heads
     float least = INFINITY;
     for (int64_t s = p.splits; s >= 1; --s) {
       const int64_t per = (tiles + s - 1) / s;
+      if (per > kPMostTiles) break;
       s = (tiles + per - 1) / per;
       const float t = tile_us * (float)per + ends_us;
       const int64_t beside = (num_sms - units * s) * per_sm * (int64_t)(t / own_us);
