@@ -180,3 +180,9 @@ def long_prefix_error(cuda, tq, fmt, P):
 @pytest.mark.parametrize("P", [2 ** 31 - 128, 2 ** 24 + 5])
 def test_long_prefixes_keep_their_sums(cuda, tqlib, fmt, P):
     assert long_prefix_error(cuda, tqlib, fmt, P) <= TOL
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "packed"])
+@pytest.mark.parametrize("P", [2 ** 31 - 1, 2 ** 31 - 127])
+def test_the_longest_prefixes(cuda, tqlib, fmt, P):
+    assert long_prefix_error(cuda, tqlib, fmt, P) <= TOL

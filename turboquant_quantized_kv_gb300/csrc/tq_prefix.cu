@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
 
   const int kvh = blockIdx.x / a.row_blocks;
   const int r0 = (blockIdx.x % a.row_blocks) * (a.pair ? 2 * kPTile : kPTile);
-  const int all_tiles = (a.len + kPTile - 1) / kPTile;
+  const int all_tiles = (a.len - 1) / kPTile + 1;  // (up to 2^31 - 1 tokens: sums stay below)
   const int tile0 = blockIdx.y * a.tiles_per_split;
   const int n = max(0, min(a.tiles_per_split, all_tiles - tile0));  // the CTA's tiles of tokens
   // stream s: tiles i (pair) or 2 i + s, i < count(s)
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
   uint32_t* const qmax = reinterpret_cast<uint32_t*>(gen + kPOffMax);
   // the producers' first pages on their way to L2 while Q is staged
   int early[2] = {-1, -1};
-  const int pw = warp - kPSoftWarps, pblocks = (a.len + kBlock - 1) / kBlock;
+  const int pw = warp - kPSoftWarps, pblocks = (a.len - 1) / kBlock + 1;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int blk = (tile0 + t) * kPBlocks + pw;
