@@ -247,6 +247,17 @@ def _heads(t, out, name, n):
     return _byref(Heads(t.data_ptr(), out.data_ptr(), t.shape[1], st[0], st[1], so[0], so[1]))
 
 
+def _check_queries(q, out):
+    """(batch, query heads) of queries [B, H_q, d]; raises for others and for an output of another size
+    (d is read and written whole, whatever the tensors hold)."""
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != TQ_HEAD_DIM:
+        raise ValueError("q must be [batch, query heads, %d], got %s" % (TQ_HEAD_DIM, tuple(shape)))
+    if out is not None and out.shape != shape and out.shape != (shape[0], shape[1] * shape[2]):
+        raise ValueError("out must be %s, got %s" % (tuple(shape), tuple(out.shape)))
+    return shape[0], shape[1]
+
+
 def _index_ptr(t, name, dtype, shape):
     """Device pointer of an index tensor after checking its type and shape."""
     if t.dtype != dtype:
@@ -434,7 +445,7 @@ class Layer:
                workspace=None, stream=None):
         """Decode attention.  q [B, H_q, d]; block_table int32 [B, max_blocks]; context_lens int32 [B]."""
         torch = _torch()
-        bsz, hq, _ = q.shape
+        bsz, hq = _check_queries(q, out)
         max_blocks = int(block_table.shape[1])
         if sm_scale is None:
             sm_scale = 1.0 / math.sqrt(self.head_dim)
@@ -457,7 +468,7 @@ class Layer:
         torch = _torch()
         ref = k if k is not None else v
         n = int(ref.shape[0]) if ref is not None else 0
-        bsz, hq, _ = q.shape
+        bsz, hq = _check_queries(q, out)
         max_blocks = int(block_table.shape[1])
         if sm_scale is None:
             sm_scale = 1.0 / math.sqrt(self.head_dim)
@@ -481,7 +492,7 @@ class Layer:
         tokens, written at position context_lens[b] - 1 of each sequence (context_lens already
         counts them), then decode(q, ...).  Returns out."""
         torch = _torch()
-        bsz, hq, _ = q.shape
+        bsz, hq = _check_queries(q, out)
         max_blocks = int(block_table.shape[1])
         if sm_scale is None:
             sm_scale = 1.0 / math.sqrt(self.head_dim)
@@ -530,9 +541,9 @@ class Layer:
         prefix_table int32 [>= ceil(prefix_len / 16)] blocks of the prefix; block_table int32
         [B, max_blocks] and context_lens int32 [B]: the sequences' own tokens (None: none)."""
         torch = _torch()
-        bsz, hq, _ = q.shape
+        bsz, hq = _check_queries(q, out)
         prefix_len = int(prefix_len)
-        if prefix_len > 0 and (prefix_table.dim() != 1 or prefix_table.shape[0] * TQ_BLOCK_SIZE < prefix_len):
+        if prefix_len > 0 and (prefix_table is None or prefix_table.dim() != 1 or prefix_table.shape[0] * TQ_BLOCK_SIZE < prefix_len):
             raise ValueError("prefix_table must be one row of at least ceil(prefix_len / %d) blocks" % TQ_BLOCK_SIZE)
         max_blocks = 0 if block_table is None else int(block_table.shape[1])
         if max_blocks > 0 and context_lens is None:
