@@ -363,8 +363,9 @@ __device__ __forceinline__ void place_q(const QRows<BF16>& q, const PrefixArgs& 
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     if (h == 1 && !a.pair) break;
-    // (a group of eight rows past the end stays unwritten: a row's products meet no other row)
-    if (r0 + h * kPTile + 8 * warp >= a.rows) break;
+    // (32 rows past the end stay unwritten: no softmax warp looks at their products.  Rows past the end
+    // beside others are zeros: what a warp decides for its rows together must not hang on old contents)
+    if (r0 + h * kPTile + 8 * (warp & ~3) >= a.rows) break;
     const int tr = 8 * warp + (lane >> 2);
     const bool live = r0 + h * kPTile + tr < a.rows;
     int d = 0;
