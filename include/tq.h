@@ -418,7 +418,8 @@ tq_status tq_rope_append(const tq_cache_desc* desc, const tq_rope* rope, const t
                          const tq_heads* v, int in_dtype, const int64_t* positions, const int64_t* slot_mapping,
                          int64_t n_tokens, void* stream);
 
-/* Workspace bytes tq_prefix_decode needs for these sizes; 0 on error. */
+/* Workspace bytes tq_prefix_decode needs for this layer's kind, batch and heads with prefixes up to
+ * prefix_len and block tables up to max_blocks_per_seq wide; 0 on error. */
 size_t tq_prefix_workspace_bytes(const tq_cache_desc* desc, int batch, int num_q_heads, int64_t prefix_len,
                                  int max_blocks_per_seq);
 

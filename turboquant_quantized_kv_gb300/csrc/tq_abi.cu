@@ -416,8 +416,14 @@ size_t tq_prefix_workspace_bytes(const tq_cache_desc* desc, int batch, int num_q
   }
   DeviceInfo di;
   if (device_info(&di) != TQ_OK) return 0;
-  return own_workspace(desc, batch, num_q_heads, max_blocks_per_seq) +
-         prefix_partial_bytes(*desc, batch, num_q_heads, prefix_len, di.num_sms);
+  // the most that any narrower table needs (its splits grow with the width up to the widest table of
+  // short contexts, and again from there), and any shorter prefix
+  size_t own = own_workspace(desc, batch, num_q_heads, max_blocks_per_seq);
+  if (max_blocks_per_seq > widest_own_table()) {
+    const size_t narrow = own_workspace(desc, batch, num_q_heads, widest_own_table());
+    own = narrow > own ? narrow : own;
+  }
+  return own + prefix_partial_bytes_upto(*desc, batch, num_q_heads, prefix_len, di.num_sms);
 }
 
 tq_status tq_prefix_decode(const tq_cache_desc* desc, const void* q, int q_dtype, int batch, int num_q_heads,

@@ -100,8 +100,11 @@ struct PrefixCall {
 // Splits of the own tokens' decode for prepare_decode (0: the automatic choice): short block
 // tables take CTAs of 16 blocks (k_own), longer ones the decode kernel.
 int own_splits(int max_blocks);
+int widest_own_table();  // the widest table for k_own
 // Bytes of the prefix's partials, which follow the workspace of the own tokens' decode.
 size_t prefix_partial_bytes(const tq_cache_desc& d, int batch, int num_q_heads, int64_t prefix_len, int num_sms);
+// The most of any prefix up to this length.
+size_t prefix_partial_bytes_upto(const tq_cache_desc& d, int batch, int num_q_heads, int64_t prefix_len, int num_sms);
 
 // The factor in [1, 2) that leaves the centroids (2^bits, antisymmetric) with the smallest
 // largest relative error when they are rounded to fp16.

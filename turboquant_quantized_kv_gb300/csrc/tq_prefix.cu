@@ -1245,6 +1245,7 @@ __global__ void __launch_bounds__(SETS * 128) k_prefix_merge(const __grid_consta
   }
 }
 
+int widest_own_table() { return kOwnMaxBlocks; }
 int own_splits(int max_blocks) { return max_blocks <= kOwnMaxBlocks ? (max_blocks + kOwnChunk - 1) / kOwnChunk : 0; }
 
 // How the prefix is cut: streams over two tiles of rows (pair) or over tiles of tokens,
@@ -1259,8 +1260,7 @@ int own_splits(int max_blocks) { return max_blocks <= kOwnMaxBlocks ? (max_block
 // that it leaves free.  When some of them would have to follow it, fewer splits may be better:
 // the times below are in us, of a tile, of the prefix kernel's start and end, and of a CTA of
 // k_own.  (64 rows, 8192 tokens, 512 CTAs of own tokens: 16 splits 37.4 us, 13 31.0, 11 29.0,
-// 10 31.0.)  Never more splits than without own tokens, so that a workspace made for them
-// serves calls that have none.
+// 10 31.0.)  Never more splits than without own tokens, which is what the workspace is made for.
 constexpr int64_t kPMostTiles = 1024;
 struct PrefixPlan {
   int pair, row_blocks, splits, tiles_per_split, partials;
@@ -1312,9 +1312,33 @@ static PrefixPlan prefix_plan(const tq_cache_desc& d, int batch, int num_q_heads
   return p;
 }
 
-size_t prefix_partial_bytes(const tq_cache_desc& d, int batch, int num_q_heads, int64_t prefix_len, int num_sms) {
+static size_t partial_bytes(const tq_cache_desc& d, int batch, int num_q_heads, size_t partials) {
   const size_t tiles = ((size_t)batch * (num_q_heads / d.num_kv_heads) + 31) / 32 * d.num_kv_heads;
-  return (size_t)prefix_plan(d, batch, num_q_heads, prefix_len, 0, num_sms).partials * tiles * 32 * (kD + 2) * sizeof(float);
+  return partials * tiles * 32 * (kD + 2) * sizeof(float);
+}
+
+size_t prefix_partial_bytes(const tq_cache_desc& d, int batch, int num_q_heads, int64_t prefix_len, int num_sms) {
+  return partial_bytes(d, batch, num_q_heads, (size_t)prefix_plan(d, batch, num_q_heads, prefix_len, 0, num_sms).partials);
+}
+
+// The most that any prefix up to prefix_len needs.  A plan of w waves has at most w num_sms / units
+// splits, one a tile, or as many as kPMostTiles asks for; and it takes w > 1 waves only where those use
+// the GPU better than one wave, S splits of it, does: w (t / (w num_sms / units) + 3) < t / S + 4 at least.
+size_t prefix_partial_bytes_upto(const tq_cache_desc& d, int batch, int num_q_heads, int64_t prefix_len, int num_sms) {
+  const PrefixPlan p = prefix_plan(d, batch, num_q_heads, prefix_len, 0, num_sms);
+  if (prefix_len < 1) return 0;
+  const int64_t units = (int64_t)p.row_blocks * d.num_kv_heads, tiles = (prefix_len + kPTile - 1) / kPTile;
+  const int64_t one = num_sms / units > 1 ? num_sms / units : 1;
+  int64_t most = (tiles + kPMostTiles - 1) / kPMostTiles;
+  for (int w = 1; w <= 4; ++w) {
+    const int64_t s = w == 1 ? one : w * num_sms / units;
+    if (w > 1 && units <= num_sms && tiles <= kPMostTiles * one &&
+        tiles * (num_sms - one * units) <= (3 * w - 4) * one * num_sms)
+      continue;
+    const int64_t splits = s < tiles ? s : tiles;
+    most = splits > most ? splits : most;
+  }
+  return partial_bytes(d, batch, num_q_heads, (size_t)most * (p.pair ? 1 : 2));
 }
 
 template <int KF, int VF>
