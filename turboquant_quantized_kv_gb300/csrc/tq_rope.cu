@@ -28,6 +28,7 @@
 // values in place of full shuffles spills at two CTAs an SM: 195 us).
 #include <cuda_fp8.h>
 
+#include <atomic>
 #include <cmath>
 
 #include "tq_async.cuh"
@@ -44,6 +45,8 @@ constexpr int kPairs = kD / 2;
 constexpr int kCsRow = kPairs + kPairs / 16;
 __host__ __device__ __forceinline__ constexpr int cs_at(int pair) { return pair + (pair >> 4); }
 constexpr int kVecTile = kRThreads / 4;  // coded vectors per tile: four lanes each
+constexpr int kMostTileTok = 8;          // tokens a tile of rows
+constexpr int kMostCodedTok = 8;         // tokens that a warp's eight coded vectors can touch
 
 // Where rows of one tensor come from and go to.
 struct RopeRows {
@@ -661,7 +664,7 @@ static void fill_common(RopeArgs& a, const RopeCall& c) {
 // spread: 12,345 tokens of 40 heads 51 us, with four 48.)
 static int rows_tile(const RopeArgs& a, int num_sms) {
   int t = 1;
-  while (t < 8 && t * a.heads * (kPairs / 8) < 4 * kRThreads && a.n_tok / (2 * t) >= 8 * (int64_t)num_sms) t *= 2;
+  while (t < kMostTileTok && t * a.heads * (kPairs / 8) < 4 * kRThreads && a.n_tok / (2 * t) >= 8 * (int64_t)num_sms) t *= 2;
   return t;
 }
 
@@ -696,9 +699,17 @@ static cudaError_t run_append(const RopeArgs& a, unsigned grid, bool pdl, cudaSt
   const int coded = (a.coded[0].tiles > 0) + (a.coded[1].tiles > 0);
   const size_t tok = (size_t)a.tile_tok + (coded ? kRThreads / 32 * (size_t)a.coded_tok : 0);
   const size_t smem = kPairs * 8 + tok * kCsRow * 8 + (coded ? 16384 + coded * kLutQBytes : 0);
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // the limit is the kernel's, for every thread of the process: the most any call needs, once a device
+  constexpr size_t kMost = kPairs * 8 + (kMostTileTok + kRThreads / 32 * kMostCodedTok) * kCsRow * 8 + 16384 + 2 * kLutQBytes;
+  static std::atomic<uint64_t> ready[2];  // [wide]: devices (up to 64) whose kernel has it
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(ready[wide].load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
     if (e != cudaSuccess) return e;
+    ready[wide].fetch_or(bit, std::memory_order_release);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
@@ -710,7 +721,7 @@ static cudaError_t run_append(const RopeArgs& a, unsigned grid, bool pdl, cudaSt
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+  e = cudaLaunchKernelEx(&cfg, kern, a);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -757,7 +768,7 @@ cudaError_t launch_rope_append(const RopeCall& c, const tq_cache_desc& d, cudaSt
   a.tile_tok = a.n_rows ? rows_tile(a, c.num_sms) : 1;
   a.row_tiles = a.n_rows ? (c.n_tokens + a.tile_tok - 1) / a.tile_tok : 0;
   const int touch = 7 / d.num_kv_heads + 2;
-  a.coded_tok = touch < 8 ? touch : 8;
+  a.coded_tok = touch < kMostCodedTok ? touch : kMostCodedTok;
   // Many rows beside codes: the rows go first in a kernel of their own, at eight CTAs an SM
   // instead of the two that the quantizer's registers leave (65,536 tokens, 64 query and 8 KV
   // heads: 341 + 200 us apart, 588 us together; 11,000 tokens, 32 heads: 41 + 37 apart, 77
