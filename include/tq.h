@@ -214,8 +214,9 @@ typedef struct {
  *     y_a = A (x_a cos - x_b sin),  y_b = A (x_b cos + x_a sin);
  * the pairs are (i, i + rotary_dim / 2) in the half layout and (2 i, 2 i + 1) in
  * the interleaved one, coordinates from rotary_dim on pass through.  The
- * frequency f_i travels as a fraction of a turn in 64 bits, so that p f_i modulo a
- * turn is exact for any position: turns[i] = round(f_i / (2 pi) mod 1 * 2^64). */
+ * frequency f_i, a double, travels as a fraction of a turn in 64 bits, turns[i] =
+ * round(f_i / (2 pi) mod 1 * 2^64), and p f_i modulo a turn is one wrapping product:
+ * off by at most |p| 2^-65 turns, whatever the position. */
 enum { TQ_ROPE_HALF = 0, TQ_ROPE_INTERLEAVED = 1 };
 
 typedef struct {
@@ -260,7 +261,7 @@ typedef struct {
 
 /* Frequencies of a rotation ("Rotary positions" above).  scaling may be NULL (none);
  * inv_freq, if not NULL, is a host array of rotary_dim / 2 frequencies in radians a
- * position that replaces base (and takes no scaling). */
+ * position (below 2^64 in magnitude) that replaces base (and takes no scaling). */
 tq_status tq_make_rope(int layout, int rotary_dim, double base, const tq_rope_scaling* scaling,
                        const double* inv_freq, tq_rope* out);
 

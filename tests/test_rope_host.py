@@ -142,3 +142,31 @@ def test_prefix_decode_refusals(tqlib):
     assert tq.lib().tq_prefix_workspace_bytes(ref(good), 2, 12, 100, 4) == 0
     assert tq.lib().tq_prefix_workspace_bytes(ref(good), 2, 8, -1, 4) == 0
     assert tq.launch_count() == n0
+
+
+def exact_turns(f, p=1):
+    """p f / (2 pi) modulo one turn, in units of 2^-64 rounded to nearest: integers, pi by Machin's formula."""
+    from fractions import Fraction
+
+    def atan_inverse(n, bits):
+        x = total = (1 << bits) // n
+        k, sign = 1, -1
+        while x:
+            x, k = x // (n * n), k + 2
+            total, sign = total + sign * (x // k), -sign
+        return total
+
+    pi = Fraction(16 * atan_inverse(5, 512) - 4 * atan_inverse(239, 512), 1 << 512)
+    return round(Fraction(float(f)) * p / (2 * pi) * 2 ** 64) % 2 ** 64
+
+
+def test_turns_hold_64_bits_of_the_frequency(tqlib):
+    """turns_i is the nearest 64-bit fraction of the frequency, a double: of one, of powers of the base, of
+    large, small and negative ones."""
+    f = [1.0, -1.0, 1e-8, 2.0 ** -64, 2.0 ** -70, 1e-300, 0.0, 3.0, 2.0 ** 63 * 1.9, -1e19, 1e6 + 1 / 3, np.pi, 2 * np.pi]
+    f += list(10000.0 ** (-np.arange(30) / 30.0)) + list(np.random.default_rng(1).standard_normal(21))
+    rope = tqlib.Rope(128, inv_freq=f)
+    assert [int(t) for t in rope.desc.turns] == [exact_turns(x) for x in f]
+    assert int(tqlib.Rope().desc.turns[0]) == exact_turns(1.0)
+    with pytest.raises(tqlib.TQError):
+        tqlib.Rope(2, inv_freq=[2.0 ** 64])

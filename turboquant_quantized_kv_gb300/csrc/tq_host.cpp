@@ -289,12 +289,27 @@ tq_status tq_make_rotation(int kind, int head_dim, uint64_t seed, int layer, flo
   return fail(TQ_ERR_INVALID_ARG, "tq_make_rotation: unknown kind %d", kind);
 }
 
-// The fraction of a turn a pair advances a position, in 2^-64 turns.
+// The fraction of a turn a pair advances a position, in 2^-64 turns, rounded once: the frequency
+// m 2^e (|f| < 2^64, so e <= 11) times 1 / (2 pi) to 192 bits, in integers.
 static uint64_t turns_of(double radians) {
-  double t = radians / 6.283185307179586476925286766559;
-  t -= std::floor(t);
-  const double scaled = std::nearbyint(std::ldexp(t, 64));
-  return scaled >= 0x1.0p64 ? 0u : (uint64_t)scaled;
+  static const uint64_t inv_two_pi[3] = {0x36d8a5664f10e410u, 0x7f09d5f47d4d3770u, 0x28be60db9391054au};  // 2^-192 each
+  int e = 0;
+  const uint64_t m = (uint64_t)std::ldexp(std::frexp(std::fabs(radians), &e), 53);
+  const int shift = 128 - (e - 53);  // the product is in 2^(e - 53 - 192) turns
+  uint64_t p[5] = {};
+  unsigned __int128 carry = 0;
+  for (int i = 0; i < 3; ++i) {
+    carry += (unsigned __int128)m * inv_two_pi[i];
+    p[i] = (uint64_t)carry;
+    carry >>= 64;
+  }
+  p[3] = (uint64_t)carry;
+  if (shift > 255) return 0;
+  const int w = shift >> 6, b = shift & 63;
+  uint64_t t = p[w] >> b;
+  if (b) t |= p[w + 1] << (64 - b);
+  t += (p[(shift - 1) >> 6] >> ((shift - 1) & 63)) & 1u;  // to nearest
+  return radians < 0.0 ? 0u - t : t;
 }
 
 tq_status tq_make_rope(int layout, int rotary_dim, double base, const tq_rope_scaling* scaling,
@@ -321,7 +336,8 @@ tq_status tq_make_rope(int layout, int rotary_dim, double base, const tq_rope_sc
   const int pairs = rotary_dim / 2;
   const double two_pi = 6.283185307179586476925286766559;
   for (int i = 0; inv_freq && i < pairs; ++i)
-    if (!std::isfinite(inv_freq[i])) return fail(TQ_ERR_INVALID_ARG, "tq_make_rope: frequency %d is not finite", i);
+    if (!(std::fabs(inv_freq[i]) < 0x1.0p64))
+      return fail(TQ_ERR_INVALID_ARG, "tq_make_rope: frequency %d is not finite and below 2^64", i);
   if (s.kind == TQ_ROPE_SCALE_NTK && rotary_dim > 2)
     base *= std::pow(s.factor, (double)rotary_dim / (rotary_dim - 2.0));
   double lo = 0.0, hi = 0.0;

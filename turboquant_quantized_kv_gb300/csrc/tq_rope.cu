@@ -8,8 +8,8 @@
 // pass through.
 //
 // The angle.  f_i is held as a 64-bit fraction of a turn, so p f_i modulo one turn
-// is one wrapping 64-bit product: the angle of a position of a million is as exact as
-// that of position one.  The top 32 bits become a fraction of a half turn in fp32
+// is one wrapping 64-bit product, off by |p| 2^-65 turns at most: the angle of a position of a
+// million is as good as exact.  The top 32 bits become a fraction of a half turn in fp32
 // (rounded to 2^-25 half turns, about 1e-7 rad) for sincospif.
 //
 // Kernels:
