@@ -49,3 +49,14 @@ def test_decode_calls_refuse_other_sizes(layer, bad):
                  lambda: layer.decode_step(kv, kv, args["q"], table, lens, out=args["out"], workspace=ws)):
         with pytest.raises(ValueError, match=SIZES):
             call()
+
+
+def test_outputs_without_their_inputs_are_refused(layer, tqlib):
+    """An output that nothing would be written to."""
+    rope, x = tqlib.Rope(), torch.zeros(3, 2, D)
+    at = torch.zeros(3, dtype=torch.int64)
+    for call in (lambda: tqlib.apply_rope(rope, at, None, x, q_out=x), lambda: tqlib.apply_rope(rope, at, x, k_out=x),
+                 lambda: layer.rope_append(rope, None, x, at, at, k_out=x),
+                 lambda: layer.rope_append(rope, x, x, at, at, q_out=x)):
+        with pytest.raises(ValueError, match="_out is given without"):
+            call()

@@ -233,6 +233,14 @@ def _check_rows(x, what, n):
     return strides
 
 
+def _check_outputs(q, q_out, k, k_out):
+    """Raises for an output that nothing would be written to."""
+    if q is None and q_out is not None:
+        raise ValueError("q_out is given without q")
+    if k is None and k_out is not None:
+        raise ValueError("k_out is given without k")
+
+
 def _heads(t, out, name, n):
     """Reference to a tq_heads of t [n, heads, d] (any token and head strides) and its output rows."""
     if t is None:
@@ -322,6 +330,7 @@ def apply_rope(rope, positions, q, k=None, q_out=None, k_out=None, transpose=Fal
     ref = q if q is not None else k
     if ref is None:
         raise ValueError("q or k is needed")
+    _check_outputs(q, q_out, k, k_out)
     dtype, device, n = ref.dtype, ref.device, ref.shape[0]
     if k is not None and k.dtype != dtype:
         raise TypeError("q and k must have one type")
@@ -517,6 +526,7 @@ class Layer:
         ref = k if k is not None else v
         if ref is None:
             raise ValueError("k or v is needed")
+        _check_outputs(q, q_out, k, k_out)
         dtype, n = ref.dtype, ref.shape[0]
         if (q is not None and q.dtype != dtype) or (v is not None and v.dtype != dtype):
             raise TypeError("q, k and v must have one type")
