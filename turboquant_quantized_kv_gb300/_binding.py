@@ -322,11 +322,53 @@ class Rope:
         return np.array(self.desc.turns[: self.rotary_dim // 2], dtype=np.uint64).astype(np.float64) * 2.0 ** -64
 
 
+_rope_function = None
+
+
+def _differentiable_rope():
+    """The rotation as a torch.autograd.Function: its gradient is the transposed rotation."""
+    global _rope_function
+    if _rope_function is None:
+        torch = _torch()
+
+        class RopeFunction(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, rope, positions, transpose, q, k):
+                ctx.set_materialize_grads(False)
+                ctx.rope, ctx.transpose = rope, transpose
+                ctx.save_for_backward(positions)
+                return apply_rope(rope, positions, q, k, transpose=transpose)
+
+            @staticmethod
+            def backward(ctx, gq, gk):
+                (positions,) = ctx.saved_tensors
+                # (gradients may be expanded: rows are read with a contiguous last dimension)
+                gq, gk = (g.contiguous() if g is not None and g.stride(2) != 1 else g for g in (gq, gk))
+                if not ctx.needs_input_grad[3]:
+                    gq = None
+                if not ctx.needs_input_grad[4]:
+                    gk = None
+                if gq is not None or gk is not None:
+                    gq, gk = apply_rope(ctx.rope, positions, gq, gk, transpose=not ctx.transpose)
+                return None, None, None, gq, gk
+
+        _rope_function = RopeFunction
+    return _rope_function
+
+
 def apply_rope(rope, positions, q, k=None, q_out=None, k_out=None, transpose=False, stream=None):
     """Rotary positions of q and k [n_tokens, heads, d] (tq_rope_apply); positions int64
     [n_tokens].  transpose: the transposed rotation (the gradient).  q_out / k_out may be
-    q / k (in place).  Returns (q_out, k_out), contiguous where they were not given."""
+    q / k (in place).  Returns (q_out, k_out), contiguous where they were not given.  Where q or k
+    requires a gradient the results are differentiable, and outputs cannot be given."""
     torch = _torch()
+    if torch.is_grad_enabled() and ((q is not None and q.requires_grad) or (k is not None and k.requires_grad)):
+        if q_out is not None or k_out is not None:
+            raise ValueError("q_out and k_out take no part in differentiation: leave them out or use torch.no_grad()")
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return _differentiable_rope().apply(rope, positions, transpose, q, k)
+        return _differentiable_rope().apply(rope, positions, transpose, q, k)
     ref = q if q is not None else k
     if ref is None:
         raise ValueError("q or k is needed")
@@ -521,7 +563,8 @@ class Layer:
         """Append with the rotation applied on the way (tq_rope_append): k [n_tokens, H_kv, d]
         rotated to positions [n_tokens] (int64), stored with v in slot_mapping [n_tokens]
         (int64).  q [n_tokens, H_q, d] is rotated to q_out (may be q); k_out, if given, takes
-        the rotated keys.  Token and head strides are free.  Returns q_out."""
+        the rotated keys.  Token and head strides are free.  Nothing is recorded for
+        differentiation (apply_rope is differentiable).  Returns q_out."""
         torch = _torch()
         ref = k if k is not None else v
         if ref is None:
