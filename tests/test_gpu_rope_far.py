@@ -25,3 +25,18 @@ def test_far_positions_by_exact_angles(cuda, tqlib):
     want = np.concatenate([xs[..., :64] * c - xs[..., 64:] * s, xs[..., 64:] * c + xs[..., :64] * s], -1)
     slack = ROT + 2 * np.pi * np.abs(pos)[:, None, None] * 2.0 ** -65
     assert np.all(np.abs(got - want) <= slack * pair_norm(xs, 128, "half"))
+
+
+@pytest.mark.parametrize("heads", [6640020, 8388607, 12000001])
+def test_millions_of_heads_at_one_position(cuda, tqlib, heads):
+    """One token whose head count is past the integers that an fp32 quotient tells apart (heads of many
+    sequences at the same position, taken as one token): as rows of a token each."""
+    tq = tqlib
+    rope = tq.Rope()
+    x = cuda.randn(1, heads, D, device="cuda", dtype=cuda.bfloat16)
+    at = cuda.tensor([77], device="cuda")
+    got = tq.apply_rope(rope, at, x)[0]
+    for lo in (0, heads // 2, heads - 5000):
+        rows = x[0, lo:lo + 5000].view(-1, 1, D)
+        want = tq.apply_rope(rope, at.expand(rows.shape[0]).contiguous(), rows)[0]
+        assert cuda.equal(got[0, lo:lo + 5000].view(-1, 1, D), want)

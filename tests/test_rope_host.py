@@ -170,3 +170,10 @@ def test_turns_hold_64_bits_of_the_frequency(tqlib):
     assert int(tqlib.Rope().desc.turns[0]) == exact_turns(1.0)
     with pytest.raises(tqlib.TQError):
         tqlib.Rope(2, inv_freq=[2.0 ** 64])
+
+
+def test_more_heads_than_a_token_can_have_are_refused(tqlib):
+    tq = tqlib
+    h = heads(tq, n=(1 << 28) + 1)
+    assert tq.lib().tq_rope_apply(ref(tq.Rope().desc), 0, ref(h), None, tq.TQ_BF16, ctypes.c_void_p(0x30000), 1, None) == tq.TQ_ERR_INVALID_ARG
+    assert "num_heads" in tq.last_error()

@@ -169,7 +169,7 @@ tq_status check_rope(const tq_rope* r, const char* fn) {
 tq_status check_heads(const tq_heads& h, int dtype, int64_t n_tokens, bool need_out, const char* what) {
   const uintptr_t mask = dtype == TQ_F32 ? 3 : 1;
   if (n_tokens > 0 && (!h.in || (need_out && !h.out))) return fail(TQ_ERR_INVALID_ARG, "%s: null rows", what);
-  if (h.num_heads < 1) return fail(TQ_ERR_INVALID_ARG, "%s: num_heads %d", what, h.num_heads);
+  if (h.num_heads < 1 || h.num_heads > (1 << 28)) return fail(TQ_ERR_INVALID_ARG, "%s: num_heads %d", what, h.num_heads);
   if ((reinterpret_cast<uintptr_t>(h.in) | reinterpret_cast<uintptr_t>(h.out)) & mask)
     return fail(TQ_ERR_INVALID_ARG, "%s: rows not aligned to their elements", what);
   return TQ_OK;

@@ -279,7 +279,10 @@ __device__ __forceinline__ void rope_rows(const RopeArgs& a, int64_t tile, float
   // a thread always has item c of a head; heads of the tile's tokens in steps of the CTA
   constexpr int STEP = kRThreads / PER;
   const int c = tid % PER, heads = nt * a.heads;
-  const float inv_heads = 1.0f / (float)a.heads;  // (quotients below 2^13 of a few: exact)
+  // (tiles of several tokens have less than 128 heads a token, and the quotient is exact; a token alone may
+  // have millions, where it can round up to one)
+  const float inv_heads = 1.0f / (float)a.heads;
+  auto token_of = [&](int head) { return min((int)(((float)head + 0.5f) * inv_heads), nt - 1); };
   auto rows_of_head = [&](int& h) -> const RopeRows& {  // the tensor of head h, h its head there
     int s = 0;
     while (s + 1 < a.n_rows && h >= a.rows[s].heads) h -= a.rows[s++].heads;
@@ -290,7 +293,7 @@ __device__ __forceinline__ void rope_rows(const RopeArgs& a, int64_t tile, float
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) {
       if (th + k * STEP >= heads) break;
-      const int tok = (int)(((float)(th + k * STEP) + 0.5f) * inv_heads);
+      const int tok = token_of(th + k * STEP);
       int h = th + k * STEP - tok * a.heads;
       const RopeRows& r = rows_of_head(h);
       item_place<T, W>(it[k], c, r.rotate ? a.pairs : 0, inter);
@@ -310,7 +313,7 @@ __device__ __forceinline__ void rope_rows(const RopeArgs& a, int64_t tile, float
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) {
       if (th + k * STEP >= heads) break;
-      const int tok = (int)(((float)(th + k * STEP) + 0.5f) * inv_heads);
+      const int tok = token_of(th + k * STEP);
       int h = th + k * STEP - tok * a.heads;
       const RopeRows& r = rows_of_head(h);
       item_widen<T, W>(it[k]);
