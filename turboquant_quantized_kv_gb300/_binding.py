@@ -217,6 +217,15 @@ def _stream(stream):
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
+def _new(make, shape, dtype, device, stream):
+    """make(shape) (torch.empty or torch.zeros) for a call on `stream`: the memory comes from that stream's pool, free
+    of what other streams still do with it, and is filled there."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with _torch().cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
 _byref = ctypes.byref
 
 
@@ -377,9 +386,9 @@ def apply_rope(rope, positions, q, k=None, q_out=None, k_out=None, transpose=Fal
     if k is not None and k.dtype != dtype:
         raise TypeError("q and k must have one type")
     if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=dtype, device=device)
+        q_out = _new(torch.empty, q.shape, dtype, device, stream)
     if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=dtype, device=device)
+        k_out = _new(torch.empty, k.shape, dtype, device, stream)
     pos = _index_ptr(positions, "positions", torch.int64, (n,))
     _check(lib().tq_rope_apply(rope.ref, 1 if transpose else 0, _heads(q, q_out, "q", n), _heads(k, k_out, "k", n),
                                _dtype_code(ref), pos, n, _stream(stream)))
@@ -501,10 +510,10 @@ class Layer:
         if sm_scale is None:
             sm_scale = 1.0 / math.sqrt(self.head_dim)
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype if out_dtype is None else out_dtype, device=q.device)
+            out = _new(torch.empty, q.shape, q.dtype if out_dtype is None else out_dtype, q.device, stream)
         if workspace is None:
-            workspace = torch.zeros(self.workspace_bytes(bsz, hq, max_blocks, num_splits), dtype=torch.uint8,
-                                    device=q.device)
+            workspace = _new(torch.zeros, self.workspace_bytes(bsz, hq, max_blocks, num_splits), torch.uint8, q.device,
+                             stream)
         _check(lib().tq_decode_attention(ctypes.byref(self.desc), _ptr(q, "q"), _dtype_code(q), bsz, hq,
                                          _ptr(block_table, "block_table"), max_blocks,
                                          _ptr(context_lens, "context_lens"), ctypes.c_float(sm_scale),
@@ -524,10 +533,10 @@ class Layer:
         if sm_scale is None:
             sm_scale = 1.0 / math.sqrt(self.head_dim)
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype if out_dtype is None else out_dtype, device=q.device)
+            out = _new(torch.empty, q.shape, q.dtype if out_dtype is None else out_dtype, q.device, stream)
         if workspace is None:
-            workspace = torch.zeros(self.workspace_bytes(bsz, hq, max_blocks, num_splits), dtype=torch.uint8,
-                                    device=q.device)
+            workspace = _new(torch.zeros, self.workspace_bytes(bsz, hq, max_blocks, num_splits), torch.uint8, q.device,
+                             stream)
         _check(lib().tq_append_decode(ctypes.byref(self.desc), _ptr(k, "k"), _ptr(v, "v"),
                                       _dtype_code(ref) if ref is not None else TQ_BF16,
                                       _ptr(slot_mapping, "slot_mapping"), n, _ptr(q, "q"), _dtype_code(q), bsz, hq,
@@ -548,10 +557,10 @@ class Layer:
         if sm_scale is None:
             sm_scale = 1.0 / math.sqrt(self.head_dim)
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype if out_dtype is None else out_dtype, device=q.device)
+            out = _new(torch.empty, q.shape, q.dtype if out_dtype is None else out_dtype, q.device, stream)
         if workspace is None:
-            workspace = torch.zeros(self.workspace_bytes(bsz, hq, max_blocks, num_splits), dtype=torch.uint8,
-                                    device=q.device)
+            workspace = _new(torch.zeros, self.workspace_bytes(bsz, hq, max_blocks, num_splits), torch.uint8, q.device,
+                             stream)
         _check(lib().tq_decode_step(ctypes.byref(self.desc), _ptr(k_new, "k_new"), _ptr(v_new, "v_new"),
                                     _dtype_code(k_new), _ptr(q, "q"), _dtype_code(q), bsz, hq,
                                     _ptr(block_table, "block_table"), max_blocks, _ptr(context_lens, "context_lens"),
@@ -576,7 +585,7 @@ class Layer:
         pos = _index_ptr(positions, "positions", torch.int64, (n,))
         slots = _index_ptr(slot_mapping, "slot_mapping", torch.int64, (n,))
         if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
+            q_out = _new(torch.empty, q.shape, dtype, q.device, stream)
         _check(lib().tq_rope_append(_byref(self.desc), rope.ref, _heads(q, q_out, "q", n), _heads(k, k_out, "k", n),
                                     _heads(v, None, "v", n), _dtype_code(ref), pos, slots, n, _stream(stream)))
         return q_out
@@ -604,10 +613,10 @@ class Layer:
         if sm_scale is None:
             sm_scale = 1.0 / math.sqrt(self.head_dim)
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype if out_dtype is None else out_dtype, device=q.device)
+            out = _new(torch.empty, q.shape, q.dtype if out_dtype is None else out_dtype, q.device, stream)
         if workspace is None and bsz > 0:
-            workspace = torch.zeros(self.prefix_workspace_bytes(bsz, hq, prefix_len, max_blocks), dtype=torch.uint8,
-                                    device=q.device)
+            workspace = _new(torch.zeros, self.prefix_workspace_bytes(bsz, hq, prefix_len, max_blocks), torch.uint8,
+                             q.device, stream)
         table = None if prefix_len <= 0 else _index_ptr(prefix_table, "prefix_table", torch.int32, prefix_table.shape)
         rows = lens = None
         if max_blocks > 0:
@@ -650,7 +659,7 @@ class Layer:
         """x_hat [n, H_kv, d] of the K (which=0) or V (which=1) records at slots [n] (int64)."""
         torch = _torch()
         dt = torch.float32 if out_dtype is None else out_dtype
-        out = torch.empty((int(slots.shape[0]), self.num_kv_heads, self.head_dim), dtype=dt, device=slots.device)
+        out = _new(torch.empty, (int(slots.shape[0]), self.num_kv_heads, self.head_dim), dt, slots.device, stream)
         _check(lib().tq_dequantize(ctypes.byref(self.desc), which, _ptr(slots, "slots"), int(slots.shape[0]),
                                    _ptr(out, "out"), _dtype_code(out), _stream(stream)))
         return out
