@@ -36,3 +36,24 @@ def test_one_workspace_serves_narrower_tables_and_shorter_prefixes(cuda, tqlib, 
             one = run(cuda, tq, part, P, workspace=ws)
             assert cuda.equal(one, run(cuda, tq, part, P))
     check(cuda, tq, case, 2600)
+
+
+def test_more_units_than_the_counter_region_holds(cuda, tqlib):
+    """2,100 sequences of 8 KV heads with a wide table: the own tokens' partials take no counters, so no pass
+    zeroes them, and the workspace serves decode calls before and after."""
+    tq = tqlib
+    B, P, width = 2100, 40, 129
+    lens = workloads.rng(7).integers(0, 5, B)
+    case = build(cuda, tq, "packed", 4, 4, B=B, hq=8, hkv=8, P=P, lens=lens, seed=7, width=1)
+    layer, q, ptab, table, lens = case
+    wide = layer, q, ptab, np.repeat(table, width, 1), lens
+    ws = cuda.zeros(layer.prefix_workspace_bytes(B, 8, P, width), dtype=cuda.uint8, device="cuda")
+    n0 = tq.launch_count()
+    one = run(cuda, tq, wide, P, workspace=ws)
+    assert tq.launch_count() - n0 == 3
+    args = q[:4].contiguous(), cuda.from_numpy(table[:4]).cuda(), cuda.from_numpy(lens[:4]).cuda()
+    plain = layer.decode(*args)
+    for _ in range(3):
+        assert cuda.equal(layer.decode(*args, workspace=ws), plain)
+        assert cuda.equal(run(cuda, tq, wide, P, workspace=ws), one)
+    check(cuda, tq, wide, P)

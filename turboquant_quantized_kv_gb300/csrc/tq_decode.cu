@@ -1750,7 +1750,9 @@ cudaError_t launch_decode(const DecodeCall& c, cudaStream_t st) {
   // workspace (its contents must be zero before the first call).
   const int g = c.num_q_heads / d.num_kv_heads;
   const int64_t units = (int64_t)c.batch * d.num_kv_heads * ((g + (g <= 4 ? 3 : 7)) / (g <= 4 ? 4 : 8));
-  const bool prep = !q_in_kernel || (size_t)units * sizeof(int32_t) > kCounterRegionBytes;
+  // (Partials that the caller merges need no counters.  A pass that the decode never waits for could still be
+  // zeroing them when later calls on the stream count.)
+  const bool prep = !q_in_kernel || (!c.partials_only && (size_t)units * sizeof(int32_t) > kCounterRegionBytes);
   if (prep) {
     const int64_t rot_rows = q_in_kernel ? 0 : rows;
     const int n_counters = (int)rows;  // >= batch * kv heads * head groups
