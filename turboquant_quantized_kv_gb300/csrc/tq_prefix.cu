@@ -1259,13 +1259,15 @@ int own_splits(int max_blocks) { return max_blocks <= kOwnMaxBlocks ? (max_block
 // The own tokens' CTAs (own_ctas of them, a few an SM) run next to the prefix kernel on the SMs
 // that it leaves free.  When some of them would have to follow it, fewer splits may be better:
 // the times below are in us, of a tile, of the prefix kernel's start and end, and of a CTA of
-// k_own.  (64 rows, 8192 tokens, 512 CTAs of own tokens: 16 splits 37.4 us, 13 31.0, 11 29.0,
-// 10 31.0.)  Never more splits than without own tokens, which is what the workspace is made for.
+// k_own, by the blocks it has; a gain that they put below 2 us is not taken.  (64 rows, 8192 tokens,
+// 512 CTAs of own tokens: 16 splits 37.4 us, 13 31.0, 11 29.0, 10 31.0.  Over bf16, k8v4 and 4 bits, 32 to
+// 512 rows, 2,048 to 32,768 tokens, own contexts of up to 40, 300 and 1,000: 0.95 of the time without,
+// from 0.64 -- 32 rows, 2,048 tokens, own 1,000: 28.2 -> 18.0 us -- to 1.07 -- 192 rows, 32,768, own 300.)  Never more splits than without own tokens, which is what the workspace is made for.
 constexpr int64_t kPMostTiles = 1024;
 struct PrefixPlan {
   int pair, row_blocks, splits, tiles_per_split, partials;
 };
-static PrefixPlan prefix_plan(const tq_cache_desc& d, int batch, int num_q_heads, int64_t len, int64_t own_ctas,
+static PrefixPlan prefix_plan(const tq_cache_desc& d, int batch, int num_q_heads, int64_t len, int max_blocks,
                               int num_sms) {
   PrefixPlan p = {};
   if (len < 1) return p;
@@ -1289,10 +1291,14 @@ static PrefixPlan prefix_plan(const tq_cache_desc& d, int batch, int num_q_heads
       p.tiles_per_split = (int)per;
     }
   }
-  if (own_ctas > 0 && units * p.splits <= num_sms) {
-    const float tile_us = p.pair ? 2.9f : 1.3f, ends_us = p.pair ? 8.7f : 10.4f, own_us = 7.0f;
+  const int own = own_splits(max_blocks);
+  if (own > 0 && units * p.splits <= num_sms) {
+    const int64_t own_ctas = (int64_t)own * batch * d.num_kv_heads * ((num_q_heads / d.num_kv_heads + 7) / 8);
+    const float tile_us = p.pair ? 2.9f : 1.3f, ends_us = p.pair ? 8.7f : 10.4f;
+    const float own_us = 2.0f + 5.0f * (float)max_blocks / (float)(own * kOwnChunk);
     const int64_t per_sm = d.fmt.kv_format == TQ_KV_BF16 ? 3 : 4;
     float least = INFINITY;
+    float margin = 0.0f;  // (of the first, the splits without own tokens)
     for (int64_t s = p.splits; s >= 1; --s) {
       const int64_t per = (tiles + s - 1) / s;
       if (per > kPMostTiles) break;
@@ -1301,7 +1307,8 @@ static PrefixPlan prefix_plan(const tq_cache_desc& d, int batch, int num_q_heads
       const int64_t beside = (num_sms - units * s) * per_sm * (int64_t)(t / own_us);
       const int64_t left = own_ctas > beside ? own_ctas - beside : 0;
       const float all = t + own_us * (float)((left + num_sms * per_sm - 1) / (num_sms * per_sm));
-      if (all < least) {
+      if (all < least - margin) {
+        if (margin == 0.0f) margin = 2.0f;
         least = all;
         p.splits = (int)s;
         p.tiles_per_split = (int)per;
@@ -1391,10 +1398,7 @@ cudaError_t launch_prefix_decode(const PrefixCall& c, cudaStream_t st) {
   }
   if (c.prefix_len > 0) {
     PrefixArgs a = {};
-    const int64_t own_ctas = c.own.max_blocks > 0 ? (int64_t)own_splits(c.own.max_blocks) * c.own.batch * d.num_kv_heads *
-                                                        ((c.own.num_q_heads / d.num_kv_heads + 7) / 8)
-                                                  : 0;
-    const PrefixPlan p = prefix_plan(d, c.own.batch, c.own.num_q_heads, c.prefix_len, own_ctas, c.num_sms);
+    const PrefixPlan p = prefix_plan(d, c.own.batch, c.own.num_q_heads, c.prefix_len, c.own.max_blocks, c.num_sms);
     a.split_q = d.fmt.kv_format == TQ_KV_PACKED || c.own.q_dtype == TQ_F32 ? 1 : 0;
     a.v_stages = p.pair && a.split_q ? 1 : 2;
     a.kpool = reinterpret_cast<const uint8_t*>(d.k_cache);
