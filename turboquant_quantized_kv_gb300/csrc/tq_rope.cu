@@ -754,12 +754,13 @@ cudaError_t launch_rope_append(const RopeCall& c, const tq_cache_desc& d, cudaSt
   const int touch = 7 / d.num_kv_heads + 2;
   a.coded_tok = touch < kMostCodedTok ? touch : kMostCodedTok;
   // Many rows beside codes: the rows go first in a kernel of their own, at eight CTAs an SM
-  // instead of the two that the quantizer's registers leave (65,536 tokens, 64 query and 8 KV
-  // heads: 341 + 200 us apart, 588 us together; 11,000 tokens, 32 heads: 41 + 37 apart, 77
-  // together).
+  // instead of the two that the quantizer's registers leave.  Device times together and apart, us, 4 bits,
+  // 32 query and 8 KV heads: 2^15 rows 12.6, 11.3; 2^16 20.3, 16.0; 2^17 30.5, 26.7; 2^18 58.7, 51.8;
+  // 2^20 213, 179; k8v4, 64 and 8 heads: 2^15 9.3, 10.1; 2^16 13.7, 12.9; 2^17 23.4, 17.2; 2^20 161, 114.
+  // Below 2^17 the call's host time, 28 us from Python, is the longer one, and one launch costs less of it.
   const int64_t coded = a.coded[0].tiles + a.coded[1].tiles;
   bool apart = false;
-  if (coded > 0 && a.row_tiles > 0 && c.n_tokens * a.heads >= (1 << 18)) {
+  if (coded > 0 && a.row_tiles > 0 && c.n_tokens * a.heads >= (1 << 17)) {
     const cudaError_t e = c.dtype == TQ_F32 ? run_apply<float>(a, c.num_sms, st) : run_apply<__nv_bfloat16>(a, c.num_sms, st);
     if (e != cudaSuccess) return e;
     a.row_tiles = 0;
