@@ -1461,9 +1461,10 @@ cudaError_t launch_prefix_decode(const PrefixCall& c, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(m.um.Hkv * ((m.rows + 7) / 8)));
   // Sets of warps that share a row's partials: more where there are many partials or the CTAs are
-  // few.  Calls of 64 CTAs with 26 partials take 28.5 us with four sets, 28.9 with two; of 192 CTAs
-  // with 13 partials 24.8 with two, 26.8 with one; of 512 CTAs with 9 partials 51.3 with two,
-  // 49.2 with one.
+  // few.  Whole calls of 4 bits from a graph, us with one, two and four sets (CTAs, partials):
+  //   (32, 33) 19.5 17.8 16.2   (64, 33) 27.7 24.9 23.4   (128, 27) 31.1 28.8 27.2    (256, 17) 35.2 33.2 35.9
+  //   (64, 5) 14.4 14.4 14.9    (32, 9) 14.7 14.4 14.9    (192, 13) 32.6 31.1 33.6    (256, 9) 20.8 20.6 23.4
+  //   (512, 5) 25.2 27.5 33.1   (512, 8) 55.1 57.4 63.6   (512, 11) 324.7 326.5 332.1 (1024, 7) 174.0 178.9 189.9
   const int all = m.partials + m.own_splits, ctas = (int)cfg.gridDim.x;
   const int sets = all > 16 ? (ctas <= c.num_sms ? 4 : 2) : (all > 8 && ctas <= 2 * c.num_sms ? 2 : 1);
   cfg.blockDim = dim3(128 * sets);
