@@ -186,3 +186,21 @@ def test_long_prefixes_keep_their_sums(cuda, tqlib, fmt, P):
 @pytest.mark.parametrize("P", [2 ** 31 - 1, 2 ** 31 - 127])
 def test_the_longest_prefixes(cuda, tqlib, fmt, P):
     assert long_prefix_error(cuda, tqlib, fmt, P) <= TOL
+
+
+@pytest.mark.parametrize("fmt,bk,bv", FORMATS[:2])
+@pytest.mark.parametrize("own", [0, 40])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** 30])
+def test_a_key_that_is_not_a_number_shows(cuda, tqlib, fmt, bk, bv, own, size):
+    """In the prefix, or among a sequence's own tokens, under ordinary logits and under large ones: every row
+    that attends it is NaN, the other sequences are not."""
+    P, B = 300, 3
+    layer, q, ptab, table, lens = graded(cuda, tqlib, fmt, bk, bv, P=P, own=own, outlier=1.0, B=B)
+    q = q.float() * size
+    bad = cuda.full((1, 1, D), float("nan"), device="cuda")
+    slot = int(table[1, 1]) * 16 + 3 if own else int(ptab[7]) * 16 + 3
+    layer.append(bad, None, cuda.tensor([slot], device="cuda"))
+    out = run(cuda, tqlib, (layer, q, ptab, table, lens), P, cuda.float32)
+    nan = out.isnan().all(-1).all(-1).tolist()
+    assert nan == ([False, True, False] if own else [True] * 3)
+    assert bool(out[~cuda.tensor(nan, device="cuda")].isfinite().all())

@@ -761,7 +761,25 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
             }
           }
           // P = 2^(u + et - C + shift); the denominator's terms are P 2^-et
-          const float off = (C == -INFINITY ? 0.0f : C) - kPShift - (float)et;
+          float off = (C == -INFINITY ? 0.0f : C) - kPShift - (float)et;
+          if (__any_sync(0xffffffffu, fabsf(C) > kPLarge && C != -INFINITY)) {
+            // the difference is taken here, of rounded values, and stands in the logit's place
+            const float ref = (C == -INFINITY ? 0.0f : C) - kPShift;
+            off = 0.0f;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              tmem_ld32_async(ts + 32 * c, ra);
+              tmem_wait_ld32(ra);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) {
+                const float g = kCodedK ? gs[slot * kPTile + 32 * c + k] : rsr;
+                const float u = __fadd_rn(__fmul_rn(__uint_as_float(ra[k]), g), (float)et) - ref;
+                ra[k] = __float_as_uint((u > kPSlack + kPShift ? kPSlack + kPShift : u) / g);  // (NaN stays)
+              }
+              tmem_st32(ts + 32 * c, ra);
+            }
+            tmem_wait_st();
+          }
           float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
           auto weights = [&](uint32_t(&r)[32], int c) {
             uint32_t p[16];
@@ -781,42 +799,18 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
             }
             tmem_st16(ts + 16 * c, p);  // over logits that have been read
           };
-          if (__any_sync(0xffffffffu, fabsf(C) > kPLarge && C != -INFINITY)) {
-            const float ref = (C == -INFINITY ? 0.0f : C) - kPShift;
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              tmem_ld32_async(ts + 32 * c, ra);
-              tmem_wait_ld32(ra);
-              uint32_t p[16];
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float4 g = kCodedK ? g4[8 * c + k] : make_float4(rsr, rsr, rsr, rsr);
-                auto weight = [&](uint32_t x, float gx) {
-                  return ex2(fminf(__fadd_rn(__fmul_rn(__uint_as_float(x), gx), (float)et) - ref, kPSlack + kPShift));
-                };
-                const float2 u0 = make_float2(weight(ra[4 * k], g.x), weight(ra[4 * k + 1], g.y));
-                const float2 u1 = make_float2(weight(ra[4 * k + 2], g.z), weight(ra[4 * k + 3], g.w));
-                sum0 = __fadd2_rn(sum0, u0);
-                sum1 = __fadd2_rn(sum1, u1);
-                p[2 * k] = pack_h2(u0.x, u0.y);
-                p[2 * k + 1] = pack_h2(u1.x, u1.y);
-              }
-              tmem_st16(ts + 16 * c, p);
-            }
-          } else {
-            tmem_ld32_async(ts, ra);
-            tmem_wait_ld32(ra);
-            tmem_ld32_async(ts + 32, rb);
-            weights(ra, 0);
-            tmem_wait_ld32(rb);
-            tmem_ld32_async(ts + 64, ra);
-            weights(rb, 1);
-            tmem_wait_ld32(ra);
-            tmem_ld32_async(ts + 96, rb);
-            weights(ra, 2);
-            tmem_wait_ld32(rb);
-            weights(rb, 3);
-          }
+          tmem_ld32_async(ts, ra);
+          tmem_wait_ld32(ra);
+          tmem_ld32_async(ts + 32, rb);
+          weights(ra, 0);
+          tmem_wait_ld32(rb);
+          tmem_ld32_async(ts + 64, ra);
+          weights(rb, 1);
+          tmem_wait_ld32(ra);
+          tmem_ld32_async(ts + 96, rb);
+          weights(ra, 2);
+          tmem_wait_ld32(rb);
+          weights(rb, 3);
           l = fmaf((sum0.x + sum0.y) + (sum1.x + sum1.y), to_l, l);
         }
         tmem_wait_st();
