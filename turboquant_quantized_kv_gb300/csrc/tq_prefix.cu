@@ -53,6 +53,7 @@
 #include <cuda_fp8.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "tq_async.cuh"
 #include "tq_device.cuh"
@@ -603,21 +604,30 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
     const bool scaled = kCodedK && __any_sync(0xffffffffu, rd != 0);
     const float rsr = KF == 8 ? fmaxf(rs * exp2i(rd), 1e-30f) : rs;
     float C = -INFINITY, l = 0.0f;  // reference of u + et; sum of 2^(u - C + shift)
-    for (int i = 0; i < count && ok; ++i) {
+    int i = 0;
+    // One tile.  Of coded keys, plain tiles -- every token there, values that share an exponent, logits of
+    // ordinary size, no row with an exponent of its own -- go through a loop of their own, which ends at
+    // the first tile that is not one; the careful loop takes it and the rest.  (In one loop for all, the
+    // registers and the code of the rare cases cost the plain ones a tenth: a call of 100,000 tokens and
+    // 512 rows 367 us for 338; 8-bit and bf16 keys, with registers to spare, gain nothing.)
+    auto tile = [&](auto careful) {  // whether the tile is done
+      constexpr bool kCareful = decltype(careful)::value;
       const int t = a.pair ? i : 2 * i + s, slot = t & (kPNormSlots - 1);
       ok = mbar_wait(gfull + slot, (t / kPNormSlots) & 1) && mbar_wait(efull + slot, (t / kPNormSlots) & 1) &&
            mbar_wait(sfull + s, i & 1);
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
+      if (!ok) return false;
       tc_fence_after();
       if (live) {
         const uint4 mw = *reinterpret_cast<const uint4*>(gen + kPOffMask + slot * 16);
         const float4* g4 = reinterpret_cast<const float4*>(gs + slot * kPTile);
         const TileRange range = tile_range<VF>(gen + kPOffExp + slot * 16);
         const int et = range.et;
-        const float to_l = VF != 0 && range.wide ? 0.0f : exp2i(-et);  // the denominator's terms of a P of one
+        const bool full = (mw.x & mw.y & mw.z & mw.w) == 0xFFFFFFFFu;
+        if (!kCareful && (range.wide || !full)) return false;
+        const float to_l = kCareful && VF != 0 && range.wide ? 0.0f : exp2i(-et);  // the denominator's terms of a P of one
         uint32_t ra[32], rb[32];
-        if (scaled || (kCodedV && range.wide) || (mw.x & mw.y & mw.z & mw.w) != 0xFFFFFFFFu) {
+        if (kCareful && (scaled || (kCodedV && range.wide) || !full)) {
           // logits of the tile's masked tokens to -inf, of rows with an exponent of their own to the CTA's
           const float f = kCodedK ? exp2i(rd) : 1.0f;
 #pragma unroll 1
@@ -693,7 +703,7 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
             tmem_wait_st();
           }
         }
-        if (VF == 0 && range.wide) {
+        if (kCareful && VF == 0 && range.wide) {
           const float2 n2 = wide_bf16_tile(ts, to, rsr, range.lo, i == 0, C, l);
           C = n2.x;
           l = n2.y;
@@ -728,7 +738,7 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
           } else {
             m = __fmul_rn(m, rsr);
           }
-          if (__any_sync(0xffffffffu, m + (float)et > C + (fabsf(C) > kPLarge ? 0.0f : kPSlack))) {
+          if (__any_sync(0xffffffffu, m + (float)et > C + (kCareful && fabsf(C) > kPLarge ? 0.0f : kPSlack))) {
             if constexpr (kCodedK) {  // the exact maximum
               m = -INFINITY;
 #pragma unroll 1
@@ -758,11 +768,12 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
                 }
               }
               C = nc;
+              if (!kCareful && __any_sync(0xffffffffu, fabsf(C) > kPLarge && C != -INFINITY)) return false;
             }
           }
           // P = 2^(u + et - C + shift); the denominator's terms are P 2^-et
           float off = (C == -INFINITY ? 0.0f : C) - kPShift - (float)et;
-          if (__any_sync(0xffffffffu, fabsf(C) > kPLarge && C != -INFINITY)) {
+          if (kCareful && __any_sync(0xffffffffu, fabsf(C) > kPLarge && C != -INFINITY)) {
             // the difference is taken here, of rounded values, and stands in the logit's place
             const float ref = (C == -INFINITY ? 0.0f : C) - kPShift;
             off = 0.0f;
@@ -818,7 +829,11 @@ __global__ void __launch_bounds__(kPThreads<KF>, 1) k_prefix(const __grid_consta
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(pfull + s);
-    }
+      return true;
+    };
+    if (kCodedK && !scaled)
+      while (i < count && tile(std::false_type())) ++i;
+    while (i < count && ok && tile(std::true_type())) ++i;
     // ---- the stream's partial: (accumulator, reference, denominator) of each row
     if (ok && count > 0) ok = __all_sync(0xffffffffu, mbar_wait(odone + s, 0));
     tc_fence_after();
