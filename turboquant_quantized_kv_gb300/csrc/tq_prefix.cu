@@ -45,11 +45,11 @@
 // What bounds it.  With few rows the prefix's bytes would (8192 tokens, 8 heads, 4 bits: 2.7 us),
 // but a CTA's start, first loads and end are 8 us and its chain of steps comes on top: 16 us for
 // 64 rows.  With 512 rows the products would (100,000 tokens, 8 heads, 3 and 4 bits: 210 GFLOP,
-// 315 with the queries' second part); the kernel takes 291 us, 1.08 PFLOP/s, the tensor pipe half
-// of the time busy: a step of two streams is 5,600 clocks for 48 products of 77 clocks (64 at
-// best: the logits' operands both come from shared memory, at its full rate), the rest is what
-// two streams do not hide of the chain logits - softmax - weights - values.  16,384 tokens of
-// bf16, 512 rows: 43 us, 0.8 PFLOP/s.
+// 315 with the queries' second part); the kernel takes 297 us, 0.71 PFLOP/s of the operator's products
+// and 1.06 with the second part, the tensor pipe half of the time busy: a step of two streams is 5,600
+// clocks for 48 products of 77 clocks (64 at best: the logits' operands both come from shared memory,
+// at its full rate), the rest is what two streams do not hide of the chain logits - softmax - weights -
+// values.  16,384 tokens of bf16, 512 rows, seven splits beside the own tokens: 59 us, 0.58 PFLOP/s.
 #include <cuda_fp8.h>
 
 #include <atomic>

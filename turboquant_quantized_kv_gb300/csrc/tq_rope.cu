@@ -22,10 +22,11 @@
 //                  between the load and the quantizer.
 // Both read and write each element once.  Rows are bound by memory: 65,536 tokens of 64 heads in
 // bf16 (2.1 GB) 341 us, 6.3 TB/s; 12,345 tokens of 40 heads (253 MB) 51 us, 5.0 TB/s, start and
-// end of the kernel being a tenth of it.  Codes are bound by the issue of instructions: keys and
-// values of 65,536 tokens of 8 heads, 3 and 4 bits, 190 us for 1,048,576 vectors, 1,140 warp
-// instructions for eight vectors, 64 of them shuffles of the transform (an exchange of half the
-// values in place of full shuffles spills at two CTAs an SM: 195 us).
+// end of the kernel being a tenth of it.  Codes are bound by the issue of this kernel's instructions:
+// keys and values of 65,536 tokens of 8 heads, 3 and 4 bits, 190 to 205 us for 1,048,576 vectors, 1,140
+// warp instructions for eight vectors, 64 of them shuffles of the transform (an exchange of half the
+// values in place of full shuffles spills at two CTAs an SM: 195 us for 190).  It is not a floor: the
+// append without a rotation, a lane a vector, takes 535 for eight.
 #include <cuda_fp8.h>
 
 #include <atomic>
