@@ -64,6 +64,20 @@
  *    s_t = sm_scale r_t <Pi q, y_hat_t>; values are summed in the rotated
  *    domain as for the packed layers.
  *
+ *  int8 layers (no counterpart in the pages: the plain 8-bit cache beside the coded
+ *  ones) store keys and values as 8-bit codes with one step for each block and
+ *  head, for the keys and for the values: s = max(2^-126, fp32(a / 127)) with a the
+ *  largest magnitude of the block's records, code = x / s rounded to the nearest,
+ *  ties to even.  The tokens of one append that go to one block share its step;
+ *  if they need a larger one than the block has, the codes that are there are
+ *  rounded to it, code' = code s_old / s_new to the nearest.  An append that writes
+ *  slot 0 of a block begins it: the step comes from that call's tokens alone and
+ *  the records that the call does not write become zeros, so a block is to be
+ *  filled from slot 0 on, as sequences fill it.  A token with an infinite coordinate or
+ *  a NaN takes no part in the step and reads as not a number in every coordinate;
+ *  the other tokens keep their values.  Of a slot given twice in one call the
+ *  later token stays.
+ *
  * ------------------------------------------------------------------------
  * Readings of the pages (they leave these open; the library and the oracle
  * both follow them)
@@ -111,6 +125,9 @@
  *  (level 1 angles 0..d/2-1, then level 2, ..., the last level's one angle at
  *  slot d-2) and slot d-1 = 0.  d = 128: 1056 B (4-bit), 800 B (3-bit),
  *  544 B (2-bit).
+ *  int8 pools: one page per (block, kv head) = [16][d] bytes, byte = code + 128 with
+ *  codes -127 .. 127, then {fp32 step, uint32 bits, 8 bytes of no meaning}; a value
+ *  is code * step, bit r says that record r is not a number.  2064 B.
  *  Pools must be 16-byte aligned.
  *
  * ------------------------------------------------------------------------
@@ -163,7 +180,7 @@ enum { TQ_F32 = 0, TQ_BF16 = 1 };
 enum { TQ_ROT_HADAMARD = 1, TQ_ROT_DENSE = 2, TQ_RNG_QJL = 3 };
 
 /* layer storage */
-enum { TQ_KV_PACKED = 0, TQ_KV_BF16 = 1, TQ_KV_K8V4 = 2, TQ_KV_POLAR = 3 };
+enum { TQ_KV_PACKED = 0, TQ_KV_BF16 = 1, TQ_KV_K8V4 = 2, TQ_KV_POLAR = 3, TQ_KV_INT8 = 4 };
 
 /* norm handling */
 enum { TQ_NORM_CORRECTED = 0, TQ_NORM_RAW = 1 };
@@ -174,13 +191,15 @@ enum {
   TQ_DEV_BAD_BLOCK = 2,       /* block table entry outside [0, num_blocks) */
   TQ_DEV_BAD_CONTEXT = 4,     /* context length < 0 or > max_blocks_per_seq * 16 */
   TQ_DEV_WAIT_TIMEOUT = 8,    /* a bounded wait on a copy gave up */
+  TQ_DEV_BAD_ROW = 32,        /* parent row outside [-1, rows) in a reordering */
+  TQ_DEV_NO_BLOCK = 64,       /* a call asked for more blocks than were free */
   TQ_DEV_LAYOUT = 16          /* decode found less shared memory than its layout needs (no work done) */
 };
 
 typedef struct {
-  int32_t kv_format; /* TQ_KV_PACKED, TQ_KV_BF16, TQ_KV_K8V4 or TQ_KV_POLAR */
-  int32_t bits_k;    /* packed: 2, 3 or 4; k8v4: 8 (FP8 E4M3 keys); polar: 2, 3 or 4 bits per angle */
-  int32_t bits_v;    /* packed, k8v4 and polar: 2, 3 or 4 */
+  int32_t kv_format; /* TQ_KV_PACKED, TQ_KV_BF16, TQ_KV_K8V4, TQ_KV_POLAR or TQ_KV_INT8 */
+  int32_t bits_k;    /* packed: 2, 3 or 4; k8v4: 8 (FP8 E4M3 keys); polar: 2, 3 or 4 bits per angle; int8: 8 */
+  int32_t bits_v;    /* packed, k8v4 and polar: 2, 3 or 4; int8: 8 */
   int32_t qjl_k;     /* packed: 1 = keys carry the 1-bit QJL residual (m = head_dim); k8v4, polar: 0 */
   int32_t rot_kind;  /* packed and k8v4 (values): TQ_ROT_HADAMARD or TQ_ROT_DENSE; polar: TQ_ROT_HADAMARD */
   int32_t norm_mode; /* TQ_NORM_CORRECTED or TQ_NORM_RAW */
@@ -419,6 +438,26 @@ tq_status tq_rope_append(const tq_cache_desc* desc, const tq_rope* rope, const t
                          const tq_heads* v, int in_dtype, const int64_t* positions, const int64_t* slot_mapping,
                          int64_t n_tokens, void* stream);
 
+/* Workspace bytes tq_attend needs, for any n_tokens, batch and block tables up to these; 0 on error. */
+size_t tq_attend_workspace_bytes(const tq_cache_desc* desc, int64_t n_tokens, int batch, int num_q_heads,
+                                 int max_blocks_per_seq);
+
+/* Causal attention of the last tokens of each sequence over the cache: a prompt, a chunk
+ * of one, drafted tokens to verify.  The queries of sequence b are the rows query_starts[b]
+ * .. query_starts[b + 1] - 1 of q (device int32 [batch + 1], ascending, from 0 on) and the last
+ * n_b = query_starts[b + 1] - query_starts[b] of its context_lens[b] tokens, whose keys and
+ * values are in the cache already; row i of them attends to its first context_lens[b] - n_b + 1
+ * + i tokens (to none, with a zero row, where that is not positive).  A sequence may have
+ * no queries.  Rows from query_starts[batch] on are neither read nor written.  q: rows of
+ * q_dtype and output rows of out_dtype with free token and head strides; out == in is allowed
+ * for equal types and strides.  block_table, context_lens, sm_scale, the workspace contract (at
+ * least tq_attend_workspace_bytes(...), zero before the first call) and errors as for
+ * tq_decode_attention; one workspace serves both calls.  int8 layers only
+ * (TQ_ERR_UNSUPPORTED otherwise). */
+tq_status tq_attend(const tq_cache_desc* desc, const tq_heads* q, int q_dtype, int out_dtype, int64_t n_tokens,
+                    const int32_t* query_starts, int batch, const int32_t* block_table, int max_blocks_per_seq,
+                    const int32_t* context_lens, float sm_scale, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Workspace bytes tq_prefix_decode needs for this layer's kind, batch and heads with prefixes up to
  * prefix_len and block tables up to max_blocks_per_seq wide; 0 on error. */
 size_t tq_prefix_workspace_bytes(const tq_cache_desc* desc, int batch, int num_q_heads, int64_t prefix_len,
@@ -514,6 +553,72 @@ tq_status tq_decode_attention_static(const tq_cache_desc* desc, const void* q, i
                                      int num_q_heads, const int32_t* block_table, int max_blocks_per_seq,
                                      const int32_t* context_lens, float sm_scale, void* out, int out_dtype,
                                      int num_splits, void* stream);
+
+/* ---- blocks that sequences share ------------------------------------------
+ *
+ * One count a block, refs[id]: how many entries of the caller's tables hold it; 0: it is
+ * free.  Rows of a table hold the blocks of their first lens[row] tokens, ceil(lens / 16)
+ * entries; what stands behind them has no meaning.  Full blocks may be held by several
+ * rows; a block that is not full belongs to one.  Free blocks are given out lowest
+ * first, in the order of the rows and of the entries in a row, so that every call is a
+ * function of its inputs.  All decisions are taken on the device: a call that runs out of
+ * blocks records TQ_DEV_NO_BLOCK and leaves -1 in the entries that got none, entries outside
+ * [0, num_blocks) are left as they are, counted nowhere and recorded (TQ_DEV_BAD_BLOCK, as is a
+ * count that would fall below zero), lengths outside a row are cut to it and recorded
+ * (TQ_DEV_BAD_CONTEXT).  Calls on one pool change its counts and share its workspace: they follow
+ * one another on a stream (or are ordered by events).
+ * Layers (an array of descriptors, as in tq_quantize_append_layers) are those whose pages move
+ * with the ids: distinct caches of any formats, each with the pool's num_blocks; every layer that
+ * the tables index belongs among them.  n_layers may be 0 (but for tq_copy_blocks). */
+typedef struct {
+  int64_t num_blocks;     /* up to 2^30 */
+  int32_t* refs;          /* device [num_blocks] */
+  void* workspace;        /* device, 256-byte aligned, any contents */
+  size_t workspace_bytes; /* at least tq_blocks_workspace_bytes(num_blocks, rows of the call) */
+} tq_block_pool;
+
+typedef struct {
+  int32_t* table; /* device [rows][max_blocks] */
+  int32_t* lens;  /* device [rows]: tokens of each row */
+  int32_t rows;   /* up to 2^20 */
+  int32_t max_blocks;
+} tq_block_rows;
+
+/* Workspace bytes for calls of up to so many rows (of a reordering: the old or the new ones, whichever
+ * are more); 0 on error. */
+size_t tq_blocks_workspace_bytes(int64_t num_blocks, int rows);
+
+/* Pages of block src[i] to block dst[i] in both pools of every layer, i < n (device int32 arrays).  A pair
+ * of two negative ids is skipped; of pairs with the same destination the last one counts; a pair
+ * whose source is the destination of another one, or with an id outside the pool, is skipped and
+ * recorded (TQ_DEV_BAD_BLOCK).  Counts are not touched. */
+tq_status tq_copy_blocks(const tq_cache_desc* const* descs, int n_layers, const int32_t* src, const int32_t* dst, int64_t n,
+                         void* stream);
+
+/* Blocks for more tokens: the entries of row b from ceil(lens[b] / 16) up to ceil(new_lens[b] / 16)
+ * (device int32 [rows]) take free blocks, each held once from then on.  lens stays. */
+tq_status tq_blocks_extend(const tq_block_pool* pool, const tq_block_rows* rows, const int32_t* new_lens, void* stream);
+
+/* The rows b with which[b] != 0 (device bytes [rows]; NULL: all) give up their blocks: counts go down,
+ * their entries become -1 and their lengths 0. */
+tq_status tq_blocks_release(const tq_block_pool* pool, const tq_block_rows* rows, const uint8_t* which, void* stream);
+
+/* Rows in a new order: new row i is a fork of old row parents[i] (device int32 [to->rows]; -1: an empty
+ * row; any other value outside the rows as well, recorded as TQ_DEV_BAD_ROW).  A parent may have any number
+ * of children; the blocks of a row without children are given up.  Children share their parent's full
+ * blocks; its last block, if it is not full, goes to the first child, and each other child takes a
+ * free block with a copy of its pages in every layer (free after what this call gives up).  Entries of `to`
+ * behind a row's last block become -1, its lens are written.  `to` has from's max_blocks and memory of its
+ * own; the old rows hold nothing afterwards. */
+tq_status tq_blocks_reorder(const tq_block_pool* pool, const tq_cache_desc* const* descs, int n_layers, const tq_block_rows* from,
+                            const int32_t* parents, const tq_block_rows* to, void* stream);
+
+/* The used blocks, `live` of them, to the ids [0, live): the k-th used block from `live` on moves to the k-th
+ * free one below, with its pages in every layer and its count.  The entries of the given tables follow (every
+ * table that indexes the layers belongs among them, none twice); live (device int32, may be NULL)
+ * takes the number, moved (device int32 [num_blocks], may be NULL) where each block is now. */
+tq_status tq_blocks_compact(const tq_block_pool* pool, const tq_cache_desc* const* descs, int n_layers, const tq_block_rows* tables,
+                            int n_tables, int32_t* live, int32_t* moved, void* stream);
 
 /* ---- status ------------------------------------------------------------- */
 

@@ -23,11 +23,12 @@ TQ_MAX_GROUP = 8
 TQ_OK, TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED, TQ_ERR_WORKSPACE, TQ_ERR_CUDA, TQ_ERR_DEVICE, TQ_ERR_VERSION = range(7)
 TQ_F32, TQ_BF16 = 0, 1
 TQ_ROT_HADAMARD, TQ_ROT_DENSE, TQ_RNG_QJL = 1, 2, 3
-TQ_KV_PACKED, TQ_KV_BF16, TQ_KV_K8V4, TQ_KV_POLAR = 0, 1, 2, 3
+TQ_KV_PACKED, TQ_KV_BF16, TQ_KV_K8V4, TQ_KV_POLAR, TQ_KV_INT8 = 0, 1, 2, 3, 4
 TQ_NORM_CORRECTED, TQ_NORM_RAW = 0, 1
 TQ_ROPE_HALF, TQ_ROPE_INTERLEAVED = 0, 1
 TQ_ROPE_SCALE_NONE, TQ_ROPE_SCALE_LINEAR, TQ_ROPE_SCALE_NTK, TQ_ROPE_SCALE_BANDED, TQ_ROPE_SCALE_YARN = range(5)
 TQ_DEV_BAD_SLOT, TQ_DEV_BAD_BLOCK, TQ_DEV_BAD_CONTEXT, TQ_DEV_WAIT_TIMEOUT = 1, 2, 4, 8
+TQ_DEV_BAD_ROW, TQ_DEV_NO_BLOCK = 32, 64
 
 STATUS_NAMES = {
     TQ_OK: "TQ_OK", TQ_ERR_INVALID_ARG: "TQ_ERR_INVALID_ARG", TQ_ERR_UNSUPPORTED: "TQ_ERR_UNSUPPORTED",
@@ -72,6 +73,16 @@ class Heads(ctypes.Structure):
                 ("out_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64)]
 
 
+class BlockPool(ctypes.Structure):
+    _fields_ = [("num_blocks", ctypes.c_int64), ("refs", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
+class BlockRows(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("rows", ctypes.c_int32),
+                ("max_blocks", ctypes.c_int32)]
+
+
 _P = ctypes.POINTER
 _D = ctypes.POINTER(CacheDesc)
 _R = ctypes.POINTER(RopeDesc)
@@ -107,6 +118,10 @@ _SIGNATURES = {
                                      ctypes.c_void_p]),
     "tq_rope_append": (ctypes.c_int, [_D, _R, _H, _H, _H, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
                                       ctypes.c_int64, ctypes.c_void_p]),
+    "tq_attend_workspace_bytes": (ctypes.c_size_t, [_D, ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int]),
+    "tq_attend": (ctypes.c_int, [_D, _H, ctypes.c_int, ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int,
+                                 ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p,
+                                 ctypes.c_size_t, ctypes.c_void_p]),
     "tq_prefix_workspace_bytes": (ctypes.c_size_t, [_D, ctypes.c_int, ctypes.c_int, ctypes.c_int64, ctypes.c_int]),
     "tq_prefix_decode": (ctypes.c_int, [_D, ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                         ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int,
@@ -114,6 +129,15 @@ _SIGNATURES = {
                                         ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "tq_dequantize": (ctypes.c_int, [_D, ctypes.c_int, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
                                      ctypes.c_int, ctypes.c_void_p]),
+    "tq_blocks_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int]),
+    "tq_copy_blocks": (ctypes.c_int, [_P(_D), ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                                      ctypes.c_void_p]),
+    "tq_blocks_extend": (ctypes.c_int, [_P(BlockPool), _P(BlockRows), ctypes.c_void_p, ctypes.c_void_p]),
+    "tq_blocks_release": (ctypes.c_int, [_P(BlockPool), _P(BlockRows), ctypes.c_void_p, ctypes.c_void_p]),
+    "tq_blocks_reorder": (ctypes.c_int, [_P(BlockPool), _P(_D), ctypes.c_int, _P(BlockRows), ctypes.c_void_p,
+                                         _P(BlockRows), ctypes.c_void_p]),
+    "tq_blocks_compact": (ctypes.c_int, [_P(BlockPool), _P(_D), ctypes.c_int, _P(BlockRows), ctypes.c_int,
+                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
     "tq_image_bytes": (ctypes.c_size_t, [_D, ctypes.c_int64]),
     "tq_offload_blocks": (ctypes.c_int, [_D, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t,
                                          ctypes.c_void_p]),
@@ -399,8 +423,9 @@ class Layer:
     """One layer of the paged cache: device pools, rotation and codebooks.
 
     kv_format: "packed" (TurboQuant codes), "bf16" (boundary layers), "k8v4"
-    (FP8 E4M3 keys with TurboQuant values of bits_v) or "polar" (PolarQuant
-    angle codes of bits_k / bits_v bits with an fp16 radius; Hadamard only).
+    (FP8 E4M3 keys with TurboQuant values of bits_v), "polar" (PolarQuant
+    angle codes of bits_k / bits_v bits with an fp16 radius; Hadamard only) or
+    "int8" (8-bit codes with one step for each block and head; no rotation).
     The descriptor (`desc`) points at tensors owned by this object.
     """
 
@@ -411,8 +436,8 @@ class Layer:
         self.num_blocks = int(num_blocks)
         self.num_kv_heads = int(num_kv_heads)
         self.head_dim = TQ_HEAD_DIM
-        if kv_format not in ("packed", "bf16", "k8v4", "polar"):
-            raise ValueError("kv_format must be 'packed', 'bf16', 'k8v4' or 'polar'")
+        if kv_format not in ("packed", "bf16", "k8v4", "polar", "int8"):
+            raise ValueError("kv_format must be 'packed', 'bf16', 'k8v4', 'polar' or 'int8'")
         self.kv_format = kv_format
         self.packed = kv_format == "packed"
         self.k8v4 = kv_format == "k8v4"
@@ -425,11 +450,14 @@ class Layer:
         d.block_size = TQ_BLOCK_SIZE
         d.num_blocks = self.num_blocks
         d.fmt.kv_format = {"packed": TQ_KV_PACKED, "bf16": TQ_KV_BF16, "k8v4": TQ_KV_K8V4,
-                           "polar": TQ_KV_POLAR}[kv_format]
-        if self.k8v4:
+                           "polar": TQ_KV_POLAR, "int8": TQ_KV_INT8}[kv_format]
+        self.int8 = kv_format == "int8"
+        if self.k8v4 or self.int8:
             bits_k = 8
-        d.fmt.bits_k = bits_k if coded_v else 0
-        d.fmt.bits_v = bits_v if coded_v else 0
+        if self.int8:
+            bits_v = 8
+        d.fmt.bits_k = bits_k if coded_v or self.int8 else 0
+        d.fmt.bits_v = bits_v if coded_v or self.int8 else 0
         d.fmt.qjl_k = 1 if (qjl and self.packed) else 0
         d.fmt.rot_kind = rot_kind if coded_v else 0
         d.fmt.norm_mode = norm_mode
@@ -590,6 +618,44 @@ class Layer:
                                     _heads(v, None, "v", n), _dtype_code(ref), pos, slots, n, _stream(stream)))
         return q_out
 
+    def attend_workspace_bytes(self, n_tokens, batch, num_q_heads, max_blocks_per_seq):
+        n = lib().tq_attend_workspace_bytes(ctypes.byref(self.desc), n_tokens, batch, num_q_heads, max_blocks_per_seq)
+        if n == 0:
+            raise TQError(TQ_ERR_INVALID_ARG, last_error() or "invalid sizes")
+        return int(n)
+
+    def attend(self, q, query_starts, block_table, context_lens, sm_scale=None, out=None, out_dtype=None,
+               workspace=None, stream=None):
+        """Causal attention of the last tokens of each sequence (tq_attend; int8 layers).  q
+        [n_tokens, H_q, d], any token and head strides; query_starts int32 [B + 1]: rows
+        query_starts[b] .. query_starts[b + 1] - 1 are the last tokens of sequence b, whose
+        context_lens[b] tokens are in the cache already; block_table int32 [B, max_blocks];
+        context_lens int32 [B].  Rows from query_starts[B] on are left as they were.  Returns out."""
+        torch = _torch()
+        n = int(q.shape[0])
+        _check_rows(q, "q", n)
+        if out is None:
+            out = _new(torch.empty, q.shape, q.dtype if out_dtype is None else out_dtype, q.device, stream)
+        elif out.shape != q.shape:
+            raise ValueError("out must be %s, got %s" % (tuple(q.shape), tuple(out.shape)))
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [batch, blocks]")
+        bsz, max_blocks = block_table.shape
+        starts = _index_ptr(query_starts, "query_starts", torch.int32, (bsz + 1,))
+        table = _index_ptr(block_table, "block_table", torch.int32, block_table.shape)
+        lens = _index_ptr(context_lens, "context_lens", torch.int32, (bsz,))
+        if sm_scale is None:
+            sm_scale = 1.0 / math.sqrt(self.head_dim)
+        if workspace is None:
+            workspace = _new(torch.zeros, self.attend_workspace_bytes(n, bsz, q.shape[1], max(1, max_blocks)), torch.uint8,
+                             q.device, stream)
+        sq, so = q.stride(), _check_rows(out, "out", n)
+        rows = Heads(q.data_ptr(), out.data_ptr(), q.shape[1], sq[0], sq[1], so[0], so[1])
+        _check(lib().tq_attend(_byref(self.desc), _byref(rows), _dtype_code(q), _dtype_code(out), n, starts, bsz, table,
+                               max_blocks, lens, ctypes.c_float(sm_scale), _ptr(workspace, "workspace"), workspace.numel(),
+                               _stream(stream)))
+        return out
+
     def prefix_workspace_bytes(self, batch, num_q_heads, prefix_len, max_blocks_per_seq):
         n = lib().tq_prefix_workspace_bytes(ctypes.byref(self.desc), batch, num_q_heads, prefix_len,
                                             max_blocks_per_seq)
@@ -677,6 +743,100 @@ def append_layers(layers, ks, vs, slot_mapping, stream=None):
     ref = (ks if ks is not None else vs)[0]
     _check(lib().tq_quantize_append_layers(descs, n_layers, ptrs(ks, "k"), ptrs(vs, "v"), _dtype_code(ref),
                                            _ptr(slot_mapping, "slot_mapping"), int(ref.shape[0]), _stream(stream)))
+
+
+def _descs(layers):
+    return (ctypes.POINTER(CacheDesc) * len(layers))(*[ctypes.pointer(ly.desc) for ly in layers])
+
+
+def copy_blocks(layers, src, dst, stream=None):
+    """Pages of block src[i] to block dst[i] (int32, on the device) in both pools of every layer (tq_copy_blocks)."""
+    torch = _torch()
+    n = int(src.shape[0])
+    _check(lib().tq_copy_blocks(_descs(layers), len(layers), _index_ptr(src, "src", torch.int32, (n,)),
+                                _index_ptr(dst, "dst", torch.int32, (n,)), n, _stream(stream)))
+
+
+class Blocks:
+    """The blocks of the layers that share block ids: how many table entries hold each (`refs`, int32
+    [num_blocks], 0: free), and the calls that hand them out, share, copy and move them.
+
+    A row of a block table [rows, max_blocks] (int32) holds the blocks of its first context_lens[row]
+    tokens (int32).  All calls are enqueued and decided on the device, lowest free block first; what went
+    wrong stands in get_device_status().  Calls of one object follow one another on a stream.
+    `layers`: the layers whose pages go with the ids (any formats, num_blocks blocks each)."""
+
+    def __init__(self, num_blocks, device="cuda"):
+        torch = _torch()
+        self.num_blocks = int(num_blocks)
+        self.refs = torch.zeros(self.num_blocks, dtype=torch.int32, device=device)
+        self._workspaces = []  # (earlier ones too: captured graphs may use them)
+        self._rows = -1
+
+    def _pool(self, rows, stream):
+        torch = _torch()
+        if rows > self._rows:
+            size = lib().tq_blocks_workspace_bytes(self.num_blocks, rows)
+            if size == 0:
+                raise TQError(TQ_ERR_INVALID_ARG, last_error() or "invalid sizes")
+            self._workspaces.append(_new(torch.empty, (int(size),), torch.uint8, self.refs.device, stream))
+            self._rows = rows
+        ws = self._workspaces[-1]
+        refs = _index_ptr(self.refs, "refs", torch.int32, (self.num_blocks,))
+        return _byref(BlockPool(self.num_blocks, refs, ws.data_ptr(), ws.numel()))
+
+    @staticmethod
+    def _table(block_table, context_lens):
+        torch = _torch()
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [rows, blocks], got %s" % (tuple(block_table.shape),))
+        rows, width = block_table.shape
+        return BlockRows(_index_ptr(block_table, "block_table", torch.int32, (rows, width)),
+                         _index_ptr(context_lens, "context_lens", torch.int32, (rows,)), rows, width)
+
+    def extend(self, block_table, context_lens, new_lens, stream=None):
+        """Blocks for new_lens [rows] (int32) tokens a row, written into block_table (tq_blocks_extend)."""
+        rows = self._table(block_table, context_lens)
+        grown = _index_ptr(new_lens, "new_lens", _torch().int32, (rows.rows,))
+        _check(lib().tq_blocks_extend(self._pool(rows.rows, stream), _byref(rows), grown, _stream(stream)))
+
+    def release(self, block_table, context_lens, which=None, stream=None):
+        """The rows with which[row] (bool; None: all) give up their blocks, in place (tq_blocks_release)."""
+        rows = self._table(block_table, context_lens)
+        mask = None if which is None else _index_ptr(which, "which", _torch().bool, (rows.rows,))
+        _check(lib().tq_blocks_release(self._pool(0, stream), _byref(rows), mask, _stream(stream)))
+
+    def reorder(self, layers, block_table, context_lens, parents, stream=None):
+        """New rows [len(parents)], each a fork of old row parents[i] (int32; -1: an empty row): full blocks
+        are shared, a last block that is not full is copied for all children but the first, rows without
+        children give up theirs (tq_blocks_reorder).  Returns (block_table, context_lens) of the new rows."""
+        torch = _torch()
+        old = self._table(block_table, context_lens)
+        if parents.dim() != 1:
+            raise ValueError("parents must be one row, got %s" % (tuple(parents.shape),))
+        n = int(parents.shape[0])
+        index = _index_ptr(parents, "parents", torch.int32, (n,))
+        table = _new(torch.empty, (n, old.max_blocks), torch.int32, block_table.device, stream)
+        lens = _new(torch.empty, (n,), torch.int32, block_table.device, stream)
+        new = self._table(table, lens)
+        _check(lib().tq_blocks_reorder(self._pool(max(old.rows, n), stream), _descs(layers), len(layers), _byref(old), index,
+                                       _byref(new), _stream(stream)))
+        return table, lens
+
+    def compact(self, layers, block_table, context_lens, *more, moved=None, stream=None):
+        """The used blocks to the lowest ids, tables rewritten in place (tq_blocks_compact); `more`: further
+        tables and lengths in turn; moved: int32 [num_blocks] that takes where each block is now.  Returns the
+        number of used blocks (int32 [1], on the device)."""
+        torch = _torch()
+        if len(more) % 2 != 0:
+            raise ValueError("further tables come with their lengths")
+        pairs = [(block_table, context_lens)] + [(more[i], more[i + 1]) for i in range(0, len(more), 2)]
+        tables = (BlockRows * len(pairs))(*[self._table(t, n) for t, n in pairs])
+        live = _new(torch.empty, (1,), torch.int32, self.refs.device, stream)
+        to = None if moved is None else _index_ptr(moved, "moved", torch.int32, (self.num_blocks,))
+        _check(lib().tq_blocks_compact(self._pool(0, stream), _descs(layers), len(layers), tables, len(pairs), live.data_ptr(), to,
+                                       _stream(stream)))
+        return live
 
 
 def get_device_status(stream=None):

@@ -64,6 +64,8 @@ tq_status check_append(const tq_cache_desc* desc, const void* k, const void* v, 
   if (!k && !v) return fail(TQ_ERR_INVALID_ARG, "%s: both k and v are null", fn);
   if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15)
     return fail(TQ_ERR_INVALID_ARG, "%s: k/v must be 16-byte aligned", fn);
+  if (desc->fmt.kv_format == TQ_KV_INT8 && n_tokens > (1 << 30))
+    return fail(TQ_ERR_UNSUPPORTED, "%s: more than 2^30 tokens of an int8 layer", fn);
   const tq_layer_format& f = desc->fmt;
   const bool packed_k = f.kv_format == TQ_KV_PACKED,
              packed_v = f.kv_format == TQ_KV_PACKED || f.kv_format == TQ_KV_K8V4;  // codebook quantizers
@@ -79,6 +81,8 @@ tq_status run_append(const tq_cache_desc* desc, const void* k, const void* v, in
                      const int64_t* slot_mapping, int64_t n_tokens, const DeviceInfo& di, cudaStream_t st,
                      bool pdl = false) {
   const tq_layer_format& f = desc->fmt;
+  if (f.kv_format == TQ_KV_INT8)
+    return cuda_result(launch_int8_append(*desc, k, v, in_dtype, slot_mapping, n_tokens, di.status, di.num_sms, st), "int8 append");
   const bool same_tables = std::memcmp(desc->centroids_k, desc->centroids_v, sizeof(desc->centroids_k)) == 0 &&
                            std::memcmp(desc->boundaries_k, desc->boundaries_v, sizeof(desc->boundaries_k)) == 0;
   if (k && v && f.kv_format == TQ_KV_PACKED && f.bits_k == f.bits_v && !f.qjl_k && same_tables)  // one launch
@@ -104,12 +108,19 @@ int resolve_splits(const tq_cache_desc* desc, int batch, int num_q_heads, int ma
   return tq_auto_splits(desc, batch, num_q_heads, max_blocks);
 }
 
+// Workspace of a decode or attend call over an int8 layer.
+size_t int8_workspace(int num_sms) { return kCounterRegionBytes + int8_partial_bytes(num_sms); }
+
+cudaError_t run_decode(const DecodeCall& c, const DeviceInfo& di, cudaStream_t st) {
+  return c.desc->fmt.kv_format == TQ_KV_INT8 ? launch_int8_decode(c, di.num_sms, st) : launch_decode(c, st);
+}
+
 // Checks of tq_decode_attention's arguments and the call they describe (batch
 // == 0 passes with *c unset: nothing to do).
 tq_status prepare_decode(const tq_cache_desc* desc, const void* q, int q_dtype, int batch, int num_q_heads,
                          const int32_t* block_table, int max_blocks_per_seq, const int32_t* context_lens,
                          float sm_scale, void* out, int out_dtype, void* workspace, size_t workspace_bytes,
-                         int num_splits, const char* fn, DecodeCall* c) {
+                         int num_splits, const char* fn, DecodeCall* c, DeviceInfo* di_out = nullptr) {
   tq_status s = check_desc(desc);
   if (s != TQ_OK) return s;
   if (batch < 0) return fail(TQ_ERR_INVALID_ARG, "%s: batch < 0", fn);
@@ -128,10 +139,11 @@ tq_status prepare_decode(const tq_cache_desc* desc, const void* q, int q_dtype, 
   if (reinterpret_cast<uintptr_t>(q) & 15) return fail(TQ_ERR_INVALID_ARG, "%s: q must be 16-byte aligned", fn);
   DeviceInfo di;
   if ((s = device_info(&di)) != TQ_OK) return s;
-  const int splits = resolve_splits(desc, batch, num_q_heads, max_blocks_per_seq, num_splits);
-  if (splits < 1) return fail(TQ_ERR_INVALID_ARG, "%s: could not choose a split count", fn);
+  const bool int8 = desc->fmt.kv_format == TQ_KV_INT8;
+  const int splits = int8 ? num_splits : resolve_splits(desc, batch, num_q_heads, max_blocks_per_seq, num_splits);
+  if (!int8 && splits < 1) return fail(TQ_ERR_INVALID_ARG, "%s: could not choose a split count", fn);
   const bool qjl = desc->fmt.kv_format == TQ_KV_PACKED && desc->fmt.qjl_k;
-  const size_t need = decode_workspace(batch, num_q_heads, splits, desc->head_dim, qjl).total;
+  const size_t need = int8 ? int8_workspace(di.num_sms) : decode_workspace(batch, num_q_heads, splits, desc->head_dim, qjl).total;
   if (!workspace || workspace_bytes < need)
     return fail(TQ_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, workspace_bytes, need);
   if (reinterpret_cast<uintptr_t>(workspace) & 255)
@@ -151,6 +163,7 @@ tq_status prepare_decode(const tq_cache_desc* desc, const void* q, int q_dtype, 
   c->splits = splits;
   c->status = di.status;
   c->after_append = false;
+  if (di_out) *di_out = di;
   return TQ_OK;
 }
 
@@ -184,6 +197,16 @@ size_t own_workspace(const tq_cache_desc* desc, int batch, int num_q_heads, int 
 }
 
 }  // namespace
+
+tq_status device_status(unsigned** status, int* num_sms) {
+  DeviceInfo di;
+  const tq_status s = device_info(&di);
+  if (s != TQ_OK) return s;
+  *status = di.status;
+  *num_sms = di.num_sms;
+  return TQ_OK;
+}
+
 }  // namespace tq
 
 using namespace tq;
@@ -253,6 +276,8 @@ int tq_auto_splits(const tq_cache_desc* desc, int batch, int num_q_heads, int ma
   DeviceInfo di;
   if (device_info(&di) != TQ_OK) return 0;
   const int g = num_q_heads / desc->num_kv_heads;
+  if (desc->fmt.kv_format == TQ_KV_INT8)  // (ranges of the whole batch: on average so many a unit)
+    return auto_splits(di.num_sms, 16, batch, desc->num_kv_heads * ((g + 7) / 8), max_blocks_per_seq);
   const int hpw = g <= 4 ? 4 : 8;  // heads per decode warp
   const int groups = (g + hpw - 1) / hpw;
   return auto_splits(di.num_sms, decode_warps(*desc, g), batch, desc->num_kv_heads * groups, max_blocks_per_seq);
@@ -263,6 +288,10 @@ size_t tq_workspace_bytes(const tq_cache_desc* desc, int batch, int num_q_heads,
                           int num_splits) {
   clear_error();
   if (check_desc(desc, false) != TQ_OK || batch < 1 || num_q_heads < 1 || max_blocks_per_seq < 1 || num_splits < 0) return 0;
+  if (desc->fmt.kv_format == TQ_KV_INT8) {
+    DeviceInfo di;
+    return device_info(&di) == TQ_OK ? int8_workspace(di.num_sms) : 0;
+  }
   const int splits = resolve_splits(desc, batch, num_q_heads, max_blocks_per_seq, num_splits);
   if (splits < 1) return 0;
   const bool qjl = desc->fmt.kv_format == TQ_KV_PACKED && desc->fmt.qjl_k;
@@ -275,11 +304,12 @@ tq_status tq_decode_attention(const tq_cache_desc* desc, const void* q, int q_dt
                               int num_splits, void* stream) {
   clear_error();
   DecodeCall c;
+  DeviceInfo di;
   tq_status s = prepare_decode(desc, q, q_dtype, batch, num_q_heads, block_table, max_blocks_per_seq, context_lens,
                                sm_scale, out, out_dtype, workspace, workspace_bytes, num_splits, "tq_decode_attention",
-                               &c);
+                               &c, &di);
   if (s != TQ_OK || batch == 0) return s;
-  return cuda_result(launch_decode(c, reinterpret_cast<cudaStream_t>(stream)), "decode attention");
+  return cuda_result(run_decode(c, di, reinterpret_cast<cudaStream_t>(stream)), "decode attention");
 }
 
 tq_status tq_decode_step(const tq_cache_desc* desc, const void* k_new, const void* v_new, int in_dtype,
@@ -317,18 +347,18 @@ tq_status tq_append_decode(const tq_cache_desc* desc, const void* k, const void*
   tq_status s = check_append(desc, k, v, in_dtype, slot_mapping, n_tokens, "tq_append_decode");
   if (s != TQ_OK) return s;
   DecodeCall c;
+  DeviceInfo di;
   s = prepare_decode(desc, q, q_dtype, batch, num_q_heads, block_table, max_blocks_per_seq, context_lens, sm_scale,
-                     out, out_dtype, workspace, workspace_bytes, num_splits, "tq_append_decode", &c);
+                     out, out_dtype, workspace, workspace_bytes, num_splits, "tq_append_decode", &c, &di);
   if (s != TQ_OK) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (n_tokens > 0) {
-    DeviceInfo di;
     if ((s = device_info(&di)) != TQ_OK) return s;
     if ((s = run_append(desc, k, v, in_dtype, slot_mapping, n_tokens, di, st)) != TQ_OK) return s;
     c.after_append = true;
   }
   if (batch == 0) return TQ_OK;
-  return cuda_result(launch_decode(c, st), "decode attention");
+  return cuda_result(run_decode(c, di, st), "decode attention");
 }
 
 tq_status tq_rope_apply(const tq_rope* rope, int transpose, const tq_heads* q, const tq_heads* k, int dtype,
@@ -367,7 +397,7 @@ tq_status tq_rope_append(const tq_cache_desc* desc, const tq_rope* rope, const t
   if (s != TQ_OK) return s;
   if ((s = check_rope(rope, "tq_rope_append")) != TQ_OK) return s;
   const tq_layer_format& f = desc->fmt;
-  if (f.kv_format == TQ_KV_POLAR || (f.kv_format == TQ_KV_PACKED && f.qjl_k) ||
+  if (f.kv_format == TQ_KV_POLAR || f.kv_format == TQ_KV_INT8 || (f.kv_format == TQ_KV_PACKED && f.qjl_k) ||
       (f.kv_format != TQ_KV_BF16 && f.rot_kind != TQ_ROT_HADAMARD))
     return fail(TQ_ERR_UNSUPPORTED,
                 "tq_rope_append: bf16, k8v4 and packed layers with a Hadamard rotation and no QJL keys only; rotate "
@@ -404,6 +434,68 @@ tq_status tq_rope_append(const tq_cache_desc* desc, const tq_rope* rope, const t
   return cuda_result(launch_rope_append(c, *desc, reinterpret_cast<cudaStream_t>(stream)), "rotated append");
 }
 
+size_t tq_attend_workspace_bytes(const tq_cache_desc* desc, int64_t n_tokens, int batch, int num_q_heads,
+                                 int max_blocks_per_seq) {
+  clear_error();
+  if (check_desc(desc, false) != TQ_OK) return 0;
+  if (desc->fmt.kv_format != TQ_KV_INT8 || n_tokens < 0 || batch < 0 || num_q_heads < 1 ||
+      num_q_heads % desc->num_kv_heads != 0 || max_blocks_per_seq < 1) {
+    fail(TQ_ERR_INVALID_ARG, "tq_attend_workspace_bytes: an int8 layer, n_tokens %lld, batch %d, num_q_heads %d, max_blocks %d",
+         (long long)n_tokens, batch, num_q_heads, max_blocks_per_seq);
+    return 0;
+  }
+  DeviceInfo di;
+  return device_info(&di) == TQ_OK ? int8_workspace(di.num_sms) : 0;
+}
+
+tq_status tq_attend(const tq_cache_desc* desc, const tq_heads* q, int q_dtype, int out_dtype, int64_t n_tokens,
+                    const int32_t* query_starts, int batch, const int32_t* block_table, int max_blocks_per_seq,
+                    const int32_t* context_lens, float sm_scale, void* workspace, size_t workspace_bytes, void* stream) {
+  clear_error();
+  const char* fn = "tq_attend";
+  tq_status s = check_desc(desc);
+  if (s != TQ_OK) return s;
+  if (desc->fmt.kv_format != TQ_KV_INT8) return fail(TQ_ERR_UNSUPPORTED, "%s: int8 layers only", fn);
+  if (!q) return fail(TQ_ERR_INVALID_ARG, "%s: null q", fn);
+  if (!valid_dtype(q_dtype) || !valid_dtype(out_dtype))
+    return fail(TQ_ERR_INVALID_ARG, "%s: q_dtype %d / out_dtype %d", fn, q_dtype, out_dtype);
+  if (n_tokens < 0 || batch < 0) return fail(TQ_ERR_INVALID_ARG, "%s: n_tokens %lld, batch %d", fn, (long long)n_tokens, batch);
+  if ((s = check_heads(*q, q_dtype, n_tokens, true, "tq_attend: q")) != TQ_OK) return s;
+  if (reinterpret_cast<uintptr_t>(q->out) & (out_dtype == TQ_F32 ? 3 : 1))
+    return fail(TQ_ERR_INVALID_ARG, "%s: output rows not aligned to their elements", fn);
+  if (q->num_heads % desc->num_kv_heads != 0)
+    return fail(TQ_ERR_INVALID_ARG, "%s: %d heads not a multiple of num_kv_heads %d", fn, q->num_heads, desc->num_kv_heads);
+  if (max_blocks_per_seq < 1) return fail(TQ_ERR_INVALID_ARG, "%s: max_blocks_per_seq < 1", fn);
+  if (!(sm_scale == sm_scale)) return fail(TQ_ERR_INVALID_ARG, "%s: sm_scale is NaN", fn);
+  if (n_tokens == 0 || batch == 0) return TQ_OK;
+  if (n_tokens > (1 << 26) || batch > 65535)
+    return fail(TQ_ERR_UNSUPPORTED, "%s: more than 2^26 tokens or 65535 sequences", fn);
+  if (!query_starts || !block_table || !context_lens)
+    return fail(TQ_ERR_INVALID_ARG, "%s: null query_starts/block_table/context_lens", fn);
+  DeviceInfo di;
+  if ((s = device_info(&di)) != TQ_OK) return s;
+  const size_t need = int8_workspace(di.num_sms);
+  if (!workspace || workspace_bytes < need)
+    return fail(TQ_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, workspace_bytes, need);
+  if (reinterpret_cast<uintptr_t>(workspace) & 255)
+    return fail(TQ_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", fn);
+  AttendCall c = {};
+  c.desc = desc;
+  c.q = q;
+  c.q_dtype = q_dtype;
+  c.out_dtype = out_dtype;
+  c.n_tokens = n_tokens;
+  c.starts = query_starts;
+  c.batch = batch;
+  c.block_table = block_table;
+  c.max_blocks = max_blocks_per_seq;
+  c.ctx_lens = context_lens;
+  c.sm_scale = sm_scale;
+  c.workspace = reinterpret_cast<uint8_t*>(workspace);
+  c.status = di.status;
+  return cuda_result(launch_int8_attend(c, di.num_sms, reinterpret_cast<cudaStream_t>(stream)), "attend");
+}
+
 size_t tq_prefix_workspace_bytes(const tq_cache_desc* desc, int batch, int num_q_heads, int64_t prefix_len,
                                  int max_blocks_per_seq) {
   clear_error();
@@ -435,7 +527,7 @@ tq_status tq_prefix_decode(const tq_cache_desc* desc, const void* q, int q_dtype
   tq_status s = check_desc(desc);
   if (s != TQ_OK) return s;
   const tq_layer_format& f = desc->fmt;
-  if (f.kv_format == TQ_KV_POLAR || (f.kv_format == TQ_KV_PACKED && f.qjl_k) ||
+  if (f.kv_format == TQ_KV_POLAR || f.kv_format == TQ_KV_INT8 || (f.kv_format == TQ_KV_PACKED && f.qjl_k) ||
       (f.kv_format != TQ_KV_BF16 && f.rot_kind != TQ_ROT_HADAMARD))
     return fail(TQ_ERR_UNSUPPORTED, "%s: bf16, k8v4 and packed layers with a Hadamard rotation and no QJL keys only", fn);
   if (prefix_len < 0 || prefix_len > INT32_MAX)

@@ -377,6 +377,7 @@ namespace tq {
 size_t page_bytes_of(const tq_cache_desc& d, int which) {
   const size_t blk = (size_t)d.block_size;
   if (d.fmt.kv_format == TQ_KV_BF16) return blk * (size_t)d.head_dim * 2;
+  if (d.fmt.kv_format == TQ_KV_INT8) return blk * (size_t)d.head_dim + 16;  // codes, step and bits
   if (d.fmt.kv_format == TQ_KV_K8V4 && which == 0) return blk * (size_t)d.head_dim;  // FP8 E4M3 keys
   if (d.fmt.kv_format == TQ_KV_POLAR)  // angle-code records + fp16 radii
     return blk * (size_t)(d.head_dim * (which == 0 ? d.fmt.bits_k : d.fmt.bits_v) / 8) + blk * 2;
@@ -447,6 +448,11 @@ tq_status check_desc(const tq_cache_desc* d, bool need_data) {
   if (f.norm_mode != TQ_NORM_CORRECTED && f.norm_mode != TQ_NORM_RAW)
     return fail(TQ_ERR_INVALID_ARG, "norm_mode %d", f.norm_mode);
   if (f.kv_format == TQ_KV_BF16) return TQ_OK;
+  if (f.kv_format == TQ_KV_INT8) {
+    if (f.bits_k != 8 || f.bits_v != 8) return fail(TQ_ERR_INVALID_ARG, "int8: bits_k %d / bits_v %d must be 8", f.bits_k, f.bits_v);
+    if (f.qjl_k != 0) return fail(TQ_ERR_INVALID_ARG, "int8: keys carry no QJL residual");
+    return TQ_OK;
+  }
   if (f.kv_format == TQ_KV_K8V4) {  // FP8 E4M3 keys, packed values
     if (f.bits_k != 8) return fail(TQ_ERR_INVALID_ARG, "k8v4: bits_k %d must be 8", f.bits_k);
     if (f.bits_v < 2 || f.bits_v > 4) return fail(TQ_ERR_INVALID_ARG, "k8v4: bits_v %d not in 2..4", f.bits_v);

@@ -1,0 +1,32 @@
+// int8 layers of the cache: the page, and codes as fp16 operands (libtq, sm_103a).
+//
+// A page is one block of one KV head: 16 records of 128 bytes, byte = code + 128, then the tail
+// {fp32 step, uint32 bits of the tokens that hold a coordinate that is not finite, 8 bytes that an
+// append uses while it runs}.  A value is code * step, |code| <= 127.
+#pragma once
+
+#include "tq_device.cuh"
+#include "tq_internal.h"
+
+namespace tq {
+
+constexpr int kI8Codes = kBlock * kD;          // bytes of a page's records
+constexpr int kI8Page = kI8Codes + 16;         // and of a page
+constexpr float kI8Least = 1.1754943508222875e-38f;  // 2^-126, the least step
+
+struct I8Tail {
+  float step;
+  uint32_t bad;       // bit r: record r is not a number
+  uint32_t marks;     // (append) bit r: record r is written by this call
+  uint32_t first;     // (append) the first token of this call in the block
+};
+
+// Bytes lo and hi of w as two fp16 codes: the byte under the exponent of 1024 is 1024 + byte, exactly, and
+// 1024 + 128 comes off again.  `sel`: 0x4140 for bytes 0 and 1, 0x4342 for bytes 2 and 3.
+__device__ __forceinline__ uint32_t i8_pair(uint32_t w, uint32_t sel) {
+  const uint32_t u = prmt(w, 0x64646464u, sel);
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half((unsigned short)0x6480u)));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+}  // namespace tq

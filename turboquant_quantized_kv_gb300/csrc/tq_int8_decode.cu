@@ -1,0 +1,730 @@
+// Decode attention over int8 layers (libtq, sm_103a).
+//
+//     out[row] = softmax(sm_scale q[row] K^T) V,  K = codes * step of the block, V likewise
+//
+// for rows of one query token each: the sequences of tq_decode_attention, or the tokens of tq_int8_attend.
+// A unit is (row, KV head, group of up to eight query heads); a step is one block of 16 tokens of a unit.
+//
+// Work.  All steps of all units stand in one line (row by row, unit by unit, block by block) and the line
+// is cut into equal ranges, one a warp: whatever the contexts' lengths, every warp has the same number of
+// blocks.  A unit inside one range is finished by its warp; the warps of a CTA that share a unit meet in
+// shared memory, CTAs that share one (at most one unit begins in a CTA and goes on behind it) in the
+// workspace, where the CTA that arrives last joins the partials in the order of the line.
+//
+// A step.  A warp has the block's two pages (4 KB) copied into its ring two blocks ahead, 16-byte chunk c
+// of record r at c ^ (r & 7), so that all 128-bit reads are free of conflicts.  Codes become fp16 exactly
+// (i8_pair) and both products run as mma.sync m16n8k16 with fp32 sums:
+//     S [16 tokens x 8 columns] = K Q^T,  O^T [128 x 8 columns] += V^T P^T;
+// columns are four heads x (high part, low part) or eight heads in two passes, so that queries and weights
+// keep 22 bits.  A transpose in registers (movmatrix) brings P from the one layout to the other.
+//
+// Scales.  With u = log2 of a weight, m a running reference (moved only when u exceeds it by 16) and T one
+// for weight times step of V, p = 2^(u - m) goes into the denominator and w = p step 2^(m - T) <= 2^15 into
+// the product, so that a block with large values that nobody attends costs the others nothing.
+#include <math_constants.h>
+
+#include <atomic>
+
+#include "tq_async.cuh"
+#include "tq_int8.cuh"
+
+namespace tq {
+namespace {
+
+constexpr int kDecWarps = 16;
+constexpr int kDecThreads = kDecWarps * 32;
+constexpr int kDecStages = 2;
+constexpr int kDecStage = 2 * kI8Codes + 128;  // records of K, of V, both tails
+constexpr int kDecMinBlocks = 2;               // blocks a range at least
+constexpr int kPartRow = kD + 4;               // floats of a partial row in shared memory
+
+struct DecArgs {
+  const uint8_t* kpool;
+  const uint8_t* vpool;
+  int64_t num_blocks;
+  const int32_t* table;
+  int max_blocks;
+  const int32_t* ctx_lens;
+  const int32_t* starts;  // attend: first token of each sequence (null: a row is a sequence)
+  int seqs;
+  const void* q;
+  int q_bf16;
+  int64_t q_row, q_head;  // strides in elements
+  void* out;
+  int out_bf16;
+  int64_t o_row, o_head;
+  int rows, Hq, Hkv, g, ngroups;
+  float scale;  // sm_scale * log2 e
+  int splits;   // ranges a unit on average (0: one a warp of the GPU)
+  int* counters;
+  float* part;  // [2 grid][8][d]
+  float2* ml;   // [2 grid][8]
+  unsigned* status;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+
+// The sequence and the context of a row.
+__device__ __forceinline__ int row_seq(const DecArgs& a, int row) {
+  if (!a.starts) return row;
+  int lo = 0, hi = a.seqs - 1;  // the last sequence that starts at or before the row
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(a.starts + mid) <= row) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+__device__ __forceinline__ int row_ctx(const DecArgs& a, int row, int seq, bool flag) {
+  int ctx = __ldg(a.ctx_lens + seq);
+  const int most = a.max_blocks * kBlock;
+  if (ctx < 0 || ctx > most) {
+    if (flag) flag_status(a.status, TQ_DEV_BAD_CONTEXT);
+    ctx = ctx < 0 ? 0 : most;
+  }
+  if (a.starts) {  // causal: the sequence's last token sees all of it
+    const int next = __ldg(a.starts + seq + 1);
+    if (row < __ldg(a.starts + seq) || row >= next) return -1;  // behind the last sequence
+    ctx = max(0, ctx - (next - 1 - row));
+  }
+  return ctx;
+}
+__device__ __forceinline__ int blocks_of(int ctx) { return ctx > 0 ? (ctx + kBlock - 1) / kBlock : 0; }
+
+template <int NH>  // query heads of a unit: 4 or 8
+struct DecSmem {
+  alignas(128) unsigned char ring[kDecWarps][kDecStages][kDecStage];
+  float part[kDecWarps][NH][kPartRow];  // a warp's first segment, of a unit that began before
+  float2 ml[kDecWarps][2][8];           // references and denominators of the first and the last segment
+  int64_t unit0[kDecWarps][2];          // position in the line of the unit of either
+  int unit_row[kDecWarps][2], unit_sub[kDecWarps][2], unit_blocks[kDecWarps][2];
+  int kind[kDecWarps];                  // bit 0: has a first segment, bit 1: which does not end its unit, bit 2: has a last one
+  int64_t sums[kDecWarps];
+  int at_row[kDecWarps], at_sub[kDecWarps], at_block[kDecWarps], at_blocks[kDecWarps];
+  int arrived;
+};
+
+template <int NH>
+__global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_constant__ DecArgs a) {
+  constexpr int HL = NH / 4;  // heads a lane has logits of: lane & 3 (of four), 2 (lane & 3) and the next (of eight)
+  extern __shared__ __align__(128) unsigned char gen[];
+  DecSmem<NH>& sm = *reinterpret_cast<DecSmem<NH>*>(gen);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lg = lane >> 2, lt = lane & 3;
+  const int subs = a.Hkv * a.ngroups;  // units a row
+
+  // ---- the line: blocks before each thread's rows, and in all
+  const int per = (a.rows + kDecThreads - 1) / kDecThreads;
+  const int row0 = min(a.rows, (int)threadIdx.x * per), row1 = min(a.rows, row0 + per);
+  int64_t mine = 0;
+  for (int r = row0; r < row1; ++r) mine += blocks_of(row_ctx(a, r, row_seq(a, r), blockIdx.x == 0));
+  int64_t before = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t o = __shfl_up_sync(0xffffffffu, before, d);
+    if (lane >= d) before += o;
+  }
+  if (lane == 31) sm.sums[warp] = before;
+  if (threadIdx.x < kDecWarps) sm.kind[threadIdx.x] = 0;
+  __syncthreads();
+  int64_t total = 0;
+  before -= mine;
+#pragma unroll
+  for (int w = 0; w < kDecWarps; ++w) {
+    if (w < warp) before += sm.sums[w];
+    total += sm.sums[w];
+  }
+  total *= subs;
+  before *= subs;
+  mine *= subs;
+  // ---- ranges: R in all, `wide` of them a CTA
+  int64_t most = (total + kDecMinBlocks - 1) / kDecMinBlocks;
+  int64_t want = (int64_t)gridDim.x * kDecWarps;
+  if (a.splits > 0) want = min(want, (int64_t)a.rows * subs * a.splits);
+  const int64_t R = most < 1 ? 1 : (most < want ? most : want);
+  const int wide = (int)min((int64_t)kDecWarps, max((int64_t)4, (R + gridDim.x - 1) / gridDim.x));
+  auto cut = [&](int64_t r) { return total * min(r, R) / R; };
+  const int64_t r0 = (int64_t)blockIdx.x * wide;
+  for (int w = 0; w < wide; ++w) {
+    const int64_t at = cut(r0 + w);
+    if (r0 + w >= R || at < before || at >= before + mine) continue;
+    int64_t left = at - before;
+    for (int r = row0; r < row1; ++r) {
+      const int n = blocks_of(row_ctx(a, r, row_seq(a, r), false));
+      if (left < (int64_t)n * subs) {
+        sm.at_row[w] = r;
+        sm.at_sub[w] = (int)(left / n);
+        sm.at_block[w] = (int)(left % n);
+        sm.at_blocks[w] = n;
+        break;
+      }
+      left -= (int64_t)n * subs;
+    }
+  }
+  // rows without a token
+  for (int r = blockIdx.x + gridDim.x * warp; r < a.rows; r += gridDim.x * kDecWarps) {
+    if (row_ctx(a, r, row_seq(a, r), false) != 0) continue;
+    for (int i = lane; i < a.Hq * kD; i += 32) {
+      const int64_t o = (int64_t)r * a.o_row + (int64_t)(i / kD) * a.o_head + i % kD;
+      if (a.out_bf16) store_elem(reinterpret_cast<__nv_bfloat16*>(a.out) + o, 0.0f);
+      else store_elem(reinterpret_cast<float*>(a.out) + o, 0.0f);
+    }
+  }
+  __syncthreads();
+
+  float acc[8][4];
+  float m[HL], T[HL], l[HL];
+  auto clear = [&] {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[i][k] = 0.0f;
+#pragma unroll
+    for (int h = 0; h < HL; ++h) {
+      m[h] = T[h] = -INFINITY;
+      l[h] = 0.0f;
+    }
+  };
+  auto unit_heads = [&](int sub) { return min(8, a.g - 8 * (sub % a.ngroups)); };
+  auto first_head = [&](int sub) { return (sub / a.ngroups) * a.g + 8 * (sub % a.ngroups); };
+  auto store_row = [&](int row, int head, int c, const float* v, int n) {  // n coordinates from c on
+    const int64_t o = (int64_t)row * a.o_row + (int64_t)head * a.o_head + c;
+    if (a.out_bf16) {
+      __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(a.out) + o;
+      if ((reinterpret_cast<uintptr_t>(p) & 7u) == 0u) {
+        for (int k = 0; k < n; k += 4) {
+          const __nv_bfloat162 x = __floats2bfloat162_rn(v[k], v[k + 1]), y = __floats2bfloat162_rn(v[k + 2], v[k + 3]);
+          *reinterpret_cast<uint2*>(p + k) = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+        }
+      } else {
+        for (int k = 0; k < n; ++k) p[k] = __float2bfloat16_rn(v[k]);
+      }
+    } else {
+      float* p = reinterpret_cast<float*>(a.out) + o;
+      if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0u) {
+        for (int k = 0; k < n; k += 4) *reinterpret_cast<float4*>(p + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+      } else {
+        for (int k = 0; k < n; ++k) p[k] = v[k];
+      }
+    }
+  };
+
+  if (warp < wide && r0 + warp < R && total > 0) {
+    const int64_t begin = cut(r0 + warp), end = cut(r0 + warp + 1);
+    // the cursor of the copies
+    int irow = sm.at_row[warp], isub = sm.at_sub[warp], ij = sm.at_block[warp], in = sm.at_blocks[warp];
+    int row = irow, sub = isub, j = ij, nb = in;  // and of the steps
+    int iseq = row_seq(a, irow);
+    int ids = -1, window = -1;
+    int64_t ahead = begin;
+    const uint32_t ring = smem_u32(sm.ring[warp]);
+    int* const live = reinterpret_cast<int*>(sm.ring[warp][0] + 2 * kI8Codes + 32);  // (of stage s: kDecStage further)
+    const uint32_t dst = (uint32_t)((lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4));      // records lane / 8 + 8 i
+    const uint32_t dst4 = (uint32_t)(((lane >> 3) + 4) * 128 + (((lane & 7) ^ ((lane >> 3) + 4)) << 4));  // and the fourth after
+    auto issue = [&](int stage) {
+      if (ahead < end) {
+        if ((ij >> 5) != window) {
+          window = ij >> 5;
+          const int at = 32 * window + lane;
+          ids = at < in ? __ldg(a.table + (int64_t)iseq * a.max_blocks + at) : -1;
+        }
+        const int id = __shfl_sync(0xffffffffu, ids, ij & 31);
+        const bool ok = id >= 0 && id < a.num_blocks;
+        if (!ok && lane == 0) flag_status(a.status, TQ_DEV_BAD_BLOCK);
+        if (ok) {
+          const int64_t page = ((int64_t)id * a.Hkv + isub / a.ngroups) * kI8Page;
+          const uint8_t* k = a.kpool + page + 16 * lane;
+          const uint8_t* v = a.vpool + page + 16 * lane;
+          const uint32_t s = ring + (uint32_t)stage * kDecStage;
+          copy16(s + dst, k);
+          copy16(s + dst4, k + 512);
+          copy16(s + dst + 1024, k + 1024);
+          copy16(s + dst4 + 1024, k + 1536);
+          copy16(s + 2048 + dst, v);
+          copy16(s + 2048 + dst4, v + 512);
+          copy16(s + 2048 + dst + 1024, v + 1024);
+          copy16(s + 2048 + dst4 + 1024, v + 1536);
+          if (lane == 0) copy16(s + 4096, k + kI8Codes);
+          if (lane == 1) copy16(s + 4112, v + kI8Codes - 16);
+        }
+        if (lane == 0) live[stage * (kDecStage / 4)] = ok ? 1 : 0;
+        ++ahead;
+        if (++ij == in) {
+          ij = 0;
+          window = -1;
+          if (++isub == subs) {
+            isub = 0;
+            if (ahead < end) {
+              do {
+                ++irow;
+                iseq = row_seq(a, irow);
+                in = blocks_of(row_ctx(a, irow, iseq, false));
+              } while (in == 0);
+            }
+          }
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    issue(0);
+    issue(1);
+
+    clear();
+    uint32_t qh[8][2], ql[NH == 8 ? 8 : 1][2];
+    float cq[HL];
+    int ctx = 0;
+    auto load_unit = [&] {  // queries of the unit as operands: column lg, coordinates 32 lt + 4 i .. + 3 in step i
+      const int heads = unit_heads(sub), head = NH == 4 ? lg >> 1 : lg;
+      ctx = row_ctx(a, row, row_seq(a, row), false);
+      float x[32];
+      if (head < heads) {
+        const int64_t at = (int64_t)row * a.q_row + (int64_t)(first_head(sub) + head) * a.q_head + 32 * lt;
+        if (a.q_bf16) {
+          const __nv_bfloat16* p = reinterpret_cast<const __nv_bfloat16*>(a.q) + at;
+          if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0u) {
+            load32(p, x);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = __bfloat162float(p[i]);
+          }
+        } else {
+          const float* p = reinterpret_cast<const float*>(a.q) + at;
+          if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0u) {
+            load32(p, x);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = p[i];
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = 0.0f;
+      }
+      uint32_t top = 0u;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        x[i] *= a.scale;
+        top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+      }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // the row by a power of two, its largest magnitude below 2^8; a row that is not finite gives NaN
+      const int e = max((int)(top >> 23) - 126, -110);
+      const bool fine = top < 0x7F800000u;
+      const float f = __uint_as_float((uint32_t)(127 + 8 - min(e, 128)) << 23);
+      const float back = fine ? __uint_as_float((uint32_t)(127 + e - 8) << 23) : CUDART_NAN_F;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float x0 = fine ? x[4 * i + 2 * k] * f : 0.0f, x1 = fine ? x[4 * i + 2 * k + 1] * f : 0.0f;
+          const uint32_t hi = half2_bits(x0, x1);
+          const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+          const uint32_t lo = half2_bits(x0 - h.x, x1 - h.y);
+          if constexpr (NH == 4) {
+            qh[i][k] = lg & 1 ? lo : hi;
+          } else {
+            qh[i][k] = hi;
+            ql[i][k] = lo;
+          }
+        }
+      }
+      // lane lt's heads sit in columns (two columns a head of four)
+#pragma unroll
+      for (int h = 0; h < HL; ++h) cq[h] = __shfl_sync(0xffffffffu, back, 4 * (NH == 4 ? 2 * lt : 2 * lt + h));
+    };
+    load_unit();
+
+    bool began = j == 0;  // the segment begins its unit
+    for (int64_t at = begin; at < end; ++at) {
+      const int stage = (int)((at - begin) & 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      __syncwarp();
+      const uint32_t s = ring + (uint32_t)stage * kDecStage;
+      if (live[stage * (kDecStage / 4)]) {
+        const I8Tail* tails = reinterpret_cast<const I8Tail*>(sm.ring[warp][stage] + 2 * kI8Codes);
+        const float kstep = tails[0].step, vstep = tails[1].step;
+        const uint32_t kbad = tails[0].bad, vbad = tails[1].bad;
+        const int count = ctx - kBlock * j;  // tokens of the block, or more
+        // ---- logits
+        float S[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t col = (uint32_t)(((2 * lt + c) ^ lg) << 4);
+          const uint4 x = lds128(s + (uint32_t)lg * 128 + col), y = lds128(s + (uint32_t)(lg + 8) * 128 + col);
+          const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t a0 = i8_pair(xw[i], 0x4140u), a1 = i8_pair(yw[i], 0x4140u), a2 = i8_pair(xw[i], 0x4342u),
+                           a3 = i8_pair(yw[i], 0x4342u);
+            mma_f16(S, a0, a1, a2, a3, qh[4 * c + i][0], qh[4 * c + i][1]);
+            if constexpr (NH == 8) mma_f16(S, a0, a1, a2, a3, ql[4 * c + i][0], ql[4 * c + i][1]);
+          }
+        }
+        float u[HL][2];
+        const bool in0 = lg < count, in1 = lg + 8 < count;
+#pragma unroll
+        for (int h = 0; h < HL; ++h) {
+          const float k = kstep * cq[h];
+          u[h][0] = (NH == 4 ? S[0] + S[1] : S[h]) * k;
+          u[h][1] = (NH == 4 ? S[2] + S[3] : S[2 + h]) * k;
+        }
+        if (kbad) {
+#pragma unroll
+          for (int h = 0; h < HL; ++h) {
+            if ((kbad >> lg) & 1u) u[h][0] = CUDART_NAN_F;
+            if ((kbad >> (lg + 8)) & 1u) u[h][1] = CUDART_NAN_F;
+          }
+        }
+        // ---- references
+        const int vbits = (int)((__float_as_uint(vstep) >> 23) & 255u), ev = vbits - 127;
+        const float vmant = vbits == 0 ? 0.0f : __uint_as_float((__float_as_uint(vstep) & 0x7FFFFFu) | 0x3F800000u);
+        bool move = false;
+#pragma unroll
+        for (int h = 0; h < HL; ++h) {
+          const float most_u = fminf(m[h] + 16.0f, T[h] + (float)(14 - ev));
+          move |= (in0 && u[h][0] > most_u) || (in1 && u[h][1] > most_u);
+        }
+        if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+          for (int h = 0; h < HL; ++h) {
+            float top = fmaxf(in0 ? u[h][0] : -INFINITY, in1 ? u[h][1] : -INFINITY);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = ceilf(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)));
+            const float nm = fmaxf(m[h], top), nT = fmaxf(T[h], top + (float)(ev + 1 - 8));
+            if (nm != m[h]) l[h] *= exp2f(m[h] - nm);
+            m[h] = nm;
+            const float f = nT != T[h] ? exp2f(T[h] - nT) : 1.0f;
+            T[h] = nT;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              acc[i][HL == 1 ? 0 : h] *= f;
+              acc[i][HL == 1 ? 2 : 2 + h] *= f;
+              if constexpr (HL == 1) {
+                acc[i][1] *= f;
+                acc[i][3] *= f;
+              }
+            }
+          }
+        }
+        // ---- weights
+        uint32_t ph[2], pl[2];
+        float w[HL][2];
+#pragma unroll
+        for (int h = 0; h < HL; ++h) {
+          const float p0 = in0 ? ex2(u[h][0] - m[h]) : 0.0f, p1 = in1 ? ex2(u[h][1] - m[h]) : 0.0f;
+          l[h] += p0 + p1;
+          const float f = T[h] == -INFINITY ? 0.0f : vmant * ex2(fminf((float)ev + m[h] - T[h], 120.0f));
+          w[h][0] = p0 * f;
+          w[h][1] = p1 * f;
+        }
+        if (vbad) {
+#pragma unroll
+          for (int h = 0; h < HL; ++h) {
+            if (in0 && ((vbad >> lg) & 1u)) w[h][0] = CUDART_NAN_F;
+            if (in1 && ((vbad >> (lg + 8)) & 1u)) w[h][1] = CUDART_NAN_F;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if constexpr (NH == 4) {  // columns: high part, low part of the lane's head
+            const float hi = __half2float(__float2half_rn(w[0][k]));
+            ph[k] = transpose8(half2_bits(hi, w[0][k] - hi));
+          } else {
+            const uint32_t hi = half2_bits(w[0][k], w[HL - 1][k]);
+            const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+            ph[k] = transpose8(hi);
+            pl[k] = transpose8(half2_bits(w[0][k] - hf.x, w[HL - 1][k] - hf.y));
+          }
+        }
+        // ---- values: row lg of product i is coordinate 16 lg + 2 i, row lg + 8 the next
+        uint4 r[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int tok = 2 * lt + (k & 1) + 8 * (k >> 1);
+          r[k] = lds128(s + 2048u + (uint32_t)tok * 128 + (uint32_t)((lg ^ (tok & 7)) << 4));
+        }
+        const uint32_t* rw[4] = {&r[0].x, &r[1].x, &r[2].x, &r[3].x};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t sel = i & 1 ? 0x7362u : 0x5140u;
+          const uint32_t x = prmt(rw[0][i >> 1], rw[1][i >> 1], sel), y = prmt(rw[2][i >> 1], rw[3][i >> 1], sel);
+          const uint32_t a0 = i8_pair(x, 0x4140u), a1 = i8_pair(x, 0x4342u), a2 = i8_pair(y, 0x4140u), a3 = i8_pair(y, 0x4342u);
+          mma_f16(acc[i], a0, a1, a2, a3, ph[0], ph[1]);
+          if constexpr (NH == 8) mma_f16(acc[i], a0, a1, a2, a3, pl[0], pl[1]);
+        }
+      }
+      __syncwarp();
+      issue(stage);
+      // ---- the end of a unit or of the range
+      const bool last = at + 1 == end, done = j + 1 == nb;
+      if (done || last) {
+        float inv[HL];
+        float2 ml[HL];
+#pragma unroll
+        for (int h = 0; h < HL; ++h) {
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], d);
+          inv[h] = l[h] == 0.0f ? 0.0f : 1.0f / l[h];
+          ml[h] = make_float2(m[h], l[h]);
+        }
+        // normalised values of head hh of the lane: coordinates 16 lg .. 16 lg + 15
+        auto values = [&](int h, float (&o)[16]) {
+          const float shift = T[h] == -INFINITY ? 0.0f : T[h] - m[h], half = truncf(0.5f * shift);
+          const float f0 = exp2f(half), f1 = exp2f(shift - half);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float x = NH == 4 ? acc[i][0] + acc[i][1] : acc[i][h], y = NH == 4 ? acc[i][2] + acc[i][3] : acc[i][2 + h];
+            o[2 * i] = x * inv[h] * f0 * f1;
+            o[2 * i + 1] = y * inv[h] * f0 * f1;
+          }
+        };
+        const int heads = unit_heads(sub);
+        if (began && done) {
+#pragma unroll
+          for (int h = 0; h < HL; ++h) {
+            const int head = NH == 4 ? lt : 2 * lt + h;
+            float o[16];
+            values(h, o);
+            if (head < heads) store_row(row, first_head(sub) + head, 16 * lg, o, 16);
+          }
+        } else {
+          // slot 0: a segment of a unit that began before; slot 1: the beginning of one that goes on
+          const int slot = began ? 1 : 0;
+          float(*p)[kPartRow] = sm.part[warp];
+          if (slot) {  // (the ring is free: the range ends here)
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            __syncwarp();
+            p = reinterpret_cast<float(*)[kPartRow]>(sm.ring[warp]);
+          }
+#pragma unroll
+          for (int h = 0; h < HL; ++h) {
+            const int head = NH == 4 ? lt : 2 * lt + h;
+            float o[16];
+            values(h, o);
+#pragma unroll
+            for (int k = 0; k < 16; k += 4)
+              *reinterpret_cast<float4*>(&p[head][16 * lg + k]) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+            if (lg == 0) sm.ml[warp][slot][head] = ml[h];
+          }
+          if (lane == 0) {
+            sm.unit0[warp][slot] = at - j;
+            sm.unit_row[warp][slot] = row;
+            sm.unit_sub[warp][slot] = sub;
+            sm.unit_blocks[warp][slot] = nb;
+            sm.kind[warp] |= slot ? 4 : (done ? 1 : 3);
+          }
+        }
+        clear();
+      }
+      if (!last) {
+        if (done) {
+          j = 0;
+          began = true;
+          if (++sub == subs) {
+            sub = 0;
+            do {
+              ++row;
+              nb = blocks_of(row_ctx(a, row, row_seq(a, row), false));
+            } while (nb == 0);
+          }
+          load_unit();
+        } else {
+          ++j;
+        }
+      }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  }
+  __syncthreads();
+
+  // ---- units that several warps share: chains of segments, warp after warp
+  auto part_of = [&](int w, int slot) {
+    return slot ? reinterpret_cast<const float(*)[kPartRow]>(sm.ring[w]) : reinterpret_cast<const float(*)[kPartRow]>(sm.part[w]);
+  };
+  int w = 0, slot = 0;
+  while (true) {
+    // the next chain's first segment
+    while (w < wide && !(slot == 0 ? (w == 0 && (sm.kind[0] & 1)) : (sm.kind[w] & 4))) {
+      if (slot == 0) slot = 1;
+      else ++w;
+    }
+    if (w >= wide) break;
+    const int w0 = w, s0 = slot;
+    bool open = s0 ? true : (sm.kind[w0] & 2) != 0;  // the unit goes on behind the segment
+    int we = w0;  // its last warp here
+    while (open && we + 1 < wide && (sm.kind[we + 1] & 1)) {
+      ++we;
+      open = (sm.kind[we] & 2) != 0;
+    }
+    const int row = sm.unit_row[w0][s0], sub = sm.unit_sub[w0][s0], nb = sm.unit_blocks[w0][s0];
+    const int64_t unit0 = sm.unit0[w0][s0];
+    const int heads = unit_heads(sub);
+    const bool whole = s0 == 1 && !open;
+    const int64_t place = 2 * (int64_t)blockIdx.x + s0;
+    if (warp < heads) {
+      const int h = warp;
+      float M = -INFINITY, L = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int x = w0; x <= we; ++x) M = fmaxf(M, sm.ml[x][x == w0 ? s0 : 0][h].x);
+      for (int x = w0; x <= we; ++x) {
+        const float2 e = sm.ml[x][x == w0 ? s0 : 0][h];
+        const float f = e.x == -INFINITY ? e.y : e.y * exp2f(e.x - M);
+        const float4 v = *reinterpret_cast<const float4*>(&part_of(x, x == w0 ? s0 : 0)[h][4 * lane]);
+        L += f;
+        o[0] = fmaf(f, v.x, o[0]); o[1] = fmaf(f, v.y, o[1]); o[2] = fmaf(f, v.z, o[2]); o[3] = fmaf(f, v.w, o[3]);
+      }
+      const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] *= inv;
+      if (whole) {
+        store_row(row, first_head(sub) + h, 4 * lane, o, 4);
+      } else {
+        reinterpret_cast<float4*>(a.part)[(place * 8 + h) * (kD / 4) + lane] = make_float4(o[0], o[1], o[2], o[3]);
+        if (lane == 0) a.ml[place * 8 + h] = make_float2(M, L);
+      }
+    }
+    if (!whole) {
+      // the CTAs of the unit: from that of its first block to that of its last
+      auto cta_of = [&](int64_t p) { return (((p + 1) * R - 1) / total) / wide; };
+      const int64_t c0 = cta_of(unit0), c1 = cta_of(unit0 + nb - 1);
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        const int n = atomicAdd(a.counters + c0, 1);
+        sm.arrived = n == (int)(c1 - c0);
+        if (sm.arrived) a.counters[c0] = 0;
+        __threadfence();
+      }
+      __syncthreads();
+      if (sm.arrived && warp < heads) {
+        const int h = warp;
+        float M = -INFINITY, L = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int64_t c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(&a.ml[(2 * c + (c == c0 ? 1 : 0)) * 8 + h]).x);
+        for (int64_t c = c0; c <= c1; ++c) {
+          const int64_t p = (2 * c + (c == c0 ? 1 : 0)) * 8 + h;
+          const float2 e = __ldcg(&a.ml[p]);
+          const float f = e.x == -INFINITY ? e.y : e.y * exp2f(e.x - M);
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part) + p * (kD / 4) + lane);
+          L += f;
+          o[0] = fmaf(f, v.x, o[0]); o[1] = fmaf(f, v.y, o[1]); o[2] = fmaf(f, v.z, o[2]); o[3] = fmaf(f, v.w, o[3]);
+        }
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] *= inv;
+        store_row(row, first_head(sub) + h, 4 * lane, o, 4);
+      }
+    }
+    // on behind the chain
+    if (we == w0) {
+      if (s0 == 0) slot = 1;
+      else ++w;
+    } else {
+      w = we;
+      slot = 1;
+    }
+  }
+}
+
+template <int NH>
+cudaError_t run_decode(const DecArgs& a, int num_sms, cudaStream_t st) {
+  static std::atomic<uint64_t> ready{0};  // devices (up to 64) whose kernel has its shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(ready.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(k_int8_decode<NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(DecSmem<NH>));
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_release);
+  }
+  k_int8_decode<NH><<<num_sms, kDecThreads, sizeof(DecSmem<NH>), st>>>(a);
+  count_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t int8_partial_bytes(int num_sms) { return (size_t)2 * num_sms * 8 * (kD + 2) * sizeof(float); }
+
+static cudaError_t launch_rows(const tq_cache_desc& d, DecArgs& a, uint8_t* workspace, int num_sms, cudaStream_t st) {
+  a.kpool = reinterpret_cast<const uint8_t*>(d.k_cache);
+  a.vpool = reinterpret_cast<const uint8_t*>(d.v_cache);
+  a.num_blocks = d.num_blocks;
+  a.Hkv = d.num_kv_heads;
+  a.g = a.Hq / a.Hkv;
+  a.ngroups = (a.g + 7) / 8;
+  a.counters = reinterpret_cast<int*>(workspace);
+  a.part = reinterpret_cast<float*>(workspace + kCounterRegionBytes);
+  a.ml = reinterpret_cast<float2*>(a.part + (size_t)2 * num_sms * 8 * kD);
+  return a.g <= 4 ? run_decode<4>(a, num_sms, st) : run_decode<8>(a, num_sms, st);
+}
+
+cudaError_t launch_int8_decode(const DecodeCall& c, int num_sms, cudaStream_t st) {
+  DecArgs a = {};
+  a.table = c.block_table;
+  a.max_blocks = c.max_blocks;
+  a.ctx_lens = c.ctx_lens;
+  a.q = c.q;
+  a.q_bf16 = c.q_dtype == TQ_BF16 ? 1 : 0;
+  a.Hq = c.num_q_heads;
+  a.q_row = a.o_row = (int64_t)c.num_q_heads * kD;
+  a.q_head = a.o_head = kD;
+  a.out = c.out;
+  a.out_bf16 = c.out_dtype == TQ_BF16 ? 1 : 0;
+  a.rows = c.batch;
+  a.splits = c.splits;
+  a.scale = c.sm_scale * 1.4426950408889634f;
+  a.status = c.status;
+  return launch_rows(*c.desc, a, c.workspace, num_sms, st);
+}
+
+cudaError_t launch_int8_attend(const AttendCall& c, int num_sms, cudaStream_t st) {
+  DecArgs a = {};
+  a.table = c.block_table;
+  a.max_blocks = c.max_blocks;
+  a.ctx_lens = c.ctx_lens;
+  a.starts = c.starts;
+  a.seqs = c.batch;
+  a.q = c.q->in;
+  a.q_bf16 = c.q_dtype == TQ_BF16 ? 1 : 0;
+  a.Hq = c.q->num_heads;
+  a.q_row = c.q->in_token_stride;
+  a.q_head = c.q->in_head_stride;
+  a.out = c.q->out;
+  a.out_bf16 = c.out_dtype == TQ_BF16 ? 1 : 0;
+  a.o_row = c.q->out_token_stride;
+  a.o_head = c.q->out_head_stride;
+  a.rows = (int)c.n_tokens;
+  a.scale = c.sm_scale * 1.4426950408889634f;
+  a.status = c.status;
+  return launch_rows(*c.desc, a, c.workspace, num_sms, st);
+}
+
+}  // namespace tq

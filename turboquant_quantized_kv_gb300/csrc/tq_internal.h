@@ -18,6 +18,9 @@ void clear_error();
 // Adds one to the count tq_launch_count() reports; called after each kernel launch.
 void count_launch();
 
+// The status word and the number of SMs of the current device.
+tq_status device_status(unsigned** status, int* num_sms);
+
 // Host-side validation of a descriptor.  Returns TQ_OK or an error (message set).
 // need_data = false skips the device-pointer checks (sizes only).
 tq_status check_desc(const tq_cache_desc* desc, bool need_data = true);
@@ -60,7 +63,7 @@ struct DecodeCall {
   void* out;
   int out_dtype;
   uint8_t* workspace;
-  int splits;
+  int splits;  // (int8 layers: as asked for, 0 = automatic)
   unsigned* status;
   bool after_append;  // enqueued right after this library's append on the same stream (tq_append_decode)
   // tq_decode_step: the new token of sequence b ([batch][H_kv][head_dim], new_dtype)
@@ -106,6 +109,22 @@ size_t prefix_partial_bytes(const tq_cache_desc& d, int batch, int num_q_heads, 
 // The most of any prefix up to this length.
 size_t prefix_partial_bytes_upto(const tq_cache_desc& d, int batch, int num_q_heads, int64_t prefix_len, int num_sms);
 
+// One validated call of tq_attend.
+struct AttendCall {
+  const tq_cache_desc* desc;
+  const tq_heads* q;  // and the output rows
+  int q_dtype, out_dtype;
+  int64_t n_tokens;
+  const int32_t* starts;
+  int batch;
+  const int32_t* block_table;
+  int max_blocks;
+  const int32_t* ctx_lens;
+  float sm_scale;
+  uint8_t* workspace;
+  unsigned* status;
+};
+
 // The factor in [1, 2) that leaves the centroids (2^bits, antisymmetric) with the smallest
 // largest relative error when they are rounded to fp16.
 float table_factor(const float* centroids, int bits);
@@ -132,6 +151,15 @@ cudaError_t launch_decode(const DecodeCall& c, cudaStream_t st);
 cudaError_t launch_prefix_decode(const PrefixCall& c, cudaStream_t st);
 cudaError_t launch_rope_apply(const RopeCall& c, cudaStream_t st);
 cudaError_t launch_rope_append(const RopeCall& c, const tq_cache_desc& d, cudaStream_t st);
+// int8 layers (tq_int8.cu, tq_int8_decode.cu): keys and values in one launch, either may be null;
+// their decode's workspace is the counter region and int8_partial_bytes behind it.
+cudaError_t launch_int8_append(const tq_cache_desc& d, const void* k, const void* v, int in_dtype, const int64_t* slots,
+                               int64_t n_tok, unsigned* status, int num_sms, cudaStream_t st);
+cudaError_t launch_int8_dequant(const tq_cache_desc& d, int which, const int64_t* slots, int64_t n, void* out, int out_dtype,
+                                unsigned* status, int num_sms, cudaStream_t st);
+size_t int8_partial_bytes(int num_sms);
+cudaError_t launch_int8_decode(const DecodeCall& c, int num_sms, cudaStream_t st);
+cudaError_t launch_int8_attend(const AttendCall& c, int num_sms, cudaStream_t st);
 // Polar layers (tq_polar.cu); the generic launchers above route them here.
 cudaError_t launch_polar_append(const tq_cache_desc& d, int which, const void* x, int in_dtype,
                                 const int64_t* slots, int64_t n_tok, unsigned* status, int num_sms, cudaStream_t st);

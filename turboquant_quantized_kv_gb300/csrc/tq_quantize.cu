@@ -1482,6 +1482,7 @@ static cudaError_t dequant_bits(const tq_cache_desc& d, int which, const int64_t
 cudaError_t launch_dequant(const tq_cache_desc& d, int which, const int64_t* slots, int64_t n, void* out,
                            int out_dtype, unsigned* status, int num_sms, cudaStream_t st) {
   if (n <= 0) return cudaSuccess;
+  if (d.fmt.kv_format == TQ_KV_INT8) return launch_int8_dequant(d, which, slots, n, out, out_dtype, status, num_sms, st);
   if (d.fmt.kv_format == TQ_KV_POLAR) return launch_polar_dequant(d, which, slots, n, out, out_dtype, status, num_sms, st);
   const int64_t n_vec = n * d.num_kv_heads;
   if (d.fmt.kv_format == TQ_KV_K8V4 && which == 0) {
