@@ -51,12 +51,13 @@ def values(codes, steps, bits):
     return np.where(((bits[..., None] >> np.arange(BLOCK, dtype=np.uint32)) & 1).astype(bool)[..., None], np.nan, v)
 
 
-def attention(q, k, v, table, ctx, scale):
+def attention(q, k, v, table, ctx, scale, weights=0.0):
     """(out [Hq, D], bound [Hq]) of one query token: q [Hq, D]; k, v [blocks, heads, 16, D]; `bound` is what
     fp32 sums and 22-bit parts may cost: the products of a logit lose at most 2^-19 of the sum of their
     magnitudes (2^-22 the two parts of a query, 2^-23 each of 8 sums and the last scalings, with room for a
     tensor core that cuts off instead of rounding), a weight as much and 2^-20 for its own two parts,
-    exponential and the denominator; relative to the largest value attended."""
+    exponential and the denominator; relative to the largest value attended.  `weights`: half a step of the type
+    that weights are rounded to."""
     hq, heads = q.shape[0], k.shape[1]
     out, bound = np.zeros((hq, D)), np.zeros(hq)
     ids = [(int(table[p // BLOCK]), p % BLOCK) for p in range(ctx)]
@@ -71,5 +72,5 @@ def attention(q, k, v, table, ctx, scale):
         w /= w.sum()
         out[h] = w @ vh
         delta = 2.0 ** -19 * (np.abs(kh) @ np.abs(q[h])).max() * abs(scale)
-        bound[h] = (2 * delta + 2.0 ** -20) * np.abs(vh).max()
+        bound[h] = (2 * delta + 2.0 ** -20 + weights) * np.abs(vh).max()
     return out, bound

@@ -310,27 +310,100 @@ def test_decode_ranges(cuda, tqlib, hq):
     check_rows(out, wants)
 
 
-def test_attend(cuda, tqlib):
-    for seed, (heads, group, new, past) in enumerate([(2, 4, [1], [0]), (1, 8, [5, 0, 17, 1], [0, 30, 100, 15]),
-                                                      (2, 3, [40, 33], [0, 7]), (1, 1, [130], [20]), (1, 12, [3, 64], [250, 1])]):
-        hq, blocks = heads * group, 40
-        layer = filled(cuda, tqlib, 41 + seed, blocks, heads)
-        lens = [a + b for a, b in zip(new, past)]
-        table, g = tables(seed, lens, blocks), np.random.default_rng(seed)
-        starts = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
-        rows = int(starts[-1]) + 3
-        for dtype in (cuda.float32, cuda.bfloat16):
-            fused = dev(cuda, g.standard_normal((rows, hq + 2, D)).astype(np.float32), dtype)
-            q = fused[:, 1:hq + 1]  # a view of a fused projection
-            out = cuda.full((rows, hq, D), 7.0, dtype=cuda.float32, device="cuda")
-            got = layer.attend(q, dev(cuda, starts), dev(cuda, table), dev(cuda, np.array(lens, np.int32)), out=out)
-            assert got is out
-            got = out.cpu().numpy()
-            assert (got[starts[-1]:] == 7.0).all()  # rows behind the last sequence
-            k, v = (ref.values(*pages(layer, w)) for w in (0, 1))
-            wants = []
-            for b, n in enumerate(new):
-                for i in range(n):
-                    wants.append(ref.attention(host(q)[starts[b] + i].astype(np.float64), k, v, table[b], past[b] + i + 1, SCALE))
-            check_rows(got, wants, half=2.0 ** -8)
-        assert tqlib.get_device_status() == 0
+ATTEND = [(2, 4, [1], [0]), (1, 8, [5, 0, 17, 1], [0, 30, 100, 15]), (2, 3, [40, 33], [0, 7]), (1, 1, [130], [20]),
+          (1, 12, [3, 64], [250, 1]),
+          # tiles: one row past a stream, past a tile; groups that do not divide one; several tiles and steps
+          (1, 4, [33], [0]), (1, 4, [64, 65], [0, 300]), (2, 8, [100, 3, 33], [50, 20, 0]), (1, 3, [300], [200]),
+          (3, 5, [60, 0, 52], [1000, 8, 3]), (1, 1, [257, 40], [0, 128]), (1, 7, [37], [400]), (1, 128, [5], [77]),
+          (1, 300, [2], [40])]
+
+
+def attend_case(cuda, tqlib, seed, heads, group, new, past, dtype, change=None, scale=SCALE, pool=None):
+    """One call over a filled layer (`change`: of its keys and values first); rows against 64 bits."""
+    hq, lens = heads * group, [a + b for a, b in zip(new, past)]
+    blocks = -(-max(lens) // BLOCK) + 3
+    g = np.random.default_rng(seed)
+    n = blocks * BLOCK
+    k, v = (g.standard_normal((n, heads, D)).astype(np.float32) for _ in "kv")
+    starts = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    rows = int(starts[-1]) + 3
+    q = g.standard_normal((rows, hq + 2, D)).astype(np.float32)
+    table = tables(seed, lens, blocks)
+    if change is not None:
+        change(k, v, q, table)
+    layer = layer_of(tqlib, blocks, heads)
+    layer.append(dev(cuda, k), dev(cuda, v), cuda.arange(n, device="cuda"))
+    q = dev(cuda, q, dtype)[:, 1:hq + 1]  # a view of a fused projection
+    out = cuda.full((rows, hq, D), 7.0, dtype=cuda.float32, device="cuda")
+    ws = cuda.zeros(layer.attend_workspace_bytes(rows, len(new), hq, table.shape[1]), dtype=cuda.uint8, device="cuda")
+    args = (dev(cuda, starts), dev(cuda, table), dev(cuda, np.array(lens, np.int32)))
+    assert layer.attend(q, *args, out=out, workspace=ws, sm_scale=scale) is out
+    got = out.cpu().numpy()
+    assert (got[starts[-1]:] == 7.0).all()  # rows behind the last sequence
+    assert not ws[:65536].any()
+    again = layer.attend(q, *args, out=out.clone(), workspace=ws, sm_scale=scale)
+    assert np.array_equal(again.cpu().numpy(), got, equal_nan=True)  # the same bits
+    half = layer.attend(q, *args, out_dtype=cuda.bfloat16, workspace=ws, sm_scale=scale)[:starts[-1]]
+    assert cuda.equal(half.nan_to_num(3e4), out[:starts[-1]].to(cuda.bfloat16).nan_to_num(3e4))
+    kk, vv = (ref.values(*pages(layer, w)) for w in (0, 1))
+    weights = 2.0 ** -11 if dtype == cuda.bfloat16 else 0.0
+    qh = host(q).astype(np.float64)
+    with np.errstate(all="ignore"):
+        wants = [ref.attention(qh[starts[b] + i], kk, vv, table[b], past[b] + i + 1, scale, weights)
+                 for b, m in enumerate(new) for i in range(m)]
+    return got[:starts[-1]], wants, kk, vv
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("case", range(len(ATTEND)))
+def test_attend(cuda, tqlib, case, dtype):
+    got, wants, _, _ = attend_case(cuda, tqlib, case, *ATTEND[case], cuda.bfloat16 if dtype == "bf16" else cuda.float32,
+                                   scale=SCALE if case % 3 else -0.2)
+    check_rows(got, wants)
+    assert tqlib.get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attend_ranges(cuda, tqlib, dtype):
+    """Blocks of values far above and below the others', NaN tokens that only later rows see, tiny, large and
+    infinite queries, bad block ids, in tiles: each row only pays for itself."""
+    def change(k, v, q, table):
+        v[32:48] *= 2.0 ** 40
+        v[96:112] *= 2.0 ** -60
+        k[130, 0, 5], v[160, 0, 9] = np.nan, np.inf
+        table[0] = np.arange(table.shape[1])  # (these blocks are tokens of the first sequence in order)
+        table[0, 3] = -1
+        table[1, 2] = 1 << 28
+        q[5] *= 1e-30
+        q[6] *= 200.0
+        q[7, 2] = np.inf
+        table[1][table[1] == 2] = 5
+        table[1][table[1] == 8] = 6
+        table[1][table[1] == 10] = 7
+
+    got, wants, kk, vv = attend_case(cuda, tqlib, 99, 1, 4, [180, 50], [10, 100], cuda.bfloat16 if dtype == "bf16" else cuda.float32, change)
+    wants[7][0][1] = np.nan
+    assert np.abs(vv[2]).max() > 1e9
+    for i, (want, _) in enumerate(wants[:180]):  # row i of the first sequence sees tokens 0 .. 10 + i
+        assert np.isnan(want).all() == (i >= 130 - 10), i
+    check_rows(got, wants)
+    assert tqlib.get_device_status() == tqlib.TQ_DEV_BAD_BLOCK
+
+
+def test_attend_lengths(cuda, tqlib):
+    """Contexts shorter than the queries (zero rows), outside the table, empty sequences."""
+    heads, group = 1, 4
+    layer = filled(cuda, tqlib, 61, 12, heads)
+    new, lens = [40, 20, 10, 3], [25, 0, 400, -3]
+    table = np.tile(np.arange(8, dtype=np.int32), (4, 1))
+    starts = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    q = np.random.default_rng(4).standard_normal((int(starts[-1]), 4, D)).astype(np.float32)
+    out = layer.attend(dev(cuda, q), dev(cuda, starts), dev(cuda, table), dev(cuda, np.array(lens, np.int32))).cpu().numpy()
+    k, v = (ref.values(*pages(layer, w)) for w in (0, 1))
+    wants = []
+    for b, n in enumerate(new):
+        ctx = min(max(lens[b], 0), 128)
+        wants += [ref.attention(q[starts[b] + i].astype(np.float64), k, v, table[b], max(0, ctx - n + i + 1), SCALE) for i in range(n)]
+    check_rows(out, wants)
+    assert not out[:15].any() and not out[40:60].any()
+    assert tqlib.get_device_status() == tqlib.TQ_DEV_BAD_CONTEXT

@@ -445,7 +445,7 @@ size_t tq_attend_workspace_bytes(const tq_cache_desc* desc, int64_t n_tokens, in
     return 0;
   }
   DeviceInfo di;
-  return device_info(&di) == TQ_OK ? int8_workspace(di.num_sms) : 0;
+  return device_info(&di) == TQ_OK ? int8_workspace(di.num_sms) + int8_attend_partial_bytes(di.num_sms) : 0;
 }
 
 tq_status tq_attend(const tq_cache_desc* desc, const tq_heads* q, int q_dtype, int out_dtype, int64_t n_tokens,
@@ -474,7 +474,7 @@ tq_status tq_attend(const tq_cache_desc* desc, const tq_heads* q, int q_dtype, i
     return fail(TQ_ERR_INVALID_ARG, "%s: null query_starts/block_table/context_lens", fn);
   DeviceInfo di;
   if ((s = device_info(&di)) != TQ_OK) return s;
-  const size_t need = int8_workspace(di.num_sms);
+  const size_t need = int8_workspace(di.num_sms) + int8_attend_partial_bytes(di.num_sms);
   if (!workspace || workspace_bytes < need)
     return fail(TQ_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, workspace_bytes, need);
   if (reinterpret_cast<uintptr_t>(workspace) & 255)

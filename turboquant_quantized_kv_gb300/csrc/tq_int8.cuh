@@ -14,6 +14,11 @@ constexpr int kI8Codes = kBlock * kD;          // bytes of a page's records
 constexpr int kI8Page = kI8Codes + 16;         // and of a page
 constexpr float kI8Least = 1.1754943508222875e-38f;  // 2^-126, the least step
 
+// Sequences with more rows (tokens x query heads of a KV head) than this go through the tiles of
+// tq_int8_attend.cu, the others through the decode kernel.
+constexpr int kAttRows = 32;
+constexpr int kAttMostGroup = 256;  // query heads of a KV head, with more of them every sequence does the latter
+
 struct I8Tail {
   float step;
   uint32_t bad;       // bit r: record r is not a number
@@ -28,5 +33,8 @@ __device__ __forceinline__ uint32_t i8_pair(uint32_t w, uint32_t sel) {
   const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half((unsigned short)0x6480u)));
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+
+// The sequences of a call that take tiles (the rest of the call is launch_int8_attend's).
+cudaError_t launch_int8_tiles(const AttendCall& c, uint8_t* partials, int num_sms, cudaStream_t st);
 
 }  // namespace tq

@@ -1,0 +1,845 @@
+// Causal attention of the last tokens of each sequence over int8 layers (libtq, sm_103a).
+//
+//     out[row] = softmax(sm_scale q[row] K[0, lim)^T) V[0, lim),  lim = context - tokens behind the row's
+//
+// Rows are (token, query head of a KV head's group), token by token.  Sequences with more rows a KV head than
+// kAttRows go through the fifth-generation tensor cores here; those with fewer are rows of the decode
+// kernel (tq_int8_decode.cu).
+//
+// Work.  A unit is (sequence, KV head, tile of up to 256 rows), a step is 128 tokens of its context.  All
+// steps of all units stand in one line, cut into equal parts, one a CTA (an SM): causal tiles of any length
+// balance.  A unit that is cut leaves partials (normalised values, reference, denominator) in the
+// workspace, which the CTA that arrives last joins in the order of the line.
+//
+// A CTA: two streams of 128 rows over the same tokens.
+//   8 producer warps  turn 8 blocks of codes into fp16 (exact, i8_pair) in shared memory, K ahead of V;
+//   1 MMA warp        S = Q K^T (shared memory), O += P V (P in tensor memory), one elected thread;
+//   8 softmax warps   a thread a row: maxima, base-2 weights, P over the logits in tensor memory.
+// Scales.  Queries go in as fp16 after a power of two for each row (bf16 queries lose nothing but what
+// lies 2^-24 below the row's largest; fp32 ones go in as two parts).  A block's step of K is one factor for
+// 16 logits, its step of V one for 16 weights, so that both operands hold plain codes: with m a running
+// reference of a row's log2-logits u and C one of weight times step of V, both of what the row attends to,
+//     e = 2^(u - m),  denominator += e,  P = e step 2^(m - C) <= 2^14,
+// so that a block of large values costs a row nothing unless it attends to them.  P is fp16 (half a step 2^-11), for fp32 queries in two parts as well.
+#include <math_constants.h>
+
+#include <atomic>
+#include <type_traits>
+
+#include "tq_async.cuh"
+#include "tq_int8.cuh"
+#include "tq_tcgen05.cuh"
+
+namespace tq {
+namespace {
+
+constexpr int kTile = 128;          // tokens a step, rows a stream
+constexpr int kTileBlocks = kTile / kBlock;
+constexpr int kUnitRows = 2 * kTile;
+constexpr int kSoftWarps = 8, kProdWarps = 8, kMmaWarp = kSoftWarps + kProdWarps;
+constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr uint32_t kPanel = kTile * 128;    // 128 rows of 64 16-bit elements, swizzled
+constexpr uint32_t kOperand = 2 * kPanel;
+constexpr int kSlots = 4;                   // tiles whose steps are kept
+constexpr float kRoom = 14.0f, kTop = 8.0f; // log2 of P at most, and of its largest when the reference moves
+constexpr float kMoveM = 16.0f;
+
+// Shared memory: operands of 32 KB -- Q of the streams in 0 and 1 (low parts in 2 and 3), K in two stages,
+// V in two (with low parts in one) -- then the rest.
+constexpr uint32_t kOffStep = 7 * kOperand;                    // float [slots][3][8]: steps of K and V, exponents above V's
+constexpr uint32_t kOffBits = kOffStep + kSlots * 96;          // u32 [slots][8]: valid tokens << 16 | bad ones
+constexpr uint32_t kOffRow = kOffBits + kSlots * 32;           // float [256]: a row's power of two
+constexpr uint32_t kOffBar = kOffRow + kUnitRows * 4;
+constexpr int kBars = 2 + 2 + 2 + 2 + kSlots + 2 + 2 + 2;
+constexpr uint32_t kOffMisc = kOffBar + kBars * 8;
+constexpr uint32_t kSmem = kOffMisc + 128;
+static_assert(kSmem <= 232448, "the shared memory of one CTA an SM");
+
+struct Misc {
+  uint32_t tmem;
+  int dead;     // a wait gave up
+  int arrived;
+  int seq, kvh, tile, step;  // where the CTA's part begins
+  int pad;
+  int64_t sums[2];
+};
+
+struct AttArgs {
+  const uint8_t* kpool;
+  const uint8_t* vpool;
+  int64_t num_blocks;
+  const int32_t* table;
+  int max_blocks;
+  const int32_t* ctx_lens;
+  const int32_t* starts;
+  int seqs;
+  const void* q;
+  int q_bf16;
+  int64_t q_row, q_head;
+  void* out;
+  int out_bf16;
+  int64_t o_row, o_head;
+  int n_tokens, Hkv, g;
+  int per;      // tokens a unit
+  float scale;  // sm_scale * log2 e
+  int* counters;
+  float4* part; // [2 grid][8][32][32]: (32 rows, 4 coordinates) of a partial
+  float2* ml;   // [2 grid][256]
+  unsigned* status;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+
+// A sequence: its first query token, their number, its context (cut to the table).
+struct Seq {
+  int first, n, ctx;
+  bool large;  // goes through this kernel
+};
+__device__ __forceinline__ Seq seq_of(const AttArgs& a, int b, bool flag) {
+  Seq s;
+  s.first = __ldg(a.starts + b);
+  const int next = __ldg(a.starts + b + 1);
+  s.ctx = __ldg(a.ctx_lens + b);
+  s.first = min(max(s.first, 0), a.n_tokens);
+  s.n = max(0, min(next, a.n_tokens) - s.first);
+  s.large = (int64_t)s.n * a.g > kAttRows;
+  const int most = a.max_blocks * kBlock;
+  if (s.ctx < 0 || s.ctx > most) {
+    if (flag && s.large) flag_status(a.status, TQ_DEV_BAD_CONTEXT);
+    s.ctx = s.ctx < 0 ? 0 : most;
+  }
+  return s;
+}
+// Steps of tile k of a sequence: one at least, which gives rows without a token their zeros.
+__device__ __forceinline__ int steps_of(const AttArgs& a, const Seq& s, int k) {
+  const int lim = s.ctx - s.n + min(s.n, (k + 1) * a.per);
+  return max(1, (lim + kTile - 1) / kTile);
+}
+__device__ __forceinline__ int tiles_of(const AttArgs& a, const Seq& s) { return s.large ? (s.n + a.per - 1) / a.per : 0; }
+
+// Rows of Q of one unit to the operands: a quad of lanes a row, lane q coordinates [32 q, 32 q + 32).
+template <bool BF16, bool EXACT>
+__device__ __forceinline__ void stage_q(const AttArgs& a, const Seq& s, int kvh, int tok0, int rows, uint32_t base, float* scales,
+                                        int warp, int lane) {
+  const int quad = lane & 3;
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    const int r = h * kTile + 8 * warp + (lane >> 2);
+    if (h * kTile + 8 * (warp & ~3) >= rows) break;  // (32 rows past the end: nobody looks at their products)
+    float x[32];
+    if (r < rows) {
+      const int t = r / a.g;
+      const int64_t at = (int64_t)(s.first + tok0 + t) * a.q_row + (int64_t)(kvh * a.g + r - t * a.g) * a.q_head + 32 * quad;
+      if constexpr (BF16) {
+        const __nv_bfloat16* p = reinterpret_cast<const __nv_bfloat16*>(a.q) + at;
+        if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0u) {
+          load32(p, x);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = __bfloat162float(p[i]);
+        }
+      } else {
+        const float* p = reinterpret_cast<const float*>(a.q) + at;
+        if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0u) {
+          load32(p, x);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = p[i];
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = 0.0f;
+    }
+    uint32_t top = 0u;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // the row by a power of two, its largest magnitude below 2^8; a row that is not finite gives NaN
+    const int e = max((int)(top >> 23) - 126, -110);
+    const bool fine = top < 0x7F800000u;
+    const float f = (a.scale < 0.0f ? -1.0f : 1.0f) * exp2i(8 - min(e, 128));  // (so that no factor of a logit is negative)
+    if (quad == 0) scales[r] = fine ? exp2i(e - 8) * fabsf(a.scale) : CUDART_NAN_F;
+    const uint32_t hi = base + (uint32_t)h * kOperand + (uint32_t)(r & 127) * 128u, lo = hi + 2 * kOperand;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t w[4], v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float x0 = fine ? x[8 * c + 2 * k] * f : 0.0f, x1 = fine ? x[8 * c + 2 * k + 1] * f : 0.0f;
+        w[k] = half2_bits(x0, x1);
+        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+        v[k] = half2_bits(x0 - y.x, x1 - y.y);
+      }
+      const int at = 4 * quad + c;
+      const uint32_t off = (uint32_t)(at >> 3) * kPanel + (uint32_t)(((at & 7) ^ (r & 7)) << 4);
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(hi + off), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+      if constexpr (EXACT)
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(lo + off), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+    }
+  }
+}
+
+// A lane's four 16-byte pieces of a page (piece lane + 32 i: record 4 i + lane / 8, coordinates 16 (lane & 7) ..).
+struct Page {
+  uint4 w[4];
+};
+__device__ __forceinline__ void load_page(Page& p, const uint8_t* at, int lane) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p.w[i] = __ldg(reinterpret_cast<const uint4*>(at) + lane + 32 * i);
+}
+// To the operand at dst as fp16: panel = half of the head, row = token, 16-byte chunk c at c ^ (row & 7).
+__device__ __forceinline__ void store_page(const Page& p, uint32_t dst, int block, int lane) {
+  const int c16 = lane & 7, panel = c16 >> 2;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = block * kBlock + 4 * i + (lane >> 3);
+    const uint32_t at = dst + (uint32_t)panel * kPanel + (uint32_t)row * 128u;
+    const uint32_t w[4] = {p.w[i].x, p.w[i].y, p.w[i].z, p.w[i].w};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int half = h ^ panel;  // (the two panels' lanes hit different columns)
+      const uint32_t a = half ? w[2] : w[0], b = half ? w[3] : w[1];
+      const uint32_t chunk = (uint32_t)(((2 * (c16 & 3) + half) ^ (row & 7)) << 4);
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + chunk), "r"(i8_pair(a, 0x4140u)), "r"(i8_pair(a, 0x4342u)),
+                   "r"(i8_pair(b, 0x4140u)), "r"(i8_pair(b, 0x4342u))
+                   : "memory");
+    }
+  }
+}
+
+template <bool EXACT>  // queries and weights in two parts
+__global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_constant__ AttArgs a) {
+  extern __shared__ __align__(128) unsigned char gen[];
+  const uint32_t base = smem_u32(gen);
+  if (base & 1023u) {  // (uniform) the swizzled operands need it; the window starts so on sm_103a
+    if (threadIdx.x == 0) flag_status(a.status, TQ_DEV_LAYOUT);
+    return;
+  }
+  Misc& misc = *reinterpret_cast<Misc*>(gen + kOffMisc);
+  float* const scales = reinterpret_cast<float*>(gen + kOffRow);
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(gen + kOffBar);
+  uint64_t *const kfull = bars, *const kempty = bars + 2, *const vfull = bars + 4, *const vempty = bars + 6;
+  uint64_t* const gfull = bars + 8;         // [kSlots] steps and bits of a tile
+  uint64_t* const sfull = gfull + kSlots;   // [2] logits of a stream are in tensor memory
+  uint64_t* const pfull = sfull + 2;        // [2] weights
+  uint64_t* const odone = pfull + 2;        // [2] accumulator complete
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // ---- the line: its length, and where the CTA's part begins
+  const int per = (a.seqs + kThreads - 1) / kThreads;
+  const int b0 = min(a.seqs, (int)threadIdx.x * per), b1 = min(a.seqs, b0 + per);
+  auto length = [&](const Seq& s) {
+    int64_t n = 0;
+    const int tiles = tiles_of(a, s);
+    for (int k = 0; k < tiles; ++k) n += steps_of(a, s, k);
+    return n;
+  };
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) mine += length(seq_of(a, b, blockIdx.x == 0)) * a.Hkv;
+  int64_t* const sums = reinterpret_cast<int64_t*>(gen);  // (the operands are not in use yet)
+  int64_t before = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t o = __shfl_up_sync(0xffffffffu, before, d);
+    if (lane >= d) before += o;
+  }
+  if (lane == 31) sums[warp] = before;
+  __syncthreads();
+  int64_t total = 0;
+  before -= mine;
+  for (int w = 0; w <= kMmaWarp; ++w) {
+    if (w < warp) before += sums[w];
+    total += sums[w];
+  }
+  if (total == 0) return;
+  const int64_t R = total < gridDim.x ? total : gridDim.x;
+  if (blockIdx.x >= R) return;
+  const int64_t begin = total * blockIdx.x / R, end = total * (blockIdx.x + 1) / R;
+  if (begin >= before && begin < before + mine) {
+    int64_t left = begin - before;
+    for (int b = b0; b < b1; ++b) {
+      const Seq s = seq_of(a, b, false);
+      const int64_t n = length(s);
+      if (left < n * a.Hkv) {
+        misc.seq = b;
+        misc.kvh = (int)(left / n);
+        left %= n;
+        int k = 0;
+        for (int st = steps_of(a, s, 0); left >= st; st = steps_of(a, s, k)) {
+          left -= st;
+          ++k;
+        }
+        misc.tile = k;
+        misc.step = (int)left;
+        break;
+      }
+      left -= n * a.Hkv;
+    }
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(kfull + i, kProdWarps);
+      mbar_init(kempty + i, 1);
+      mbar_init(vfull + i, kProdWarps);
+      mbar_init(vempty + i, 1);
+      mbar_init(sfull + i, 1);
+      mbar_init(pfull + i, 4);
+      mbar_init(odone + i, 1);
+    }
+    for (int i = 0; i < kSlots; ++i) mbar_init(gfull + i, kProdWarps);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    misc.dead = 0;
+  }
+  if (warp == kMmaWarp) tmem_alloc(base + kOffMisc, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc.tmem;
+  const uint32_t k_op = base + (EXACT ? 4u : 2u) * kOperand, v_op = k_op + 2 * kOperand;
+  constexpr int vbit = EXACT ? 0 : 1;  // stages of V less one
+
+  int seq = misc.seq, kvh = misc.kvh, tile = misc.tile, step = misc.step;
+  Seq s = seq_of(a, seq, false);
+  int done0 = 0, done1 = 0;  // steps of the streams so far
+  int turns0 = 0, turns1 = 0;  // segments of the streams so far
+  for (int64_t at = begin; at < end;) {
+    // ---- a segment: steps [step, step + n) of one unit
+    const int all = steps_of(a, s, tile), n = (int)min((int64_t)(all - step), end - at);
+    const int tok0 = tile * a.per, rows = min(a.per, s.n - tok0) * a.g;
+    const bool two = rows > kTile;
+    if (warp < kMmaWarp) {
+      if (a.q_bf16) stage_q<true, EXACT>(a, s, kvh, tok0, rows, base, scales, warp, lane);
+      else stage_q<false, EXACT>(a, s, kvh, tok0, rows, base, scales, warp, lane);
+    }
+    fence_proxy_async();
+    __syncthreads();
+    bool ok = true;
+    if (warp < kSoftWarps) {
+      // ----------------------------------------------------------- softmax
+      const int st = warp >> 2, w = warp & 3, r = st * kTile + 32 * w + lane;
+      const uint32_t ts = tmem + (uint32_t)(st * kTile) + ((uint32_t)(32 * w) << 16);
+      const uint32_t to = tmem + (uint32_t)((2 + st) * kTile) + ((uint32_t)(32 * w) << 16);
+      const bool live = st * kTile + 32 * w < rows;
+      const int done = st ? done1 : done0;
+      const float cq = live ? scales[r] : 0.0f;
+      // tokens the row attends to (a row past the end, whose queries are zeros: all, so that it holds nobody up)
+      const int lim = r < rows ? s.ctx - s.n + tok0 + r / a.g + 1 : 1 << 30;
+      const int least = __reduce_min_sync(0xffffffffu, lim);
+      float C = -INFINITY, m = -INFINITY, l = 0.0f;
+      int i = 0;
+      auto one = [&](auto careful) {  // one step; whether it is done
+        constexpr bool kCareful = decltype(careful)::value;
+        const int turn = done0 + i, slot = turn & (kSlots - 1);
+        ok = mbar_wait(gfull + slot, (turn / kSlots) & 1) && mbar_wait(sfull + st, (done + i) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return false;
+        tc_fence_after();
+        if (live) {
+          const float4* sp = reinterpret_cast<const float4*>(gen + kOffStep + slot * 96);
+          const uint4* bp = reinterpret_cast<const uint4*>(gen + kOffBits + slot * 32);
+          const uint4 q0 = bp[0], q1 = bp[1];
+          const int t0 = (step + i) * kTile;
+          const bool plain = (q0.x & q0.y & q0.z & q0.w & q1.x & q1.y & q1.z & q1.w) == 0xFFFF0000u &&
+                             ((q0.x | q0.y | q0.z | q0.w | q1.x | q1.y | q1.z | q1.w) & 0xFFFFu) == 0u && t0 + kTile <= least;
+          if (!kCareful && !plain) return false;
+          uint32_t mask[4] = {~0u, ~0u, ~0u, ~0u};
+          if (kCareful && !plain) {
+            const uint32_t bits[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+            uint32_t bad = 0u;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int k = min(max(lim - t0 - 32 * c, 0), 32);  // tokens of the chunk before the limit
+              mask[c] = ((bits[2 * c] >> 16) | (bits[2 * c + 1] & 0xFFFF0000u)) & (k == 32 ? ~0u : (1u << k) - 1u);
+              bad |= mask[c] & ((bits[2 * c] & 0xFFFFu) | (bits[2 * c + 1] << 16));
+            }
+            if (bad) l = CUDART_NAN_F;  // the row attends to what is not a number
+          }
+          float ks[8], vs[8], ev[8];
+          auto eight = [&](float(&x)[8], int i) {
+            const float4 y = sp[2 * i], z = sp[2 * i + 1];
+            x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
+            x[4] = z.x; x[5] = z.y; x[6] = z.z; x[7] = z.w;
+          };
+          eight(ks, 0);
+          eight(ev, 2);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) ks[k] *= cq;
+          uint32_t ra[32], rb[32];
+          // the largest u of the row, and the largest with the exponent of its block's values
+          float top = -INFINITY, topv = -INFINITY;
+          auto tops = [&](const uint32_t(&x)[32], int c) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float hi = -INFINITY;  // (of raw logits; no factor is negative)
+#pragma unroll
+              for (int k = 0; k < 16; k += 2) {
+                float y0 = __uint_as_float(x[16 * h + k]), y1 = __uint_as_float(x[16 * h + k + 1]);
+                if (kCareful) {
+                  y0 = (mask[c] >> (16 * h + k)) & 1u ? y0 : -INFINITY;
+                  y1 = (mask[c] >> (16 * h + k + 1)) & 1u ? y1 : -INFINITY;
+                }
+                hi = max3(hi, y0, y1);
+              }
+              float u = hi * ks[2 * c + h];
+              if (kCareful && hi == -INFINITY) u = hi;
+              top = fmaxf(top, u);
+              topv = fmaxf(topv, u + ev[2 * c + h]);
+            }
+          };
+          tmem_ld32_async(ts, ra);
+          tmem_wait_ld32(ra);
+          tmem_ld32_async(ts + 32, rb);
+          tops(ra, 0);
+          tmem_wait_ld32(rb);
+          tmem_ld32_async(ts + 64, ra);
+          tops(rb, 1);
+          tmem_wait_ld32(ra);
+          tmem_ld32_async(ts + 96, rb);
+          tops(ra, 2);
+          tmem_wait_ld32(rb);
+          tops(rb, 3);
+          if (__any_sync(0xffffffffu, top > m + kMoveM || topv > C + kRoom)) {
+            const float nm = fmaxf(m, ceilf(top)), nC = fmaxf(C, ceilf(topv) - kTop);
+            if (nm != m) l *= exp2f(m - nm);
+            m = nm;
+            const float f = nC != C ? exp2f(C - nC) : 1.0f;
+            C = nC;
+            if (i > 0 && __any_sync(0xffffffffu, f != 1.0f)) {  // (the last product into it precedes S)
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                tmem_ld32_async(to + 32 * c, ra);
+                tmem_wait_ld32(ra);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) ra[k] = __float_as_uint(__uint_as_float(ra[k]) * f);
+                tmem_st32(to + 32 * c, ra);
+              }
+            }
+          }
+          const float off = m == -INFINITY ? 0.0f : m, rho = C == -INFINITY ? 0.0f : exp2f(fminf(m - C, 120.0f));
+          eight(vs, 1);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) vs[k] = fminf(vs[k] * rho, 1.329227995784916e36f);  // (2^120; times a weight of zero)
+          float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
+          auto weights = [&](const uint32_t(&x)[32], int c) {
+            uint32_t p[16];
+            [[maybe_unused]] uint32_t p2[16];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int b = 2 * c + (k >> 2);
+              float2 u0 = make_float2(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1]));
+              float2 u1 = make_float2(__uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3]));
+              u0 = __ffma2_rn(u0, make_float2(ks[b], ks[b]), make_float2(-off, -off));
+              u1 = __ffma2_rn(u1, make_float2(ks[b], ks[b]), make_float2(-off, -off));
+              u0 = make_float2(ex2(u0.x), ex2(u0.y));
+              u1 = make_float2(ex2(u1.x), ex2(u1.y));
+              if (kCareful) {
+                const uint32_t bit = mask[c] >> (4 * k);
+                u0.x = bit & 1u ? u0.x : 0.0f;
+                u0.y = bit & 2u ? u0.y : 0.0f;
+                u1.x = bit & 4u ? u1.x : 0.0f;
+                u1.y = bit & 8u ? u1.y : 0.0f;
+              }
+              sum0 = __fadd2_rn(sum0, u0);
+              sum1 = __fadd2_rn(sum1, u1);
+              u0 = __fmul2_rn(u0, make_float2(vs[b], vs[b]));
+              u1 = __fmul2_rn(u1, make_float2(vs[b], vs[b]));
+              p[2 * k] = half2_bits(u0.x, u0.y);
+              p[2 * k + 1] = half2_bits(u1.x, u1.y);
+              if constexpr (EXACT) {
+                const float2 h0 = __half22float2(*reinterpret_cast<const __half2*>(&p[2 * k]));
+                const float2 h1 = __half22float2(*reinterpret_cast<const __half2*>(&p[2 * k + 1]));
+                p2[2 * k] = half2_bits(u0.x - h0.x, u0.y - h0.y);
+                p2[2 * k + 1] = half2_bits(u1.x - h1.x, u1.y - h1.y);
+              }
+            }
+            // over logits that have been read: high parts, low parts behind them
+            tmem_st16(ts + 32 * c, p);
+            if constexpr (EXACT) tmem_st16(ts + 32 * c + 16, p2);
+          };
+          tmem_ld32_async(ts, ra);
+          tmem_wait_ld32(ra);
+          tmem_ld32_async(ts + 32, rb);
+          weights(ra, 0);
+          tmem_wait_ld32(rb);
+          tmem_ld32_async(ts + 64, ra);
+          weights(rb, 1);
+          tmem_wait_ld32(ra);
+          tmem_ld32_async(ts + 96, rb);
+          weights(ra, 2);
+          tmem_wait_ld32(rb);
+          weights(rb, 3);
+          l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pfull + st);
+        return true;
+      };
+      if (st == 0 || two) {
+        while (i < n && one(std::false_type())) ++i;
+        while (i < n && ok && one(std::true_type())) ++i;
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(odone + st, (st ? turns1 : turns0) & 1));
+        tc_fence_after();
+        if (live && ok) {
+          // ---- the rows' values: out, or a partial
+          const bool whole = step == 0 && n == all;
+          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+          const float shift = C == -INFINITY ? 0.0f : C - m, half = truncf(0.5f * shift);
+          const float f0 = exp2f(half) * inv, f1 = exp2f(shift - half);
+          const int64_t place = 2 * (int64_t)blockIdx.x + (step == 0 ? 1 : 0);
+          float4* const part = a.part + (place * 8 + st * 4 + w) * (32 * 32) + lane;
+          if (!whole) a.ml[place * kUnitRows + r] = make_float2(m, l);
+          const int t = r / a.g;
+          const int64_t o = (int64_t)(s.first + tok0 + t) * a.o_row + (int64_t)(kvh * a.g + r - t * a.g) * a.o_head;
+          uint32_t ra[32];
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld32_async(to + 32 * c, ra);
+            tmem_wait_ld32(ra);
+            float x[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(ra[k]) * f0 * f1;
+            if (!whole) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) part[(8 * c + k) * 32] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+            } else if (r < rows) {
+              if (a.out_bf16) {
+                __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(a.out) + o + 32 * c;
+                if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0u) {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    uint32_t y[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                      const __nv_bfloat162 z = __floats2bfloat162_rn(x[8 * k + 2 * j], x[8 * k + 2 * j + 1]);
+                      y[j] = *reinterpret_cast<const uint32_t*>(&z);
+                    }
+                    reinterpret_cast<uint4*>(p)[k] = make_uint4(y[0], y[1], y[2], y[3]);
+                  }
+                } else {
+#pragma unroll
+                  for (int k = 0; k < 32; ++k) p[k] = __float2bfloat16_rn(x[k]);
+                }
+              } else {
+                float* p = reinterpret_cast<float*>(a.out) + o + 32 * c;
+                if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0u) {
+#pragma unroll
+                  for (int k = 0; k < 8; ++k)
+                    reinterpret_cast<float4*>(p)[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+                } else {
+#pragma unroll
+                  for (int k = 0; k < 32; ++k) p[k] = x[k];
+                }
+              }
+            }
+          }
+        }
+      }
+    } else if (warp < kMmaWarp) {
+      // --------------------------------------------------------- producers
+      const int w = warp - kSoftWarps;
+      const int blocks = (min(s.ctx, s.ctx - s.n + tok0 + min(a.per, s.n - tok0)) + kBlock - 1) / kBlock;  // of the unit's context
+      const int32_t* const row = a.table + (int64_t)seq * a.max_blocks;
+      auto block_id = [&](int t) {  // of the warp's block of step t: -1 past the end
+        const int j = (step + t) * kTileBlocks + w;
+        return t < n && j < blocks ? __ldg(row + j) : -1;
+      };
+      auto valid = [&](int id) { return id >= 0 && id < a.num_blocks; };
+      Page pk, pv;
+      auto page_of = [&](const uint8_t* pool, int id) { return pool + ((int64_t)id * a.Hkv + kvh) * kI8Page; };
+      auto fetch = [&](Page& p, const uint8_t* pool, int id) {
+        if (valid(id)) {
+          load_page(p, page_of(pool, id), lane);
+        } else {  // (finite operands, whatever the weights)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) p.w[i] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+        }
+      };
+      // lanes 0 and 1: step and bits of the block's K and V, requested a step ahead
+      auto tail_of = [&](int id) {
+        uint2 t = make_uint2(0u, 0u);
+        if (valid(id) && lane < 2) t = __ldg(reinterpret_cast<const uint2*>(page_of(lane ? a.vpool : a.kpool, id) + kI8Codes));
+        return t;
+      };
+      auto put_k = [&](int t) {
+        const int turn = done0 + t, st = turn & 1;
+        if (turn >= 2 && !__all_sync(0xffffffffu, mbar_wait(kempty + st, ((turn >> 1) & 1) ^ 1))) return false;
+        store_page(pk, k_op + (uint32_t)st * kOperand, w, lane);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(kfull + st);
+        return true;
+      };
+      int id = block_id(0), id1 = block_id(1);
+      uint2 tail = tail_of(id);
+      fetch(pk, a.kpool, id);
+      fetch(pv, a.vpool, id);
+      ok = put_k(0);
+      if (n > 1) fetch(pk, a.kpool, id1);
+      for (int t = 0; t < n && ok; ++t) {
+        const int turn = done0 + t, slot = turn & (kSlots - 1);
+        const int id2 = block_id(t + 2);
+        const uint32_t bad = (tail.y | __shfl_down_sync(0xffffffffu, tail.y, 1)) & 0xFFFFu;  // (lane 0: of K and V)
+        if (lane < 2) {
+          float* const sp = reinterpret_cast<float*>(gen + kOffStep + slot * 96) + w;
+          sp[8 * lane] = __uint_as_float(tail.x);
+          if (lane == 1) sp[16] = (float)((int)((tail.x >> 23) & 255u) - 126);
+        }
+        if (lane == 0) {
+          if (!valid(id) && (step + t) * kTileBlocks + w < blocks) flag_status(a.status, TQ_DEV_BAD_BLOCK);
+          reinterpret_cast<uint32_t*>(gen + kOffBits + slot * 32)[w] = (valid(id) ? 0xFFFF0000u : 0u) | bad;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(gfull + slot);
+        tail = tail_of(id1);
+        // the next step's K goes ahead of this one's V: the tensor cores want it first
+        if (t + 1 < n && !(ok = put_k(t + 1))) break;
+        if (t + 2 < n) fetch(pk, a.kpool, id2);
+        const int vst = turn & vbit;
+        if (turn > vbit) ok = __all_sync(0xffffffffu, mbar_wait(vempty + vst, ((turn >> vbit) & 1) ^ 1));
+        if (!ok) break;
+        store_page(pv, v_op + (uint32_t)vst * kOperand, w, lane);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(vfull + vst);
+        if (t + 1 < n) fetch(pv, a.vpool, id1);
+        id = id1;
+        id1 = id2;
+      }
+    } else {
+      // --------------------------------------------------------------- MMA
+      const bool issue = elect_one();
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      constexpr uint32_t idesc_s = umma_idesc_16(false, false, kTile, kTile), idesc_o = umma_idesc_16(false, true, kTile, kTile);
+      const uint64_t dq = umma_desc_sw128(base), dk = umma_desc_sw128(k_op), dv = umma_desc_sw128_mn(v_op, kPanel);
+      auto logits = [&](int i, int st) {
+        const int turn = done0 + i, ks = turn & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(kfull + ks, (turn >> 1) & 1))) return false;
+        tc_fence_after();
+        const uint64_t q = dq + (uint64_t)(st * (kOperand >> 4)), k = dk + (uint64_t)(ks * (kOperand >> 4));
+        const uint32_t d = tm + (uint32_t)(st * kTile);
+        if (issue) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint64_t off = (uint64_t)((j >> 2) * (kPanel >> 4) + (j & 3) * 2);
+            umma_bf16(d, q + off, k + off, idesc_s, j > 0);
+          }
+          if constexpr (EXACT) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint64_t off = (uint64_t)((j >> 2) * (kPanel >> 4) + (j & 3) * 2);
+              umma_bf16(d, q + (uint64_t)(2 * kOperand >> 4) + off, k + off, idesc_s, true);
+            }
+          }
+          umma_commit(smem_u32(sfull + st));
+          if (!two || st == 1) umma_commit(smem_u32(kempty + ks));
+        }
+        __syncwarp();
+        return true;
+      };
+      auto values = [&](int i, int st) {
+        const int turn = done0 + i, vst = turn & vbit;
+        if (!__all_sync(0xffffffffu, mbar_wait(pfull + st, ((st ? done1 : done0) + i) & 1) &&
+                                         mbar_wait(vfull + vst, (turn >> vbit) & 1)))
+          return false;
+        tc_fence_after();
+        const uint64_t v = dv + (uint64_t)(vst * (kOperand >> 4));
+        const uint32_t d = tm + (uint32_t)((2 + st) * kTile), p = tm + (uint32_t)(st * kTile);
+        if (issue) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            umma_16_ts(d, p + (uint32_t)(32 * (j >> 1) + 8 * (j & 1)), v + (uint64_t)(j * (16 * 128 >> 4)), idesc_o, i > 0 || j > 0);
+          if constexpr (EXACT) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              umma_16_ts(d, p + (uint32_t)(32 * (j >> 1) + 8 * (j & 1) + 16), v + (uint64_t)(j * (16 * 128 >> 4)), idesc_o, true);
+          }
+          if (!two || st == 1) umma_commit(smem_u32(vempty + vst));
+          if (i + 1 == n) umma_commit(smem_u32(odone + st));
+        }
+        __syncwarp();
+        return true;
+      };
+      ok = logits(0, 0);
+      if (ok && two) ok = logits(0, 1);
+      for (int i = 0; i < n && ok; ++i) {
+        ok = values(i, 0);
+        if (ok && i + 1 < n) ok = logits(i + 1, 0);
+        if (ok && two) ok = values(i, 1);
+        if (ok && two && i + 1 < n) ok = logits(i + 1, 1);
+      }
+    }
+    if (!ok && lane == 0) {
+      flag_status(a.status, TQ_DEV_WAIT_TIMEOUT);
+      misc.dead = 1;
+    }
+    // ---- the unit's other parts, if it was cut
+    const bool cut = !(step == 0 && n == all);
+    if (cut) __threadfence();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (misc.dead) break;
+    if (cut) {
+      auto cta_of = [&](int64_t p) { return ((p + 1) * R - 1) / total; };
+      const int64_t unit0 = at - step, c0 = cta_of(unit0), c1 = cta_of(unit0 + all - 1);
+      if (threadIdx.x == 0) {
+        const int k = atomicAdd(a.counters + c0, 1);
+        misc.arrived = k == (int)(c1 - c0);
+        if (misc.arrived) a.counters[c0] = 0;
+        __threadfence();
+      }
+      __syncthreads();
+      if (misc.arrived && warp < kSoftWarps && 32 * warp < rows) {
+        const int r = 32 * warp + lane;
+        auto place = [&](int64_t c) { return 2 * c + (c == c0 ? 1 : 0); };
+        float M = -INFINITY, L = 0.0f;
+        for (int64_t c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(&a.ml[place(c) * kUnitRows + r]).x);
+        for (int64_t c = c0; c <= c1; ++c) {
+          const float2 e = __ldcg(&a.ml[place(c) * kUnitRows + r]);
+          L += e.x == -INFINITY ? e.y : e.y * exp2f(e.x - M);
+        }
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+        const int t = r / a.g;
+        const int64_t o = (int64_t)(s.first + tok0 + t) * a.o_row + (int64_t)(kvh * a.g + r - t * a.g) * a.o_head;
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          float4 x[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          for (int64_t c = c0; c <= c1; ++c) {
+            const float2 e = __ldcg(&a.ml[place(c) * kUnitRows + r]);
+            const float f = (e.x == -INFINITY ? e.y : e.y * exp2f(e.x - M)) * inv;
+            const float4* p = a.part + (place(c) * 8 + warp) * (32 * 32) + lane;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float4 v = __ldcg(p + (8 * q + k) * 32);
+              x[k].x = fmaf(f, v.x, x[k].x);
+              x[k].y = fmaf(f, v.y, x[k].y);
+              x[k].z = fmaf(f, v.z, x[k].z);
+              x[k].w = fmaf(f, v.w, x[k].w);
+            }
+          }
+          if (r >= rows) continue;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int64_t j = o + 32 * q + 4 * k;
+            if (a.out_bf16) {
+              __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(a.out) + j;
+              p[0] = __float2bfloat16_rn(x[k].x);
+              p[1] = __float2bfloat16_rn(x[k].y);
+              p[2] = __float2bfloat16_rn(x[k].z);
+              p[3] = __float2bfloat16_rn(x[k].w);
+            } else {
+              float* p = reinterpret_cast<float*>(a.out) + j;
+              p[0] = x[k].x;
+              p[1] = x[k].y;
+              p[2] = x[k].z;
+              p[3] = x[k].w;
+            }
+          }
+        }
+      }
+      __syncthreads();
+    }
+    // ---- on
+    at += n;
+    done0 += n;
+    ++turns0;
+    if (two) {
+      done1 += n;
+      ++turns1;
+    }
+    if (at < end) {
+      step = 0;
+      if (++tile == tiles_of(a, s)) {
+        tile = 0;
+        if (++kvh == a.Hkv) {
+          kvh = 0;
+          do s = seq_of(a, ++seq, false);
+          while (!s.large);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <bool EXACT>
+cudaError_t run_tiles(const AttArgs& a, int num_sms, cudaStream_t st) {
+  static std::atomic<uint64_t> ready{0};  // devices (up to 64) whose kernel has its shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(ready.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(k_int8_attend<EXACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_release);
+  }
+  k_int8_attend<EXACT><<<num_sms, kThreads, kSmem, st>>>(a);
+  count_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t int8_attend_partial_bytes(int num_sms) {
+  return (size_t)2 * num_sms * kUnitRows * (kD * sizeof(float) + sizeof(float2));
+}
+
+cudaError_t launch_int8_tiles(const AttendCall& c, uint8_t* partials, int num_sms, cudaStream_t st) {
+  const tq_cache_desc& d = *c.desc;
+  AttArgs a = {};
+  a.kpool = reinterpret_cast<const uint8_t*>(d.k_cache);
+  a.vpool = reinterpret_cast<const uint8_t*>(d.v_cache);
+  a.num_blocks = d.num_blocks;
+  a.table = c.block_table;
+  a.max_blocks = c.max_blocks;
+  a.ctx_lens = c.ctx_lens;
+  a.starts = c.starts;
+  a.seqs = c.batch;
+  a.q = c.q->in;
+  a.q_bf16 = c.q_dtype == TQ_BF16 ? 1 : 0;
+  a.q_row = c.q->in_token_stride;
+  a.q_head = c.q->in_head_stride;
+  a.out = c.q->out;
+  a.out_bf16 = c.out_dtype == TQ_BF16 ? 1 : 0;
+  a.o_row = c.q->out_token_stride;
+  a.o_head = c.q->out_head_stride;
+  a.n_tokens = (int)c.n_tokens;
+  a.Hkv = d.num_kv_heads;
+  a.g = c.q->num_heads / d.num_kv_heads;
+  a.per = kUnitRows / a.g;
+  a.scale = c.sm_scale * 1.4426950408889634f;
+  a.counters = reinterpret_cast<int*>(c.workspace);
+  a.part = reinterpret_cast<float4*>(partials);
+  a.ml = reinterpret_cast<float2*>(partials + (size_t)2 * num_sms * kUnitRows * kD * sizeof(float));
+  a.status = c.status;
+  return c.q_dtype == TQ_F32 ? run_tiles<true>(a, num_sms, st) : run_tiles<false>(a, num_sms, st);
+}
+
+}  // namespace tq

@@ -47,6 +47,7 @@ struct DecArgs {
   const int32_t* ctx_lens;
   const int32_t* starts;  // attend: first token of each sequence (null: a row is a sequence)
   int seqs;
+  int64_t most_rows;  // attend: rows a KV head of a sequence that is not left to the tiles
   const void* q;
   int q_bf16;
   int64_t q_row, q_head;  // strides in elements
@@ -110,8 +111,9 @@ __device__ __forceinline__ int row_ctx(const DecArgs& a, int row, int seq, bool 
     ctx = ctx < 0 ? 0 : most;
   }
   if (a.starts) {  // causal: the sequence's last token sees all of it
-    const int next = __ldg(a.starts + seq + 1);
-    if (row < __ldg(a.starts + seq) || row >= next) return -1;  // behind the last sequence
+    const int start = __ldg(a.starts + seq), next = __ldg(a.starts + seq + 1);
+    if (row < start || row >= next) return -1;               // behind the last sequence
+    if ((int64_t)(next - start) * a.g > a.most_rows) return -1;  // takes tiles
     ctx = max(0, ctx - (next - 1 - row));
   }
   return ctx;
@@ -671,7 +673,7 @@ cudaError_t run_decode(const DecArgs& a, int num_sms, cudaStream_t st) {
 
 }  // namespace
 
-size_t int8_partial_bytes(int num_sms) { return (size_t)2 * num_sms * 8 * (kD + 2) * sizeof(float); }
+size_t int8_partial_bytes(int num_sms) { return ((size_t)2 * num_sms * 8 * (kD + 2) * sizeof(float) + 255) & ~(size_t)255; }
 
 static cudaError_t launch_rows(const tq_cache_desc& d, DecArgs& a, uint8_t* workspace, int num_sms, cudaStream_t st) {
   a.kpool = reinterpret_cast<const uint8_t*>(d.k_cache);
@@ -724,7 +726,12 @@ cudaError_t launch_int8_attend(const AttendCall& c, int num_sms, cudaStream_t st
   a.rows = (int)c.n_tokens;
   a.scale = c.sm_scale * 1.4426950408889634f;
   a.status = c.status;
-  return launch_rows(*c.desc, a, c.workspace, num_sms, st);
+  const int g = a.Hq / c.desc->num_kv_heads;
+  const bool tiles = g <= kAttMostGroup && c.n_tokens * g > kAttRows;
+  a.most_rows = tiles ? kAttRows : INT64_MAX;
+  const cudaError_t e = launch_rows(*c.desc, a, c.workspace, num_sms, st);
+  if (e != cudaSuccess || !tiles) return e;
+  return launch_int8_tiles(c, c.workspace + kCounterRegionBytes + int8_partial_bytes(num_sms), num_sms, st);
 }
 
 }  // namespace tq

@@ -157,7 +157,8 @@ cudaError_t launch_int8_append(const tq_cache_desc& d, const void* k, const void
                                int64_t n_tok, unsigned* status, int num_sms, cudaStream_t st);
 cudaError_t launch_int8_dequant(const tq_cache_desc& d, int which, const int64_t* slots, int64_t n, void* out, int out_dtype,
                                 unsigned* status, int num_sms, cudaStream_t st);
-size_t int8_partial_bytes(int num_sms);
+size_t int8_partial_bytes(int num_sms);         // (a multiple of 256)
+size_t int8_attend_partial_bytes(int num_sms);  // behind it, for attend
 cudaError_t launch_int8_decode(const DecodeCall& c, int num_sms, cudaStream_t st);
 cudaError_t launch_int8_attend(const AttendCall& c, int num_sms, cudaStream_t st);
 // Polar layers (tq_polar.cu); the generic launchers above route them here.
