@@ -9,16 +9,17 @@
 // Both roundings are those of the exact quotient, whatever the order of operations: the fp32 product with
 // 1 / s is off by less than 2^-16 of a code, and where it lies that near to the middle between two codes
 // the quotient is formed in 64 bits, which holds what decides (two 24-bit numbers, 31 bits with the code).
+#include "tq_async.cuh"
 #include "tq_int8.cuh"
 
 namespace tq {
 namespace {
 
-constexpr int kAppWarps = 8;
-constexpr int kAppChunk = 16;  // tokens a CTA of a large call
+constexpr int kAppWarps = 16;  // of a CTA at most
+constexpr int kAppChunk = 64;  // tokens of a CTA at most
 // Tokens up to which a CTA looks for the other tokens of its blocks itself.  Beyond, two passes over the
 // slots leave the tokens of a block in its own page first.
-constexpr int kScanMost = 8192;
+constexpr int kScanMost = 2048;
 
 struct AppendArgs {
   const void* x[2];   // keys, values (null: none)
@@ -32,147 +33,203 @@ struct AppendArgs {
   unsigned* status;
 };
 
-// x / s to the nearest code; inv = 1 / s rounded.
-__device__ __forceinline__ int code_of(float x, float s, float inv) {
-  const float t = x * inv;
-  float k = rintf(t);
-  if (fabsf(fabsf(t - k) - 0.5f) < 3.0517578125e-5f) k = (float)rint((double)x / (double)s);
-  return min(max((int)k, -127), 127);
+// Codes of four values x / s: the product with inv = 1 / s, rounded once, goes next to 1.5 * 2^23 + 128, whose
+// last byte is the code + 128.  *far takes the largest distance of a product from its code.
+__device__ __forceinline__ uint32_t codes4(const float (&x)[4], float inv, float* far) {
+  constexpr float kMagic = 12582912.0f + 128.0f;
+  uint32_t y[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float m = fmaf(x[k], inv, kMagic);
+    y[k] = __float_as_uint(m);
+    *far = fmaxf(*far, fabsf(fmaf(x[k], inv, -(m - kMagic))));
+  }
+  return prmt(prmt(y[0], y[1], 0x0040u), prmt(y[2], y[3], 0x0040u), 0x5410u);
 }
-// code * r to the nearest code, r = s_old / s_new <= 1.
-__device__ __forceinline__ int recode(int c, float s_old, float s_new, float r) {
-  const float t = (float)c * r;
-  float k = rintf(t);
-  if (fabsf(fabsf(t - k) - 0.5f) < 3.0517578125e-5f) k = (float)rint((double)c * (double)s_old / (double)s_new);
-  return (int)k;
-}
+// The code of the exact quotient x / s.
+__device__ __noinline__ uint32_t exact_code(double x, float s) { return (uint32_t)((int)rint(x / (double)s) + 128); }
+// Products this near to the middle between two codes do not decide.
+constexpr float kMiddle = 0.5f - 3.0517578125e-5f;
 
 // One page by one warp, a lane four coordinates of each record; token[r] (shared memory): what record r
-// takes, -1 for none.
+// takes, if bit r of rows is set.
 template <typename T>
 __device__ __forceinline__ void append_page(const T* x, int64_t stride, uint8_t* page, const int* token, uint32_t rows,
                                             int lane) {
+  constexpr int W = sizeof(T);  // words of four values
   I8Tail* const tail = reinterpret_cast<I8Tail*>(page + kI8Codes);
-  const float s_old = tail->step;
-  const uint32_t bad_old = tail->bad;
-  float v[kBlock][4];
-  uint32_t top = 0u;  // bits of the largest magnitude
+  uint32_t* const at = reinterpret_cast<uint32_t*>(page) + lane;
+  const uint2 t_old = *reinterpret_cast<const uint2*>(tail);
+  uint32_t v[kBlock][W];
+  // (the codes that are there come along: few calls begin in the middle of a block, and those wait for latency)
+  const bool there = !(rows & 1u);
 #pragma unroll
   for (int r = 0; r < kBlock; ++r) {
-    if (!((rows >> r) & 1u)) continue;
-    const T* p = x + (int64_t)token[r] * stride + 4 * lane;
-    if constexpr (sizeof(T) == 2) {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
-      v[r][0] = __uint_as_float(w.x << 16);
-      v[r][1] = __uint_as_float(w.x & 0xFFFF0000u);
-      v[r][2] = __uint_as_float(w.y << 16);
-      v[r][3] = __uint_as_float(w.y & 0xFFFF0000u);
-    } else {
-      const float4 w = __ldg(reinterpret_cast<const float4*>(p));
-      v[r][0] = w.x; v[r][1] = w.y; v[r][2] = w.z; v[r][3] = w.w;
+    if ((rows >> r) & 1u) {
+      const T* p = x + (int64_t)token[r] * stride + 4 * lane;
+      if constexpr (W == 2) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+        v[r][0] = w.x;
+        v[r][1] = w.y;
+      } else {
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
+        v[r][0] = w.x; v[r][1] = w.y; v[r][W - 2] = w.z; v[r][W - 1] = w.w;
+      }
+    } else if (there) {
+      v[r][0] = at[32 * r];
     }
   }
+  // the largest magnitude (bits of it)
+  auto top_of = [&](int r) {
+    uint32_t m = 0u;
+    if constexpr (W == 2) {
+      m = __vmaxu2(v[r][0] & 0x7FFF7FFFu, v[r][1] & 0x7FFF7FFFu);  // two halves
+    } else {
 #pragma unroll
-  for (int r = 0; r < kBlock; ++r) {
-    if (!((rows >> r) & 1u)) continue;
+      for (int k = 0; k < W; ++k) m = max(m, v[r][k] & 0x7FFFFFFFu);
+    }
+    return m;
+  };
+  auto whole = [&](uint32_t m) {  // of all lanes and halves
+    if constexpr (W == 2) m = max(m << 16, m & 0xFFFF0000u);
+    return __reduce_max_sync(0xffffffffu, m);
+  };
+  uint32_t top = 0u;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) top = max(top, __float_as_uint(v[r][k]) & 0x7FFFFFFFu);
-  }
-  top = __reduce_max_sync(0xffffffffu, top);
+  for (int r = 0; r < kBlock; ++r)
+    if ((rows >> r) & 1u) {
+      if constexpr (W == 2) top = __vmaxu2(top, top_of(r));
+      else top = max(top, top_of(r));
+    }
+  top = whole(top);
   uint32_t bad = 0u;
   if (top >= 0x7F800000u) {  // records that are not finite stay out
     top = 0u;
 #pragma unroll
     for (int r = 0; r < kBlock; ++r) {
       if (!((rows >> r) & 1u)) continue;
-      uint32_t m = 0u;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) m = max(m, __float_as_uint(v[r][k]) & 0x7FFFFFFFu);
-      m = __reduce_max_sync(0xffffffffu, m);
+      const uint32_t m = whole(top_of(r));
       if (m >= 0x7F800000u) {
         bad |= 1u << r;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[r][k] = 0.0f;
+        for (int k = 0; k < W; ++k) v[r][k] = 0u;
       } else {
         top = max(top, m);
       }
     }
   }
   // (a step that no append has left counts as none)
-  const bool begins = (rows & 1u) || !(s_old >= kI8Least && s_old < INFINITY);
+  const float s_old = __uint_as_float(t_old.x);
+  const bool begins = !there || !(s_old >= kI8Least && s_old < INFINITY);
   float s = fmaxf(__fdiv_rn(__uint_as_float(top), 127.0f), kI8Least);
   if (!begins) s = fmaxf(s, s_old);
-  const float inv = __fdiv_rn(1.0f, s);
-  uint32_t* const at = reinterpret_cast<uint32_t*>(page) + lane;
-  if (begins) {
-#pragma unroll
-    for (int r = 0; r < kBlock; ++r)
-      if (!((rows >> r) & 1u)) at[32 * r] = 0x80808080u;
-  } else if (s != s_old) {
-    const float ratio = __fdiv_rn(s_old, s);
-#pragma unroll 4
-    for (int r = 0; r < kBlock; ++r) {
-      if ((rows >> r) & 1u) continue;
-      const uint32_t w = at[32 * r];
-      uint32_t o = 0u;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) o |= (uint32_t)(recode((int)((w >> (8 * k)) & 255u) - 128, s_old, s, ratio) + 128) << (8 * k);
-      at[32 * r] = o;
-    }
-  }
+  const float inv = __fdiv_rn(1.0f, s), ratio = begins ? 0.0f : __fdiv_rn(s_old, s);
+  const bool recode = !begins && s != s_old;
+  uint32_t again = 0u;  // records with a value near the middle between two codes
 #pragma unroll
   for (int r = 0; r < kBlock; ++r) {
-    if (!((rows >> r) & 1u)) continue;
-    uint32_t o = 0u;
+    float far = 0.0f;
+    if ((rows >> r) & 1u) {
+      float f[4];
+      if constexpr (W == 2) {
+        f[0] = __uint_as_float(v[r][0] << 16);
+        f[1] = __uint_as_float(v[r][0] & 0xFFFF0000u);
+        f[2] = __uint_as_float(v[r][1] << 16);
+        f[3] = __uint_as_float(v[r][1] & 0xFFFF0000u);
+      } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) o |= (uint32_t)(code_of(v[r][k], s, inv) + 128) << (8 * k);
-    at[32 * r] = o;
+        for (int k = 0; k < 4; ++k) f[k] = __uint_as_float(v[r][k & (W - 1)]);
+      }
+      at[32 * r] = codes4(f, inv, &far);
+    } else if (begins) {
+      at[32 * r] = 0x80808080u;
+    } else if (recode) {
+      float f[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f[k] = (float)((int)((v[r][0] >> (8 * k)) & 255u) - 128);
+      at[32 * r] = codes4(f, ratio, &far);
+    }
+    if (far > kMiddle) again |= 1u << r;
   }
-  if (lane == 0) *reinterpret_cast<float2*>(tail) = make_float2(s, __uint_as_float((begins ? 0u : bad_old & ~rows) | bad));
+  while (again) {  // (a lane at a time, a code in ten thousand)
+    const int r = __ffs(again) - 1;
+    again &= again - 1u;
+    const bool fresh = (rows >> r) & 1u;
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+      double y;
+      if (fresh) {
+        y = (double)load_elem(x + (int64_t)token[r] * stride + 4 * lane + k);
+      } else {
+        uint32_t w = 0u;  // (the page has the new codes by now)
+#pragma unroll
+        for (int i = 0; i < kBlock; ++i) w = i == r ? v[i][0] : w;
+        y = (double)((int)((w >> (8 * k)) & 255u) - 128) * (double)s_old;
+      }
+      page[r * kD + 4 * lane + k] = (uint8_t)exact_code(y, s);
+    }
+  }
+  if (lane == 0) *reinterpret_cast<uint2*>(tail) = make_uint2(__float_as_uint(s), (begins ? 0u : t_old.y & ~rows) | bad);
 }
 
 // A CTA takes the blocks whose first token (of the call) is one of its `chunk` tokens.  With a slot given
 // twice the later token stays.
 template <typename T>
 __global__ void __launch_bounds__(kAppWarps * 32) k_int8_append(const __grid_constant__ AppendArgs a) {
-  __shared__ int block_of[kAppChunk];       // distinct blocks of the chunk's tokens, -1 for none
+  __shared__ int block_of[kAppChunk];       // distinct blocks of the chunk's tokens; their number in `blocks`
   __shared__ int first[kAppChunk];
   __shared__ int token[kAppChunk][kBlock];  // 1 + the token of each record, 0 for none
-  const int t0 = blockIdx.x * a.chunk, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int head_page = a.x[0] ? 0 : 1;
-  if (threadIdx.x < kAppChunk * kBlock) token[threadIdx.x / kBlock][threadIdx.x % kBlock] = 0;
-  if (threadIdx.x < kAppChunk) {
-    const int t = t0 + threadIdx.x;
-    int64_t s = threadIdx.x < a.chunk && t < a.n ? __ldg(a.slots + t) : -1;
-    if (s >= a.max_slot) {
-      flag_status(a.status, TQ_DEV_BAD_SLOT);
-      s = -1;
+  __shared__ int own[kAppChunk];            // which of the blocks are the CTA's
+  __shared__ int blocks, owned;
+  const int t0 = blockIdx.x * a.chunk, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  if (a.marked) grid_dep_wait();
+  for (int i = threadIdx.x; i < kAppChunk * kBlock; i += blockDim.x) (&token[0][0])[i] = 0;
+  if (threadIdx.x < kAppChunk) first[threadIdx.x] = 0x7FFFFFFF;
+  if (threadIdx.x == 0) owned = 0;
+  if (warp == 0) {
+    int n = 0;
+    for (int i0 = 0; i0 < a.chunk; i0 += 32) {
+      const int t = t0 + i0 + lane;
+      int64_t s = i0 + lane < a.chunk && t < a.n ? __ldg(a.slots + t) : -1;
+      if (s >= a.max_slot) {
+        flag_status(a.status, TQ_DEV_BAD_SLOT);
+        s = -1;
+      }
+      const int b = s < 0 ? -1 : (int)(s / kBlock);
+      // the lowest lane of each block that is not in the list yet
+      const uint32_t same = __match_any_sync(0xffffffffu, b);  // (by all lanes, those without a block too)
+      bool fresh = b >= 0 && __ffs(same) - 1 == lane;
+      for (int i = 0; i < n; ++i) fresh = fresh && block_of[i] != b;
+      const uint32_t take = __ballot_sync(0xffffffffu, fresh);
+      if (fresh) block_of[n + __popc(take & ((1u << lane) - 1u))] = b;
+      n += __popc(take);
+      __syncwarp();
     }
-    block_of[threadIdx.x] = s < 0 ? -1 : (int)(s / kBlock);
-    first[threadIdx.x] = 0x7FFFFFFF;
+    if (lane == 0) blocks = n;
   }
   __syncthreads();
-  bool again = false;  // one entry a block
-  if (threadIdx.x < kAppChunk)
-    for (int i = 0; i < (int)threadIdx.x; ++i) again |= block_of[i] == block_of[threadIdx.x];
-  __syncthreads();
-  if (again) block_of[threadIdx.x] = -1;
-  __syncthreads();
+  const int nb = blocks;
+  if (nb == 0) return;
   if (!a.marked) {
-    for (int t = threadIdx.x; t < a.n; t += blockDim.x) {
-      const int64_t s = __ldg(a.slots + t);
-      if (s < 0 || s >= a.max_slot) continue;
-      const int b = (int)(s / kBlock);
-      for (int i = 0; i < a.chunk; ++i) {
-        if (block_of[i] != b) continue;
-        atomicMax(&token[i][s % kBlock], t + 1);
-        atomicMin(&first[i], t);
+    constexpr int kAhead = 4;
+    for (int tb = threadIdx.x; tb < a.n; tb += kAhead * blockDim.x) {
+      int64_t s[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) s[k] = tb + k * (int)blockDim.x < a.n ? __ldg(a.slots + tb + k * blockDim.x) : -1;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (s[k] < 0 || s[k] >= a.max_slot) continue;
+        const int b = (int)(s[k] / kBlock), t = tb + k * (int)blockDim.x;
+        for (int i = 0; i < nb; ++i) {
+          if (block_of[i] != b) continue;
+          atomicMax(&token[i][s[k] % kBlock], t + 1);
+          atomicMin(&first[i], t);
+        }
       }
     }
   } else {
-    for (int i = warp; i < a.chunk; i += kAppWarps) {
-      if (block_of[i] < 0) continue;
-      const uint8_t* page = a.pool[head_page] + (int64_t)block_of[i] * a.Hkv * kI8Page;
+    for (int i = warp; i < nb; i += warps) {
+      const uint8_t* page = a.pool[a.x[0] ? 0 : 1] + (int64_t)block_of[i] * a.Hkv * kI8Page;
       const I8Tail* tail = reinterpret_cast<const I8Tail*>(page + kI8Codes);
       const int f = (int)tail->first;
       if (f < t0 || f >= t0 + a.chunk) continue;  // (another CTA's, which may be writing it)
@@ -181,28 +238,22 @@ __global__ void __launch_bounds__(kAppWarps * 32) k_int8_append(const __grid_con
     }
   }
   __syncthreads();
-  if (threadIdx.x < kAppChunk) {
-    if (first[threadIdx.x] < t0) block_of[threadIdx.x] = -1;
-    if (first[threadIdx.x] >= t0 + a.chunk) block_of[threadIdx.x] = -1;
-  }
-  if (threadIdx.x < kAppChunk * kBlock) token[threadIdx.x / kBlock][threadIdx.x % kBlock] -= 1;
+  if (threadIdx.x < nb && first[threadIdx.x] >= t0 && first[threadIdx.x] < t0 + a.chunk) own[atomicAdd(&owned, 1)] = threadIdx.x;
+  for (int i = threadIdx.x; i < kAppChunk * kBlock; i += blockDim.x) (&token[0][0])[i] -= 1;
   __syncthreads();
-  for (int i = 0; i < a.chunk; ++i) {
-    const int b = block_of[i];
-    if (b < 0) continue;
+  for (int p = warp; p < owned * 2 * a.Hkv; p += warps) {
+    const int i = own[p / (2 * a.Hkv)], q = p % (2 * a.Hkv), w = q / a.Hkv, h = q - w * a.Hkv;
+    if (!a.x[w]) continue;
     const uint32_t rows = __ballot_sync(0xffffffffu, lane < kBlock && token[i][lane & 15] >= 0);
-    for (int p = warp; p < 2 * a.Hkv; p += kAppWarps) {
-      const int w = p / a.Hkv, h = p - w * a.Hkv;
-      if (!a.x[w]) continue;
-      append_page(reinterpret_cast<const T*>(a.x[w]) + (int64_t)h * kD, (int64_t)a.Hkv * kD,
-                  a.pool[w] + ((int64_t)b * a.Hkv + h) * kI8Page, token[i], rows, lane);
-    }
+    append_page(reinterpret_cast<const T*>(a.x[w]) + (int64_t)h * kD, (int64_t)a.Hkv * kD,
+                a.pool[w] + ((int64_t)block_of[i] * a.Hkv + h) * kI8Page, token[i], rows, lane);
   }
 }
 
 // The two passes of a large call.  A record that the call writes holds 1 + its token until then, the tail
 // which records these are and the first token; all in the first page of the block.
 __global__ void k_int8_clear(uint8_t* pool, int Hkv, const int64_t* slots, int n, int64_t max_slot) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int t = blockIdx.x * blockDim.x + threadIdx.x; t < n; t += gridDim.x * blockDim.x) {
     const int64_t s = __ldg(slots + t);
     if (s < 0 || s >= max_slot) continue;
@@ -213,6 +264,8 @@ __global__ void k_int8_clear(uint8_t* pool, int Hkv, const int64_t* slots, int n
   }
 }
 __global__ void k_int8_mark(uint8_t* pool, int Hkv, const int64_t* slots, int n, int64_t max_slot) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_dep_wait();
   for (int t = blockIdx.x * blockDim.x + threadIdx.x; t < n; t += gridDim.x * blockDim.x) {
     const int64_t s = __ldg(slots + t);
     if (s < 0 || s >= max_slot) continue;
@@ -272,18 +325,34 @@ cudaError_t launch_int8_append(const tq_cache_desc& d, const void* k, const void
   a.max_slot = d.num_blocks * kBlock;
   a.status = status;
   a.marked = n_tok > kScanMost ? 1 : 0;
-  a.chunk = n_tok <= 4 * num_sms ? 1 : kAppChunk;
+  // a warp a page: CTAs of 16 tokens (a block, in a prompt) or of more where a block has few heads; with few tokens
+  // each has a CTA
+  const bool few = n_tok <= 2 * num_sms;
+  a.chunk = few ? 1 : kBlock * (a.Hkv < 4 ? 4 / a.Hkv : 1);
+  const int threads = few ? kAppWarps * 32 : 256;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.marked;  // (dependents of this call's own kernels)
+  cudaError_t e = cudaSuccess;
   if (a.marked) {
     uint8_t* pool = a.pool[k ? 0 : 1];
     const unsigned grid = (unsigned)((n_tok + 255) / 256 < 8 * num_sms ? (n_tok + 255) / 256 : 8 * num_sms);
     k_int8_clear<<<grid, 256, 0, st>>>(pool, a.Hkv, slots, a.n, a.max_slot);
     count_launch();
-    k_int8_mark<<<grid, 256, 0, st>>>(pool, a.Hkv, slots, a.n, a.max_slot);
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(256);
+    e = cudaLaunchKernelEx(&cfg, k_int8_mark, pool, a.Hkv, slots, a.n, a.max_slot);
+    if (e != cudaSuccess) return e;
     count_launch();
   }
-  const unsigned grid = (unsigned)((n_tok + a.chunk - 1) / a.chunk);
-  if (in_dtype == TQ_F32) k_int8_append<float><<<grid, kAppWarps * 32, 0, st>>>(a);
-  else k_int8_append<__nv_bfloat16><<<grid, kAppWarps * 32, 0, st>>>(a);
+  cfg.gridDim = dim3((unsigned)((n_tok + a.chunk - 1) / a.chunk));
+  cfg.blockDim = dim3(threads);
+  e = in_dtype == TQ_F32 ? cudaLaunchKernelEx(&cfg, k_int8_append<float>, a) : cudaLaunchKernelEx(&cfg, k_int8_append<__nv_bfloat16>, a);
+  if (e != cudaSuccess) return e;
   count_launch();
   return cudaGetLastError();
 }
