@@ -573,7 +573,7 @@ tq_status tq_decode_attention_static(const tq_cache_desc* desc, const void* q, i
 typedef struct {
   int64_t num_blocks;     /* up to 2^30 */
   int32_t* refs;          /* device [num_blocks] */
-  void* workspace;        /* device, 256-byte aligned, any contents */
+  void* workspace;        /* device, 256-byte aligned, zero before the first call (every call leaves it ready for the next) */
   size_t workspace_bytes; /* at least tq_blocks_workspace_bytes(num_blocks, rows of the call) */
 } tq_block_pool;
 

@@ -492,6 +492,7 @@ class Layer:
                 self.qjl_proj = torch.from_numpy(np.ascontiguousarray(s)).to(device)
                 d.qjl_proj = self.qjl_proj.data_ptr()
         self.desc = d
+        self.desc_ptr = ctypes.pointer(d)
         self.page_bytes_k = self.page_bytes(0)
         self.page_bytes_v = self.page_bytes(1)
         nk = self.num_blocks * self.num_kv_heads * self.page_bytes_k
@@ -735,7 +736,7 @@ def append_layers(layers, ks, vs, slot_mapping, stream=None):
     """Quantize-on-append of the same tokens into several layers (tq_quantize_append_layers):
     ks[l], vs[l] [n_tokens, H_kv, d] are layer l's inputs (either list may be None)."""
     n_layers = len(layers)
-    descs = (ctypes.POINTER(CacheDesc) * n_layers)(*[ctypes.pointer(ly.desc) for ly in layers])
+    descs = _descs(layers)
     def ptrs(ts, name):
         if ts is None:
             return None
@@ -746,7 +747,7 @@ def append_layers(layers, ks, vs, slot_mapping, stream=None):
 
 
 def _descs(layers):
-    return (ctypes.POINTER(CacheDesc) * len(layers))(*[ctypes.pointer(ly.desc) for ly in layers])
+    return (_D * len(layers))(*[ly.desc_ptr for ly in layers])
 
 
 def copy_blocks(layers, src, dst, stream=None):
@@ -779,7 +780,7 @@ class Blocks:
             size = lib().tq_blocks_workspace_bytes(self.num_blocks, rows)
             if size == 0:
                 raise TQError(TQ_ERR_INVALID_ARG, last_error() or "invalid sizes")
-            self._workspaces.append(_new(torch.empty, (int(size),), torch.uint8, self.refs.device, stream))
+            self._workspaces.append(_new(torch.zeros, (int(size),), torch.uint8, self.refs.device, stream))
             self._rows = rows
         ws = self._workspaces[-1]
         refs = _index_ptr(self.refs, "refs", torch.int32, (self.num_blocks,))

@@ -3,11 +3,12 @@
 //
 // Everything is decided on the device; no call waits for it.  Free blocks are given out lowest first,
 // in the order of the rows (and columns) that ask, which makes every call a function of its inputs and
-// keeps the pool dense.  A call is a few small kernels in a row:
-//   reorder  k_children (which rows are kept, which need a copy of their last block), k_rows (counts, the
-//            new table), k_free + k_take (the lowest free blocks), k_fork (pages, all layers)
-//   extend   k_need, k_free + k_take, k_put
-//   compact  k_free (used blocks a segment), k_lists (holes below, used blocks above), k_move, k_remap
+// keeps the pool dense.  What has to be decided in one place is decided by one CTA, in which a thread has 16
+// counts of the pool at a time: a launch costs more than its few microseconds.
+//   reorder  k_rows (counts, the new table; the CTA that arrives last finds who needs a copy and takes the
+//            blocks), k_fork (pages, all layers)
+//   extend   k_extend
+//   compact  k_lists (who moves where), k_move (pages, all layers, and the tables)
 // The pages are the bytes that count: a part is one pool (keys or values) of one layer, and a CTA copies
 // one block of one part at a time, 16 bytes a thread and load.
 #include <cuda_runtime.h>
@@ -21,9 +22,8 @@
 namespace tq {
 namespace {
 
-constexpr int kSegment = 2048;   // blocks of the pool a CTA looks through
-constexpr int kSegThreads = 256;
 constexpr int kMaxParts = 128;   // pools a launch: 64 layers
+constexpr int kFewRows = 4096;   // rows whose children are found without a kernel of their own
 
 struct Part {
   uint8_t* pool;
@@ -40,17 +40,17 @@ struct Rows {
   int rows, max_blocks;
 };
 
-// Workspace of a call: arrays of ints.
+// Workspace of a call: arrays of ints.  The ticket is zero between calls.
 struct Work {
-  int* count;   // [rows] new rows of an old row
-  int* first;   // [rows] the first of them
-  int* rank;    // [rows] of a new row among those that need a block, -1; extend: entries before the row's
-  int* row_of;  // [rows] the other way round
-  int* segment; // [segments] free (compact: used) blocks
+  int* ticket;
+  int* sums;    // [2] blocks asked for (compact: to move), blocks there are
   int* list;    // [num_blocks] blocks taken, lowest first; compact: holes
   int* movers;  // [num_blocks] compact: used blocks to move
   int* map;     // [num_blocks] compact: where a block went
-  int* sums;    // [4] blocks asked for, blocks there are, (compact) used blocks, blocks to move
+  int* count;   // [rows] new rows of an old row (many rows)
+  int* first;   // [rows] the first of them (many rows)
+  int* rank;    // [rows] extend: entries before the row's
+  int* row_of;  // [rows] new rows that need a block, in order
 };
 
 __device__ __forceinline__ int tokens_of(const Rows& r, int row, unsigned* status, bool flag) {
@@ -84,12 +84,10 @@ __device__ __forceinline__ int cta_scan(int v, int* smem, int* all) {
 }
 
 constexpr int kPlanThreads = 1024;
+constexpr int kRowThreads = 256;
 
-// Children of each old row, and the new rows that need a block of their own: all but the first of an old
-// row whose last block is not full.
-__global__ void __launch_bounds__(kPlanThreads) k_children(Rows from, const int32_t* parents, int n_new, int64_t num_blocks,
-                                                           Work w, unsigned* status) {
-  __shared__ int smem[32];
+// Children of each old row, for calls of many rows.
+__global__ void __launch_bounds__(kPlanThreads) k_children(Rows from, const int32_t* parents, int n_new, Work w) {
   for (int b = threadIdx.x; b < from.rows; b += kPlanThreads) {
     w.count[b] = 0;
     w.first[b] = n_new;
@@ -97,44 +95,75 @@ __global__ void __launch_bounds__(kPlanThreads) k_children(Rows from, const int3
   __syncthreads();
   for (int i = threadIdx.x; i < n_new; i += kPlanThreads) {
     const int p = __ldg(parents + i);
-    if (p >= 0 && p < from.rows) {
-      atomicAdd(w.count + p, 1);
-      atomicMin(w.first + p, i);
-    } else if (p != -1) {
-      flag_status(status, TQ_DEV_BAD_ROW);
-    }
+    if (p < 0 || p >= from.rows) continue;
+    atomicAdd(w.count + p, 1);
+    atomicMin(w.first + p, i);
   }
-  __syncthreads();
-  int before = 0;
-  for (int i0 = 0; i0 < n_new; i0 += kPlanThreads) {
-    const int i = i0 + threadIdx.x;
-    int need = 0;
-    if (i < n_new) {
-      const int p = __ldg(parents + i);
-      if (p >= 0 && p < from.rows && __ldcg(w.first + p) != i) {
-        const int n = tokens_of(from, p, status, false);
-        if (n % kBlock != 0) {
-          const int id = __ldg(from.table + (int64_t)p * from.max_blocks + n / kBlock);
-          need = id >= 0 && id < num_blocks ? 1 : 0;
-        }
-      }
-    }
-    int all;
-    const int at = before + cta_scan<kPlanThreads>(need, smem, &all) - need;
-    if (i < n_new) w.rank[i] = need ? at : -1;
-    if (need) w.row_of[at] = i;
-    before += all;
-  }
-  if (threadIdx.x == 0) w.sums[0] = before;
 }
 
-// CTAs 0 .. from.rows - 1: the counts of an old row's blocks; the others: a new row.
-__global__ void __launch_bounds__(128) k_rows(Rows from, Rows to, const int32_t* parents, int32_t* refs, int64_t num_blocks,
-                                              Work w, unsigned* status) {
+// Sixteen counts of the pool from block i on (what lies past its end counts as used).
+struct Counts {
+  int v[16];
+};
+__device__ __forceinline__ void load_counts(Counts& c, const int32_t* refs, int64_t i, int64_t num_blocks) {
+  if (i + 16 <= num_blocks && (reinterpret_cast<uintptr_t>(refs) & 15u) == 0u) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int4 x = __ldcg(reinterpret_cast<const int4*>(refs + i) + k);
+      c.v[4 * k] = x.x; c.v[4 * k + 1] = x.y; c.v[4 * k + 2] = x.z; c.v[4 * k + 3] = x.w;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) c.v[k] = i + k < num_blocks ? __ldcg(refs + i + k) : 1;
+  }
+}
+
+// The `want` lowest free blocks are held once from here on; put(rank, block) takes each.  Returns how many there were.
+template <int THREADS, typename Put>
+__device__ __forceinline__ int take_blocks(int32_t* refs, int64_t num_blocks, int want, int* smem, Put put) {
+  int before = 0;
+  for (int64_t i0 = 0; i0 < num_blocks && before < want; i0 += 16 * THREADS) {
+    const int64_t i = i0 + 16 * (int64_t)threadIdx.x;
+    Counts c;
+    load_counts(c, refs, i, num_blocks);
+    int n = 0, all;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) n += c.v[k] <= 0 ? 1 : 0;
+    int at = before + cta_scan<THREADS>(n, smem, &all) - n;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      if (c.v[k] > 0) continue;
+      if (at < want) {
+        put(at, (int)(i + k));
+        refs[i + k] = 1;
+      }
+      ++at;
+    }
+    before += all;
+  }
+  return min(before, want);
+}
+
+// CTAs 0 .. from.rows - 1: the counts of an old row's blocks; the others: a new row.  The CTA that arrives last
+// finds the new rows that need a block of their own -- all but the first of an old row whose last block is
+// not full -- and takes blocks for them.
+__global__ void __launch_bounds__(kRowThreads) k_rows(Rows from, Rows to, const int32_t* parents, int32_t* refs, int64_t num_blocks,
+                                                      Work w, unsigned* status) {
+  __shared__ int smem[32];
+  __shared__ int first[kFewRows];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const bool few = max(from.rows, to.rows) <= kFewRows;
   if ((int)blockIdx.x < from.rows) {
     const int b = blockIdx.x, n = tokens_of(from, b, status, threadIdx.x == 0), used = blocks_of(n);
-    const int children = __ldcg(w.count + b);
-    for (int j = threadIdx.x; j < used; j += blockDim.x) {
+    int children = 0;
+    if (few) {
+      int mine = 0;
+      for (int i = threadIdx.x; i < to.rows; i += kRowThreads) mine += __ldg(parents + i) == b ? 1 : 0;
+      cta_scan<kRowThreads>(mine, smem, &children);
+    } else {
+      children = __ldcg(w.count + b);
+    }
+    for (int j = threadIdx.x; j < used; j += kRowThreads) {
       const int id = __ldg(from.table + (int64_t)b * from.max_blocks + j);
       if (id < 0 || id >= num_blocks) {
         flag_status(status, TQ_DEV_BAD_BLOCK);
@@ -143,66 +172,71 @@ __global__ void __launch_bounds__(128) k_rows(Rows from, Rows to, const int32_t*
       const int more = (j + 1) * kBlock > n ? min(children, 1) - 1 : children - 1;
       if (more != 0 && atomicAdd(refs + id, more) + more < 0) flag_status(status, TQ_DEV_BAD_BLOCK);
     }
-    return;
-  }
-  const int i = blockIdx.x - from.rows, p = __ldg(parents + i);
-  const bool there = p >= 0 && p < from.rows;
-  const int n = there ? tokens_of(from, p, status, false) : 0, used = blocks_of(n);
-  const bool own = __ldcg(w.rank + i) >= 0;
-  for (int j = threadIdx.x; j < to.max_blocks; j += blockDim.x) {
-    int id = -1;
-    if (j < used && !(own && j == used - 1)) id = __ldg(from.table + (int64_t)p * from.max_blocks + j);
-    to.table[(int64_t)i * to.max_blocks + j] = id;
-  }
-  if (threadIdx.x == 0) to.lens[i] = n;
-}
-
-// Free (or, for a compaction, used) blocks of each segment of the pool.
-__global__ void __launch_bounds__(kSegThreads) k_free(const int32_t* refs, int64_t num_blocks, int used, Work w) {
-  __shared__ int smem[32];
-  const int64_t i0 = (int64_t)blockIdx.x * kSegment;
-  int n = 0;
-  for (int k = threadIdx.x; k < kSegment; k += kSegThreads)
-    if (i0 + k < num_blocks) n += (__ldcg(refs + i0 + k) > 0) == (used != 0) ? 1 : 0;
-  int all;
-  cta_scan<kSegThreads>(n, smem, &all);
-  if (threadIdx.x == 0) w.segment[blockIdx.x] = all;
-}
-
-// Sum of w.segment over [0, n).
-__device__ __forceinline__ int segments_before(const Work& w, int n, int* smem) {
-  int v = 0, all;
-  for (int s = threadIdx.x; s < n; s += kSegThreads) v += __ldcg(w.segment + s);
-  cta_scan<kSegThreads>(v, smem, &all);
-  return all;
-}
-
-// The sums[0] lowest free blocks are held once from here on.
-__global__ void __launch_bounds__(kSegThreads) k_take(int32_t* refs, int64_t num_blocks, Work w, unsigned* status) {
-  __shared__ int smem[32];
-  const int want = __ldcg(w.sums);
-  const bool last = blockIdx.x + 1 == gridDim.x;
-  if (want == 0) {
-    if (last && threadIdx.x == 0) w.sums[1] = 0;
-    return;
-  }
-  int before = segments_before(w, blockIdx.x, smem);
-  if (before >= want && !last) return;
-  const int64_t i0 = (int64_t)blockIdx.x * kSegment;
-  for (int k = 0; k < kSegment; k += kSegThreads) {
-    const int64_t i = i0 + k + threadIdx.x;
-    const int free = i < num_blocks && __ldcg(refs + i) <= 0 ? 1 : 0;
-    int all;
-    const int at = before + cta_scan<kSegThreads>(free, smem, &all) - free;
-    if (free && at < want) {
-      w.list[at] = (int)i;
-      refs[i] = 1;
+  } else {
+    const int i = blockIdx.x - from.rows, p = __ldg(parents + i);
+    const bool there = p >= 0 && p < from.rows;
+    if (!there && p != -1 && threadIdx.x == 0) flag_status(status, TQ_DEV_BAD_ROW);
+    const int n = there ? tokens_of(from, p, status, false) : 0, used = blocks_of(n);
+    int again = 0;  // an earlier row has the same parent
+    if (few) {
+      for (int k = threadIdx.x; k < i; k += kRowThreads) again |= __ldg(parents + k) == p;
+      again = __syncthreads_or(again);
+    } else if (there) {
+      again = __ldcg(w.first + p) != i;
     }
-    before += all;
+    const bool own = again && n % kBlock != 0;  // (an entry outside the pool stays as it is)
+    for (int j = threadIdx.x; j < to.max_blocks; j += kRowThreads) {
+      int id = -1;
+      if (j < used) {
+        id = __ldg(from.table + (int64_t)p * from.max_blocks + j);
+        if (own && j == used - 1 && id >= 0 && id < num_blocks) id = -1;
+      }
+      to.table[(int64_t)i * to.max_blocks + j] = id;
+    }
+    if (threadIdx.x == 0) to.lens[i] = n;
   }
-  if (last && threadIdx.x == 0) {
-    w.sums[1] = min(before, want);
-    if (before < want) flag_status(status, TQ_DEV_NO_BLOCK);
+  __threadfence();
+  __shared__ int last;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    last = atomicAdd(w.ticket, 1) == (int)gridDim.x - 1;
+    if (last) *w.ticket = 0;
+    __threadfence();
+  }
+  __syncthreads();
+  if (!last) return;
+  if (few) {
+    for (int b = threadIdx.x; b < from.rows; b += kRowThreads) first[b] = to.rows;
+    __syncthreads();
+    for (int i = threadIdx.x; i < to.rows; i += kRowThreads) {
+      const int p = __ldg(parents + i);
+      if (p >= 0 && p < from.rows) atomicMin(first + p, i);
+    }
+    __syncthreads();
+  }
+  int want = 0;
+  for (int i0 = 0; i0 < to.rows; i0 += kRowThreads) {
+    const int i = i0 + threadIdx.x;
+    int need = 0;
+    if (i < to.rows) {
+      const int p = __ldg(parents + i);
+      if (p >= 0 && p < from.rows && (few ? first[p] : __ldcg(w.first + p)) != i) {
+        const int n = tokens_of(from, p, status, false);
+        if (n % kBlock != 0) {
+          const int id = __ldg(from.table + (int64_t)p * from.max_blocks + n / kBlock);
+          need = id >= 0 && id < num_blocks ? 1 : 0;
+        }
+      }
+    }
+    int all;
+    const int at = want + cta_scan<kRowThreads>(need, smem, &all) - need;
+    if (need) w.row_of[at] = i;
+    want += all;
+  }
+  const int got = take_blocks<kRowThreads>(refs, num_blocks, want, smem, [&](int at, int id) { w.list[at] = id; });
+  if (threadIdx.x == 0) {
+    w.sums[1] = got;
+    if (got < want) flag_status(status, TQ_DEV_NO_BLOCK);
   }
 }
 
@@ -223,6 +257,7 @@ __device__ __forceinline__ void copy_block(const Part& p, int64_t src, int64_t d
 
 // The copies of a reordering: new row row_of[k] takes block list[k], with the pages of its parent's last.
 __global__ void __launch_bounds__(256) k_fork(const __grid_constant__ Parts parts, Rows from, Rows to, const int32_t* parents, Work w) {
+  grid_dep_wait();
   const int n = __ldcg(w.sums + 1), per = max(parts.n, 1);
   for (int64_t u = blockIdx.x; u < (int64_t)n * per; u += gridDim.x) {
     const int k = (int)(u / per), part = (int)(u - (int64_t)k * per);
@@ -233,32 +268,47 @@ __global__ void __launch_bounds__(256) k_fork(const __grid_constant__ Parts part
   }
 }
 
-// Entries that the rows need, and how many before each row.
-__global__ void __launch_bounds__(kPlanThreads) k_need(Rows r, const int32_t* new_lens, Work w, unsigned* status) {
+// Entries that the rows need, how many before each row, and the blocks for them: the block of rank k goes to the last
+// row with no more than k entries before its own.
+__global__ void __launch_bounds__(kPlanThreads) k_extend(Rows r, const int32_t* new_lens, int32_t* refs, int64_t num_blocks, Work w,
+                                                         unsigned* status) {
   __shared__ int smem[32];
-  int before = 0;
+  __shared__ int rank[kPlanThreads], spot[kPlanThreads];  // (of the first rows; spot: the first entry to fill)
+  int want = 0;
   for (int b0 = 0; b0 < r.rows; b0 += kPlanThreads) {
     const int b = b0 + threadIdx.x;
-    int need = 0;
+    int need = 0, used = 0;
     if (b < r.rows) {
       const Rows grown = {nullptr, const_cast<int32_t*>(new_lens), r.rows, r.max_blocks};
-      need = max(0, blocks_of(tokens_of(grown, b, status, true)) - blocks_of(tokens_of(r, b, status, true)));
+      used = blocks_of(tokens_of(r, b, status, true));
+      need = max(0, blocks_of(tokens_of(grown, b, status, true)) - used);
     }
     int all;
-    const int at = before + cta_scan<kPlanThreads>(need, smem, &all) - need;
+    const int at = want + cta_scan<kPlanThreads>(need, smem, &all) - need;
     if (b < r.rows) {
       w.rank[b] = at;
-      w.count[b] = need;
+      if (b < kPlanThreads) {
+        rank[b] = at;
+        spot[b] = used;
+      }
     }
-    before += all;
+    want += all;
   }
-  if (threadIdx.x == 0) w.sums[0] = before;
-}
-__global__ void __launch_bounds__(128) k_put(Rows r, Work w) {
-  const int b = blockIdx.x, need = __ldcg(w.count + b), at = __ldcg(w.rank + b), there = __ldcg(w.sums + 1);
-  if (need == 0) return;
-  int32_t* row = r.table + (int64_t)b * r.max_blocks + blocks_of(tokens_of(r, b, nullptr, false));
-  for (int j = threadIdx.x; j < need; j += blockDim.x) row[j] = at + j < there ? __ldcg(w.list + at + j) : -1;
+  __syncthreads();
+  auto put = [&](int k, int id) {
+    int lo = 0, hi = r.rows - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if ((mid < kPlanThreads ? rank[mid] : w.rank[mid]) <= k) lo = mid;
+      else hi = mid - 1;
+    }
+    const bool near = lo < kPlanThreads;
+    const int from = near ? spot[lo] : blocks_of(tokens_of(r, lo, status, false));
+    r.table[(int64_t)lo * r.max_blocks + from + k - (near ? rank[lo] : w.rank[lo])] = id;
+  };
+  const int got = take_blocks<kPlanThreads>(refs, num_blocks, want, smem, put);
+  for (int k = got + threadIdx.x; k < want; k += kPlanThreads) put(k, -1);
+  if (threadIdx.x == 0 && got < want) flag_status(status, TQ_DEV_NO_BLOCK);
 }
 
 __global__ void __launch_bounds__(128) k_release(Rows r, const uint8_t* which, int32_t* refs, int64_t num_blocks, unsigned* status) {
@@ -275,54 +325,82 @@ __global__ void __launch_bounds__(128) k_release(Rows r, const uint8_t* which, i
   if (threadIdx.x == 0) r.lens[b] = 0;
 }
 
-// Holes (free blocks below the number of used ones) and movers (used blocks from there on), lowest first.
-__global__ void __launch_bounds__(kSegThreads) k_lists(const int32_t* refs, int64_t num_blocks, Work w, int32_t* live_out) {
+// Holes (free blocks below the number of used ones) and movers (used blocks from there on), lowest first, and
+// where every block goes.
+__global__ void __launch_bounds__(kPlanThreads) k_lists(int32_t* refs, int64_t num_blocks, Work w, int32_t* live_out) {
   __shared__ int smem[32];
-  const int live = segments_before(w, gridDim.x, smem);
-  // used blocks below `live`: whole segments, and a part of one
-  const int split = live / kSegment;
-  int below = segments_before(w, split, smem);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int live = 0;
+  for (int64_t i0 = 0; i0 < num_blocks; i0 += 16 * kPlanThreads) {
+    Counts c;
+    load_counts(c, refs, i0 + 16 * (int64_t)threadIdx.x, num_blocks);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) live += i0 + 16 * (int64_t)threadIdx.x + k < num_blocks && c.v[k] > 0 ? 1 : 0;
+  }
   {
-    int n = 0, all;
-    for (int k = threadIdx.x; k < kSegment; k += kSegThreads) {
-      const int64_t i = (int64_t)split * kSegment + k;
-      if (i < live && __ldcg(refs + i) > 0) ++n;
-    }
-    cta_scan<kSegThreads>(n, smem, &all);
-    below += all;
-  }
-  int before = segments_before(w, blockIdx.x, smem);
-  const int64_t i0 = (int64_t)blockIdx.x * kSegment;
-  for (int k = 0; k < kSegment; k += kSegThreads) {
-    const int64_t i = i0 + k + threadIdx.x;
-    const int used = i < num_blocks && __ldcg(refs + i) > 0 ? 1 : 0;
     int all;
-    const int at = before + cta_scan<kSegThreads>(used, smem, &all) - used;  // used blocks before i
-    if (i < num_blocks) w.map[i] = (int)i;
-    if (!used && i < live) w.list[i - at] = (int)i;
-    if (used && i >= live) w.movers[at - below] = (int)i;
-    before += all;
+    cta_scan<kPlanThreads>(live, smem, &all);
+    live = all;
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    w.sums[3] = live - below;
+  int holes = 0, movers = 0;  // before the round's blocks
+  for (int64_t i0 = 0; i0 < num_blocks; i0 += 16 * kPlanThreads) {
+    const int64_t i = i0 + 16 * (int64_t)threadIdx.x;
+    Counts c;
+    load_counts(c, refs, i, num_blocks);
+    int h = 0, m = 0, all_h, all_m;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      h += i + k < live && c.v[k] <= 0 ? 1 : 0;
+      m += i + k >= live && i + k < num_blocks && c.v[k] > 0 ? 1 : 0;
+    }
+    int at_h = holes + cta_scan<kPlanThreads>(h, smem, &all_h) - h, at_m = movers + cta_scan<kPlanThreads>(m, smem, &all_m) - m;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      if (i + k >= num_blocks) break;
+      w.map[i + k] = (int)(i + k);
+      if (i + k < live) {
+        if (c.v[k] <= 0) w.list[at_h++] = (int)(i + k);
+      } else if (c.v[k] > 0) {
+        w.movers[at_m++] = (int)(i + k);
+      }
+    }
+    holes += all_h;
+    movers += all_m;
+  }
+  __syncthreads();
+  for (int k = threadIdx.x; k < movers; k += kPlanThreads) {  // (as many as holes)
+    const int src = w.movers[k], dst = w.list[k];
+    w.map[src] = dst;
+    refs[dst] = refs[src];
+    refs[src] = 0;
+  }
+  if (threadIdx.x == 0) {
+    w.sums[0] = movers;
     if (live_out) *live_out = live;
   }
 }
-__global__ void __launch_bounds__(256) k_move(const __grid_constant__ Parts parts, int32_t* refs, Work w, int first_launch) {
-  const int n = __ldcg(w.sums + 3), per = max(parts.n, 1);
-  for (int64_t u = blockIdx.x; u < (int64_t)n * per; u += gridDim.x) {
-    const int k = (int)(u / per), part = (int)(u - (int64_t)k * per);
-    const int src = __ldcg(w.movers + k), dst = __ldcg(w.list + k);
-    if (first_launch && part == 0 && threadIdx.x == 0) {
-      w.map[src] = dst;
-      refs[dst] = refs[src];
-      refs[src] = 0;
+
+constexpr int kMaxTables = 8;  // tables a launch
+struct Tables {
+  int n;
+  Rows t[kMaxTables];
+};
+// CTAs from `copies` on: the rows of the tables.
+__global__ void __launch_bounds__(256) k_move(const __grid_constant__ Parts parts, const __grid_constant__ Tables tables, int copies,
+                                              int64_t num_blocks, Work w, unsigned* status) {
+  grid_dep_wait();
+  if ((int)blockIdx.x < copies) {
+    const int n = __ldcg(w.sums);
+    for (int64_t u = blockIdx.x; u < (int64_t)n * parts.n; u += copies) {
+      const int k = (int)(u / parts.n), part = (int)(u - (int64_t)k * parts.n);
+      copy_block(parts.part[part], __ldcg(w.movers + k), __ldcg(w.list + k));
     }
-    if (part < parts.n) copy_block(parts.part[part], src, dst);
+    return;
   }
-}
-__global__ void __launch_bounds__(128) k_remap(Rows r, int64_t num_blocks, Work w, unsigned* status) {
-  const int b = blockIdx.x, used = blocks_of(tokens_of(r, b, status, threadIdx.x == 0));
+  int b = blockIdx.x - copies, t = 0;
+  while (b >= tables.t[t].rows) b -= tables.t[t++].rows;
+  const Rows& r = tables.t[t];
+  const int used = blocks_of(tokens_of(r, b, status, threadIdx.x == 0));
   for (int j = threadIdx.x; j < used; j += blockDim.x) {
     int32_t* at = r.table + (int64_t)b * r.max_blocks + j;
     const int id = *at;
@@ -362,7 +440,6 @@ __global__ void __launch_bounds__(256) k_copy_pairs(const __grid_constant__ Part
 
 // ------------------------------------------------------------------- host side
 
-int segments_of(int64_t num_blocks) { return (int)((num_blocks + kSegment - 1) / kSegment); }
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 size_t layout(int64_t num_blocks, int rows, uint8_t* base, Work* w) {
@@ -373,8 +450,8 @@ size_t layout(int64_t num_blocks, int rows, uint8_t* base, Work* w) {
     return p;
   };
   Work x;
-  x.sums = take(4);
-  x.segment = take(segments_of(num_blocks));
+  x.ticket = take(1);
+  x.sums = take(2);
   x.list = take(num_blocks);
   x.movers = take(num_blocks);
   x.map = take(num_blocks);
@@ -448,12 +525,20 @@ tq_status launched(const char* what) {
   return e == cudaSuccess ? TQ_OK : fail(TQ_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-void take_blocks(const tq_block_pool& p, const Work& w, unsigned* status, cudaStream_t st) {
-  const int segs = segments_of(p.num_blocks);
-  k_free<<<segs, kSegThreads, 0, st>>>(p.refs, p.num_blocks, 0, w);
+// A launch as a programmatic dependent of this call's kernel before it.
+template <typename... A, typename... B>
+cudaError_t follow(void (*kernel)(A...), unsigned grid, unsigned threads, cudaStream_t st, B... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   count_launch();
-  k_take<<<segs, kSegThreads, 0, st>>>(p.refs, p.num_blocks, w, status);
-  count_launch();
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace
@@ -510,10 +595,7 @@ tq_status tq_blocks_extend(const tq_block_pool* pool, const tq_block_rows* rows,
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   Work w;
   layout(pool->num_blocks, rows->rows, reinterpret_cast<uint8_t*>(pool->workspace), &w);
-  k_need<<<1, kPlanThreads, 0, st>>>(rows_of(*rows), new_lens, w, status);
-  count_launch();
-  take_blocks(*pool, w, status, st);
-  k_put<<<rows->rows, 128, 0, st>>>(rows_of(*rows), w);
+  k_extend<<<1, kPlanThreads, 0, st>>>(rows_of(*rows), new_lens, pool->refs, pool->num_blocks, w, status);
   count_launch();
   return launched(fn);
 }
@@ -551,14 +633,17 @@ tq_status tq_blocks_reorder(const tq_block_pool* pool, const tq_cache_desc* cons
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   Work w;
   layout(pool->num_blocks, from->rows > to->rows ? from->rows : to->rows, reinterpret_cast<uint8_t*>(pool->workspace), &w);
-  k_children<<<1, kPlanThreads, 0, st>>>(rows_of(*from), parents, to->rows, pool->num_blocks, w, status);
-  count_launch();
-  k_rows<<<from->rows + to->rows, 128, 0, st>>>(rows_of(*from), rows_of(*to), parents, pool->refs, pool->num_blocks, w, status);
-  count_launch();
-  take_blocks(*pool, w, status, st);
-  for (int l0 = 0; l0 == 0 || l0 < n_layers; l0 += kMaxParts / 2) {
-    k_fork<<<8 * sms, 256, 0, st>>>(parts_of(descs, n_layers, l0), rows_of(*from), rows_of(*to), parents, w);
+  if ((from->rows > to->rows ? from->rows : to->rows) > kFewRows) {
+    k_children<<<1, kPlanThreads, 0, st>>>(rows_of(*from), parents, to->rows, w);
     count_launch();
+  }
+  k_rows<<<from->rows + to->rows, kRowThreads, 0, st>>>(rows_of(*from), rows_of(*to), parents, pool->refs, pool->num_blocks, w, status);
+  count_launch();
+  for (int l0 = 0; l0 == 0 || l0 < n_layers; l0 += kMaxParts / 2) {
+    const cudaError_t e = l0 == 0 ? follow(k_fork, 8 * sms, 256, st, parts_of(descs, n_layers, l0), rows_of(*from), rows_of(*to), parents, w)
+                                  : (k_fork<<<8 * sms, 256, 0, st>>>(parts_of(descs, n_layers, l0), rows_of(*from), rows_of(*to), parents, w),
+                                     count_launch(), cudaGetLastError());
+    if (e != cudaSuccess) return fail(TQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
   }
   return launched(fn);
 }
@@ -582,19 +667,30 @@ tq_status tq_blocks_compact(const tq_block_pool* pool, const tq_cache_desc* cons
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   Work w;
   layout(pool->num_blocks, 0, reinterpret_cast<uint8_t*>(pool->workspace), &w);
-  const int segs = segments_of(pool->num_blocks);
-  k_free<<<segs, kSegThreads, 0, st>>>(pool->refs, pool->num_blocks, 1, w);
+  k_lists<<<1, kPlanThreads, 0, st>>>(pool->refs, pool->num_blocks, w, live);
   count_launch();
-  k_lists<<<segs, kSegThreads, 0, st>>>(pool->refs, pool->num_blocks, w, live);
-  count_launch();
-  for (int l0 = 0; l0 == 0 || l0 < n_layers; l0 += kMaxParts / 2) {
-    k_move<<<8 * sms, 256, 0, st>>>(parts_of(descs, n_layers, l0), pool->refs, w, l0 == 0 ? 1 : 0);
-    count_launch();
-  }
-  for (int t = 0; t < n_tables; ++t) {
-    if (tables[t].rows == 0) continue;
-    k_remap<<<tables[t].rows, 128, 0, st>>>(rows_of(tables[t]), pool->num_blocks, w, status);
-    count_launch();
+  // pages of 64 layers and rows of kMaxTables tables a launch, the first of them behind k_lists
+  for (int l0 = 0, t0 = 0; (l0 == 0 && t0 == 0) || l0 < n_layers || t0 < n_tables; l0 += kMaxParts / 2, t0 += kMaxTables) {
+    const Parts p = parts_of(descs, n_layers, l0 < n_layers ? l0 : n_layers);
+    Tables ts;
+    ts.n = 0;
+    int64_t rows = 0;
+    for (int t = t0; t < n_tables && ts.n < kMaxTables; ++t) {
+      ts.t[ts.n++] = rows_of(tables[t]);
+      rows += tables[t].rows;
+    }
+    const int copies = p.n > 0 ? 8 * sms : 0;
+    if (copies + rows == 0) continue;
+    const unsigned grid = (unsigned)(copies + rows);
+    cudaError_t e = cudaSuccess;
+    if (l0 == 0) {
+      e = follow(k_move, grid, 256, st, p, ts, copies, pool->num_blocks, w, status);
+    } else {
+      k_move<<<grid, 256, 0, st>>>(p, ts, copies, pool->num_blocks, w, status);
+      count_launch();
+      e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) return fail(TQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
   }
   if (moved) {
     const int64_t grid = (pool->num_blocks + 255) / 256;

@@ -277,35 +277,49 @@ __global__ void k_int8_mark(uint8_t* pool, int Hkv, const int64_t* slots, int n,
   }
 }
 
+// A warp a token, its heads' records four at a time.
 template <typename O>
 __global__ void __launch_bounds__(256) k_int8_dequant(const uint8_t* pool, int Hkv, int64_t max_slot, const int64_t* slots,
-                                                      int64_t n_vec, O* out, unsigned* status) {
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n_vec * 32; i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t vec = i >> 5, t = vec / Hkv;
-    const int lane = (int)(i & 31), h = (int)(vec - t * Hkv);
+                                                      int64_t n, O* out, unsigned* status) {
+  constexpr int kAhead = 4;
+  const int lane = threadIdx.x & 31;
+  const bool wide = (reinterpret_cast<uintptr_t>(out) & (4 * sizeof(O) - 1)) == 0u;
+  for (int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); t < n; t += (int64_t)gridDim.x * 8) {
     const int64_t s = __ldg(slots + t);
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (s >= max_slot) {
-      if (lane == 0) flag_status(status, TQ_DEV_BAD_SLOT);
-    } else if (s >= 0) {
-      const uint8_t* page = pool + (s / kBlock * Hkv + h) * kI8Page;
-      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(page + s % kBlock * kD) + lane);
-      const uint2 tail = __ldg(reinterpret_cast<const uint2*>(page + kI8Codes));
-      const float step = (tail.y >> (s % kBlock)) & 1u ? NAN : __uint_as_float(tail.x);
+    if (s >= max_slot && lane == 0) flag_status(status, TQ_DEV_BAD_SLOT);
+    const bool there = s >= 0 && s < max_slot;
+    const int r = (int)(s & (kBlock - 1));
+    const uint8_t* page = pool + (there ? s / kBlock * Hkv : 0) * kI8Page;
+    O* o = out + t * Hkv * kD + 4 * lane;
+    for (int h0 = 0; h0 < Hkv; h0 += kAhead) {
+      uint32_t w[kAhead];
+      uint2 tail[kAhead];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = (float)((int)((w >> (8 * k)) & 255u) - 128) * step;
-    }
-    O* o = out + vec * kD + 4 * lane;
-    if ((reinterpret_cast<uintptr_t>(out) & (4 * sizeof(O) - 1)) == 0u) {
-      if constexpr (sizeof(O) == 4) {
-        *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
-      } else {
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
-        *reinterpret_cast<uint2*>(o) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      for (int k = 0; k < kAhead; ++k) {
+        w[k] = 0x80808080u;
+        tail[k] = make_uint2(0u, 0u);
+        if (!there || h0 + k >= Hkv) continue;
+        w[k] = __ldg(reinterpret_cast<const uint32_t*>(page + (int64_t)(h0 + k) * kI8Page + r * kD) + lane);
+        tail[k] = __ldg(reinterpret_cast<const uint2*>(page + (int64_t)(h0 + k) * kI8Page + kI8Codes));
       }
-    } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) store_elem(o + k, v[k]);
+      for (int k = 0; k < kAhead; ++k) {
+        if (h0 + k >= Hkv) break;
+        const float step = (tail[k].y >> r) & 1u ? NAN : __uint_as_float(tail[k].x);
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = (float)((int)((w[k] >> (8 * i)) & 255u) - 128) * step;
+        O* p = o + (int64_t)(h0 + k) * kD;
+        if (!wide) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) store_elem(p + i, v[i]);
+        } else if constexpr (sizeof(O) == 4) {
+          *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
+          *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        }
+      }
     }
   }
 }
@@ -360,14 +374,13 @@ cudaError_t launch_int8_append(const tq_cache_desc& d, const void* k, const void
 cudaError_t launch_int8_dequant(const tq_cache_desc& d, int which, const int64_t* slots, int64_t n, void* out, int out_dtype,
                                 unsigned* status, int num_sms, cudaStream_t st) {
   const uint8_t* pool = reinterpret_cast<const uint8_t*>(which == 0 ? d.k_cache : d.v_cache);
-  const int64_t n_vec = n * d.num_kv_heads;
-  int64_t grid = (n_vec * 32 + 255) / 256;
-  if (grid > (int64_t)num_sms * 16) grid = (int64_t)num_sms * 16;
+  int64_t grid = (n + 7) / 8;
+  if (grid > (int64_t)num_sms * 64) grid = (int64_t)num_sms * 64;
   if (out_dtype == TQ_F32)
-    k_int8_dequant<float><<<(unsigned)grid, 256, 0, st>>>(pool, d.num_kv_heads, d.num_blocks * kBlock, slots, n_vec,
+    k_int8_dequant<float><<<(unsigned)grid, 256, 0, st>>>(pool, d.num_kv_heads, d.num_blocks * kBlock, slots, n,
                                                           reinterpret_cast<float*>(out), status);
   else
-    k_int8_dequant<__nv_bfloat16><<<(unsigned)grid, 256, 0, st>>>(pool, d.num_kv_heads, d.num_blocks * kBlock, slots, n_vec,
+    k_int8_dequant<__nv_bfloat16><<<(unsigned)grid, 256, 0, st>>>(pool, d.num_kv_heads, d.num_blocks * kBlock, slots, n,
                                                                   reinterpret_cast<__nv_bfloat16*>(out), status);
   count_launch();
   return cudaGetLastError();
