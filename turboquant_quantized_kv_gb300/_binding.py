@@ -770,21 +770,26 @@ class Blocks:
     def __init__(self, num_blocks, device="cuda"):
         torch = _torch()
         self.num_blocks = int(num_blocks)
-        self.refs = torch.zeros(self.num_blocks, dtype=torch.int32, device=device)
+        self._refs = torch.zeros(self.num_blocks, dtype=torch.int32, device=device)
         self._workspaces = []  # (earlier ones too: captured graphs may use them)
-        self._rows = -1
+        self._rows, self._pool_ref = -1, None
+
+    @property
+    def refs(self):
+        return self._refs
 
     def _pool(self, rows, stream):
-        torch = _torch()
+        """Reference to the tq_block_pool of `refs` and a workspace for calls of so many rows."""
         if rows > self._rows:
+            torch = _torch()
             size = lib().tq_blocks_workspace_bytes(self.num_blocks, rows)
             if size == 0:
                 raise TQError(TQ_ERR_INVALID_ARG, last_error() or "invalid sizes")
-            self._workspaces.append(_new(torch.zeros, (int(size),), torch.uint8, self.refs.device, stream))
-            self._rows = rows
-        ws = self._workspaces[-1]
-        refs = _index_ptr(self.refs, "refs", torch.int32, (self.num_blocks,))
-        return _byref(BlockPool(self.num_blocks, refs, ws.data_ptr(), ws.numel()))
+            refs = _index_ptr(self.refs, "refs", torch.int32, (self.num_blocks,))
+            ws = _new(torch.zeros, (int(size),), torch.uint8, self.refs.device, stream)
+            self._workspaces.append(ws)
+            self._rows, self._pool_ref = rows, _byref(BlockPool(self.num_blocks, refs, ws.data_ptr(), ws.numel()))
+        return self._pool_ref
 
     @staticmethod
     def _table(block_table, context_lens):
@@ -817,9 +822,10 @@ class Blocks:
             raise ValueError("parents must be one row, got %s" % (tuple(parents.shape),))
         n = int(parents.shape[0])
         index = _index_ptr(parents, "parents", torch.int32, (n,))
-        table = _new(torch.empty, (n, old.max_blocks), torch.int32, block_table.device, stream)
-        lens = _new(torch.empty, (n,), torch.int32, block_table.device, stream)
-        new = self._table(table, lens)
+        device, width = block_table.device, old.max_blocks
+        table = _new(torch.empty, (n, width), torch.int32, device, stream)
+        lens = _new(torch.empty, (n,), torch.int32, device, stream)
+        new = BlockRows(table.data_ptr(), lens.data_ptr(), n, width)
         _check(lib().tq_blocks_reorder(self._pool(max(old.rows, n), stream), _descs(layers), len(layers), _byref(old), index,
                                        _byref(new), _stream(stream)))
         return table, lens

@@ -295,7 +295,9 @@ __global__ void __launch_bounds__(kPlanThreads) k_extend(Rows r, const int32_t* 
     want += all;
   }
   __syncthreads();
-  auto put = [&](int k, int id) {
+  const int got = take_blocks<kPlanThreads>(refs, num_blocks, want, smem, [&](int at, int id) { w.list[at] = id; });
+  __syncthreads();
+  for (int k = threadIdx.x; k < want; k += kPlanThreads) {
     int lo = 0, hi = r.rows - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -304,10 +306,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_extend(Rows r, const int32_t* 
     }
     const bool near = lo < kPlanThreads;
     const int from = near ? spot[lo] : blocks_of(tokens_of(r, lo, status, false));
-    r.table[(int64_t)lo * r.max_blocks + from + k - (near ? rank[lo] : w.rank[lo])] = id;
-  };
-  const int got = take_blocks<kPlanThreads>(refs, num_blocks, want, smem, put);
-  for (int k = got + threadIdx.x; k < want; k += kPlanThreads) put(k, -1);
+    r.table[(int64_t)lo * r.max_blocks + from + k - (near ? rank[lo] : w.rank[lo])] = k < got ? w.list[k] : -1;
+  }
   if (threadIdx.x == 0 && got < want) flag_status(status, TQ_DEV_NO_BLOCK);
 }
 
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_lists(int32_t* refs, int64_t n
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
       if (i + k >= num_blocks) break;
-      w.map[i + k] = (int)(i + k);
+      if ((k & 3) == 0) *reinterpret_cast<int4*>(w.map + i + k) = make_int4((int)i + k, (int)i + k + 1, (int)i + k + 2, (int)i + k + 3);
       if (i + k < live) {
         if (c.v[k] <= 0) w.list[at_h++] = (int)(i + k);
       } else if (c.v[k] > 0) {
@@ -454,7 +454,7 @@ size_t layout(int64_t num_blocks, int rows, uint8_t* base, Work* w) {
   x.sums = take(2);
   x.list = take(num_blocks);
   x.movers = take(num_blocks);
-  x.map = take(num_blocks);
+  x.map = take(num_blocks + 3);  // (written four at a time)
   x.count = take(rows);
   x.first = take(rows);
   x.rank = take(rows);

@@ -7,8 +7,9 @@
 // coordinate that is not finite takes no part in the step and is marked in the tail.
 //
 // Both roundings are those of the exact quotient, whatever the order of operations: the fp32 product with
-// 1 / s is off by less than 2^-16 of a code, and where it lies that near to the middle between two codes
-// the quotient is formed in 64 bits, which holds what decides (two 24-bit numbers, 31 bits with the code).
+// 1 / s is off by less than 2^-16 of a code, and where it lies that near to the middle between two codes, the
+// sign of x - middle * s decides, which one fused product gives exactly.  (Among bf16 values a middle is not
+// rare: both x and s have few bits.)
 #include "tq_async.cuh"
 #include "tq_int8.cuh"
 
@@ -46,10 +47,27 @@ __device__ __forceinline__ uint32_t codes4(const float (&x)[4], float inv, float
   }
   return prmt(prmt(y[0], y[1], 0x0040u), prmt(y[2], y[3], 0x0040u), 0x5410u);
 }
-// The code of the exact quotient x / s.
-__device__ __noinline__ uint32_t exact_code(double x, float s) { return (uint32_t)((int)rint(x / (double)s) + 128); }
 // Products this near to the middle between two codes do not decide.
 constexpr float kMiddle = 0.5f - 3.0517578125e-5f;
+// The same four codes where some are near a middle h: the sign of a b - h s (b = 1 for values, the old step for
+// codes).  p + e is h s exactly, and so are the differences: a b and h s agree in their first 13 bits.  (`up`: a power
+// of two that keeps small products whole.)
+__device__ __forceinline__ uint32_t middles4(uint32_t codes, const float (&x)[4], float inv, float b, float s) {
+  const float up = s < 1.0f ? 4294967296.0f : 1.0f;
+  const float bu = b * up, su = s * up;
+  uint32_t o = codes;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float c = (float)((int)((codes >> (8 * k)) & 255u) - 128), t = fmaf(x[k], inv, -c);
+    if (fabsf(t) <= kMiddle) continue;
+    const float h = c + copysignf(0.5f, t), p = h * su, e = fmaf(h, su, -p);
+    const float d = fmaf(x[k], bu, -p) - e;
+    const int low = (int)floorf(h);
+    const int code = d < 0.0f ? low : (d > 0.0f ? low + 1 : low + (low & 1));
+    o = (o & ~(255u << (8 * k))) | ((uint32_t)(code + 128) << (8 * k));
+  }
+  return o;
+}
 
 // One page by one warp, a lane four coordinates of each record; token[r] (shared memory): what record r
 // takes, if bit r of rows is set.
@@ -125,7 +143,6 @@ __device__ __forceinline__ void append_page(const T* x, int64_t stride, uint8_t*
   if (!begins) s = fmaxf(s, s_old);
   const float inv = __fdiv_rn(1.0f, s), ratio = begins ? 0.0f : __fdiv_rn(s_old, s);
   const bool recode = !begins && s != s_old;
-  uint32_t again = 0u;  // records with a value near the middle between two codes
 #pragma unroll
   for (int r = 0; r < kBlock; ++r) {
     float far = 0.0f;
@@ -140,33 +157,18 @@ __device__ __forceinline__ void append_page(const T* x, int64_t stride, uint8_t*
 #pragma unroll
         for (int k = 0; k < 4; ++k) f[k] = __uint_as_float(v[r][k & (W - 1)]);
       }
-      at[32 * r] = codes4(f, inv, &far);
+      uint32_t o = codes4(f, inv, &far);
+      if (far > kMiddle) o = middles4(o, f, inv, 1.0f, s);
+      at[32 * r] = o;
     } else if (begins) {
       at[32 * r] = 0x80808080u;
     } else if (recode) {
       float f[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) f[k] = (float)((int)((v[r][0] >> (8 * k)) & 255u) - 128);
-      at[32 * r] = codes4(f, ratio, &far);
-    }
-    if (far > kMiddle) again |= 1u << r;
-  }
-  while (again) {  // (a lane at a time, a code in ten thousand)
-    const int r = __ffs(again) - 1;
-    again &= again - 1u;
-    const bool fresh = (rows >> r) & 1u;
-#pragma unroll 1
-    for (int k = 0; k < 4; ++k) {
-      double y;
-      if (fresh) {
-        y = (double)load_elem(x + (int64_t)token[r] * stride + 4 * lane + k);
-      } else {
-        uint32_t w = 0u;  // (the page has the new codes by now)
-#pragma unroll
-        for (int i = 0; i < kBlock; ++i) w = i == r ? v[i][0] : w;
-        y = (double)((int)((w >> (8 * k)) & 255u) - 128) * (double)s_old;
-      }
-      page[r * kD + 4 * lane + k] = (uint8_t)exact_code(y, s);
+      uint32_t o = codes4(f, ratio, &far);
+      if (far > kMiddle) o = middles4(o, f, ratio, s_old, s);
+      at[32 * r] = o;
     }
   }
   if (lane == 0) *reinterpret_cast<uint2*>(tail) = make_uint2(__float_as_uint(s), (begins ? 0u : t_old.y & ~rows) | bad);
