@@ -45,7 +45,7 @@ def test_calls_of_other_layers(tqlib, layer, rot):
     assert status(tqlib, "tq_prefix_decode", ref, p, 0, 4, 2, p, 16, None, 0, None, 1.0, p, 0, p, 1 << 20, None) == tqlib.TQ_ERR_UNSUPPORTED
     assert status(tqlib, "tq_decode_step", ref, p, p, 0, p, 0, 4, 2, p, 1, p, 1.0, p, 0, p, 1 << 20, 0, None) == tqlib.TQ_ERR_UNSUPPORTED
     assert status(tqlib, "tq_quantize_rotated", ref, 0, p, p, p, 4, None) == tqlib.TQ_ERR_INVALID_ARG
-    assert status(tqlib, "tq_quantize_append", ref, p, None, 0, p, (1 << 30) + 1, None) == tqlib.TQ_ERR_UNSUPPORTED
+    assert status(tqlib, "tq_quantize_append", ref, p, None, 0, p, 1 << 28, None) == tqlib.TQ_ERR_UNSUPPORTED
 
 
 def test_attend_refusals(tqlib, layer):

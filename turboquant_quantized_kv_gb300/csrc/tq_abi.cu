@@ -64,8 +64,8 @@ tq_status check_append(const tq_cache_desc* desc, const void* k, const void* v, 
   if (!k && !v) return fail(TQ_ERR_INVALID_ARG, "%s: both k and v are null", fn);
   if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15)
     return fail(TQ_ERR_INVALID_ARG, "%s: k/v must be 16-byte aligned", fn);
-  if (desc->fmt.kv_format == TQ_KV_INT8 && n_tokens > (1 << 30))
-    return fail(TQ_ERR_UNSUPPORTED, "%s: more than 2^30 tokens of an int8 layer", fn);
+  if (desc->fmt.kv_format == TQ_KV_INT8 && n_tokens >= (1 << 28))
+    return fail(TQ_ERR_UNSUPPORTED, "%s: 2^28 or more tokens of an int8 layer", fn);
   const tq_layer_format& f = desc->fmt;
   const bool packed_k = f.kv_format == TQ_KV_PACKED,
              packed_v = f.kv_format == TQ_KV_PACKED || f.kv_format == TQ_KV_K8V4;  // codebook quantizers

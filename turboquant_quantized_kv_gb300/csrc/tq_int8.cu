@@ -8,8 +8,7 @@
 //
 // Both roundings are those of the exact quotient, whatever the order of operations: the fp32 product with
 // 1 / s is off by less than 2^-16 of a code, and where it lies that near to the middle between two codes, the
-// sign of x - middle * s decides, which one fused product gives exactly.  (Among bf16 values a middle is not
-// rare: both x and s have few bits.)
+// sign of x - middle * s decides, which one fused product gives exactly.
 #include "tq_async.cuh"
 #include "tq_int8.cuh"
 
@@ -48,11 +47,12 @@ __device__ __forceinline__ uint32_t codes4(const float (&x)[4], float inv, float
   return prmt(prmt(y[0], y[1], 0x0040u), prmt(y[2], y[3], 0x0040u), 0x5410u);
 }
 // Products this near to the middle between two codes do not decide.
-constexpr float kMiddle = 0.5f - 3.0517578125e-5f;
+constexpr float kMiddle = 0.5f - 1.52587890625e-5f;
 // The same four codes where some are near a middle h: the sign of a b - h s (b = 1 for values, the old step for
 // codes).  p + e is h s exactly, and so are the differences: a b and h s agree in their first 13 bits.  (`up`: a power
 // of two that keeps small products whole.)
-__device__ __forceinline__ uint32_t middles4(uint32_t codes, const float (&x)[4], float inv, float b, float s) {
+__device__ __noinline__ uint32_t middles4(uint32_t codes, float4 y, float inv, float b, float s) {
+  const float x[4] = {y.x, y.y, y.z, y.w};
   const float up = s < 1.0f ? 4294967296.0f : 1.0f;
   const float bu = b * up, su = s * up;
   uint32_t o = codes;
@@ -158,7 +158,7 @@ __device__ __forceinline__ void append_page(const T* x, int64_t stride, uint8_t*
         for (int k = 0; k < 4; ++k) f[k] = __uint_as_float(v[r][k & (W - 1)]);
       }
       uint32_t o = codes4(f, inv, &far);
-      if (far > kMiddle) o = middles4(o, f, inv, 1.0f, s);
+      if (far > kMiddle) o = middles4(o, make_float4(f[0], f[1], f[2], f[3]), inv, 1.0f, s);
       at[32 * r] = o;
     } else if (begins) {
       at[32 * r] = 0x80808080u;
@@ -167,26 +167,34 @@ __device__ __forceinline__ void append_page(const T* x, int64_t stride, uint8_t*
 #pragma unroll
       for (int k = 0; k < 4; ++k) f[k] = (float)((int)((v[r][0] >> (8 * k)) & 255u) - 128);
       uint32_t o = codes4(f, ratio, &far);
-      if (far > kMiddle) o = middles4(o, f, ratio, s_old, s);
+      if (far > kMiddle) o = middles4(o, make_float4(f[0], f[1], f[2], f[3]), ratio, s_old, s);
       at[32 * r] = o;
     }
   }
   if (lane == 0) *reinterpret_cast<uint2*>(tail) = make_uint2(__float_as_uint(s), (begins ? 0u : t_old.y & ~rows) | bad);
 }
 
-// A CTA takes the blocks whose first token (of the call) is one of its `chunk` tokens.  With a slot given
-// twice the later token stays.
+// A block belongs to one of its tokens, that of the least key: a record that a hash of the block picks, if the
+// call writes it, or else the next one that it writes; of a slot given twice the later token.  A CTA takes
+// the blocks that belong to its `chunk` tokens: one a CTA on average, for prompts token by token as for
+// sequences in turn (16,384 tokens of 64 sequences in turn: 158 us with the first token for all, 42 so).
+__device__ __forceinline__ uint32_t key_of(int block, int record, int t) {
+  return (((uint32_t)record - ((uint32_t)block * 0x9E3779B1u >> 28)) & 15u) << 28 | (0x0FFFFFFEu - (uint32_t)t);
+}
+constexpr uint32_t kNoKey = 0xFFFFFFFFu;
+__device__ __forceinline__ int token_of(uint32_t key) { return (int)(0x0FFFFFFEu - (key & 0x0FFFFFFFu)); }  // (of none: -1)
+
 template <typename T>
-__global__ void __launch_bounds__(kAppWarps * 32) k_int8_append(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kAppWarps * 32, sizeof(T) == 2 ? 2 : 1) k_int8_append(const __grid_constant__ AppendArgs a) {
   __shared__ int block_of[kAppChunk];       // distinct blocks of the chunk's tokens; their number in `blocks`
-  __shared__ int first[kAppChunk];
+  __shared__ uint32_t first[kAppChunk];     // the least key of each
   __shared__ int token[kAppChunk][kBlock];  // 1 + the token of each record, 0 for none
   __shared__ int own[kAppChunk];            // which of the blocks are the CTA's
   __shared__ int blocks, owned;
   const int t0 = blockIdx.x * a.chunk, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   if (a.marked) grid_dep_wait();
   for (int i = threadIdx.x; i < kAppChunk * kBlock; i += blockDim.x) (&token[0][0])[i] = 0;
-  if (threadIdx.x < kAppChunk) first[threadIdx.x] = 0x7FFFFFFF;
+  if (threadIdx.x < kAppChunk) first[threadIdx.x] = kNoKey;
   if (threadIdx.x == 0) owned = 0;
   if (warp == 0) {
     int n = 0;
@@ -221,11 +229,11 @@ __global__ void __launch_bounds__(kAppWarps * 32) k_int8_append(const __grid_con
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         if (s[k] < 0 || s[k] >= a.max_slot) continue;
-        const int b = (int)(s[k] / kBlock), t = tb + k * (int)blockDim.x;
+        const int b = (int)(s[k] / kBlock), r = (int)(s[k] % kBlock), t = tb + k * (int)blockDim.x;
         for (int i = 0; i < nb; ++i) {
           if (block_of[i] != b) continue;
-          atomicMax(&token[i][s[k] % kBlock], t + 1);
-          atomicMin(&first[i], t);
+          atomicMax(&token[i][r], t + 1);
+          atomicMin(&first[i], key_of(b, r, t));
         }
       }
     }
@@ -233,14 +241,16 @@ __global__ void __launch_bounds__(kAppWarps * 32) k_int8_append(const __grid_con
     for (int i = warp; i < nb; i += warps) {
       const uint8_t* page = a.pool[a.x[0] ? 0 : 1] + (int64_t)block_of[i] * a.Hkv * kI8Page;
       const I8Tail* tail = reinterpret_cast<const I8Tail*>(page + kI8Codes);
-      const int f = (int)tail->first;
+      const uint2 t = *reinterpret_cast<const uint2*>(&tail->marks);
+      const int taken = lane < kBlock ? *reinterpret_cast<const int*>(page + lane * kD) : 0;
+      const int f = token_of(t.y);
       if (f < t0 || f >= t0 + a.chunk) continue;  // (another CTA's, which may be writing it)
-      if (lane < kBlock && (tail->marks >> lane) & 1u) token[i][lane] = *reinterpret_cast<const int*>(page + lane * kD);
-      if (lane == 0) first[i] = f;
+      if (lane < kBlock && (t.x >> lane) & 1u) token[i][lane] = taken;
+      if (lane == 0) first[i] = t.y;
     }
   }
   __syncthreads();
-  if (threadIdx.x < nb && first[threadIdx.x] >= t0 && first[threadIdx.x] < t0 + a.chunk) own[atomicAdd(&owned, 1)] = threadIdx.x;
+  if (threadIdx.x < nb && token_of(first[threadIdx.x]) >= t0 && token_of(first[threadIdx.x]) < t0 + a.chunk) own[atomicAdd(&owned, 1)] = threadIdx.x;
   for (int i = threadIdx.x; i < kAppChunk * kBlock; i += blockDim.x) (&token[0][0])[i] -= 1;
   __syncthreads();
   for (int p = warp; p < owned * 2 * a.Hkv; p += warps) {
@@ -261,7 +271,7 @@ __global__ void k_int8_clear(uint8_t* pool, int Hkv, const int64_t* slots, int n
     if (s < 0 || s >= max_slot) continue;
     uint8_t* page = pool + s / kBlock * Hkv * kI8Page;
     I8Tail* tail = reinterpret_cast<I8Tail*>(page + kI8Codes);
-    *reinterpret_cast<uint2*>(&tail->marks) = make_uint2(0u, 0xFFFFFFFFu);
+    *reinterpret_cast<uint2*>(&tail->marks) = make_uint2(0u, kNoKey);
     *reinterpret_cast<int*>(page + s % kBlock * kD) = 0;
   }
 }
@@ -274,7 +284,7 @@ __global__ void k_int8_mark(uint8_t* pool, int Hkv, const int64_t* slots, int n,
     uint8_t* page = pool + s / kBlock * Hkv * kI8Page;
     I8Tail* tail = reinterpret_cast<I8Tail*>(page + kI8Codes);
     atomicOr(&tail->marks, 1u << (s % kBlock));
-    atomicMin(&tail->first, (uint32_t)t);
+    atomicMin(&tail->first, key_of((int)(s / kBlock), (int)(s % kBlock), t));
     atomicMax(reinterpret_cast<int*>(page + s % kBlock * kD), t + 1);
   }
 }

@@ -23,7 +23,7 @@ struct I8Tail {
   float step;
   uint32_t bad;       // bit r: record r is not a number
   uint32_t marks;     // (append) bit r: record r is written by this call
-  uint32_t first;     // (append) the first token of this call in the block
+  uint32_t first;     // (append) the least key of this call's tokens in the block
 };
 
 // Bytes lo and hi of w as two fp16 codes: the byte under the exponent of 1024 is 1024 + byte, exactly, and
