@@ -7,14 +7,18 @@
 // kernel (tq_int8_decode.cu).
 //
 // Work.  A unit is (sequence, KV head, tile of up to 256 rows), a step is 128 tokens of its context.  All
-// steps of all units stand in one line, cut into equal parts, one a CTA (an SM): causal tiles of any length
-// balance.  A unit that is cut leaves partials (normalised values, reference, denominator) in the
-// workspace, which the CTA that arrives last joins in the order of the line.
+// steps of all units stand in one line, kUnitCost more places for each unit, cut into equal parts, one a CTA
+// (an SM): causal tiles of any length balance.  A unit that is cut leaves partials (normalised values,
+// reference, denominator) in the workspace, which the CTA that arrives last joins in the order of the line.
 //
 // A CTA: two streams of 128 rows over the same tokens.
-//   8 producer warps  turn 8 blocks of codes into fp16 (exact, i8_pair) in shared memory, K ahead of V;
-//   1 MMA warp        S = Q K^T (shared memory), O += P V (P in tensor memory), one elected thread;
-//   8 softmax warps   a thread a row: maxima, base-2 weights, P over the logits in tensor memory.
+//   8 softmax warps   a thread a row: maxima, base-2 weights, P over the logits in tensor memory; then
+//                     the rows' values out;
+//   4 producer warps  turn 8 blocks of codes into fp16 (exact, i8_pair) in shared memory, K ahead of V, a
+//                     step of pages in registers; before a unit its queries;
+//   1 MMA warp        S = Q K^T (shared memory), O += P V (P in tensor memory), one elected thread.
+// Nothing waits for the CTA as a whole between units: the next unit's queries, pages and first logits come
+// while the softmax warps finish the last one.
 // Scales.  Queries go in as fp16 after a power of two for each row (bf16 queries lose nothing but what
 // lies 2^-24 below the row's largest; fp32 ones go in as two parts).  A block's step of K is one factor for
 // 16 logits, its step of V one for 16 weights, so that both operands hold plain codes: with m a running
@@ -36,8 +40,11 @@ namespace {
 constexpr int kTile = 128;          // tokens a step, rows a stream
 constexpr int kTileBlocks = kTile / kBlock;
 constexpr int kUnitRows = 2 * kTile;
-constexpr int kSoftWarps = 8, kProdWarps = 8, kMmaWarp = kSoftWarps + kProdWarps;
-constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kSoftWarps = 8, kProdWarps = 4;
+constexpr int kMmaWarp = kSoftWarps + kProdWarps;
+constexpr int kThreads = 512;  // (16 warps of 128 registers, dealt out again below)
+constexpr int kWarps = kThreads / 32;
+constexpr int kUnitCost = 2;   // steps that the beginning and end of a unit are worth
 constexpr uint32_t kPanel = kTile * 128;    // 128 rows of 64 16-bit elements, swizzled
 constexpr uint32_t kOperand = 2 * kPanel;
 constexpr int kSlots = 4;                   // tiles whose steps are kept
@@ -48,20 +55,17 @@ constexpr float kMoveM = 16.0f;
 // V in two (with low parts in one) -- then the rest.
 constexpr uint32_t kOffStep = 7 * kOperand;                    // float [slots][3][8]: steps of K and V, exponents above V's
 constexpr uint32_t kOffBits = kOffStep + kSlots * 96;          // u32 [slots][8]: valid tokens << 16 | bad ones
-constexpr uint32_t kOffRow = kOffBits + kSlots * 32;           // float [256]: a row's power of two
-constexpr uint32_t kOffBar = kOffRow + kUnitRows * 4;
-constexpr int kBars = 2 + 2 + 2 + 2 + kSlots + 2 + 2 + 2;
+constexpr uint32_t kOffRow = kOffBits + kSlots * 32;           // float [2][256]: a row's power of two, of units in turn
+constexpr uint32_t kOffBar = kOffRow + 2 * kUnitRows * 4;
+constexpr int kBars = 2 + 2 + 2 + 2 + kSlots + 2 + 2 + 2 + 2;
 constexpr uint32_t kOffMisc = kOffBar + kBars * 8;
 constexpr uint32_t kSmem = kOffMisc + 128;
 static_assert(kSmem <= 232448, "the shared memory of one CTA an SM");
 
 struct Misc {
   uint32_t tmem;
-  int dead;     // a wait gave up
   int arrived;
-  int seq, kvh, tile, step;  // where the CTA's part begins
-  int pad;
-  int64_t sums[2];
+  int seq, kvh, tile, place;  // where the CTA's part begins
 };
 
 struct AttArgs {
@@ -83,7 +87,7 @@ struct AttArgs {
   int per;      // tokens a unit
   float scale;  // sm_scale * log2 e
   int* counters;
-  float4* part; // [2 grid][8][32][32]: (32 rows, 4 coordinates) of a partial
+  float* part;  // [2 grid][256][d]
   float2* ml;   // [2 grid][256]
   unsigned* status;
 };
@@ -138,9 +142,8 @@ __device__ __forceinline__ void stage_q(const AttArgs& a, const Seq& s, int kvh,
                                         int warp, int lane) {
   const int quad = lane & 3;
 #pragma unroll 1
-  for (int h = 0; h < 2; ++h) {
-    const int r = h * kTile + 8 * warp + (lane >> 2);
-    if (h * kTile + 8 * (warp & ~3) >= rows) break;  // (32 rows past the end: nobody looks at their products)
+  for (int r0 = 0; r0 < rows; r0 += 8 * kProdWarps) {  // (32 rows past the end: nobody looks at their products)
+    const int r = r0 + 8 * warp + (lane >> 2), h = r0 >> 7;
     float x[32];
     if (r < rows) {
       const int t = r / a.g;
@@ -224,6 +227,51 @@ __device__ __forceinline__ void store_page(const Page& p, uint32_t dst, int bloc
   }
 }
 
+// Registers a thread from here on (four warps together).
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+constexpr int kSoftRegs = 176, kProdRegs = 104, kMmaRegs = 56;
+static_assert(2 * kSoftRegs + kProdRegs + kMmaRegs <= 4 * 128, "what the launch has");
+
+// The unit that holds a place of the line, and the steps of a CTA's part in it.
+struct Unit {
+  int seq, kvh, tile;
+  Seq s;
+  int place;        // of the part's beginning in the unit
+  int all;          // steps of the unit
+  int tok0, rows;
+  __device__ __forceinline__ void look(const AttArgs& a) {
+    all = steps_of(a, s, tile);
+    tok0 = tile * a.per;
+    rows = min(a.per, s.n - tok0) * a.g;
+  }
+  // Places up to `left` of the unit: steps [step, step + n).
+  __device__ __forceinline__ int part(int64_t left, int* step, int* n) const {
+    const int places = (int)min((int64_t)(all + kUnitCost - place), left);
+    *step = max(0, place - kUnitCost);
+    *n = max(0, place + places - kUnitCost) - *step;
+    return places;
+  }
+  __device__ __forceinline__ void next(const AttArgs& a) {
+    place = 0;
+    if (++tile == tiles_of(a, s)) {
+      tile = 0;
+      if (++kvh == a.Hkv) {
+        kvh = 0;
+        do s = seq_of(a, ++seq, false);
+        while (!s.large);
+      }
+    }
+    look(a);
+  }
+};
+
 template <bool EXACT>  // queries and weights in two parts
 __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_constant__ AttArgs a) {
   extern __shared__ __align__(128) unsigned char gen[];
@@ -240,15 +288,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
   uint64_t* const sfull = gfull + kSlots;   // [2] logits of a stream are in tensor memory
   uint64_t* const pfull = sfull + 2;        // [2] weights
   uint64_t* const odone = pfull + 2;        // [2] accumulator complete
+  uint64_t* const qfull = odone + 2;        // queries of a unit are there
+  uint64_t* const qempty = qfull + 1;       // and read
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // ---- the line: its length, and where the CTA's part begins
   const int per = (a.seqs + kThreads - 1) / kThreads;
   const int b0 = min(a.seqs, (int)threadIdx.x * per), b1 = min(a.seqs, b0 + per);
-  auto length = [&](const Seq& s) {
+  auto length = [&](const Seq& s) {  // places of a KV head
     int64_t n = 0;
     const int tiles = tiles_of(a, s);
-    for (int k = 0; k < tiles; ++k) n += steps_of(a, s, k);
+    for (int k = 0; k < tiles; ++k) n += steps_of(a, s, k) + kUnitCost;
     return n;
   };
   int64_t mine = 0;
@@ -264,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
   __syncthreads();
   int64_t total = 0;
   before -= mine;
-  for (int w = 0; w <= kMmaWarp; ++w) {
+  for (int w = 0; w < kWarps; ++w) {
     if (w < warp) before += sums[w];
     total += sums[w];
   }
@@ -282,12 +332,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
         misc.kvh = (int)(left / n);
         left %= n;
         int k = 0;
-        for (int st = steps_of(a, s, 0); left >= st; st = steps_of(a, s, k)) {
+        for (int st = steps_of(a, s, 0) + kUnitCost; left >= st; st = steps_of(a, s, k) + kUnitCost) {
           left -= st;
           ++k;
         }
         misc.tile = k;
-        misc.step = (int)left;
+        misc.place = (int)left;
         break;
       }
       left -= n * a.Hkv;
@@ -304,8 +354,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
       mbar_init(odone + i, 1);
     }
     for (int i = 0; i < kSlots; ++i) mbar_init(gfull + i, kProdWarps);
+    mbar_init(qfull, kProdWarps);
+    mbar_init(qempty, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    misc.dead = 0;
   }
   if (warp == kMmaWarp) tmem_alloc(base + kOffMisc, 512);
   tc_fence_before();
@@ -315,471 +366,533 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
   const uint32_t k_op = base + (EXACT ? 4u : 2u) * kOperand, v_op = k_op + 2 * kOperand;
   constexpr int vbit = EXACT ? 0 : 1;  // stages of V less one
 
-  int seq = misc.seq, kvh = misc.kvh, tile = misc.tile, step = misc.step;
-  Seq s = seq_of(a, seq, false);
-  int done0 = 0, done1 = 0;  // steps of the streams so far
-  int turns0 = 0, turns1 = 0;  // segments of the streams so far
-  for (int64_t at = begin; at < end;) {
-    // ---- a segment: steps [step, step + n) of one unit
-    const int all = steps_of(a, s, tile), n = (int)min((int64_t)(all - step), end - at);
-    const int tok0 = tile * a.per, rows = min(a.per, s.n - tok0) * a.g;
-    const bool two = rows > kTile;
-    if (warp < kMmaWarp) {
-      if (a.q_bf16) stage_q<true, EXACT>(a, s, kvh, tok0, rows, base, scales, warp, lane);
-      else stage_q<false, EXACT>(a, s, kvh, tok0, rows, base, scales, warp, lane);
-    }
-    fence_proxy_async();
-    __syncthreads();
-    bool ok = true;
-    if (warp < kSoftWarps) {
-      // ----------------------------------------------------------- softmax
-      const int st = warp >> 2, w = warp & 3, r = st * kTile + 32 * w + lane;
-      const uint32_t ts = tmem + (uint32_t)(st * kTile) + ((uint32_t)(32 * w) << 16);
-      const uint32_t to = tmem + (uint32_t)((2 + st) * kTile) + ((uint32_t)(32 * w) << 16);
-      const bool live = st * kTile + 32 * w < rows;
-      const int done = st ? done1 : done0;
-      const float cq = live ? scales[r] : 0.0f;
-      // tokens the row attends to (a row past the end, whose queries are zeros: all, so that it holds nobody up)
-      const int lim = r < rows ? s.ctx - s.n + tok0 + r / a.g + 1 : 1 << 30;
-      const int least = __reduce_min_sync(0xffffffffu, lim);
+  Unit u;
+  u.seq = misc.seq;
+  u.kvh = misc.kvh;
+  u.tile = misc.tile;
+  u.place = misc.place;
+  u.s = seq_of(a, u.seq, false);
+  u.look(a);
+  int64_t at = begin;
+  bool ok = true;  // no wait gave up
+  int done0 = 0, units = 0;  // steps and units so far
+
+  if (warp < kSoftWarps) {
+    // ------------------------------------------------------------- softmax
+    more_registers<kSoftRegs>();
+    const int st = warp >> 2, w = warp & 3, r = st * kTile + 32 * w + lane;
+    const uint32_t ts = tmem + (uint32_t)(st * kTile) + ((uint32_t)(32 * w) << 16);
+    const uint32_t to = tmem + (uint32_t)((2 + st) * kTile) + ((uint32_t)(32 * w) << 16);
+    int done = 0, turns = 0;  // steps and units of the stream so far
+    while (true) {
+      int step, n;
+      const int places = u.part(end - at, &step, &n);
+      const bool part_of_it = n > 0 && (st == 0 || u.rows > kTile);
       float C = -INFINITY, m = -INFINITY, l = 0.0f;
-      int i = 0;
-      auto one = [&](auto careful) {  // one step; whether it is done
-        constexpr bool kCareful = decltype(careful)::value;
-        const int turn = done0 + i, slot = turn & (kSlots - 1);
-        ok = mbar_wait(gfull + slot, (turn / kSlots) & 1) && mbar_wait(sfull + st, (done + i) & 1);
+      const bool live = st * kTile + 32 * w < u.rows;
+      const int first = u.s.ctx - u.s.n + u.tok0;  // the unit's first token attends to this many and itself
+      if (part_of_it) {
+        ok = ok && mbar_wait(qfull, units & 1);
         ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return false;
-        tc_fence_after();
-        if (live) {
-          const float4* sp = reinterpret_cast<const float4*>(gen + kOffStep + slot * 96);
-          const uint4* bp = reinterpret_cast<const uint4*>(gen + kOffBits + slot * 32);
-          const uint4 q0 = bp[0], q1 = bp[1];
-          const int t0 = (step + i) * kTile;
-          const bool plain = (q0.x & q0.y & q0.z & q0.w & q1.x & q1.y & q1.z & q1.w) == 0xFFFF0000u &&
-                             ((q0.x | q0.y | q0.z | q0.w | q1.x | q1.y | q1.z | q1.w) & 0xFFFFu) == 0u && t0 + kTile <= least;
-          if (!kCareful && !plain) return false;
-          uint32_t mask[4] = {~0u, ~0u, ~0u, ~0u};
-          if (kCareful && !plain) {
-            const uint32_t bits[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-            uint32_t bad = 0u;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int k = min(max(lim - t0 - 32 * c, 0), 32);  // tokens of the chunk before the limit
-              mask[c] = ((bits[2 * c] >> 16) | (bits[2 * c + 1] & 0xFFFF0000u)) & (k == 32 ? ~0u : (1u << k) - 1u);
-              bad |= mask[c] & ((bits[2 * c] & 0xFFFFu) | (bits[2 * c + 1] << 16));
-            }
-            if (bad) l = CUDART_NAN_F;  // the row attends to what is not a number
-          }
-          float ks[8], vs[8], ev[8];
-          auto eight = [&](float(&x)[8], int i) {
-            const float4 y = sp[2 * i], z = sp[2 * i + 1];
-            x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
-            x[4] = z.x; x[5] = z.y; x[6] = z.z; x[7] = z.w;
-          };
-          eight(ks, 0);
-          eight(ev, 2);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) ks[k] *= cq;
-          uint32_t ra[32], rb[32];
-          // the largest u of the row, and the largest with the exponent of its block's values
-          float top = -INFINITY, topv = -INFINITY;
-          auto tops = [&](const uint32_t(&x)[32], int c) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float hi = -INFINITY;  // (of raw logits; no factor is negative)
-#pragma unroll
-              for (int k = 0; k < 16; k += 2) {
-                float y0 = __uint_as_float(x[16 * h + k]), y1 = __uint_as_float(x[16 * h + k + 1]);
-                if (kCareful) {
-                  y0 = (mask[c] >> (16 * h + k)) & 1u ? y0 : -INFINITY;
-                  y1 = (mask[c] >> (16 * h + k + 1)) & 1u ? y1 : -INFINITY;
-                }
-                hi = max3(hi, y0, y1);
-              }
-              float u = hi * ks[2 * c + h];
-              if (kCareful && hi == -INFINITY) u = hi;
-              top = fmaxf(top, u);
-              topv = fmaxf(topv, u + ev[2 * c + h]);
-            }
-          };
-          tmem_ld32_async(ts, ra);
-          tmem_wait_ld32(ra);
-          tmem_ld32_async(ts + 32, rb);
-          tops(ra, 0);
-          tmem_wait_ld32(rb);
-          tmem_ld32_async(ts + 64, ra);
-          tops(rb, 1);
-          tmem_wait_ld32(ra);
-          tmem_ld32_async(ts + 96, rb);
-          tops(ra, 2);
-          tmem_wait_ld32(rb);
-          tops(rb, 3);
-          if (__any_sync(0xffffffffu, top > m + kMoveM || topv > C + kRoom)) {
-            const float nm = fmaxf(m, ceilf(top)), nC = fmaxf(C, ceilf(topv) - kTop);
-            if (nm != m) l *= exp2f(m - nm);
-            m = nm;
-            const float f = nC != C ? exp2f(C - nC) : 1.0f;
-            C = nC;
-            if (i > 0 && __any_sync(0xffffffffu, f != 1.0f)) {  // (the last product into it precedes S)
-#pragma unroll 1
-              for (int c = 0; c < 4; ++c) {
-                tmem_ld32_async(to + 32 * c, ra);
-                tmem_wait_ld32(ra);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) ra[k] = __float_as_uint(__uint_as_float(ra[k]) * f);
-                tmem_st32(to + 32 * c, ra);
-              }
-            }
-          }
-          const float off = m == -INFINITY ? 0.0f : m, rho = C == -INFINITY ? 0.0f : exp2f(fminf(m - C, 120.0f));
-          eight(vs, 1);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) vs[k] = fminf(vs[k] * rho, 1.329227995784916e36f);  // (2^120; times a weight of zero)
-          float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
-          auto weights = [&](const uint32_t(&x)[32], int c) {
-            uint32_t p[16];
-            [[maybe_unused]] uint32_t p2[16];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int b = 2 * c + (k >> 2);
-              float2 u0 = make_float2(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1]));
-              float2 u1 = make_float2(__uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3]));
-              u0 = __ffma2_rn(u0, make_float2(ks[b], ks[b]), make_float2(-off, -off));
-              u1 = __ffma2_rn(u1, make_float2(ks[b], ks[b]), make_float2(-off, -off));
-              u0 = make_float2(ex2(u0.x), ex2(u0.y));
-              u1 = make_float2(ex2(u1.x), ex2(u1.y));
+        const float cq = live ? scales[(units & 1) * kUnitRows + r] : 0.0f;
+        // tokens the row attends to (a row past the end, whose queries are zeros: all, so that it holds nobody up)
+        const int lim = r < u.rows ? first + r / a.g + 1 : 1 << 30;
+        const int least = __reduce_min_sync(0xffffffffu, lim);
+        int i = 0;
+        auto one = [&](auto careful) {  // one step; whether it is done
+          constexpr bool kCareful = decltype(careful)::value;
+          const int turn = done0 + i, slot = turn & (kSlots - 1);
+          ok = mbar_wait(gfull + slot, (turn / kSlots) & 1) && mbar_wait(sfull + st, (done + i) & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) return false;
+          tc_fence_after();
+          if (live) {
+            const float4* sp = reinterpret_cast<const float4*>(gen + kOffStep + slot * 96);
+            const uint4* bp = reinterpret_cast<const uint4*>(gen + kOffBits + slot * 32);
+            const int t0 = (step + i) * kTile;
+            uint32_t mask[4];
+            {
+              const uint4 q0 = bp[0], q1 = bp[1];
+              const bool plain = (q0.x & q0.y & q0.z & q0.w & q1.x & q1.y & q1.z & q1.w) == 0xFFFF0000u &&
+                                 ((q0.x | q0.y | q0.z | q0.w | q1.x | q1.y | q1.z | q1.w) & 0xFFFFu) == 0u && t0 + kTile <= least;
+              if (!kCareful && !plain) return false;
               if (kCareful) {
-                const uint32_t bit = mask[c] >> (4 * k);
-                u0.x = bit & 1u ? u0.x : 0.0f;
-                u0.y = bit & 2u ? u0.y : 0.0f;
-                u1.x = bit & 4u ? u1.x : 0.0f;
-                u1.y = bit & 8u ? u1.y : 0.0f;
-              }
-              sum0 = __fadd2_rn(sum0, u0);
-              sum1 = __fadd2_rn(sum1, u1);
-              u0 = __fmul2_rn(u0, make_float2(vs[b], vs[b]));
-              u1 = __fmul2_rn(u1, make_float2(vs[b], vs[b]));
-              p[2 * k] = half2_bits(u0.x, u0.y);
-              p[2 * k + 1] = half2_bits(u1.x, u1.y);
-              if constexpr (EXACT) {
-                const float2 h0 = __half22float2(*reinterpret_cast<const __half2*>(&p[2 * k]));
-                const float2 h1 = __half22float2(*reinterpret_cast<const __half2*>(&p[2 * k + 1]));
-                p2[2 * k] = half2_bits(u0.x - h0.x, u0.y - h0.y);
-                p2[2 * k + 1] = half2_bits(u1.x - h1.x, u1.y - h1.y);
+                const uint32_t bits[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+                uint32_t bad = 0u;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  const int k = min(max(lim - t0 - 32 * c, 0), 32);  // tokens of the chunk before the limit
+                  mask[c] = ((bits[2 * c] >> 16) | (bits[2 * c + 1] & 0xFFFF0000u)) & (k == 32 ? ~0u : (1u << k) - 1u);
+                  bad |= mask[c] & ((bits[2 * c] & 0xFFFFu) | (bits[2 * c + 1] << 16));
+                }
+                if (bad) l = CUDART_NAN_F;  // the row attends to what is not a number
               }
             }
-            // over logits that have been read: high parts, low parts behind them
-            tmem_st16(ts + 32 * c, p);
-            if constexpr (EXACT) tmem_st16(ts + 32 * c + 16, p2);
-          };
-          tmem_ld32_async(ts, ra);
-          tmem_wait_ld32(ra);
-          tmem_ld32_async(ts + 32, rb);
-          weights(ra, 0);
-          tmem_wait_ld32(rb);
-          tmem_ld32_async(ts + 64, ra);
-          weights(rb, 1);
-          tmem_wait_ld32(ra);
-          tmem_ld32_async(ts + 96, rb);
-          weights(ra, 2);
-          tmem_wait_ld32(rb);
-          weights(rb, 3);
-          l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
-          tmem_wait_st();
-          tc_fence_before();
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(pfull + st);
-        return true;
-      };
-      if (st == 0 || two) {
-        while (i < n && one(std::false_type())) ++i;
-        while (i < n && ok && one(std::true_type())) ++i;
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(odone + st, (st ? turns1 : turns0) & 1));
-        tc_fence_after();
-        if (live && ok) {
-          // ---- the rows' values: out, or a partial
-          const bool whole = step == 0 && n == all;
-          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-          const float shift = C == -INFINITY ? 0.0f : C - m, half = truncf(0.5f * shift);
-          const float f0 = exp2f(half) * inv, f1 = exp2f(shift - half);
-          const int64_t place = 2 * (int64_t)blockIdx.x + (step == 0 ? 1 : 0);
-          float4* const part = a.part + (place * 8 + st * 4 + w) * (32 * 32) + lane;
-          if (!whole) a.ml[place * kUnitRows + r] = make_float2(m, l);
-          const int t = r / a.g;
-          const int64_t o = (int64_t)(s.first + tok0 + t) * a.o_row + (int64_t)(kvh * a.g + r - t * a.g) * a.o_head;
-          uint32_t ra[32];
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            tmem_ld32_async(to + 32 * c, ra);
-            tmem_wait_ld32(ra);
-            float x[32];
+            auto eight = [&](float(&x)[8], int k) {
+              const float4 y = sp[2 * k], z = sp[2 * k + 1];
+              x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
+              x[4] = z.x; x[5] = z.y; x[6] = z.z; x[7] = z.w;
+            };
+            uint32_t S[4][32];
+            float top = -INFINITY, topv = -INFINITY;  // the largest u of the row, and with the exponent of its block's values
+            {
+              float ks[8], ev[8];
+              tmem_ld32_async(ts, S[0]);
+              tmem_ld32_async(ts + 32, S[1]);
+              eight(ks, 0);
+              eight(ev, 2);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(ra[k]) * f0 * f1;
-            if (!whole) {
+              for (int k = 0; k < 8; ++k) ks[k] *= cq;
+              auto tops = [&](const uint32_t(&x)[32], int c) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k) part[(8 * c + k) * 32] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
-            } else if (r < rows) {
-              if (a.out_bf16) {
-                __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(a.out) + o + 32 * c;
-                if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0u) {
+                for (int h = 0; h < 2; ++h) {
+                  float hi[2] = {-INFINITY, -INFINITY};  // (of raw logits; no factor is negative)
 #pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    uint32_t y[4];
+                  for (int k = 0; k < 16; k += 4) {
+                    float y[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                      const __nv_bfloat162 z = __floats2bfloat162_rn(x[8 * k + 2 * j], x[8 * k + 2 * j + 1]);
-                      y[j] = *reinterpret_cast<const uint32_t*>(&z);
+                      y[j] = __uint_as_float(x[16 * h + k + j]);
+                      if (kCareful) y[j] = (mask[c] >> (16 * h + k + j)) & 1u ? y[j] : -INFINITY;
                     }
-                    reinterpret_cast<uint4*>(p)[k] = make_uint4(y[0], y[1], y[2], y[3]);
+                    hi[0] = max3(hi[0], y[0], y[1]);
+                    hi[1] = max3(hi[1], y[2], y[3]);
                   }
-                } else {
-#pragma unroll
-                  for (int k = 0; k < 32; ++k) p[k] = __float2bfloat16_rn(x[k]);
+                  hi[0] = fmaxf(hi[0], hi[1]);
+                  float v = hi[0] * ks[2 * c + h];
+                  if (kCareful && hi[0] == -INFINITY) v = hi[0];
+                  top = fmaxf(top, v);
+                  topv = fmaxf(topv, v + ev[2 * c + h]);
                 }
-              } else {
-                float* p = reinterpret_cast<float*>(a.out) + o + 32 * c;
-                if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0u) {
+              };
+              tmem_wait_ld32(S[0]);
+              tmem_wait_ld32(S[1]);
+              tmem_ld32_async(ts + 64, S[2]);
+              tmem_ld32_async(ts + 96, S[3]);
+              tops(S[0], 0);
+              tops(S[1], 1);
+              tmem_wait_ld32(S[2]);
+              tmem_wait_ld32(S[3]);
+              tops(S[2], 2);
+              tops(S[3], 3);
+            }
+            if (__any_sync(0xffffffffu, top > m + kMoveM || topv > C + kRoom)) {
+              const float nm = fmaxf(m, ceilf(top)), nC = fmaxf(C, ceilf(topv) - kTop);
+              if (nm != m) l *= exp2f(m - nm);
+              m = nm;
+              const float f = nC != C ? exp2f(C - nC) : 1.0f;
+              C = nC;
+              if (i > 0 && __any_sync(0xffffffffu, f != 1.0f)) {  // (the last product into it precedes S)
+#pragma unroll 1
+                for (int c = 0; c < 8; ++c) {
+                  uint32_t x[16];
+                  tmem_ld16(to + 16 * c, x);
 #pragma unroll
-                  for (int k = 0; k < 8; ++k)
-                    reinterpret_cast<float4*>(p)[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+                  for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
+                  tmem_st16(to + 16 * c, x);
+                }
+              }
+            }
+            const float off = m == -INFINITY ? 0.0f : m, rho = C == -INFINITY ? 0.0f : exp2f(fminf(m - C, 120.0f));
+            float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const float2 k2 = reinterpret_cast<const float2*>(sp)[c], v2 = reinterpret_cast<const float2*>(sp)[4 + c];
+              // (2^120 at most; times a weight of zero)
+              const float ks[2] = {k2.x * cq, k2.y * cq}, vs[2] = {fminf(v2.x * rho, 1.329227995784916e36f), fminf(v2.y * rho, 1.329227995784916e36f)};
+              uint32_t p[16];
+              [[maybe_unused]] uint32_t p2[16];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const int b = k >> 2;
+                float2 u0 = make_float2(__uint_as_float(S[c][4 * k]), __uint_as_float(S[c][4 * k + 1]));
+                float2 u1 = make_float2(__uint_as_float(S[c][4 * k + 2]), __uint_as_float(S[c][4 * k + 3]));
+                u0 = __ffma2_rn(u0, make_float2(ks[b], ks[b]), make_float2(-off, -off));
+                u1 = __ffma2_rn(u1, make_float2(ks[b], ks[b]), make_float2(-off, -off));
+                u0 = make_float2(ex2(u0.x), ex2(u0.y));
+                u1 = make_float2(ex2(u1.x), ex2(u1.y));
+                if (kCareful) {
+                  const uint32_t bit = mask[c] >> (4 * k);
+                  u0.x = bit & 1u ? u0.x : 0.0f;
+                  u0.y = bit & 2u ? u0.y : 0.0f;
+                  u1.x = bit & 4u ? u1.x : 0.0f;
+                  u1.y = bit & 8u ? u1.y : 0.0f;
+                }
+                sum0 = __fadd2_rn(sum0, u0);
+                sum1 = __fadd2_rn(sum1, u1);
+                u0 = __fmul2_rn(u0, make_float2(vs[b], vs[b]));
+                u1 = __fmul2_rn(u1, make_float2(vs[b], vs[b]));
+                p[2 * k] = half2_bits(u0.x, u0.y);
+                p[2 * k + 1] = half2_bits(u1.x, u1.y);
+                if constexpr (EXACT) {
+                  const float2 h0 = __half22float2(*reinterpret_cast<const __half2*>(&p[2 * k]));
+                  const float2 h1 = __half22float2(*reinterpret_cast<const __half2*>(&p[2 * k + 1]));
+                  p2[2 * k] = half2_bits(u0.x - h0.x, u0.y - h0.y);
+                  p2[2 * k + 1] = half2_bits(u1.x - h1.x, u1.y - h1.y);
+                }
+              }
+              // over logits that have been read: high parts, low parts behind them
+              tmem_st16(ts + 32 * c, p);
+              if constexpr (EXACT) tmem_st16(ts + 32 * c + 16, p2);
+            }
+            l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+            tmem_wait_st();
+            tc_fence_before();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(pfull + st);
+          return true;
+        };
+        while (i < n && ok && one(std::false_type())) ++i;
+        while (i < n && ok && one(std::true_type())) ++i;
+        ok = ok && mbar_wait(odone + st, turns & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+        done += n;
+        ++turns;
+      }
+      const bool whole = step == 0 && n == u.all;
+      if (part_of_it && live) {
+        // ---- the rows' values, out or to a partial, by lanes of a quad next to each other
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const float shift = C == -INFINITY ? 0.0f : C - m, half = truncf(0.5f * shift);
+        const float f0 = exp2f(half) * inv, f1 = exp2f(shift - half);
+        const int64_t place = 2 * (int64_t)blockIdx.x + (step == 0 ? 1 : 0);
+        if (!whole) a.ml[place * kUnitRows + r] = make_float2(m, l);
+        const int quad = lane & 3;
+#pragma unroll 1
+        for (int h = 0; h < 4; ++h) {  // rows 8 h + lane / 4 of the warp's 32 (of a load's 16 rows, half)
+          const int rr = 8 * h + (lane >> 2), ru = st * kTile + 32 * w + rr;
+          const float g0 = __shfl_sync(0xffffffffu, f0, rr), g1 = __shfl_sync(0xffffffffu, f1, rr);
+          const int t = ru / a.g;
+          const int64_t o = (int64_t)(u.s.first + u.tok0 + t) * a.o_row + (int64_t)(u.kvh * a.g + ru - t * a.g) * a.o_head;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[16];
+            tmem_ld16x32(to + ((uint32_t)(16 * (h >> 1)) << 16) + 32 * c, x);
+            float y[8];  // columns 32 c + 8 j + 2 quad and the next
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              y[2 * j] = __uint_as_float(h & 1 ? x[4 * j + 2] : x[4 * j]) * g0 * g1;
+              y[2 * j + 1] = __uint_as_float(h & 1 ? x[4 * j + 3] : x[4 * j + 1]) * g0 * g1;
+            }
+            if (!whole) {
+              float* p = a.part + (place * kUnitRows + ru) * kD + 32 * c + 2 * quad;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) *reinterpret_cast<float2*>(p + 8 * j) = make_float2(y[2 * j], y[2 * j + 1]);
+            } else if (a.out_bf16) {
+              uint32_t q[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const __nv_bfloat162 z = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
+                q[j] = *reinterpret_cast<const uint32_t*>(&z);
+              }
+              // the quad's four pairs of each eight columns to one lane
+#pragma unroll
+              for (int d = 1; d <= 2; d <<= 1) {
+                const bool up = (quad & d) != 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  if (j & d) continue;
+                  const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? q[j] : q[j + d], d);
+                  if (up) q[j] = got;
+                  else q[j + d] = got;
+                }
+              }
+              __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(a.out) + o + 32 * c + 8 * quad;
+              if (ru < u.rows) {
+                if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0u) {
+                  *reinterpret_cast<uint4*>(p) = make_uint4(q[0], q[1], q[2], q[3]);
                 } else {
 #pragma unroll
-                  for (int k = 0; k < 32; ++k) p[k] = x[k];
+                  for (int j = 0; j < 4; ++j) {
+                    p[2 * j] = __ushort_as_bfloat16((unsigned short)(q[j] & 0xFFFFu));
+                    p[2 * j + 1] = __ushort_as_bfloat16((unsigned short)(q[j] >> 16));
+                  }
+                }
+              }
+            } else if (ru < u.rows) {
+              float* p = reinterpret_cast<float*>(a.out) + o + 32 * c + 2 * quad;
+              if ((reinterpret_cast<uintptr_t>(p) & 7u) == 0u) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) *reinterpret_cast<float2*>(p + 8 * j) = make_float2(y[2 * j], y[2 * j + 1]);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  p[8 * j] = y[2 * j];
+                  p[8 * j + 1] = y[2 * j + 1];
                 }
               }
             }
           }
         }
+        tc_fence_before();
       }
-    } else if (warp < kMmaWarp) {
-      // --------------------------------------------------------- producers
-      const int w = warp - kSoftWarps;
-      const int blocks = (min(s.ctx, s.ctx - s.n + tok0 + min(a.per, s.n - tok0)) + kBlock - 1) / kBlock;  // of the unit's context
-      const int32_t* const row = a.table + (int64_t)seq * a.max_blocks;
-      auto block_id = [&](int t) {  // of the warp's block of step t: -1 past the end
-        const int j = (step + t) * kTileBlocks + w;
-        return t < n && j < blocks ? __ldg(row + j) : -1;
-      };
-      auto valid = [&](int id) { return id >= 0 && id < a.num_blocks; };
-      Page pk, pv;
-      auto page_of = [&](const uint8_t* pool, int id) { return pool + ((int64_t)id * a.Hkv + kvh) * kI8Page; };
-      auto fetch = [&](Page& p, const uint8_t* pool, int id) {
-        if (valid(id)) {
-          load_page(p, page_of(pool, id), lane);
-        } else {  // (finite operands, whatever the weights)
+      if (n > 0 && !whole) {
+        // ---- the unit's other parts (by the softmax warps alone, whether waits gave up or not)
+        auto cta_of = [&](int64_t p) { return ((p + 1) * R - 1) / total; };
+        const int64_t unit0 = at - u.place, c0 = cta_of(unit0 + kUnitCost), c1 = cta_of(unit0 + u.all + kUnitCost - 1);
+        __threadfence();
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (threadIdx.x == 0) {
+          const int k = atomicAdd(a.counters + c0, 1);
+          misc.arrived = k == (int)(c1 - c0);
+          if (misc.arrived) a.counters[c0] = 0;
+          __threadfence();
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (misc.arrived) {
+          // a warp a row, a lane four coordinates
+          for (int row = warp; row < u.rows; row += kSoftWarps) {
+            auto place = [&](int64_t c) { return (2 * c + (c == c0 ? 1 : 0)) * kUnitRows + row; };
+            float M = -INFINITY, L = 0.0f;
+            for (int64_t c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(&a.ml[place(c)]).x);
+            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int64_t c = c0; c <= c1; ++c) {
+              const float2 e = __ldcg(&a.ml[place(c)]);
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part + place(c) * kD) + lane);
+              const float f = e.x == -INFINITY ? e.y : e.y * exp2f(e.x - M);
+              L += f;
+              x.x = fmaf(f, v.x, x.x);
+              x.y = fmaf(f, v.y, x.y);
+              x.z = fmaf(f, v.z, x.z);
+              x.w = fmaf(f, v.w, x.w);
+            }
+            const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+            const int t = row / a.g;
+            const int64_t o = (int64_t)(u.s.first + u.tok0 + t) * a.o_row + (int64_t)(u.kvh * a.g + row - t * a.g) * a.o_head + 4 * lane;
+            if (a.out_bf16) {
+              __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(a.out) + o;
+              const __nv_bfloat162 y = __floats2bfloat162_rn(x.x * inv, x.y * inv), z = __floats2bfloat162_rn(x.z * inv, x.w * inv);
+              if ((reinterpret_cast<uintptr_t>(p) & 7u) == 0u) {
+                *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&y), *reinterpret_cast<const uint32_t*>(&z));
+              } else {
+                p[0] = y.x;
+                p[1] = y.y;
+                p[2] = z.x;
+                p[3] = z.y;
+              }
+            } else {
+              float* p = reinterpret_cast<float*>(a.out) + o;
+              p[0] = x.x * inv;
+              p[1] = x.y * inv;
+              p[2] = x.z * inv;
+              p[3] = x.w * inv;
+            }
+          }
+        }
+      }
+      // ---- on
+      if (n > 0) {
+        done0 += n;
+        ++units;
+      }
+      at += places;
+      if (at >= end) break;
+      u.next(a);
+    }
+  } else if (warp < kMmaWarp) {
+    // ----------------------------------------------------------- producers
+    fewer_registers<kProdRegs>();
+    const int w = warp - kSoftWarps;  // blocks 2 w and 2 w + 1 of a step
+    while (ok) {
+      int step, n;
+      const int places = u.part(end - at, &step, &n);
+      if (n > 0) {
+        const int blocks = (u.s.ctx - u.s.n + u.tok0 + min(a.per, u.s.n - u.tok0) + kBlock - 1) / kBlock;  // of the unit's context
+        const int32_t* const row = a.table + (int64_t)u.seq * a.max_blocks;
+        auto block_id = [&](int t, int b) {  // of the warp's block b of step t: -1 past the end
+          const int j = (step + t) * kTileBlocks + 2 * w + b;
+          return t < n && j < blocks ? __ldg(row + j) : -1;
+        };
+        auto valid = [&](int id) { return id >= 0 && id < a.num_blocks; };
+        auto page_of = [&](const uint8_t* pool, int id) { return pool + ((int64_t)id * a.Hkv + u.kvh) * kI8Page; };
+        auto fetch = [&](Page& p, const uint8_t* pool, int id) {
+          if (valid(id)) {
+            load_page(p, page_of(pool, id), lane);
+          } else {  // (finite operands, whatever the weights)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) p.w[i] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+            for (int i = 0; i < 4; ++i) p.w[i] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+          }
+        };
+        // lanes 0 to 3: step and bits of K and V of block 0, then of block 1, requested a step ahead
+        auto tails_of = [&](const int(&id)[2]) {
+          uint2 t = make_uint2(0u, 0u);
+          const int i = lane & 2 ? id[1] : id[0];
+          if (valid(i) && lane < 4) t = __ldg(reinterpret_cast<const uint2*>(page_of(lane & 1 ? a.vpool : a.kpool, i) + kI8Codes));
+          return t;
+        };
+        auto put_k = [&](const Page(&p)[2], int t) {
+          const int turn = done0 + t, ks = turn & 1;
+          if (turn >= 2 && !__all_sync(0xffffffffu, mbar_wait(kempty + ks, ((turn >> 1) & 1) ^ 1))) return false;
+          store_page(p[0], k_op + (uint32_t)ks * kOperand, 2 * w, lane);
+          store_page(p[1], k_op + (uint32_t)ks * kOperand, 2 * w + 1, lane);
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(kfull + ks);
+          return true;
+        };
+        int id[2], id1[2], id2[2];  // of steps t, t + 1, t + 2
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          id[b] = block_id(0, b);
+          id1[b] = block_id(1, b);
+          id2[b] = block_id(2, b);
         }
-      };
-      // lanes 0 and 1: step and bits of the block's K and V, requested a step ahead
-      auto tail_of = [&](int id) {
-        uint2 t = make_uint2(0u, 0u);
-        if (valid(id) && lane < 2) t = __ldg(reinterpret_cast<const uint2*>(page_of(lane ? a.vpool : a.kpool, id) + kI8Codes));
-        return t;
-      };
-      auto put_k = [&](int t) {
-        const int turn = done0 + t, st = turn & 1;
-        if (turn >= 2 && !__all_sync(0xffffffffu, mbar_wait(kempty + st, ((turn >> 1) & 1) ^ 1))) return false;
-        store_page(pk, k_op + (uint32_t)st * kOperand, w, lane);
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(kfull + st);
-        return true;
-      };
-      int id = block_id(0), id1 = block_id(1);
-      uint2 tail = tail_of(id);
-      fetch(pk, a.kpool, id);
-      fetch(pv, a.vpool, id);
-      ok = put_k(0);
-      if (n > 1) fetch(pk, a.kpool, id1);
-      for (int t = 0; t < n && ok; ++t) {
-        const int turn = done0 + t, slot = turn & (kSlots - 1);
-        const int id2 = block_id(t + 2);
-        const uint32_t bad = (tail.y | __shfl_down_sync(0xffffffffu, tail.y, 1)) & 0xFFFFu;  // (lane 0: of K and V)
-        if (lane < 2) {
-          float* const sp = reinterpret_cast<float*>(gen + kOffStep + slot * 96) + w;
-          sp[8 * lane] = __uint_as_float(tail.x);
-          if (lane == 1) sp[16] = (float)((int)((tail.x >> 23) & 255u) - 126);
-        }
-        if (lane == 0) {
-          if (!valid(id) && (step + t) * kTileBlocks + w < blocks) flag_status(a.status, TQ_DEV_BAD_BLOCK);
-          reinterpret_cast<uint32_t*>(gen + kOffBits + slot * 32)[w] = (valid(id) ? 0xFFFF0000u : 0u) | bad;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(gfull + slot);
-        tail = tail_of(id1);
-        // the next step's K goes ahead of this one's V: the tensor cores want it first
-        if (t + 1 < n && !(ok = put_k(t + 1))) break;
-        if (t + 2 < n) fetch(pk, a.kpool, id2);
-        const int vst = turn & vbit;
-        if (turn > vbit) ok = __all_sync(0xffffffffu, mbar_wait(vempty + vst, ((turn >> vbit) & 1) ^ 1));
+        Page pk[2], pv[2];
+        uint2 tail = tails_of(id);
+        fetch(pk[0], a.kpool, id[0]);
+        fetch(pk[1], a.kpool, id[1]);
+        ok = put_k(pk, 0);
+        if (ok && units > 0) ok = __all_sync(0xffffffffu, mbar_wait(qempty, (units & 1) ^ 1));
         if (!ok) break;
-        store_page(pv, v_op + (uint32_t)vst * kOperand, w, lane);
+        float* const sc = scales + (units & 1) * kUnitRows;
+        if (a.q_bf16) stage_q<true, EXACT>(a, u.s, u.kvh, u.tok0, u.rows, base, sc, w, lane);
+        else stage_q<false, EXACT>(a, u.s, u.kvh, u.tok0, u.rows, base, sc, w, lane);
         fence_proxy_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(vfull + vst);
-        if (t + 1 < n) fetch(pv, a.vpool, id1);
-        id = id1;
-        id1 = id2;
+        if (lane == 0) mbar_arrive(qfull);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          fetch(pk[b], a.kpool, id1[b]);
+          fetch(pv[b], a.vpool, id[b]);
+        }
+        for (int t = 0; t < n; ++t) {
+          const int turn = done0 + t, slot = turn & (kSlots - 1);
+          const int id3[2] = {block_id(t + 3, 0), block_id(t + 3, 1)};
+          const uint32_t bad = (tail.y | __shfl_down_sync(0xffffffffu, tail.y, 1)) & 0xFFFFu;  // (lanes 0 and 2: of K and V)
+          if (lane < 4) {
+            const int blk = 2 * w + (lane >> 1), i = lane & 2 ? id[1] : id[0];
+            float* const sp = reinterpret_cast<float*>(gen + kOffStep + slot * 96) + blk;
+            sp[8 * (lane & 1)] = __uint_as_float(tail.x);
+            if (lane & 1) {
+              sp[16] = (float)((int)((tail.x >> 23) & 255u) - 126);
+            } else {
+              if (!valid(i) && (step + t) * kTileBlocks + blk < blocks) flag_status(a.status, TQ_DEV_BAD_BLOCK);
+              reinterpret_cast<uint32_t*>(gen + kOffBits + slot * 32)[blk] = (valid(i) ? 0xFFFF0000u : 0u) | bad;
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(gfull + slot);
+          tail = tails_of(id1);
+          // the next step's K goes ahead of this one's V: the tensor cores want it first
+          if (t + 1 < n) {
+            if (!(ok = put_k(pk, t + 1))) break;
+            fetch(pk[0], a.kpool, id2[0]);
+            fetch(pk[1], a.kpool, id2[1]);
+          }
+          const int vst = turn & vbit;
+          if (turn > vbit) ok = __all_sync(0xffffffffu, mbar_wait(vempty + vst, ((turn >> vbit) & 1) ^ 1));
+          if (!ok) break;
+          store_page(pv[0], v_op + (uint32_t)vst * kOperand, 2 * w, lane);
+          store_page(pv[1], v_op + (uint32_t)vst * kOperand, 2 * w + 1, lane);
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(vfull + vst);
+          if (t + 1 < n) {
+            fetch(pv[0], a.vpool, id1[0]);
+            fetch(pv[1], a.vpool, id1[1]);
+          }
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            id[b] = id1[b];
+            id1[b] = id2[b];
+            id2[b] = id3[b];
+          }
+        }
+        done0 += n;
+        ++units;
       }
-    } else {
+      at += places;
+      if (at >= end) break;
+      u.next(a);
+    }
+  } else {
+    fewer_registers<kMmaRegs>();
+    if (warp == kMmaWarp) {
       // --------------------------------------------------------------- MMA
       const bool issue = elect_one();
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       constexpr uint32_t idesc_s = umma_idesc_16(false, false, kTile, kTile), idesc_o = umma_idesc_16(false, true, kTile, kTile);
       const uint64_t dq = umma_desc_sw128(base), dk = umma_desc_sw128(k_op), dv = umma_desc_sw128_mn(v_op, kPanel);
-      auto logits = [&](int i, int st) {
-        const int turn = done0 + i, ks = turn & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(kfull + ks, (turn >> 1) & 1))) return false;
-        tc_fence_after();
-        const uint64_t q = dq + (uint64_t)(st * (kOperand >> 4)), k = dk + (uint64_t)(ks * (kOperand >> 4));
-        const uint32_t d = tm + (uint32_t)(st * kTile);
-        if (issue) {
+      int done1 = 0;  // steps of the second stream so far
+      while (ok) {
+        int step, n;
+        const int places = u.part(end - at, &step, &n);
+        const bool two = u.rows > kTile;
+        if (n > 0) {
+          auto logits = [&](int i, int st) {
+            const int turn = done0 + i, ks = turn & 1;
+            if (!__all_sync(0xffffffffu, mbar_wait(kfull + ks, (turn >> 1) & 1))) return false;
+            tc_fence_after();
+            const uint64_t q = dq + (uint64_t)(st * (kOperand >> 4)), k = dk + (uint64_t)(ks * (kOperand >> 4));
+            const uint32_t d = tm + (uint32_t)(st * kTile);
+            if (issue) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint64_t off = (uint64_t)((j >> 2) * (kPanel >> 4) + (j & 3) * 2);
-            umma_bf16(d, q + off, k + off, idesc_s, j > 0);
-          }
-          if constexpr (EXACT) {
+              for (int j = 0; j < 8; ++j) {
+                const uint64_t off = (uint64_t)((j >> 2) * (kPanel >> 4) + (j & 3) * 2);
+                umma_bf16(d, q + off, k + off, idesc_s, j > 0);
+              }
+              if constexpr (EXACT) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint64_t off = (uint64_t)((j >> 2) * (kPanel >> 4) + (j & 3) * 2);
-              umma_bf16(d, q + (uint64_t)(2 * kOperand >> 4) + off, k + off, idesc_s, true);
+                for (int j = 0; j < 8; ++j) {
+                  const uint64_t off = (uint64_t)((j >> 2) * (kPanel >> 4) + (j & 3) * 2);
+                  umma_bf16(d, q + (uint64_t)(2 * kOperand >> 4) + off, k + off, idesc_s, true);
+                }
+              }
+              umma_commit(smem_u32(sfull + st));
+              if (!two || st == 1) {
+                umma_commit(smem_u32(kempty + ks));
+                if (i + 1 == n) umma_commit(smem_u32(qempty));
+              }
             }
-          }
-          umma_commit(smem_u32(sfull + st));
-          if (!two || st == 1) umma_commit(smem_u32(kempty + ks));
-        }
-        __syncwarp();
-        return true;
-      };
-      auto values = [&](int i, int st) {
-        const int turn = done0 + i, vst = turn & vbit;
-        if (!__all_sync(0xffffffffu, mbar_wait(pfull + st, ((st ? done1 : done0) + i) & 1) &&
-                                         mbar_wait(vfull + vst, (turn >> vbit) & 1)))
-          return false;
-        tc_fence_after();
-        const uint64_t v = dv + (uint64_t)(vst * (kOperand >> 4));
-        const uint32_t d = tm + (uint32_t)((2 + st) * kTile), p = tm + (uint32_t)(st * kTile);
-        if (issue) {
+            __syncwarp();
+            return true;
+          };
+          auto values = [&](int i, int st) {
+            const int turn = done0 + i, vst = turn & vbit;
+            if (!__all_sync(0xffffffffu, mbar_wait(pfull + st, ((st ? done1 : done0) + i) & 1) &&
+                                             mbar_wait(vfull + vst, (turn >> vbit) & 1)))
+              return false;
+            tc_fence_after();
+            const uint64_t v = dv + (uint64_t)(vst * (kOperand >> 4));
+            const uint32_t d = tm + (uint32_t)((2 + st) * kTile), p = tm + (uint32_t)(st * kTile);
+            if (issue) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            umma_16_ts(d, p + (uint32_t)(32 * (j >> 1) + 8 * (j & 1)), v + (uint64_t)(j * (16 * 128 >> 4)), idesc_o, i > 0 || j > 0);
-          if constexpr (EXACT) {
+              for (int j = 0; j < 8; ++j)
+                umma_16_ts(d, p + (uint32_t)(32 * (j >> 1) + 8 * (j & 1)), v + (uint64_t)(j * (16 * 128 >> 4)), idesc_o, i > 0 || j > 0);
+              if constexpr (EXACT) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              umma_16_ts(d, p + (uint32_t)(32 * (j >> 1) + 8 * (j & 1) + 16), v + (uint64_t)(j * (16 * 128 >> 4)), idesc_o, true);
-          }
-          if (!two || st == 1) umma_commit(smem_u32(vempty + vst));
-          if (i + 1 == n) umma_commit(smem_u32(odone + st));
-        }
-        __syncwarp();
-        return true;
-      };
-      ok = logits(0, 0);
-      if (ok && two) ok = logits(0, 1);
-      for (int i = 0; i < n && ok; ++i) {
-        ok = values(i, 0);
-        if (ok && i + 1 < n) ok = logits(i + 1, 0);
-        if (ok && two) ok = values(i, 1);
-        if (ok && two && i + 1 < n) ok = logits(i + 1, 1);
-      }
-    }
-    if (!ok && lane == 0) {
-      flag_status(a.status, TQ_DEV_WAIT_TIMEOUT);
-      misc.dead = 1;
-    }
-    // ---- the unit's other parts, if it was cut
-    const bool cut = !(step == 0 && n == all);
-    if (cut) __threadfence();
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (misc.dead) break;
-    if (cut) {
-      auto cta_of = [&](int64_t p) { return ((p + 1) * R - 1) / total; };
-      const int64_t unit0 = at - step, c0 = cta_of(unit0), c1 = cta_of(unit0 + all - 1);
-      if (threadIdx.x == 0) {
-        const int k = atomicAdd(a.counters + c0, 1);
-        misc.arrived = k == (int)(c1 - c0);
-        if (misc.arrived) a.counters[c0] = 0;
-        __threadfence();
-      }
-      __syncthreads();
-      if (misc.arrived && warp < kSoftWarps && 32 * warp < rows) {
-        const int r = 32 * warp + lane;
-        auto place = [&](int64_t c) { return 2 * c + (c == c0 ? 1 : 0); };
-        float M = -INFINITY, L = 0.0f;
-        for (int64_t c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(&a.ml[place(c) * kUnitRows + r]).x);
-        for (int64_t c = c0; c <= c1; ++c) {
-          const float2 e = __ldcg(&a.ml[place(c) * kUnitRows + r]);
-          L += e.x == -INFINITY ? e.y : e.y * exp2f(e.x - M);
-        }
-        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-        const int t = r / a.g;
-        const int64_t o = (int64_t)(s.first + tok0 + t) * a.o_row + (int64_t)(kvh * a.g + r - t * a.g) * a.o_head;
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          float4 x[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          for (int64_t c = c0; c <= c1; ++c) {
-            const float2 e = __ldcg(&a.ml[place(c) * kUnitRows + r]);
-            const float f = (e.x == -INFINITY ? e.y : e.y * exp2f(e.x - M)) * inv;
-            const float4* p = a.part + (place(c) * 8 + warp) * (32 * 32) + lane;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float4 v = __ldcg(p + (8 * q + k) * 32);
-              x[k].x = fmaf(f, v.x, x[k].x);
-              x[k].y = fmaf(f, v.y, x[k].y);
-              x[k].z = fmaf(f, v.z, x[k].z);
-              x[k].w = fmaf(f, v.w, x[k].w);
+                for (int j = 0; j < 8; ++j)
+                  umma_16_ts(d, p + (uint32_t)(32 * (j >> 1) + 8 * (j & 1) + 16), v + (uint64_t)(j * (16 * 128 >> 4)), idesc_o, true);
+              }
+              if (!two || st == 1) umma_commit(smem_u32(vempty + vst));
+              if (i + 1 == n) umma_commit(smem_u32(odone + st));
             }
+            __syncwarp();
+            return true;
+          };
+          ok = __all_sync(0xffffffffu, mbar_wait(qfull, units & 1));
+          if (ok) ok = logits(0, 0);
+          if (ok && two) ok = logits(0, 1);
+          for (int i = 0; i < n && ok; ++i) {
+            ok = values(i, 0);
+            if (ok && i + 1 < n) ok = logits(i + 1, 0);
+            if (ok && two) ok = values(i, 1);
+            if (ok && two && i + 1 < n) ok = logits(i + 1, 1);
           }
-          if (r >= rows) continue;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int64_t j = o + 32 * q + 4 * k;
-            if (a.out_bf16) {
-              __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(a.out) + j;
-              p[0] = __float2bfloat16_rn(x[k].x);
-              p[1] = __float2bfloat16_rn(x[k].y);
-              p[2] = __float2bfloat16_rn(x[k].z);
-              p[3] = __float2bfloat16_rn(x[k].w);
-            } else {
-              float* p = reinterpret_cast<float*>(a.out) + j;
-              p[0] = x[k].x;
-              p[1] = x[k].y;
-              p[2] = x[k].z;
-              p[3] = x[k].w;
-            }
-          }
+          done0 += n;
+          if (two) done1 += n;
+          ++units;
         }
-      }
-      __syncthreads();
-    }
-    // ---- on
-    at += n;
-    done0 += n;
-    ++turns0;
-    if (two) {
-      done1 += n;
-      ++turns1;
-    }
-    if (at < end) {
-      step = 0;
-      if (++tile == tiles_of(a, s)) {
-        tile = 0;
-        if (++kvh == a.Hkv) {
-          kvh = 0;
-          do s = seq_of(a, ++seq, false);
-          while (!s.large);
-        }
+        at += places;
+        if (at >= end) break;
+        u.next(a);
       }
     }
   }
+  if (!ok && lane == 0) flag_status(a.status, TQ_DEV_WAIT_TIMEOUT);
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -836,7 +949,7 @@ cudaError_t launch_int8_tiles(const AttendCall& c, uint8_t* partials, int num_sm
   a.per = kUnitRows / a.g;
   a.scale = c.sm_scale * 1.4426950408889634f;
   a.counters = reinterpret_cast<int*>(c.workspace);
-  a.part = reinterpret_cast<float4*>(partials);
+  a.part = reinterpret_cast<float*>(partials);
   a.ml = reinterpret_cast<float2*>(partials + (size_t)2 * num_sms * kUnitRows * kD * sizeof(float));
   a.status = c.status;
   return c.q_dtype == TQ_F32 ? run_tiles<true>(a, num_sms, st) : run_tiles<false>(a, num_sms, st);
