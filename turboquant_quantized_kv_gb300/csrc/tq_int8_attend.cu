@@ -50,11 +50,12 @@ constexpr uint32_t kOperand = 2 * kPanel;
 constexpr int kSlots = 4;                   // tiles whose steps are kept
 constexpr float kRoom = 14.0f, kTop = 8.0f; // log2 of P at most, and of its largest when the reference moves
 constexpr float kMoveM = 16.0f;
+constexpr float kMostSum = 60000.0f;         // of 16 weights in fp16
 
 // Shared memory: operands of 32 KB -- Q of the streams in 0 and 1 (low parts in 2 and 3), K in two stages,
 // V in two (with low parts in one) -- then the rest.
-constexpr uint32_t kOffStep = 7 * kOperand;                    // float [slots][3][8]: steps of K and V, exponents above V's
-constexpr uint32_t kOffBits = kOffStep + kSlots * 96;          // u32 [slots][8]: valid tokens << 16 | bad ones
+constexpr uint32_t kOffStep = 7 * kOperand;                    // float [slots][4][8]: steps of K and V, exponents above V's, their log2
+constexpr uint32_t kOffBits = kOffStep + kSlots * 128;         // u32 [slots][8]: valid tokens << 16 | bad ones
 constexpr uint32_t kOffRow = kOffBits + kSlots * 32;           // float [2][256]: a row's power of two, of units in turn
 constexpr uint32_t kOffBar = kOffRow + 2 * kUnitRows * 4;
 constexpr int kBars = 2 + 2 + 2 + 2 + kSlots + 2 + 2 + 2 + 2;
@@ -407,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
           if (!ok) return false;
           tc_fence_after();
           if (live) {
-            const float4* sp = reinterpret_cast<const float4*>(gen + kOffStep + slot * 96);
+            const float4* sp = reinterpret_cast<const float4*>(gen + kOffStep + slot * 128);
             const uint4* bp = reinterpret_cast<const uint4*>(gen + kOffBits + slot * 32);
             const int t0 = (step + i) * kTile;
             uint32_t mask[4];
@@ -543,8 +544,80 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
           if (lane == 0) mbar_arrive(pfull + st);
           return true;
         };
-        while (i < n && ok && one(std::false_type())) ++i;
-        while (i < n && ok && one(std::true_type())) ++i;
+        // A step of plain tokens by the references that the row has: nothing is looked for first, P comes straight
+        // from the logits, 2^(u + log2 step - C), and the sums say whether the references hold (all terms are
+        // positive, so a sum of 16 bounds each of them); P waits in registers until then.  A block whose values
+        // are 2^100 below the others' counts as that, which keeps its weights.
+        auto quick = [&] {
+          const int turn = done0 + i, slot = turn & (kSlots - 1);
+          ok = mbar_wait(gfull + slot, (turn / kSlots) & 1) && mbar_wait(sfull + st, (done + i) & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) return false;
+          tc_fence_after();
+          if (live) {
+            const uint4* bp = reinterpret_cast<const uint4*>(gen + kOffBits + slot * 32);
+            const uint4 q0 = bp[0], q1 = bp[1];
+            const bool plain = (q0.x & q0.y & q0.z & q0.w & q1.x & q1.y & q1.z & q1.w) == 0xFFFF0000u &&
+                               ((q0.x | q0.y | q0.z | q0.w | q1.x | q1.y | q1.z | q1.w) & 0xFFFFu) == 0u &&
+                               (step + i + 1) * kTile <= least;
+            if (!plain) return false;
+            const float2* const sp = reinterpret_cast<const float2*>(gen + kOffStep + slot * 128);
+            uint32_t p[4][16], ra[32], rb[32];
+            float most = 0.0f, more = 0.0f, sum = 0.0f;
+            const float low = C - m - 100.0f;
+            auto chunk = [&](const uint32_t(&x)[32], int c) {
+              const float2 k2 = sp[c], v2 = sp[12 + c];
+              const float ks[2] = {k2.x * cq, k2.y * cq}, o[2] = {fmaxf(v2.x, low) - C, fmaxf(v2.y, low) - C};
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {
+                float2 s0, s1;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  float2 u0 = make_float2(__uint_as_float(x[16 * b + 4 * k]), __uint_as_float(x[16 * b + 4 * k + 1]));
+                  float2 u1 = make_float2(__uint_as_float(x[16 * b + 4 * k + 2]), __uint_as_float(x[16 * b + 4 * k + 3]));
+                  u0 = __ffma2_rn(u0, make_float2(ks[b], ks[b]), make_float2(o[b], o[b]));
+                  u1 = __ffma2_rn(u1, make_float2(ks[b], ks[b]), make_float2(o[b], o[b]));
+                  u0 = make_float2(ex2(u0.x), ex2(u0.y));
+                  u1 = make_float2(ex2(u1.x), ex2(u1.y));
+                  s0 = k == 0 ? u0 : __fadd2_rn(s0, u0);
+                  s1 = k == 0 ? u1 : __fadd2_rn(s1, u1);
+                  p[c][8 * b + 2 * k] = half2_bits(u0.x, u0.y);
+                  p[c][8 * b + 2 * k + 1] = half2_bits(u1.x, u1.y);
+                }
+                const float t = (s0.x + s0.y) + (s1.x + s1.y), e = t * ex2(-o[b] - m);
+                most = fmaxf(most, t);
+                more = fmaxf(more, e);
+                sum += e;
+              }
+            };
+            tmem_ld32_async(ts, ra);
+            tmem_wait_ld32(ra);
+            tmem_ld32_async(ts + 32, rb);
+            chunk(ra, 0);
+            tmem_wait_ld32(rb);
+            tmem_ld32_async(ts + 64, ra);
+            chunk(rb, 1);
+            tmem_wait_ld32(ra);
+            tmem_ld32_async(ts + 96, rb);
+            chunk(ra, 2);
+            tmem_wait_ld32(rb);
+            chunk(rb, 3);
+            if (__any_sync(0xffffffffu, most > kMostSum || more > 1.2676506e30f)) return false;  // (2^100)
+            l += sum;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_st16(ts + 32 * c, p[c]);
+            tmem_wait_st();
+            tc_fence_before();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(pfull + st);
+          return true;
+        };
+        for (; i < n && ok; ++i) {
+          if (!EXACT && i > 0 && quick()) continue;
+          if (ok && one(std::false_type())) continue;
+          if (ok) one(std::true_type());
+        }
         ok = ok && mbar_wait(odone + st, turns & 1);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
@@ -561,66 +634,77 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
         if (!whole) a.ml[place * kUnitRows + r] = make_float2(m, l);
         const int quad = lane & 3;
 #pragma unroll 1
-        for (int h = 0; h < 4; ++h) {  // rows 8 h + lane / 4 of the warp's 32 (of a load's 16 rows, half)
-          const int rr = 8 * h + (lane >> 2), ru = st * kTile + 32 * w + rr;
-          const float g0 = __shfl_sync(0xffffffffu, f0, rr), g1 = __shfl_sync(0xffffffffu, f1, rr);
-          const int t = ru / a.g;
-          const int64_t o = (int64_t)(u.s.first + u.tok0 + t) * a.o_row + (int64_t)(u.kvh * a.g + ru - t * a.g) * a.o_head;
+        for (int h = 0; h < 2; ++h) {  // 16 rows, a lane two of them
+          float g0[2], g1[2];
+          int ru[2];
+          int64_t o[2];
 #pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int rr = 16 * h + 8 * i + (lane >> 2);
+            ru[i] = st * kTile + 32 * w + rr;
+            g0[i] = __shfl_sync(0xffffffffu, f0, rr);
+            g1[i] = __shfl_sync(0xffffffffu, f1, rr);
+            const int t = ru[i] / a.g;
+            o[i] = (int64_t)(u.s.first + u.tok0 + t) * a.o_row + (int64_t)(u.kvh * a.g + ru[i] - t * a.g) * a.o_head;
+          }
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t x[16];
-            tmem_ld16x32(to + ((uint32_t)(16 * (h >> 1)) << 16) + 32 * c, x);
-            float y[8];  // columns 32 c + 8 j + 2 quad and the next
+            tmem_ld16x32(to + ((uint32_t)(16 * h) << 16) + 32 * c, x);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              y[2 * j] = __uint_as_float(h & 1 ? x[4 * j + 2] : x[4 * j]) * g0 * g1;
-              y[2 * j + 1] = __uint_as_float(h & 1 ? x[4 * j + 3] : x[4 * j + 1]) * g0 * g1;
-            }
-            if (!whole) {
-              float* p = a.part + (place * kUnitRows + ru) * kD + 32 * c + 2 * quad;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) *reinterpret_cast<float2*>(p + 8 * j) = make_float2(y[2 * j], y[2 * j + 1]);
-            } else if (a.out_bf16) {
-              uint32_t q[4];
+            for (int i = 0; i < 2; ++i) {
+              float y[8];  // columns 32 c + 8 j + 2 quad and the next
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                const __nv_bfloat162 z = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
-                q[j] = *reinterpret_cast<const uint32_t*>(&z);
+                y[2 * j] = __uint_as_float(x[4 * j + 2 * i]) * g0[i] * g1[i];
+                y[2 * j + 1] = __uint_as_float(x[4 * j + 2 * i + 1]) * g0[i] * g1[i];
               }
-              // the quad's four pairs of each eight columns to one lane
+              if (!whole) {
+                float* p = a.part + (place * kUnitRows + ru[i]) * kD + 32 * c + 2 * quad;
 #pragma unroll
-              for (int d = 1; d <= 2; d <<= 1) {
-                const bool up = (quad & d) != 0;
+                for (int j = 0; j < 4; ++j) *reinterpret_cast<float2*>(p + 8 * j) = make_float2(y[2 * j], y[2 * j + 1]);
+              } else if (a.out_bf16) {
+                uint32_t q[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                  if (j & d) continue;
-                  const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? q[j] : q[j + d], d);
-                  if (up) q[j] = got;
-                  else q[j + d] = got;
+                  const __nv_bfloat162 z = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
+                  q[j] = *reinterpret_cast<const uint32_t*>(&z);
                 }
-              }
-              __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(a.out) + o + 32 * c + 8 * quad;
-              if (ru < u.rows) {
-                if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0u) {
-                  *reinterpret_cast<uint4*>(p) = make_uint4(q[0], q[1], q[2], q[3]);
+                // the quad's four pairs of each eight columns to one lane
+#pragma unroll
+                for (int d = 1; d <= 2; d <<= 1) {
+                  const bool up = (quad & d) != 0;
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    if (j & d) continue;
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? q[j] : q[j + d], d);
+                    if (up) q[j] = got;
+                    else q[j + d] = got;
+                  }
+                }
+                __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(a.out) + o[i] + 32 * c + 8 * quad;
+                if (ru[i] < u.rows) {
+                  if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0u) {
+                    *reinterpret_cast<uint4*>(p) = make_uint4(q[0], q[1], q[2], q[3]);
+                  } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                      p[2 * j] = __ushort_as_bfloat16((unsigned short)(q[j] & 0xFFFFu));
+                      p[2 * j + 1] = __ushort_as_bfloat16((unsigned short)(q[j] >> 16));
+                    }
+                  }
+                }
+              } else if (ru[i] < u.rows) {
+                float* p = reinterpret_cast<float*>(a.out) + o[i] + 32 * c + 2 * quad;
+                if ((reinterpret_cast<uintptr_t>(p) & 7u) == 0u) {
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) *reinterpret_cast<float2*>(p + 8 * j) = make_float2(y[2 * j], y[2 * j + 1]);
                 } else {
 #pragma unroll
                   for (int j = 0; j < 4; ++j) {
-                    p[2 * j] = __ushort_as_bfloat16((unsigned short)(q[j] & 0xFFFFu));
-                    p[2 * j + 1] = __ushort_as_bfloat16((unsigned short)(q[j] >> 16));
+                    p[8 * j] = y[2 * j];
+                    p[8 * j + 1] = y[2 * j + 1];
                   }
-                }
-              }
-            } else if (ru < u.rows) {
-              float* p = reinterpret_cast<float*>(a.out) + o + 32 * c + 2 * quad;
-              if ((reinterpret_cast<uintptr_t>(p) & 7u) == 0u) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) *reinterpret_cast<float2*>(p + 8 * j) = make_float2(y[2 * j], y[2 * j + 1]);
-              } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  p[8 * j] = y[2 * j];
-                  p[8 * j + 1] = y[2 * j + 1];
                 }
               }
             }
@@ -763,10 +847,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
           const uint32_t bad = (tail.y | __shfl_down_sync(0xffffffffu, tail.y, 1)) & 0xFFFFu;  // (lanes 0 and 2: of K and V)
           if (lane < 4) {
             const int blk = 2 * w + (lane >> 1), i = lane & 2 ? id[1] : id[0];
-            float* const sp = reinterpret_cast<float*>(gen + kOffStep + slot * 96) + blk;
+            float* const sp = reinterpret_cast<float*>(gen + kOffStep + slot * 128) + blk;
             sp[8 * (lane & 1)] = __uint_as_float(tail.x);
             if (lane & 1) {
               sp[16] = (float)((int)((tail.x >> 23) & 255u) - 126);
+              sp[24] = __log2f(__uint_as_float(tail.x));
             } else {
               if (!valid(i) && (step + t) * kTileBlocks + blk < blocks) flag_status(a.status, TQ_DEV_BAD_BLOCK);
               reinterpret_cast<uint32_t*>(gen + kOffBits + slot * 32)[blk] = (valid(i) ? 0xFFFF0000u : 0u) | bad;
