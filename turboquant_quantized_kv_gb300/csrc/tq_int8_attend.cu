@@ -14,8 +14,9 @@
 // A CTA: two streams of 128 rows over the same tokens.
 //   8 softmax warps   a thread a row: maxima, base-2 weights, P over the logits in tensor memory; then
 //                     the rows' values out;
-//   4 producer warps  turn 8 blocks of codes into fp16 (exact, i8_pair) in shared memory, K ahead of V, a
-//                     step of pages in registers; before a unit its queries;
+//   8 producer warps  turn codes into fp16 (exact, i8_pair) in shared memory, four of them two blocks of K
+//                     each and four of V, the next step's pages in registers meanwhile; before a unit
+//                     its queries;
 //   1 MMA warp        S = Q K^T (shared memory), O += P V (P in tensor memory), one elected thread.
 // Nothing waits for the CTA as a whole between units: the next unit's queries, pages and first logits come
 // while the softmax warps finish the last one.
@@ -40,9 +41,9 @@ namespace {
 constexpr int kTile = 128;          // tokens a step, rows a stream
 constexpr int kTileBlocks = kTile / kBlock;
 constexpr int kUnitRows = 2 * kTile;
-constexpr int kSoftWarps = 8, kProdWarps = 4;
+constexpr int kSoftWarps = 8, kProdWarps = 8;
 constexpr int kMmaWarp = kSoftWarps + kProdWarps;
-constexpr int kThreads = 512;  // (16 warps of 128 registers, dealt out again below)
+constexpr int kThreads = 640;  // (20 warps of 96 registers, dealt out again below)
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnitCost = 2;   // steps that the beginning and end of a unit are worth
 constexpr uint32_t kPanel = kTile * 128;    // 128 rows of 64 16-bit elements, swizzled
@@ -237,8 +238,8 @@ template <int N>
 __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
-constexpr int kSoftRegs = 176, kProdRegs = 104, kMmaRegs = 56;
-static_assert(2 * kSoftRegs + kProdRegs + kMmaRegs <= 4 * 128, "what the launch has");
+constexpr int kSoftRegs = 152, kProdRegs = 72, kMmaRegs = 32;
+static_assert(2 * kSoftRegs + 2 * kProdRegs + kMmaRegs <= 5 * 96, "what the launch has");
 
 // The unit that holds a place of the line, and the steps of a CTA's part in it.
 struct Unit {
@@ -346,15 +347,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(kfull + i, kProdWarps);
+      mbar_init(kfull + i, kProdWarps / 2);
       mbar_init(kempty + i, 1);
-      mbar_init(vfull + i, kProdWarps);
+      mbar_init(vfull + i, kProdWarps / 2);
       mbar_init(vempty + i, 1);
       mbar_init(sfull + i, 1);
       mbar_init(pfull + i, 4);
       mbar_init(odone + i, 1);
     }
-    for (int i = 0; i < kSlots; ++i) mbar_init(gfull + i, kProdWarps);
+    for (int i = 0; i < kSlots; ++i) mbar_init(gfull + i, kProdWarps / 2);
     mbar_init(qfull, kProdWarps);
     mbar_init(qempty, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -393,20 +394,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
       const bool live = st * kTile + 32 * w < u.rows;
       const int first = u.s.ctx - u.s.n + u.tok0;  // the unit's first token attends to this many and itself
       if (part_of_it) {
-        ok = ok && mbar_wait(qfull, units & 1);
-        ok = __all_sync(0xffffffffu, ok);
-        const float cq = live ? scales[(units & 1) * kUnitRows + r] : 0.0f;
+        float cq = 0.0f;
         // tokens the row attends to (a row past the end, whose queries are zeros: all, so that it holds nobody up)
         const int lim = r < u.rows ? first + r / a.g + 1 : 1 << 30;
         const int least = __reduce_min_sync(0xffffffffu, lim);
         int i = 0;
+        // A step's logits, then its steps (in this order: logits of a stream cannot run ahead of it, while units
+        // that the stream has no part in go by).  The first step's steps come with the rows' powers of two.
+        auto logits_of = [&](int slot, int turn, int phase) {
+          const bool there = __all_sync(0xffffffffu, mbar_wait(sfull + st, phase) && mbar_wait(gfull + slot, turn));
+          tc_fence_after();
+          return there;
+        };
         auto one = [&](auto careful) {  // one step; whether it is done
           constexpr bool kCareful = decltype(careful)::value;
           const int turn = done0 + i, slot = turn & (kSlots - 1);
-          ok = mbar_wait(gfull + slot, (turn / kSlots) & 1) && mbar_wait(sfull + st, (done + i) & 1);
-          ok = __all_sync(0xffffffffu, ok);
+          ok = logits_of(slot, (turn / kSlots) & 1, (done + i) & 1);
           if (!ok) return false;
-          tc_fence_after();
+          if (i == 0 && live) cq = scales[(units & 1) * kUnitRows + r];
           if (live) {
             const float4* sp = reinterpret_cast<const float4*>(gen + kOffStep + slot * 128);
             const uint4* bp = reinterpret_cast<const uint4*>(gen + kOffBits + slot * 32);
@@ -434,12 +439,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
               x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
               x[4] = z.x; x[5] = z.y; x[6] = z.z; x[7] = z.w;
             };
-            uint32_t S[4][32];
+            uint32_t ra[32], rb[32];
             float top = -INFINITY, topv = -INFINITY;  // the largest u of the row, and with the exponent of its block's values
             {
               float ks[8], ev[8];
-              tmem_ld32_async(ts, S[0]);
-              tmem_ld32_async(ts + 32, S[1]);
               eight(ks, 0);
               eight(ev, 2);
 #pragma unroll
@@ -466,16 +469,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
                   topv = fmaxf(topv, v + ev[2 * c + h]);
                 }
               };
-              tmem_wait_ld32(S[0]);
-              tmem_wait_ld32(S[1]);
-              tmem_ld32_async(ts + 64, S[2]);
-              tmem_ld32_async(ts + 96, S[3]);
-              tops(S[0], 0);
-              tops(S[1], 1);
-              tmem_wait_ld32(S[2]);
-              tmem_wait_ld32(S[3]);
-              tops(S[2], 2);
-              tops(S[3], 3);
+              tmem_ld32_async(ts, ra);
+              tmem_wait_ld32(ra);
+              tmem_ld32_async(ts + 32, rb);
+              tops(ra, 0);
+              tmem_wait_ld32(rb);
+              tmem_ld32_async(ts + 64, ra);
+              tops(rb, 1);
+              tmem_wait_ld32(ra);
+              tmem_ld32_async(ts + 96, rb);
+              tops(ra, 2);
+              tmem_wait_ld32(rb);
+              tops(rb, 3);
             }
             if (__any_sync(0xffffffffu, top > m + kMoveM || topv > C + kRoom)) {
               const float nm = fmaxf(m, ceilf(top)), nC = fmaxf(C, ceilf(topv) - kTop);
@@ -496,8 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
             }
             const float off = m == -INFINITY ? 0.0f : m, rho = C == -INFINITY ? 0.0f : exp2f(fminf(m - C, 120.0f));
             float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            auto weights = [&](const uint32_t(&x)[32], int c) {
               const float2 k2 = reinterpret_cast<const float2*>(sp)[c], v2 = reinterpret_cast<const float2*>(sp)[4 + c];
               // (2^120 at most; times a weight of zero)
               const float ks[2] = {k2.x * cq, k2.y * cq}, vs[2] = {fminf(v2.x * rho, 1.329227995784916e36f), fminf(v2.y * rho, 1.329227995784916e36f)};
@@ -506,8 +510,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
                 const int b = k >> 2;
-                float2 u0 = make_float2(__uint_as_float(S[c][4 * k]), __uint_as_float(S[c][4 * k + 1]));
-                float2 u1 = make_float2(__uint_as_float(S[c][4 * k + 2]), __uint_as_float(S[c][4 * k + 3]));
+                float2 u0 = make_float2(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1]));
+                float2 u1 = make_float2(__uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3]));
                 u0 = __ffma2_rn(u0, make_float2(ks[b], ks[b]), make_float2(-off, -off));
                 u1 = __ffma2_rn(u1, make_float2(ks[b], ks[b]), make_float2(-off, -off));
                 u0 = make_float2(ex2(u0.x), ex2(u0.y));
@@ -535,7 +539,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
               // over logits that have been read: high parts, low parts behind them
               tmem_st16(ts + 32 * c, p);
               if constexpr (EXACT) tmem_st16(ts + 32 * c + 16, p2);
-            }
+            };
+            tmem_ld32_async(ts, ra);
+            tmem_wait_ld32(ra);
+            tmem_ld32_async(ts + 32, rb);
+            weights(ra, 0);
+            tmem_wait_ld32(rb);
+            tmem_ld32_async(ts + 64, ra);
+            weights(rb, 1);
+            tmem_wait_ld32(ra);
+            tmem_ld32_async(ts + 96, rb);
+            weights(ra, 2);
+            tmem_wait_ld32(rb);
+            weights(rb, 3);
             l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
             tmem_wait_st();
             tc_fence_before();
@@ -550,10 +566,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
         // are 2^100 below the others' counts as that, which keeps its weights.
         auto quick = [&] {
           const int turn = done0 + i, slot = turn & (kSlots - 1);
-          ok = mbar_wait(gfull + slot, (turn / kSlots) & 1) && mbar_wait(sfull + st, (done + i) & 1);
-          ok = __all_sync(0xffffffffu, ok);
+          ok = logits_of(slot, (turn / kSlots) & 1, (done + i) & 1);
           if (!ok) return false;
-          tc_fence_after();
           if (live) {
             const uint4* bp = reinterpret_cast<const uint4*>(gen + kOffBits + slot * 32);
             const uint4 q0 = bp[0], q1 = bp[1];
@@ -778,43 +792,40 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
   } else if (warp < kMmaWarp) {
     // ----------------------------------------------------------- producers
     fewer_registers<kProdRegs>();
-    const int w = warp - kSoftWarps;  // blocks 2 w and 2 w + 1 of a step
+    const int w = warp - kSoftWarps, pair = w & 3;  // blocks 2 pair and 2 pair + 1 of a step
+    const bool values = w >= kProdWarps / 2;
+    const uint8_t* const pool = values ? a.vpool : a.kpool;
+    const uint32_t op = values ? v_op : k_op;
+    uint64_t *const full = values ? vfull : kfull, *const empty = values ? vempty : kempty;
+    const int sbit = values ? vbit : 1;
     while (ok) {
       int step, n;
       const int places = u.part(end - at, &step, &n);
       if (n > 0) {
         const int blocks = (u.s.ctx - u.s.n + u.tok0 + min(a.per, u.s.n - u.tok0) + kBlock - 1) / kBlock;  // of the unit's context
         const int32_t* const row = a.table + (int64_t)u.seq * a.max_blocks;
+        const int64_t stride = (int64_t)a.Hkv * kI8Page;
+        const uint8_t* const mine = pool + (int64_t)u.kvh * kI8Page;
         auto block_id = [&](int t, int b) {  // of the warp's block b of step t: -1 past the end
-          const int j = (step + t) * kTileBlocks + 2 * w + b;
+          const int j = (step + t) * kTileBlocks + 2 * pair + b;
           return t < n && j < blocks ? __ldg(row + j) : -1;
         };
         auto valid = [&](int id) { return id >= 0 && id < a.num_blocks; };
-        auto page_of = [&](const uint8_t* pool, int id) { return pool + ((int64_t)id * a.Hkv + u.kvh) * kI8Page; };
-        auto fetch = [&](Page& p, const uint8_t* pool, int id) {
+        auto fetch = [&](Page& p, int id) {
           if (valid(id)) {
-            load_page(p, page_of(pool, id), lane);
+            load_page(p, mine + id * stride, lane);
           } else {  // (finite operands, whatever the weights)
 #pragma unroll
             for (int i = 0; i < 4; ++i) p.w[i] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
           }
         };
-        // lanes 0 to 3: step and bits of K and V of block 0, then of block 1, requested a step ahead
-        auto tails_of = [&](const int(&id)[2]) {
+        // lanes 0 to 3 of K's warps: step and bits of K and V of block 0, then of block 1, requested a step ahead
+        auto tails_of = [&](int i0, int i1) {
           uint2 t = make_uint2(0u, 0u);
-          const int i = lane & 2 ? id[1] : id[0];
-          if (valid(i) && lane < 4) t = __ldg(reinterpret_cast<const uint2*>(page_of(lane & 1 ? a.vpool : a.kpool, i) + kI8Codes));
+          const int i = lane & 2 ? i1 : i0;
+          if (!values && valid(i) && lane < 4)
+            t = __ldg(reinterpret_cast<const uint2*>((lane & 1 ? a.vpool : a.kpool) + (int64_t)u.kvh * kI8Page + i * stride + kI8Codes));
           return t;
-        };
-        auto put_k = [&](const Page(&p)[2], int t) {
-          const int turn = done0 + t, ks = turn & 1;
-          if (turn >= 2 && !__all_sync(0xffffffffu, mbar_wait(kempty + ks, ((turn >> 1) & 1) ^ 1))) return false;
-          store_page(p[0], k_op + (uint32_t)ks * kOperand, 2 * w, lane);
-          store_page(p[1], k_op + (uint32_t)ks * kOperand, 2 * w + 1, lane);
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(kfull + ks);
-          return true;
         };
         int id[2], id1[2], id2[2];  // of steps t, t + 1, t + 2
 #pragma unroll
@@ -823,60 +834,52 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
           id1[b] = block_id(1, b);
           id2[b] = block_id(2, b);
         }
-        Page pk[2], pv[2];
-        uint2 tail = tails_of(id);
-        fetch(pk[0], a.kpool, id[0]);
-        fetch(pk[1], a.kpool, id[1]);
-        ok = put_k(pk, 0);
-        if (ok && units > 0) ok = __all_sync(0xffffffffu, mbar_wait(qempty, (units & 1) ^ 1));
-        if (!ok) break;
-        float* const sc = scales + (units & 1) * kUnitRows;
-        if (a.q_bf16) stage_q<true, EXACT>(a, u.s, u.kvh, u.tok0, u.rows, base, sc, w, lane);
-        else stage_q<false, EXACT>(a, u.s, u.kvh, u.tok0, u.rows, base, sc, w, lane);
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(qfull);
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          fetch(pk[b], a.kpool, id1[b]);
-          fetch(pv[b], a.vpool, id[b]);
-        }
+        uint2 tail = tails_of(id[0], id[1]);
+        Page p[2];
+        fetch(p[0], id[0]);
+        fetch(p[1], id[1]);
         for (int t = 0; t < n; ++t) {
-          const int turn = done0 + t, slot = turn & (kSlots - 1);
+          const int turn = done0 + t, slot = turn & (kSlots - 1), stage = turn & sbit;
           const int id3[2] = {block_id(t + 3, 0), block_id(t + 3, 1)};
-          const uint32_t bad = (tail.y | __shfl_down_sync(0xffffffffu, tail.y, 1)) & 0xFFFFu;  // (lanes 0 and 2: of K and V)
-          if (lane < 4) {
-            const int blk = 2 * w + (lane >> 1), i = lane & 2 ? id[1] : id[0];
-            float* const sp = reinterpret_cast<float*>(gen + kOffStep + slot * 128) + blk;
-            sp[8 * (lane & 1)] = __uint_as_float(tail.x);
-            if (lane & 1) {
-              sp[16] = (float)((int)((tail.x >> 23) & 255u) - 126);
-              sp[24] = __log2f(__uint_as_float(tail.x));
-            } else {
-              if (!valid(i) && (step + t) * kTileBlocks + blk < blocks) flag_status(a.status, TQ_DEV_BAD_BLOCK);
-              reinterpret_cast<uint32_t*>(gen + kOffBits + slot * 32)[blk] = (valid(i) ? 0xFFFF0000u : 0u) | bad;
-            }
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(gfull + slot);
-          tail = tails_of(id1);
-          // the next step's K goes ahead of this one's V: the tensor cores want it first
-          if (t + 1 < n) {
-            if (!(ok = put_k(pk, t + 1))) break;
-            fetch(pk[0], a.kpool, id2[0]);
-            fetch(pk[1], a.kpool, id2[1]);
-          }
-          const int vst = turn & vbit;
-          if (turn > vbit) ok = __all_sync(0xffffffffu, mbar_wait(vempty + vst, ((turn >> vbit) & 1) ^ 1));
+          // (a step's K goes in ahead of the unit's queries, which wait for the last unit's logits)
+          if (turn > sbit) ok = __all_sync(0xffffffffu, mbar_wait(empty + stage, ((turn >> sbit) & 1) ^ 1));
           if (!ok) break;
-          store_page(pv[0], v_op + (uint32_t)vst * kOperand, 2 * w, lane);
-          store_page(pv[1], v_op + (uint32_t)vst * kOperand, 2 * w + 1, lane);
+          store_page(p[0], op + (uint32_t)stage * kOperand, 2 * pair, lane);
+          store_page(p[1], op + (uint32_t)stage * kOperand, 2 * pair + 1, lane);
           fence_proxy_async();
           __syncwarp();
-          if (lane == 0) mbar_arrive(vfull + vst);
-          if (t + 1 < n) {
-            fetch(pv[0], a.vpool, id1[0]);
-            fetch(pv[1], a.vpool, id1[1]);
+          if (lane == 0) mbar_arrive(full + stage);
+          if (t == 0) {
+            if (units > 0) ok = __all_sync(0xffffffffu, mbar_wait(qempty, (units & 1) ^ 1));
+            if (!ok) break;
+            float* const sc = scales + (units & 1) * kUnitRows;
+            if (a.q_bf16) stage_q<true, EXACT>(a, u.s, u.kvh, u.tok0, u.rows, base, sc, w, lane);
+            else stage_q<false, EXACT>(a, u.s, u.kvh, u.tok0, u.rows, base, sc, w, lane);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(qfull);
+          }
+          fetch(p[0], id1[0]);
+          fetch(p[1], id1[1]);
+          if (t == 0) ok = __all_sync(0xffffffffu, mbar_wait(qfull, units & 1));  // (the others' rows, for who waits for gfull)
+          if (!ok) break;
+          if (!values) {
+            const uint32_t bad = (tail.y | __shfl_down_sync(0xffffffffu, tail.y, 1)) & 0xFFFFu;  // (lanes 0 and 2: of K and V)
+            if (lane < 4) {
+              const int blk = 2 * pair + (lane >> 1), i = lane & 2 ? id[1] : id[0];
+              float* const sp = reinterpret_cast<float*>(gen + kOffStep + slot * 128) + blk;
+              sp[8 * (lane & 1)] = __uint_as_float(tail.x);
+              if (lane & 1) {
+                sp[16] = (float)((int)((tail.x >> 23) & 255u) - 126);
+                sp[24] = __log2f(__uint_as_float(tail.x));
+              } else {
+                if (!valid(i) && (step + t) * kTileBlocks + blk < blocks) flag_status(a.status, TQ_DEV_BAD_BLOCK);
+                reinterpret_cast<uint32_t*>(gen + kOffBits + slot * 32)[blk] = (valid(i) ? 0xFFFF0000u : 0u) | bad;
+              }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(gfull + slot);
+            tail = tails_of(id1[0], id1[1]);
           }
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
