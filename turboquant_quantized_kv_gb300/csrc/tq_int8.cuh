@@ -16,7 +16,7 @@ constexpr float kI8Least = 1.1754943508222875e-38f;  // 2^-126, the least step
 
 // Sequences with more rows (tokens x query heads of a KV head) than this go through the tiles of
 // tq_int8_attend.cu, the others through the decode kernel.
-constexpr int kAttRows = 32;
+constexpr int kAttRows = 20;
 constexpr int kAttMostGroup = 256;  // query heads of a KV head, with more of them every sequence does the latter
 
 struct I8Tail {

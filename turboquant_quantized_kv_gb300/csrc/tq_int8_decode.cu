@@ -2,10 +2,11 @@
 //
 //     out[row] = softmax(sm_scale q[row] K^T) V,  K = codes * step of the block, V likewise
 //
-// for rows of one query token each: the sequences of tq_decode_attention, or the tokens of tq_int8_attend.
-// A unit is (row, KV head, group of up to eight query heads); a step is one block of 16 tokens of a unit.
+// for the one query token of each sequence (tq_decode_attention) or the few that tq_attend leaves to it.  The
+// rows of a sequence are (token, query head of a KV head's group), token by token; a unit is (sequence, KV
+// head, up to eight rows), a step one block of 16 tokens of its context.
 //
-// Work.  All steps of all units stand in one line (row by row, unit by unit, block by block) and the line
+// Work.  All steps of all units stand in one line (sequence by sequence, unit by unit, block by block) and the line
 // is cut into equal ranges, one a warp: whatever the contexts' lengths, every warp has the same number of
 // blocks.  A unit inside one range is finished by its warp; the warps of a CTA that share a unit meet in
 // shared memory, CTAs that share one (at most one unit begins in a CTA and goes on behind it) in the
@@ -15,7 +16,7 @@
 // of record r at c ^ (r & 7), so that all 128-bit reads are free of conflicts.  Codes become fp16 exactly
 // (i8_pair) and both products run as mma.sync m16n8k16 with fp32 sums:
 //     S [16 tokens x 8 columns] = K Q^T,  O^T [128 x 8 columns] += V^T P^T;
-// columns are four heads x (high part, low part) or eight heads in two passes, so that queries and weights
+// columns are four rows x (high part, low part) or eight rows in two passes, so that queries and weights
 // keep 22 bits.  A transpose in registers (movmatrix) brings P from the one layout to the other.
 //
 // Scales.  With u = log2 of a weight, m a running reference (moved only when u exceeds it by 16) and T one
@@ -45,16 +46,16 @@ struct DecArgs {
   const int32_t* table;
   int max_blocks;
   const int32_t* ctx_lens;
-  const int32_t* starts;  // attend: first token of each sequence (null: a row is a sequence)
-  int seqs;
-  int64_t most_rows;  // attend: rows a KV head of a sequence that is not left to the tiles
+  const int32_t* starts;  // attend: first token of each sequence (null: one each)
+  int n_tokens;       // attend: rows of q
+  int64_t most_rows;  // rows a KV head of a sequence that is not left to the tiles
   const void* q;
   int q_bf16;
   int64_t q_row, q_head;  // strides in elements
   void* out;
   int out_bf16;
   int64_t o_row, o_head;
-  int rows, Hq, Hkv, g, ngroups;
+  int seqs, Hq, Hkv, g;
   float scale;  // sm_scale * log2 e
   int splits;   // ranges a unit on average (0: one a warp of the GPU)
   int* counters;
@@ -92,83 +93,84 @@ __device__ __forceinline__ uint4 lds128(uint32_t at) {
   return v;
 }
 
-// The sequence and the context of a row.
-__device__ __forceinline__ int row_seq(const DecArgs& a, int row) {
-  if (!a.starts) return row;
-  int lo = 0, hi = a.seqs - 1;  // the last sequence that starts at or before the row
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(a.starts + mid) <= row) lo = mid;
-    else hi = mid - 1;
+// A sequence: its first query token, their number, its context (cut to the table), blocks of it, units a KV head
+// (none where the tiles have it).
+struct DecSeq {
+  int first, n, ctx, blocks, groups;
+};
+__device__ __forceinline__ DecSeq dec_seq(const DecArgs& a, int b, bool flag) {
+  DecSeq s = {b, 1, __ldg(a.ctx_lens + b), 0, 0};
+  if (a.starts) {
+    const int next = min(__ldg(a.starts + b + 1), a.n_tokens);
+    s.first = min(max(__ldg(a.starts + b), 0), a.n_tokens);
+    s.n = max(0, next - s.first);
   }
-  return lo;
-}
-__device__ __forceinline__ int row_ctx(const DecArgs& a, int row, int seq, bool flag) {
-  int ctx = __ldg(a.ctx_lens + seq);
+  if ((int64_t)s.n * a.g <= a.most_rows) s.groups = (s.n * a.g + 7) / 8;
   const int most = a.max_blocks * kBlock;
-  if (ctx < 0 || ctx > most) {
-    if (flag) flag_status(a.status, TQ_DEV_BAD_CONTEXT);
-    ctx = ctx < 0 ? 0 : most;
+  if (s.ctx < 0 || s.ctx > most) {
+    if (flag && s.groups > 0) flag_status(a.status, TQ_DEV_BAD_CONTEXT);
+    s.ctx = s.ctx < 0 ? 0 : most;
   }
-  if (a.starts) {  // causal: the sequence's last token sees all of it
-    const int start = __ldg(a.starts + seq), next = __ldg(a.starts + seq + 1);
-    if (row < start || row >= next) return -1;               // behind the last sequence
-    if ((int64_t)(next - start) * a.g > a.most_rows) return -1;  // takes tiles
-    ctx = max(0, ctx - (next - 1 - row));
-  }
-  return ctx;
+  s.blocks = s.groups > 0 ? (s.ctx + kBlock - 1) / kBlock : 0;
+  return s;
 }
-__device__ __forceinline__ int blocks_of(int ctx) { return ctx > 0 ? (ctx + kBlock - 1) / kBlock : 0; }
 
-template <int NH>  // query heads of a unit: 4 or 8
+template <int NH>  // rows of a unit: 4 or 8
 struct DecSmem {
   alignas(128) unsigned char ring[kDecWarps][kDecStages][kDecStage];
   float part[kDecWarps][NH][kPartRow];  // a warp's first segment, of a unit that began before
   float2 ml[kDecWarps][2][8];           // references and denominators of the first and the last segment
   int64_t unit0[kDecWarps][2];          // position in the line of the unit of either
-  int unit_row[kDecWarps][2], unit_sub[kDecWarps][2], unit_blocks[kDecWarps][2];
+  int unit_seq[kDecWarps][2], unit_sub[kDecWarps][2];
   int kind[kDecWarps];                  // bit 0: has a first segment, bit 1: which does not end its unit, bit 2: has a last one
-  int64_t sums[kDecWarps];
-  int at_row[kDecWarps], at_sub[kDecWarps], at_block[kDecWarps], at_blocks[kDecWarps];
+  int64_t sums[kDecWarps][2];
+  int at_seq[kDecWarps], at_sub[kDecWarps], at_block[kDecWarps];
   int arrived;
 };
 
 template <int NH>
 __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_constant__ DecArgs a) {
-  constexpr int HL = NH / 4;  // heads a lane has logits of: lane & 3 (of four), 2 (lane & 3) and the next (of eight)
+  constexpr int HL = NH / 4;  // rows a lane has logits of: lane & 3 (of four), 2 (lane & 3) and the next (of eight)
   extern __shared__ __align__(128) unsigned char gen[];
   DecSmem<NH>& sm = *reinterpret_cast<DecSmem<NH>*>(gen);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lg = lane >> 2, lt = lane & 3;
-  const int subs = a.Hkv * a.ngroups;  // units a row
 
-  // ---- the line: blocks before each thread's rows, and in all
-  const int per = (a.rows + kDecThreads - 1) / kDecThreads;
-  const int row0 = min(a.rows, (int)threadIdx.x * per), row1 = min(a.rows, row0 + per);
-  int64_t mine = 0;
-  for (int r = row0; r < row1; ++r) mine += blocks_of(row_ctx(a, r, row_seq(a, r), blockIdx.x == 0));
+  // ---- the line: steps before each thread's sequences, and in all
+  const int per = (a.seqs + kDecThreads - 1) / kDecThreads;
+  const int seq0 = min(a.seqs, (int)threadIdx.x * per), seq1 = min(a.seqs, seq0 + per);
+  int64_t mine = 0, units = 0;
+  for (int b = seq0; b < seq1; ++b) {
+    const DecSeq s = dec_seq(a, b, blockIdx.x == 0);
+    mine += (int64_t)s.blocks * s.groups;
+    if (s.blocks > 0) units += s.groups;
+  }
+  mine *= a.Hkv;
   int64_t before = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int64_t o = __shfl_up_sync(0xffffffffu, before, d);
     if (lane >= d) before += o;
+    units += __shfl_xor_sync(0xffffffffu, units, d);
   }
-  if (lane == 31) sm.sums[warp] = before;
+  if (lane == 31) {
+    sm.sums[warp][0] = before;
+    sm.sums[warp][1] = units;
+  }
   if (threadIdx.x < kDecWarps) sm.kind[threadIdx.x] = 0;
   __syncthreads();
   int64_t total = 0;
   before -= mine;
+  units = 0;
 #pragma unroll
   for (int w = 0; w < kDecWarps; ++w) {
-    if (w < warp) before += sm.sums[w];
-    total += sm.sums[w];
+    if (w < warp) before += sm.sums[w][0];
+    total += sm.sums[w][0];
+    units += sm.sums[w][1];
   }
-  total *= subs;
-  before *= subs;
-  mine *= subs;
   // ---- ranges: R in all, `wide` of them a CTA
   int64_t most = (total + kDecMinBlocks - 1) / kDecMinBlocks;
   int64_t want = (int64_t)gridDim.x * kDecWarps;
-  if (a.splits > 0) want = min(want, (int64_t)a.rows * subs * a.splits);
+  if (a.splits > 0) want = min(want, units * a.Hkv * a.splits);
   const int64_t R = most < 1 ? 1 : (most < want ? most : want);
   const int wide = (int)min((int64_t)kDecWarps, max((int64_t)4, (R + gridDim.x - 1) / gridDim.x));
   auto cut = [&](int64_t r) { return total * min(r, R) / R; };
@@ -177,23 +179,25 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
     const int64_t at = cut(r0 + w);
     if (r0 + w >= R || at < before || at >= before + mine) continue;
     int64_t left = at - before;
-    for (int r = row0; r < row1; ++r) {
-      const int n = blocks_of(row_ctx(a, r, row_seq(a, r), false));
-      if (left < (int64_t)n * subs) {
-        sm.at_row[w] = r;
-        sm.at_sub[w] = (int)(left / n);
-        sm.at_block[w] = (int)(left % n);
-        sm.at_blocks[w] = n;
+    for (int b = seq0; b < seq1; ++b) {
+      const DecSeq s = dec_seq(a, b, false);
+      const int64_t n = (int64_t)s.blocks * s.groups * a.Hkv;
+      if (left < n) {
+        sm.at_seq[w] = b;
+        sm.at_sub[w] = (int)(left / s.blocks);
+        sm.at_block[w] = (int)(left % s.blocks);
         break;
       }
-      left -= (int64_t)n * subs;
+      left -= n;
     }
   }
-  // rows without a token
-  for (int r = blockIdx.x + gridDim.x * warp; r < a.rows; r += gridDim.x * kDecWarps) {
-    if (row_ctx(a, r, row_seq(a, r), false) != 0) continue;
-    for (int i = lane; i < a.Hq * kD; i += 32) {
-      const int64_t o = (int64_t)r * a.o_row + (int64_t)(i / kD) * a.o_head + i % kD;
+  // sequences without a token
+  for (int b = blockIdx.x + gridDim.x * warp; b < a.seqs; b += gridDim.x * kDecWarps) {
+    const DecSeq s = dec_seq(a, b, false);
+    if (s.groups == 0 || s.blocks > 0) continue;
+    for (int64_t i = lane; i < (int64_t)s.n * a.Hq * kD; i += 32) {
+      const int t = (int)(i / (a.Hq * kD)), j = (int)(i - (int64_t)t * a.Hq * kD);
+      const int64_t o = (int64_t)(s.first + t) * a.o_row + (int64_t)(j / kD) * a.o_head + j % kD;
       if (a.out_bf16) store_elem(reinterpret_cast<__nv_bfloat16*>(a.out) + o, 0.0f);
       else store_elem(reinterpret_cast<float*>(a.out) + o, 0.0f);
     }
@@ -213,10 +217,15 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
       l[h] = 0.0f;
     }
   };
-  auto unit_heads = [&](int sub) { return min(8, a.g - 8 * (sub % a.ngroups)); };
-  auto first_head = [&](int sub) { return (sub / a.ngroups) * a.g + 8 * (sub % a.ngroups); };
-  auto store_row = [&](int row, int head, int c, const float* v, int n) {  // n coordinates from c on
-    const int64_t o = (int64_t)row * a.o_row + (int64_t)head * a.o_head + c;
+  auto unit_rows = [&](const DecSeq& s, int sub) { return min(8, s.n * a.g - 8 * (sub % s.groups)); };
+  // where row c of a unit is: its token among the sequence's, its query head
+  auto row_at = [&](const DecSeq& s, int sub, int c) {
+    const int r = 8 * (sub % s.groups) + c, t = r / a.g;
+    return make_int2(t, (sub / s.groups) * a.g + r - t * a.g);
+  };
+  auto store_row = [&](const DecSeq& s, int sub, int r, int c, const float* v, int n) {  // n coordinates from c on
+    const int2 at = row_at(s, sub, r);
+    const int64_t o = (int64_t)(s.first + at.x) * a.o_row + (int64_t)at.y * a.o_head + c;
     if (a.out_bf16) {
       __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(a.out) + o;
       if ((reinterpret_cast<uintptr_t>(p) & 7u) == 0u) {
@@ -240,9 +249,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
   if (warp < wide && r0 + warp < R && total > 0) {
     const int64_t begin = cut(r0 + warp), end = cut(r0 + warp + 1);
     // the cursor of the copies
-    int irow = sm.at_row[warp], isub = sm.at_sub[warp], ij = sm.at_block[warp], in = sm.at_blocks[warp];
-    int row = irow, sub = isub, j = ij, nb = in;  // and of the steps
-    int iseq = row_seq(a, irow);
+    int iseq = sm.at_seq[warp], isub = sm.at_sub[warp], ij = sm.at_block[warp];
+    int seq = iseq, sub = isub, j = ij;  // and of the steps
+    DecSeq s = dec_seq(a, seq, false);
+    int in = s.blocks, igroups = s.groups;
     int ids = -1, window = -1;
     int64_t ahead = begin;
     const uint32_t ring = smem_u32(sm.ring[warp]);
@@ -260,7 +270,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
         const bool ok = id >= 0 && id < a.num_blocks;
         if (!ok && lane == 0) flag_status(a.status, TQ_DEV_BAD_BLOCK);
         if (ok) {
-          const int64_t page = ((int64_t)id * a.Hkv + isub / a.ngroups) * kI8Page;
+          const int64_t page = ((int64_t)id * a.Hkv + isub / igroups) * kI8Page;
           const uint8_t* k = a.kpool + page + 16 * lane;
           const uint8_t* v = a.vpool + page + 16 * lane;
           const uint32_t s = ring + (uint32_t)stage * kDecStage;
@@ -280,13 +290,13 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
         if (++ij == in) {
           ij = 0;
           window = -1;
-          if (++isub == subs) {
+          if (++isub == igroups * a.Hkv) {
             isub = 0;
             if (ahead < end) {
               do {
-                ++irow;
-                iseq = row_seq(a, irow);
-                in = blocks_of(row_ctx(a, irow, iseq, false));
+                const DecSeq t = dec_seq(a, ++iseq, false);
+                in = t.blocks;
+                igroups = t.groups;
               } while (in == 0);
             }
           }
@@ -300,13 +310,15 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
     clear();
     uint32_t qh[8][2], ql[NH == 8 ? 8 : 1][2];
     float cq[HL];
-    int ctx = 0;
+    int lim[HL];  // tokens that the lane's rows attend to
     auto load_unit = [&] {  // queries of the unit as operands: column lg, coordinates 32 lt + 4 i .. + 3 in step i
-      const int heads = unit_heads(sub), head = NH == 4 ? lg >> 1 : lg;
-      ctx = row_ctx(a, row, row_seq(a, row), false);
+      const int rows = unit_rows(s, sub), col = NH == 4 ? lg >> 1 : lg;
+#pragma unroll
+      for (int h = 0; h < HL; ++h) lim[h] = s.ctx - s.n + 1 + row_at(s, sub, NH == 4 ? lt : 2 * lt + h).x;
       float x[32];
-      if (head < heads) {
-        const int64_t at = (int64_t)row * a.q_row + (int64_t)(first_head(sub) + head) * a.q_head + 32 * lt;
+      if (col < rows) {
+        const int2 r = row_at(s, sub, col);
+        const int64_t at = (int64_t)(s.first + r.x) * a.q_row + (int64_t)r.y * a.q_head + 32 * lt;
         if (a.q_bf16) {
           const __nv_bfloat16* p = reinterpret_cast<const __nv_bfloat16*>(a.q) + at;
           if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0u) {
@@ -357,7 +369,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
           }
         }
       }
-      // lane lt's heads sit in columns (two columns a head of four)
+      // lane lt's rows sit in columns (two columns a row of four)
 #pragma unroll
       for (int h = 0; h < HL; ++h) cq[h] = __shfl_sync(0xffffffffu, back, 4 * (NH == 4 ? 2 * lt : 2 * lt + h));
     };
@@ -368,18 +380,17 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
       const int stage = (int)((at - begin) & 1);
       asm volatile("cp.async.wait_group 1;" ::: "memory");
       __syncwarp();
-      const uint32_t s = ring + (uint32_t)stage * kDecStage;
+      const uint32_t pages = ring + (uint32_t)stage * kDecStage;
       if (live[stage * (kDecStage / 4)]) {
         const I8Tail* tails = reinterpret_cast<const I8Tail*>(sm.ring[warp][stage] + 2 * kI8Codes);
         const float kstep = tails[0].step, vstep = tails[1].step;
         const uint32_t kbad = tails[0].bad, vbad = tails[1].bad;
-        const int count = ctx - kBlock * j;  // tokens of the block, or more
         // ---- logits
         float S[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const uint32_t col = (uint32_t)(((2 * lt + c) ^ lg) << 4);
-          const uint4 x = lds128(s + (uint32_t)lg * 128 + col), y = lds128(s + (uint32_t)(lg + 8) * 128 + col);
+          const uint4 x = lds128(pages + (uint32_t)lg * 128 + col), y = lds128(pages + (uint32_t)(lg + 8) * 128 + col);
           const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -390,10 +401,12 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
           }
         }
         float u[HL][2];
-        const bool in0 = lg < count, in1 = lg + 8 < count;
+        bool in0[HL], in1[HL];
 #pragma unroll
         for (int h = 0; h < HL; ++h) {
           const float k = kstep * cq[h];
+          in0[h] = lg < lim[h] - kBlock * j;
+          in1[h] = lg + 8 < lim[h] - kBlock * j;
           u[h][0] = (NH == 4 ? S[0] + S[1] : S[h]) * k;
           u[h][1] = (NH == 4 ? S[2] + S[3] : S[2 + h]) * k;
         }
@@ -411,12 +424,12 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
 #pragma unroll
         for (int h = 0; h < HL; ++h) {
           const float most_u = fminf(m[h] + 16.0f, T[h] + (float)(14 - ev));
-          move |= (in0 && u[h][0] > most_u) || (in1 && u[h][1] > most_u);
+          move |= (in0[h] && u[h][0] > most_u) || (in1[h] && u[h][1] > most_u);
         }
         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
           for (int h = 0; h < HL; ++h) {
-            float top = fmaxf(in0 ? u[h][0] : -INFINITY, in1 ? u[h][1] : -INFINITY);
+            float top = fmaxf(in0[h] ? u[h][0] : -INFINITY, in1[h] ? u[h][1] : -INFINITY);
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = ceilf(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)));
@@ -441,7 +454,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
         float w[HL][2];
 #pragma unroll
         for (int h = 0; h < HL; ++h) {
-          const float p0 = in0 ? ex2(u[h][0] - m[h]) : 0.0f, p1 = in1 ? ex2(u[h][1] - m[h]) : 0.0f;
+          const float p0 = in0[h] ? ex2(u[h][0] - m[h]) : 0.0f, p1 = in1[h] ? ex2(u[h][1] - m[h]) : 0.0f;
           l[h] += p0 + p1;
           const float f = T[h] == -INFINITY ? 0.0f : vmant * ex2(fminf((float)ev + m[h] - T[h], 120.0f));
           w[h][0] = p0 * f;
@@ -450,8 +463,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
         if (vbad) {
 #pragma unroll
           for (int h = 0; h < HL; ++h) {
-            if (in0 && ((vbad >> lg) & 1u)) w[h][0] = CUDART_NAN_F;
-            if (in1 && ((vbad >> (lg + 8)) & 1u)) w[h][1] = CUDART_NAN_F;
+            if (in0[h] && ((vbad >> lg) & 1u)) w[h][0] = CUDART_NAN_F;
+            if (in1[h] && ((vbad >> (lg + 8)) & 1u)) w[h][1] = CUDART_NAN_F;
           }
         }
 #pragma unroll
@@ -471,7 +484,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int tok = 2 * lt + (k & 1) + 8 * (k >> 1);
-          r[k] = lds128(s + 2048u + (uint32_t)tok * 128 + (uint32_t)((lg ^ (tok & 7)) << 4));
+          r[k] = lds128(pages + 2048u + (uint32_t)tok * 128 + (uint32_t)((lg ^ (tok & 7)) << 4));
         }
         const uint32_t* rw[4] = {&r[0].x, &r[1].x, &r[2].x, &r[3].x};
 #pragma unroll
@@ -486,7 +499,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
       __syncwarp();
       issue(stage);
       // ---- the end of a unit or of the range
-      const bool last = at + 1 == end, done = j + 1 == nb;
+      const bool last = at + 1 == end, done = j + 1 == s.blocks;
       if (done || last) {
         float inv[HL];
         float2 ml[HL];
@@ -497,7 +510,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
           inv[h] = l[h] == 0.0f ? 0.0f : 1.0f / l[h];
           ml[h] = make_float2(m[h], l[h]);
         }
-        // normalised values of head hh of the lane: coordinates 16 lg .. 16 lg + 15
+        // normalised values of row h of the lane: coordinates 16 lg .. 16 lg + 15
         auto values = [&](int h, float (&o)[16]) {
           const float shift = T[h] == -INFINITY ? 0.0f : T[h] - m[h], half = truncf(0.5f * shift);
           const float f0 = exp2f(half), f1 = exp2f(shift - half);
@@ -508,14 +521,14 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
             o[2 * i + 1] = y * inv[h] * f0 * f1;
           }
         };
-        const int heads = unit_heads(sub);
+        const int rows = unit_rows(s, sub);
         if (began && done) {
 #pragma unroll
           for (int h = 0; h < HL; ++h) {
-            const int head = NH == 4 ? lt : 2 * lt + h;
+            const int row = NH == 4 ? lt : 2 * lt + h;
             float o[16];
             values(h, o);
-            if (head < heads) store_row(row, first_head(sub) + head, 16 * lg, o, 16);
+            if (row < rows) store_row(s, sub, row, 16 * lg, o, 16);
           }
         } else {
           // slot 0: a segment of a unit that began before; slot 1: the beginning of one that goes on
@@ -528,19 +541,18 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
           }
 #pragma unroll
           for (int h = 0; h < HL; ++h) {
-            const int head = NH == 4 ? lt : 2 * lt + h;
+            const int row = NH == 4 ? lt : 2 * lt + h;
             float o[16];
             values(h, o);
 #pragma unroll
             for (int k = 0; k < 16; k += 4)
-              *reinterpret_cast<float4*>(&p[head][16 * lg + k]) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-            if (lg == 0) sm.ml[warp][slot][head] = ml[h];
+              *reinterpret_cast<float4*>(&p[row][16 * lg + k]) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+            if (lg == 0) sm.ml[warp][slot][row] = ml[h];
           }
           if (lane == 0) {
             sm.unit0[warp][slot] = at - j;
-            sm.unit_row[warp][slot] = row;
+            sm.unit_seq[warp][slot] = seq;
             sm.unit_sub[warp][slot] = sub;
-            sm.unit_blocks[warp][slot] = nb;
             sm.kind[warp] |= slot ? 4 : (done ? 1 : 3);
           }
         }
@@ -550,12 +562,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
         if (done) {
           j = 0;
           began = true;
-          if (++sub == subs) {
+          if (++sub == s.groups * a.Hkv) {
             sub = 0;
-            do {
-              ++row;
-              nb = blocks_of(row_ctx(a, row, row_seq(a, row), false));
-            } while (nb == 0);
+            do s = dec_seq(a, ++seq, false);
+            while (s.blocks == 0);
           }
           load_unit();
         } else {
@@ -586,12 +596,13 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
       ++we;
       open = (sm.kind[we] & 2) != 0;
     }
-    const int row = sm.unit_row[w0][s0], sub = sm.unit_sub[w0][s0], nb = sm.unit_blocks[w0][s0];
+    const DecSeq s = dec_seq(a, sm.unit_seq[w0][s0], false);
+    const int sub = sm.unit_sub[w0][s0], nb = s.blocks;
     const int64_t unit0 = sm.unit0[w0][s0];
-    const int heads = unit_heads(sub);
+    const int rows = unit_rows(s, sub);
     const bool whole = s0 == 1 && !open;
     const int64_t place = 2 * (int64_t)blockIdx.x + s0;
-    if (warp < heads) {
+    if (warp < rows) {
       const int h = warp;
       float M = -INFINITY, L = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       for (int x = w0; x <= we; ++x) M = fmaxf(M, sm.ml[x][x == w0 ? s0 : 0][h].x);
@@ -606,7 +617,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
 #pragma unroll
       for (int k = 0; k < 4; ++k) o[k] *= inv;
       if (whole) {
-        store_row(row, first_head(sub) + h, 4 * lane, o, 4);
+        store_row(s, sub, h, 4 * lane, o, 4);
       } else {
         reinterpret_cast<float4*>(a.part)[(place * 8 + h) * (kD / 4) + lane] = make_float4(o[0], o[1], o[2], o[3]);
         if (lane == 0) a.ml[place * 8 + h] = make_float2(M, L);
@@ -625,7 +636,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
         __threadfence();
       }
       __syncthreads();
-      if (sm.arrived && warp < heads) {
+      if (sm.arrived && warp < rows) {
         const int h = warp;
         float M = -INFINITY, L = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         for (int64_t c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(&a.ml[(2 * c + (c == c0 ? 1 : 0)) * 8 + h]).x);
@@ -640,7 +651,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
         const float inv = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[k] *= inv;
-        store_row(row, first_head(sub) + h, 4 * lane, o, 4);
+        store_row(s, sub, h, 4 * lane, o, 4);
       }
     }
     // on behind the chain
@@ -675,17 +686,16 @@ cudaError_t run_decode(const DecArgs& a, int num_sms, cudaStream_t st) {
 
 size_t int8_partial_bytes(int num_sms) { return ((size_t)2 * num_sms * 8 * (kD + 2) * sizeof(float) + 255) & ~(size_t)255; }
 
-static cudaError_t launch_rows(const tq_cache_desc& d, DecArgs& a, uint8_t* workspace, int num_sms, cudaStream_t st) {
+static cudaError_t launch_rows(const tq_cache_desc& d, DecArgs& a, bool few, uint8_t* workspace, int num_sms, cudaStream_t st) {
   a.kpool = reinterpret_cast<const uint8_t*>(d.k_cache);
   a.vpool = reinterpret_cast<const uint8_t*>(d.v_cache);
   a.num_blocks = d.num_blocks;
   a.Hkv = d.num_kv_heads;
   a.g = a.Hq / a.Hkv;
-  a.ngroups = (a.g + 7) / 8;
   a.counters = reinterpret_cast<int*>(workspace);
   a.part = reinterpret_cast<float*>(workspace + kCounterRegionBytes);
   a.ml = reinterpret_cast<float2*>(a.part + (size_t)2 * num_sms * 8 * kD);
-  return a.g <= 4 ? run_decode<4>(a, num_sms, st) : run_decode<8>(a, num_sms, st);
+  return few ? run_decode<4>(a, num_sms, st) : run_decode<8>(a, num_sms, st);
 }
 
 cudaError_t launch_int8_decode(const DecodeCall& c, int num_sms, cudaStream_t st) {
@@ -693,6 +703,7 @@ cudaError_t launch_int8_decode(const DecodeCall& c, int num_sms, cudaStream_t st
   a.table = c.block_table;
   a.max_blocks = c.max_blocks;
   a.ctx_lens = c.ctx_lens;
+  a.most_rows = INT64_MAX;
   a.q = c.q;
   a.q_bf16 = c.q_dtype == TQ_BF16 ? 1 : 0;
   a.Hq = c.num_q_heads;
@@ -700,11 +711,11 @@ cudaError_t launch_int8_decode(const DecodeCall& c, int num_sms, cudaStream_t st
   a.q_head = a.o_head = kD;
   a.out = c.out;
   a.out_bf16 = c.out_dtype == TQ_BF16 ? 1 : 0;
-  a.rows = c.batch;
+  a.seqs = c.batch;
   a.splits = c.splits;
   a.scale = c.sm_scale * 1.4426950408889634f;
   a.status = c.status;
-  return launch_rows(*c.desc, a, c.workspace, num_sms, st);
+  return launch_rows(*c.desc, a, a.Hq / c.desc->num_kv_heads <= 4, c.workspace, num_sms, st);
 }
 
 cudaError_t launch_int8_attend(const AttendCall& c, int num_sms, cudaStream_t st) {
@@ -714,6 +725,7 @@ cudaError_t launch_int8_attend(const AttendCall& c, int num_sms, cudaStream_t st
   a.ctx_lens = c.ctx_lens;
   a.starts = c.starts;
   a.seqs = c.batch;
+  a.n_tokens = (int)c.n_tokens;
   a.q = c.q->in;
   a.q_bf16 = c.q_dtype == TQ_BF16 ? 1 : 0;
   a.Hq = c.q->num_heads;
@@ -723,13 +735,12 @@ cudaError_t launch_int8_attend(const AttendCall& c, int num_sms, cudaStream_t st
   a.out_bf16 = c.out_dtype == TQ_BF16 ? 1 : 0;
   a.o_row = c.q->out_token_stride;
   a.o_head = c.q->out_head_stride;
-  a.rows = (int)c.n_tokens;
   a.scale = c.sm_scale * 1.4426950408889634f;
   a.status = c.status;
   const int g = a.Hq / c.desc->num_kv_heads;
   const bool tiles = g <= kAttMostGroup && c.n_tokens * g > kAttRows;
   a.most_rows = tiles ? kAttRows : INT64_MAX;
-  const cudaError_t e = launch_rows(*c.desc, a, c.workspace, num_sms, st);
+  const cudaError_t e = launch_rows(*c.desc, a, c.n_tokens * g <= 4, c.workspace, num_sms, st);
   if (e != cudaSuccess || !tiles) return e;
   return launch_int8_tiles(c, c.workspace + kCounterRegionBytes + int8_partial_bytes(num_sms), num_sms, st);
 }
