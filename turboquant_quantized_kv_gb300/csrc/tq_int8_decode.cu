@@ -173,10 +173,11 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
   if (a.splits > 0) want = min(want, units * a.Hkv * a.splits);
   const int64_t R = most < 1 ? 1 : (most < want ? most : want);
   const int wide = (int)min((int64_t)kDecWarps, max((int64_t)4, (R + gridDim.x - 1) / gridDim.x));
-  auto cut = [&](int64_t r) { return total * min(r, R) / R; };
   const int64_t r0 = (int64_t)blockIdx.x * wide;
+  // lane w: where the CTA's range w begins
+  const int64_t cuts = total * min(r0 + min(lane, kDecWarps), R) / R;
   for (int w = 0; w < wide; ++w) {
-    const int64_t at = cut(r0 + w);
+    const int64_t at = __shfl_sync(0xffffffffu, cuts, w);
     if (r0 + w >= R || at < before || at >= before + mine) continue;
     int64_t left = at - before;
     for (int b = seq0; b < seq1; ++b) {
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
   };
 
   if (warp < wide && r0 + warp < R && total > 0) {
-    const int64_t begin = cut(r0 + warp), end = cut(r0 + warp + 1);
+    const int64_t begin = __shfl_sync(0xffffffffu, cuts, warp), end = __shfl_sync(0xffffffffu, cuts, warp + 1);
     // the cursor of the copies
     int iseq = sm.at_seq[warp], isub = sm.at_sub[warp], ij = sm.at_block[warp];
     int seq = iseq, sub = isub, j = ij;  // and of the steps
@@ -256,7 +257,15 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
     int ids = -1, window = -1;
     int64_t ahead = begin;
     const uint32_t ring = smem_u32(sm.ring[warp]);
-    int* const live = reinterpret_cast<int*>(sm.ring[warp][0] + 2 * kI8Codes + 32);  // (of stage s: kDecStage further)
+    uint32_t live = 0u;  // bit s: stage s has a block of the pool
+    const uint32_t stride = (uint32_t)a.Hkv * kI8Page;  // bytes between blocks of a head
+    const uint8_t *kbase = nullptr, *vbase = nullptr;   // the lane's part of block 0 of the copies' KV head
+    auto head_of_copies = [&] {
+      const int64_t o = (int64_t)(isub / igroups) * kI8Page + 16 * lane;
+      kbase = a.kpool + o;
+      vbase = a.vpool + o;
+    };
+    head_of_copies();
     const uint32_t dst = (uint32_t)((lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4));      // records lane / 8 + 8 i
     const uint32_t dst4 = (uint32_t)(((lane >> 3) + 4) * 128 + (((lane & 7) ^ ((lane >> 3) + 4)) << 4));  // and the fourth after
     auto issue = [&](int stage) {
@@ -268,29 +277,29 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
         }
         const int id = __shfl_sync(0xffffffffu, ids, ij & 31);
         const bool ok = id >= 0 && id < a.num_blocks;
-        if (!ok && lane == 0) flag_status(a.status, TQ_DEV_BAD_BLOCK);
         if (ok) {
-          const int64_t page = ((int64_t)id * a.Hkv + isub / igroups) * kI8Page;
-          const uint8_t* k = a.kpool + page + 16 * lane;
-          const uint8_t* v = a.vpool + page + 16 * lane;
-          const uint32_t s = ring + (uint32_t)stage * kDecStage;
-          copy16(s + dst, k);
-          copy16(s + dst4, k + 512);
-          copy16(s + dst + 1024, k + 1024);
-          copy16(s + dst4 + 1024, k + 1536);
-          copy16(s + 2048 + dst, v);
-          copy16(s + 2048 + dst4, v + 512);
-          copy16(s + 2048 + dst + 1024, v + 1024);
-          copy16(s + 2048 + dst4 + 1024, v + 1536);
-          if (lane == 0) copy16(s + 4096, k + kI8Codes);
-          if (lane == 1) copy16(s + 4112, v + kI8Codes - 16);
+          const uint8_t* k = kbase + (uint64_t)(uint32_t)id * stride;
+          const uint8_t* v = vbase + (uint64_t)(uint32_t)id * stride;
+          const uint32_t to = ring + (uint32_t)stage * kDecStage;
+          copy16(to + dst, k);
+          copy16(to + dst4, k + 512);
+          copy16(to + dst + 1024, k + 1024);
+          copy16(to + dst4 + 1024, k + 1536);
+          copy16(to + 2048 + dst, v);
+          copy16(to + 2048 + dst4, v + 512);
+          copy16(to + 2048 + dst + 1024, v + 1024);
+          copy16(to + 2048 + dst4 + 1024, v + 1536);
+          if (lane < 2) copy16(to + 4096 + 16 * lane, (lane ? v - 16 : k) + kI8Codes);
+        } else if (lane == 0) {
+          flag_status(a.status, TQ_DEV_BAD_BLOCK);
         }
-        if (lane == 0) live[stage * (kDecStage / 4)] = ok ? 1 : 0;
+        live = (live & ~(1u << stage)) | (ok ? 1u << stage : 0u);
         ++ahead;
         if (++ij == in) {
           ij = 0;
           window = -1;
-          if (++isub == igroups * a.Hkv) {
+          ++isub;
+          if (isub == igroups * a.Hkv) {
             isub = 0;
             if (ahead < end) {
               do {
@@ -300,6 +309,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
               } while (in == 0);
             }
           }
+          head_of_copies();
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
@@ -381,7 +391,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
       asm volatile("cp.async.wait_group 1;" ::: "memory");
       __syncwarp();
       const uint32_t pages = ring + (uint32_t)stage * kDecStage;
-      if (live[stage * (kDecStage / 4)]) {
+      if ((live >> stage) & 1u) {
         const I8Tail* tails = reinterpret_cast<const I8Tail*>(sm.ring[warp][stage] + 2 * kI8Codes);
         const float kstep = tails[0].step, vstep = tails[1].step;
         const uint32_t kbad = tails[0].bad, vbad = tails[1].bad;
