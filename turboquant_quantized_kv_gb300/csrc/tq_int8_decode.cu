@@ -12,7 +12,7 @@
 // shared memory, CTAs that share one (at most one unit begins in a CTA and goes on behind it) in the
 // workspace, where the CTA that arrives last joins the partials in the order of the line.
 //
-// A step.  A warp has the block's two pages (4 KB) copied into its ring two blocks ahead, 16-byte chunk c
+// A step.  A warp has the block's two pages (4 KB) copied into its ring two or three blocks ahead, 16-byte chunk c
 // of record r at c ^ (r & 7), so that all 128-bit reads are free of conflicts.  Codes become fp16 exactly
 // (i8_pair) and both products run as mma.sync m16n8k16 with fp32 sums:
 //     S [16 tokens x 8 columns] = K Q^T,  O^T [128 x 8 columns] += V^T P^T;
@@ -32,9 +32,12 @@
 namespace tq {
 namespace {
 
-constexpr int kDecWarps = 16;
-constexpr int kDecThreads = kDecWarps * 32;
-constexpr int kDecStages = 2;
+// Units of four rows: 16 warps of 128 registers, a ring of two blocks; of eight rows, with twice the operands of queries:
+// 12 warps of 168, a ring of three (4 sequences of 131,072 tokens, groups of eight: 194 us, with 16 warps 220).
+template <int NH>
+constexpr int kDecWarps = NH == 4 ? 16 : 12;
+template <int NH>
+constexpr int kDecStages = NH == 4 ? 2 : 3;
 constexpr int kDecStage = 2 * kI8Codes + 128;  // records of K, of V, both tails
 constexpr int kDecMinBlocks = 2;               // blocks a range at least
 constexpr int kPartRow = kD + 4;               // floats of a partial row in shared memory
@@ -71,7 +74,7 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -84,8 +87,11 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// Sixteen bytes to shared memory if `there`, without a branch around it.
+__device__ __forceinline__ void copy16_if(uint32_t dst, const void* src, bool there) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %2, 0;\n @p cp.async.cg.shared.global [%0], [%1], 16;\n}\n" ::"r"(dst), "l"(src),
+               "r"((int)there)
+               : "memory");
 }
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
   uint4 v;
@@ -117,26 +123,26 @@ __device__ __forceinline__ DecSeq dec_seq(const DecArgs& a, int b, bool flag) {
 
 template <int NH>  // rows of a unit: 4 or 8
 struct DecSmem {
-  alignas(128) unsigned char ring[kDecWarps][kDecStages][kDecStage];
-  float part[kDecWarps][NH][kPartRow];  // a warp's first segment, of a unit that began before
-  float2 ml[kDecWarps][2][8];           // references and denominators of the first and the last segment
-  int64_t unit0[kDecWarps][2];          // position in the line of the unit of either
-  int unit_seq[kDecWarps][2], unit_sub[kDecWarps][2];
-  int kind[kDecWarps];                  // bit 0: has a first segment, bit 1: which does not end its unit, bit 2: has a last one
-  int64_t sums[kDecWarps][2];
-  int at_seq[kDecWarps], at_sub[kDecWarps], at_block[kDecWarps];
+  alignas(128) unsigned char ring[kDecWarps<NH>][kDecStages<NH>][kDecStage];
+  float part[kDecWarps<NH>][NH][kPartRow];  // a warp's first segment, of a unit that began before
+  float2 ml[kDecWarps<NH>][2][8];           // references and denominators of the first and the last segment
+  int64_t unit0[kDecWarps<NH>][2];          // position in the line of the unit of either
+  int unit_seq[kDecWarps<NH>][2], unit_sub[kDecWarps<NH>][2];
+  int kind[kDecWarps<NH>];                  // bit 0: has a first segment, bit 1: which does not end its unit, bit 2: has a last one
+  int64_t sums[kDecWarps<NH>][2];
+  int at_seq[kDecWarps<NH>], at_sub[kDecWarps<NH>], at_block[kDecWarps<NH>];
   int arrived;
 };
 
 template <int NH>
-__global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_constant__ DecArgs a) {
+__global__ void __launch_bounds__(kDecWarps<NH> * 32, 1) k_int8_decode(const __grid_constant__ DecArgs a) {
   constexpr int HL = NH / 4;  // rows a lane has logits of: lane & 3 (of four), 2 (lane & 3) and the next (of eight)
   extern __shared__ __align__(128) unsigned char gen[];
   DecSmem<NH>& sm = *reinterpret_cast<DecSmem<NH>*>(gen);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lg = lane >> 2, lt = lane & 3;
 
   // ---- the line: steps before each thread's sequences, and in all
-  const int per = (a.seqs + kDecThreads - 1) / kDecThreads;
+  const int per = (a.seqs + (kDecWarps<NH> * 32) - 1) / (kDecWarps<NH> * 32);
   const int seq0 = min(a.seqs, (int)threadIdx.x * per), seq1 = min(a.seqs, seq0 + per);
   int64_t mine = 0, units = 0;
   for (int b = seq0; b < seq1; ++b) {
@@ -156,26 +162,26 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
     sm.sums[warp][0] = before;
     sm.sums[warp][1] = units;
   }
-  if (threadIdx.x < kDecWarps) sm.kind[threadIdx.x] = 0;
+  if (threadIdx.x < kDecWarps<NH>) sm.kind[threadIdx.x] = 0;
   __syncthreads();
   int64_t total = 0;
   before -= mine;
   units = 0;
 #pragma unroll
-  for (int w = 0; w < kDecWarps; ++w) {
+  for (int w = 0; w < kDecWarps<NH>; ++w) {
     if (w < warp) before += sm.sums[w][0];
     total += sm.sums[w][0];
     units += sm.sums[w][1];
   }
   // ---- ranges: R in all, `wide` of them a CTA
   int64_t most = (total + kDecMinBlocks - 1) / kDecMinBlocks;
-  int64_t want = (int64_t)gridDim.x * kDecWarps;
+  int64_t want = (int64_t)gridDim.x * kDecWarps<NH>;
   if (a.splits > 0) want = min(want, units * a.Hkv * a.splits);
   const int64_t R = most < 1 ? 1 : (most < want ? most : want);
-  const int wide = (int)min((int64_t)kDecWarps, max((int64_t)4, (R + gridDim.x - 1) / gridDim.x));
+  const int wide = (int)min((int64_t)kDecWarps<NH>, max((int64_t)4, (R + gridDim.x - 1) / gridDim.x));
   const int64_t r0 = (int64_t)blockIdx.x * wide;
   // lane w: where the CTA's range w begins
-  const int64_t cuts = total * min(r0 + min(lane, kDecWarps), R) / R;
+  const int64_t cuts = total * min(r0 + min(lane, kDecWarps<NH>), R) / R;
   for (int w = 0; w < wide; ++w) {
     const int64_t at = __shfl_sync(0xffffffffu, cuts, w);
     if (r0 + w >= R || at < before || at >= before + mine) continue;
@@ -193,7 +199,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
     }
   }
   // sequences without a token
-  for (int b = blockIdx.x + gridDim.x * warp; b < a.seqs; b += gridDim.x * kDecWarps) {
+  for (int b = blockIdx.x + gridDim.x * warp; b < a.seqs; b += gridDim.x * kDecWarps<NH>) {
     const DecSeq s = dec_seq(a, b, false);
     if (s.groups == 0 || s.blocks > 0) continue;
     for (int64_t i = lane; i < (int64_t)s.n * a.Hq * kD; i += 32) {
@@ -277,22 +283,19 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
         }
         const int id = __shfl_sync(0xffffffffu, ids, ij & 31);
         const bool ok = id >= 0 && id < a.num_blocks;
-        if (ok) {
-          const uint8_t* k = kbase + (uint64_t)(uint32_t)id * stride;
-          const uint8_t* v = vbase + (uint64_t)(uint32_t)id * stride;
-          const uint32_t to = ring + (uint32_t)stage * kDecStage;
-          copy16(to + dst, k);
-          copy16(to + dst4, k + 512);
-          copy16(to + dst + 1024, k + 1024);
-          copy16(to + dst4 + 1024, k + 1536);
-          copy16(to + 2048 + dst, v);
-          copy16(to + 2048 + dst4, v + 512);
-          copy16(to + 2048 + dst + 1024, v + 1024);
-          copy16(to + 2048 + dst4 + 1024, v + 1536);
-          if (lane < 2) copy16(to + 4096 + 16 * lane, (lane ? v - 16 : k) + kI8Codes);
-        } else if (lane == 0) {
-          flag_status(a.status, TQ_DEV_BAD_BLOCK);
-        }
+        const uint8_t* k = kbase + (uint64_t)(uint32_t)id * stride;
+        const uint8_t* v = vbase + (uint64_t)(uint32_t)id * stride;
+        const uint32_t to = ring + (uint32_t)stage * kDecStage;
+        copy16_if(to + dst, k, ok);
+        copy16_if(to + dst4, k + 512, ok);
+        copy16_if(to + dst + 1024, k + 1024, ok);
+        copy16_if(to + dst4 + 1024, k + 1536, ok);
+        copy16_if(to + 2048 + dst, v, ok);
+        copy16_if(to + 2048 + dst4, v + 512, ok);
+        copy16_if(to + 2048 + dst + 1024, v + 1024, ok);
+        copy16_if(to + 2048 + dst4 + 1024, v + 1536, ok);
+        copy16_if(to + 4096 + 16 * lane, (lane ? v - 16 : k) + kI8Codes, ok && lane < 2);
+        if (!ok && lane == 0) flag_status(a.status, TQ_DEV_BAD_BLOCK);
         live = (live & ~(1u << stage)) | (ok ? 1u << stage : 0u);
         ++ahead;
         if (++ij == in) {
@@ -314,8 +317,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    issue(0);
-    issue(1);
+#pragma unroll
+    for (int i = 0; i < kDecStages<NH>; ++i) issue(i);
 
     clear();
     uint32_t qh[8][2], ql[NH == 8 ? 8 : 1][2];
@@ -386,9 +389,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
     load_unit();
 
     bool began = j == 0;  // the segment begins its unit
+    int stage = 0;
     for (int64_t at = begin; at < end; ++at) {
-      const int stage = (int)((at - begin) & 1);
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      asm volatile("cp.async.wait_group %0;" ::"n"(kDecStages<NH> - 1) : "memory");
       __syncwarp();
       const uint32_t pages = ring + (uint32_t)stage * kDecStage;
       if ((live >> stage) & 1u) {
@@ -508,6 +511,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
       }
       __syncwarp();
       issue(stage);
+      stage = stage + 1 == kDecStages<NH> ? 0 : stage + 1;
       // ---- the end of a unit or of the range
       const bool last = at + 1 == end, done = j + 1 == s.blocks;
       if (done || last) {
@@ -687,7 +691,7 @@ cudaError_t run_decode(const DecArgs& a, int num_sms, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_release);
   }
-  k_int8_decode<NH><<<num_sms, kDecThreads, sizeof(DecSmem<NH>), st>>>(a);
+  k_int8_decode<NH><<<num_sms, kDecWarps<NH> * 32, sizeof(DecSmem<NH>), st>>>(a);
   count_launch();
   return cudaGetLastError();
 }
