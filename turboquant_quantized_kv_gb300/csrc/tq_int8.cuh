@@ -19,6 +19,10 @@ constexpr float kI8Least = 1.1754943508222875e-38f;  // 2^-126, the least step
 constexpr int kAttRows = 20;
 constexpr int kAttMostGroup = 256;  // query heads of a KV head, with more of them every sequence does the latter
 
+// Counters of a call in its workspace: the decode kernel's from 0 on, the tiles' from here on, one a CTA.
+constexpr int kAttCounters = 8192;
+static_assert(2 * kAttCounters * sizeof(int) <= kCounterRegionBytes, "the counter region");
+
 struct I8Tail {
   float step;
   uint32_t bad;       // bit r: record r is not a number

@@ -45,7 +45,7 @@ constexpr int kSoftWarps = 8, kProdWarps = 8;
 constexpr int kMmaWarp = kSoftWarps + kProdWarps;
 constexpr int kThreads = 640;  // (20 warps of 96 registers, dealt out again below)
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnitCost = 2;   // steps that the beginning and end of a unit are worth
+constexpr int kUnitCost = 3;   // steps that the beginning and end of a unit are worth (prompts of up to 4097 tokens: 2 434 us, 3 412, 4 425)
 constexpr uint32_t kPanel = kTile * 128;    // 128 rows of 64 16-bit elements, swizzled
 constexpr uint32_t kOperand = 2 * kPanel;
 constexpr int kSlots = 4;                   // tiles whose steps are kept
@@ -280,6 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
   const uint32_t base = smem_u32(gen);
   if (base & 1023u) {  // (uniform) the swizzled operands need it; the window starts so on sm_103a
     if (threadIdx.x == 0) flag_status(a.status, TQ_DEV_LAYOUT);
+    grid_dep_wait();
     return;
   }
   Misc& misc = *reinterpret_cast<Misc*>(gen + kOffMisc);
@@ -320,9 +321,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
     if (w < warp) before += sums[w];
     total += sums[w];
   }
-  if (total == 0) return;
   const int64_t R = total < gridDim.x ? total : gridDim.x;
-  if (blockIdx.x >= R) return;
+  if (blockIdx.x >= R) {  // (nothing, or nothing left)
+    grid_dep_wait();
+    return;
+  }
   const int64_t begin = total * blockIdx.x / R, end = total * (blockIdx.x + 1) / R;
   if (begin >= before && begin < before + mine) {
     int64_t left = begin - before;
@@ -643,7 +646,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
         // ---- the rows' values, out or to a partial, by lanes of a quad next to each other
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const float shift = C == -INFINITY ? 0.0f : C - m, half = truncf(0.5f * shift);
-        const float f0 = exp2f(half) * inv, f1 = exp2f(shift - half);
+        // (two factors where one would leave the range of exponents)
+        const bool far = __any_sync(0xffffffffu, !(fabsf(shift) < 100.0f));
+        const float f0 = far ? exp2f(half) * inv : exp2f(shift) * inv, f1 = far ? exp2f(shift - half) : 1.0f;
         const int64_t place = 2 * (int64_t)blockIdx.x + (step == 0 ? 1 : 0);
         if (!whole) a.ml[place * kUnitRows + r] = make_float2(m, l);
         const int quad = lane & 3;
@@ -661,17 +666,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
             const int t = ru[i] / a.g;
             o[i] = (int64_t)(u.s.first + u.tok0 + t) * a.o_row + (int64_t)(u.kvh * a.g + ru[i] - t * a.g) * a.o_head;
           }
-#pragma unroll 1
+          uint32_t all4[4][16];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld16x32_async(to + ((uint32_t)(16 * h) << 16) + 32 * c, all4[c]);
+#pragma unroll
           for (int c = 0; c < 4; ++c) {
-            uint32_t x[16];
-            tmem_ld16x32(to + ((uint32_t)(16 * h) << 16) + 32 * c, x);
+            uint32_t(&x)[16] = all4[c];
+            tmem_wait_ld16(x);
+            if (far) {
+#pragma unroll
+              for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * g1[(k >> 1) & 1]);
+            }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               float y[8];  // columns 32 c + 8 j + 2 quad and the next
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                y[2 * j] = __uint_as_float(x[4 * j + 2 * i]) * g0[i] * g1[i];
-                y[2 * j + 1] = __uint_as_float(x[4 * j + 2 * i + 1]) * g0[i] * g1[i];
+                y[2 * j] = __uint_as_float(x[4 * j + 2 * i]) * g0[i];
+                y[2 * j + 1] = __uint_as_float(x[4 * j + 2 * i + 1]) * g0[i];
               }
               if (!whole) {
                 float* p = a.part + (place * kUnitRows + ru[i]) * kD + 32 * c + 2 * quad;
@@ -740,42 +752,63 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
         }
         asm volatile("bar.sync 1, 256;" ::: "memory");
         if (misc.arrived) {
-          // a warp a row, a lane four coordinates
-          for (int row = warp; row < u.rows; row += kSoftWarps) {
-            auto place = [&](int64_t c) { return (2 * c + (c == c0 ? 1 : 0)) * kUnitRows + row; };
+          // a warp every eighth batch of 32 rows: references and denominators a lane a row, values a lane four
+          // coordinates of eight rows at a time
+          for (int row0 = 32 * warp; row0 < u.rows; row0 += 32 * kSoftWarps) {
+            auto place = [&](int64_t c) { return (2 * c + (c == c0 ? 1 : 0)) * kUnitRows + row0; };
             float M = -INFINITY, L = 0.0f;
-            for (int64_t c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(&a.ml[place(c)]).x);
-            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int64_t c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(&a.ml[place(c) + lane]).x);
             for (int64_t c = c0; c <= c1; ++c) {
-              const float2 e = __ldcg(&a.ml[place(c)]);
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part + place(c) * kD) + lane);
-              const float f = e.x == -INFINITY ? e.y : e.y * exp2f(e.x - M);
-              L += f;
-              x.x = fmaf(f, v.x, x.x);
-              x.y = fmaf(f, v.y, x.y);
-              x.z = fmaf(f, v.z, x.z);
-              x.w = fmaf(f, v.w, x.w);
+              const float2 e = __ldcg(&a.ml[place(c) + lane]);
+              L += e.x == -INFINITY ? e.y : e.y * exp2f(e.x - M);
             }
             const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-            const int t = row / a.g;
-            const int64_t o = (int64_t)(u.s.first + u.tok0 + t) * a.o_row + (int64_t)(u.kvh * a.g + row - t * a.g) * a.o_head + 4 * lane;
-            if (a.out_bf16) {
-              __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(a.out) + o;
-              const __nv_bfloat162 y = __floats2bfloat162_rn(x.x * inv, x.y * inv), z = __floats2bfloat162_rn(x.z * inv, x.w * inv);
-              if ((reinterpret_cast<uintptr_t>(p) & 7u) == 0u) {
-                *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&y), *reinterpret_cast<const uint32_t*>(&z));
-              } else {
-                p[0] = y.x;
-                p[1] = y.y;
-                p[2] = z.x;
-                p[3] = z.y;
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              if (row0 + 8 * q >= u.rows) break;
+              float4 x[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              for (int64_t c = c0; c <= c1; ++c) {
+                const float2 e = __ldcg(&a.ml[place(c) + lane]);
+                const float4* p = reinterpret_cast<const float4*>(a.part + (place(c) + 8 * q) * kD) + lane;
+                float4 v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = __ldcg(p + k * (kD / 4));
+                const float mine = (e.x == -INFINITY ? e.y : e.y * exp2f(e.x - M)) * inv;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const float f = __shfl_sync(0xffffffffu, mine, 8 * q + k);
+                  x[k].x = fmaf(f, v[k].x, x[k].x);
+                  x[k].y = fmaf(f, v[k].y, x[k].y);
+                  x[k].z = fmaf(f, v[k].z, x[k].z);
+                  x[k].w = fmaf(f, v[k].w, x[k].w);
+                }
               }
-            } else {
-              float* p = reinterpret_cast<float*>(a.out) + o;
-              p[0] = x.x * inv;
-              p[1] = x.y * inv;
-              p[2] = x.z * inv;
-              p[3] = x.w * inv;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const int row = row0 + 8 * q + k, t = row / a.g;
+                if (row >= u.rows) break;
+                const int64_t o = (int64_t)(u.s.first + u.tok0 + t) * a.o_row + (int64_t)(u.kvh * a.g + row - t * a.g) * a.o_head + 4 * lane;
+                if (a.out_bf16) {
+                  __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(a.out) + o;
+                  const __nv_bfloat162 y = __floats2bfloat162_rn(x[k].x, x[k].y), z = __floats2bfloat162_rn(x[k].z, x[k].w);
+                  if ((reinterpret_cast<uintptr_t>(p) & 7u) == 0u) {
+                    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&y), *reinterpret_cast<const uint32_t*>(&z));
+                  } else {
+                    p[0] = y.x;
+                    p[1] = y.y;
+                    p[2] = z.x;
+                    p[3] = z.y;
+                  }
+                } else {
+                  float* p = reinterpret_cast<float*>(a.out) + o;
+                  p[0] = x[k].x;
+                  p[1] = x[k].y;
+                  p[2] = x[k].z;
+                  p[3] = x[k].w;
+                }
+              }
             }
           }
         }
@@ -897,6 +930,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
     }
   } else {
     fewer_registers<kMmaRegs>();
+    if (warp > kMmaWarp) {  // the first unit's queries on their way to L2
+      const int width = kD * (a.q_bf16 ? 2 : 4);
+      for (int i = 32 * (warp - kMmaWarp - 1) + lane; i < u.rows * (width / 128); i += 96) {
+        const int r = i / (width / 128), t = r / a.g;
+        const uint8_t* p = reinterpret_cast<const uint8_t*>(a.q) +
+                           ((int64_t)(u.s.first + u.tok0 + t) * a.q_row + (int64_t)(u.kvh * a.g + r - t * a.g) * a.q_head) * (width / kD);
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p + 128 * (i - r * (width / 128))));
+      }
+    }
     if (warp == kMmaWarp) {
       // --------------------------------------------------------------- MMA
       const bool issue = elect_one();
@@ -980,6 +1022,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
     }
   }
   if (!ok && lane == 0) flag_status(a.status, TQ_DEV_WAIT_TIMEOUT);
+  // (the decode kernel runs beside this one, on other sequences; who follows finds both done)
+  grid_dep_wait();
   __syncwarp();
   tc_fence_before();
   __syncthreads();
@@ -1001,9 +1045,18 @@ cudaError_t run_tiles(const AttArgs& a, int num_sms, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_release);
   }
-  k_int8_attend<EXACT><<<num_sms, kThreads, kSmem, st>>>(a);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)num_sms);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;  // a dependent of this call's decode kernel
   count_launch();
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, k_int8_attend<EXACT>, a);
 }
 
 }  // namespace
@@ -1036,7 +1089,7 @@ cudaError_t launch_int8_tiles(const AttendCall& c, uint8_t* partials, int num_sm
   a.g = c.q->num_heads / d.num_kv_heads;
   a.per = kUnitRows / a.g;
   a.scale = c.sm_scale * 1.4426950408889634f;
-  a.counters = reinterpret_cast<int*>(c.workspace);
+  a.counters = reinterpret_cast<int*>(c.workspace) + kAttCounters;
   a.part = reinterpret_cast<float*>(partials);
   a.ml = reinterpret_cast<float2*>(partials + (size_t)2 * num_sms * kUnitRows * kD * sizeof(float));
   a.status = c.status;

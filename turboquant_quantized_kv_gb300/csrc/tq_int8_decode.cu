@@ -12,7 +12,7 @@
 // shared memory, CTAs that share one (at most one unit begins in a CTA and goes on behind it) in the
 // workspace, where the CTA that arrives last joins the partials in the order of the line.
 //
-// A step.  A warp has the block's two pages (4 KB) copied into its ring two or three blocks ahead, 16-byte chunk c
+// A step.  A warp has the block's two pages (4 KB) copied into its ring three blocks ahead, 16-byte chunk c
 // of record r at c ^ (r & 7), so that all 128-bit reads are free of conflicts.  Codes become fp16 exactly
 // (i8_pair) and both products run as mma.sync m16n8k16 with fp32 sums:
 //     S [16 tokens x 8 columns] = K Q^T,  O^T [128 x 8 columns] += V^T P^T;
@@ -32,12 +32,12 @@
 namespace tq {
 namespace {
 
-// Units of four rows: 16 warps of 128 registers, a ring of two blocks; of eight rows, with twice the operands of queries:
-// 12 warps of 168, a ring of three (4 sequences of 131,072 tokens, groups of eight: 194 us, with 16 warps 220).
-template <int NH>
-constexpr int kDecWarps = NH == 4 ? 16 : 12;
-template <int NH>
-constexpr int kDecStages = NH == 4 ? 2 : 3;
+// Registers count for more than warps: units of eight rows, with twice the operands of queries, spill in 16 warps of
+// 128 registers (4 sequences of 131,072 tokens, groups of eight: 220 us, 194 with 12 of 168); units of four
+// rows run the same either way (16 sequences of 8192 tokens: 67 us).
+constexpr int kDecWarps = 12;
+constexpr int kDecThreads = kDecWarps * 32;
+constexpr int kDecStages = 3;
 constexpr int kDecStage = 2 * kI8Codes + 128;  // records of K, of V, both tails
 constexpr int kDecMinBlocks = 2;               // blocks a range at least
 constexpr int kPartRow = kD + 4;               // floats of a partial row in shared memory
@@ -123,26 +123,27 @@ __device__ __forceinline__ DecSeq dec_seq(const DecArgs& a, int b, bool flag) {
 
 template <int NH>  // rows of a unit: 4 or 8
 struct DecSmem {
-  alignas(128) unsigned char ring[kDecWarps<NH>][kDecStages<NH>][kDecStage];
-  float part[kDecWarps<NH>][NH][kPartRow];  // a warp's first segment, of a unit that began before
-  float2 ml[kDecWarps<NH>][2][8];           // references and denominators of the first and the last segment
-  int64_t unit0[kDecWarps<NH>][2];          // position in the line of the unit of either
-  int unit_seq[kDecWarps<NH>][2], unit_sub[kDecWarps<NH>][2];
-  int kind[kDecWarps<NH>];                  // bit 0: has a first segment, bit 1: which does not end its unit, bit 2: has a last one
-  int64_t sums[kDecWarps<NH>][2];
-  int at_seq[kDecWarps<NH>], at_sub[kDecWarps<NH>], at_block[kDecWarps<NH>];
+  alignas(128) unsigned char ring[kDecWarps][kDecStages][kDecStage];
+  float part[kDecWarps][NH][kPartRow];  // a warp's first segment, of a unit that began before
+  float2 ml[kDecWarps][2][8];           // references and denominators of the first and the last segment
+  int64_t unit0[kDecWarps][2];          // position in the line of the unit of either
+  int unit_seq[kDecWarps][2], unit_sub[kDecWarps][2];
+  int kind[kDecWarps];                  // bit 0: has a first segment, bit 1: which does not end its unit, bit 2: has a last one
+  int64_t sums[kDecWarps][2];
+  int at_seq[kDecWarps], at_sub[kDecWarps], at_block[kDecWarps];
   int arrived;
 };
 
 template <int NH>
-__global__ void __launch_bounds__(kDecWarps<NH> * 32, 1) k_int8_decode(const __grid_constant__ DecArgs a) {
+__global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_constant__ DecArgs a) {
   constexpr int HL = NH / 4;  // rows a lane has logits of: lane & 3 (of four), 2 (lane & 3) and the next (of eight)
   extern __shared__ __align__(128) unsigned char gen[];
   DecSmem<NH>& sm = *reinterpret_cast<DecSmem<NH>*>(gen);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lg = lane >> 2, lt = lane & 3;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the tiles of tq_attend: other sequences)
 
   // ---- the line: steps before each thread's sequences, and in all
-  const int per = (a.seqs + (kDecWarps<NH> * 32) - 1) / (kDecWarps<NH> * 32);
+  const int per = (a.seqs + kDecThreads - 1) / kDecThreads;
   const int seq0 = min(a.seqs, (int)threadIdx.x * per), seq1 = min(a.seqs, seq0 + per);
   int64_t mine = 0, units = 0;
   for (int b = seq0; b < seq1; ++b) {
@@ -162,26 +163,26 @@ __global__ void __launch_bounds__(kDecWarps<NH> * 32, 1) k_int8_decode(const __g
     sm.sums[warp][0] = before;
     sm.sums[warp][1] = units;
   }
-  if (threadIdx.x < kDecWarps<NH>) sm.kind[threadIdx.x] = 0;
+  if (threadIdx.x < kDecWarps) sm.kind[threadIdx.x] = 0;
   __syncthreads();
   int64_t total = 0;
   before -= mine;
   units = 0;
 #pragma unroll
-  for (int w = 0; w < kDecWarps<NH>; ++w) {
+  for (int w = 0; w < kDecWarps; ++w) {
     if (w < warp) before += sm.sums[w][0];
     total += sm.sums[w][0];
     units += sm.sums[w][1];
   }
   // ---- ranges: R in all, `wide` of them a CTA
   int64_t most = (total + kDecMinBlocks - 1) / kDecMinBlocks;
-  int64_t want = (int64_t)gridDim.x * kDecWarps<NH>;
+  int64_t want = (int64_t)gridDim.x * kDecWarps;
   if (a.splits > 0) want = min(want, units * a.Hkv * a.splits);
   const int64_t R = most < 1 ? 1 : (most < want ? most : want);
-  const int wide = (int)min((int64_t)kDecWarps<NH>, max((int64_t)4, (R + gridDim.x - 1) / gridDim.x));
+  const int wide = (int)min((int64_t)kDecWarps, max((int64_t)4, (R + gridDim.x - 1) / gridDim.x));
   const int64_t r0 = (int64_t)blockIdx.x * wide;
   // lane w: where the CTA's range w begins
-  const int64_t cuts = total * min(r0 + min(lane, kDecWarps<NH>), R) / R;
+  const int64_t cuts = total * min(r0 + min(lane, kDecWarps), R) / R;
   for (int w = 0; w < wide; ++w) {
     const int64_t at = __shfl_sync(0xffffffffu, cuts, w);
     if (r0 + w >= R || at < before || at >= before + mine) continue;
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(kDecWarps<NH> * 32, 1) k_int8_decode(const __g
     }
   }
   // sequences without a token
-  for (int b = blockIdx.x + gridDim.x * warp; b < a.seqs; b += gridDim.x * kDecWarps<NH>) {
+  for (int b = blockIdx.x + gridDim.x * warp; b < a.seqs; b += gridDim.x * kDecWarps) {
     const DecSeq s = dec_seq(a, b, false);
     if (s.groups == 0 || s.blocks > 0) continue;
     for (int64_t i = lane; i < (int64_t)s.n * a.Hq * kD; i += 32) {
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(kDecWarps<NH> * 32, 1) k_int8_decode(const __g
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
-    for (int i = 0; i < kDecStages<NH>; ++i) issue(i);
+    for (int i = 0; i < kDecStages; ++i) issue(i);
 
     clear();
     uint32_t qh[8][2], ql[NH == 8 ? 8 : 1][2];
@@ -391,7 +392,7 @@ __global__ void __launch_bounds__(kDecWarps<NH> * 32, 1) k_int8_decode(const __g
     bool began = j == 0;  // the segment begins its unit
     int stage = 0;
     for (int64_t at = begin; at < end; ++at) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kDecStages<NH> - 1) : "memory");
+      asm volatile("cp.async.wait_group %0;" ::"n"(kDecStages - 1) : "memory");
       __syncwarp();
       const uint32_t pages = ring + (uint32_t)stage * kDecStage;
       if ((live >> stage) & 1u) {
@@ -511,7 +512,7 @@ __global__ void __launch_bounds__(kDecWarps<NH> * 32, 1) k_int8_decode(const __g
       }
       __syncwarp();
       issue(stage);
-      stage = stage + 1 == kDecStages<NH> ? 0 : stage + 1;
+      stage = stage + 1 == kDecStages ? 0 : stage + 1;
       // ---- the end of a unit or of the range
       const bool last = at + 1 == end, done = j + 1 == s.blocks;
       if (done || last) {
@@ -691,7 +692,7 @@ cudaError_t run_decode(const DecArgs& a, int num_sms, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_release);
   }
-  k_int8_decode<NH><<<num_sms, kDecWarps<NH> * 32, sizeof(DecSmem<NH>), st>>>(a);
+  k_int8_decode<NH><<<num_sms, kDecThreads, sizeof(DecSmem<NH>), st>>>(a);
   count_launch();
   return cudaGetLastError();
 }
