@@ -19,6 +19,10 @@
 // columns are four rows x (high part, low part) or eight rows in two passes, so that queries and weights
 // keep 22 bits.  A transpose in registers (movmatrix) brings P from the one layout to the other.
 //
+// Sums.  The tensor cores cut off what does not fit an accumulator: only a block's products are added there, low
+// parts first, the blocks outside, where sums round (fp32 queries, 64 ragged sequences: 1.8e-6 -> 3.3e-7 off, 3%
+// of the time).
+//
 // Scales.  With u = log2 of a weight, m a running reference (moved only when u exceeds it by 16) and T one
 // for weight times step of V, p = 2^(u - m) goes into the denominator and w = p step 2^(m - T) <= 2^15 into
 // the product, so that a block with large values that nobody attends costs the others nothing.
@@ -401,6 +405,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
         const uint32_t kbad = tails[0].bad, vbad = tails[1].bad;
         // ---- logits
         float S[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        [[maybe_unused]] float S1[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // the low parts'
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const uint32_t col = (uint32_t)(((2 * lt + c) ^ lg) << 4);
@@ -411,8 +416,12 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
             const uint32_t a0 = i8_pair(xw[i], 0x4140u), a1 = i8_pair(yw[i], 0x4140u), a2 = i8_pair(xw[i], 0x4342u),
                            a3 = i8_pair(yw[i], 0x4342u);
             mma_f16(S, a0, a1, a2, a3, qh[4 * c + i][0], qh[4 * c + i][1]);
-            if constexpr (NH == 8) mma_f16(S, a0, a1, a2, a3, ql[4 * c + i][0], ql[4 * c + i][1]);
+            if constexpr (NH == 8) mma_f16(S1, a0, a1, a2, a3, ql[4 * c + i][0], ql[4 * c + i][1]);
           }
+        }
+        if constexpr (NH == 8) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) S[k] += S1[k];
         }
         float u[HL][2];
         bool in0[HL], in1[HL];
@@ -506,8 +515,11 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
           const uint32_t sel = i & 1 ? 0x7362u : 0x5140u;
           const uint32_t x = prmt(rw[0][i >> 1], rw[1][i >> 1], sel), y = prmt(rw[2][i >> 1], rw[3][i >> 1], sel);
           const uint32_t a0 = i8_pair(x, 0x4140u), a1 = i8_pair(x, 0x4342u), a2 = i8_pair(y, 0x4140u), a3 = i8_pair(y, 0x4342u);
-          mma_f16(acc[i], a0, a1, a2, a3, ph[0], ph[1]);
-          if constexpr (NH == 8) mma_f16(acc[i], a0, a1, a2, a3, pl[0], pl[1]);
+          float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          if constexpr (NH == 8) mma_f16(t, a0, a1, a2, a3, pl[0], pl[1]);
+          mma_f16(t, a0, a1, a2, a3, ph[0], ph[1]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[i][k] += t[k];
         }
       }
       __syncwarp();
