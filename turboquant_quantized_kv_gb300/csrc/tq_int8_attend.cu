@@ -46,6 +46,11 @@ constexpr int kMmaWarp = kSoftWarps + kProdWarps;
 constexpr int kThreads = 640;  // (20 warps of 96 registers, dealt out again below)
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnitCost = 3;   // steps that the beginning and end of a unit are worth (prompts of up to 4097 tokens: 2 434 us, 3 412, 4 425)
+// A cut this near to a unit's beginning or end goes there: a part costs its CTAs some 10 us beyond its steps, which are
+// 2.3 to 3 us each (a chunk of 2048 tokens behind 30,000: 1.98 ms without, 1.84 so; with 9 1.83, but 24 sequences of 64
+// rows 125 us for 117).  At least kUnitCost, so that a part has steps.
+constexpr int kSnap = 4;
+static_assert(kSnap >= kUnitCost, "a part has steps");
 constexpr uint32_t kPanel = kTile * 128;    // 128 rows of 64 16-bit elements, swizzled
 constexpr uint32_t kOperand = 2 * kPanel;
 constexpr int kSlots = 4;                   // tiles whose steps are kept
@@ -68,6 +73,7 @@ struct Misc {
   uint32_t tmem;
   int arrived;
   int seq, kvh, tile, place;  // where the CTA's part begins
+  int64_t begin, end;
 };
 
 struct AttArgs {
@@ -326,26 +332,38 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
     grid_dep_wait();
     return;
   }
-  const int64_t begin = total * blockIdx.x / R, end = total * (blockIdx.x + 1) / R;
-  if (begin >= before && begin < before + mine) {
-    int64_t left = begin - before;
+  if (threadIdx.x == 0) misc.end = total;
+  __syncthreads();
+#pragma unroll 1
+  for (int e = 0; e < 2; ++e) {  // the part's beginning and its end, by the thread whose sequences hold them
+    const int64_t cut = total * (blockIdx.x + e) / R;
+    if (cut < before || cut >= before + mine) continue;
+    int64_t left = cut - before;
     for (int b = b0; b < b1; ++b) {
       const Seq s = seq_of(a, b, false);
       const int64_t n = length(s);
-      if (left < n * a.Hkv) {
-        misc.seq = b;
-        misc.kvh = (int)(left / n);
-        left %= n;
-        int k = 0;
-        for (int st = steps_of(a, s, 0) + kUnitCost; left >= st; st = steps_of(a, s, k) + kUnitCost) {
-          left -= st;
-          ++k;
-        }
-        misc.tile = k;
-        misc.place = (int)left;
-        break;
+      if (left >= n * a.Hkv) {
+        left -= n * a.Hkv;
+        continue;
       }
-      left -= n * a.Hkv;
+      const int kvh = (int)(left / n);
+      left %= n;
+      int k = 0, len = steps_of(a, s, 0) + kUnitCost;
+      for (; left >= len; len = steps_of(a, s, k) + kUnitCost) {
+        left -= len;
+        ++k;
+      }
+      const int place = left <= kSnap ? 0 : (len - left <= kSnap ? len : (int)left);
+      if (e) {
+        misc.end = cut - left + place;
+      } else {
+        misc.begin = cut - left + place;
+        misc.seq = b;
+        misc.kvh = kvh;
+        misc.tile = k;
+        misc.place = place;
+      }
+      break;
     }
   }
   if (threadIdx.x == 0) {
@@ -378,7 +396,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
   u.place = misc.place;
   u.s = seq_of(a, u.seq, false);
   u.look(a);
-  int64_t at = begin;
+  int64_t at = misc.begin;
+  const int64_t end = misc.end;
+  if (at < end && u.place == u.all + kUnitCost) u.next(a);
   bool ok = true;  // no wait gave up
   int done0 = 0, units = 0;  // steps and units so far
 
@@ -389,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
     const uint32_t ts = tmem + (uint32_t)(st * kTile) + ((uint32_t)(32 * w) << 16);
     const uint32_t to = tmem + (uint32_t)((2 + st) * kTile) + ((uint32_t)(32 * w) << 16);
     int done = 0, turns = 0;  // steps and units of the stream so far
-    while (true) {
+    while (at < end) {
       int step, n;
       const int places = u.part(end - at, &step, &n);
       const bool part_of_it = n > 0 && (st == 0 || u.rows > kTile);
@@ -741,7 +761,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
       if (n > 0 && !whole) {
         // ---- the unit's other parts (by the softmax warps alone, whether waits gave up or not)
         auto cta_of = [&](int64_t p) { return ((p + 1) * R - 1) / total; };
-        const int64_t unit0 = at - u.place, c0 = cta_of(unit0 + kUnitCost), c1 = cta_of(unit0 + u.all + kUnitCost - 1);
+        // (the last CTA that begins at the unit or before, and the last that begins before its end: see kSnap)
+        const int64_t unit0 = at - u.place, c0 = cta_of(unit0 + kSnap), c1 = max(c0, cta_of(unit0 + u.all + kUnitCost - kSnap - 1));
         __threadfence();
         asm volatile("bar.sync 1, 256;" ::: "memory");
         if (threadIdx.x == 0) {
@@ -831,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
     const uint32_t op = values ? v_op : k_op;
     uint64_t *const full = values ? vfull : kfull, *const empty = values ? vempty : kempty;
     const int sbit = values ? vbit : 1;
-    while (ok) {
+    while (ok && at < end) {
       int step, n;
       const int places = u.part(end - at, &step, &n);
       if (n > 0) {
@@ -930,7 +951,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
     }
   } else {
     fewer_registers<kMmaRegs>();
-    if (warp > kMmaWarp) {  // the first unit's queries on their way to L2
+    if (warp > kMmaWarp && at < end) {  // the first unit's queries on their way to L2
       const int width = kD * (a.q_bf16 ? 2 : 4);
       for (int i = 32 * (warp - kMmaWarp - 1) + lane; i < u.rows * (width / 128); i += 96) {
         const int r = i / (width / 128), t = r / a.g;
@@ -946,7 +967,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
       constexpr uint32_t idesc_s = umma_idesc_16(false, false, kTile, kTile), idesc_o = umma_idesc_16(false, true, kTile, kTile);
       const uint64_t dq = umma_desc_sw128(base), dk = umma_desc_sw128(k_op), dv = umma_desc_sw128_mn(v_op, kPanel);
       int done1 = 0;  // steps of the second stream so far
-      while (ok) {
+      while (ok && at < end) {
         int step, n;
         const int places = u.part(end - at, &step, &n);
         const bool two = u.rows > kTile;
