@@ -64,7 +64,8 @@ def test_attend_refusals(tqlib, layer):
                 dict(table=None), dict(width=0), dict(lens=None), dict(scale=float("nan")), dict(out=None), dict(inp=None),
                 dict(out=x.data_ptr() + 2), dict(inp=x.data_ptr() + 1)):
         assert call(**bad) == tqlib.TQ_ERR_INVALID_ARG, bad
-    assert call(n=(1 << 26) + 1) == tqlib.TQ_ERR_UNSUPPORTED and call(batch=65536) == tqlib.TQ_ERR_UNSUPPORTED
+    for big in (dict(n=(1 << 26) + 1), dict(batch=65536), dict(heads=(1 << 16) + 2), dict(n=1 << 20, heads=1 << 12), dict(width=1 << 27)):
+        assert call(**big) == tqlib.TQ_ERR_UNSUPPORTED, big
     assert call(n=0) == tqlib.TQ_OK and call(batch=0) == tqlib.TQ_OK
     assert tqlib.lib().tq_attend_workspace_bytes(ctypes.byref(other.desc), 4, 1, 2, 1) == 0
 
