@@ -102,6 +102,10 @@ def test_block_refusals(tqlib, layer):
         assert lib.tq_blocks_release(ref(pool), ref(bad), None, None) == TQ.TQ_ERR_INVALID_ARG
         assert lib.tq_blocks_reorder(ref(pool), None, 0, ref(rows), at, ref(bad), None) == TQ.TQ_ERR_INVALID_ARG
         assert lib.tq_blocks_compact(ref(pool), None, 0, ref(bad), 1, None, None, None) == TQ.TQ_ERR_INVALID_ARG
+    huge = BlockRows(at, at + 1024, 1 << 16, 1 << 15)
+    pool_huge = BlockPool(4, at, at + 4096, lib.tq_blocks_workspace_bytes(4, 1 << 16))
+    assert lib.tq_blocks_extend(ref(pool_huge), ref(huge), at, None) == TQ.TQ_ERR_UNSUPPORTED
+    assert lib.tq_blocks_reorder(ref(pool_huge), None, 0, ref(huge), at, ref(rows), None) == TQ.TQ_ERR_UNSUPPORTED
     assert lib.tq_blocks_extend(ref(pool), ref(rows), None, None) == TQ.TQ_ERR_INVALID_ARG
     # old and new rows in the same memory, tables of other widths, a cache twice, a layer of another size
     assert lib.tq_blocks_reorder(ref(pool), None, 0, ref(rows), at, ref(rows), None) == TQ.TQ_ERR_INVALID_ARG

@@ -478,6 +478,8 @@ tq_status check_rows(const tq_block_rows* r, const char* fn, const char* what) {
   if (r->rows < 0 || r->rows > (1 << 20)) return fail(TQ_ERR_INVALID_ARG, "%s: %s: %d rows", fn, what, r->rows);
   if (r->max_blocks < 1 || r->max_blocks > INT32_MAX / TQ_BLOCK_SIZE)
     return fail(TQ_ERR_INVALID_ARG, "%s: %s: max_blocks %d", fn, what, r->max_blocks);
+  if ((int64_t)r->rows * r->max_blocks > INT32_MAX)  // (ranks of entries are ints)
+    return fail(TQ_ERR_UNSUPPORTED, "%s: %s: a table of %d x %d entries", fn, what, r->rows, r->max_blocks);
   if (r->rows > 0 && (!r->table || !r->lens)) return fail(TQ_ERR_INVALID_ARG, "%s: %s: null table/lens", fn, what);
   return TQ_OK;
 }
