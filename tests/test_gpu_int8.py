@@ -86,6 +86,25 @@ def test_append_bit_by_bit(cuda, tqlib, n, heads, kind, dtype):
     assert tqlib.get_device_status() == 0
 
 
+@pytest.mark.parametrize("n,heads,kind", [(1024, 2, "time"), (1025, 4, "time"), (1030, 1, "any"), (4096, 5, "time"),
+                                          (4097, 4, "time"), (4100, 2, "sequence")])
+def test_append_at_once(cuda, tqlib, n, heads, kind):
+    """One call of tokens around the sizes where tokens go to CTAs in other numbers, slots given twice and skipped ones among them."""
+    blocks = n // BLOCK + 10
+    slots = orders(kind, 3 * n, n, blocks)
+    g = np.random.default_rng(n)
+    slots[g.integers(0, n, n // 9)] = -1
+    slots[n // 2 :: 7] = slots[1 : n - n // 2 + 1 : 7]
+    layer, want = layer_of(tqlib, blocks, heads), [blank(blocks, heads), blank(blocks, heads)]
+    k, v = data(cuda, n, n, heads), data(cuda, n + 1, n, heads)
+    layer.append(k, v, cuda.from_numpy(slots.astype(np.int64)).cuda())
+    touched = np.unique(slots[slots >= 0] // BLOCK)
+    for w, x in ((0, k), (1, v)):
+        ref.append(*want[w], host(x), slots)
+        assert_pages(layer, want[w], w, touched)
+    assert tqlib.get_device_status() == 0
+
+
 def test_append_token_by_token(cuda, tqlib):
     """Sixteen decode steps into one block a sequence: the step grows, earlier codes are rounded again."""
     B, H = 5, 2

@@ -10,7 +10,8 @@
 //   extend   k_extend
 //   compact  k_lists (who moves where), k_move (pages, all layers, and the tables)
 // The pages are the bytes that count: a part is one pool (keys or values) of one layer, and a CTA copies
-// one block of one part at a time, 16 bytes a thread and load.
+// one block of one part at a time, 16 bytes a thread and load.  105 MB of pages, read and written, take
+// k_move 35 us (31 at the rate of a copy); a reordering without copies is two launches, 7 us at 16 rows, 34 at 4096.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -23,7 +24,8 @@ namespace tq {
 namespace {
 
 constexpr int kMaxParts = 128;   // pools a launch: 64 layers
-constexpr int kFewRows = 4096;   // rows whose children are found without a kernel of their own
+// Rows whose children are found without a kernel of their own (16 rows 7.0 us, 8.0 with it; 4096 33.6 and 34.5).
+constexpr int kFewRows = 4096;
 
 struct Part {
   uint8_t* pool;

@@ -9,6 +9,11 @@
 // Both roundings are those of the exact quotient, whatever the order of operations: the fp32 product with
 // 1 / s is off by less than 2^-16 of a code, and where it lies that near to the middle between two codes, the
 // sign of x - middle * s decides, which one fused product gives exactly.
+//
+// Bound.  A value is read once and its code written once: 4 + 2 bytes a coordinate of key and value in bf16.  131,072
+// tokens x 8 heads take 198 us in bf16 (4.0 TB/s) and 291 in fp32 (4.6): a warp has a page's sixteen records in
+// registers from the search for the largest to the codes, which keeps few warps on an SM, so loads
+// and arithmetic alternate.  Small calls are one or three launches' latency: 64 tokens 6 us, 1024 15, 4096 25.
 #include "tq_async.cuh"
 #include "tq_int8.cuh"
 
@@ -17,9 +22,14 @@ namespace {
 
 constexpr int kAppWarps = 16;  // of a CTA at most
 constexpr int kAppChunk = 64;  // tokens of a CTA at most
-// Tokens up to which a CTA looks for the other tokens of its blocks itself.  Beyond, two passes over the
-// slots leave the tokens of a block in its own page first.
-constexpr int kScanMost = 2048;
+// Tokens up to which a CTA looks for the other tokens of its blocks itself, and has one token.  Beyond, two passes
+// over the slots leave the tokens of a block in its own page first (8 heads, bf16, a prompt / 64 sequences in turn:
+// 608 tokens 14 / 11 us so, 18 / 19 with the passes; 1024 16 / 17 and 19 / 20; 2048 26 / 23 and 22 / 23).
+constexpr int kScanMost = 1024;
+// Tokens x heads up to which CTAs have few tokens, for sequences in turn, where each token of a CTA may own a block
+// (8 heads, 4096 tokens: 25 / 26 us with four tokens a CTA, 21 / 64 with sixteen; 16,384: 46 / 51 and 37 / 84; one
+// head, 16,384 tokens: 17 / 18 with eight, 14 / 38 with 64).
+constexpr int kTurnMost = 32768;
 
 struct AppendArgs {
   const void* x[2];   // keys, values (null: none)
@@ -177,7 +187,7 @@ __device__ __forceinline__ void append_page(const T* x, int64_t stride, uint8_t*
 // A block belongs to one of its tokens, that of the least key: a record that a hash of the block picks, if the
 // call writes it, or else the next one that it writes; of a slot given twice the later token.  A CTA takes
 // the blocks that belong to its `chunk` tokens: one a CTA on average, for prompts token by token as for
-// sequences in turn (16,384 tokens of 64 sequences in turn: 158 us with the first token for all, 42 so).
+// sequences in turn (16,384 tokens of 64 sequences in turn: 158 us with the first token for all, 84 so).
 __device__ __forceinline__ uint32_t key_of(int block, int record, int t) {
   return (((uint32_t)record - ((uint32_t)block * 0x9E3779B1u >> 28)) & 15u) << 28 | (0x0FFFFFFEu - (uint32_t)t);
 }
@@ -351,11 +361,11 @@ cudaError_t launch_int8_append(const tq_cache_desc& d, const void* k, const void
   a.max_slot = d.num_blocks * kBlock;
   a.status = status;
   a.marked = n_tok > kScanMost ? 1 : 0;
-  // a warp a page: CTAs of 16 tokens (a block, in a prompt) or of more where a block has few heads; with few tokens
-  // each has a CTA
-  const bool few = n_tok <= 2 * num_sms;
-  a.chunk = few ? 1 : kBlock * (a.Hkv < 4 ? 4 / a.Hkv : 1);
-  const int threads = few ? kAppWarps * 32 : 256;
+  // a warp a page: CTAs of 16 tokens (a block, in a prompt) or of more where a block has few heads; smaller ones up to
+  // kTurnMost, of one token up to kScanMost
+  const bool few_heads = a.Hkv < 4;
+  a.chunk = !a.marked ? 1 : (n_tok * a.Hkv <= kTurnMost ? (few_heads ? 8 : 4) : kBlock * (few_heads ? 4 / a.Hkv : 1));
+  const int threads = a.marked ? 256 : kAppWarps * 32;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
