@@ -47,8 +47,8 @@ constexpr int kThreads = 640;  // (20 warps of 96 registers, dealt out again bel
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnitCost = 3;   // steps that the beginning and end of a unit are worth (prompts of up to 4097 tokens: 2 434 us, 3 412, 4 425)
 // A cut this near to a unit's beginning or end goes there: a part costs its CTAs some 10 us beyond its steps, which are
-// 2.3 to 3 us each (a chunk of 2048 tokens behind 30,000: 1.98 ms without, 1.84 so; with 9 1.83, but 24 sequences of 64
-// rows 125 us for 117).  At least kUnitCost, so that a part has steps.
+// 2 to 3 us each (prompts of up to 4097 tokens 405 us without, 393 so, 390 with 6; 64 sequences of up to 128 tokens behind
+// 2000 183, 175, 173; 24 of up to 16 behind 3000 65, 67, 70).  At least kUnitCost, so that a part has steps.
 constexpr int kSnap = 4;
 static_assert(kSnap >= kUnitCost, "a part has steps");
 constexpr uint32_t kPanel = kTile * 128;    // 128 rows of 64 16-bit elements, swizzled
