@@ -17,7 +17,8 @@
 // (i8_pair) and both products run as mma.sync m16n8k16 with fp32 sums:
 //     S [16 tokens x 8 columns] = K Q^T,  O^T [128 x 8 columns] += V^T P^T;
 // columns are four rows x (high part, low part) or eight rows in two passes, so that queries and weights
-// keep 22 bits.  A transpose in registers (movmatrix) brings P from the one layout to the other.
+// keep 22 bits.  bf16 queries, scaled by a power of two alone, need no low part (but for what lies 2^-25 below
+// a row's largest): units of eight go without (24 sequences of up to 5 tokens 54 -> 52 us, 64 ragged ones 164 -> 158).  A transpose in registers (movmatrix) brings P from the one layout to the other.
 //
 // Sums.  The tensor cores cut off what does not fit an accumulator: only a block's products are added there, low
 // parts first, the blocks outside, where sums round (fp32 queries, 64 ragged sequences: 1.8e-6 -> 3.3e-7 off, 3%
@@ -138,7 +139,7 @@ struct DecSmem {
   int arrived;
 };
 
-template <int NH>
+template <int NH, bool LOW>  // rows of a unit; LOW: their queries have low parts
 __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_constant__ DecArgs a) {
   constexpr int HL = NH / 4;  // rows a lane has logits of: lane & 3 (of four), 2 (lane & 3) and the next (of eight)
   extern __shared__ __align__(128) unsigned char gen[];
@@ -326,7 +327,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
     for (int i = 0; i < kDecStages; ++i) issue(i);
 
     clear();
-    uint32_t qh[8][2], ql[NH == 8 ? 8 : 1][2];
+    uint32_t qh[8][2];
+    [[maybe_unused]] uint32_t ql[NH == 8 && LOW ? 8 : 1][2];
     float cq[HL];
     int lim[HL];  // tokens that the lane's rows attend to
     auto load_unit = [&] {  // queries of the unit as operands: column lg, coordinates 32 lt + 4 i .. + 3 in step i
@@ -361,7 +363,6 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
       uint32_t top = 0u;
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        x[i] *= a.scale;
         top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
       }
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -370,7 +371,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
       const int e = max((int)(top >> 23) - 126, -110);
       const bool fine = top < 0x7F800000u;
       const float f = __uint_as_float((uint32_t)(127 + 8 - min(e, 128)) << 23);
-      const float back = fine ? __uint_as_float((uint32_t)(127 + e - 8) << 23) : CUDART_NAN_F;
+      const float back = fine ? __uint_as_float((uint32_t)(127 + e - 8) << 23) * a.scale : CUDART_NAN_F;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
 #pragma unroll
@@ -383,7 +384,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
             qh[i][k] = lg & 1 ? lo : hi;
           } else {
             qh[i][k] = hi;
-            ql[i][k] = lo;
+            if constexpr (LOW) ql[i][k] = lo;
           }
         }
       }
@@ -416,10 +417,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
             const uint32_t a0 = i8_pair(xw[i], 0x4140u), a1 = i8_pair(yw[i], 0x4140u), a2 = i8_pair(xw[i], 0x4342u),
                            a3 = i8_pair(yw[i], 0x4342u);
             mma_f16(S, a0, a1, a2, a3, qh[4 * c + i][0], qh[4 * c + i][1]);
-            if constexpr (NH == 8) mma_f16(S1, a0, a1, a2, a3, ql[4 * c + i][0], ql[4 * c + i][1]);
+            if constexpr (NH == 8 && LOW) mma_f16(S1, a0, a1, a2, a3, ql[4 * c + i][0], ql[4 * c + i][1]);
           }
         }
-        if constexpr (NH == 8) {
+        if constexpr (NH == 8 && LOW) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) S[k] += S1[k];
         }
@@ -692,7 +693,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
   }
 }
 
-template <int NH>
+template <int NH, bool LOW>
 cudaError_t run_decode(const DecArgs& a, int num_sms, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};  // devices (up to 64) whose kernel has its shared memory
   int dev = 0;
@@ -700,11 +701,11 @@ cudaError_t run_decode(const DecArgs& a, int num_sms, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(ready.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(k_int8_decode<NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(DecSmem<NH>));
+    e = cudaFuncSetAttribute(k_int8_decode<NH, LOW>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(DecSmem<NH>));
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_release);
   }
-  k_int8_decode<NH><<<num_sms, kDecThreads, sizeof(DecSmem<NH>), st>>>(a);
+  k_int8_decode<NH, LOW><<<num_sms, kDecThreads, sizeof(DecSmem<NH>), st>>>(a);
   count_launch();
   return cudaGetLastError();
 }
@@ -722,7 +723,8 @@ static cudaError_t launch_rows(const tq_cache_desc& d, DecArgs& a, bool few, uin
   a.counters = reinterpret_cast<int*>(workspace);
   a.part = reinterpret_cast<float*>(workspace + kCounterRegionBytes);
   a.ml = reinterpret_cast<float2*>(a.part + (size_t)2 * num_sms * 8 * kD);
-  return few ? run_decode<4>(a, num_sms, st) : run_decode<8>(a, num_sms, st);
+  if (few) return run_decode<4, true>(a, num_sms, st);
+  return a.q_bf16 ? run_decode<8, false>(a, num_sms, st) : run_decode<8, true>(a, num_sms, st);
 }
 
 cudaError_t launch_int8_decode(const DecodeCall& c, int num_sms, cudaStream_t st) {
