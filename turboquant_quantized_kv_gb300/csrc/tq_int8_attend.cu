@@ -26,6 +26,11 @@
 // reference of a row's log2-logits u and C one of weight times step of V, both of what the row attends to,
 //     e = 2^(u - m),  denominator += e,  P = e step 2^(m - C) <= 2^14,
 // so that a block of large values costs a row nothing unless it attends to them.  P is fp16 (half a step 2^-11), for fp32 queries in two parts as well.
+//
+// Bound.  A chunk of 2048 tokens behind 30,000 (64/8 heads) 1.81 ms, 1.15 PFLOP/s; prompts of up to 4097 tokens (32/8
+// heads) 407 us, 0.5 PFLOP/s.  A step of both streams is 2048 clocks of the tensor cores and takes some 3000: each
+// stream's chain of logits (512), softmax (1700) and weights times values (512).  Short units pay 5.5 us at
+// their end and 3.3 at their first step beside it.
 #include <math_constants.h>
 
 #include <atomic>

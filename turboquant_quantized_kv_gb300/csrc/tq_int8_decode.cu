@@ -27,6 +27,10 @@
 // Scales.  With u = log2 of a weight, m a running reference (moved only when u exceeds it by 16) and T one
 // for weight times step of V, p = 2^(u - m) goes into the denominator and w = p step 2^(m - T) <= 2^15 into
 // the product, so that a block with large values that nobody attends costs the others nothing.
+//
+// Bound.  16 sequences of 8192 tokens (32/8 heads) 67 us, 40 of them the pages at the rate of a copy: the loop runs at 5.1
+// TB/s, some 14 us are the kernel's beginning and end.  Groups of eight are bound by a block's 450 warp
+// instructions: 4 sequences of 131,072 tokens 194 us (159 at the rate of a copy), 64 ragged ones in fp32 159 (97).
 #include <math_constants.h>
 
 #include <atomic>
