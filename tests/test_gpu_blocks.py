@@ -274,3 +274,48 @@ def test_captured_and_other_stream(cuda, tqlib):
     assert np.array_equal(n.cpu().numpy(), mt)
     check(cuda, blocks, layers, model)
     assert tqlib.get_device_status() == 0
+
+
+def test_captured_before_any_call(cuda, tqlib):
+    """The first calls of an object are captured, in memory that an earlier graph left full of other bytes: calls outside the
+    graph, before its first replay and after it, have a workspace of their own."""
+    g, layers, model, blocks, table, lens, t = start(cuda, tqlib, 17, 8, 5, 200, FORMATS[:1])
+    blocks = tqlib.Blocks(200)  # (without a workspace yet)
+    lens = np.minimum(lens, 60).astype(np.int32)
+    refs0 = np.zeros(200, np.int32)
+    for b in range(8):
+        for j in range(-(-lens[b] // BLOCK)):
+            refs0[table[b, j]] += 1
+    parents = g.integers(0, 8, 16).astype(np.int32)
+    d = dict(t=t, lens=dev(cuda, lens), parents=dev(cuda, parents), refs=dev(cuda, refs0))
+    cuda.cuda.synchronize()
+    first, graph = cuda.cuda.CUDAGraph(), cuda.cuda.CUDAGraph()
+    with cuda.cuda.graph(first):
+        full = [cuda.full((8192,), 0x55, dtype=cuda.uint8, device="cuda") for _ in range(240)]
+        del full
+    first.replay()
+    with cuda.cuda.graph(graph, pool=first.pool()):
+        blocks.refs.copy_(d["refs"])
+        n, nl = blocks.reorder(layers, d["t"], d["lens"], d["parents"])
+        blocks.extend(n, nl, nl + 1)
+    pages = host_pages(layers, 200)
+    model = Model(200, pages)
+
+    def want():
+        model.refs[:] = refs0
+        mt, ml = model.reorder(table, lens, parents)
+        model.extend(mt, ml, ml + 1)
+        return mt, ml
+
+    for replay in (False, True, False):
+        if replay:
+            graph.replay()
+            got = n, nl
+        else:
+            blocks.refs.copy_(d["refs"])
+            got = blocks.reorder(layers, d["t"], d["lens"], d["parents"])
+            blocks.extend(got[0], got[1], got[1] + 1)
+        mt, ml = want()
+        assert np.array_equal(got[0].cpu().numpy(), mt) and np.array_equal(got[1].cpu().numpy(), ml)
+        check(cuda, blocks, layers, model)
+    assert tqlib.get_device_status() == 0

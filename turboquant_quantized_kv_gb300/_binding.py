@@ -250,6 +250,14 @@ def _new(make, shape, dtype, device, stream):
         return make(shape, dtype=dtype, device=device)
 
 
+def _capturing(stream):
+    torch = _torch()
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 _byref = ctypes.byref
 
 
@@ -788,7 +796,10 @@ class Blocks:
             refs = _index_ptr(self.refs, "refs", torch.int32, (self.num_blocks,))
             ws = _new(torch.zeros, (int(size),), torch.uint8, self.refs.device, stream)
             self._workspaces.append(ws)
-            self._rows, self._pool_ref = rows, _byref(BlockPool(self.num_blocks, refs, ws.data_ptr(), ws.numel()))
+            pool = _byref(BlockPool(self.num_blocks, refs, ws.data_ptr(), ws.numel()))
+            if _capturing(stream):  # (zero when the graph runs, not before: the graph's alone)
+                return pool
+            self._rows, self._pool_ref = rows, pool
         return self._pool_ref
 
     @staticmethod
