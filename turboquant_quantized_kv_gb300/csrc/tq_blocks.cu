@@ -257,16 +257,24 @@ __device__ __forceinline__ void copy_block(const Part& p, int64_t src, int64_t d
   }
 }
 
-// The copies of a reordering: new row row_of[k] takes block list[k], with the pages of its parent's last.
-__global__ void __launch_bounds__(256) k_fork(const __grid_constant__ Parts parts, Rows from, Rows to, const int32_t* parents, Work w) {
+// The copies of a reordering: new row row_of[k] takes block list[k], with the pages of its parent's last.  (Ranges are
+// checked, for a workspace that was not zero.)
+__global__ void __launch_bounds__(256) k_fork(const __grid_constant__ Parts parts, Rows from, Rows to, const int32_t* parents,
+                                              int64_t num_blocks, Work w) {
   grid_dep_wait();
-  const int n = __ldcg(w.sums + 1), per = max(parts.n, 1);
+  const int n = min(__ldcg(w.sums + 1), to.rows), per = max(parts.n, 1);
   for (int64_t u = blockIdx.x; u < (int64_t)n * per; u += gridDim.x) {
     const int k = (int)(u / per), part = (int)(u - (int64_t)k * per);
-    const int i = __ldcg(w.row_of + k), p = __ldg(parents + i), dst = __ldcg(w.list + k);
+    const int i = __ldcg(w.row_of + k), dst = __ldcg(w.list + k);
+    if (i < 0 || i >= to.rows || dst < 0 || dst >= num_blocks) continue;
+    const int p = __ldg(parents + i);
+    if (p < 0 || p >= from.rows) continue;
     const int at = tokens_of(from, p, nullptr, false) / kBlock;
+    if (at >= from.max_blocks) continue;
+    const int src = __ldg(from.table + (int64_t)p * from.max_blocks + at);
+    if (src < 0 || src >= num_blocks) continue;
     if (part == 0 && threadIdx.x == 0) to.table[(int64_t)i * to.max_blocks + at] = dst;
-    if (part < parts.n) copy_block(parts.part[part], __ldg(from.table + (int64_t)p * from.max_blocks + at), dst);
+    if (part < parts.n) copy_block(parts.part[part], src, dst);
   }
 }
 
@@ -644,8 +652,8 @@ tq_status tq_blocks_reorder(const tq_block_pool* pool, const tq_cache_desc* cons
   k_rows<<<from->rows + to->rows, kRowThreads, 0, st>>>(rows_of(*from), rows_of(*to), parents, pool->refs, pool->num_blocks, w, status);
   count_launch();
   for (int l0 = 0; l0 == 0 || l0 < n_layers; l0 += kMaxParts / 2) {
-    const cudaError_t e = l0 == 0 ? follow(k_fork, 8 * sms, 256, st, parts_of(descs, n_layers, l0), rows_of(*from), rows_of(*to), parents, w)
-                                  : (k_fork<<<8 * sms, 256, 0, st>>>(parts_of(descs, n_layers, l0), rows_of(*from), rows_of(*to), parents, w),
+    const cudaError_t e = l0 == 0 ? follow(k_fork, 8 * sms, 256, st, parts_of(descs, n_layers, l0), rows_of(*from), rows_of(*to), parents, pool->num_blocks, w)
+                                  : (k_fork<<<8 * sms, 256, 0, st>>>(parts_of(descs, n_layers, l0), rows_of(*from), rows_of(*to), parents, pool->num_blocks, w),
                                      count_launch(), cudaGetLastError());
     if (e != cudaSuccess) return fail(TQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
   }
