@@ -373,7 +373,8 @@ size_t tq_workspace_bytes(const tq_cache_desc* desc, int batch, int num_q_heads,
  * int8 layers cut the blocks of the whole batch, one after another, into equal
  * ranges; num_splits bounds their number by num_splits ranges a (sequence, KV head,
  * eight query heads) on average, 0 leaves it to the size of the GPU, and their
- * workspace has one size for all calls.  They take up to 65536 query heads.  A row
+ * workspace has one size for all calls.  They take up to 65536 query heads and tables
+ * of up to 2^26 columns.  A row
  * whose logits leave fp32's range may come out as NaN. */
 tq_status tq_decode_attention(const tq_cache_desc* desc, const void* q, int q_dtype, int batch,
                               int num_q_heads, const int32_t* block_table, int max_blocks_per_seq,
@@ -458,8 +459,8 @@ size_t tq_attend_workspace_bytes(const tq_cache_desc* desc, int64_t n_tokens, in
  * for equal types and strides.  block_table, context_lens, sm_scale, the workspace contract (at
  * least tq_attend_workspace_bytes(...), zero before the first call) and errors as for
  * tq_decode_attention; one workspace serves both calls (after TQ_DEV_WAIT_TIMEOUT it
- * must be zero-filled again).  Up to 65536 query heads and 2^30 rows (tokens x query heads of
- * a KV head).  Weights are fp16 for bf16 queries, two fp16 parts for fp32 ones; in sequences of more
+ * must be zero-filled again).  Up to 65536 query heads, 2^30 rows (tokens x query heads of a KV
+ * head) and 2^26 columns of the table.  Weights are fp16 for bf16 queries, two fp16 parts for fp32 ones; in sequences of more
  * than 20 rows the tensor cores cut off what does not fit a value's sum, up to 5e-4 of a value that
  * 131,072 tokens share.  int8 layers only (TQ_ERR_UNSUPPORTED otherwise). */
 tq_status tq_attend(const tq_cache_desc* desc, const tq_heads* q, int q_dtype, int out_dtype, int64_t n_tokens,

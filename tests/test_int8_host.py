@@ -64,7 +64,7 @@ def test_attend_refusals(tqlib, layer):
                 dict(table=None), dict(width=0), dict(lens=None), dict(scale=float("nan")), dict(out=None), dict(inp=None),
                 dict(out=x.data_ptr() + 2), dict(inp=x.data_ptr() + 1)):
         assert call(**bad) == tqlib.TQ_ERR_INVALID_ARG, bad
-    for big in (dict(n=(1 << 26) + 1), dict(batch=65536), dict(heads=(1 << 16) + 2), dict(n=1 << 20, heads=1 << 12), dict(width=1 << 27)):
+    for big in (dict(n=(1 << 26) + 1), dict(batch=65536), dict(heads=(1 << 16) + 2), dict(n=1 << 20, heads=1 << 12), dict(width=(1 << 26) + 1)):
         assert call(**big) == tqlib.TQ_ERR_UNSUPPORTED, big
     assert call(n=0) == tqlib.TQ_OK and call(batch=0) == tqlib.TQ_OK
     assert tqlib.lib().tq_attend_workspace_bytes(ctypes.byref(other.desc), 4, 1, 2, 1) == 0
@@ -89,7 +89,7 @@ def test_block_refusals(tqlib, layer):
     assert lib.tq_blocks_workspace_bytes(0, 1) == 0 and lib.tq_blocks_workspace_bytes(4, -1) == 0
     assert lib.tq_blocks_workspace_bytes((1 << 30) + 1, 1) == 0
     pool = BlockPool(4, at, at + 4096, size)
-    rows, other = BlockRows(at, at + 1024, 4, 8), BlockRows(at + 2048, at + 3072, 8, 8)
+    rows, other = BlockRows(at, at + 1024, 4, 8), BlockRows(at + 2048, at + 2560, 8, 8)
     descs = (ctypes.POINTER(TQ.CacheDesc) * 2)(ctypes.pointer(layer.desc), ctypes.pointer(layer.desc))
     ref = ctypes.byref
     small = BlockPool(4, at, at + 4096, size - 1)
@@ -110,7 +110,7 @@ def test_block_refusals(tqlib, layer):
     # old and new rows in the same memory, tables of other widths, a cache twice, a layer of another size
     assert lib.tq_blocks_reorder(ref(pool), None, 0, ref(rows), at, ref(rows), None) == TQ.TQ_ERR_INVALID_ARG
     assert lib.tq_blocks_reorder(ref(pool), None, 0, ref(rows), None, ref(other), None) == TQ.TQ_ERR_INVALID_ARG
-    assert lib.tq_blocks_reorder(ref(pool), None, 0, ref(rows), at, ref(BlockRows(at + 2048, at + 3072, 8, 7)), None) == TQ.TQ_ERR_INVALID_ARG
+    assert lib.tq_blocks_reorder(ref(pool), None, 0, ref(rows), at, ref(BlockRows(at + 2048, at + 2560, 8, 7)), None) == TQ.TQ_ERR_INVALID_ARG
     assert lib.tq_blocks_reorder(ref(pool), descs, 2, ref(rows), at, ref(other), None) == TQ.TQ_ERR_INVALID_ARG
     pool5 = BlockPool(5, at, at + 4096, lib.tq_blocks_workspace_bytes(5, 8))
     assert lib.tq_blocks_reorder(ref(pool5), descs, 1, ref(rows), at, ref(other), None) == TQ.TQ_ERR_INVALID_ARG

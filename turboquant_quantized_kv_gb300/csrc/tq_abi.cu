@@ -108,8 +108,10 @@ int resolve_splits(const tq_cache_desc* desc, int batch, int num_q_heads, int ma
   return tq_auto_splits(desc, batch, num_q_heads, max_blocks);
 }
 
-// Query heads of a decode or attend call over an int8 layer (rows and coordinates are counted in 32 bits).
+// Query heads and table columns of a decode or attend call over an int8 layer (rows, coordinates and positions are
+// counted in 32 bits).
 constexpr int kInt8MostHeads = 1 << 16;
+constexpr int kInt8MostColumns = 1 << 26;
 
 // Workspace of a decode or attend call over an int8 layer.
 size_t int8_workspace(int num_sms) { return kCounterRegionBytes + int8_partial_bytes(num_sms); }
@@ -143,7 +145,7 @@ tq_status prepare_decode(const tq_cache_desc* desc, const void* q, int q_dtype, 
   DeviceInfo di;
   if ((s = device_info(&di)) != TQ_OK) return s;
   const bool int8 = desc->fmt.kv_format == TQ_KV_INT8;
-  if (int8 && (max_blocks_per_seq > INT32_MAX / TQ_BLOCK_SIZE || num_q_heads > kInt8MostHeads))
+  if (int8 && (max_blocks_per_seq > kInt8MostColumns || num_q_heads > kInt8MostHeads))
     return fail(TQ_ERR_UNSUPPORTED, "%s: max_blocks_per_seq %d / num_q_heads %d of an int8 layer", fn, max_blocks_per_seq, num_q_heads);
   const int splits = int8 ? num_splits : resolve_splits(desc, batch, num_q_heads, max_blocks_per_seq, num_splits);
   if (!int8 && splits < 1) return fail(TQ_ERR_INVALID_ARG, "%s: could not choose a split count", fn);
@@ -474,7 +476,7 @@ tq_status tq_attend(const tq_cache_desc* desc, const tq_heads* q, int q_dtype, i
   if (!(sm_scale == sm_scale)) return fail(TQ_ERR_INVALID_ARG, "%s: sm_scale is NaN", fn);
   if (n_tokens == 0 || batch == 0) return TQ_OK;
   if (n_tokens > (1 << 26) || batch > 65535 || q->num_heads > kInt8MostHeads ||
-      n_tokens * (q->num_heads / desc->num_kv_heads) > (1 << 30) || max_blocks_per_seq > INT32_MAX / TQ_BLOCK_SIZE)
+      n_tokens * (q->num_heads / desc->num_kv_heads) > (1 << 30) || max_blocks_per_seq > kInt8MostColumns)
     return fail(TQ_ERR_UNSUPPORTED, "%s: %lld tokens of %d heads, %d sequences, max_blocks_per_seq %d", fn, (long long)n_tokens,
                 q->num_heads, batch, max_blocks_per_seq);
   if (!query_starts || !block_table || !context_lens)
