@@ -62,6 +62,13 @@ constexpr int kSlots = 4;                   // tiles whose steps are kept
 constexpr float kRoom = 14.0f, kTop = 8.0f; // log2 of P at most, and of its largest when the reference moves
 constexpr float kMoveM = 16.0f;
 constexpr float kMostSum = 60000.0f;         // of 16 weights in fp16
+// Steps whose weights times values an accumulator of the tensor cores takes, for bf16 queries and for two parts; it is
+// cut off towards zero at each product, 8e-7 of its sum a step, and keep_sums() adds spans up outside, 6 us each
+// (fp32 queries, 131,072 tokens, error in the mean / at most, against 8.4e-4 / 1.2e-3 in one accumulator: 16 steps
+// 9e-6 / 1.9e-5, 8 steps 4e-6 / 1.0e-5, 4 steps 2e-6 / 7e-6; bf16: 128 steps 1.0e-4 / 2.7e-4, 64 steps 0.5e-4 / 2.2e-4, 2.2e-4
+// of that the weights'.  A chunk of 2048 tokens behind 30,000, bf16 / fp32: one accumulator 1.71 / 2.66 ms, 128 and 16
+// steps 1.72 / 2.84, 64 and 8 1.75 / 3.00; behind 120,000: 6.69 / 10.3, 6.85 / 11.1, 6.96 / 11.4).
+constexpr int kSpan = 128, kSpanExact = 8;
 
 // Shared memory: operands of 32 KB -- Q of the streams in 0 and 1 (low parts in 2 and 3), K in two stages,
 // V in two (with low parts in one) -- then the rest.
@@ -102,6 +109,7 @@ struct AttArgs {
   int* counters;
   float* part;  // [2 grid][256][d]
   float2* ml;   // [2 grid][256]
+  float4* kept; // [grid][8][8][4][32]: sums of spans of a softmax warp, as tensor memory deals them out
   unsigned* status;
 };
 
@@ -393,6 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
   const uint32_t tmem = misc.tmem;
   const uint32_t k_op = base + (EXACT ? 4u : 2u) * kOperand, v_op = k_op + 2 * kOperand;
   constexpr int vbit = EXACT ? 0 : 1;  // stages of V less one
+  constexpr int span = EXACT ? kSpanExact : kSpan;
 
   Unit u;
   u.seq = misc.seq;
@@ -414,11 +423,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
     const uint32_t ts = tmem + (uint32_t)(st * kTile) + ((uint32_t)(32 * w) << 16);
     const uint32_t to = tmem + (uint32_t)((2 + st) * kTile) + ((uint32_t)(32 * w) << 16);
     int done = 0, turns = 0;  // steps and units of the stream so far
+    float4* const kept = a.kept + ((int64_t)blockIdx.x * kSoftWarps + warp) * 1024 + lane;
     while (at < end) {
       int step, n;
       const int places = u.part(end - at, &step, &n);
       const bool part_of_it = n > 0 && (st == 0 || u.rows > kTile);
       float C = -INFINITY, m = -INFINITY, l = 0.0f;
+      float Ck = -INFINITY, lk = 0.0f;  // reference of the sums that keep_sums() has put aside, and their denominator
       const bool live = st * kTile + 32 * w < u.rows;
       const int first = u.s.ctx - u.s.n + u.tok0;  // the unit's first token attends to this many and itself
       if (part_of_it) {
@@ -512,11 +523,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
             }
             if (__any_sync(0xffffffffu, top > m + kMoveM || topv > C + kRoom)) {
               const float nm = fmaxf(m, ceilf(top)), nC = fmaxf(C, ceilf(topv) - kTop);
-              if (nm != m) l *= exp2f(m - nm);
+              if (nm != m) {
+                const float f = exp2f(m - nm);
+                l *= f;
+                lk *= f;
+              }
               m = nm;
               const float f = nC != C ? exp2f(C - nC) : 1.0f;
               C = nC;
-              if (i > 0 && __any_sync(0xffffffffu, f != 1.0f)) {  // (the last product into it precedes S)
+              if (i % span > 0 && __any_sync(0xffffffffu, f != 1.0f)) {  // (the last product into it precedes S)
 #pragma unroll 1
                 for (int c = 0; c < 8; ++c) {
                   uint32_t x[16];
@@ -655,7 +670,42 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
           if (lane == 0) mbar_arrive(pfull + st);
           return true;
         };
+        // The values' sums of the last span (the last product into them precedes S) to the warp's place in the
+        // workspace, together with those before, all by C; the accumulator begins anew.
+        auto keep_sums = [&] {
+          const int turn = done0 + i;
+          ok = logits_of(turn & (kSlots - 1), (turn / kSlots) & 1, (done + i) & 1);
+          if (!ok || !live) return;
+          const float f = Ck == C ? 1.0f : exp2f(Ck - C);
+          Ck = C;
+          lk += l;
+          l = 0.0f;
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            float4 y[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) y[j] = i > span ? __ldcg(kept + 512 * h + 32 * j) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const float g0 = __shfl_sync(0xffffffffu, f, 16 * h + (lane >> 2)), g1 = __shfl_sync(0xffffffffu, f, 16 * h + 8 + (lane >> 2));
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t x[16];
+              tmem_ld16x32_async(to + ((uint32_t)(16 * h) << 16) + 32 * c, x);
+              tmem_wait_ld16(x);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float4 z = y[4 * c + j];
+                __stcg(kept + 512 * h + 128 * c + 32 * j,
+                       make_float4(fmaf(z.x, g0, __uint_as_float(x[4 * j])), fmaf(z.y, g0, __uint_as_float(x[4 * j + 1])),
+                                   fmaf(z.z, g1, __uint_as_float(x[4 * j + 2])), fmaf(z.w, g1, __uint_as_float(x[4 * j + 3]))));
+              }
+            }
+          }
+        };
         for (; i < n && ok; ++i) {
+          if (i > 0 && i % span == 0) {
+            keep_sums();
+            if (!ok) break;
+          }
           if (!EXACT && i > 0 && quick()) continue;
           if (ok && one(std::false_type())) continue;
           if (ok) one(std::true_type());
@@ -669,7 +719,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
       const bool whole = step == 0 && n == u.all;
       if (part_of_it && live) {
         // ---- the rows' values, out or to a partial, by lanes of a quad next to each other
+        l += lk;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const float keep = Ck == C ? 1.0f : exp2f(Ck - C);
         const float shift = C == -INFINITY ? 0.0f : C - m, half = truncf(0.5f * shift);
         // (two factors where one would leave the range of exponents)
         const bool far = __any_sync(0xffffffffu, !(fabsf(shift) < 100.0f));
@@ -679,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
         const int quad = lane & 3;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {  // 16 rows, a lane two of them
-          float g0[2], g1[2];
+          float g0[2], g1[2], gk[2];
           int ru[2];
           int64_t o[2];
 #pragma unroll
@@ -688,12 +740,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
             ru[i] = st * kTile + 32 * w + rr;
             g0[i] = __shfl_sync(0xffffffffu, f0, rr);
             g1[i] = __shfl_sync(0xffffffffu, f1, rr);
+            gk[i] = __shfl_sync(0xffffffffu, keep, rr);
             const int t = ru[i] / a.g;
             o[i] = (int64_t)(u.s.first + u.tok0 + t) * a.o_row + (int64_t)(u.kvh * a.g + ru[i] - t * a.g) * a.o_head;
           }
           uint32_t all4[4][16];
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld16x32_async(to + ((uint32_t)(16 * h) << 16) + 32 * c, all4[c]);
+          if (n > span) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float4 y[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) y[j] = __ldcg(kept + 512 * h + 128 * c + 32 * j);
+              tmem_wait_ld16(all4[c]);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint32_t* const x = &all4[c][4 * j];
+                x[0] = __float_as_uint(fmaf(y[j].x, gk[0], __uint_as_float(x[0])));
+                x[1] = __float_as_uint(fmaf(y[j].y, gk[0], __uint_as_float(x[1])));
+                x[2] = __float_as_uint(fmaf(y[j].z, gk[1], __uint_as_float(x[2])));
+                x[3] = __float_as_uint(fmaf(y[j].w, gk[1], __uint_as_float(x[3])));
+              }
+            }
+          }
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t(&x)[16] = all4[c];
@@ -1016,7 +1086,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
             if (issue) {
 #pragma unroll
               for (int j = 0; j < 8; ++j)
-                umma_16_ts(d, p + (uint32_t)(32 * (j >> 1) + 8 * (j & 1)), v + (uint64_t)(j * (16 * 128 >> 4)), idesc_o, i > 0 || j > 0);
+                umma_16_ts(d, p + (uint32_t)(32 * (j >> 1) + 8 * (j & 1)), v + (uint64_t)(j * (16 * 128 >> 4)), idesc_o, i % span > 0 || j > 0);
               if constexpr (EXACT) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
@@ -1088,7 +1158,7 @@ cudaError_t run_tiles(const AttArgs& a, int num_sms, cudaStream_t st) {
 }  // namespace
 
 size_t int8_attend_partial_bytes(int num_sms) {
-  return (size_t)2 * num_sms * kUnitRows * (kD * sizeof(float) + sizeof(float2));
+  return (size_t)num_sms * kUnitRows * (3 * kD * sizeof(float) + 2 * sizeof(float2));
 }
 
 cudaError_t launch_int8_tiles(const AttendCall& c, uint8_t* partials, int num_sms, cudaStream_t st) {
@@ -1116,8 +1186,10 @@ cudaError_t launch_int8_tiles(const AttendCall& c, uint8_t* partials, int num_sm
   a.per = kUnitRows / a.g;
   a.scale = c.sm_scale * 1.4426950408889634f;
   a.counters = reinterpret_cast<int*>(c.workspace) + kAttCounters;
+  const size_t rows = (size_t)num_sms * kUnitRows;
   a.part = reinterpret_cast<float*>(partials);
-  a.ml = reinterpret_cast<float2*>(partials + (size_t)2 * num_sms * kUnitRows * kD * sizeof(float));
+  a.kept = reinterpret_cast<float4*>(a.part + 2 * rows * kD);
+  a.ml = reinterpret_cast<float2*>(a.part + 3 * rows * kD);
   a.status = c.status;
   return c.q_dtype == TQ_F32 ? run_tiles<true>(a, num_sms, st) : run_tiles<false>(a, num_sms, st);
 }
