@@ -120,3 +120,33 @@ def test_decode_long(cuda, tqlib, group):
     room = (2 * 2.0 ** -19 * size + 2.0 ** -20 + 2.0 ** -19 + 12501 * 2.0 ** -25) * np.abs(vv).max()
     assert np.abs(got[0] - want).max() <= room
     assert tqlib.get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("below", [27.5, 20.0])
+def test_attend_values_of_zero(cuda, tqlib, below, dtype):
+    """Tokens without values (zeros, whose step is the least there is) count in the denominator however far their logits
+    lie below the largest one: 2^20 of them, 27.5 binary orders below, take 0.5% of a row's result.  Room: half a step of a
+    weight's type on either side of it, and the logits' and sums' of the other tests."""
+    heads, group, new, ctx = 8, 8, 32, 1 << 20
+    k, v = np.zeros((2 * BLOCK, heads, D)), np.zeros((2 * BLOCK, heads, D))
+    k[0, :, 0] = 127.0 / 128  # the one token that counts, with a logit of 60 binary orders
+    v[0] = np.random.default_rng(3).integers(64, 128, (heads, D)) * 0.25
+    v[0, :, 0] = 127 * 0.25
+    scale = SCALE * math.log2(math.e)
+    q = np.zeros((new, heads * group, D), np.float32)
+    q[..., 0] = 474.0
+    k[BLOCK:, :, 0] = k[0, 0, 0] - below / (474.0 * scale)
+    layer = layer_with(cuda, tqlib, k, v)
+    row = np.ones(ctx // BLOCK, np.int64)
+    row[0] = 0
+    got = attend(cuda, layer, cuda.from_numpy(q).cuda().to(cuda.bfloat16 if dtype == "bf16" else cuda.float32), new, row, ctx, seqs_for(cuda, heads))
+    kk, vv = values(layer)
+    for i in (0, new - 1):
+        want, size = counted(q[i].astype(np.float64), kk, vv, row, ctx - new + i + 1)
+        alone = vv[0, :, 0].repeat(group, 0)
+        assert (want / alone).max() < 1 - (4e-3 if below == 27.5 else 0.4)
+        room = 2 * 2.0 ** -19 * size + 2.0 ** -15 + (2.0 ** -11 if dtype == "bf16" else 0.0)
+        err = np.abs(got[:, i] / want - 1)
+        assert err.max() <= room, (i, err.max(), room)
+    assert tqlib.get_device_status() == 0

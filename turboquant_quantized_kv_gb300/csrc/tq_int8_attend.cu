@@ -24,7 +24,7 @@
 // lies 2^-24 below the row's largest; fp32 ones go in as two parts).  A block's step of K is one factor for
 // 16 logits, its step of V one for 16 weights, so that both operands hold plain codes: with m a running
 // reference of a row's log2-logits u and C one of weight times step of V, both of what the row attends to,
-//     e = 2^(u - m),  denominator += e,  P = e step 2^(m - C) <= 2^14,
+//     e = 2^(u - m),  denominator += e,  P = e step 2^(m - C) < 60000 (2^14 in steps that look for their maximum),
 // so that a block of large values costs a row nothing unless it attends to them.  P is fp16 (half a step 2^-11), for fp32 queries in two parts as well.
 //
 // Bound.  A chunk of 2048 tokens behind 30,000 (64/8 heads) 1.81 ms, 1.15 PFLOP/s; prompts of up to 4097 tokens (32/8
@@ -605,8 +605,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
         };
         // A step of plain tokens by the references that the row has: nothing is looked for first, P comes straight
         // from the logits, 2^(u + log2 step - C), and the sums say whether the references hold (all terms are
-        // positive, so a sum of 16 bounds each of them); P waits in registers until then.  A block whose values
-        // are 2^100 below the others' counts as that, which keeps its weights.
+        // positive, so a sum of 16 bounds each of them); P waits in registers until then.  The denominator's terms come
+        // from P's, which end at 2^-126: where a block's values lie so far below the others' that this takes weights of more
+        // than 2^-66 of the reference (values of zero, for one), the step is not done here.
         auto quick = [&] {
           const int turn = done0 + i, slot = turn & (kSlots - 1);
           ok = logits_of(slot, (turn / kSlots) & 1, (done + i) & 1);
@@ -620,11 +621,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
             if (!plain) return false;
             const float2* const sp = reinterpret_cast<const float2*>(gen + kOffStep + slot * 128);
             uint32_t p[4][16], ra[32], rb[32];
-            float most = 0.0f, more = 0.0f, sum = 0.0f;
-            const float low = C - m - 100.0f;
+            float most = 0.0f, sum = 0.0f;
+            const float low = C - m - 60.0f;
+            bool apart = false;
             auto chunk = [&](const uint32_t(&x)[32], int c) {
               const float2 k2 = sp[c], v2 = sp[12 + c];
-              const float ks[2] = {k2.x * cq, k2.y * cq}, o[2] = {fmaxf(v2.x, low) - C, fmaxf(v2.y, low) - C};
+              const float ks[2] = {k2.x * cq, k2.y * cq}, o[2] = {v2.x - C, v2.y - C};
+              apart |= fminf(v2.x, v2.y) < low;
 #pragma unroll
               for (int b = 0; b < 2; ++b) {
                 float2 s0, s1;
@@ -641,10 +644,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
                   p[c][8 * b + 2 * k] = half2_bits(u0.x, u0.y);
                   p[c][8 * b + 2 * k + 1] = half2_bits(u1.x, u1.y);
                 }
-                const float t = (s0.x + s0.y) + (s1.x + s1.y), e = t * ex2(-o[b] - m);
+                const float t = (s0.x + s0.y) + (s1.x + s1.y);
                 most = fmaxf(most, t);
-                more = fmaxf(more, e);
-                sum += e;
+                sum += t * ex2(-o[b] - m);
               }
             };
             tmem_ld32_async(ts, ra);
@@ -659,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
             chunk(ra, 2);
             tmem_wait_ld32(rb);
             chunk(rb, 3);
-            if (__any_sync(0xffffffffu, most > kMostSum || more > 1.2676506e30f)) return false;  // (2^100)
+            if (__any_sync(0xffffffffu, most > kMostSum || apart)) return false;
             l += sum;
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_st16(ts + 32 * c, p[c]);
