@@ -24,9 +24,10 @@
 // parts first, the blocks outside, where sums round (fp32 queries, 64 ragged sequences: 1.8e-6 -> 3.3e-7 off, 3%
 // of the time).
 //
-// Scales.  With u = log2 of a weight, m a running reference (moved only when u exceeds it by 16) and T one
-// for weight times step of V, p = 2^(u - m) goes into the denominator and w = p step 2^(m - T) <= 2^15 into
-// the product, so that a block with large values that nobody attends costs the others nothing.
+// Scales.  With u = log2 of a weight, m a running reference (moved only when u exceeds it by 16) and m + T one
+// for weight times step of V, p = 2^(u - m) goes into the denominator and w = p step 2^-T <= 2^15 into
+// the product, so that a block with large values that nobody attends costs the others nothing.  (T is kept apart
+// from m: next to logits of 2^24 and more the powers of two of the steps would be lost.)
 //
 // Bound.  16 sequences of 8192 tokens (32/8 heads) 67 us, 40 of them the pages at the rate of a copy: the loop runs at 5.1
 // TB/s, some 14 us are the kernel's beginning and end.  Groups of eight are bound by a block's 450 warp
@@ -222,7 +223,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
   __syncthreads();
 
   float acc[8][4];
-  float m[HL], T[HL], l[HL];
+  float m[HL], T[HL], l[HL];  // (T relative to m)
   auto clear = [&] {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -435,8 +436,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
           const float k = kstep * cq[h];
           in0[h] = lg < lim[h] - kBlock * j;
           in1[h] = lg + 8 < lim[h] - kBlock * j;
-          u[h][0] = (NH == 4 ? S[0] + S[1] : S[h]) * k;
-          u[h][1] = (NH == 4 ? S[2] + S[3] : S[2 + h]) * k;
+          // (rounded here: the references are of logits, not of unrounded products)
+          u[h][0] = __fmul_rn(NH == 4 ? S[0] + S[1] : S[h], k);
+          u[h][1] = __fmul_rn(NH == 4 ? S[2] + S[3] : S[2 + h], k);
         }
         if (kbad) {
 #pragma unroll
@@ -451,8 +453,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
         bool move = false;
 #pragma unroll
         for (int h = 0; h < HL; ++h) {
-          const float most_u = fminf(m[h] + 16.0f, T[h] + (float)(14 - ev));
-          move |= (in0[h] && u[h][0] > most_u) || (in1[h] && u[h][1] > most_u);
+          const float most = fminf(16.0f, T[h] + (float)(14 - ev));
+          move |= (in0[h] && u[h][0] - m[h] > most) || (in1[h] && u[h][1] - m[h] > most);
         }
         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
@@ -461,9 +463,13 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = ceilf(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)));
-            const float nm = fmaxf(m[h], top), nT = fmaxf(T[h], top + (float)(ev + 1 - 8));
-            if (nm != m[h]) l[h] *= exp2f(m[h] - nm);
+            const float nm = fmaxf(m[h], top);
+            if (nm != m[h]) {
+              l[h] *= exp2f(m[h] - nm);
+              T[h] += m[h] - nm;
+            }
             m[h] = nm;
+            const float nT = top == -INFINITY ? T[h] : fmaxf(T[h], top - nm + (float)(ev + 1 - 8));
             const float f = nT != T[h] ? exp2f(T[h] - nT) : 1.0f;
             T[h] = nT;
 #pragma unroll
@@ -484,7 +490,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
         for (int h = 0; h < HL; ++h) {
           const float p0 = in0[h] ? ex2(u[h][0] - m[h]) : 0.0f, p1 = in1[h] ? ex2(u[h][1] - m[h]) : 0.0f;
           l[h] += p0 + p1;
-          const float f = T[h] == -INFINITY ? 0.0f : vmant * ex2(fminf((float)ev + m[h] - T[h], 120.0f));
+          const float f = T[h] == -INFINITY ? 0.0f : vmant * ex2(fminf((float)ev - T[h], 120.0f));
           w[h][0] = p0 * f;
           w[h][1] = p1 * f;
         }
@@ -544,7 +550,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_int8_decode(const __grid_con
         }
         // normalised values of row h of the lane: coordinates 16 lg .. 16 lg + 15
         auto values = [&](int h, float (&o)[16]) {
-          const float shift = T[h] == -INFINITY ? 0.0f : T[h] - m[h], half = truncf(0.5f * shift);
+          const float shift = T[h] == -INFINITY ? 0.0f : T[h], half = truncf(0.5f * shift);
           const float f0 = exp2f(half), f1 = exp2f(shift - half);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
