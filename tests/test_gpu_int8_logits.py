@@ -2,7 +2,7 @@
 import numpy as np
 import pytest
 
-from tests.test_gpu_int8_long import BLOCK, D, SCALE, layer_with, values
+from tests.test_gpu_int8_long import BLOCK, D, SCALE, attend, layer_with, seqs_for, values
 
 pytestmark = pytest.mark.gpu
 
@@ -52,4 +52,35 @@ def test_decode(cuda, tqlib, power, group, dtype):
     got = layer.decode(q.expand(seqs, -1, -1).contiguous(), table, lens, out_dtype=cuda.float32).cpu().numpy()
     for b in range(seqs):
         check(got[b:b + 1], want, 2.0 ** -15)
+    assert tqlib.get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("power", POWERS)
+def test_attend(cuda, tqlib, power, dtype):
+    """Room: half a step of a weight's type, 2^-11 in fp16 or 2^-22 in two parts; for steps by logarithms 2^-13 more (references
+    below 2^11); 2^-15 for what the accumulators cut off and the weights of 2^-22 and less that others keep."""
+    heads, group, new = 4, 8, 32
+    t = cuda.bfloat16 if dtype == "bf16" else cuda.float32
+    layer, q, want = inputs(cuda, tqlib, power, heads, group, new, 700, t, power, 30.0)
+    row = np.arange(layer.num_blocks)
+    got = attend(cuda, layer, q, new, row, 700, seqs_for(cuda, heads))
+    assert np.array_equal(got[0], got[-1])
+    check(got[0], want, 2.0 ** -15 + (2.0 ** -11 + 2.0 ** -13 if dtype == "bf16" else 2.0 ** -22))
+    assert tqlib.get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("power", [12, 17, 19, 40])
+def test_attend_repeats(cuda, tqlib, power, dtype):
+    """The same blocks three times over: copies of the token that decides stand in later steps too, whose references have been
+    found by then.  Room as above."""
+    heads, group, new, n = 4, 8, 32, 12 * BLOCK
+    t = cuda.bfloat16 if dtype == "bf16" else cuda.float32
+    layer, q, want = inputs(cuda, tqlib, 90 + power, heads, group, 1, n, t, power, 30.0)
+    row = np.tile(np.arange(n // BLOCK), 30)
+    got = attend(cuda, layer, q.expand(new, -1, -1).contiguous(), new, row, 30 * n - 3, seqs_for(cuda, heads))
+    room = 2.0 ** -15 + (2.0 ** -11 + 2.0 ** -13 if dtype == "bf16" else 2.0 ** -22)
+    for i in (0, new - 1):
+        check(got[0, i:i + 1], want, room)
     assert tqlib.get_device_status() == 0

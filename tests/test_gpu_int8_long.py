@@ -150,3 +150,38 @@ def test_attend_values_of_zero(cuda, tqlib, below, dtype):
         err = np.abs(got[:, i] / want - 1)
         assert err.max() <= room, (i, err.max(), room)
     assert tqlib.get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype,span", [("bf16", 128), ("f32", 8)])
+def test_attend_growing(cuda, tqlib, dtype, span):
+    """Values that grow by 2^3 with every `span` steps of the tiles, and queries that like later tokens more: the references
+    of a row move after sums of earlier steps have been put aside.  Room as above, with a span's 2^-20 a step."""
+    heads, group, new = 2, 8, 32
+    ctx = 6 * span * 128 + 77
+    n = -(-ctx // BLOCK) * BLOCK
+    g = np.random.default_rng(span)
+    k, v = g.standard_normal((n, heads, D)), 1.0 + 0.3 * g.standard_normal((n, heads, D))
+    at = np.arange(n)[:, None, None] // BLOCK * BLOCK / (128.0 * span)
+    v *= 2.0 ** (3 * at)
+    k[:, :, :1] = 4 * at
+    layer = layer_with(cuda, tqlib, k, v)
+    q = g.standard_normal((new, heads * group, D)).astype(np.float32)
+    q[..., 0] = np.arange(heads * group) % 5 * 2.0  # (logits grow by up to 2.8 a span)
+    t = cuda.from_numpy(q).cuda().to(cuda.bfloat16 if dtype == "bf16" else cuda.float32)
+    row = g.permutation(n // BLOCK)
+    order = np.argsort(row)  # (block row[j] holds tokens 16 j ..)
+    for pool in (layer.k_cache, layer.v_cache):
+        pool.copy_(pool.view(n // BLOCK, -1)[cuda.from_numpy(order).cuda()].reshape(-1))
+    seqs = seqs_for(cuda, heads)
+    got = attend(cuda, layer, t, new, row, ctx, seqs)
+    kk, vv = values(layer)
+    th = t.double().cpu().numpy()
+    for i in (0, new - 1):
+        want, size = counted(th[i], kk, vv, row, ctx - new + i + 1)
+        big = np.abs(vv).max()
+        assert (np.abs(want).max(1) > big / 40).all()
+        room = (2 * 2.0 ** -19 * size + 2.0 ** -20 + span * 2.0 ** -20 + (2.0 ** -11 if dtype == "bf16" else 0.0)) * big
+        err = np.abs(got[:, i] - want).max()
+        assert err <= room, (i, err / big, room / big)
+        assert np.array_equal(got[0], got[-1])
+    assert tqlib.get_device_status() == 0

@@ -24,8 +24,9 @@
 // lies 2^-24 below the row's largest; fp32 ones go in as two parts).  A block's step of K is one factor for
 // 16 logits, its step of V one for 16 weights, so that both operands hold plain codes: with m a running
 // reference of a row's log2-logits u and C one of weight times step of V, both of what the row attends to,
-//     e = 2^(u - m),  denominator += e,  P = e step 2^(m - C) < 60000 (2^14 in steps that look for their maximum),
-// so that a block of large values costs a row nothing unless it attends to them.  P is fp16 (half a step 2^-11), for fp32 queries in two parts as well.
+//     e = 2^(u - m),  denominator += e,  P = e step 2^(m - C) < 60000 (2^14 in steps that look for their maximum)
+// (C as its difference from m, which large logits would swallow), so that a block of large values costs a row
+// nothing unless it attends to them.  P is fp16 (half a step 2^-11), for fp32 queries in two parts as well.
 //
 // Bound.  A chunk of 2048 tokens behind 30,000 (64/8 heads) 1.81 ms, 1.15 PFLOP/s; prompts of up to 4097 tokens (32/8
 // heads) 407 us, 0.5 PFLOP/s.  A step of both streams is 2048 clocks of the tensor cores and takes some 3000: each
@@ -61,6 +62,8 @@ constexpr uint32_t kOperand = 2 * kPanel;
 constexpr int kSlots = 4;                   // tiles whose steps are kept
 constexpr float kRoom = 14.0f, kTop = 8.0f; // log2 of P at most, and of its largest when the reference moves
 constexpr float kMoveM = 16.0f;
+constexpr float kMostLogit = 1048576.0f;     // 2^20: logits up to this in the fused products of the plain steps
+constexpr float kMostQuick = 2048.0f;        // references up to this in the quick steps (2^-14 of a step's logarithm)
 constexpr float kMostSum = 60000.0f;         // of 16 weights in fp16
 // Steps whose weights times values an accumulator of the tensor cores takes, for bf16 queries and for two parts; it is
 // cut off towards zero at each product, 8e-7 of its sum a step, and keep_sums() adds spans up outside, 6 us each
@@ -428,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
       int step, n;
       const int places = u.part(end - at, &step, &n);
       const bool part_of_it = n > 0 && (st == 0 || u.rows > kTile);
-      float C = -INFINITY, m = -INFINITY, l = 0.0f;
+      float C = -INFINITY, m = -INFINITY, l = 0.0f;  // (C relative to m, as Ck)
       float Ck = -INFINITY, lk = 0.0f;  // reference of the sums that keep_sums() has put aside, and their denominator
       const bool live = st * kTile + 32 * w < u.rows;
       const int first = u.s.ctx - u.s.n + u.tok0;  // the unit's first token attends to this many and itself
@@ -479,9 +482,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
               x[4] = z.x; x[5] = z.y; x[6] = z.z; x[7] = z.w;
             };
             uint32_t ra[32], rb[32];
-            float top = -INFINITY, topv = -INFINITY;  // the largest u of the row, and with the exponent of its block's values
+            float ev[8], us[8];  // of each block: the exponent of its values' step, the row's largest u
+            float top = -INFINITY;
             {
-              float ks[8], ev[8];
+              float ks[8];
               eight(ks, 0);
               eight(ev, 2);
 #pragma unroll
@@ -502,10 +506,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
                     hi[1] = max3(hi[1], y[2], y[3]);
                   }
                   hi[0] = fmaxf(hi[0], hi[1]);
-                  float v = hi[0] * ks[2 * c + h];
+                  float v = __fmul_rn(hi[0], ks[2 * c + h]);  // (rounded here: differences from it are not of the product)
                   if (kCareful && hi[0] == -INFINITY) v = hi[0];
+                  us[2 * c + h] = v;
                   top = fmaxf(top, v);
-                  topv = fmaxf(topv, v + ev[2 * c + h]);
                 }
               };
               tmem_ld32_async(ts, ra);
@@ -521,14 +525,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
               tmem_wait_ld32(rb);
               tops(rb, 3);
             }
-            if (__any_sync(0xffffffffu, top > m + kMoveM || topv > C + kRoom)) {
-              const float nm = fmaxf(m, ceilf(top)), nC = fmaxf(C, ceilf(topv) - kTop);
+            const bool big = __any_sync(0xffffffffu, top > kMostLogit || top < -kMostLogit && top > -INFINITY);
+            if (!kCareful && big) return false;
+            // the largest u less x, with the exponent of its block's values
+            auto topv = [&](float x) {
+              float t = -INFINITY;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) t = fmaxf(t, us[k] - x + ev[k]);
+              return t;
+            };
+            if (__any_sync(0xffffffffu, top - m > kMoveM || topv(m) > C + kRoom)) {
+              const float nm = fmaxf(m, ceilf(top));
               if (nm != m) {
                 const float f = exp2f(m - nm);
                 l *= f;
                 lk *= f;
+                C += m - nm;
+                Ck += m - nm;
+                m = nm;
               }
-              m = nm;
+              const float nC = fmaxf(C, ceilf(topv(m)) - kTop);
               const float f = nC != C ? exp2f(C - nC) : 1.0f;
               C = nC;
               if (i % span > 0 && __any_sync(0xffffffffu, f != 1.0f)) {  // (the last product into it precedes S)
@@ -542,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
                 }
               }
             }
-            const float off = m == -INFINITY ? 0.0f : m, rho = C == -INFINITY ? 0.0f : exp2f(fminf(m - C, 120.0f));
+            const float off = m == -INFINITY ? 0.0f : m, rho = C == -INFINITY ? 0.0f : exp2f(fminf(-C, 120.0f));
             float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
             auto weights = [&](const uint32_t(&x)[32], int c) {
               const float2 k2 = reinterpret_cast<const float2*>(sp)[c], v2 = reinterpret_cast<const float2*>(sp)[4 + c];
@@ -555,8 +571,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
                 const int b = k >> 2;
                 float2 u0 = make_float2(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1]));
                 float2 u1 = make_float2(__uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3]));
-                u0 = __ffma2_rn(u0, make_float2(ks[b], ks[b]), make_float2(-off, -off));
-                u1 = __ffma2_rn(u1, make_float2(ks[b], ks[b]), make_float2(-off, -off));
+                if (kCareful && (EXACT || big)) {  // (logits as `top` has them: of large ones the unrounded product may lie far above it)
+                  u0 = make_float2(__fmul_rn(u0.x, ks[b]) - off, __fmul_rn(u0.y, ks[b]) - off);
+                  u1 = make_float2(__fmul_rn(u1.x, ks[b]) - off, __fmul_rn(u1.y, ks[b]) - off);
+                } else {
+                  u0 = __ffma2_rn(u0, make_float2(ks[b], ks[b]), make_float2(-off, -off));
+                  u1 = __ffma2_rn(u1, make_float2(ks[b], ks[b]), make_float2(-off, -off));
+                }
                 u0 = make_float2(ex2(u0.x), ex2(u0.y));
                 u1 = make_float2(ex2(u1.x), ex2(u1.y));
                 if (kCareful) {
@@ -607,8 +628,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
         // from the logits, 2^(u + log2 step - C), and the sums say whether the references hold (all terms are
         // positive, so a sum of 16 bounds each of them); P waits in registers until then.  The denominator's terms come
         // from P's, which end at 2^-126: where a block's values lie so far below the others' that this takes weights of more
-        // than 2^-66 of the reference (values of zero, for one), the step is not done here.
+        // than 2^-66 of the reference (values of zero, for one), the step is not done here, and neither where the logarithm
+        // of a step loses bits next to the references.
         auto quick = [&] {
+          const float mC = m + C;
+          if (__any_sync(0xffffffffu, live && fmaxf(fabsf(m), fabsf(mC)) > kMostQuick)) return false;
           const int turn = done0 + i, slot = turn & (kSlots - 1);
           ok = logits_of(slot, (turn / kSlots) & 1, (done + i) & 1);
           if (!ok) return false;
@@ -622,11 +646,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
             const float2* const sp = reinterpret_cast<const float2*>(gen + kOffStep + slot * 128);
             uint32_t p[4][16], ra[32], rb[32];
             float most = 0.0f, sum = 0.0f;
-            const float low = C - m - 60.0f;
+            const float low = C - 60.0f;
             bool apart = false;
             auto chunk = [&](const uint32_t(&x)[32], int c) {
               const float2 k2 = sp[c], v2 = sp[12 + c];
-              const float ks[2] = {k2.x * cq, k2.y * cq}, o[2] = {v2.x - C, v2.y - C};
+              const float ks[2] = {k2.x * cq, k2.y * cq}, o[2] = {v2.x - mC, v2.y - mC};
               apart |= fminf(v2.x, v2.y) < low;
 #pragma unroll
               for (int b = 0; b < 2; ++b) {
@@ -724,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_int8_attend(const __grid_consta
         l += lk;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const float keep = Ck == C ? 1.0f : exp2f(Ck - C);
-        const float shift = C == -INFINITY ? 0.0f : C - m, half = truncf(0.5f * shift);
+        const float shift = C == -INFINITY ? 0.0f : C, half = truncf(0.5f * shift);
         // (two factors where one would leave the range of exponents)
         const bool far = __any_sync(0xffffffffu, !(fabsf(shift) < 100.0f));
         const float f0 = far ? exp2f(half) * inv : exp2f(shift) * inv, f1 = far ? exp2f(shift - half) : 1.0f;
