@@ -601,7 +601,8 @@ size_t tq_blocks_workspace_bytes(int64_t num_blocks, int rows);
 /* Pages of block src[i] to block dst[i] in both pools of every layer, i < n (device int32 arrays).  A pair
  * of two negative ids is skipped; of pairs with the same destination the last one counts; a pair
  * whose source is the destination of another one, or with an id outside the pool, is skipped and
- * recorded (TQ_DEV_BAD_BLOCK).  Counts are not touched. */
+ * recorded (TQ_DEV_BAD_BLOCK).  Counts are not touched.  Up to 65,536 pairs (TQ_ERR_UNSUPPORTED beyond): each is held
+ * against all others. */
 tq_status tq_copy_blocks(const tq_cache_desc* const* descs, int n_layers, const int32_t* src, const int32_t* dst, int64_t n,
                          void* stream);
 
