@@ -779,7 +779,7 @@ class Blocks:
         torch = _torch()
         self.num_blocks = int(num_blocks)
         self._refs = torch.zeros(self.num_blocks, dtype=torch.int32, device=device)
-        self._workspaces = []  # (earlier ones too: captured graphs may use them)
+        self._workspaces = []  # (earlier ones too: captured graphs may use them; eleven at most)
         self._rows, self._pool_ref = -1, None
 
     @property
@@ -787,20 +787,23 @@ class Blocks:
         return self._refs
 
     def _pool(self, rows, stream):
-        """Reference to the tq_block_pool of `refs` and a workspace for calls of so many rows."""
-        if rows > self._rows:
-            torch = _torch()
-            size = lib().tq_blocks_workspace_bytes(self.num_blocks, rows)
-            if size == 0:
-                raise TQError(TQ_ERR_INVALID_ARG, last_error() or "invalid sizes")
-            refs = _index_ptr(self.refs, "refs", torch.int32, (self.num_blocks,))
-            ws = _new(torch.zeros, (int(size),), torch.uint8, self.refs.device, stream)
-            self._workspaces.append(ws)
-            pool = _byref(BlockPool(self.num_blocks, refs, ws.data_ptr(), ws.numel()))
-            if _capturing(stream):  # (zero when the graph runs, not before: the graph's alone)
-                return pool
-            self._rows, self._pool_ref = rows, pool
-        return self._pool_ref
+        """Reference to the tq_block_pool of `refs` and a workspace for calls of so many rows.  The object's own is made for
+        the next power of two; a call that is captured while there is none has memory of the graph's instead, which is
+        zero when the graph runs, not before, and free for the graph's later calls."""
+        if rows <= self._rows:
+            return self._pool_ref
+        most = max(1024, 1 << (rows - 1).bit_length())
+        size = lib().tq_blocks_workspace_bytes(self.num_blocks, most)
+        if size == 0:
+            raise TQError(TQ_ERR_INVALID_ARG, last_error() or "invalid sizes")
+        pool = BlockPool(self.num_blocks, _index_ptr(self.refs, "refs", _torch().int32, (self.num_blocks,)))
+        pool.memory = _new(_torch().zeros, (int(size),), _torch().uint8, self.refs.device, stream)
+        pool.workspace, pool.workspace_bytes = pool.memory.data_ptr(), pool.memory.numel()
+        if not _capturing(stream):
+            self._workspaces.append(pool.memory)
+            self._rows, self._pool_ref = most, _byref(pool)
+            return self._pool_ref
+        return _byref(pool)
 
     @staticmethod
     def _table(block_table, context_lens):
