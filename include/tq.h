@@ -340,7 +340,7 @@ tq_status tq_quantize_rotated(const tq_cache_desc* desc, int which, const float*
                               const int64_t* slot_mapping, int64_t n_tokens, void* stream);
 
 /* Number of context splits decode uses when num_splits == 0 (depends on the
- * current device's SM count); 0 on error. */
+ * current device's SM count; int8 layers: for batches without empty sequences); 0 on error. */
 int tq_auto_splits(const tq_cache_desc* desc, int batch, int num_q_heads, int max_blocks_per_seq);
 
 /* Workspace bytes tq_decode_attention needs for these sizes (num_splits = 0:

@@ -283,8 +283,8 @@ int tq_auto_splits(const tq_cache_desc* desc, int batch, int num_q_heads, int ma
   DeviceInfo di;
   if (device_info(&di) != TQ_OK) return 0;
   const int g = num_q_heads / desc->num_kv_heads;
-  if (desc->fmt.kv_format == TQ_KV_INT8)  // (ranges of the whole batch: on average so many a unit)
-    return auto_splits(di.num_sms, 16, batch, desc->num_kv_heads * ((g + 7) / 8), max_blocks_per_seq);
+  if (desc->fmt.kv_format == TQ_KV_INT8)
+    return int8_auto_splits(di.num_sms, batch, desc->num_kv_heads * ((g + 7) / 8), max_blocks_per_seq);
   const int hpw = g <= 4 ? 4 : 8;  // heads per decode warp
   const int groups = (g + hpw - 1) / hpw;
   return auto_splits(di.num_sms, decode_warps(*desc, g), batch, desc->num_kv_heads * groups, max_blocks_per_seq);

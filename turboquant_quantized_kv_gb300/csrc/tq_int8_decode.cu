@@ -722,6 +722,14 @@ cudaError_t run_decode(const DecArgs& a, int num_sms, cudaStream_t st) {
 
 }  // namespace
 
+// Ranges a unit that leave as many ranges as the automatic choice has: one a warp of the GPU, of kDecMinBlocks at least.
+int int8_auto_splits(int num_sms, int batch, int units, int max_blocks) {
+  const int64_t all = (int64_t)batch * units, ranges = (int64_t)num_sms * kDecWarps;
+  if (all < 1) return 1;  // (fewer query heads than KV heads: decode refuses them)
+  const int64_t most = (max_blocks + kDecMinBlocks - 1) / kDecMinBlocks, s = (ranges + all - 1) / all;
+  return (int)(s < most ? s : most);
+}
+
 size_t int8_partial_bytes(int num_sms) { return ((size_t)2 * num_sms * 8 * (kD + 2) * sizeof(float) + 255) & ~(size_t)255; }
 
 static cudaError_t launch_rows(const tq_cache_desc& d, DecArgs& a, bool few, uint8_t* workspace, int num_sms, cudaStream_t st) {

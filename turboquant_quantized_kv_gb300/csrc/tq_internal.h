@@ -158,6 +158,7 @@ cudaError_t launch_int8_append(const tq_cache_desc& d, const void* k, const void
 cudaError_t launch_int8_dequant(const tq_cache_desc& d, int which, const int64_t* slots, int64_t n, void* out, int out_dtype,
                                 unsigned* status, int num_sms, cudaStream_t st);
 size_t int8_partial_bytes(int num_sms);         // (a multiple of 256)
+int int8_auto_splits(int num_sms, int batch, int units, int max_blocks);  // units a sequence
 size_t int8_attend_partial_bytes(int num_sms);  // behind it, for attend
 cudaError_t launch_int8_decode(const DecodeCall& c, int num_sms, cudaStream_t st);
 cudaError_t launch_int8_attend(const AttendCall& c, int num_sms, cudaStream_t st);
