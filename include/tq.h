@@ -460,7 +460,7 @@ size_t tq_attend_workspace_bytes(const tq_cache_desc* desc, int64_t n_tokens, in
  * least tq_attend_workspace_bytes(...), zero before the first call) and errors as for
  * tq_decode_attention; one workspace serves both calls (after TQ_DEV_WAIT_TIMEOUT it
  * must be zero-filled again).  Up to 65536 query heads, 2^30 rows (tokens x query heads of a KV
- * head) and 2^26 columns of the table.  In sequences of more than 20 rows weights are fp16 for bf16 queries (half a step
+ * head) and 2^26 columns of the table.  In sequences of more than 24 rows weights are fp16 for bf16 queries (half a step
  * 2^-11), two fp16 parts for fp32 ones (so a caller of bf16 queries who wants them gives the queries in fp32), and
  * the tensor cores cut off less than 2e-4 of a value's sum for bf16 queries and 2e-5 for fp32 ones, whatever the
  * context.  int8 layers only (TQ_ERR_UNSUPPORTED otherwise). */

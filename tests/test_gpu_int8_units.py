@@ -36,7 +36,7 @@ def places(new, past, heads, group):
     """Length of the line: steps of all units, and three a unit."""
     per, total = 256 // group, 0
     for n, p in zip(new, past):
-        if n * group > 20:
+        if n * group > 24:
             total += sum(max(1, -(-(p + min(n, (k + 1) * per)) // 128)) + 3 for k in range(-(-n // per))) * heads
     return total
 

@@ -15,11 +15,19 @@ constexpr int kI8Page = kI8Codes + 16;         // and of a page
 constexpr float kI8Least = 1.1754943508222875e-38f;  // 2^-126, the least step
 
 // Sequences with more rows (tokens x query heads of a KV head) than this go through the tiles of
-// tq_int8_attend.cu, the others through the decode kernel, which reads the pages once for each eight rows
-// (24 sequences of 3000 tokens, 8 heads, by the decode kernel and by the tiles: 16 rows 74 us and 111, 20 98 and
-// 111, 24 99 and 112, 32 125 and 114; 64 of 8000: 20 rows 547 and 479, 32 721 and 483; 64 of 200: 20 rows 43
-// and 62, 32 53 and 63).
-constexpr int kAttRows = 20;
+// tq_int8_attend.cu, the others through the decode kernel, which reads the pages once for each eight rows, so the rule
+// ends with a unit of eight.  By the decode kernel / by the tiles, us a call, 8 KV heads in groups of four:
+//                          16 rows      24 rows      32 rows
+//   1 sequence  of 30,000   48 /  93     56 / 102     64 / 109
+//   4           of 30,000  126 / 153    146 / 154    203 / 158
+//   8           of  1,000   32 /  60     35 /  60     39 /  62
+//   16          of  8,000  118 / 162    169 / 164    208 / 166
+//   24          of  3,000   83 / 124    105 / 124    133 / 124
+//   64          of    200   43 /  87     49 /  88     56 /  89
+//   64          of  8,000  378 / 461    550 / 462    707 / 468
+// (Many long contexts would want the tiles from 17 rows on, few or short ones not at 32: the host knows the tables'
+// widths, not the lengths.)
+constexpr int kAttRows = 24;
 constexpr int kAttMostGroup = 256;  // query heads of a KV head, with more of them every sequence does the latter
 
 // Counters of a call in its workspace: the decode kernel's from 0 on, the tiles' from here on, one a CTA.
