@@ -76,7 +76,9 @@
  *  filled from slot 0 on, as sequences fill it.  A token with an infinite coordinate or
  *  a NaN takes no part in the step and reads as not a number in every coordinate;
  *  the other tokens keep their values.  Of a slot given twice in one call the
- *  later token stays.
+ *  later token stays.  A step never falls again but at slot 0: tokens that are given up
+ *  (drafts that were not accepted) and written over leave the step, and the codes that
+ *  were rounded to it, as they made them.
  *
  * ------------------------------------------------------------------------
  * Readings of the pages (they leave these open; the library and the oracle
@@ -574,7 +576,7 @@ tq_status tq_decode_attention_static(const tq_cache_desc* desc, const void* q, i
  * function of its inputs.  All decisions are taken on the device: a call that runs out of
  * blocks records TQ_DEV_NO_BLOCK and leaves -1 in the entries that got none, entries outside
  * [0, num_blocks) are left as they are, counted nowhere and recorded (TQ_DEV_BAD_BLOCK, as is a
- * count that would fall below zero), lengths outside a row are cut to it and recorded
+ * count that falls below zero: more entries gave the block up than held it; it is free), lengths outside a row are cut to it and recorded
  * (TQ_DEV_BAD_CONTEXT).  Calls on one pool change its counts and share its workspace: they follow
  * one another on a stream (or are ordered by events).
  * Layers (an array of descriptors, as in tq_quantize_append_layers) are those whose pages move

@@ -27,8 +27,9 @@ constexpr int kAppChunk = 64;  // tokens of a CTA at most
 // 608 tokens 14 / 11 us so, 18 / 19 with the passes; 1024 16 / 17 and 19 / 20; 2048 26 / 23 and 22 / 23).
 constexpr int kScanMost = 1024;
 // Tokens x heads up to which CTAs have few tokens, for sequences in turn, where each token of a CTA may own a block
-// (8 heads, 4096 tokens: 25 / 26 us with four tokens a CTA, 21 / 64 with sixteen; 16,384: 46 / 51 and 37 / 84; one
-// head, 16,384 tokens: 17 / 18 with eight, 14 / 38 with 64).
+// (8 heads, 4096 tokens: 25 / 26 us with four tokens a CTA, 21 / 64 with sixteen; 8192: 35 / 31 and 25 / 70; 16,384:
+// 46 / 51 and 37 / 84; one head, 16,384 tokens: 17 / 18 with eight, 14 / 38 with 64.  Beyond, prompts are the ones that
+// calls of this size are of; sequences in turn pay for it).
 constexpr int kTurnMost = 32768;
 
 struct AppendArgs {

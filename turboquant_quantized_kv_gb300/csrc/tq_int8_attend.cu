@@ -28,10 +28,13 @@
 // (C as its difference from m, which large logits would swallow), so that a block of large values costs a row
 // nothing unless it attends to them.  P is fp16 (half a step 2^-11), for fp32 queries in two parts as well.
 //
+// Sums.  An accumulator of the tensor cores is cut off at each product; it takes kSpan steps at most, which are then
+// added up in fp32 in the workspace.
+//
 // Bound.  A chunk of 2048 tokens behind 30,000 (64/8 heads) 1.81 ms, 1.15 PFLOP/s; prompts of up to 4097 tokens (32/8
-// heads) 407 us, 0.5 PFLOP/s.  A step of both streams is 2048 clocks of the tensor cores and takes some 3000: each
-// stream's chain of logits (512), softmax (1700) and weights times values (512).  Short units pay 5.5 us at
-// their end and 3.3 at their first step beside it.
+// heads) 419 us, 0.5 PFLOP/s; with fp32 queries, twice the products, 3.08 ms and 589 us.  A step of both streams is 2048
+// clocks of the tensor cores and takes some 3000: each stream's chain of logits (512), softmax (1700) and weights times
+// values (512).  Short units pay 5.5 us at their end and 3.3 at their first step beside it.
 #include <math_constants.h>
 
 #include <atomic>

@@ -29,9 +29,11 @@
 // the product, so that a block with large values that nobody attends costs the others nothing.  (T is kept apart
 // from m: next to logits of 2^24 and more the powers of two of the steps would be lost.)
 //
-// Bound.  16 sequences of 8192 tokens (32/8 heads) 67 us, 40 of them the pages at the rate of a copy: the loop runs at 5.1
-// TB/s, some 14 us are the kernel's beginning and end.  Groups of eight are bound by a block's 450 warp
-// instructions: 4 sequences of 131,072 tokens 194 us (159 at the rate of a copy), 64 ragged ones in fp32 159 (97).
+// Bound.  16 sequences of 8192 tokens (32/8 heads) 66 us, 40 of them the pages at the rate of a copy: the loop runs at 5.1
+// TB/s, some 14 us are the kernel's beginning and end, and with three warps a scheduler more than half of the issue
+// slots stay empty meanwhile (fixed latencies of products and reads of shared memory).  Groups of eight have 450 warp
+// instructions a block: 4 sequences of 131,072 tokens 194 us (159 at the rate of a copy; the same with every block in L2),
+// 64 ragged ones in fp32 159 (97).
 #include <math_constants.h>
 
 #include <atomic>
