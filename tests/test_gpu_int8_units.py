@@ -96,3 +96,85 @@ def test_attend_units(cuda, tqlib, name, dtype):
         err = (out[starts[b]:starts[b + 1]] - want).abs().amax(-1)
         assert (err <= room).all(), (b, float((err / room).max()))
     assert tqlib.get_device_status() == 0
+
+
+def small_case(cuda, tqlib, dtype, seed=0):
+    """60 ragged sequences over a layer of 4 heads in groups of four, some for the decode kernel: (layer, q, call)."""
+    new, past = drawn(seed, 60, (1, 120), (0, 300), 5)
+    heads, hq, lens = 4, 16, [a + b for a, b in zip(new, past)]
+    gen = cuda.Generator(device="cuda").manual_seed(seed)
+    used = [-(-n // BLOCK) for n in lens]
+    blocks = sum(used)
+    layer = tqlib.Layer(blocks, heads, kv_format="int8")
+    layer.append(*(cuda.randn(blocks * BLOCK, heads, D, device="cuda", generator=gen) for _ in "kv"), cuda.arange(blocks * BLOCK, device="cuda"))
+    table = cuda.full((len(lens), max(used)), -1, dtype=cuda.int32, device="cuda")
+    for b, n in enumerate(used):
+        table[b, :n] = cuda.arange(sum(used[:b]), sum(used[:b]) + n, device="cuda")
+    starts = cuda.tensor([sum(new[:b]) for b in range(len(new) + 1)], dtype=cuda.int32, device="cuda")
+    lens = cuda.tensor(lens, dtype=cuda.int32, device="cuda")
+    q = cuda.randn(sum(new), hq, D, device="cuda", generator=gen).to(dtype)
+    return layer, q, (starts, table, lens)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attend_rows_anywhere(cuda, tqlib, dtype):
+    """Rows that begin at any element, heads and tokens in any order, in place: the same bits as contiguous ones."""
+    dtype = cuda.bfloat16 if dtype == "bf16" else cuda.float32
+    layer, q, args = small_case(cuda, tqlib, dtype)
+    want = layer.attend(q, *args)
+    n, hq = q.shape[0], q.shape[1]
+
+    def views():
+        odd = cuda.full((n * (hq * 131 + 7) + 3,), 5.0, dtype=dtype, device="cuda")
+        yield odd, odd.as_strided((n, hq, D), (hq * 131 + 7, 131, 1), 3)  # no row is aligned to more than an element
+        turned = cuda.full((hq + 1, n, D + 4), 5.0, dtype=dtype, device="cuda")
+        yield turned, turned[1:, :, 4:].transpose(0, 1)  # head by head
+
+    for _, rows in views():
+        rows.copy_(q)
+        assert cuda.equal(layer.attend(rows, *args), want)
+    for whole, rows in views():
+        layer.attend(q, *args, out=rows)
+        assert cuda.equal(rows, want)
+        rows.fill_(5.0)
+        assert (whole == 5.0).all()  # nothing between the rows was written
+    for _, rows in views():
+        rows.copy_(q)
+        assert layer.attend(rows, *args, out=rows) is rows and cuda.equal(rows, want)
+    assert tqlib.get_device_status() == 0
+
+
+def test_attend_replayed(cuda, tqlib):
+    """A captured call over several units a CTA, replayed with other lengths, queries and tables; calls on two streams at once, each
+    with a workspace of its own."""
+    layer, q, (starts, table, lens) = small_case(cuda, tqlib, cuda.bfloat16)
+    other = small_case(cuda, tqlib, cuda.bfloat16, 1)
+    ws = cuda.zeros(layer.attend_workspace_bytes(q.shape[0], 60, 16, table.shape[1]), dtype=cuda.uint8, device="cuda")
+    out = cuda.zeros_like(q)
+    side = cuda.cuda.Stream()
+    side.wait_stream(cuda.cuda.current_stream())
+    with cuda.cuda.stream(side):
+        layer.attend(q, starts, table, lens, out=out, workspace=ws)
+    cuda.cuda.current_stream().wait_stream(side)
+    graph = cuda.cuda.CUDAGraph()
+    with cuda.cuda.graph(graph):
+        layer.attend(q, starts, table, lens, out=out, workspace=ws)
+    g = np.random.default_rng(5)
+    for turn in range(4):
+        lens.copy_(cuda.from_numpy(np.maximum(lens.cpu().numpy() - g.integers(0, 20, 60), 0).astype(np.int32)))
+        table.copy_(table[cuda.randperm(60, device="cuda")])
+        q.mul_(-1.0)
+        graph.replay()
+        got = out.clone()
+        tqlib.get_device_status()  # (rows whose tables have become shorter than their lengths name blocks that are not there)
+        assert cuda.equal(got, layer.attend(q, starts, table, lens, out=cuda.zeros_like(q)))
+    want = other[0].attend(other[1], *other[2])
+    tqlib.get_device_status()
+    for _ in range(5):
+        side.wait_stream(cuda.cuda.current_stream())
+        graph.replay()
+        with cuda.cuda.stream(side):
+            second = other[0].attend(other[1], *other[2])
+        cuda.cuda.current_stream().wait_stream(side)
+        assert cuda.equal(second, want) and cuda.equal(out, got)
+    tqlib.get_device_status()
