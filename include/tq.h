@@ -464,8 +464,8 @@ size_t tq_attend_workspace_bytes(const tq_cache_desc* desc, int64_t n_tokens, in
  * must be zero-filled again).  Up to 65536 query heads, 2^30 rows (tokens x query heads of a KV
  * head) and 2^26 columns of the table.  In sequences of more than 24 rows weights are fp16 for bf16 queries (half a step
  * 2^-11), two fp16 parts for fp32 ones (so a caller of bf16 queries who wants them gives the queries in fp32), and
- * the tensor cores cut off less than 2e-4 of a value's sum for bf16 queries and 2e-5 for fp32 ones, whatever the
- * context.  int8 layers only (TQ_ERR_UNSUPPORTED otherwise). */
+ * what the tensor cores cut off leaves a value's sum less than 2e-4 small for bf16 queries and 3e-5 for fp32 ones, at
+ * up to 2^20 tokens.  int8 layers only (TQ_ERR_UNSUPPORTED otherwise). */
 tq_status tq_attend(const tq_cache_desc* desc, const tq_heads* q, int q_dtype, int out_dtype, int64_t n_tokens,
                     const int32_t* query_starts, int batch, const int32_t* block_table, int max_blocks_per_seq,
                     const int32_t* context_lens, float sm_scale, void* workspace, size_t workspace_bytes, void* stream);

@@ -788,8 +788,9 @@ class Blocks:
 
     def _pool(self, rows, stream):
         """Reference to the tq_block_pool of `refs` and a workspace for calls of so many rows.  The object's own is made for
-        the next power of two; a call that is captured while there is none has memory of the graph's instead, which is
-        zero when the graph runs, not before, and free for the graph's later calls."""
+        the next power of two; a call that is captured while there is none has memory of the graph's instead
+        (torch.cuda.graph's pool, as every tensor made in a capture), which is zero when the graph runs, not before, and free
+        for the graph's later calls."""
         if rows <= self._rows:
             return self._pool_ref
         most = max(1024, 1 << (rows - 1).bit_length())
